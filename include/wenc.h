@@ -290,6 +290,126 @@ WENC_API wenc_status wenc_linear_tf32(const float* A, const float* W, const floa
 WENC_API wenc_status wenc_attention_tf32(const float* q, const float* k, const float* v, float* out,
                                          int B, int T, int H, int hd, wenc_stream_t stream);
 
+/* Arguments of wenc_kv_append. Strides are in elements; pointers are device pointers owned by the
+ * caller, 16-byte aligned, every stride a multiple of 16 bytes. */
+typedef struct {
+  int dtype;                 /* wenc_dtype of q, k, v and the pages */
+  int n_tokens;              /* rows of q, k, v (0 is a no-op) */
+  int n_seqs;                /* sequences */
+  int n_heads, n_kv_heads;   /* query heads (read only with q) and key heads, each at most 4096 */
+  int head_dim;              /* must be 64 */
+  const void* q;             /* [n_tokens][n_heads][64], or NULL with q_out NULL: no queries */
+  void* q_out;               /* where the turned queries go (may be q) */
+  const void* k;             /* [n_tokens][n_kv_heads][64] */
+  const void* v;
+  int64_t q_stride, q_out_stride, k_stride, v_stride; /* between tokens */
+  void* k_pages;             /* [n_pages][page_size][n_kv_heads][64]; pages k_page_stride apart */
+  void* v_pages;
+  int64_t k_page_stride, v_page_stride;
+  int n_pages, page_size;
+  const int32_t* block_table; /* [n_seqs][max_pages], rows block_table_stride apart */
+  int64_t block_table_stride;
+  int max_pages;             /* max_pages * page_size <= 2^31 - 1 */
+  const int32_t* lens;       /* [n_seqs] cache length of each sequence, the call's tokens included */
+  const int32_t* seq_start;  /* [n_seqs + 1], ascending from 0: sequence s owns the rows seq_start[s] ..
+                                seq_start[s+1]-1; NULL: n_tokens / n_seqs rows each */
+  const int32_t* positions;  /* [n_tokens] the position each token turns by; NULL: its cache position */
+  const float* inv_freq;     /* [rot_dim / 2] angle per position; NULL: no rotation (rot_dim ignored) */
+  int rot_dim;               /* elements of each head that turn: a multiple of 16, 16..64 */
+  int interleaved;           /* pairs (2i, 2i+1) instead of (i, i + rot_dim/2) */
+} wenc_kv_append_args;
+
+/* wenc_kv_append -- write the keys and values of new tokens to a paged cache, turning keys (and
+ * queries, into q_out) by their positions on the way (inferencelayer DEC_WRITE; oxinfer
+ * LayerCache; Whisper itself has learned positions: pass inv_freq = NULL). Token t of sequence s
+ * goes to cache position lens[s] - (seq_start[s+1] - t). Rows behind seq_start[n_seqs] are neither
+ * read nor written. Which key stays is undefined when two sequences' tables lead to one slot.
+ * A length, offset or page number out of range leaves that token unwritten and records
+ * WENC_ERR_INVALID_ARG in the device error word (wenc_sync_status(NULL)). One launch,
+ * stream-ordered. */
+WENC_API wenc_status wenc_kv_append(const wenc_kv_append_args* args, wenc_stream_t stream);
+
+/* Arguments of wenc_prefix_attention. Strides in elements, multiples of 16 bytes; buffers 16-byte
+ * aligned device pointers owned by the caller. */
+typedef struct {
+  int dtype;                 /* wenc_dtype of q, out, prefix and pages */
+  int n_seqs, q_len;         /* sequences, and query tokens of each (>= 1) */
+  int n_heads, n_kv_heads;   /* n_heads a multiple of n_kv_heads: query head h reads key head
+                                h / (n_heads / n_kv_heads) */
+  int head_dim;              /* must be 64 */
+  const void* q;             /* [n_seqs * q_len][n_heads][64], tokens q_stride apart */
+  void* out;                 /* the same, tokens out_stride apart */
+  int64_t q_stride, out_stride;
+  /* the shared prefix (k_prefix NULL: none) */
+  int n_groups;              /* groups of sequences that share one prefix */
+  int max_group;             /* sequences of the largest group */
+  const int32_t* group_start; /* [n_groups + 1], ascending from 0: group g holds the sequences
+                                group_start[g] .. group_start[g+1]-1; NULL: max_group each, and
+                                n_seqs = n_groups * max_group */
+  const void* k_prefix;      /* [n_groups][prefix_max][n_kv_heads][64] */
+  const void* v_prefix;
+  int64_t k_group_stride, k_token_stride, v_group_stride, v_token_stride;
+  int prefix_max;
+  const int32_t* prefix_lens; /* [n_groups] 0..prefix_max; NULL: prefix_max each */
+  /* each sequence's own keys (k_pages NULL: none), as written by wenc_kv_append */
+  const void* k_pages;       /* [n_pages][page_size][n_kv_heads][64] */
+  const void* v_pages;
+  int64_t k_page_stride, v_page_stride;
+  int n_pages, page_size;
+  const int32_t* block_table; /* [n_seqs][max_pages] */
+  int64_t block_table_stride;
+  int max_pages;
+  const int32_t* lens;       /* [n_seqs] own keys, the q_len newest among them */
+  float scale;               /* of the scores; 0.125 = 64^-0.5 in Whisper */
+  void* workspace;           /* wenc_prefix_attention_workspace(args) bytes, 256-byte aligned */
+  size_t workspace_bytes;
+} wenc_prefix_attention_args;
+
+/* wenc_prefix_attention -- decode-step attention of a batch whose sequences share long prefixes:
+ * the beams of a window over its cross-attention keys (the planes of wenc_cross_kv), or requests
+ * behind one prompt (inferencelayer DEC_QATTN; oxinfer CrossLayer::attend and attention_masked).
+ * Token i of a sequence sees its group's whole prefix and its own keys j <= lens - q_len + i:
+ *   out = softmax(scale * q [K_prefix; K_own]^T) [V_prefix; V_own],
+ * and zeros where it sees no key. The prefix is read once for all of a group's queries. Keys behind
+ * a length are never read as numbers (they may hold anything). Scores, statistics and accumulators
+ * are fp32; float32 products are formed from three TF32 products each. Sequences outside every
+ * group's range keep their rows of `out` as they were.
+ * A length, offset or page number out of range records WENC_ERR_INVALID_ARG in the device error
+ * word (wenc_sync_status(NULL)); nothing out of range is accessed and the output rows it concerns are
+ * undefined. The workspace belongs to the call until its work is done: calls that may overlap need
+ * one each. At most two launches, no allocation, stream-ordered. */
+WENC_API wenc_status wenc_prefix_attention(const wenc_prefix_attention_args* args, wenc_stream_t stream);
+
+/* wenc_prefix_attention_workspace -- bytes of workspace the call needs on the current device (0 for
+ * arguments it would refuse). Depends on the sizes and on which of prefix and pages is there, not on
+ * device data. */
+WENC_API size_t wenc_prefix_attention_workspace(const wenc_prefix_attention_args* args);
+
+/* wenc_quantize_rows -- rows of 8-bit integers with one scale each, the operand of wenc_linear_i8:
+ * scale[m] = fp32(max_k |x[m][k]| * fp32(1 / 127)), xq[m][k] = x[m][k] / scale[m] rounded to nearest (ties to
+ * even, of the exact quotient), within -127..127. A row of zeros has scale 0; a row that holds an
+ * infinity or a NaN has scale NaN and integers 0. x is [rows][d] in x_dtype (wenc_dtype), xq [rows][d],
+ * all contiguous; d a positive multiple of 16, rows >= 1; buffers 16-byte aligned (scale: 4).
+ * One launch, stream-ordered. */
+WENC_API wenc_status wenc_quantize_rows(const void* x, int x_dtype, int8_t* xq, float* scale, int rows, int d,
+                                        wenc_stream_t stream);
+
+/* wenc_linear_i8 -- wenc_linear on 8-bit integers with a scale for each token and each output channel
+ * (oxinfer src/whisper/model.rs make_lin Q8, with whole-row scales):
+ *   out = epilogue((sum_k xq[m][k] wq[n][k]) * x_scale[m] * w_scale[n] + bias[n]).
+ * xq int8 [M, K], wq int8 [N, K], x_scale [M], w_scale [N], bias [N] float32; resid / out as for
+ * wenc_linear. N a multiple of 128, K a multiple of 64, M >= 1; buffers 16-byte aligned (x_scale: 4).
+ * The integers run as bf16 on the tensor cores (exact; sm_103a has no integer form of its
+ * fifth-generation MMA), products are exact and sums fp32. workspace: wenc_linear_i8_workspace(M, N, K)
+ * bytes, 256-byte aligned (NULL when that is 0); it belongs to the call until its work is done.
+ * Stream-ordered; errors as wenc_linear. */
+WENC_API wenc_status wenc_linear_i8(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
+                                    const float* bias, const float* resid, void* out, int M, int N, int K,
+                                    int epilogue, void* workspace, size_t workspace_bytes, wenc_stream_t stream);
+
+/* wenc_linear_i8_workspace -- bytes of workspace wenc_linear_i8 needs for these sizes. */
+WENC_API size_t wenc_linear_i8_workspace(int M, int N, int K);
+
 /* wenc_set_device_alloc_limit -- test hook for the out-of-memory path (the pages have no
  * counterpart). Caps the device memory the library holds in its handles' arenas (weights,
  * workspace, stem, cross K/V) at `bytes`; an allocation that would exceed the cap fails as if
@@ -350,7 +470,8 @@ WENC_API wenc_status wenc_selftest_gemm_schedule(int M, int N, int pair, int max
 
 /* wenc_sync_status -- synchronise the device and read the device error word of `h`
  * (or, when h is NULL, the word shared by the handle-less entry points), clearing it.
- * Returns WENC_OK, WENC_ERR_DEVICE_TIMEOUT or WENC_ERR_CUDA. */
+ * Returns WENC_OK, WENC_ERR_DEVICE_TIMEOUT, WENC_ERR_INVALID_ARG (a kernel met a length, offset or
+ * page number out of range in device memory) or WENC_ERR_CUDA. */
 WENC_API wenc_status wenc_sync_status(wenc* h);
 
 /* wenc_destroy -- free everything the handle owns (synchronises the device first).

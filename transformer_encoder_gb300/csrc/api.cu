@@ -1171,6 +1171,10 @@ wenc_status wenc_sync_status(wenc* h) {
     }
     if (e != cudaSuccess) return cuda_fail(e, "reading the device error word");
   }
+  if (word != 0 && (word & 0xffu) == WENC_ERR_INVALID_ARG)
+    return fail(WENC_ERR_INVALID_ARG, "a kernel met a %s out of range in device memory (site %u)",
+                ((word >> 8) & 0xffu) == 80 ? "page number" : ((word >> 8) & 0xffu) == 81 ? "length" : "sequence offset",
+                (word >> 8) & 0xffu);
   if (word != 0 && (word & 0xffu) == WENC_ERR_CUDA)
     return fail(WENC_ERR_CUDA, "an index check of the bounds-checked build failed (site %u)", (word >> 8) & 0xffu);
   if (word != 0)

@@ -59,34 +59,6 @@ struct GemmCfg {
   static constexpr size_t SMEM = 1024 /*align slack*/ + STAGES * STAGE_BYTES + EPI_BYTES + NUM_BARS * 8 + 16;
 };
 
-// GELU(z) = z * Phi(z) = 0.5 z (1 + erf(z / sqrt(2))), with erf from the rational
-// approximation of Abramowitz & Stegun, Handbook of Mathematical Functions, formula 7.1.26:
-//   erf(x) = 1 - (a1 t + a2 t^2 + a3 t^3 + a4 t^4 + a5 t^5) exp(-x^2),  t = 1 / (1 + p x),  x >= 0,
-// |error| <= 1.5e-7, far below the bf16 rounding (2^-9 relative) of the fc1 output it feeds.
-// erf is odd, so erf(-x) = -erf(x). Two MUFU operations (reciprocal, exp2) per value; evaluated
-// on two values at once, the polynomial and the products as packed fp32x2 operations (one
-// instruction per pair).
-__device__ __forceinline__ void gelu_erf_x2(float& z0, float& z1) {
-  const float x0 = fabsf(z0) * 0.70710678118654752f, x1 = fabsf(z1) * 0.70710678118654752f;
-  float t0, t1;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(fmaf(0.3275911f, x0, 1.0f)));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(fmaf(0.3275911f, x1, 1.0f)));
-  const uint64_t t = pack_f32x2(t0, t1);
-  uint64_t poly = fma_f32x2(t, pack_f32x2(1.061405429f, 1.061405429f), pack_f32x2(-1.453152027f, -1.453152027f));
-  poly = fma_f32x2(t, poly, pack_f32x2(1.421413741f, 1.421413741f));
-  poly = fma_f32x2(t, poly, pack_f32x2(-0.284496736f, -0.284496736f));
-  poly = fma_f32x2(t, poly, pack_f32x2(0.254829592f, 0.254829592f));
-  poly = mul_f32x2(poly, t);
-  const uint64_t xx = pack_f32x2(x0, x1);
-  float a0, a1;
-  unpack_f32x2(mul_f32x2(mul_f32x2(xx, xx), pack_f32x2(-1.4426950408889634f, -1.4426950408889634f)), a0, a1);
-  const uint64_t neg_e = pack_f32x2(-ex2_approx(a0), -ex2_approx(a1));  // -exp(-x^2)
-  float r0, r1;
-  unpack_f32x2(fma_f32x2(poly, neg_e, pack_f32x2(1.0f, 1.0f)), r0, r1);  // erf(|x|)
-  const uint64_t one_p = pack_f32x2(1.0f + copysignf(r0, z0), 1.0f + copysignf(r1, z1));  // 1 + erf(x)
-  unpack_f32x2(mul_f32x2(mul_f32x2(pack_f32x2(z0, z1), pack_f32x2(0.5f, 0.5f)), one_p), z0, z1);
-}
-
 // ---- CTA-pair forms (cluster of two CTAs; every tcgen05 instruction of a pair kernel uses
 // cta_group::2, as the PTX ISA requires one cta_group value per kernel)
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -218,8 +190,8 @@ __device__ __forceinline__ void load_resid(float4 (&rr)[8], const float* resid, 
 }
 
 // Per-row state of the LayerNorm-related epilogues for the eight rows (4i + lane/8) a lane
-// handles in every chunk of a tile: the folded LayerNorm's mean and 1/std (EPI 5), or the
-// running (mean, M2) of the row segment being written (EPI 7).
+// handles in every chunk of a tile: the folded LayerNorm's mean and 1/std (EPI 5), the
+// running (mean, M2) of the row segment being written (EPI 7), or the row scales (EPI 8-10).
 struct RowState {
   float a[8], b[8];
 };
@@ -227,7 +199,8 @@ struct RowState {
 // EPI 0 = bias, 1 = bias + GELU, 2 = residual + bias (fp32 out), 3 = GELU(bias) + table row
 // (fp32 out), 4 = bias with planar output (plane width `plane`), 5 = LayerNorm folded in
 // (rstd (acc - mean colsum) + bias, bf16 out), 7 = as 2, plus a bf16 copy and the row
-// segment's statistics. For EPI 0, 1 and 4 the output is bf16 (F32OUT false) or fp32 rounded
+// segment's statistics, 8 / 9 / 10 = as 0 / 1 / 2 with the accumulator scaled per row and per column
+// first (integer operands). For EPI 0, 1 and 4 the output is bf16 (F32OUT false) or fp32 rounded
 // to TF32 (F32OUT true: the operand of a TF32 GEMM). `chunk` is the chunk's index within the
 // warp's column segment (EPI 7 merges the chunk statistics in that order).
 template <int EPI, bool F32OUT>
@@ -242,8 +215,9 @@ __device__ __forceinline__ void epilogue_chunk(const uint32_t (&acc)[32], uint32
   __syncwarp();
   const int sub = lane >> 3, cl = lane & 7;
   const float4 bb = __ldg(reinterpret_cast<const float4*>(bias + col) + cl);
+  constexpr bool kScaled = EPI >= 8;  // integer operands: token and channel scales
   float4 cs = make_float4(0.f, 0.f, 0.f, 0.f);
-  if constexpr (EPI == 5) cs = __ldg(reinterpret_cast<const float4*>(ex.colsum + col) + cl);
+  if constexpr (EPI == 5 || kScaled) cs = __ldg(reinterpret_cast<const float4*>(ex.colsum + col) + cl);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = 4 * i + sub;
@@ -254,6 +228,11 @@ __device__ __forceinline__ void epilogue_chunk(const uint32_t (&acc)[32], uint32
       const float mu = rs.a[i], rstd = rs.b[i];
       v = make_float4(fmaf(rstd, fmaf(-mu, cs.x, a.x), bb.x), fmaf(rstd, fmaf(-mu, cs.y, a.y), bb.y),
                       fmaf(rstd, fmaf(-mu, cs.z, a.z), bb.z), fmaf(rstd, fmaf(-mu, cs.w, a.w), bb.w));
+    }
+    if constexpr (kScaled) {
+      const float xs = rs.a[i];
+      v = make_float4(fmaf(a.x, xs * cs.x, bb.x), fmaf(a.y, xs * cs.y, bb.y), fmaf(a.z, xs * cs.z, bb.z),
+                      fmaf(a.w, xs * cs.w, bb.w));
     }
     if constexpr (EPI == 7) {
       v = make_float4(rr[i].x + v.x, rr[i].y + v.y, rr[i].z + v.z, rr[i].w + v.w);
@@ -269,8 +248,8 @@ __device__ __forceinline__ void epilogue_chunk(const uint32_t (&acc)[32], uint32
         const int pl = col / plane;
         off = (static_cast<size_t>(pl) * M + grow) * plane + (col - pl * plane) + 4 * cl;
       }
-      if constexpr (EPI == 2 || EPI == 7) {
-        if constexpr (EPI == 2) v = make_float4(rr[i].x + v.x, rr[i].y + v.y, rr[i].z + v.z, rr[i].w + v.w);
+      if constexpr (EPI == 2 || EPI == 7 || EPI == 10) {
+        if constexpr (EPI != 7) v = make_float4(rr[i].x + v.x, rr[i].y + v.y, rr[i].z + v.z, rr[i].w + v.w);
         *reinterpret_cast<float4*>(static_cast<float*>(out) + off) = v;
         if constexpr (EPI == 7)
           *reinterpret_cast<uint2*>(ex.copy + off) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
@@ -280,7 +259,7 @@ __device__ __forceinline__ void epilogue_chunk(const uint32_t (&acc)[32], uint32
         v = make_float4(v.x + rr[i].x, v.y + rr[i].y, v.z + rr[i].z, v.w + rr[i].w);
         *reinterpret_cast<float4*>(static_cast<float*>(out) + off) = v;
       } else {
-        if constexpr (EPI == 1) {
+        if constexpr (EPI == 1 || EPI == 9) {
           gelu_erf_x2(v.x, v.y);
           gelu_erf_x2(v.z, v.w);
         }
@@ -598,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto col_of = [&](int t) { return tile_n(t) * BN + col_half * (BN / 2); };
     float4 rb[2][8];
-    constexpr bool kRowInput = (EPI == 2 || EPI == 3 || EPI == 7);  // residual rows or table rows
+    constexpr bool kRowInput = (EPI == 2 || EPI == 3 || EPI == 7 || EPI == 10);  // residual rows or table rows
     // A half-width unit's BN / 2 columns sit in TMEM columns [0, BN / 2) and belong to the warps
     // of the first column half; the other warps only release the buffer.
     auto cols_of = [&](int t, int hf) { return hf < 0 ? col_of(t) : tile_n(t) * BN + hf * (BN / 2); };
@@ -654,6 +633,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           rs.a[i] = mu;
           rs.b[i] = 1.0f / sqrtf(m2 / K + ex.eps);
         }
+      }
+      if constexpr (EPI >= 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rs.a[i] = __ldg(ex.row_scale + min(grow0 + 4 * i + (lane >> 3), M - 1));
       }
       if (!mbar_wait_warp(tfull_bar(acc), acc_phase, wc, 4)) break;
       tc_fence_after();
@@ -848,6 +831,7 @@ cudaError_t launch_gemm(const CUtensorMap& tmA, const CUtensorMap& tmW, int M, i
       (!ex.colsum || !ex.stats || ex.seg_w <= 0 || K % ex.seg_w != 0 || K / ex.seg_w > 32 || tf32))
     return cudaErrorInvalidValue;
   if (epilogue == 7 && (!ex.copy || !ex.stats_out || ex.seg_w != bn / 2 || tf32)) return cudaErrorInvalidValue;
+  if (epilogue >= 8 && (!ex.colsum || !ex.row_scale || tf32)) return cudaErrorInvalidValue;
   if (epilogue == 3 && row_period <= 0) return cudaErrorInvalidValue;
   if (epilogue == 4 && (row_period <= 0 || row_period % 32 != 0 || N % row_period != 0)) return cudaErrorInvalidValue;
   if (use_pair(tf32, bn, epilogue, tmW_half)) {
@@ -857,6 +841,9 @@ cudaError_t launch_gemm(const CUtensorMap& tmA, const CUtensorMap& tmW, int M, i
       case 2: return launch_pair<2>(tmA, *tmW_half, M, N, K, bias, resid, out, err, num_sms, stream, row_period, ex);
       case 3: return launch_pair<3>(tmA, *tmW_half, M, N, K, bias, resid, out, err, num_sms, stream, row_period, ex);
       case 5: return launch_pair<5>(tmA, *tmW_half, M, N, K, bias, resid, out, err, num_sms, stream, row_period, ex);
+      case 8: return launch_pair<8>(tmA, *tmW_half, M, N, K, bias, resid, out, err, num_sms, stream, row_period, ex);
+      case 9: return launch_pair<9>(tmA, *tmW_half, M, N, K, bias, resid, out, err, num_sms, stream, row_period, ex);
+      case 10: return launch_pair<10>(tmA, *tmW_half, M, N, K, bias, resid, out, err, num_sms, stream, row_period, ex);
       case 7: return launch_pair<7>(tmA, *tmW_half, M, N, K, bias, resid, out, err, num_sms, stream, row_period, ex);
       default: break;
     }
@@ -878,6 +865,12 @@ cudaError_t launch_gemm(const CUtensorMap& tmA, const CUtensorMap& tmW, int M, i
   WENC_GEMM_CASE(128, 5, false)
   WENC_GEMM_CASE(256, 7, false)
   WENC_GEMM_CASE(128, 7, false)
+  WENC_GEMM_CASE(256, 8, false)
+  WENC_GEMM_CASE(128, 8, false)
+  WENC_GEMM_CASE(256, 9, false)
+  WENC_GEMM_CASE(128, 9, false)
+  WENC_GEMM_CASE(256, 10, false)
+  WENC_GEMM_CASE(128, 10, false)
   WENC_GEMM_CASE(256, 0, true)
   WENC_GEMM_CASE(256, 1, true)
   WENC_GEMM_CASE(256, 2, true)

@@ -88,7 +88,8 @@ constexpr int kEpiGeluTable = 3;
 //   rounded to bf16, and `stats_out`, the (mean, M2) of every seg_w-column row segment (seg_w =
 //   bn / 2), which the next LN-folded GEMM reads.
 struct GemmExtra {
-  const float* colsum = nullptr;
+  const float* colsum = nullptr;     // epilogues 8-10: the channel scales
+  const float* row_scale = nullptr;  // epilogues 8-10: the token scales
   const float2* stats = nullptr;
   float2* stats_out = nullptr;
   uint16_t* copy = nullptr;
@@ -99,6 +100,9 @@ struct GemmExtra {
   // out; -1 (every other caller) leaves the kernel unchanged.
   int stop_odd_after = -1;
 };
+// - epilogues 8, 9, 10: as 0, 1, 2 with acc row_scale_m colsum_n in place of acc (operands that hold
+//   8-bit integers as bf16; the products are exact).
+constexpr int kEpiScaled = 8;
 constexpr int kEpiLnBias = 5;
 constexpr int kEpiResidStats = 7;
 

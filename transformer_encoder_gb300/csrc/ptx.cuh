@@ -11,6 +11,7 @@ namespace wenc_dev {
 
 // Device error word codes (low byte = wenc_status, next byte = the wait or check site).
 constexpr uint32_t kErrTimeout = 5u;
+constexpr uint32_t kErrData = 1u;   // WENC_ERR_INVALID_ARG: a length, offset or page number in device memory is out of range
 constexpr uint32_t kErrIndex = 4u;  // WENC_ERR_CUDA: an index check of the bounds-checked build failed
 
 // Index checks of the bounds-checked build (compiled with -DWENC_BOUNDS_CHECK): a checked access
@@ -347,6 +348,34 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);  // .x = lo (low 16 bits), .y = hi
   return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// GELU(z) = z * Phi(z) = 0.5 z (1 + erf(z / sqrt(2))), with erf from the rational
+// approximation of Abramowitz & Stegun, Handbook of Mathematical Functions, formula 7.1.26:
+//   erf(x) = 1 - (a1 t + a2 t^2 + a3 t^3 + a4 t^4 + a5 t^5) exp(-x^2),  t = 1 / (1 + p x),  x >= 0,
+// |error| <= 1.5e-7, far below the bf16 rounding (2^-9 relative) of the fc1 output it feeds.
+// erf is odd, so erf(-x) = -erf(x). Two MUFU operations (reciprocal, exp2) per value; evaluated
+// on two values at once, the polynomial and the products as packed fp32x2 operations (one
+// instruction per pair).
+__device__ __forceinline__ void gelu_erf_x2(float& z0, float& z1) {
+  const float x0 = fabsf(z0) * 0.70710678118654752f, x1 = fabsf(z1) * 0.70710678118654752f;
+  float t0, t1;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(fmaf(0.3275911f, x0, 1.0f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(fmaf(0.3275911f, x1, 1.0f)));
+  const uint64_t t = pack_f32x2(t0, t1);
+  uint64_t poly = fma_f32x2(t, pack_f32x2(1.061405429f, 1.061405429f), pack_f32x2(-1.453152027f, -1.453152027f));
+  poly = fma_f32x2(t, poly, pack_f32x2(1.421413741f, 1.421413741f));
+  poly = fma_f32x2(t, poly, pack_f32x2(-0.284496736f, -0.284496736f));
+  poly = fma_f32x2(t, poly, pack_f32x2(0.254829592f, 0.254829592f));
+  poly = mul_f32x2(poly, t);
+  const uint64_t xx = pack_f32x2(x0, x1);
+  float a0, a1;
+  unpack_f32x2(mul_f32x2(mul_f32x2(xx, xx), pack_f32x2(-1.4426950408889634f, -1.4426950408889634f)), a0, a1);
+  const uint64_t neg_e = pack_f32x2(-ex2_approx(a0), -ex2_approx(a1));  // -exp(-x^2)
+  float r0, r1;
+  unpack_f32x2(fma_f32x2(poly, neg_e, pack_f32x2(1.0f, 1.0f)), r0, r1);  // erf(|x|)
+  const uint64_t one_p = pack_f32x2(1.0f + copysignf(r0, z0), 1.0f + copysignf(r1, z1));  // 1 + erf(x)
+  unpack_f32x2(mul_f32x2(mul_f32x2(pack_f32x2(z0, z1), pack_f32x2(0.5f, 0.5f)), one_p), z0, z1);
 }
 
 }  // namespace wenc_dev

@@ -13,7 +13,8 @@ import os
 __all__ = [
     "WencError", "lib", "lib_path", "Encoder", "attention", "attention_tf32", "layernorm", "linear", "linear_tf32",
     "sync_status", "selftest_gemm_pair_abort", "EPI_BIAS_BF16", "EPI_BIAS_GELU_BF16", "EPI_BIAS_RESID_F32", "LN_OUT_F32", "LN_OUT_BF16",
-    "LN_OUT_TF32", "PREC_BF16", "PREC_TF32", "EXPORTED_SYMBOLS",
+    "LN_OUT_TF32", "PREC_BF16", "PREC_TF32", "EXPORTED_SYMBOLS", "prefix_attention", "kv_append", "quantize_rows",
+    "linear_i8",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -36,6 +37,8 @@ EXPORTED_SYMBOLS = (
     "wenc_linear_tf32", "wenc_attention_tf32", "wenc_set_stem", "wenc_stem", "wenc_encode", "wenc_encode_launches",
     "wenc_set_cross_kv", "wenc_cross_kv", "wenc_selftest_gemm_schedule", "wenc_selftest_gemm_pair_abort",
     "wenc_set_device_alloc_limit", "wenc_device_bytes_held", "wenc_selftest_attention_abort",
+    "wenc_prefix_attention", "wenc_prefix_attention_workspace", "wenc_kv_append", "wenc_quantize_rows",
+    "wenc_linear_i8", "wenc_linear_i8_workspace",
 )
 
 
@@ -64,6 +67,34 @@ STEM_KEYS = ("conv1_w", "conv1_b", "conv2_w", "conv2_b", "positions")
 
 class StemWeights(ctypes.Structure):
     _fields_ = [("n_mels", ctypes.c_int)] + [(n, ctypes.c_void_p) for n in STEM_KEYS]
+
+
+class KvAppendArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("n_tokens", ctypes.c_int), ("n_seqs", ctypes.c_int),
+                ("n_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("k_page_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64),
+                ("max_pages", ctypes.c_int), ("lens", ctypes.c_void_p), ("seq_start", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int)]
+
+
+class PrefixAttentionArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("n_seqs", ctypes.c_int), ("q_len", ctypes.c_int), ("n_heads", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("q", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("n_groups", ctypes.c_int), ("max_group", ctypes.c_int), ("group_start", ctypes.c_void_p),
+                ("k_prefix", ctypes.c_void_p), ("v_prefix", ctypes.c_void_p), ("k_group_stride", ctypes.c_int64),
+                ("k_token_stride", ctypes.c_int64), ("v_group_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64), ("prefix_max", ctypes.c_int), ("prefix_lens", ctypes.c_void_p),
+                ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_page_stride", ctypes.c_int64),
+                ("v_page_stride", ctypes.c_int64), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int),
+                ("lens", ctypes.c_void_p), ("scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
 
 
 _lib = None
@@ -107,6 +138,14 @@ def lib() -> ctypes.CDLL:
         L.wenc_attention_static.restype = ctypes.c_int
         L.wenc_attention_static_capacity.argtypes = []
         L.wenc_attention_static_capacity.restype = ctypes.c_size_t
+        L.wenc_prefix_attention.argtypes = [ctypes.POINTER(PrefixAttentionArgs), vp]
+        L.wenc_prefix_attention_workspace.argtypes = [ctypes.POINTER(PrefixAttentionArgs)]
+        L.wenc_prefix_attention_workspace.restype = ctypes.c_size_t
+        L.wenc_kv_append.argtypes = [ctypes.POINTER(KvAppendArgs), vp]
+        L.wenc_quantize_rows.argtypes = [vp, i, vp, vp, i, i, vp]
+        L.wenc_linear_i8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, vp, ctypes.c_size_t, vp]
+        L.wenc_linear_i8_workspace.argtypes = [i, i, i]
+        L.wenc_linear_i8_workspace.restype = ctypes.c_size_t
         L.wenc_destroy.argtypes = [vp]
         L.wenc_destroy.restype = None
         L.wenc_last_error.restype = ctypes.c_char_p
@@ -115,7 +154,8 @@ def lib() -> ctypes.CDLL:
                      "wenc_layernorm", "wenc_linear", "wenc_sync_status", "wenc_forward_launches",
                      "wenc_selftest_wait_timeout", "wenc_linear_tf32", "wenc_attention_tf32", "wenc_set_stem",
                      "wenc_stem", "wenc_encode", "wenc_encode_launches", "wenc_set_cross_kv", "wenc_cross_kv",
-                     "wenc_selftest_gemm_schedule", "wenc_selftest_gemm_pair_abort", "wenc_selftest_attention_abort"):
+                     "wenc_selftest_gemm_schedule", "wenc_selftest_gemm_pair_abort", "wenc_selftest_attention_abort",
+                     "wenc_prefix_attention", "wenc_kv_append", "wenc_quantize_rows", "wenc_linear_i8"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -380,6 +420,296 @@ def attention_tf32(q, k, v, out=None, stream=None):
         out = torch.empty_like(q)
     _require(out, torch.float32, "out")
     _check(lib().wenc_attention_tf32(_ptr(q), _ptr(k), _ptr(v), _ptr(out), B, T, H, hd, _stream(stream)))
+    return out
+
+
+def _on_device(named):
+    """Every tensor on the current CUDA device (the device the library launches on)."""
+    import torch
+    dev = torch.cuda.current_device()
+    for name, t in named:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on device {t.get_device()}, the current device is {dev}")
+
+
+def _ints(t, name, shape):
+    """A contiguous int32 CUDA tensor of this shape (None passes)."""
+    import torch
+    if t is None:
+        return
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(t.shape)}")
+
+
+def _token_stride(t, name):
+    """Elements between the tokens of [..., heads, 64]: heads packed, leading axes evenly spaced."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1 or t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]:
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if t.dim() == 4 and t.shape[0] > 1 and t.shape[1] > 1 and t.stride(0) != t.shape[1] * t.stride(1):
+        raise ValueError(f"{name}: tokens must be evenly spaced over the first two axes")
+    packed = t.shape[-2] * t.shape[-1]
+    if t.dim() == 4 and t.shape[1] == 1:
+        return t.stride(0) if t.shape[0] > 1 else packed
+    return t.stride(-3) if t.shape[-3] > 1 else packed
+
+
+def _pool(k_pages, v_pages, dtype, heads):
+    """(pages, page size, stride of K pages, of V pages) of a paged cache [pages, page_size, heads, 64]."""
+    for n, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if t.dtype != dtype:
+            raise TypeError(f"{n} must be {dtype}, got {t.dtype}")
+        if t.dim() != 4 or t.shape[2] != heads:
+            raise ValueError(f"{n} must be [pages, page_size, {heads}, 64], got {tuple(t.shape)}")
+        if t.numel() and not t[0].is_contiguous():
+            raise ValueError(f"{n}: each page must be contiguous")
+    if k_pages.shape != v_pages.shape:
+        raise ValueError(f"k_pages {tuple(k_pages.shape)} and v_pages {tuple(v_pages.shape)} differ")
+    n, size = k_pages.shape[:2]
+    row = size * heads * k_pages.shape[3]
+    return n, size, (k_pages.stride(0) if n > 1 else row), (v_pages.stride(0) if n > 1 else row)
+
+
+def _table(block_table, n_seqs):
+    import torch
+    if block_table.dtype != torch.int32:
+        raise TypeError(f"block_table must be torch.int32, got {block_table.dtype}")
+    if block_table.dim() != 2 or block_table.shape[0] != n_seqs:
+        raise ValueError(f"block_table must be [{n_seqs}, pages], got {tuple(block_table.shape)}")
+    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table: the entries of a sequence must be contiguous")
+    return block_table.stride(0) if n_seqs > 1 else block_table.shape[1]
+
+
+def _dtype_code(t, name):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return 1
+    if t.dtype == torch.float32:
+        return 0
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _scratch(nbytes, like, stream):
+    """Workspace from the allocator of the stream the call runs on (so that it is reused in that
+    stream's order, and is a graph's own while it is being captured)."""
+    import torch
+    if nbytes == 0:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
+        stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    with torch.cuda.stream(s):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+
+
+def prefix_attention(q, k_prefix=None, v_prefix=None, *, prefix_lens=None, group_start=None, max_group=None,
+                     k_pages=None, v_pages=None, block_table=None, lens=None, scale: float = 0.125, out=None,
+                     workspace=None, stream=None):
+    """Decode-step attention of sequences that share prefixes (see wenc_prefix_attention).
+
+    ``q`` [n_seqs, q_len, H, 64] bf16 or float32 (the tokens may be slices of wider rows);
+    ``k_prefix``, ``v_prefix`` [n_groups, prefix_max, Hkv, 64] with ``prefix_lens`` int32 [n_groups]
+    (None: prefix_max each), for instance the planes of ``Encoder.cross_kv`` viewed as
+    [windows, seq_len, H, 64]. The sequences are grouped in order: equal groups, or
+    ``group_start`` int32 [n_groups + 1] with ``max_group`` at least the largest group (None: n_seqs).
+    ``k_pages``, ``v_pages`` [pages, page_size, Hkv, 64] with ``block_table`` int32 [n_seqs, pages]
+    and ``lens`` int32 [n_seqs]: each sequence's own keys, its q_len newest tokens included.
+    ``workspace``: a uint8 tensor to use instead of an allocation; it is busy until the call's work
+    is done.
+    """
+    import torch
+    dt = _dtype_code(q, "q")
+    if q.dim() != 4:
+        raise ValueError(f"q must be [n_seqs, q_len, heads, 64], got {tuple(q.shape)}")
+    n, t, H, hd = q.shape
+    if (k_prefix is None) != (v_prefix is None) or (k_pages is None) != (v_pages is None):
+        raise ValueError("keys and values come together")
+    if k_prefix is None and k_pages is None:
+        raise ValueError("neither a prefix nor pages")
+    if out is None:
+        out = torch.empty((n, t, H, hd), dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype or out.shape != q.shape:
+        raise ValueError(f"out must be {q.dtype} {tuple(q.shape)}, got {out.dtype} {tuple(out.shape)}")
+    _on_device((("q", q), ("k_prefix", k_prefix), ("v_prefix", v_prefix), ("prefix_lens", prefix_lens),
+                ("group_start", group_start), ("k_pages", k_pages), ("v_pages", v_pages),
+                ("block_table", block_table), ("lens", lens), ("out", out), ("workspace", workspace)))
+    a = PrefixAttentionArgs()
+    a.dtype, a.n_seqs, a.q_len, a.n_heads, a.head_dim, a.scale = dt, n, t, H, hd, scale
+    a.q, a.out = q.data_ptr(), out.data_ptr()
+    a.q_stride, a.out_stride = _token_stride(q, "q"), _token_stride(out, "out")
+    if k_prefix is not None:
+        for name, x in (("k_prefix", k_prefix), ("v_prefix", v_prefix)):
+            if x.dtype != q.dtype:
+                raise TypeError(f"{name} must be {q.dtype}, got {x.dtype}")
+            if x.dim() != 4 or x.shape[3] != hd:
+                raise ValueError(f"{name} must be [groups, tokens, heads, 64], got {tuple(x.shape)}")
+            if x.stride(3) != 1 or x.shape[2] > 1 and x.stride(2) != hd:
+                raise ValueError(f"{name}: the heads of a token must be contiguous")
+        if k_prefix.shape != v_prefix.shape:
+            raise ValueError(f"k_prefix {tuple(k_prefix.shape)} and v_prefix {tuple(v_prefix.shape)} differ")
+        G, T, kv, _ = k_prefix.shape
+        a.n_kv_heads, a.n_groups, a.prefix_max = kv, G, T
+        _ints(prefix_lens, "prefix_lens", (G,))
+        _ints(group_start, "group_start", (G + 1,))
+        if group_start is not None:
+            a.group_start = group_start.data_ptr()
+            a.max_group = n if max_group is None else min(max_group, n)
+        else:
+            if G == 0 or n % G != 0:
+                raise ValueError(f"{n} sequences are no multiple of {G} groups (pass group_start)")
+            a.max_group = n // G
+        if prefix_lens is not None:
+            a.prefix_lens = prefix_lens.data_ptr()
+        a.k_prefix, a.v_prefix = k_prefix.data_ptr(), v_prefix.data_ptr()
+        a.k_group_stride, a.v_group_stride = ((k_prefix.stride(0), v_prefix.stride(0)) if G > 1 else (0, 0))
+        a.k_token_stride, a.v_token_stride = ((k_prefix.stride(1), v_prefix.stride(1)) if T > 1 else (kv * hd, kv * hd))
+    elif prefix_lens is not None or group_start is not None:
+        raise ValueError("prefix_lens and group_start go with a prefix")
+    if k_pages is not None:
+        if block_table is None or lens is None:
+            raise ValueError("pages need block_table and lens")
+        kv = k_pages.shape[2] if k_prefix is None and k_pages.dim() == 4 else a.n_kv_heads
+        a.n_kv_heads = kv
+        a.n_pages, a.page_size, a.k_page_stride, a.v_page_stride = _pool(k_pages, v_pages, q.dtype, kv)
+        a.block_table_stride = _table(block_table, n)
+        _ints(lens, "lens", (n,))
+        a.max_pages = block_table.shape[1]
+        a.k_pages, a.v_pages = k_pages.data_ptr(), v_pages.data_ptr()
+        a.block_table, a.lens = block_table.data_ptr(), lens.data_ptr()
+    elif block_table is not None or lens is not None:
+        raise ValueError("block_table and lens go with pages")
+    L = lib()
+    if workspace is None:
+        workspace = _scratch(L.wenc_prefix_attention_workspace(a), q, stream)
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(L.wenc_prefix_attention(a, _stream(stream)))
+    return out
+
+
+def kv_append(k, v, k_pages, v_pages, block_table, lens, *, seq_start=None, q=None, q_out=None, positions=None,
+              inv_freq=None, interleaved: bool = False, stream=None):
+    """Write new tokens' keys and values into a paged cache, turning keys and queries by their
+    positions on the way (see wenc_kv_append). Returns ``q_out`` (None without ``q``).
+
+    ``k``, ``v`` [tokens, Hkv, 64] and ``q`` [tokens, H, 64], bf16 or float32 (slices of a fused
+    projection's rows will do); ``k_pages``, ``v_pages`` [pages, page_size, Hkv, 64];
+    ``block_table`` int32 [n_seqs, pages]; ``lens`` int32 [n_seqs], the call's tokens included;
+    ``seq_start`` int32 [n_seqs + 1] (None: tokens / n_seqs each); ``positions`` int32 [tokens]
+    (None: the cache positions); ``inv_freq`` float32 [rot_dim / 2] (None: no rotation). ``q_out``
+    may be ``q``; without it the turned queries go to a new tensor, whose padding rows are zeros.
+    """
+    import torch
+    dt = _dtype_code(k, "k")
+    for name, x in (("k", k), ("v", v), ("q", q), ("q_out", q_out)):
+        if x is None:
+            continue
+        if x.dtype != k.dtype:
+            raise TypeError(f"{name} must be {k.dtype}, got {x.dtype}")
+        if x.dim() != 3 or x.shape[0] != k.shape[0] or x.shape[2] != k.shape[2]:
+            raise ValueError(f"{name} must be [{k.shape[0]}, heads, {k.shape[2]}], got {tuple(x.shape)}")
+    if k.shape != v.shape:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} differ")
+    if q is None and q_out is not None:
+        raise ValueError("q_out goes with q")
+    if q is not None and q_out is None:
+        q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    if q is not None and q_out.shape != q.shape:
+        raise ValueError(f"q_out must be {tuple(q.shape)}, got {tuple(q_out.shape)}")
+    _on_device((("k", k), ("v", v), ("q", q), ("q_out", q_out), ("k_pages", k_pages), ("v_pages", v_pages),
+                ("block_table", block_table), ("lens", lens), ("seq_start", seq_start), ("positions", positions),
+                ("inv_freq", inv_freq)))
+    n, kv, hd = k.shape
+    n_seqs = lens.shape[0]
+    if n == 0:
+        return q_out
+    a = KvAppendArgs()
+    a.dtype, a.n_tokens, a.n_seqs, a.n_kv_heads, a.head_dim = dt, n, n_seqs, kv, hd
+    a.k, a.v, a.k_stride, a.v_stride = k.data_ptr(), v.data_ptr(), _token_stride(k, "k"), _token_stride(v, "v")
+    if q is not None:
+        a.n_heads, a.q, a.q_out = q.shape[1], q.data_ptr(), q_out.data_ptr()
+        a.q_stride, a.q_out_stride = _token_stride(q, "q"), _token_stride(q_out, "q_out")
+    a.n_pages, a.page_size, a.k_page_stride, a.v_page_stride = _pool(k_pages, v_pages, k.dtype, kv)
+    a.block_table_stride = _table(block_table, n_seqs)
+    a.max_pages = block_table.shape[1]
+    _ints(lens, "lens", (n_seqs,))
+    _ints(seq_start, "seq_start", (n_seqs + 1,))
+    _ints(positions, "positions", (n,))
+    a.k_pages, a.v_pages = k_pages.data_ptr(), v_pages.data_ptr()
+    a.block_table, a.lens = block_table.data_ptr(), lens.data_ptr()
+    if seq_start is not None:
+        a.seq_start = seq_start.data_ptr()
+    if positions is not None:
+        a.positions = positions.data_ptr()
+    if inv_freq is not None:
+        _require(inv_freq, torch.float32, "inv_freq")
+        if inv_freq.dim() != 1:
+            raise ValueError(f"inv_freq must be [rot_dim / 2], got {tuple(inv_freq.shape)}")
+        a.inv_freq, a.rot_dim, a.interleaved = inv_freq.data_ptr(), 2 * inv_freq.shape[0], int(interleaved)
+    _check(lib().wenc_kv_append(a, _stream(stream)))
+    return q_out
+
+
+def quantize_rows(x, out=None, scale=None, stream=None):
+    """(int8 rows, float32 scales) of x [..., d] bf16 or float32: scale = max|row| * (1 / 127) (see
+    wenc_quantize_rows)."""
+    import torch
+    dt = _dtype_code(x, "x")
+    _require(x, x.dtype, "x")
+    d = x.shape[-1]
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _require(out, torch.int8, "out")
+    _require(scale, torch.float32, "scale")
+    if out.shape != x.shape or scale.shape != x.shape[:-1]:
+        raise ValueError(f"out must be {tuple(x.shape)} and scale {tuple(x.shape[:-1])}")
+    _on_device((("x", x), ("out", out), ("scale", scale)))
+    _check(lib().wenc_quantize_rows(_ptr(x), dt, _ptr(out), _ptr(scale), x.numel() // d if d else 0, d,
+                                    _stream(stream)))
+    return out, scale
+
+
+def linear_i8(a, a_scale, w, w_scale, bias, epilogue: int = EPI_BIAS_BF16, resid=None, out=None, workspace=None,
+              stream=None):
+    """out = epilogue((a w^T) * a_scale[:, None] * w_scale + bias) on 8-bit integers: a int8 [M, K]
+    with float32 scales [M] (``quantize_rows``), w int8 [N, K] with float32 scales [N]; epilogues
+    and outputs as ``linear``."""
+    import torch
+    for name, t, want in (("a", a, torch.int8), ("w", w, torch.int8), ("a_scale", a_scale, torch.float32),
+                          ("w_scale", w_scale, torch.float32), ("bias", bias, torch.float32)):
+        _require(t, want, name)
+    if a.dim() != 2 or w.dim() != 2 or a.shape[1] != w.shape[1]:
+        raise ValueError(f"a {tuple(a.shape)} and w {tuple(w.shape)} must be [M, K] and [N, K]")
+    M, K = a.shape
+    N = w.shape[0]
+    if a_scale.numel() != M or w_scale.numel() != N or bias.numel() != N:
+        raise ValueError(f"a_scale must hold {M} scales, w_scale and bias {N}")
+    dt = torch.float32 if epilogue == EPI_BIAS_RESID_F32 else torch.bfloat16
+    if out is None:
+        out = torch.empty((M, N), dtype=dt, device=a.device)
+    _require(out, dt, "out")
+    if resid is not None:
+        _require(resid, torch.float32, "resid")
+    if tuple(out.shape) != (M, N) or resid is not None and tuple(resid.shape) != (M, N):
+        raise ValueError(f"out and resid must be {(M, N)}")
+    _on_device((("a", a), ("a_scale", a_scale), ("w", w), ("w_scale", w_scale), ("bias", bias), ("resid", resid),
+                ("out", out), ("workspace", workspace)))
+    L = lib()
+    if workspace is None:
+        workspace = _scratch(L.wenc_linear_i8_workspace(M, N, K), a, stream)
+    _check(L.wenc_linear_i8(_ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(resid), _ptr(out), M, N,
+                            K, epilogue, _ptr(workspace),
+                            0 if workspace is None else workspace.numel() * workspace.element_size(),
+                            _stream(stream)))
     return out
 
 
