@@ -51,8 +51,21 @@ def test_prefix_attention_workspace_is_sized_on_the_host(L):
     assert L.wenc_prefix_attention(None, None) == 1
     assert L.wenc_prefix_attention_workspace(None) == 0
     assert L.wenc_prefix_attention_workspace(ctypes.byref(_attn(head_dim=32))) == 0
-    both = L.wenc_prefix_attention_workspace(ctypes.byref(_attn()))
-    assert both >= 2 * 4 * 8 * (64 * 4 + 8)  # at least a share of the prefix and one of the own keys
+    assert L.wenc_prefix_attention_workspace(ctypes.byref(_attn())) == 0  # 4 rows per key head: joined on chip
+    many = dict(n_seqs=200, n_groups=1, max_group=200)
+    both = L.wenc_prefix_attention_workspace(ctypes.byref(_attn(**many)))
+    assert both >= 2 * 200 * 8 * (64 * 4 + 8)  # at least a share of the prefix and one of the own keys
+    a = _attn(**many, workspace=256, workspace_bytes=both - 1)
+    assert L.wenc_prefix_attention(ctypes.byref(a), None) in (1, 2)  # too small (or, first, no sm_103a device)
+
+
+def test_the_binding_packs_the_structures_as_declared():
+    from transformer_encoder_gb300 import wenc
+    for cls, pack in ((wenc.PrefixAttentionArgs, wenc._PREFIX_PACK), (wenc.KvAppendArgs, wenc._APPEND_PACK)):
+        values = [i + 1 for i in range(len(cls._fields_))]
+        raw = pack.pack(*values)
+        a = cls.from_buffer_copy(raw + bytes(ctypes.sizeof(cls) - len(raw)))
+        assert [getattr(a, n) for n, _ in cls._fields_] == values
 
 
 def _append(**kw):

@@ -100,11 +100,13 @@ uint32_t* global_error_word(std::string* why) {
 }
 
 bool device_is_sm103(std::string* why) {
+  static std::atomic<bool> known[64] = {};  // devices found right before
   int dev = 0, major = 0, minor = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     *why = "no CUDA device";
     return false;
   }
+  if (dev >= 0 && dev < 64 && known[dev].load(std::memory_order_relaxed)) return true;
   cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
   cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
   if (major != 10 || minor != 3) {
@@ -113,13 +115,17 @@ bool device_is_sm103(std::string* why) {
     *why = b;
     return false;
   }
+  if (dev >= 0 && dev < 64) known[dev].store(true, std::memory_order_relaxed);
   return true;
 }
 
 int sm_count() {
+  static std::atomic<int> known[64] = {};
   int dev = 0, n = 0;
   cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  if (n > 0 && dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n > 0 ? n : 1;
 }
 

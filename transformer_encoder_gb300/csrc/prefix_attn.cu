@@ -8,17 +8,22 @@
 // (inferencelayer 0.2.4 src/whisper_gpu.rs, DEC_QATTN; oxinfer 0.0.5 src/whisper/model.rs,
 // CrossLayer::attend and attention_masked).
 //
-// The two key sets are attended separately and joined by their maxima and sums, which is exact:
-// a work item is (group, key head, rows, share of the prefix) with the query rows of all the group's
-// sequences and of all query heads of the key head, so the prefix is read once for all of them; or
-// (sequence, key head, rows, share of its own keys). Rows of one item: (token, query head of the key
-// head), token-major. Items write partial results (m, l, O) to the workspace and a second kernel
-// joins them; an item that holds all of its rows' keys writes `out` itself.
+// Rows of one key head: (sequence of the group, token, query head of the key head), so the prefix is read
+// once for all of a group. What bounds it: bytes of K and V for a few rows (a decode step), the tensor
+// pipe for hundreds. Hence two forms:
 //
-// What bounds it: bytes of K and V for a few rows (a decode step), the tensor pipe for hundreds.
-// Up to 16 rows per key head: the four warps of a CTA split the keys of each tile, each warp with
-// its own ring of cp.async stages, no barrier between them, joined once at the end. More rows: the
-// warps split the rows (16 each) and share the tiles.
+// Up to 64 rows per key head (beams): one launch. A cluster of 1 to 8 CTAs attends one (group, key
+// head): its key list is the prefix followed by the own keys of each sequence of the group, cut into
+// tiles that belong to one of these segments each, and every CTA takes an equal run of tiles. Own keys
+// are scored against all the item's rows (the MMA is 16 rows high whether one or 16 are wanted) and
+// masked to their sequence's. The CTAs' results (m, l, O) are joined through distributed shared memory:
+// no workspace and no second kernel.
+// More rows: a work item is a share of a group's prefix, or of one sequence's own keys; items write
+// partial results to the workspace and a second kernel joins them.
+//
+// Inside a CTA, up to 16 rows: the four warps split the keys of each tile, each warp with its own ring
+// of cp.async stages, no barrier between them, joined once at the end. More rows: the warps split the
+// rows (16 each) and share the tiles.
 // Scores use mma.sync (m16n8k16 bf16, m16n8k8 TF32): 16 rows is its height, where a tcgen05 tile
 // would be 64 or 128 rows high and mostly empty.
 // bf16: P is split into two bf16 parts before P V, so its rounding (2^-16 after the split) does not
@@ -104,10 +109,11 @@ struct PrefixParams {
   const int32_t *group_start, *prefix_lens, *table, *lens;
   long long table_stride;
   int n_seqs, q_len, H, Hkv, r, n_groups, max_group, prefix_max, n_pages, page_size, page_shift, max_pages;
-  int np, ns;                    // prefix and own-key splits (0: no such keys)
-  int p_tiles_rows, s_tiles_rows;  // row tiles per prefix item and per own-key item
-  int n_prefix_items;            // CTAs of the prefix part (the own keys' follow)
-  float scale_log2;
+  int np, ns;                    // prefix and own-key splits of the two-launch form (0: no such keys)
+  int row_tiles;                 // row tiles per item of this launch (two-launch form)
+  int cluster;                   // CTAs per item (one-launch form)
+  float scale_log2;              // >= 0
+  uint32_t q_flip, q_keep;       // a negative scale turns the queries' signs (per 32 bits), a zero one clears them
   float* part_o;                 // [(token * H + head) * (np + ns) + slot][64]
   float2* part_ml;               // the same without [64]: (maximum in log2 units, sum)
 };
@@ -127,15 +133,22 @@ struct Cfg {
   static_assert(SMEM >= 4u * 16 * HD * 4 + 4 * 16 * 8, "the ring also holds the warps' results");
 };
 
-// What one CTA attends: rows [row0, row0 + 16 WR) of n_rows against keys [0, n_keys) of one key head,
-// of which it takes the tiles of its split.
+// What one CTA attends: rows [row0, row0 + 16 WR) of the n_rows of one key head, against its run of the
+// tiles of a list of segments: segment 0 is the prefix, segment i the own keys of sequence i - 1 of the
+// item, which only that sequence's rows see.
 struct Item {
-  const uint8_t *k, *v;    // prefix: first key; own keys: the pages' key head
-  const int32_t* table;    // own keys: the sequence's page row (null: prefix)
-  int n_keys, row0, n_rows;
-  int token0, head0;       // row x is token token0 + x / r, query head head0 + x % r
-  int tail;                // own keys: q_len (row x sees n_keys - tail + 1 + x / r keys); prefix: 0
-  int split, n_splits, slot;
+  const uint8_t *kp, *vp;   // first prefix key of the key head
+  int prefix_len;
+  int seq0, n_own;          // first sequence, and how many bring own keys (0: none do)
+  int row0, n_rows;
+  int token0, hk;           // row x is token token0 + x / r, query head hk r + x % r
+  int split, n_splits;
+};
+
+constexpr int kMaxOwn = 64;  // own-key segments of an item: at most one per row of a 64-row tile
+struct SegTable {
+  int tile0[kMaxOwn + 2];    // first tile of each segment, and the end
+  int len[kMaxOwn + 1];      // its keys
 };
 
 // 16-byte granule `c` of key row `row` within a tile. bf16 rows have 8 granules (all 32 banks), fp32
@@ -149,8 +162,12 @@ __device__ __forceinline__ uint32_t granule(int row, int c) {
     return row * 128u + ((c ^ (row & 7)) << 4);
 }
 
+// One CTA's share: leaves O (unnormalised) in shared memory as [16 WR][64] floats and (m, l) per row
+// behind it at kMlOffset, m in log2 units. All threads return after a barrier.
+constexpr uint32_t kMlOffset = 4 * 16 * HD * 4;
+
 template <typename T, int WR>
-__device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, uint8_t* smem, uint32_t* err) {
+__device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, uint8_t* smem, SegTable& seg, uint32_t* err) {
   using C = Cfg<T, WR>;
   constexpr bool F32 = C::F32;
   constexpr int WK = C::WK, KW = C::KW, KT = C::KT, ST = C::STAGES;
@@ -160,7 +177,36 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
   const int g = lane >> 2, tq = lane & 3;
   const uint32_t s0 = smem_u32(smem);
 
-  const int n_tiles = (it.n_keys + KT - 1) / KT;
+  // ---- the segments' tiles: a running sum over up to 65 lengths, by warp 0
+  if (warp == 0) {
+    int base = (it.prefix_len + KT - 1) / KT;
+    if (lane == 0) {
+      seg.tile0[0] = 0;
+      seg.len[0] = it.prefix_len;
+      seg.tile0[1] = base;
+    }
+    for (int i0 = 0; i0 < it.n_own; i0 += 32) {
+      const int i = i0 + lane;
+      int n = i < it.n_own ? p.lens[it.seq0 + i] : 0;
+      if (n < 0 || n > static_cast<long long>(p.max_pages) * p.page_size) {
+        *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (81u << 8);
+        n = 0;
+      }
+      int sum = (n + KT - 1) / KT;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += up;
+      }
+      if (i < it.n_own) {
+        seg.len[1 + i] = n;
+        seg.tile0[2 + i] = base + sum;
+      }
+      base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+  __syncthreads();
+  const int n_tiles = seg.tile0[1 + it.n_own];
   const int per = (n_tiles + it.n_splits - 1) / it.n_splits;
   const int tile0 = it.split * per;
   const int n_mine = max(0, min(per, n_tiles - tile0));
@@ -171,35 +217,42 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
   constexpr int NL = LROWS * CH / LOADERS;
   const int lt = WK == 4 ? lane : threadIdx.x;
   const int lc = lt % CH, lr = (WK == 4 ? wk * KW : 0) + lt / CH;
+  int lseg = 0;  // segment of the next tile to load
   auto load = [&](int j, int stage) {
+    while (tile0 + j >= seg.tile0[lseg + 1]) ++lseg;
     const uint32_t sk = s0 + stage * C::STAGE, sv = sk + C::HALF;
-    const int key0 = (tile0 + j) * KT;
+    const int key0 = (tile0 + j - seg.tile0[lseg]) * KT, n_keys = seg.len[lseg];
+    if (lseg == 0) {
+      const uint8_t* ks = it.kp + (key0 + lr) * p.k_token + lc * 16;
+      const uint8_t* vs = it.vp + (key0 + lr) * p.v_token + lc * 16;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int row = lr + i * (LOADERS / CH);
-      const int key = key0 + row;
-      const bool there = key < it.n_keys;
-      const uint8_t *ks = it.k, *vs = it.v;
-      bool ok = there;
-      if (there) {
-        if (it.table) {
-          const int pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-          const int page = it.table[pi];
-          const int slot = key - pi * p.page_size;
-          ok = page >= 0 && page < p.n_pages;
-          if (ok) {
-            ks += page * p.k_page + slot * p.page_row;
-            vs += page * p.v_page + slot * p.page_row;
-          } else {
-            *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (80u << 8);
-          }
-        } else {
-          ks += key * p.k_token;
-          vs += key * p.v_token;
-        }
+      for (int i = 0; i < NL; ++i) {
+        const int row = lr + i * (LOADERS / CH);
+        const bool ok = key0 + row < n_keys;
+        cp_async16(sk + granule<F32>(row, lc), ok ? ks : it.kp, ok);
+        cp_async16(sv + granule<F32>(row, lc), ok ? vs : it.vp, ok);
+        ks += (LOADERS / CH) * p.k_token;
+        vs += (LOADERS / CH) * p.v_token;
       }
-      cp_async16(sk + granule<F32>(row, lc), ks + lc * 16, ok);
-      cp_async16(sv + granule<F32>(row, lc), vs + lc * 16, ok);
+    } else {
+      const int32_t* table = p.table + (it.seq0 + lseg - 1) * p.table_stride;
+      int page[NL], slot[NL];
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int key = key0 + lr + i * (LOADERS / CH);
+        const int pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+        slot[i] = key - pi * p.page_size;
+        page[i] = key < n_keys ? table[pi] : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int row = lr + i * (LOADERS / CH);
+        const bool ok = page[i] >= 0 && page[i] < p.n_pages;
+        if (!ok && key0 + row < n_keys) *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (80u << 8);
+        const long long at = slot[i] * p.page_row + it.hk * C::ROWB + lc * 16;
+        cp_async16(sk + granule<F32>(row, lc), ok ? p.k_pages + page[i] * p.k_page + at : p.k_pages, ok);
+        cp_async16(sv + granule<F32>(row, lc), ok ? p.v_pages + page[i] * p.v_page + at : p.v_pages, ok);
+      }
     }
   };
 #pragma unroll
@@ -210,10 +263,9 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
 
   // ---- the warp's 16 query rows as A fragments; rows past the end are zeros
   const int ra = it.row0 + wr * 16 + g, rb = ra + 8;
-  const bool warp_rows = it.row0 + wr * 16 < it.n_rows;  // warp-uniform
   auto q_row = [&](int x) {
     const int tok = x / p.r;
-    return p.q + static_cast<long long>(it.token0 + tok) * p.q_stride + (it.head0 + x - tok * p.r) * C::ROWB;
+    return p.q + static_cast<long long>(it.token0 + tok) * p.q_stride + (it.hk * p.r + x - tok * p.r) * C::ROWB;
   };
   constexpr int KS = F32 ? 8 : 4;  // k steps of one score product
   uint32_t qa[KS][4], ql[F32 ? KS : 1][4];
@@ -223,33 +275,38 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
       // k index tq (and tq + 4) of step 2j (and 2j + 1) stands for element 4 (tq + 4j) + {0, 1} ({2, 3})
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4 a = pa ? *reinterpret_cast<const float4*>(pa + (tq + 4 * j) * 16) : z;
-        const float4 b = pb ? *reinterpret_cast<const float4*>(pb + (tq + 4 * j) * 16) : z;
-        split_tf32(a.x, qa[2 * j][0], ql[2 * j][0]);
-        split_tf32(b.x, qa[2 * j][1], ql[2 * j][1]);
-        split_tf32(a.y, qa[2 * j][2], ql[2 * j][2]);
-        split_tf32(b.y, qa[2 * j][3], ql[2 * j][3]);
-        split_tf32(a.z, qa[2 * j + 1][0], ql[2 * j + 1][0]);
-        split_tf32(b.z, qa[2 * j + 1][1], ql[2 * j + 1][1]);
-        split_tf32(a.w, qa[2 * j + 1][2], ql[2 * j + 1][2]);
-        split_tf32(b.w, qa[2 * j + 1][3], ql[2 * j + 1][3]);
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        uint4 a = pa ? *reinterpret_cast<const uint4*>(pa + (tq + 4 * j) * 16) : z;
+        uint4 b = pb ? *reinterpret_cast<const uint4*>(pb + (tq + 4 * j) * 16) : z;
+        auto part = [&](uint32_t x, uint32_t& hi, uint32_t& lo) {
+          split_tf32(__uint_as_float((x & p.q_keep) ^ p.q_flip), hi, lo);
+        };
+        part(a.x, qa[2 * j][0], ql[2 * j][0]);
+        part(b.x, qa[2 * j][1], ql[2 * j][1]);
+        part(a.y, qa[2 * j][2], ql[2 * j][2]);
+        part(b.y, qa[2 * j][3], ql[2 * j][3]);
+        part(a.z, qa[2 * j + 1][0], ql[2 * j + 1][0]);
+        part(b.z, qa[2 * j + 1][1], ql[2 * j + 1][1]);
+        part(a.w, qa[2 * j + 1][2], ql[2 * j + 1][2]);
+        part(b.w, qa[2 * j + 1][3], ql[2 * j + 1][3]);
       }
     } else {
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const int e = (16 * k + 2 * tq) * 2;
-        qa[k][0] = pa ? *reinterpret_cast<const uint32_t*>(pa + e) : 0u;
-        qa[k][1] = pb ? *reinterpret_cast<const uint32_t*>(pb + e) : 0u;
-        qa[k][2] = pa ? *reinterpret_cast<const uint32_t*>(pa + e + 16) : 0u;
-        qa[k][3] = pb ? *reinterpret_cast<const uint32_t*>(pb + e + 16) : 0u;
+        auto part = [&](const uint8_t* x) { return x ? (*reinterpret_cast<const uint32_t*>(x) & p.q_keep) ^ p.q_flip : 0u; };
+        qa[k][0] = part(pa ? pa + e : nullptr);
+        qa[k][1] = part(pb ? pb + e : nullptr);
+        qa[k][2] = part(pa ? pa + e + 16 : nullptr);
+        qa[k][3] = part(pb ? pb + e + 16 : nullptr);
       }
     }
   }
-  // keys each of this thread's two rows sees
-  const int lim_a = it.tail ? it.n_keys - it.tail + 1 + ra / p.r : it.n_keys;
-  const int lim_b = it.tail ? it.n_keys - it.tail + 1 + rb / p.r : it.n_keys;
-  const int lim_all = it.tail ? it.n_keys - it.tail + 1 : it.n_keys;  // keys every row sees
+  // sequence of the item and token of this thread's two rows
+  const int per_seq = p.q_len * p.r;
+  const int sa = ra / per_seq, sb = rb / per_seq;
+  const int ta = (ra - sa * per_seq) / p.r, tb = (rb - sb * per_seq) / p.r;
+  const int row_first = it.row0 + wr * 16, row_end = min(row_first + 16, it.n_rows);  // warp-uniform
 
   float o[8][4];
 #pragma unroll
@@ -257,16 +314,22 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
   float ma = -CUDART_INF_F, mb = -CUDART_INF_F, la = 0.0f, lb = 0.0f;
+  const float sc = p.scale_log2;
 
+  int cseg = 0;
   for (int j = 0; j < n_mine; ++j) {
     cp_async_wait<ST - 2>();
     if constexpr (WK == 4) __syncwarp();
     else __syncthreads();
     if (j + ST - 1 < n_mine) load(j + ST - 1, (j + ST - 1) % ST);
     cp_async_commit();
-    if (WK == 1 && !warp_rows) continue;
-    const uint32_t sk = s0 + (j % ST) * C::STAGE, sv = sk + C::HALF;
+    while (tile0 + j >= seg.tile0[cseg + 1]) ++cseg;
     const int kb = wk * KW;  // first key of the tile this warp scores
+    const int key0 = (tile0 + j - seg.tile0[cseg]) * KT + kb, n_keys = seg.len[cseg];
+    // nothing to score: no rows, no keys, or own keys of a sequence none of the warp's rows belong to
+    if (row_first >= row_end || key0 >= n_keys) continue;
+    if (cseg > 0 && (row_end <= (cseg - 1) * per_seq || row_first >= cseg * per_seq)) continue;
+    const uint32_t sk = s0 + (j % ST) * C::STAGE, sv = sk + C::HALF;
 
     // ---- scores of 16 rows x KW keys
     float s[KW / 8][4];
@@ -301,19 +364,19 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
       }
     }
     // ---- mask, running maximum and sum (log2 units)
-    const int key0 = (tile0 + j) * KT + kb;
-    float xa = -CUDART_INF_F, xb = -CUDART_INF_F;
-#pragma unroll
-    for (int n = 0; n < KW / 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] *= p.scale_log2;
-    if (key0 + KW > lim_all) {
+    int lim_a = n_keys, lim_b = n_keys;  // keys of this segment each of this thread's rows sees
+    if (cseg > 0) {
+      lim_a = sa == cseg - 1 ? n_keys - p.q_len + 1 + ta : 0;
+      lim_b = sb == cseg - 1 ? n_keys - p.q_len + 1 + tb : 0;
+    }
+    if (cseg > 0 || key0 + KW > n_keys) {
 #pragma unroll
       for (int n = 0; n < KW / 8; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (key0 + 8 * n + 2 * tq + (e & 1) >= (e < 2 ? lim_a : lim_b)) s[n][e] = -CUDART_INF_F;
     }
+    float xa = -CUDART_INF_F, xb = -CUDART_INF_F;
 #pragma unroll
     for (int n = 0; n < KW / 8; ++n) {
       xa = fmax3(xa, s[n][0], s[n][1]);
@@ -323,8 +386,8 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
     xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 1));
     xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2));
     xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2));
-    xa = fmaxf(xa, ma);
-    xb = fmaxf(xb, mb);
+    xa = fmaxf(xa * sc, ma);
+    xb = fmaxf(xb * sc, mb);
     const float ua = xa == -CUDART_INF_F ? 0.0f : xa, ub = xb == -CUDART_INF_F ? 0.0f : xb;
     const float fa = ex2_approx(ma - ua), fb = ex2_approx(mb - ub);
     ma = xa;
@@ -332,22 +395,31 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
     la *= fa;
     lb *= fb;
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      o[n][0] *= fa;
-      o[n][1] *= fa;
-      o[n][2] *= fb;
-      o[n][3] *= fb;
-    }
-#pragma unroll
     for (int n = 0; n < KW / 8; ++n) {
-      s[n][0] = ex2_approx(s[n][0] - ua);
-      s[n][1] = ex2_approx(s[n][1] - ua);
-      s[n][2] = ex2_approx(s[n][2] - ub);
-      s[n][3] = ex2_approx(s[n][3] - ub);
+      s[n][0] = ex2_approx(fmaf(s[n][0], sc, -ua));
+      s[n][1] = ex2_approx(fmaf(s[n][1], sc, -ua));
+      s[n][2] = ex2_approx(fmaf(s[n][2], sc, -ub));
+      s[n][3] = ex2_approx(fmaf(s[n][3], sc, -ub));
       la += s[n][0] + s[n][1];
       lb += s[n][2] + s[n][3];
     }
-    // ---- O += P V
+    // ---- O += P V. fp32: the tile's product is formed on its own and added in one rounding, so that the
+    // tensor core's accumulation (which truncates) runs over one tile only
+    float t[F32 ? 8 : 1][4];
+    if constexpr (F32) {
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[n][e] = 0.0f;
+    } else {
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        o[n][0] *= fa;
+        o[n][1] *= fa;
+        o[n][2] *= fb;
+        o[n][3] *= fb;
+      }
+    }
     if constexpr (F32) {
       // k index t of a step stands for key 2t, t + 4 for key 2t + 1 (where the scores already are);
       // column index g of product n for element 4g + n % 4 + 32 (n / 4)
@@ -368,11 +440,18 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
             uint32_t h0, l0, h1, l1;
             split_tf32(w0[n], h0, l0);
             split_tf32(w1[n], h1, l1);
-            mma_tf32(o[4 * c + n], pl, h0, h1);
-            mma_tf32(o[4 * c + n], ph, l0, l1);
-            mma_tf32(o[4 * c + n], ph, h0, h1);
+            mma_tf32(t[4 * c + n], pl, h0, h1);
+            mma_tf32(t[4 * c + n], ph, l0, l1);
+            mma_tf32(t[4 * c + n], ph, h0, h1);
           }
         }
+      }
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        o[n][0] = fmaf(o[n][0], fa, t[n][0]);
+        o[n][1] = fmaf(o[n][1], fa, t[n][1]);
+        o[n][2] = fmaf(o[n][2], fb, t[n][2]);
+        o[n][3] = fmaf(o[n][3], fb, t[n][3]);
       }
     } else {
 #pragma unroll
@@ -401,11 +480,11 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
   la += __shfl_xor_sync(0xffffffffu, la, 2);
   lb += __shfl_xor_sync(0xffffffffu, lb, 2);
 
-  // ---- the warps' results through shared memory: O [4][16][64], (m, l) [4][16]
+  // ---- the warps' results through shared memory (over the ring): O [4][16][64], (m, l) [4][16]
   cp_async_wait<0>();
   __syncthreads();
   float* so = reinterpret_cast<float*>(smem);
-  float2* sml = reinterpret_cast<float2*>(smem + 4 * 16 * HD * 4);
+  float2* sml = reinterpret_cast<float2*>(smem + kMlOffset);
 #pragma unroll
   for (int n = 0; n < 8; ++n) {
     float* d0 = so + (warp * 16 + g) * HD;
@@ -421,54 +500,39 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
     sml[warp * 16 + g + 8] = make_float2(mb, lb);
   }
   __syncthreads();
-  // 8 threads a row, 8 elements each
-  const int n_slots = p.np + p.ns;
-#pragma unroll
-  for (int pass = 0; pass < WR; ++pass) {
-    const int lrow = pass * 16 + (threadIdx.x >> 3), c8 = (threadIdx.x & 7) * 8;
-    const int x = it.row0 + lrow;
-    if (x >= it.n_rows) continue;
+  if constexpr (WK == 4) {  // join of the four warps: 8 threads a row, 8 elements each
+    const int x = threadIdx.x >> 3, c8 = (threadIdx.x & 7) * 8;
     float m = -CUDART_INF_F, l = 0.0f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if constexpr (WK == 1) {
-      m = sml[lrow].x;
-      l = sml[lrow].y;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = so[lrow * HD + c8 + e];
-    } else {
+    for (int w = 0; w < WK; ++w) m = fmaxf(m, sml[w * 16 + x].x);
+    const float u = m == -CUDART_INF_F ? 0.0f : m;
 #pragma unroll
-      for (int w = 0; w < WK; ++w) m = fmaxf(m, sml[w * 16 + lrow].x);
-      const float u = m == -CUDART_INF_F ? 0.0f : m;
+    for (int w = 0; w < WK; ++w) {
+      const float2 ml = sml[w * 16 + x];
+      const float f = ex2_approx(ml.x - u);
+      l += f * ml.y;
 #pragma unroll
-      for (int w = 0; w < WK; ++w) {
-        const float2 ml = sml[w * 16 + lrow];
-        const float f = ex2_approx(ml.x - u);
-        l += f * ml.y;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += f * so[(w * 16 + lrow) * HD + c8 + e];
-      }
+      for (int e = 0; e < 8; ++e) v[e] += f * so[(w * 16 + x) * HD + c8 + e];
     }
-    const int tok = x / p.r, head = it.head0 + x - tok * p.r;
-    if (n_slots == 1) {
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;  // no visible key: zeros
+    __syncthreads();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= inv;
-      uint8_t* dst = p.out + static_cast<long long>(it.token0 + tok) * p.out_stride + head * C::ROWB + c8 * sizeof(T);
-      if constexpr (F32) {
-        reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                    pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-      }
-    } else {
-      const size_t at = (static_cast<size_t>(it.token0 + tok) * p.H + head) * n_slots + it.slot;
-      if (l > 0.0f) {
-        float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + c8);
-        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-      }
-      if (c8 == 0) p.part_ml[at] = make_float2(m, l);
-    }
+    for (int e = 0; e < 8; ++e) so[x * HD + c8 + e] = v[e];
+    if (c8 == 0) sml[x] = make_float2(m, l);
+    __syncthreads();
+  }
+}
+
+// Eight elements of an output row, normalised (a row without a visible key: zeros).
+template <typename T>
+__device__ __forceinline__ void write_out8(const PrefixParams& p, int token, int head, int c8, const float (&v)[8], float l) {
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  uint8_t* dst = p.out + static_cast<long long>(token) * p.out_stride + (head * HD + c8) * static_cast<int>(sizeof(T));
+  if constexpr (sizeof(T) == 4) {
+    reinterpret_cast<float4*>(dst)[0] = make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    reinterpret_cast<float4*>(dst)[1] = make_float4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+  } else {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv),
+                                                pack_bf16x2(v[4] * inv, v[5] * inv), pack_bf16x2(v[6] * inv, v[7] * inv));
   }
 }
 
@@ -489,64 +553,143 @@ __device__ __forceinline__ void group_range(const PrefixParams& p, int g, int& b
   }
 }
 
-template <typename T, int WRP, int WRS>
-__global__ void __launch_bounds__(kThreads) prefix_attn_kernel(const PrefixParams p, uint32_t* err) {
+__device__ __forceinline__ int prefix_len_of(const PrefixParams& p, int grp, uint32_t* err) {
+  int n = p.prefix_lens ? p.prefix_lens[grp] : p.prefix_max;
+  if (n < 0 || n > p.prefix_max) {
+    *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (81u << 8);
+    n = 0;
+  }
+  return n;
+}
+
+__device__ __forceinline__ void cluster_arrive_wait() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t rank_addr(uint32_t saddr, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+// One-launch form: cluster blockIdx.x / cluster attends one (group, key head), all of its rows.
+template <typename T, int WR>
+__global__ void __launch_bounds__(kThreads) prefix_cluster_kernel(const PrefixParams p, uint32_t* err) {
   extern __shared__ __align__(128) uint8_t smem_dyn[];
+  __shared__ SegTable seg;
   pdl_trigger();
   pdl_wait();
-  constexpr int ROWB = HD * sizeof(T);
+  const int item = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
+  Item it;
+  const int grp = item / p.Hkv;
+  it.hk = item % p.Hkv;
+  int begin, count;
+  group_range(p, grp, begin, count, err);
+  if (count == 0) return;  // the whole cluster
+  it.kp = p.kp + grp * p.k_group + it.hk * static_cast<int>(HD * sizeof(T));
+  it.vp = p.vp + grp * p.v_group + it.hk * static_cast<int>(HD * sizeof(T));
+  it.prefix_len = p.kp ? prefix_len_of(p, grp, err) : 0;
+  it.seq0 = begin;
+  it.n_own = p.k_pages ? count : 0;
+  it.row0 = 0;
+  it.n_rows = count * p.q_len * p.r;
+  it.token0 = begin * p.q_len;
+  it.split = rank;
+  it.n_splits = p.cluster;
+  attend<T, WR>(p, it, smem_dyn, seg, err);
+  if (p.cluster > 1) cluster_arrive_wait();
+  // the ranks share the rows out: 8 threads a row, 8 elements each
+  const uint32_t so = smem_u32(smem_dyn);
+  const int c8 = (threadIdx.x & 7) * 8;
+  for (int x = rank + p.cluster * (threadIdx.x >> 3); x < it.n_rows; x += p.cluster * (kThreads / 8)) {
+    float m = -CUDART_INF_F, l = 0.0f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float2 ml[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i < p.cluster) {
+        ml[i] = ld_cluster_f2(rank_addr(so + kMlOffset + x * 8, i));
+        m = fmaxf(m, ml[i].x);
+      }
+    }
+    const float u = m == -CUDART_INF_F ? 0.0f : m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i < p.cluster) {
+        const float f = ex2_approx(ml[i].x - u);
+        const uint32_t a = rank_addr(so + (x * HD + c8) * 4, i);
+        const float4 o0 = ld_cluster_f4(a), o1 = ld_cluster_f4(a + 16);
+        l += f * ml[i].y;
+        v[0] += f * o0.x; v[1] += f * o0.y; v[2] += f * o0.z; v[3] += f * o0.w;
+        v[4] += f * o1.x; v[5] += f * o1.y; v[6] += f * o1.z; v[7] += f * o1.w;
+      }
+    }
+    const int tok = x / p.r;
+    write_out8<T>(p, it.token0 + tok, it.hk * p.r + x - tok * p.r, c8, v, l);
+  }
+  if (p.cluster > 1) cluster_arrive_wait();  // no CTA leaves while another reads its results
+}
+
+// Two-launch form: one CTA per (group, key head, split of the prefix, row tile), or (OWN) per
+// (sequence, key head, split of its own keys, row tile); writes its rows' partial results.
+template <typename T, int WR, bool OWN>
+__global__ void __launch_bounds__(kThreads) prefix_part_kernel(const PrefixParams p, uint32_t* err) {
+  extern __shared__ __align__(128) uint8_t smem_dyn[];
+  __shared__ SegTable seg;
+  pdl_trigger();
+  pdl_wait();
   int b = blockIdx.x;
   Item it;
-  if (b < p.n_prefix_items) {
-    const int rt = b % p.p_tiles_rows;
-    b /= p.p_tiles_rows;
-    it.split = b % p.np;
-    b /= p.np;
-    const int hk = b % p.Hkv, grp = b / p.Hkv;
-    int begin, count;
-    group_range(p, grp, begin, count, err);
-    it.row0 = rt * 16 * WRP;
-    it.n_rows = count * p.q_len * p.r;
-    if (it.row0 >= it.n_rows) return;
-    int n = p.prefix_lens ? p.prefix_lens[grp] : p.prefix_max;
-    if (n < 0 || n > p.prefix_max) {
-      *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (81u << 8);
-      n = 0;
+  it.row0 = (b % p.row_tiles) * 16 * WR;
+  b /= p.row_tiles;
+  it.n_splits = OWN ? p.ns : p.np;
+  it.split = b % it.n_splits;
+  b /= it.n_splits;
+  it.hk = b % p.Hkv;
+  const int which = b / p.Hkv;
+  int begin = which, count = 1;
+  it.kp = p.kp;
+  it.vp = p.vp;
+  it.prefix_len = 0;
+  it.n_own = 1;
+  if (!OWN) {
+    group_range(p, which, begin, count, err);
+    it.kp = p.kp + which * p.k_group + it.hk * static_cast<int>(HD * sizeof(T));
+    it.vp = p.vp + which * p.v_group + it.hk * static_cast<int>(HD * sizeof(T));
+    it.prefix_len = prefix_len_of(p, which, err);
+    it.n_own = 0;
+  }
+  it.n_rows = count * p.q_len * p.r;
+  if (it.row0 >= it.n_rows) return;
+  it.seq0 = begin;
+  it.token0 = begin * p.q_len;
+  attend<T, WR>(p, it, smem_dyn, seg, err);
+  const float* so = reinterpret_cast<const float*>(smem_dyn);
+  const float2* sml = reinterpret_cast<const float2*>(smem_dyn + kMlOffset);
+  const int n_slots = p.np + p.ns, slot = (OWN ? p.np : 0) + it.split, c8 = (threadIdx.x & 7) * 8;
+  for (int y = threadIdx.x >> 3; y < 16 * WR; y += kThreads / 8) {
+    const int x = it.row0 + y;
+    if (x >= it.n_rows) break;
+    const int tok = x / p.r, head = it.hk * p.r + x - tok * p.r;
+    const float2 ml = sml[y];
+    const size_t at = (static_cast<size_t>(it.token0 + tok) * p.H + head) * n_slots + slot;
+    if (ml.y > 0.0f) {
+      float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + c8);
+      dst[0] = *reinterpret_cast<const float4*>(so + y * HD + c8);
+      dst[1] = *reinterpret_cast<const float4*>(so + y * HD + c8 + 4);
     }
-    it.n_keys = n;
-    it.k = p.kp + grp * p.k_group + hk * ROWB;
-    it.v = p.vp + grp * p.v_group + hk * ROWB;
-    it.table = nullptr;
-    it.token0 = begin * p.q_len;
-    it.head0 = hk * p.r;
-    it.tail = 0;
-    it.n_splits = p.np;
-    it.slot = it.split;
-    attend<T, WRP>(p, it, smem_dyn, err);
-  } else {
-    b -= p.n_prefix_items;
-    const int rt = b % p.s_tiles_rows;
-    b /= p.s_tiles_rows;
-    it.split = b % p.ns;
-    b /= p.ns;
-    const int hk = b % p.Hkv, seq = b / p.Hkv;
-    it.row0 = rt * 16 * WRS;
-    it.n_rows = p.q_len * p.r;
-    int n = p.lens[seq];
-    if (n < 0 || n > static_cast<long long>(p.max_pages) * p.page_size) {
-      *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (81u << 8);
-      n = 0;
-    }
-    it.n_keys = n;
-    it.k = p.k_pages + hk * ROWB;
-    it.v = p.v_pages + hk * ROWB;
-    it.table = p.table + seq * p.table_stride;
-    it.token0 = seq * p.q_len;
-    it.head0 = hk * p.r;
-    it.tail = p.q_len;
-    it.n_splits = p.ns;
-    it.slot = p.np + it.split;
-    attend<T, WRS>(p, it, smem_dyn, err);
+    if (c8 == 0) p.part_ml[at] = ml;
   }
 }
 
@@ -608,10 +751,12 @@ wenc_status bad(wenc_status s, const char* fmt, long long a = 0, long long b = 0
 
 // How one call is divided, from its sizes alone.
 struct Plan {
-  int wr_p = 0, wr_s = 0;       // warps along the rows of prefix and own-key items
+  int cluster = 0;              // > 0: the one-launch form, CTAs per item
+  int wr = 0;                   // its warps along the rows
+  int wr_p = 0, wr_s = 0;       // two-launch form: warps along the rows of prefix and own-key items
   int rows_p = 0, rows_s = 0;   // row tiles
   int np = 0, ns = 0;           // key splits
-  long long items_p = 0, items_s = 0;
+  long long items_p = 0, items_s = 0;  // CTAs (one-launch form: items_p)
   size_t part_o = 0, bytes = 0;  // offset of the (m, l) pairs; workspace bytes
 };
 
@@ -624,7 +769,22 @@ Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
   Plan pl;
   const bool f32 = a->dtype == WENC_DTYPE_F32;
   const long long r = a->n_heads / a->n_kv_heads;
-  const long long rows_s = a->q_len * r;
+  const long long rows_s = a->q_len * r;  // rows of one sequence per key head
+  const long long group = a->k_prefix ? a->max_group : 1, n_groups = a->k_prefix ? a->n_groups : a->n_seqs;
+  const long long rows = group * rows_s;
+  const long long own_cap = a->k_pages ? static_cast<long long>(a->max_pages) * a->page_size : 0;
+  const long long prefix = a->k_prefix ? a->prefix_max : 0;
+  if (rows <= 64) {
+    pl.wr = rows <= 16 ? 1 : 4;
+    const int kt = tile_keys(f32, pl.wr);
+    const long long tiles = (prefix + kt - 1) / kt + group * ((own_cap + kt - 1) / kt);
+    const long long items = n_groups * a->n_kv_heads;
+    // enough CTAs for about three rounds of two per SM, none without a tile of its own
+    pl.cluster = 1;
+    while (pl.cluster < 8 && pl.cluster < tiles && items * pl.cluster < 6ll * sms) pl.cluster *= 2;
+    pl.items_p = items * pl.cluster;
+    return pl;
+  }
   auto splits = [&](long long items, long long keys, int wr) {
     const long long tiles = (keys + tile_keys(f32, wr) - 1) / tile_keys(f32, wr);
     long long n = (6ll * sms + items - 1) / items;
@@ -633,26 +793,22 @@ Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
     return static_cast<int>(n < 1 ? 1 : n);
   };
   if (a->k_prefix) {
-    const long long rows = static_cast<long long>(a->max_group) * rows_s;
-    pl.wr_p = rows <= 16 ? 1 : 4;
-    pl.rows_p = static_cast<int>((rows + 16 * pl.wr_p - 1) / (16 * pl.wr_p));
-    const long long items = static_cast<long long>(a->n_groups) * a->n_kv_heads * pl.rows_p;
-    pl.np = splits(items, a->prefix_max, pl.wr_p);
+    pl.wr_p = 4;
+    pl.rows_p = static_cast<int>((rows + 63) / 64);
+    const long long items = n_groups * a->n_kv_heads * pl.rows_p;
+    pl.np = splits(items, prefix, pl.wr_p);
     pl.items_p = items * pl.np;
   }
   if (a->k_pages) {
     pl.wr_s = rows_s <= 16 ? 1 : 4;
     pl.rows_s = static_cast<int>((rows_s + 16 * pl.wr_s - 1) / (16 * pl.wr_s));
     const long long items = static_cast<long long>(a->n_seqs) * a->n_kv_heads * pl.rows_s;
-    pl.ns = splits(items, static_cast<long long>(a->max_pages) * a->page_size, pl.wr_s);
+    pl.ns = splits(items, own_cap, pl.wr_s);
     pl.items_s = items * pl.ns;
   }
-  const int slots = pl.np + pl.ns;
-  if (slots > 1) {
-    const size_t n = static_cast<size_t>(a->n_seqs) * a->q_len * a->n_heads * slots;
-    pl.part_o = n * HD * sizeof(float);
-    pl.bytes = pl.part_o + n * sizeof(float2);
-  }
+  const size_t n = static_cast<size_t>(a->n_seqs) * a->q_len * a->n_heads * (pl.np + pl.ns);
+  pl.part_o = n * HD * sizeof(float);
+  pl.bytes = pl.part_o + n * sizeof(float2);
   return pl;
 }
 
@@ -696,32 +852,63 @@ bool check_sizes(const wenc_prefix_attention_args* a, wenc_status* st) {
   return true;
 }
 
-template <typename T, int WRP, int WRS>
-cudaError_t launch_main(const PrefixParams& p, long long blocks, uint32_t* err, cudaStream_t stream) {
-  auto kern = prefix_attn_kernel<T, WRP, WRS>;
-  constexpr uint32_t smem = Cfg<T, WRP>::SMEM > Cfg<T, WRS>::SMEM ? Cfg<T, WRP>::SMEM : Cfg<T, WRS>::SMEM;
+// Shared-memory opt-in, once per device and kernel (a repeat by a racing host thread is harmless).
+template <typename K>
+cudaError_t opt_in(K kern, uint32_t smem, std::atomic<int>& configured_device) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  // Shared-memory opt-in, once per device and instantiation (a repeat by a racing host thread is harmless).
-  static std::atomic<int> configured_device{-1};
   if (configured_device.load(std::memory_order_acquire) != dev) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     configured_device.store(dev, std::memory_order_release);
   }
-  return wenc_host::launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), smem, stream, p, err);
+  return cudaSuccess;
+}
+
+template <typename T, int WR>
+cudaError_t launch_cluster(const PrefixParams& p, long long blocks, uint32_t* err, cudaStream_t stream) {
+  auto kern = prefix_cluster_kernel<T, WR>;
+  static std::atomic<int> configured{-1};
+  const cudaError_t e = opt_in(kern, Cfg<T, WR>::SMEM, configured);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg<T, WR>::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, p, err);
+}
+
+template <typename T, int WR, bool OWN>
+cudaError_t launch_part(PrefixParams p, int row_tiles, long long blocks, uint32_t* err, cudaStream_t stream) {
+  auto kern = prefix_part_kernel<T, WR, OWN>;
+  static std::atomic<int> configured{-1};
+  const cudaError_t e = opt_in(kern, Cfg<T, WR>::SMEM, configured);
+  if (e != cudaSuccess) return e;
+  p.row_tiles = row_tiles;
+  return wenc_host::launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), Cfg<T, WR>::SMEM, stream, p, err);
 }
 
 template <typename T>
 cudaError_t launch_all(const PrefixParams& p, const Plan& pl, uint32_t* err, cudaStream_t stream) {
-  const long long blocks = pl.items_p + pl.items_s;
-  const int wp = pl.wr_p ? pl.wr_p : pl.wr_s, ws = pl.wr_s ? pl.wr_s : pl.wr_p;
-  cudaError_t e;
-  if (wp == 1 && ws == 1) e = launch_main<T, 1, 1>(p, blocks, err, stream);
-  else if (wp == 4 && ws == 1) e = launch_main<T, 4, 1>(p, blocks, err, stream);
-  else e = launch_main<T, 4, 4>(p, blocks, err, stream);  // own rows never outnumber a group's
-  if (e != cudaSuccess || pl.np + pl.ns == 1) return e;
+  if (pl.cluster > 0)
+    return pl.wr == 1 ? launch_cluster<T, 1>(p, pl.items_p, err, stream) : launch_cluster<T, 4>(p, pl.items_p, err, stream);
+  cudaError_t e = cudaSuccess;
+  if (pl.items_p > 0) e = launch_part<T, 4, false>(p, pl.rows_p, pl.items_p, err, stream);
+  if (e == cudaSuccess && pl.items_s > 0)
+    e = pl.wr_s == 1 ? launch_part<T, 1, true>(p, pl.rows_s, pl.items_s, err, stream)
+                     : launch_part<T, 4, true>(p, pl.rows_s, pl.items_s, err, stream);
+  if (e != cudaSuccess) return e;
   const long long threads = static_cast<long long>(p.n_seqs) * p.q_len * p.H * 16;
   return wenc_host::launch_pdl(prefix_join_kernel<T>, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0,
                                stream, p);
@@ -769,8 +956,8 @@ extern "C" wenc_status wenc_prefix_attention(const wenc_prefix_attention_args* a
   uint32_t* err = wenc_internal_error_word(&why);
   if (!err) return wenc_internal_fail(WENC_ERR_CUDA, why.c_str());
   const Plan pl = make_plan(a, wenc_internal_sm_count());
-  if (pl.items_p + pl.items_s > 0x7fffffffll)
-    return bad(WENC_ERR_UNSUPPORTED, "prefix_attention: %lld work items pass 2^31 - 1", pl.items_p + pl.items_s);
+  if (pl.items_p > 0x7fffffffll || pl.items_s > 0x7fffffffll)
+    return bad(WENC_ERR_UNSUPPORTED, "prefix_attention: %lld work items pass 2^31 - 1", pl.items_p > pl.items_s ? pl.items_p : pl.items_s);
   if (pl.bytes > 0 && (!a->workspace || a->workspace_bytes < pl.bytes))
     return bad(WENC_ERR_INVALID_ARG, "prefix_attention: workspace of %lld bytes needed, %lld given", static_cast<long long>(pl.bytes),
                a->workspace ? static_cast<long long>(a->workspace_bytes) : 0ll);
@@ -816,12 +1003,18 @@ extern "C" wenc_status wenc_prefix_attention(const wenc_prefix_attention_args* a
     for (int s = 0; s < 31; ++s)
       if (a->page_size == 1 << s) p.page_shift = s;
   }
+  if (!a->k_prefix) {  // every sequence a group of its own
+    p.n_groups = a->n_seqs;
+    p.max_group = 1;
+  }
   p.np = pl.np;
   p.ns = pl.ns;
-  p.p_tiles_rows = pl.rows_p;
-  p.s_tiles_rows = pl.rows_s;
-  p.n_prefix_items = static_cast<int>(pl.items_p);
-  p.scale_log2 = a->scale * 1.4426950408889634f;
+  p.cluster = pl.cluster;
+  // |scale| and the queries' signs; a scale of 0 is 1 on queries of 0
+  const bool bf = a->dtype == WENC_DTYPE_BF16;
+  p.q_flip = a->scale < 0.0f ? (bf ? 0x80008000u : 0x80000000u) : 0u;
+  p.q_keep = a->scale == 0.0f ? 0u : 0xffffffffu;
+  p.scale_log2 = (a->scale == 0.0f ? 1.0f : a->scale < 0.0f ? -a->scale : a->scale) * 1.4426950408889634f;
   p.part_o = static_cast<float*>(a->workspace);
   p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(a->workspace) + pl.part_o);
   const cudaError_t e = a->dtype == WENC_DTYPE_F32

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 __all__ = [
     "WencError", "lib", "lib_path", "Encoder", "attention", "attention_tf32", "layernorm", "linear", "linear_tf32",
@@ -97,6 +98,13 @@ class PrefixAttentionArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+# The same structures as one pack() each: a decode step makes these calls for every layer and token,
+# and a ctypes field assignment each costs more there than everything else in the call.
+_PREFIX_PACK = struct.Struct("@6i2P2q2i3P4qi3P2q2iPqiPfPN")
+_APPEND_PACK = struct.Struct("@6i4P4q2P2q2iPqi4P2i")
+assert _PREFIX_PACK.size == ctypes.sizeof(PrefixAttentionArgs) - ctypes.sizeof(PrefixAttentionArgs) % 8
+assert _APPEND_PACK.size == ctypes.sizeof(KvAppendArgs)
+
 _lib = None
 
 
@@ -138,10 +146,11 @@ def lib() -> ctypes.CDLL:
         L.wenc_attention_static.restype = ctypes.c_int
         L.wenc_attention_static_capacity.argtypes = []
         L.wenc_attention_static_capacity.restype = ctypes.c_size_t
-        L.wenc_prefix_attention.argtypes = [ctypes.POINTER(PrefixAttentionArgs), vp]
-        L.wenc_prefix_attention_workspace.argtypes = [ctypes.POINTER(PrefixAttentionArgs)]
+        # (pointers to the argument structures: a byref() of one, or its packed bytes)
+        L.wenc_prefix_attention.argtypes = [vp, vp]
+        L.wenc_prefix_attention_workspace.argtypes = [vp]
         L.wenc_prefix_attention_workspace.restype = ctypes.c_size_t
-        L.wenc_kv_append.argtypes = [ctypes.POINTER(KvAppendArgs), vp]
+        L.wenc_kv_append.argtypes = [vp, vp]
         L.wenc_quantize_rows.argtypes = [vp, i, vp, vp, i, i, vp]
         L.wenc_linear_i8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, vp, ctypes.c_size_t, vp]
         L.wenc_linear_i8_workspace.argtypes = [i, i, i]
@@ -423,74 +432,89 @@ def attention_tf32(q, k, v, out=None, stream=None):
     return out
 
 
-def _on_device(named):
-    """Every tensor on the current CUDA device (the device the library launches on)."""
-    import torch
-    dev = torch.cuda.current_device()
+def _elsewhere(dev, named):
+    """The error for a tensor that is not on the current CUDA device, where the library launches."""
     for name, t in named:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on device {t.get_device()}, the current device is {dev}")
+        if t is not None and not t.is_cuda:
+            return TypeError(f"{name} must be a CUDA tensor")
+        if t is not None and t.get_device() != dev:
+            return ValueError(f"{name} is on device {t.get_device()}, the current device is {dev}")
+    return RuntimeError("tensors on several devices")
+
+
+def _current_device():
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_available() else -2
+
+
+def _raw_stream(stream, dev):
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _ints(t, name, shape):
-    """A contiguous int32 CUDA tensor of this shape (None passes)."""
+    """The address of a contiguous int32 tensor of this shape."""
     import torch
-    if t is None:
-        return
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(t.shape)}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _token_stride(t, name):
     """Elements between the tokens of [..., heads, 64]: heads packed, leading axes evenly spaced."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1 or t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]:
+    shape, st = t.shape, t.stride()
+    hd, heads = shape[-1], shape[-2]
+    if shape[0] == 0:
+        return heads * hd
+    if hd > 1 and st[-1] != 1 or heads > 1 and st[-2] != hd:
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if t.dim() == 4 and t.shape[0] > 1 and t.shape[1] > 1 and t.stride(0) != t.shape[1] * t.stride(1):
-        raise ValueError(f"{name}: tokens must be evenly spaced over the first two axes")
-    packed = t.shape[-2] * t.shape[-1]
-    if t.dim() == 4 and t.shape[1] == 1:
-        return t.stride(0) if t.shape[0] > 1 else packed
-    return t.stride(-3) if t.shape[-3] > 1 else packed
+    if len(shape) == 4:
+        if shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * st[1]:
+            raise ValueError(f"{name}: tokens must be evenly spaced over the first two axes")
+        if shape[1] == 1:
+            return st[0] if shape[0] > 1 else heads * hd
+        return st[1]
+    return st[0] if shape[0] > 1 else heads * hd
 
 
 def _pool(k_pages, v_pages, dtype, heads):
     """(pages, page size, stride of K pages, of V pages) of a paged cache [pages, page_size, heads, 64]."""
-    for n, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if t.dtype != dtype:
-            raise TypeError(f"{n} must be {dtype}, got {t.dtype}")
-        if t.dim() != 4 or t.shape[2] != heads:
-            raise ValueError(f"{n} must be [pages, page_size, {heads}, 64], got {tuple(t.shape)}")
-        if t.numel() and not t[0].is_contiguous():
-            raise ValueError(f"{n}: each page must be contiguous")
-    if k_pages.shape != v_pages.shape:
-        raise ValueError(f"k_pages {tuple(k_pages.shape)} and v_pages {tuple(v_pages.shape)} differ")
-    n, size = k_pages.shape[:2]
-    row = size * heads * k_pages.shape[3]
-    return n, size, (k_pages.stride(0) if n > 1 else row), (v_pages.stride(0) if n > 1 else row)
+    shape, ks, vs = k_pages.shape, k_pages.stride(), v_pages.stride()
+    if k_pages.dtype is not dtype or v_pages.dtype is not dtype:
+        raise TypeError(f"k_pages and v_pages must be {dtype}, got {k_pages.dtype} and {v_pages.dtype}")
+    if len(shape) != 4 or shape[2] != heads or v_pages.shape != shape:
+        raise ValueError(f"k_pages and v_pages must be [pages, page_size, {heads}, 64], got {tuple(shape)} and "
+                         f"{tuple(v_pages.shape)}")
+    n, size, _, hd = shape
+    row = size * heads * hd
+    for name, st in (("k_pages", ks), ("v_pages", vs)):
+        if st[3] != 1 or st[2] != hd and heads > 1 or st[1] != heads * hd and size > 1:
+            raise ValueError(f"{name}: each page must be contiguous")
+    return n, size, (ks[0] if n > 1 else row), (vs[0] if n > 1 else row)
 
 
-def _table(block_table, n_seqs):
+def _table(t, n_seqs):
+    """(address, row stride, columns) of a block table."""
     import torch
-    if block_table.dtype != torch.int32:
-        raise TypeError(f"block_table must be torch.int32, got {block_table.dtype}")
-    if block_table.dim() != 2 or block_table.shape[0] != n_seqs:
-        raise ValueError(f"block_table must be [{n_seqs}, pages], got {tuple(block_table.shape)}")
-    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+    shape, st = t.shape, t.stride()
+    if t.dtype is not torch.int32:
+        raise TypeError(f"block_table must be torch.int32, got {t.dtype}")
+    if len(shape) != 2 or shape[0] != n_seqs:
+        raise ValueError(f"block_table must be [{n_seqs}, pages], got {tuple(shape)}")
+    if shape[1] > 1 and st[1] != 1:
         raise ValueError("block_table: the entries of a sequence must be contiguous")
-    return block_table.stride(0) if n_seqs > 1 else block_table.shape[1]
+    return t.data_ptr(), (st[0] if n_seqs > 1 else shape[1]), shape[1]
 
 
 def _dtype_code(t, name):
     import torch
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return 1
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return 0
     raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
@@ -499,8 +523,6 @@ def _scratch(nbytes, like, stream):
     """Workspace from the allocator of the stream the call runs on (so that it is reused in that
     stream's order, and is a graph's own while it is being captured)."""
     import torch
-    if nbytes == 0:
-        return None
     if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
@@ -521,76 +543,95 @@ def prefix_attention(q, k_prefix=None, v_prefix=None, *, prefix_lens=None, group
     ``group_start`` int32 [n_groups + 1] with ``max_group`` at least the largest group (None: n_seqs).
     ``k_pages``, ``v_pages`` [pages, page_size, Hkv, 64] with ``block_table`` int32 [n_seqs, pages]
     and ``lens`` int32 [n_seqs]: each sequence's own keys, its q_len newest tokens included.
-    ``workspace``: a uint8 tensor to use instead of an allocation; it is busy until the call's work
-    is done.
+    ``workspace``: a uint8 tensor to use instead of an allocation where one is needed; it is busy
+    until the call's work is done.
     """
     import torch
+    dtype = q.dtype
     dt = _dtype_code(q, "q")
     if q.dim() != 4:
         raise ValueError(f"q must be [n_seqs, q_len, heads, 64], got {tuple(q.shape)}")
-    n, t, H, hd = q.shape
     if (k_prefix is None) != (v_prefix is None) or (k_pages is None) != (v_pages is None):
         raise ValueError("keys and values come together")
     if k_prefix is None and k_pages is None:
         raise ValueError("neither a prefix nor pages")
+    n, t, H, hd = q.shape
+    dev = q.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise _elsewhere(_current_device(), (("q", q),))
     if out is None:
-        out = torch.empty((n, t, H, hd), dtype=q.dtype, device=q.device)
-    elif out.dtype != q.dtype or out.shape != q.shape:
-        raise ValueError(f"out must be {q.dtype} {tuple(q.shape)}, got {out.dtype} {tuple(out.shape)}")
-    _on_device((("q", q), ("k_prefix", k_prefix), ("v_prefix", v_prefix), ("prefix_lens", prefix_lens),
-                ("group_start", group_start), ("k_pages", k_pages), ("v_pages", v_pages),
-                ("block_table", block_table), ("lens", lens), ("out", out), ("workspace", workspace)))
-    a = PrefixAttentionArgs()
-    a.dtype, a.n_seqs, a.q_len, a.n_heads, a.head_dim, a.scale = dt, n, t, H, hd, scale
-    a.q, a.out = q.data_ptr(), out.data_ptr()
-    a.q_stride, a.out_stride = _token_stride(q, "q"), _token_stride(out, "out")
+        out = torch.empty((n, t, H, hd), dtype=dtype, device=q.device)
+        out_stride = H * hd
+    else:
+        if out.dtype is not dtype or out.shape != q.shape:
+            raise ValueError(f"out must be {dtype} {tuple(q.shape)}, got {out.dtype} {tuple(out.shape)}")
+        out_stride = _token_stride(out, "out")
+        if out.get_device() != dev:
+            raise _elsewhere(dev, (("out", out),))
+    kv = G = S = T = kp = vp = kg = kt = vg = vt = p_lens = g_start = 0
     if k_prefix is not None:
-        for name, x in (("k_prefix", k_prefix), ("v_prefix", v_prefix)):
-            if x.dtype != q.dtype:
-                raise TypeError(f"{name} must be {q.dtype}, got {x.dtype}")
-            if x.dim() != 4 or x.shape[3] != hd:
-                raise ValueError(f"{name} must be [groups, tokens, heads, 64], got {tuple(x.shape)}")
-            if x.stride(3) != 1 or x.shape[2] > 1 and x.stride(2) != hd:
-                raise ValueError(f"{name}: the heads of a token must be contiguous")
-        if k_prefix.shape != v_prefix.shape:
-            raise ValueError(f"k_prefix {tuple(k_prefix.shape)} and v_prefix {tuple(v_prefix.shape)} differ")
-        G, T, kv, _ = k_prefix.shape
-        a.n_kv_heads, a.n_groups, a.prefix_max = kv, G, T
-        _ints(prefix_lens, "prefix_lens", (G,))
-        _ints(group_start, "group_start", (G + 1,))
+        shape, ks, vs = k_prefix.shape, k_prefix.stride(), v_prefix.stride()
+        if k_prefix.dtype is not dtype or v_prefix.dtype is not dtype:
+            raise TypeError(f"k_prefix and v_prefix must be {dtype}, got {k_prefix.dtype} and {v_prefix.dtype}")
+        if len(shape) != 4 or shape[3] != hd or v_prefix.shape != shape:
+            raise ValueError(f"k_prefix and v_prefix must be [groups, tokens, heads, {hd}], got {tuple(shape)} and "
+                             f"{tuple(v_prefix.shape)}")
+        G, T, kv, _ = shape
+        if ks[3] != 1 or vs[3] != 1 or kv > 1 and (ks[2] != hd or vs[2] != hd):
+            raise ValueError("k_prefix and v_prefix: the heads of a token must be contiguous")
+        if k_prefix.get_device() != dev or v_prefix.get_device() != dev:
+            raise _elsewhere(dev, (("k_prefix", k_prefix), ("v_prefix", v_prefix)))
+        if G > 1:
+            kg, vg = ks[0], vs[0]
+        kt, vt = (ks[1], vs[1]) if T > 1 else (kv * hd, kv * hd)
+        kp, vp = k_prefix.data_ptr(), v_prefix.data_ptr()
         if group_start is not None:
-            a.group_start = group_start.data_ptr()
-            a.max_group = n if max_group is None else min(max_group, n)
+            g_start = _ints(group_start, "group_start", (G + 1,))
+            S = n if max_group is None else min(max_group, n)
+            if group_start.get_device() != dev:
+                raise _elsewhere(dev, (("group_start", group_start),))
+        elif G == 0 or n % G != 0:
+            raise ValueError(f"{n} sequences are no multiple of {G} groups (pass group_start)")
         else:
-            if G == 0 or n % G != 0:
-                raise ValueError(f"{n} sequences are no multiple of {G} groups (pass group_start)")
-            a.max_group = n // G
+            S = n // G
         if prefix_lens is not None:
-            a.prefix_lens = prefix_lens.data_ptr()
-        a.k_prefix, a.v_prefix = k_prefix.data_ptr(), v_prefix.data_ptr()
-        a.k_group_stride, a.v_group_stride = ((k_prefix.stride(0), v_prefix.stride(0)) if G > 1 else (0, 0))
-        a.k_token_stride, a.v_token_stride = ((k_prefix.stride(1), v_prefix.stride(1)) if T > 1 else (kv * hd, kv * hd))
+            p_lens = _ints(prefix_lens, "prefix_lens", (G,))
+            if prefix_lens.get_device() != dev:
+                raise _elsewhere(dev, (("prefix_lens", prefix_lens),))
     elif prefix_lens is not None or group_start is not None:
         raise ValueError("prefix_lens and group_start go with a prefix")
+    pages = size = kps = vps = kpg = vpg = tab = tab_stride = max_pages = own = 0
     if k_pages is not None:
         if block_table is None or lens is None:
             raise ValueError("pages need block_table and lens")
-        kv = k_pages.shape[2] if k_prefix is None and k_pages.dim() == 4 else a.n_kv_heads
-        a.n_kv_heads = kv
-        a.n_pages, a.page_size, a.k_page_stride, a.v_page_stride = _pool(k_pages, v_pages, q.dtype, kv)
-        a.block_table_stride = _table(block_table, n)
-        _ints(lens, "lens", (n,))
-        a.max_pages = block_table.shape[1]
-        a.k_pages, a.v_pages = k_pages.data_ptr(), v_pages.data_ptr()
-        a.block_table, a.lens = block_table.data_ptr(), lens.data_ptr()
+        if k_prefix is None and k_pages.dim() == 4:
+            kv = k_pages.shape[2]
+        pages, size, kps, vps = _pool(k_pages, v_pages, dtype, kv)
+        tab, tab_stride, max_pages = _table(block_table, n)
+        own = _ints(lens, "lens", (n,))
+        kpg, vpg = k_pages.data_ptr(), v_pages.data_ptr()
+        if (k_pages.get_device() != dev or v_pages.get_device() != dev or block_table.get_device() != dev
+                or lens.get_device() != dev):
+            raise _elsewhere(dev, (("k_pages", k_pages), ("v_pages", v_pages), ("block_table", block_table),
+                                   ("lens", lens)))
     elif block_table is not None or lens is not None:
         raise ValueError("block_table and lens go with pages")
-    L = lib()
-    if workspace is None:
-        workspace = _scratch(L.wenc_prefix_attention_workspace(a), q, stream)
-    if workspace is not None:
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(L.wenc_prefix_attention(a, _stream(stream)))
+    L = _lib or lib()
+    args = (dt, n, t, H, kv, hd, q.data_ptr(), out.data_ptr(), _token_stride(q, "q"), out_stride, G, S, g_start, kp, vp, kg,
+            kt, vg, vt, T, p_lens, kpg, vpg, kps, vps, pages, size, tab, tab_stride, max_pages, own, scale)
+    ws = ws_bytes = 0
+    # (up to 64 rows per key head need no workspace, as the library's own count confirms)
+    if workspace is not None or (S or 1) * t * H > 64 * kv:
+        if workspace is None:
+            need = L.wenc_prefix_attention_workspace(_PREFIX_PACK.pack(*args, 0, 0))
+            workspace = _scratch(need, q, stream) if need else None
+        elif workspace.get_device() != dev:
+            raise _elsewhere(dev, (("workspace", workspace),))
+        if workspace is not None:
+            ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    status = L.wenc_prefix_attention(_PREFIX_PACK.pack(*args, ws, ws_bytes), _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return out
 
 
@@ -607,53 +648,55 @@ def kv_append(k, v, k_pages, v_pages, block_table, lens, *, seq_start=None, q=No
     may be ``q``; without it the turned queries go to a new tensor, whose padding rows are zeros.
     """
     import torch
+    dtype = k.dtype
     dt = _dtype_code(k, "k")
-    for name, x in (("k", k), ("v", v), ("q", q), ("q_out", q_out)):
-        if x is None:
-            continue
-        if x.dtype != k.dtype:
-            raise TypeError(f"{name} must be {k.dtype}, got {x.dtype}")
-        if x.dim() != 3 or x.shape[0] != k.shape[0] or x.shape[2] != k.shape[2]:
-            raise ValueError(f"{name} must be [{k.shape[0]}, heads, {k.shape[2]}], got {tuple(x.shape)}")
-    if k.shape != v.shape:
-        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} differ")
-    if q is None and q_out is not None:
-        raise ValueError("q_out goes with q")
-    if q is not None and q_out is None:
-        q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
-    if q is not None and q_out.shape != q.shape:
-        raise ValueError(f"q_out must be {tuple(q.shape)}, got {tuple(q_out.shape)}")
-    _on_device((("k", k), ("v", v), ("q", q), ("q_out", q_out), ("k_pages", k_pages), ("v_pages", v_pages),
-                ("block_table", block_table), ("lens", lens), ("seq_start", seq_start), ("positions", positions),
-                ("inv_freq", inv_freq)))
+    if k.dim() != 3 or v.shape != k.shape or v.dtype is not dtype:
+        raise ValueError(f"k and v must be {dtype} [tokens, heads, 64], got {tuple(k.shape)} and {v.dtype} {tuple(v.shape)}")
     n, kv, hd = k.shape
+    dev = k.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise _elsewhere(_current_device(), (("k", k),))
+    H = qp = qo = qs = qos = 0
+    if q is not None:
+        if q.dtype is not dtype:
+            raise TypeError(f"q must be {dtype}, got {q.dtype}")
+        if q.dim() != 3 or q.shape[0] != n or q.shape[2] != hd:
+            raise ValueError(f"q must be [{n}, heads, {hd}], got {tuple(q.shape)}")
+        if q_out is None:
+            q_out = torch.zeros(q.shape, dtype=dtype, device=q.device)
+        elif q_out.dtype is not dtype or q_out.shape != q.shape:
+            raise ValueError(f"q_out must be {dtype} {tuple(q.shape)}, got {q_out.dtype} {tuple(q_out.shape)}")
+        H, qp, qo = q.shape[1], q.data_ptr(), q_out.data_ptr()
+        qs, qos = _token_stride(q, "q"), _token_stride(q_out, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out goes with q")
     n_seqs = lens.shape[0]
+    pages, size, kps, vps = _pool(k_pages, v_pages, dtype, kv)
+    tab, tab_stride, max_pages = _table(block_table, n_seqs)
+    own = _ints(lens, "lens", (n_seqs,))
+    start = 0 if seq_start is None else _ints(seq_start, "seq_start", (n_seqs + 1,))
+    pos = 0 if positions is None else _ints(positions, "positions", (n,))
+    freq = rot = 0
+    if inv_freq is not None:
+        if inv_freq.dtype is not torch.float32:
+            raise TypeError(f"inv_freq must be torch.float32, got {inv_freq.dtype}")
+        if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError(f"inv_freq must be contiguous [rot_dim / 2], got {tuple(inv_freq.shape)}")
+        freq, rot = inv_freq.data_ptr(), 2 * inv_freq.shape[0]
+    for x in (v, q, q_out, k_pages, v_pages, block_table, lens, seq_start, positions, inv_freq):
+        if x is not None and x.get_device() != dev:
+            raise _elsewhere(dev, (("v", v), ("q", q), ("q_out", q_out), ("k_pages", k_pages), ("v_pages", v_pages),
+                                   ("block_table", block_table), ("lens", lens), ("seq_start", seq_start),
+                                   ("positions", positions), ("inv_freq", inv_freq)))
     if n == 0:
         return q_out
-    a = KvAppendArgs()
-    a.dtype, a.n_tokens, a.n_seqs, a.n_kv_heads, a.head_dim = dt, n, n_seqs, kv, hd
-    a.k, a.v, a.k_stride, a.v_stride = k.data_ptr(), v.data_ptr(), _token_stride(k, "k"), _token_stride(v, "v")
-    if q is not None:
-        a.n_heads, a.q, a.q_out = q.shape[1], q.data_ptr(), q_out.data_ptr()
-        a.q_stride, a.q_out_stride = _token_stride(q, "q"), _token_stride(q_out, "q_out")
-    a.n_pages, a.page_size, a.k_page_stride, a.v_page_stride = _pool(k_pages, v_pages, k.dtype, kv)
-    a.block_table_stride = _table(block_table, n_seqs)
-    a.max_pages = block_table.shape[1]
-    _ints(lens, "lens", (n_seqs,))
-    _ints(seq_start, "seq_start", (n_seqs + 1,))
-    _ints(positions, "positions", (n,))
-    a.k_pages, a.v_pages = k_pages.data_ptr(), v_pages.data_ptr()
-    a.block_table, a.lens = block_table.data_ptr(), lens.data_ptr()
-    if seq_start is not None:
-        a.seq_start = seq_start.data_ptr()
-    if positions is not None:
-        a.positions = positions.data_ptr()
-    if inv_freq is not None:
-        _require(inv_freq, torch.float32, "inv_freq")
-        if inv_freq.dim() != 1:
-            raise ValueError(f"inv_freq must be [rot_dim / 2], got {tuple(inv_freq.shape)}")
-        a.inv_freq, a.rot_dim, a.interleaved = inv_freq.data_ptr(), 2 * inv_freq.shape[0], int(interleaved)
-    _check(lib().wenc_kv_append(a, _stream(stream)))
+    status = (_lib or lib()).wenc_kv_append(
+        _APPEND_PACK.pack(dt, n, n_seqs, H, kv, hd, qp, qo, k.data_ptr(), v.data_ptr(), qs, qos, _token_stride(k, "k"),
+                          _token_stride(v, "v"), k_pages.data_ptr(), v_pages.data_ptr(), kps, vps, pages, size, tab,
+                          tab_stride, max_pages, own, start, pos, freq, rot, 1 if interleaved else 0),
+        _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return q_out
 
 
@@ -662,19 +705,27 @@ def quantize_rows(x, out=None, scale=None, stream=None):
     wenc_quantize_rows)."""
     import torch
     dt = _dtype_code(x, "x")
-    _require(x, x.dtype, "x")
-    d = x.shape[-1]
+    shape = x.shape
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    dev = x.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise _elsewhere(_current_device(), (("x", x),))
+    d = shape[-1]
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        out = torch.empty(shape, dtype=torch.int8, device=x.device)
+    elif out.dtype is not torch.int8 or out.shape != shape or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous int8 {tuple(shape)}, got {out.dtype} {tuple(out.shape)}")
     if scale is None:
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    _require(out, torch.int8, "out")
-    _require(scale, torch.float32, "scale")
-    if out.shape != x.shape or scale.shape != x.shape[:-1]:
-        raise ValueError(f"out must be {tuple(x.shape)} and scale {tuple(x.shape[:-1])}")
-    _on_device((("x", x), ("out", out), ("scale", scale)))
-    _check(lib().wenc_quantize_rows(_ptr(x), dt, _ptr(out), _ptr(scale), x.numel() // d if d else 0, d,
-                                    _stream(stream)))
+        scale = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+    elif scale.dtype is not torch.float32 or scale.shape != shape[:-1] or not scale.is_contiguous():
+        raise ValueError(f"scale must be contiguous float32 {tuple(shape[:-1])}, got {scale.dtype} {tuple(scale.shape)}")
+    if out.get_device() != dev or scale.get_device() != dev:
+        raise _elsewhere(dev, (("out", out), ("scale", scale)))
+    status = (_lib or lib()).wenc_quantize_rows(x.data_ptr(), dt, out.data_ptr(), scale.data_ptr(),
+                                                x.numel() // d if d else 0, d, _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return out, scale
 
 
@@ -682,34 +733,50 @@ def linear_i8(a, a_scale, w, w_scale, bias, epilogue: int = EPI_BIAS_BF16, resid
               stream=None):
     """out = epilogue((a w^T) * a_scale[:, None] * w_scale + bias) on 8-bit integers: a int8 [M, K]
     with float32 scales [M] (``quantize_rows``), w int8 [N, K] with float32 scales [N]; epilogues
-    and outputs as ``linear``."""
+    and outputs as ``linear``. ``workspace``: a uint8 tensor to use instead of an allocation where
+    one is needed."""
     import torch
-    for name, t, want in (("a", a, torch.int8), ("w", w, torch.int8), ("a_scale", a_scale, torch.float32),
-                          ("w_scale", w_scale, torch.float32), ("bias", bias, torch.float32)):
-        _require(t, want, name)
+    dev = a.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise _elsewhere(_current_device(), (("a", a),))
+    i8, f32 = torch.int8, torch.float32
+    if a.dtype is not i8 or w.dtype is not i8:
+        raise TypeError(f"a and w must be torch.int8, got {a.dtype} and {w.dtype}")
+    if a_scale.dtype is not f32 or w_scale.dtype is not f32 or bias.dtype is not f32:
+        raise TypeError("a_scale, w_scale and bias must be torch.float32")
     if a.dim() != 2 or w.dim() != 2 or a.shape[1] != w.shape[1]:
         raise ValueError(f"a {tuple(a.shape)} and w {tuple(w.shape)} must be [M, K] and [N, K]")
     M, K = a.shape
     N = w.shape[0]
     if a_scale.numel() != M or w_scale.numel() != N or bias.numel() != N:
         raise ValueError(f"a_scale must hold {M} scales, w_scale and bias {N}")
-    dt = torch.float32 if epilogue == EPI_BIAS_RESID_F32 else torch.bfloat16
+    dt = f32 if epilogue == EPI_BIAS_RESID_F32 else torch.bfloat16
     if out is None:
         out = torch.empty((M, N), dtype=dt, device=a.device)
-    _require(out, dt, "out")
-    if resid is not None:
-        _require(resid, torch.float32, "resid")
-    if tuple(out.shape) != (M, N) or resid is not None and tuple(resid.shape) != (M, N):
-        raise ValueError(f"out and resid must be {(M, N)}")
-    _on_device((("a", a), ("a_scale", a_scale), ("w", w), ("w_scale", w_scale), ("bias", bias), ("resid", resid),
-                ("out", out), ("workspace", workspace)))
-    L = lib()
+    elif out.dtype is not dt or out.shape != (M, N):
+        raise ValueError(f"out must be {dt} {(M, N)}, got {out.dtype} {tuple(out.shape)}")
+    if resid is not None and (resid.dtype is not f32 or resid.shape != (M, N)):
+        raise ValueError(f"resid must be float32 {(M, N)}, got {resid.dtype} {tuple(resid.shape)}")
+    for x in (a, a_scale, w, w_scale, bias, out, resid):
+        if x is None:
+            continue
+        if not x.is_contiguous():
+            raise ValueError("linear_i8 takes contiguous tensors")
+        if x.get_device() != dev:
+            raise _elsewhere(dev, (("a_scale", a_scale), ("w", w), ("w_scale", w_scale), ("bias", bias), ("out", out),
+                                   ("resid", resid)))
+    L = _lib or lib()
     if workspace is None:
-        workspace = _scratch(L.wenc_linear_i8_workspace(M, N, K), a, stream)
-    _check(L.wenc_linear_i8(_ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(resid), _ptr(out), M, N,
-                            K, epilogue, _ptr(workspace),
-                            0 if workspace is None else workspace.numel() * workspace.element_size(),
-                            _stream(stream)))
+        need = L.wenc_linear_i8_workspace(M, N, K)
+        workspace = _scratch(need, a, stream) if need else None
+    elif workspace.get_device() != dev:
+        raise _elsewhere(dev, (("workspace", workspace),))
+    ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    status = L.wenc_linear_i8(a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), bias.data_ptr(),
+                              0 if resid is None else resid.data_ptr(), out.data_ptr(), M, N, K, epilogue, ws, ws_bytes,
+                              _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return out
 
 
