@@ -9,25 +9,27 @@
 // CrossLayer::attend and attention_masked).
 //
 // Rows of one key head: (sequence of the group, token, query head of the key head), so the prefix is read
-// once for all of a group. What bounds it: bytes of K and V for a few rows (a decode step), the tensor
-// pipe for hundreds. Hence two forms:
+// once for all of a group's rows. What bounds it: bytes of K and V, and at these sizes the latency of
+// getting at them.
 //
 // Up to 64 rows per key head (beams): one launch. A cluster of 1 to 8 CTAs attends one (group, key
-// head): its key list is the prefix followed by the own keys of each sequence of the group, cut into
-// tiles that belong to one of these segments each, and every CTA takes an equal run of tiles. Own keys
-// are scored against all the item's rows (the MMA is 16 rows high whether one or 16 are wanted) and
-// masked to their sequence's. The CTAs' results (m, l, O) are joined through distributed shared memory:
-// no workspace and no second kernel.
+// head, tile of rows): its key list is the prefix followed by the own keys of each sequence of the tile,
+// cut into tiles of keys that belong to one of these segments each, and every CTA takes an equal run of
+// them. Own keys are scored against all of the tile's rows and masked to their sequence's. The CTAs'
+// results (m, l, O) are joined through distributed shared memory: no workspace and no second kernel.
 // More rows: a work item is a share of a group's prefix, or of one sequence's own keys; items write
 // partial results to the workspace and a second kernel joins them.
 //
-// Inside a CTA, up to 16 rows: the four warps split the keys of each tile, each warp with its own ring
-// of cp.async stages, no barrier between them, joined once at the end. More rows: the warps split the
-// rows (16 each) and share the tiles.
-// Scores use mma.sync (m16n8k16 bf16, m16n8k8 TF32): 16 rows is its height, where a tcgen05 tile
-// would be 64 or 128 rows high and mostly empty.
-// bf16: P is split into two bf16 parts before P V, so its rounding (2^-16 after the split) does not
-// add to the output's own. fp32: every product is three TF32 products of two-part operands.
+// Inside a CTA every warp takes 16 keys of each tile, through a ring of cp.async stages of its own, with
+// no barrier between warps until their results are joined at the end. The products are transposed:
+// S^T = K Q^T and O^T = V^T P^T, with 16 keys (or 16 elements of V) as the MMA's M and 8 query rows as its
+// N, so that five beams cost eight columns instead of sixteen rows, and the fragments of K and V
+// are loaded once for any number of rows. The running maximum is followed lazily: P keeps its reference
+// until a score exceeds it by 2^8, so most tiles need no reduction over lanes and no rescaling.
+// mma.sync (m16n8k16 bf16, m16n8k8 TF32): a tcgen05 tile would be 64 or 128 rows and mostly empty.
+// bf16: P is split into two bf16 parts before the product with V, so its rounding (2^-16 after the
+// split) does not add to the output's own. fp32: every product is three TF32 products of two-part
+// operands.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -51,7 +53,6 @@ namespace {
 using namespace wenc_dev;
 
 constexpr int HD = 64;
-constexpr int kThreads = 128;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
   const int n = there ? 16 : 0;  // 0 source bytes: the 16 are filled with zeros
@@ -92,10 +93,16 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // x = hi + lo with both parts TF32 (11 significant bits each, nearest, ties away): the parts
-// miss x by at most 2^-24 |x|.
+// miss x by at most 2^-24 |x|. The MMA ignores the 13 low bits of a TF32 operand, so lo keeps them.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
   hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-  lo = (__float_as_uint(x - __uint_as_float(hi)) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+}
+// Transpose of an 8 x 8 matrix of 16-bit elements (lane: row lane / 4, columns 2 (lane % 4) and the next).
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 struct PrefixParams {
@@ -110,7 +117,7 @@ struct PrefixParams {
   long long table_stride;
   int n_seqs, q_len, H, Hkv, r, n_groups, max_group, prefix_max, n_pages, page_size, page_shift, max_pages;
   int np, ns;                    // prefix and own-key splits of the two-launch form (0: no such keys)
-  int row_tiles;                 // row tiles per item of this launch (two-launch form)
+  int row_tiles;                 // row tiles per item of this launch
   int cluster;                   // CTAs per item (one-launch form)
   float scale_log2;              // >= 0
   uint32_t q_flip, q_keep;       // a negative scale turns the queries' signs (per 32 bits), a zero one clears them
@@ -118,91 +125,95 @@ struct PrefixParams {
   float2* part_ml;               // the same without [64]: (maximum in log2 units, sum)
 };
 
-// WR warps along the rows, WK along the keys of a tile.
-template <typename T, int WR>
+// NR groups of 8 query rows per CTA.
+template <typename T, int NR>
 struct Cfg {
   static constexpr bool F32 = sizeof(T) == 4;
-  static constexpr int WK = 4 / WR;
-  static constexpr int KW = (F32 ? 16 : 32) * (WR == 4 ? 2 : 1);  // keys of a tile one warp scores
-  static constexpr int KT = KW * WK;                              // keys per tile
+  static constexpr int NW = F32 ? 4 : 8;       // warps
+  static constexpr int THREADS = 32 * NW;
+  static constexpr int KW = 16;                // keys of a tile one warp scores
+  static constexpr int KT = KW * NW;           // keys per tile
+  static constexpr int ROWS = 8 * NR;
   static constexpr int ROWB = HD * sizeof(T);
-  static constexpr int STAGES = WR == 4 ? 4 : 3;
-  static constexpr uint32_t HALF = KT * ROWB;  // bytes of K (or V) per stage
-  static constexpr uint32_t STAGE = 2 * HALF;
-  static constexpr uint32_t SMEM = STAGES * STAGE;
-  static_assert(SMEM >= 4u * 16 * HD * 4 + 4 * 16 * 8, "the ring also holds the warps' results");
+  static constexpr int STAGES = 2;
+  static constexpr uint32_t HALF = KW * ROWB;  // bytes of K (or V) per warp and stage
+  static constexpr uint32_t RING = NW * STAGES * 2 * HALF;
+  static constexpr uint32_t P_BYTES = F32 ? NW * NR * 16 * 8 * 4 : 0;  // fp32: P on its way to B fragments
+  // results over the ring: O [NW][ROWS][OS] floats, (m, l) [NW][ROWS]
+  static constexpr int OS = HD + 4;
+  static constexpr uint32_t ML = NW * ROWS * OS * 4;
+  static constexpr uint32_t RESULTS = ML + NW * ROWS * 8;
+  static constexpr uint32_t SMEM = (RING + P_BYTES > RESULTS ? RING + P_BYTES : RESULTS);
 };
 
-// What one CTA attends: rows [row0, row0 + 16 WR) of the n_rows of one key head, against its run of the
-// tiles of a list of segments: segment 0 is the prefix, segment i the own keys of sequence i - 1 of the
-// item, which only that sequence's rows see.
+// What one CTA attends: rows [row0, row0 + n_rows) of one key head of a group, against its run of the
+// tiles of a list of segments: segment 0 is the prefix, segment i the own keys of sequence seq0 + i - 1,
+// which only that sequence's rows see.
 struct Item {
   const uint8_t *kp, *vp;   // first prefix key of the key head
   int prefix_len;
-  int seq0, n_own;          // first sequence, and how many bring own keys (0: none do)
-  int row0, n_rows;
-  int token0, hk;           // row x is token token0 + x / r, query head hk r + x % r
+  int seq0, n_own;          // first sequence of the rows, and how many bring own keys (0: none do)
+  int row_off;              // row x of the tile is row row_off + x of sequence seq0's first row on
+  int n_rows;
+  int hk;
   int split, n_splits;
 };
 
-constexpr int kMaxOwn = 64;  // own-key segments of an item: at most one per row of a 64-row tile
+constexpr int kMaxOwn = 32;  // own-key segments of an item: at most one per row of a tile
 struct SegTable {
   int tile0[kMaxOwn + 2];    // first tile of each segment, and the end
   int len[kMaxOwn + 1];      // its keys
 };
 
-// 16-byte granule `c` of key row `row` within a tile. bf16 rows have 8 granules (all 32 banks), fp32
-// rows 16; the XOR spreads the rows an ldmatrix (or the quads of a fragment load) touches at once
-// over all banks.
+// 16-byte granule `c` of key row `row` within a warp's stage. bf16 rows have 8 granules (all 32 banks),
+// fp32 rows 16; the XOR spreads the rows that an ldmatrix (or a quarter of a fragment load) touches at
+// once over all banks.
 template <bool F32>
 __device__ __forceinline__ uint32_t granule(int row, int c) {
   if constexpr (F32)
-    return row * 256u + ((c ^ ((((row >> 1) & 3) << 1) ^ ((row & 1) << 2))) << 4);
+    return row * 256u + ((c ^ (((row & 1) << 2) | (row & 2))) << 4);
   else
     return row * 128u + ((c ^ (row & 7)) << 4);
 }
 
-// One CTA's share: leaves O (unnormalised) in shared memory as [16 WR][64] floats and (m, l) per row
-// behind it at kMlOffset, m in log2 units. All threads return after a barrier.
-constexpr uint32_t kMlOffset = 4 * 16 * HD * 4;
-
-template <typename T, int WR>
+// One CTA's share. Leaves every warp's O (unnormalised) and (m, l) (m in log2 units) in shared memory
+// and returns after a barrier.
+template <typename T, int NR>
 __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, uint8_t* smem, SegTable& seg, uint32_t* err) {
-  using C = Cfg<T, WR>;
+  using C = Cfg<T, NR>;
   constexpr bool F32 = C::F32;
-  constexpr int WK = C::WK, KW = C::KW, KT = C::KT, ST = C::STAGES;
+  constexpr int KW = C::KW, KT = C::KT, ST = C::STAGES;
   constexpr int CH = C::ROWB / 16;  // granules per row
+  constexpr int RPI = 32 / CH;      // rows a warp's copy instruction covers
+  constexpr int NL = KW / RPI;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wr = WR == 4 ? warp : 0, wk = WK == 4 ? warp : 0;
   const int g = lane >> 2, tq = lane & 3;
-  const uint32_t s0 = smem_u32(smem);
+  const uint32_t s0 = smem_u32(smem) + warp * (ST * 2 * C::HALF);
 
-  // ---- the segments' tiles: a running sum over up to 65 lengths, by warp 0
+  // ---- the segments' tiles: a running sum over up to 33 lengths, by warp 0
   if (warp == 0) {
-    int base = (it.prefix_len + KT - 1) / KT;
-    if (lane == 0) {
-      seg.tile0[0] = 0;
-      seg.len[0] = it.prefix_len;
-      seg.tile0[1] = base;
+    const int base = (it.prefix_len + KT - 1) / KT;
+    int n = lane < it.n_own ? p.lens[it.seq0 + lane] : 0;
+    if (n < 0 || n > static_cast<long long>(p.max_pages) * p.page_size) {
+      *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (81u << 8);
+      n = 0;
     }
-    for (int i0 = 0; i0 < it.n_own; i0 += 32) {
-      const int i = i0 + lane;
-      int n = i < it.n_own ? p.lens[it.seq0 + i] : 0;
-      if (n < 0 || n > static_cast<long long>(p.max_pages) * p.page_size) {
-        *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (81u << 8);
-        n = 0;
-      }
-      int sum = (n + KT - 1) / KT;
+    int sum = (n + KT - 1) / KT;
+    if (it.n_own > 1) {
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int up = __shfl_up_sync(0xffffffffu, sum, d);
         if (lane >= d) sum += up;
       }
-      if (i < it.n_own) {
-        seg.len[1 + i] = n;
-        seg.tile0[2 + i] = base + sum;
-      }
-      base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) {
+      seg.tile0[0] = 0;
+      seg.len[0] = it.prefix_len;
+      seg.tile0[1] = base;
+    }
+    if (lane < it.n_own) {
+      seg.len[1 + lane] = n;
+      seg.tile0[2 + lane] = base + sum;
     }
   }
   __syncthreads();
@@ -211,314 +222,340 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
   const int tile0 = it.split * per;
   const int n_mine = max(0, min(per, n_tiles - tile0));
 
-  // ---- tile loads: a warp of the key-split form loads the keys it scores itself; else the CTA
-  constexpr int LOADERS = WK == 4 ? 32 : kThreads;
-  constexpr int LROWS = WK == 4 ? KW : KT;
-  constexpr int NL = LROWS * CH / LOADERS;
-  const int lt = WK == 4 ? lane : threadIdx.x;
-  const int lc = lt % CH, lr = (WK == 4 ? wk * KW : 0) + lt / CH;
-  int lseg = 0;  // segment of the next tile to load
-  auto load = [&](int j, int stage) {
+  // ---- tile loads: every warp copies the keys it scores itself
+  const int lc = lane % CH, lr = lane / CH;
+  int lseg = 0;       // segment of the next tile to load
+  int next_page = 0;  // its page of the key in row lane % 16 (own keys), read one tile ahead
+  auto page_of = [&](int j) {  // moves lseg to tile j's
     while (tile0 + j >= seg.tile0[lseg + 1]) ++lseg;
-    const uint32_t sk = s0 + stage * C::STAGE, sv = sk + C::HALF;
-    const int key0 = (tile0 + j - seg.tile0[lseg]) * KT, n_keys = seg.len[lseg];
+    if (lseg == 0) return;
+    const int key = (tile0 + j - seg.tile0[lseg]) * KT + warp * KW + (lane & 15);
+    const int pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+    next_page = key < seg.len[lseg] ? p.table[(it.seq0 + lseg - 1) * p.table_stride + pi] : -1;
+  };
+  auto load = [&](int j, int stage) {
+    const uint32_t sk = s0 + stage * (2 * C::HALF), sv = sk + C::HALF;
+    const int key0 = (tile0 + j - seg.tile0[lseg]) * KT + warp * KW, n_keys = seg.len[lseg];
     if (lseg == 0) {
       const uint8_t* ks = it.kp + (key0 + lr) * p.k_token + lc * 16;
       const uint8_t* vs = it.vp + (key0 + lr) * p.v_token + lc * 16;
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        const int row = lr + i * (LOADERS / CH);
+        const int row = lr + i * RPI;
         const bool ok = key0 + row < n_keys;
         cp_async16(sk + granule<F32>(row, lc), ok ? ks : it.kp, ok);
         cp_async16(sv + granule<F32>(row, lc), ok ? vs : it.vp, ok);
-        ks += (LOADERS / CH) * p.k_token;
-        vs += (LOADERS / CH) * p.v_token;
+        ks += RPI * p.k_token;
+        vs += RPI * p.v_token;
       }
     } else {
-      const int32_t* table = p.table + (it.seq0 + lseg - 1) * p.table_stride;
-      int page[NL], slot[NL];
+      const int key = key0 + (lane & 15);
+      const int pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+      const int slot = key - pi * p.page_size;
+      const bool in = next_page >= 0 && next_page < p.n_pages;
+      if (!in && key < n_keys) *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (80u << 8);
+      const int page = in ? next_page : -1;
+      const int head = it.hk * C::ROWB + lc * 16;
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        const int key = key0 + lr + i * (LOADERS / CH);
-        const int pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-        slot[i] = key - pi * p.page_size;
-        page[i] = key < n_keys ? table[pi] : -1;
-      }
-#pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const int row = lr + i * (LOADERS / CH);
-        const bool ok = page[i] >= 0 && page[i] < p.n_pages;
-        if (!ok && key0 + row < n_keys) *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (80u << 8);
-        const long long at = slot[i] * p.page_row + it.hk * C::ROWB + lc * 16;
-        cp_async16(sk + granule<F32>(row, lc), ok ? p.k_pages + page[i] * p.k_page + at : p.k_pages, ok);
-        cp_async16(sv + granule<F32>(row, lc), ok ? p.v_pages + page[i] * p.v_page + at : p.v_pages, ok);
+        const int row = lr + i * RPI;
+        const int pg = __shfl_sync(0xffffffffu, page, row), sl = __shfl_sync(0xffffffffu, slot, row);
+        const bool ok = pg >= 0;
+        const long long at = sl * p.page_row + head;
+        cp_async16(sk + granule<F32>(row, lc), ok ? p.k_pages + pg * p.k_page + at : p.k_pages, ok);
+        cp_async16(sv + granule<F32>(row, lc), ok ? p.v_pages + pg * p.v_page + at : p.v_pages, ok);
       }
     }
   };
+  if (n_mine > 0) page_of(0);
 #pragma unroll
   for (int j = 0; j < ST - 1; ++j) {
-    if (j < n_mine) load(j, j);
+    if (j < n_mine) {
+      load(j, j);
+      if (j + 1 < n_mine) page_of(j + 1);
+    }
     cp_async_commit();
   }
 
-  // ---- the warp's 16 query rows as A fragments; rows past the end are zeros
-  const int ra = it.row0 + wr * 16 + g, rb = ra + 8;
-  auto q_row = [&](int x) {
-    const int tok = x / p.r;
-    return p.q + static_cast<long long>(it.token0 + tok) * p.q_stride + (it.hk * p.r + x - tok * p.r) * C::ROWB;
-  };
+  // ---- the query rows as B fragments (column g of group r: row 8 r + g); rows past the end are zeros
   constexpr int KS = F32 ? 8 : 4;  // k steps of one score product
-  uint32_t qa[KS][4], ql[F32 ? KS : 1][4];
-  {
-    const uint8_t *pa = ra < it.n_rows ? q_row(ra) : nullptr, *pb = rb < it.n_rows ? q_row(rb) : nullptr;
+  uint32_t qh[NR][KS][2], ql[F32 ? NR : 1][KS][2];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    const int x = it.row_off + 8 * r + g;
+    const int tok = x / p.r;
+    const bool in = 8 * r + g < it.n_rows;
+    const uint8_t* q = p.q + (static_cast<long long>(it.seq0) * p.q_len + tok) * p.q_stride + (it.hk * p.r + x - tok * p.r) * C::ROWB;
     if constexpr (F32) {
-      // k index tq (and tq + 4) of step 2j (and 2j + 1) stands for element 4 (tq + 4j) + {0, 1} ({2, 3})
+      // k index tq (and tq + 4) of step 2j (and 2j + 1) stands for element 4 (tq + 4j) + 0, 1 (2, 3)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-        uint4 a = pa ? *reinterpret_cast<const uint4*>(pa + (tq + 4 * j) * 16) : z;
-        uint4 b = pb ? *reinterpret_cast<const uint4*>(pb + (tq + 4 * j) * 16) : z;
-        auto part = [&](uint32_t x, uint32_t& hi, uint32_t& lo) {
-          split_tf32(__uint_as_float((x & p.q_keep) ^ p.q_flip), hi, lo);
+        const uint4 a = in ? *reinterpret_cast<const uint4*>(q + (tq + 4 * j) * 16) : make_uint4(0u, 0u, 0u, 0u);
+        auto part = [&](uint32_t v, uint32_t& hi, uint32_t& lo) {
+          split_tf32(__uint_as_float((v & p.q_keep) ^ p.q_flip), hi, lo);
         };
-        part(a.x, qa[2 * j][0], ql[2 * j][0]);
-        part(b.x, qa[2 * j][1], ql[2 * j][1]);
-        part(a.y, qa[2 * j][2], ql[2 * j][2]);
-        part(b.y, qa[2 * j][3], ql[2 * j][3]);
-        part(a.z, qa[2 * j + 1][0], ql[2 * j + 1][0]);
-        part(b.z, qa[2 * j + 1][1], ql[2 * j + 1][1]);
-        part(a.w, qa[2 * j + 1][2], ql[2 * j + 1][2]);
-        part(b.w, qa[2 * j + 1][3], ql[2 * j + 1][3]);
+        part(a.x, qh[r][2 * j][0], ql[r][2 * j][0]);
+        part(a.y, qh[r][2 * j][1], ql[r][2 * j][1]);
+        part(a.z, qh[r][2 * j + 1][0], ql[r][2 * j + 1][0]);
+        part(a.w, qh[r][2 * j + 1][1], ql[r][2 * j + 1][1]);
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const int e = (16 * k + 2 * tq) * 2;
-        auto part = [&](const uint8_t* x) { return x ? (*reinterpret_cast<const uint32_t*>(x) & p.q_keep) ^ p.q_flip : 0u; };
-        qa[k][0] = part(pa ? pa + e : nullptr);
-        qa[k][1] = part(pb ? pb + e : nullptr);
-        qa[k][2] = part(pa ? pa + e + 16 : nullptr);
-        qa[k][3] = part(pb ? pb + e + 16 : nullptr);
-      }
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          qh[r][k][h] = in ? (*reinterpret_cast<const uint32_t*>(q + (16 * k + 8 * h + 2 * tq) * 2) & p.q_keep) ^ p.q_flip : 0u;
     }
   }
-  // sequence of the item and token of this thread's two rows
+  // this thread's columns of S^T and O^T: rows 8 r + 2 tq + e; their sequence and token
   const int per_seq = p.q_len * p.r;
-  const int sa = ra / per_seq, sb = rb / per_seq;
-  const int ta = (ra - sa * per_seq) / p.r, tb = (rb - sb * per_seq) / p.r;
-  const int row_first = it.row0 + wr * 16, row_end = min(row_first + 16, it.n_rows);  // warp-uniform
+  int seq_of[NR][2], tok_of[NR][2];
+#pragma unroll
+  for (int r = 0; r < NR; ++r)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int x = it.row_off + 8 * r + 2 * tq + e;
+      seq_of[r][e] = x / per_seq;
+      tok_of[r][e] = (x - seq_of[r][e] * per_seq) / p.r;
+    }
 
-  float o[8][4];
+  float o[NR][4][4], m[NR][2], u[NR][2], l[NR][2];  // u: the reference in use, 0 while m is -inf
 #pragma unroll
-  for (int n = 0; n < 8; ++n)
+  for (int r = 0; r < NR; ++r) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
-  float ma = -CUDART_INF_F, mb = -CUDART_INF_F, la = 0.0f, lb = 0.0f;
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[r][i][e] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m[r][e] = -CUDART_INF_F;
+      u[r][e] = l[r][e] = 0.0f;
+    }
+  }
   const float sc = p.scale_log2;
 
   int cseg = 0;
   for (int j = 0; j < n_mine; ++j) {
     cp_async_wait<ST - 2>();
-    if constexpr (WK == 4) __syncwarp();
-    else __syncthreads();
-    if (j + ST - 1 < n_mine) load(j + ST - 1, (j + ST - 1) % ST);
+    __syncwarp();
+    if (j + ST - 1 < n_mine) {
+      load(j + ST - 1, (j + ST - 1) % ST);
+      if (j + ST < n_mine) page_of(j + ST);
+    }
     cp_async_commit();
     while (tile0 + j >= seg.tile0[cseg + 1]) ++cseg;
-    const int kb = wk * KW;  // first key of the tile this warp scores
-    const int key0 = (tile0 + j - seg.tile0[cseg]) * KT + kb, n_keys = seg.len[cseg];
-    // nothing to score: no rows, no keys, or own keys of a sequence none of the warp's rows belong to
-    if (row_first >= row_end || key0 >= n_keys) continue;
-    if (cseg > 0 && (row_end <= (cseg - 1) * per_seq || row_first >= cseg * per_seq)) continue;
-    const uint32_t sk = s0 + (j % ST) * C::STAGE, sv = sk + C::HALF;
+    const int key0 = (tile0 + j - seg.tile0[cseg]) * KT + warp * KW, n_keys = seg.len[cseg];
+    if (key0 >= n_keys) continue;
+    const uint32_t sk = s0 + (j % ST) * (2 * C::HALF), sv = sk + C::HALF;
 
-    // ---- scores of 16 rows x KW keys
-    float s[KW / 8][4];
+    // ---- S^T: 16 keys x 8 NR rows
+    float s[NR][4];
 #pragma unroll
-    for (int n = 0; n < KW / 8; ++n) {
+    for (int r = 0; r < NR; ++r)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
-      if constexpr (F32) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float4 kv = lds_f4(sk + granule<true>(kb + 8 * n + g, tq + 4 * c));
-          uint32_t h0, h1, h2, h3, l0, l1, l2, l3;
-          split_tf32(kv.x, h0, l0);
-          split_tf32(kv.y, h1, l1);
-          split_tf32(kv.z, h2, l2);
-          split_tf32(kv.w, h3, l3);
-          mma_tf32(s[n], ql[2 * c], h0, h1);
-          mma_tf32(s[n], qa[2 * c], l0, l1);
-          mma_tf32(s[n], qa[2 * c], h0, h1);
-          mma_tf32(s[n], ql[2 * c + 1], h2, h3);
-          mma_tf32(s[n], qa[2 * c + 1], l2, l3);
-          mma_tf32(s[n], qa[2 * c + 1], h2, h3);
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {  // 32 elements of d at a time
-          uint32_t b[4];
-          ldsm_x4(b, sk + granule<false>(kb + 8 * n + (lane & 7), 4 * c + (lane >> 3)));
-          mma_bf16(s[n], qa[2 * c], b[0], b[1]);
-          mma_bf16(s[n], qa[2 * c + 1], b[2], b[3]);
-        }
-      }
-    }
-    // ---- mask, running maximum and sum (log2 units)
-    int lim_a = n_keys, lim_b = n_keys;  // keys of this segment each of this thread's rows sees
-    if (cseg > 0) {
-      lim_a = sa == cseg - 1 ? n_keys - p.q_len + 1 + ta : 0;
-      lim_b = sb == cseg - 1 ? n_keys - p.q_len + 1 + tb : 0;
-    }
-    if (cseg > 0 || key0 + KW > n_keys) {
-#pragma unroll
-      for (int n = 0; n < KW / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (key0 + 8 * n + 2 * tq + (e & 1) >= (e < 2 ? lim_a : lim_b)) s[n][e] = -CUDART_INF_F;
-    }
-    float xa = -CUDART_INF_F, xb = -CUDART_INF_F;
-#pragma unroll
-    for (int n = 0; n < KW / 8; ++n) {
-      xa = fmax3(xa, s[n][0], s[n][1]);
-      xb = fmax3(xb, s[n][2], s[n][3]);
-    }
-    xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 1));
-    xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 1));
-    xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2));
-    xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2));
-    xa = fmaxf(xa * sc, ma);
-    xb = fmaxf(xb * sc, mb);
-    const float ua = xa == -CUDART_INF_F ? 0.0f : xa, ub = xb == -CUDART_INF_F ? 0.0f : xb;
-    const float fa = ex2_approx(ma - ua), fb = ex2_approx(mb - ub);
-    ma = xa;
-    mb = xb;
-    la *= fa;
-    lb *= fb;
-#pragma unroll
-    for (int n = 0; n < KW / 8; ++n) {
-      s[n][0] = ex2_approx(fmaf(s[n][0], sc, -ua));
-      s[n][1] = ex2_approx(fmaf(s[n][1], sc, -ua));
-      s[n][2] = ex2_approx(fmaf(s[n][2], sc, -ub));
-      s[n][3] = ex2_approx(fmaf(s[n][3], sc, -ub));
-      la += s[n][0] + s[n][1];
-      lb += s[n][2] + s[n][3];
-    }
-    // ---- O += P V. fp32: the tile's product is formed on its own and added in one rounding, so that the
-    // tensor core's accumulation (which truncates) runs over one tile only
-    float t[F32 ? 8 : 1][4];
+      for (int e = 0; e < 4; ++e) s[r][e] = 0.0f;
     if constexpr (F32) {
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
+      for (int c = 0; c < 4; ++c) {
+        const float4 ka = lds_f4(sk + granule<true>(g, tq + 4 * c)), kb = lds_f4(sk + granule<true>(g + 8, tq + 4 * c));
+        uint32_t h[2][4], w[2][4];
+        split_tf32(ka.x, h[0][0], w[0][0]);
+        split_tf32(kb.x, h[0][1], w[0][1]);
+        split_tf32(ka.y, h[0][2], w[0][2]);
+        split_tf32(kb.y, h[0][3], w[0][3]);
+        split_tf32(ka.z, h[1][0], w[1][0]);
+        split_tf32(kb.z, h[1][1], w[1][1]);
+        split_tf32(ka.w, h[1][2], w[1][2]);
+        split_tf32(kb.w, h[1][3], w[1][3]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) t[n][e] = 0.0f;
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            mma_tf32(s[r], h[i], ql[r][2 * c + i][0], ql[r][2 * c + i][1]);
+            mma_tf32(s[r], w[i], qh[r][2 * c + i][0], qh[r][2 * c + i][1]);
+            mma_tf32(s[r], h[i], qh[r][2 * c + i][0], qh[r][2 * c + i][1]);
+          }
+      }
     } else {
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        o[n][0] *= fa;
-        o[n][1] *= fa;
-        o[n][2] *= fb;
-        o[n][3] *= fb;
+      for (int k = 0; k < KS; ++k) {
+        uint32_t a[4];
+        ldsm_x4(a, sk + granule<false>(lane & 15, 2 * k + (lane >> 4)));
+#pragma unroll
+        for (int r = 0; r < NR; ++r) mma_bf16(s[r], a, qh[r][k][0], qh[r][k][1]);
       }
     }
+    // ---- mask (element e: key g + 8 (e / 2), row column e % 2), then P
+    if (cseg > 0 || key0 + KW > n_keys) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          int lim = n_keys;  // keys of this segment the row sees
+          if (cseg > 0) lim = seq_of[r][e & 1] == cseg - 1 ? n_keys - p.q_len + 1 + tok_of[r][e & 1] : 0;
+          if (key0 + g + 8 * (e >> 1) >= lim) s[r][e] = -CUDART_INF_F;
+        }
+    }
+    bool move = false;  // some score exceeds its row's reference by more than 2^8
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) move |= fmaxf(s[r][e], s[r][e + 2]) * sc > m[r][e] + 8.0f;
+    if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(s[r][e], s[r][e + 2]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          x = fmaxf(x * sc, m[r][e]);
+          const float ref = x == -CUDART_INF_F ? 0.0f : x;
+          const float f = ex2_approx(m[r][e] - ref);
+          m[r][e] = x;
+          u[r][e] = ref;
+          l[r][e] *= f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[r][i][e] *= f;
+            o[r][i][e + 2] *= f;
+          }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[r][e] = ex2_approx(fmaf(s[r][e], sc, -u[r][e & 1]));
+        l[r][e & 1] += s[r][e];
+      }
+    // ---- O^T += V^T P^T
     if constexpr (F32) {
-      // k index t of a step stands for key 2t, t + 4 for key 2t + 1 (where the scores already are);
-      // column index g of product n for element 4g + n % 4 + 32 (n / 4)
+      // P through shared memory: written as [key][row], read as B fragments (key tq, row g). The tile's
+      // product is formed on its own and added in one rounding, so that the tensor core's accumulation
+      // (which truncates) runs over one tile only.
+      const uint32_t sp = smem_u32(smem) + C::RING + warp * (NR * 512);
 #pragma unroll
-      for (int k = 0; k < KW / 8; ++k) {
-        uint32_t ph[4], pl[4];
-        split_tf32(s[k][0], ph[0], pl[0]);
-        split_tf32(s[k][2], ph[1], pl[1]);
-        split_tf32(s[k][1], ph[2], pl[2]);
-        split_tf32(s[k][3], ph[3], pl[3]);
+      for (int r = 0; r < NR; ++r) {
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sp + r * 512 + (g * 8 + 2 * tq) * 4), "f"(s[r][0]), "f"(s[r][1]) : "memory");
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sp + r * 512 + ((g + 8) * 8 + 2 * tq) * 4), "f"(s[r][2]), "f"(s[r][3]) : "memory");
+      }
+      __syncwarp();
+      uint32_t ph[NR][2][2], pl[NR][2][2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float4 v0 = lds_f4(sv + granule<true>(kb + 8 * k + 2 * tq, g + 8 * c));
-          const float4 v1 = lds_f4(sv + granule<true>(kb + 8 * k + 2 * tq + 1, g + 8 * c));
-          const float w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+      for (int r = 0; r < NR; ++r)
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            uint32_t h0, l0, h1, l1;
-            split_tf32(w0[n], h0, l0);
-            split_tf32(w1[n], h1, l1);
-            mma_tf32(t[4 * c + n], pl, h0, h1);
-            mma_tf32(t[4 * c + n], ph, l0, l1);
-            mma_tf32(t[4 * c + n], ph, h0, h1);
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(sp + r * 512 + ((8 * k + 4 * h + tq) * 8 + g) * 4) : "memory");
+            split_tf32(x, ph[r][k][h], pl[r][k][h]);
+          }
+      __syncwarp();
+      // row g (g + 8) of product i stands for element 4 g + i (32 + 4 g + i)
+      float t[NR][4][4];
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t[r][i][e] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float4 v0 = lds_f4(sv + granule<true>(8 * k + tq, g)), v1 = lds_f4(sv + granule<true>(8 * k + tq, g + 8));
+        const float4 v2 = lds_f4(sv + granule<true>(8 * k + tq + 4, g)), v3 = lds_f4(sv + granule<true>(8 * k + tq + 4, g + 8));
+        const float w[4][4] = {{v0.x, v1.x, v2.x, v3.x}, {v0.y, v1.y, v2.y, v3.y}, {v0.z, v1.z, v2.z, v3.z}, {v0.w, v1.w, v2.w, v3.w}};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t vh[4], vl[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split_tf32(w[i][e], vh[e], vl[e]);
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            mma_tf32(t[r][i], vh, pl[r][k][0], pl[r][k][1]);
+            mma_tf32(t[r][i], vl, ph[r][k][0], ph[r][k][1]);
+            mma_tf32(t[r][i], vh, ph[r][k][0], ph[r][k][1]);
           }
         }
       }
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        o[n][0] = fmaf(o[n][0], fa, t[n][0]);
-        o[n][1] = fmaf(o[n][1], fa, t[n][1]);
-        o[n][2] = fmaf(o[n][2], fb, t[n][2]);
-        o[n][3] = fmaf(o[n][3], fb, t[n][3]);
-      }
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[r][i][e] += t[r][i][e];
     } else {
+      uint32_t ph[NR][2], pl[NR][2];
 #pragma unroll
-      for (int k = 0; k < KW / 16; ++k) {
-        uint32_t ph[4], pl[4];
+      for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = s[2 * k + (e >> 1)][2 * (e & 1)], y = s[2 * k + (e >> 1)][2 * (e & 1) + 1];
-          ph[e] = pack_bf16x2(x, y);
-          pl[e] = pack_bf16x2(x - __uint_as_float(ph[e] << 16), y - __uint_as_float(ph[e] & 0xffff0000u));
+        for (int h = 0; h < 2; ++h) {
+          const float x = s[r][2 * h], y = s[r][2 * h + 1];
+          const uint32_t hi = pack_bf16x2(x, y);
+          const uint32_t lo = pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+          ph[r][h] = movm_t(hi);
+          pl[r][h] = movm_t(lo);
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // 16 elements of d at a time
-          uint32_t b[4];
-          ldsm_x4_t(b, sv + granule<false>(kb + 16 * k + (lane & 15), 2 * c + (lane >> 4)));
-          mma_bf16(o[2 * c], ph, b[0], b[1]);
-          mma_bf16(o[2 * c + 1], ph, b[2], b[3]);
-          mma_bf16(o[2 * c], pl, b[0], b[1]);
-          mma_bf16(o[2 * c + 1], pl, b[2], b[3]);
+      for (int i = 0; i < 4; ++i) {  // 16 elements of V at a time
+        uint32_t a[4];
+        ldsm_x4_t(a, sv + granule<false>((lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)));
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          mma_bf16(o[r][i], a, ph[r][0], ph[r][1]);
+          mma_bf16(o[r][i], a, pl[r][0], pl[r][1]);
         }
       }
     }
   }
-  la += __shfl_xor_sync(0xffffffffu, la, 1);
-  lb += __shfl_xor_sync(0xffffffffu, lb, 1);
-  la += __shfl_xor_sync(0xffffffffu, la, 2);
-  lb += __shfl_xor_sync(0xffffffffu, lb, 2);
 
-  // ---- the warps' results through shared memory (over the ring): O [4][16][64], (m, l) [4][16]
+  // ---- the warps' results through shared memory (over the rings)
   cp_async_wait<0>();
   __syncthreads();
-  float* so = reinterpret_cast<float*>(smem);
-  float2* sml = reinterpret_cast<float2*>(smem + kMlOffset);
+  float* so = reinterpret_cast<float*>(smem) + warp * C::ROWS * C::OS;
+  float2* sml = reinterpret_cast<float2*>(smem + C::ML) + warp * C::ROWS;
 #pragma unroll
-  for (int n = 0; n < 8; ++n) {
-    float* d0 = so + (warp * 16 + g) * HD;
-    float* d1 = d0 + 8 * HD;
-    const int c0 = F32 ? 8 * tq + (n & 3) + 32 * (n >> 2) : 8 * n + 2 * tq, c1 = F32 ? c0 + 4 : c0 + 1;
-    d0[c0] = o[n][0];
-    d0[c1] = o[n][1];
-    d1[c0] = o[n][2];
-    d1[c1] = o[n][3];
-  }
-  if (tq == 0) {
-    sml[warp * 16 + g] = make_float2(ma, la);
-    sml[warp * 16 + g + 8] = make_float2(mb, lb);
-  }
-  __syncthreads();
-  if constexpr (WK == 4) {  // join of the four warps: 8 threads a row, 8 elements each
-    const int x = threadIdx.x >> 3, c8 = (threadIdx.x & 7) * 8;
-    float m = -CUDART_INF_F, l = 0.0f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int r = 0; r < NR; ++r)
 #pragma unroll
-    for (int w = 0; w < WK; ++w) m = fmaxf(m, sml[w * 16 + x].x);
-    const float u = m == -CUDART_INF_F ? 0.0f : m;
+    for (int e = 0; e < 2; ++e) {
+      l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], 4);
+      l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], 8);
+      l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], 16);
+      const int x = 8 * r + 2 * tq + e;
+      if (g == 0) sml[x] = make_float2(m[r][e], l[r][e]);
 #pragma unroll
-    for (int w = 0; w < WK; ++w) {
-      const float2 ml = sml[w * 16 + x];
-      const float f = ex2_approx(ml.x - u);
-      l += f * ml.y;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += f * so[(w * 16 + x) * HD + c8 + e];
+      for (int i = 0; i < 4; ++i) {
+        so[x * C::OS + (F32 ? 4 * g + i : 16 * i + g)] = o[r][i][e];
+        so[x * C::OS + (F32 ? 32 + 4 * g + i : 16 * i + g + 8)] = o[r][i][e + 2];
+      }
     }
-    __syncthreads();
+  __syncthreads();
+}
+
+// Join of the warps' results for row x of the tile, elements c8 .. c8 + 7.
+template <typename T, int NR>
+__device__ __forceinline__ void join_warps(const uint8_t* smem, int x, int c8, float (&v)[8], float& m, float& l) {
+  using C = Cfg<T, NR>;
+  const float* so = reinterpret_cast<const float*>(smem);
+  const float2* sml = reinterpret_cast<const float2*>(smem + C::ML);
+  m = -CUDART_INF_F;
+  l = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) so[x * HD + c8 + e] = v[e];
-    if (c8 == 0) sml[x] = make_float2(m, l);
-    __syncthreads();
+  for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < C::NW; ++w) m = fmaxf(m, sml[w * C::ROWS + x].x);
+  const float u = m == -CUDART_INF_F ? 0.0f : m;
+#pragma unroll
+  for (int w = 0; w < C::NW; ++w) {
+    const float2 ml = sml[w * C::ROWS + x];
+    const float f = ex2_approx(ml.x - u);
+    l += f * ml.y;
+    const float4* o = reinterpret_cast<const float4*>(so + (w * C::ROWS + x) * C::OS + c8);
+    const float4 a = o[0], b = o[1];
+    v[0] += f * a.x; v[1] += f * a.y; v[2] += f * a.z; v[3] += f * a.w;
+    v[4] += f * b.x; v[5] += f * b.y; v[6] += f * b.z; v[7] += f * b.w;
   }
 }
 
@@ -584,74 +621,99 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t a) {
   return v;
 }
 
-// One-launch form: cluster blockIdx.x / cluster attends one (group, key head), all of its rows.
-template <typename T, int WR>
-__global__ void __launch_bounds__(kThreads) prefix_cluster_kernel(const PrefixParams p, uint32_t* err) {
+// One-launch form: a cluster of p.cluster CTAs attends one (group, key head, tile of rows).
+template <typename T, int NR>
+__global__ void __launch_bounds__(Cfg<T, NR>::THREADS) prefix_cluster_kernel(const PrefixParams p, uint32_t* err) {
+  using C = Cfg<T, NR>;
   extern __shared__ __align__(128) uint8_t smem_dyn[];
   __shared__ SegTable seg;
   pdl_trigger();
   pdl_wait();
-  const int item = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
+  const int rank = blockIdx.x % p.cluster;
+  int b = blockIdx.x / p.cluster;
+  const int tile = b % p.row_tiles;
+  b /= p.row_tiles;
   Item it;
-  const int grp = item / p.Hkv;
-  it.hk = item % p.Hkv;
+  const int grp = b / p.Hkv;
+  it.hk = b % p.Hkv;
   int begin, count;
   group_range(p, grp, begin, count, err);
-  if (count == 0) return;  // the whole cluster
-  it.kp = p.kp + grp * p.k_group + it.hk * static_cast<int>(HD * sizeof(T));
-  it.vp = p.vp + grp * p.v_group + it.hk * static_cast<int>(HD * sizeof(T));
+  const int per_seq = p.q_len * p.r, row0 = tile * C::ROWS;
+  it.n_rows = min(count * per_seq - row0, C::ROWS);
+  if (it.n_rows <= 0) return;  // the whole cluster
+  it.kp = p.kp + grp * p.k_group + it.hk * C::ROWB;
+  it.vp = p.vp + grp * p.v_group + it.hk * C::ROWB;
   it.prefix_len = p.kp ? prefix_len_of(p, grp, err) : 0;
-  it.seq0 = begin;
-  it.n_own = p.k_pages ? count : 0;
-  it.row0 = 0;
-  it.n_rows = count * p.q_len * p.r;
-  it.token0 = begin * p.q_len;
+  const int first = row0 / per_seq;  // sequences of the tile's rows
+  it.seq0 = begin + first;
+  it.row_off = row0 - first * per_seq;
+  it.n_own = p.k_pages ? (row0 + it.n_rows - 1) / per_seq - first + 1 : 0;
   it.split = rank;
   it.n_splits = p.cluster;
-  attend<T, WR>(p, it, smem_dyn, seg, err);
-  if (p.cluster > 1) cluster_arrive_wait();
-  // the ranks share the rows out: 8 threads a row, 8 elements each
-  const uint32_t so = smem_u32(smem_dyn);
-  const int c8 = (threadIdx.x & 7) * 8;
-  for (int x = rank + p.cluster * (threadIdx.x >> 3); x < it.n_rows; x += p.cluster * (kThreads / 8)) {
-    float m = -CUDART_INF_F, l = 0.0f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  attend<T, NR>(p, it, smem_dyn, seg, err);
+  const int x = threadIdx.x >> 3, c8 = (threadIdx.x & 7) * 8;  // 8 threads a row, 8 elements each
+  auto put = [&](int row, const float (&v)[8], float l) {
+    const int y = it.row_off + row, tok = y / p.r;
+    write_out8<T>(p, it.seq0 * p.q_len + tok, it.hk * p.r + y - tok * p.r, c8, v, l);
+  };
+  float v[8], m, l;
+  if (x < C::ROWS) join_warps<T, NR>(smem_dyn, x, c8, v, m, l);
+  if (p.cluster == 1) {
+    if (x < it.n_rows) put(x, v, l);
+    return;
+  }
+  // the CTAs' results over the first warp's; then the ranks share the rows out
+  __syncthreads();
+  const uint32_t so = smem_u32(smem_dyn), sml = so + C::ML;
+  if (x < C::ROWS) {
+    float4* d = reinterpret_cast<float4*>(smem_dyn + (x * C::OS + c8) * 4);
+    d[0] = make_float4(v[0], v[1], v[2], v[3]);
+    d[1] = make_float4(v[4], v[5], v[6], v[7]);
+    if (c8 == 0) *reinterpret_cast<float2*>(smem_dyn + C::ML + x * 8) = make_float2(m, l);
+  }
+  cluster_arrive_wait();
+  for (int y = rank + p.cluster * x; y < it.n_rows; y += p.cluster * (C::THREADS / 8)) {
     float2 ml[8];
+    m = -CUDART_INF_F;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (i < p.cluster) {
-        ml[i] = ld_cluster_f2(rank_addr(so + kMlOffset + x * 8, i));
+        ml[i] = ld_cluster_f2(rank_addr(sml + y * 8, i));
         m = fmaxf(m, ml[i].x);
       }
     }
     const float u = m == -CUDART_INF_F ? 0.0f : m;
+    l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (i < p.cluster) {
         const float f = ex2_approx(ml[i].x - u);
-        const uint32_t a = rank_addr(so + (x * HD + c8) * 4, i);
+        const uint32_t a = rank_addr(so + (y * C::OS + c8) * 4, i);
         const float4 o0 = ld_cluster_f4(a), o1 = ld_cluster_f4(a + 16);
         l += f * ml[i].y;
         v[0] += f * o0.x; v[1] += f * o0.y; v[2] += f * o0.z; v[3] += f * o0.w;
         v[4] += f * o1.x; v[5] += f * o1.y; v[6] += f * o1.z; v[7] += f * o1.w;
       }
     }
-    const int tok = x / p.r;
-    write_out8<T>(p, it.token0 + tok, it.hk * p.r + x - tok * p.r, c8, v, l);
+    put(y, v, l);
   }
-  if (p.cluster > 1) cluster_arrive_wait();  // no CTA leaves while another reads its results
+  cluster_arrive_wait();  // no CTA leaves while another reads its results
 }
 
 // Two-launch form: one CTA per (group, key head, split of the prefix, row tile), or (OWN) per
 // (sequence, key head, split of its own keys, row tile); writes its rows' partial results.
-template <typename T, int WR, bool OWN>
-__global__ void __launch_bounds__(kThreads) prefix_part_kernel(const PrefixParams p, uint32_t* err) {
+template <typename T, int NR, bool OWN>
+__global__ void __launch_bounds__(Cfg<T, NR>::THREADS) prefix_part_kernel(const PrefixParams p, uint32_t* err) {
+  using C = Cfg<T, NR>;
   extern __shared__ __align__(128) uint8_t smem_dyn[];
   __shared__ SegTable seg;
   pdl_trigger();
   pdl_wait();
   int b = blockIdx.x;
   Item it;
-  it.row0 = (b % p.row_tiles) * 16 * WR;
+  const int row0 = (b % p.row_tiles) * C::ROWS;
   b /= p.row_tiles;
   it.n_splits = OWN ? p.ns : p.np;
   it.split = b % it.n_splits;
@@ -665,32 +727,29 @@ __global__ void __launch_bounds__(kThreads) prefix_part_kernel(const PrefixParam
   it.n_own = 1;
   if (!OWN) {
     group_range(p, which, begin, count, err);
-    it.kp = p.kp + which * p.k_group + it.hk * static_cast<int>(HD * sizeof(T));
-    it.vp = p.vp + which * p.v_group + it.hk * static_cast<int>(HD * sizeof(T));
+    it.kp = p.kp + which * p.k_group + it.hk * C::ROWB;
+    it.vp = p.vp + which * p.v_group + it.hk * C::ROWB;
     it.prefix_len = prefix_len_of(p, which, err);
     it.n_own = 0;
   }
-  it.n_rows = count * p.q_len * p.r;
-  if (it.row0 >= it.n_rows) return;
+  it.n_rows = min(count * p.q_len * p.r - row0, C::ROWS);
+  if (it.n_rows <= 0) return;
   it.seq0 = begin;
-  it.token0 = begin * p.q_len;
-  attend<T, WR>(p, it, smem_dyn, seg, err);
-  const float* so = reinterpret_cast<const float*>(smem_dyn);
-  const float2* sml = reinterpret_cast<const float2*>(smem_dyn + kMlOffset);
-  const int n_slots = p.np + p.ns, slot = (OWN ? p.np : 0) + it.split, c8 = (threadIdx.x & 7) * 8;
-  for (int y = threadIdx.x >> 3; y < 16 * WR; y += kThreads / 8) {
-    const int x = it.row0 + y;
-    if (x >= it.n_rows) break;
-    const int tok = x / p.r, head = it.hk * p.r + x - tok * p.r;
-    const float2 ml = sml[y];
-    const size_t at = (static_cast<size_t>(it.token0 + tok) * p.H + head) * n_slots + slot;
-    if (ml.y > 0.0f) {
-      float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + c8);
-      dst[0] = *reinterpret_cast<const float4*>(so + y * HD + c8);
-      dst[1] = *reinterpret_cast<const float4*>(so + y * HD + c8 + 4);
-    }
-    if (c8 == 0) p.part_ml[at] = ml;
+  it.row_off = row0;
+  attend<T, NR>(p, it, smem_dyn, seg, err);
+  const int n_slots = p.np + p.ns, slot = (OWN ? p.np : 0) + it.split;
+  const int x = threadIdx.x >> 3, c8 = (threadIdx.x & 7) * 8;
+  if (x >= it.n_rows) return;
+  float v[8], m, l;
+  join_warps<T, NR>(smem_dyn, x, c8, v, m, l);
+  const int y = row0 + x, tok = y / p.r, head = it.hk * p.r + y - tok * p.r;
+  const size_t at = ((static_cast<size_t>(begin) * p.q_len + tok) * p.H + head) * n_slots + slot;
+  if (l > 0.0f) {
+    float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + c8);
+    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
   }
+  if (c8 == 0) p.part_ml[at] = make_float2(m, l);
 }
 
 // Join of the partial results of one (token, head): sixteen lanes, four elements each.
@@ -752,58 +811,55 @@ wenc_status bad(wenc_status s, const char* fmt, long long a = 0, long long b = 0
 // How one call is divided, from its sizes alone.
 struct Plan {
   int cluster = 0;              // > 0: the one-launch form, CTAs per item
-  int wr = 0;                   // its warps along the rows
-  int wr_p = 0, wr_s = 0;       // two-launch form: warps along the rows of prefix and own-key items
+  int nr_p = 0, nr_s = 0;       // groups of 8 rows per tile: prefix (or one-launch) and own-key items
   int rows_p = 0, rows_s = 0;   // row tiles
   int np = 0, ns = 0;           // key splits
   long long items_p = 0, items_s = 0;  // CTAs (one-launch form: items_p)
   size_t part_o = 0, bytes = 0;  // offset of the (m, l) pairs; workspace bytes
 };
 
-int tile_keys(bool f32, int wr) {
-  if (wr == 4) return f32 ? Cfg<float, 4>::KT : Cfg<__nv_bfloat16, 4>::KT;
-  return f32 ? Cfg<float, 1>::KT : Cfg<__nv_bfloat16, 1>::KT;
-}
+// Groups of 8 rows per tile: as few as hold the rows, within the registers (fp32 keeps two parts of
+// every query).
+int row_groups(long long rows, bool f32) { return rows <= 8 ? 1 : rows <= 16 || f32 ? 2 : 4; }
 
 Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
   Plan pl;
   const bool f32 = a->dtype == WENC_DTYPE_F32;
+  const int kt = f32 ? Cfg<float, 1>::KT : Cfg<__nv_bfloat16, 1>::KT;
   const long long r = a->n_heads / a->n_kv_heads;
   const long long rows_s = a->q_len * r;  // rows of one sequence per key head
   const long long group = a->k_prefix ? a->max_group : 1, n_groups = a->k_prefix ? a->n_groups : a->n_seqs;
   const long long rows = group * rows_s;
   const long long own_cap = a->k_pages ? static_cast<long long>(a->max_pages) * a->page_size : 0;
   const long long prefix = a->k_prefix ? a->prefix_max : 0;
+  pl.nr_p = row_groups(rows, f32);
+  pl.rows_p = static_cast<int>((rows + 8 * pl.nr_p - 1) / (8 * pl.nr_p));
   if (rows <= 64) {
-    pl.wr = rows <= 16 ? 1 : 4;
-    const int kt = tile_keys(f32, pl.wr);
     const long long tiles = (prefix + kt - 1) / kt + group * ((own_cap + kt - 1) / kt);
-    const long long items = n_groups * a->n_kv_heads;
-    // enough CTAs for about three rounds of two per SM, none without a tile of its own
+    const long long items = n_groups * a->n_kv_heads * pl.rows_p;
+    // CTAs for about one round of the machine, none without a tile of its own
     pl.cluster = 1;
-    while (pl.cluster < 8 && pl.cluster < tiles && items * pl.cluster < 6ll * sms) pl.cluster *= 2;
+    while (pl.cluster < 8 && pl.cluster < tiles && 2 * items * pl.cluster <= 3ll * sms) pl.cluster *= 2;
     pl.items_p = items * pl.cluster;
     return pl;
   }
-  auto splits = [&](long long items, long long keys, int wr) {
-    const long long tiles = (keys + tile_keys(f32, wr) - 1) / tile_keys(f32, wr);
+  auto splits = [&](long long items, long long keys) {
+    const long long tiles = (keys + kt - 1) / kt;
     long long n = (6ll * sms + items - 1) / items;
     if (n > tiles) n = tiles;
     if (n > 32) n = 32;
     return static_cast<int>(n < 1 ? 1 : n);
   };
   if (a->k_prefix) {
-    pl.wr_p = 4;
-    pl.rows_p = static_cast<int>((rows + 63) / 64);
     const long long items = n_groups * a->n_kv_heads * pl.rows_p;
-    pl.np = splits(items, prefix, pl.wr_p);
+    pl.np = splits(items, prefix);
     pl.items_p = items * pl.np;
   }
   if (a->k_pages) {
-    pl.wr_s = rows_s <= 16 ? 1 : 4;
-    pl.rows_s = static_cast<int>((rows_s + 16 * pl.wr_s - 1) / (16 * pl.wr_s));
+    pl.nr_s = row_groups(rows_s, f32);
+    pl.rows_s = static_cast<int>((rows_s + 8 * pl.nr_s - 1) / (8 * pl.nr_s));
     const long long items = static_cast<long long>(a->n_seqs) * a->n_kv_heads * pl.rows_s;
-    pl.ns = splits(items, own_cap, pl.wr_s);
+    pl.ns = splits(items, own_cap);
     pl.items_s = items * pl.ns;
   }
   const size_t n = static_cast<size_t>(a->n_seqs) * a->q_len * a->n_heads * (pl.np + pl.ns);
@@ -866,16 +922,17 @@ cudaError_t opt_in(K kern, uint32_t smem, std::atomic<int>& configured_device) {
   return cudaSuccess;
 }
 
-template <typename T, int WR>
+template <typename T, int NR>
 cudaError_t launch_cluster(const PrefixParams& p, long long blocks, uint32_t* err, cudaStream_t stream) {
-  auto kern = prefix_cluster_kernel<T, WR>;
+  using C = Cfg<T, NR>;
+  auto kern = prefix_cluster_kernel<T, NR>;
   static std::atomic<int> configured{-1};
-  const cudaError_t e = opt_in(kern, Cfg<T, WR>::SMEM, configured);
+  const cudaError_t e = opt_in(kern, C::SMEM, configured);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg<T, WR>::SMEM;
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -889,25 +946,35 @@ cudaError_t launch_cluster(const PrefixParams& p, long long blocks, uint32_t* er
   return cudaLaunchKernelEx(&cfg, kern, p, err);
 }
 
-template <typename T, int WR, bool OWN>
+template <typename T, int NR, bool OWN>
 cudaError_t launch_part(PrefixParams p, int row_tiles, long long blocks, uint32_t* err, cudaStream_t stream) {
-  auto kern = prefix_part_kernel<T, WR, OWN>;
+  using C = Cfg<T, NR>;
+  auto kern = prefix_part_kernel<T, NR, OWN>;
   static std::atomic<int> configured{-1};
-  const cudaError_t e = opt_in(kern, Cfg<T, WR>::SMEM, configured);
+  const cudaError_t e = opt_in(kern, C::SMEM, configured);
   if (e != cudaSuccess) return e;
   p.row_tiles = row_tiles;
-  return wenc_host::launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), Cfg<T, WR>::SMEM, stream, p, err);
+  return wenc_host::launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(C::THREADS), C::SMEM, stream, p, err);
 }
 
 template <typename T>
-cudaError_t launch_all(const PrefixParams& p, const Plan& pl, uint32_t* err, cudaStream_t stream) {
-  if (pl.cluster > 0)
-    return pl.wr == 1 ? launch_cluster<T, 1>(p, pl.items_p, err, stream) : launch_cluster<T, 4>(p, pl.items_p, err, stream);
+cudaError_t launch_all(PrefixParams p, const Plan& pl, uint32_t* err, cudaStream_t stream) {
+  constexpr bool F32 = sizeof(T) == 4;
+  if (pl.cluster > 0) {
+    p.row_tiles = pl.rows_p;
+    if (pl.nr_p == 1) return launch_cluster<T, 1>(p, pl.items_p, err, stream);
+    if (pl.nr_p == 2) return launch_cluster<T, 2>(p, pl.items_p, err, stream);
+    if constexpr (!F32) return launch_cluster<T, 4>(p, pl.items_p, err, stream);
+    return cudaErrorInvalidValue;
+  }
+  constexpr int kMost = F32 ? 2 : 4;  // (more than 64 rows: the largest tiles)
   cudaError_t e = cudaSuccess;
-  if (pl.items_p > 0) e = launch_part<T, 4, false>(p, pl.rows_p, pl.items_p, err, stream);
-  if (e == cudaSuccess && pl.items_s > 0)
-    e = pl.wr_s == 1 ? launch_part<T, 1, true>(p, pl.rows_s, pl.items_s, err, stream)
-                     : launch_part<T, 4, true>(p, pl.rows_s, pl.items_s, err, stream);
+  if (pl.items_p > 0) e = launch_part<T, kMost, false>(p, pl.rows_p, pl.items_p, err, stream);
+  if (e == cudaSuccess && pl.items_s > 0) {
+    if (pl.nr_s == 1) e = launch_part<T, 1, true>(p, pl.rows_s, pl.items_s, err, stream);
+    else if (pl.nr_s == 2) e = launch_part<T, 2, true>(p, pl.rows_s, pl.items_s, err, stream);
+    else e = launch_part<T, kMost, true>(p, pl.rows_s, pl.items_s, err, stream);
+  }
   if (e != cudaSuccess) return e;
   const long long threads = static_cast<long long>(p.n_seqs) * p.q_len * p.H * 16;
   return wenc_host::launch_pdl(prefix_join_kernel<T>, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0,
