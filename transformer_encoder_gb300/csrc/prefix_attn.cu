@@ -112,7 +112,7 @@ struct PrefixParams {
   const uint8_t *kp, *vp;
   long long k_group, k_token, v_group, v_token;  // bytes
   const uint8_t *k_pages, *v_pages;
-  long long k_page, v_page, page_row;  // bytes between pages; bytes of one page slot
+  uint32_t k_page16, v_page16, row16;  // between pages, and between a page's slots, in units of 16 bytes
   const int32_t *group_start, *prefix_lens, *table, *lens;
   long long table_stride;
   int n_seqs, q_len, H, Hkv, r, n_groups, max_group, prefix_max, n_pages, page_size, page_shift, max_pages;
@@ -136,6 +136,7 @@ struct Cfg {
   static constexpr int ROWS = 8 * NR;
   static constexpr int ROWB = HD * sizeof(T);
   static constexpr int STAGES = 2;
+  static constexpr int CTAS = F32 ? (NR == 1 ? 3 : 2) : NR == 1 ? 3 : NR == 2 ? 2 : 1;  // per SM, for the registers
   static constexpr uint32_t HALF = KW * ROWB;  // bytes of K (or V) per warp and stage
   static constexpr uint32_t RING = NW * STAGES * 2 * HALF;
   static constexpr uint32_t P_BYTES = F32 ? NW * NR * 16 * 8 * 4 : 0;  // fp32: P on its way to B fragments
@@ -222,48 +223,56 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
   const int tile0 = it.split * per;
   const int n_mine = max(0, min(per, n_tiles - tile0));
 
-  // ---- tile loads: every warp copies the keys it scores itself
+  // ---- tile loads: every warp copies the keys it scores itself. Addresses in units of 16 bytes (32-bit
+  // factors, 64-bit sums). Rows RPI i + lr of a stage: two swizzled positions alternate with i.
   const int lc = lane % CH, lr = lane / CH;
-  int lseg = 0;       // segment of the next tile to load
-  int next_page = 0;  // its page of the key in row lane % 16 (own keys), read one tile ahead
-  auto page_of = [&](int j) {  // moves lseg to tile j's
-    while (tile0 + j >= seg.tile0[lseg + 1]) ++lseg;
+  const uint32_t at0 = granule<F32>(lr, lc), at1 = granule<F32>(lr + RPI, lc) - 512u;
+  static_assert(RPI * C::ROWB == 512, "a copy instruction covers 512 bytes of a stage");
+  int lseg = 0, lbegin = 0, lend = 0, lkeys = 0;  // segment of the next tile to load, its tiles and keys
+  int next_page = 0;  // page of the key in the next tile's row lane % 16 (own keys), read one tile ahead
+  auto advance = [&](int t, int& sg, int& begin, int& end, int& keys) {
+    while (t >= seg.tile0[sg + 1]) ++sg;
+    begin = seg.tile0[sg];
+    end = seg.tile0[sg + 1];
+    keys = seg.len[sg];
+  };
+  auto page_of = [&](int j) {
+    if (tile0 + j >= lend) advance(tile0 + j, lseg, lbegin, lend, lkeys);
     if (lseg == 0) return;
-    const int key = (tile0 + j - seg.tile0[lseg]) * KT + warp * KW + (lane & 15);
+    const int key = (tile0 + j - lbegin) * KT + warp * KW + (lane & 15);
     const int pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-    next_page = key < seg.len[lseg] ? p.table[(it.seq0 + lseg - 1) * p.table_stride + pi] : -1;
+    next_page = key < lkeys ? p.table[(it.seq0 + lseg - 1) * p.table_stride + pi] : -1;
   };
   auto load = [&](int j, int stage) {
     const uint32_t sk = s0 + stage * (2 * C::HALF), sv = sk + C::HALF;
-    const int key0 = (tile0 + j - seg.tile0[lseg]) * KT + warp * KW, n_keys = seg.len[lseg];
+    const int key0 = (tile0 + j - lbegin) * KT + warp * KW;
     if (lseg == 0) {
       const uint8_t* ks = it.kp + (key0 + lr) * p.k_token + lc * 16;
       const uint8_t* vs = it.vp + (key0 + lr) * p.v_token + lc * 16;
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        const int row = lr + i * RPI;
-        const bool ok = key0 + row < n_keys;
-        cp_async16(sk + granule<F32>(row, lc), ok ? ks : it.kp, ok);
-        cp_async16(sv + granule<F32>(row, lc), ok ? vs : it.vp, ok);
+        const bool ok = key0 + lr + i * RPI < lkeys;
+        const uint32_t at = ((i & 1) ? at1 : at0) + i * 512;
+        cp_async16(sk + at, ok ? ks : it.kp, ok);
+        cp_async16(sv + at, ok ? vs : it.vp, ok);
         ks += RPI * p.k_token;
         vs += RPI * p.v_token;
       }
     } else {
       const int key = key0 + (lane & 15);
       const int pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-      const int slot = key - pi * p.page_size;
-      const bool in = next_page >= 0 && next_page < p.n_pages;
-      if (!in && key < n_keys) *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (80u << 8);
+      const bool in = static_cast<uint32_t>(next_page) < static_cast<uint32_t>(p.n_pages);
+      if (!in && key < lkeys) *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (80u << 8);
       const int page = in ? next_page : -1;
-      const int head = it.hk * C::ROWB + lc * 16;
+      const uint32_t slot = (key - pi * p.page_size) * p.row16, head = it.hk * CH + lc;
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        const int row = lr + i * RPI;
-        const int pg = __shfl_sync(0xffffffffu, page, row), sl = __shfl_sync(0xffffffffu, slot, row);
+        const int pg = __shfl_sync(0xffffffffu, page, lr + i * RPI);
+        const uint32_t x = __shfl_sync(0xffffffffu, slot, lr + i * RPI) + head;
         const bool ok = pg >= 0;
-        const long long at = sl * p.page_row + head;
-        cp_async16(sk + granule<F32>(row, lc), ok ? p.k_pages + pg * p.k_page + at : p.k_pages, ok);
-        cp_async16(sv + granule<F32>(row, lc), ok ? p.v_pages + pg * p.v_page + at : p.v_pages, ok);
+        const uint32_t upg = ok ? pg : 0, at = ((i & 1) ? at1 : at0) + i * 512;
+        cp_async16(sk + at, p.k_pages + ((static_cast<uint64_t>(upg) * p.k_page16 + x) << 4), ok);
+        cp_async16(sv + at, p.v_pages + ((static_cast<uint64_t>(upg) * p.v_page16 + x) << 4), ok);
       }
     }
   };
@@ -334,7 +343,8 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
   }
   const float sc = p.scale_log2;
 
-  int cseg = 0;
+  int cseg = 0, cbegin = 0, cend = 0, n_keys = 0;  // the segment being scored
+  int lim[NR][2] = {};                             // its keys that each of this thread's rows sees
   for (int j = 0; j < n_mine; ++j) {
     cp_async_wait<ST - 2>();
     __syncwarp();
@@ -343,8 +353,15 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
       if (j + ST < n_mine) page_of(j + ST);
     }
     cp_async_commit();
-    while (tile0 + j >= seg.tile0[cseg + 1]) ++cseg;
-    const int key0 = (tile0 + j - seg.tile0[cseg]) * KT + warp * KW, n_keys = seg.len[cseg];
+    if (tile0 + j >= cend) {
+      advance(tile0 + j, cseg, cbegin, cend, n_keys);
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          lim[r][e] = cseg == 0 ? n_keys : seq_of[r][e] == cseg - 1 ? n_keys - p.q_len + 1 + tok_of[r][e] : 0;
+    }
+    const int key0 = (tile0 + j - cbegin) * KT + warp * KW;
     if (key0 >= n_keys) continue;
     const uint32_t sk = s0 + (j % ST) * (2 * C::HALF), sv = sk + C::HALF;
 
@@ -390,11 +407,8 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
 #pragma unroll
       for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          int lim = n_keys;  // keys of this segment the row sees
-          if (cseg > 0) lim = seq_of[r][e & 1] == cseg - 1 ? n_keys - p.q_len + 1 + tok_of[r][e & 1] : 0;
-          if (key0 + g + 8 * (e >> 1) >= lim) s[r][e] = -CUDART_INF_F;
-        }
+        for (int e = 0; e < 4; ++e)
+          if (key0 + g + 8 * (e >> 1) >= lim[r][e & 1]) s[r][e] = -CUDART_INF_F;
     }
     bool move = false;  // some score exceeds its row's reference by more than 2^8
 #pragma unroll
@@ -623,7 +637,7 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t a) {
 
 // One-launch form: a cluster of p.cluster CTAs attends one (group, key head, tile of rows).
 template <typename T, int NR>
-__global__ void __launch_bounds__(Cfg<T, NR>::THREADS) prefix_cluster_kernel(const PrefixParams p, uint32_t* err) {
+__global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_cluster_kernel(const PrefixParams p, uint32_t* err) {
   using C = Cfg<T, NR>;
   extern __shared__ __align__(128) uint8_t smem_dyn[];
   __shared__ SegTable seg;
@@ -705,7 +719,7 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS) prefix_cluster_kernel(con
 // Two-launch form: one CTA per (group, key head, split of the prefix, row tile), or (OWN) per
 // (sequence, key head, split of its own keys, row tile); writes its rows' partial results.
 template <typename T, int NR, bool OWN>
-__global__ void __launch_bounds__(Cfg<T, NR>::THREADS) prefix_part_kernel(const PrefixParams p, uint32_t* err) {
+__global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_part_kernel(const PrefixParams p, uint32_t* err) {
   using C = Cfg<T, NR>;
   extern __shared__ __align__(128) uint8_t smem_dyn[];
   __shared__ SegTable seg;
@@ -1008,6 +1022,8 @@ extern "C" wenc_status wenc_prefix_attention(const wenc_prefix_attention_args* a
   if (a->k_pages && a->n_seqs > 1 && a->block_table_stride < a->max_pages)
     return bad(WENC_ERR_INVALID_ARG, "prefix_attention: block_table_stride %lld < max_pages %lld", a->block_table_stride,
                a->max_pages);
+  if (a->k_pages && (a->k_page_stride / per16 > 0xffffffffll || a->v_page_stride / per16 > 0xffffffffll))
+    return bad(WENC_ERR_UNSUPPORTED, "prefix_attention: a page stride passes 2^36 bytes");
   const void* ptrs[] = {a->q, a->out, a->k_prefix, a->v_prefix, a->k_pages, a->v_pages};
   for (const void* x : ptrs)
     if (reinterpret_cast<uintptr_t>(x) & 15u) return bad(WENC_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
@@ -1057,9 +1073,9 @@ extern "C" wenc_status wenc_prefix_attention(const wenc_prefix_attention_args* a
   if (a->k_pages) {
     p.k_pages = static_cast<const uint8_t*>(a->k_pages);
     p.v_pages = static_cast<const uint8_t*>(a->v_pages);
-    p.k_page = a->k_page_stride * es;
-    p.v_page = a->v_page_stride * es;
-    p.page_row = kv_row * es;
+    p.k_page16 = static_cast<uint32_t>(a->k_page_stride / per16);
+    p.v_page16 = static_cast<uint32_t>(a->v_page_stride / per16);
+    p.row16 = static_cast<uint32_t>(kv_row / per16);
     p.table = a->block_table;
     p.table_stride = a->block_table_stride;
     p.lens = a->lens;
