@@ -377,12 +377,12 @@ typedef struct {
  * A length, offset or page number out of range records WENC_ERR_INVALID_ARG in the device error
  * word (wenc_sync_status(NULL)); nothing out of range is accessed and the output rows it concerns are
  * undefined. The workspace belongs to the call until its work is done: calls that may overlap need
- * one each. At most two launches, no allocation, stream-ordered. */
+ * one each. At most three launches, no allocation, stream-ordered. */
 WENC_API wenc_status wenc_prefix_attention(const wenc_prefix_attention_args* args, wenc_stream_t stream);
 
 /* wenc_prefix_attention_workspace -- bytes of workspace the call needs on the current device (0 for
- * arguments it would refuse). Depends on the sizes and on which of prefix and pages is there, not on
- * device data. */
+ * arguments it would refuse). Depends on the sizes, the scale's sign, the group strides and on which of
+ * prefix and pages is there, not on device data. */
 WENC_API size_t wenc_prefix_attention_workspace(const wenc_prefix_attention_args* args);
 
 /* wenc_quantize_rows -- rows of 8-bit integers with one scale each, the operand of wenc_linear_i8:

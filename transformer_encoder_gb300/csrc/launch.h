@@ -156,6 +156,26 @@ cudaError_t launch_attention_tf32(const CUtensorMap& tq, const CUtensorMap& tk, 
                                   int k_col0, int v_col0, float* out, int out_stride, int B, int T, int H,
                                   uint32_t* err, cudaStream_t stream);
 
+// ---------------------------------------------------------------- shared prefixes (tcgen05)
+// The prefix part of wenc_prefix_attention for many bf16 query rows (prefix_tc.cu). tq: 3-D bf16 map
+// [tokens][H][64], box 64 x r x `tokens`; tk, tv: [groups][prefix_max][row], box 64 x 128. Work items
+// w = ((group * Hkv + key head) * n_x + row-tile pair) * np + split.
+struct PrefixTcArgs {
+  const int32_t *group_start, *prefix_lens;
+  int n_seqs, q_len, H, Hkv, r, max_group, prefix_max;
+  int tokens;  // per row tile: 128 / r
+  int n_x, np, n_items, n_slots;
+  float scale_log2;
+  float* part_o;    // [(token * H + head) * n_slots + split][64]
+  float2* part_ml;
+};
+cudaError_t launch_prefix_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PrefixTcArgs& p,
+                             uint32_t* err, int num_sms, cudaStream_t stream);
+// 3-D bf16 view [dim2][dim1][inner] with a box of box_inner x box1 x box2 (128-byte swizzle).
+bool make_tmap_3d_bf16_box(CUtensorMap* map, const void* base, uint64_t inner, uint64_t dim1, uint64_t dim2,
+                           uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box_inner, uint32_t box1,
+                           uint32_t box2, std::string* why);
+
 // ---------------------------------------------------------------- convolutional stem
 // Unfold for a kernel-3, padding-1 convolution over time: x [B, t_in, C] (fp32, or the operand
 // format: bf16 / TF32-rounded fp32) -> A [B * t_out, k_pad] in the operand format with

@@ -18,7 +18,8 @@
 // them. Own keys are scored against all of the tile's rows and masked to their sequence's. The CTAs'
 // results (m, l, O) are joined through distributed shared memory: no workspace and no second kernel.
 // More rows: a work item is a share of a group's prefix, or of one sequence's own keys; items write
-// partial results to the workspace and a second kernel joins them.
+// partial results to the workspace and a second kernel joins them. The bf16 prefix then runs on the
+// fifth-generation tensor cores (prefix_tc.cu).
 //
 // Inside a CTA every warp takes 16 keys of each tile, through a ring of cp.async stages of its own, with
 // no barrier between warps until their results are joined at the end. The products are transposed:
@@ -828,7 +829,9 @@ struct Plan {
   int nr_p = 0, nr_s = 0;       // groups of 8 rows per tile: prefix (or one-launch) and own-key items
   int rows_p = 0, rows_s = 0;   // row tiles
   int np = 0, ns = 0;           // key splits
-  long long items_p = 0, items_s = 0;  // CTAs (one-launch form: items_p)
+  long long items_p = 0, items_s = 0;  // CTAs (one-launch form: items_p; tcgen05 form: work items)
+  bool tc = false;              // the prefix runs in prefix_tc.cu
+  int tokens = 0;               // its tokens per row tile
   size_t part_o = 0, bytes = 0;  // offset of the (m, l) pairs; workspace bytes
 };
 
@@ -864,7 +867,20 @@ Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
     if (n > 32) n = 32;
     return static_cast<int>(n < 1 ? 1 : n);
   };
-  if (a->k_prefix) {
+  // (a negative or zero scale, a group stride of 0 and more than 128 query heads per key head stay with
+  // the general form)
+  pl.tc = !f32 && a->k_prefix && r <= 128 && a->scale > 0.0f && (n_groups == 1 || (a->k_group_stride > 0 && a->v_group_stride > 0));
+  if (pl.tc) {
+    pl.tokens = static_cast<int>(128 / r);
+    pl.rows_p = static_cast<int>((group * a->q_len + 2 * pl.tokens - 1) / (2 * pl.tokens));  // pairs of row tiles
+    const long long items = n_groups * a->n_kv_heads * pl.rows_p, tiles = (prefix + 127) / 128;
+    // fill one round of the persistent CTAs, if the keys reach; at most 32 shares
+    long long n = sms / items;
+    if (n > tiles) n = tiles;
+    if (n > 32) n = 32;
+    pl.np = static_cast<int>(n < 1 ? 1 : n);
+    pl.items_p = items * pl.np;
+  } else if (a->k_prefix) {
     const long long items = n_groups * a->n_kv_heads * pl.rows_p;
     pl.np = splits(items, prefix);
     pl.items_p = items * pl.np;
@@ -971,6 +987,46 @@ cudaError_t launch_part(PrefixParams p, int row_tiles, long long blocks, uint32_
   return wenc_host::launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(C::THREADS), C::SMEM, stream, p, err);
 }
 
+// The prefix part on tcgen05.
+wenc_status launch_tc(const wenc_prefix_attention_args* a, const PrefixParams& p, const Plan& pl, uint32_t* err, int sms,
+                      cudaStream_t stream) {
+  CUtensorMap tq, tk, tv;
+  std::string why;
+  const uint64_t tokens = static_cast<uint64_t>(a->n_seqs) * a->q_len, cols = static_cast<uint64_t>(a->n_kv_heads) * HD;
+  // (with one group its stride may be anything)
+  const uint64_t kg = a->n_groups > 1 ? p.k_group : p.k_token * a->prefix_max, vg = a->n_groups > 1 ? p.v_group : p.v_token * a->prefix_max;
+  const bool ok =
+      wenc_host::make_tmap_3d_bf16_box(&tq, a->q, HD, a->n_heads, tokens, HD * 2, p.q_stride, HD, p.r, pl.tokens, &why) &&
+      wenc_host::make_tmap_3d_bf16(&tk, a->k_prefix, cols, a->prefix_max, a->n_groups, p.k_token, kg, HD, 128, &why) &&
+      wenc_host::make_tmap_3d_bf16(&tv, a->v_prefix, cols, a->prefix_max, a->n_groups, p.v_token, vg, HD, 128, &why);
+  if (!ok) return wenc_internal_fail(WENC_ERR_INVALID_ARG, why.c_str());
+  wenc_host::PrefixTcArgs t;
+  t.group_start = p.group_start;
+  t.prefix_lens = p.prefix_lens;
+  t.n_seqs = p.n_seqs;
+  t.q_len = p.q_len;
+  t.H = p.H;
+  t.Hkv = p.Hkv;
+  t.r = p.r;
+  t.max_group = p.max_group;
+  t.prefix_max = p.prefix_max;
+  t.tokens = pl.tokens;
+  t.n_x = pl.rows_p;
+  t.np = pl.np;
+  t.n_items = static_cast<int>(pl.items_p);
+  t.n_slots = pl.np + pl.ns;
+  t.scale_log2 = p.scale_log2;
+  t.part_o = p.part_o;
+  t.part_ml = p.part_ml;
+  const cudaError_t e = wenc_host::launch_prefix_tc(tq, tk, tv, t, err, sms, stream);
+  if (e != cudaSuccess) {
+    char buf[200];
+    snprintf(buf, sizeof(buf), "prefix_attention launch: %s", cudaGetErrorString(e));
+    return wenc_internal_fail(WENC_ERR_CUDA, buf);
+  }
+  return WENC_OK;
+}
+
 template <typename T>
 cudaError_t launch_all(PrefixParams p, const Plan& pl, uint32_t* err, cudaStream_t stream) {
   constexpr bool F32 = sizeof(T) == 4;
@@ -983,7 +1039,7 @@ cudaError_t launch_all(PrefixParams p, const Plan& pl, uint32_t* err, cudaStream
   }
   constexpr int kMost = F32 ? 2 : 4;  // (more than 64 rows: the largest tiles)
   cudaError_t e = cudaSuccess;
-  if (pl.items_p > 0) e = launch_part<T, kMost, false>(p, pl.rows_p, pl.items_p, err, stream);
+  if (pl.items_p > 0 && !pl.tc) e = launch_part<T, kMost, false>(p, pl.rows_p, pl.items_p, err, stream);
   if (e == cudaSuccess && pl.items_s > 0) {
     if (pl.nr_s == 1) e = launch_part<T, 1, true>(p, pl.rows_s, pl.items_s, err, stream);
     else if (pl.nr_s == 2) e = launch_part<T, 2, true>(p, pl.rows_s, pl.items_s, err, stream);
@@ -1100,6 +1156,10 @@ extern "C" wenc_status wenc_prefix_attention(const wenc_prefix_attention_args* a
   p.scale_log2 = (a->scale == 0.0f ? 1.0f : a->scale < 0.0f ? -a->scale : a->scale) * 1.4426950408889634f;
   p.part_o = static_cast<float*>(a->workspace);
   p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(a->workspace) + pl.part_o);
+  if (pl.tc) {
+    st = launch_tc(a, p, pl, err, wenc_internal_sm_count(), reinterpret_cast<cudaStream_t>(stream));
+    if (st != WENC_OK) return st;
+  }
   const cudaError_t e = a->dtype == WENC_DTYPE_F32
                             ? launch_all<float>(p, pl, err, reinterpret_cast<cudaStream_t>(stream))
                             : launch_all<__nv_bfloat16>(p, pl, err, reinterpret_cast<cudaStream_t>(stream));
