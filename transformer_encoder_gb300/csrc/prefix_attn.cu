@@ -21,8 +21,8 @@
 // partial results to the workspace and a second kernel joins them. The bf16 prefix then runs on the
 // fifth-generation tensor cores (prefix_tc.cu).
 //
-// Inside a CTA every warp takes 16 keys of each tile, through a ring of cp.async stages of its own, with
-// no barrier between warps until their results are joined at the end. The products are transposed:
+// Every warp has a ring of cp.async stages of its own and no barrier with other warps until their results
+// are joined at the end; an own-key item of the second form is one warp's. The products are transposed:
 // S^T = K Q^T and O^T = V^T P^T, with 16 keys (or 16 elements of V) as the MMA's M and 8 query rows as its
 // N, so that five beams cost eight columns instead of sixteen rows, and the fragments of K and V
 // are loaded once for any number of rows. The running maximum is followed lazily: P keeps its reference
@@ -132,8 +132,7 @@ struct Cfg {
   static constexpr bool F32 = sizeof(T) == 4;
   static constexpr int NW = F32 ? 4 : 8;       // warps
   static constexpr int THREADS = 32 * NW;
-  static constexpr int KW = 16;                // keys of a tile one warp scores
-  static constexpr int KT = KW * NW;           // keys per tile
+  static constexpr int KW = 16;                // keys per step of a warp
   static constexpr int ROWS = 8 * NR;
   static constexpr int ROWB = HD * sizeof(T);
   static constexpr int STAGES = 2;
@@ -148,9 +147,9 @@ struct Cfg {
   static constexpr uint32_t SMEM = (RING + P_BYTES > RESULTS ? RING + P_BYTES : RESULTS);
 };
 
-// What one CTA attends: rows [row0, row0 + n_rows) of one key head of a group, against its run of the
-// tiles of a list of segments: segment 0 is the prefix, segment i the own keys of sequence seq0 + i - 1,
-// which only that sequence's rows see.
+// What one CTA (or warp) attends: n_rows rows of one key head of a group, against a run of the steps of a list
+// of segments: segment 0 is the prefix, segment i the own keys of sequence seq0 + i - 1, which only
+// that sequence's rows see.
 struct Item {
   const uint8_t *kp, *vp;   // first prefix key of the key head
   int prefix_len;
@@ -158,14 +157,56 @@ struct Item {
   int row_off;              // row x of the tile is row row_off + x of sequence seq0's first row on
   int n_rows;
   int hk;
-  int split, n_splits;
 };
 
 constexpr int kMaxOwn = 32;  // own-key segments of an item: at most one per row of a tile
 struct SegTable {
-  int tile0[kMaxOwn + 2];    // first tile of each segment, and the end
+  int step0[kMaxOwn + 2];    // first step of each segment, and the end
   int len[kMaxOwn + 1];      // its keys
 };
+
+__device__ __forceinline__ int own_len_of(const PrefixParams& p, int seq, uint32_t* err) {
+  int n = p.lens[seq];
+  if (n < 0 || n > static_cast<long long>(p.max_pages) * p.page_size) {
+    *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (81u << 8);
+    n = 0;
+  }
+  return n;
+}
+
+// The segments' steps: a running sum over up to 33 lengths, by warp 0. Ends with a barrier.
+__device__ __forceinline__ void fill_segments(const PrefixParams& p, const Item& it, SegTable& seg, uint32_t* err) {
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x < 32) {
+    const int base = (it.prefix_len + 15) / 16;
+    const int n = lane < it.n_own ? own_len_of(p, it.seq0 + lane, err) : 0;
+    int sum = (n + 15) / 16;
+    if (it.n_own > 1) {
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += up;
+      }
+    }
+    if (lane == 0) {
+      seg.step0[0] = 0;
+      seg.len[0] = it.prefix_len;
+      seg.step0[1] = base;
+    }
+    if (lane < it.n_own) {
+      seg.len[1 + lane] = n;
+      seg.step0[2 + lane] = base + sum;
+    }
+  }
+  __syncthreads();
+}
+
+// Share `part` of `parts` equal runs of n steps.
+__device__ __forceinline__ void run_of(int n, int part, int parts, int& first, int& count) {
+  const int per = (n + parts - 1) / parts;
+  first = part * per;
+  count = max(0, min(per, n - first));
+}
 
 // 16-byte granule `c` of key row `row` within a warp's stage. bf16 rows have 8 granules (all 32 banks),
 // fp32 rows 16; the XOR spreads the rows that an ldmatrix (or a quarter of a fragment load) touches at
@@ -178,13 +219,20 @@ __device__ __forceinline__ uint32_t granule(int row, int c) {
     return row * 128u + ((c ^ (row & 7)) << 4);
 }
 
-// One CTA's share. Leaves every warp's O (unnormalised) and (m, l) (m in log2 units) in shared memory
-// and returns after a barrier.
-template <typename T, int NR>
-__device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, uint8_t* smem, SegTable& seg, uint32_t* err) {
+// The state of a warp's rows: this thread's columns of O^T and S^T are rows 8 r + 2 (lane % 4) + e.
+template <int NR>
+struct RowState {
+  float o[NR][4][4], m[NR][2], l[NR][2];  // m in log2 units; l of this thread's keys alone until reduced
+};
+
+// One warp's run of steps [step0, step0 + n_mine). SOLO: the item is one own-key segment of solo_len keys
+// (no table); else the segments are in `seg`.
+template <typename T, int NR, bool SOLO>
+__device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, uint8_t* smem, const SegTable* seg, int solo_len,
+                                       int step0, int n_mine, RowState<NR>& st, uint32_t* err) {
   using C = Cfg<T, NR>;
   constexpr bool F32 = C::F32;
-  constexpr int KW = C::KW, KT = C::KT, ST = C::STAGES;
+  constexpr int KW = C::KW, ST = C::STAGES;
   constexpr int CH = C::ROWB / 16;  // granules per row
   constexpr int RPI = 32 / CH;      // rows a warp's copy instruction covers
   constexpr int NL = KW / RPI;
@@ -192,62 +240,37 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
   const int g = lane >> 2, tq = lane & 3;
   const uint32_t s0 = smem_u32(smem) + warp * (ST * 2 * C::HALF);
 
-  // ---- the segments' tiles: a running sum over up to 33 lengths, by warp 0
-  if (warp == 0) {
-    const int base = (it.prefix_len + KT - 1) / KT;
-    int n = lane < it.n_own ? p.lens[it.seq0 + lane] : 0;
-    if (n < 0 || n > static_cast<long long>(p.max_pages) * p.page_size) {
-      *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (81u << 8);
-      n = 0;
-    }
-    int sum = (n + KT - 1) / KT;
-    if (it.n_own > 1) {
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, sum, d);
-        if (lane >= d) sum += up;
-      }
-    }
-    if (lane == 0) {
-      seg.tile0[0] = 0;
-      seg.len[0] = it.prefix_len;
-      seg.tile0[1] = base;
-    }
-    if (lane < it.n_own) {
-      seg.len[1 + lane] = n;
-      seg.tile0[2 + lane] = base + sum;
-    }
-  }
-  __syncthreads();
-  const int n_tiles = seg.tile0[1 + it.n_own];
-  const int per = (n_tiles + it.n_splits - 1) / it.n_splits;
-  const int tile0 = it.split * per;
-  const int n_mine = max(0, min(per, n_tiles - tile0));
-
-  // ---- tile loads: every warp copies the keys it scores itself. Addresses in units of 16 bytes (32-bit
+  // ---- loads of a step: 16 keys and values. Addresses in units of 16 bytes (32-bit
   // factors, 64-bit sums). Rows RPI i + lr of a stage: two swizzled positions alternate with i.
   const int lc = lane % CH, lr = lane / CH;
   const uint32_t at0 = granule<F32>(lr, lc), at1 = granule<F32>(lr + RPI, lc) - 512u;
   static_assert(RPI * C::ROWB == 512, "a copy instruction covers 512 bytes of a stage");
-  int lseg = 0, lbegin = 0, lend = 0, lkeys = 0;  // segment of the next tile to load, its tiles and keys
-  int next_page = 0;  // page of the key in the next tile's row lane % 16 (own keys), read one tile ahead
+  int lseg = 0, lbegin = 0, lend = 0, lkeys = 0;  // segment of the next step to load, its steps and keys
+  int next_page = 0;  // page of the key in the next step's row lane % 16 (own keys), read one step ahead
   auto advance = [&](int t, int& sg, int& begin, int& end, int& keys) {
-    while (t >= seg.tile0[sg + 1]) ++sg;
-    begin = seg.tile0[sg];
-    end = seg.tile0[sg + 1];
-    keys = seg.len[sg];
+    if constexpr (SOLO) {
+      sg = 1;
+      begin = 0;
+      end = 0x7fffffff;
+      keys = solo_len;
+    } else {
+      while (t >= seg->step0[sg + 1]) ++sg;
+      begin = seg->step0[sg];
+      end = seg->step0[sg + 1];
+      keys = seg->len[sg];
+    }
   };
   auto page_of = [&](int j) {
-    if (tile0 + j >= lend) advance(tile0 + j, lseg, lbegin, lend, lkeys);
-    if (lseg == 0) return;
-    const int key = (tile0 + j - lbegin) * KT + warp * KW + (lane & 15);
+    if (step0 + j >= lend) advance(step0 + j, lseg, lbegin, lend, lkeys);
+    if (!SOLO && lseg == 0) return;
+    const int key = (step0 + j - lbegin) * KW + (lane & 15);
     const int pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
     next_page = key < lkeys ? p.table[(it.seq0 + lseg - 1) * p.table_stride + pi] : -1;
   };
   auto load = [&](int j, int stage) {
     const uint32_t sk = s0 + stage * (2 * C::HALF), sv = sk + C::HALF;
-    const int key0 = (tile0 + j - lbegin) * KT + warp * KW;
-    if (lseg == 0) {
+    const int key0 = (step0 + j - lbegin) * KW;
+    if (!SOLO && lseg == 0) {
       const uint8_t* ks = it.kp + (key0 + lr) * p.k_token + lc * 16;
       const uint8_t* vs = it.vp + (key0 + lr) * p.v_token + lc * 16;
 #pragma unroll
@@ -329,7 +352,9 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
       tok_of[r][e] = (x - seq_of[r][e] * per_seq) / p.r;
     }
 
-  float o[NR][4][4], m[NR][2], u[NR][2], l[NR][2];  // u: the reference in use, 0 while m is -inf
+  auto &o = st.o;
+  auto &m = st.m, &l = st.l;
+  float u[NR][2];  // the reference in use: m, or 0 while that is -inf
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
 #pragma unroll
@@ -354,16 +379,15 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
       if (j + ST < n_mine) page_of(j + ST);
     }
     cp_async_commit();
-    if (tile0 + j >= cend) {
-      advance(tile0 + j, cseg, cbegin, cend, n_keys);
+    if (step0 + j >= cend) {
+      advance(step0 + j, cseg, cbegin, cend, n_keys);
 #pragma unroll
       for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           lim[r][e] = cseg == 0 ? n_keys : seq_of[r][e] == cseg - 1 ? n_keys - p.q_len + 1 + tok_of[r][e] : 0;
     }
-    const int key0 = (tile0 + j - cbegin) * KT + warp * KW;
-    if (key0 >= n_keys) continue;
+    const int key0 = (step0 + j - cbegin) * KW;
     const uint32_t sk = s0 + (j % ST) * (2 * C::HALF), sv = sk + C::HALF;
 
     // ---- S^T: 16 keys x 8 NR rows
@@ -404,7 +428,8 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
       }
     }
     // ---- mask (element e: key g + 8 (e / 2), row column e % 2), then P
-    if (cseg > 0 || key0 + KW > n_keys) {
+    // (one sequence's own keys: only the newest q_len are hidden from some of its rows)
+    if (SOLO ? key0 + KW > n_keys - p.q_len + 1 : cseg > 0 || key0 + KW > n_keys) {
 #pragma unroll
       for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -526,11 +551,7 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
     }
   }
 
-  // ---- the warps' results through shared memory (over the rings)
   cp_async_wait<0>();
-  __syncthreads();
-  float* so = reinterpret_cast<float*>(smem) + warp * C::ROWS * C::OS;
-  float2* sml = reinterpret_cast<float2*>(smem + C::ML) + warp * C::ROWS;
 #pragma unroll
   for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -538,12 +559,27 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
       l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], 4);
       l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], 8);
       l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], 16);
+    }
+}
+
+// All warps' results into shared memory, over the rings; begins and ends with a barrier.
+template <typename T, int NR>
+__device__ __forceinline__ void share_results(uint8_t* smem, const RowState<NR>& st) {
+  using C = Cfg<T, NR>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+  __syncthreads();
+  float* so = reinterpret_cast<float*>(smem) + warp * C::ROWS * C::OS;
+  float2* sml = reinterpret_cast<float2*>(smem + C::ML) + warp * C::ROWS;
+#pragma unroll
+  for (int r = 0; r < NR; ++r)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
       const int x = 8 * r + 2 * tq + e;
-      if (g == 0) sml[x] = make_float2(m[r][e], l[r][e]);
+      if (g == 0) sml[x] = make_float2(st.m[r][e], st.l[r][e]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        so[x * C::OS + (F32 ? 4 * g + i : 16 * i + g)] = o[r][i][e];
-        so[x * C::OS + (F32 ? 32 + 4 * g + i : 16 * i + g + 8)] = o[r][i][e + 2];
+        so[x * C::OS + (C::F32 ? 4 * g + i : 16 * i + g)] = st.o[r][i][e];
+        so[x * C::OS + (C::F32 ? 32 + 4 * g + i : 16 * i + g + 8)] = st.o[r][i][e + 2];
       }
     }
   __syncthreads();
@@ -663,9 +699,12 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
   it.seq0 = begin + first;
   it.row_off = row0 - first * per_seq;
   it.n_own = p.k_pages ? (row0 + it.n_rows - 1) / per_seq - first + 1 : 0;
-  it.split = rank;
-  it.n_splits = p.cluster;
-  attend<T, NR>(p, it, smem_dyn, seg, err);
+  fill_segments(p, it, seg, err);
+  int step0, n_steps;
+  run_of(seg.step0[1 + it.n_own], rank * C::NW + (threadIdx.x >> 5), p.cluster * C::NW, step0, n_steps);
+  RowState<NR> st;
+  attend<T, NR, false>(p, it, smem_dyn, &seg, 0, step0, n_steps, st, err);
+  share_results<T, NR>(smem_dyn, st);
   const int x = threadIdx.x >> 3, c8 = (threadIdx.x & 7) * 8;  // 8 threads a row, 8 elements each
   auto put = [&](int row, const float (&v)[8], float l) {
     const int y = it.row_off + row, tok = y / p.r;
@@ -717,9 +756,19 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
   cluster_arrive_wait();  // no CTA leaves while another reads its results
 }
 
-// Two-launch form: one CTA per (group, key head, split of the prefix, row tile), or (OWN) per
-// (sequence, key head, split of its own keys, row tile); writes its rows' partial results.
-template <typename T, int NR, bool OWN>
+__device__ __forceinline__ void write_partial(const PrefixParams& p, int token, int head, int slot, int c8, const float (&v)[8],
+                                             float m, float l) {
+  const size_t at = (static_cast<size_t>(token) * p.H + head) * (p.np + p.ns) + slot;
+  if (l > 0.0f) {
+    float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + c8);
+    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  if (c8 == 0) p.part_ml[at] = make_float2(m, l);
+}
+
+// Second form, the prefix: one CTA per (group, key head, split, row tile); writes its rows' partial results.
+template <typename T, int NR>
 __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_part_kernel(const PrefixParams p, uint32_t* err) {
   using C = Cfg<T, NR>;
   extern __shared__ __align__(128) uint8_t smem_dyn[];
@@ -730,41 +779,89 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
   Item it;
   const int row0 = (b % p.row_tiles) * C::ROWS;
   b /= p.row_tiles;
-  it.n_splits = OWN ? p.ns : p.np;
-  it.split = b % it.n_splits;
-  b /= it.n_splits;
+  const int split = b % p.np;
+  b /= p.np;
   it.hk = b % p.Hkv;
-  const int which = b / p.Hkv;
-  int begin = which, count = 1;
-  it.kp = p.kp;
-  it.vp = p.vp;
-  it.prefix_len = 0;
-  it.n_own = 1;
-  if (!OWN) {
-    group_range(p, which, begin, count, err);
-    it.kp = p.kp + which * p.k_group + it.hk * C::ROWB;
-    it.vp = p.vp + which * p.v_group + it.hk * C::ROWB;
-    it.prefix_len = prefix_len_of(p, which, err);
-    it.n_own = 0;
-  }
+  const int grp = b / p.Hkv;
+  int begin, count;
+  group_range(p, grp, begin, count, err);
+  it.kp = p.kp + grp * p.k_group + it.hk * C::ROWB;
+  it.vp = p.vp + grp * p.v_group + it.hk * C::ROWB;
+  it.prefix_len = prefix_len_of(p, grp, err);
+  it.n_own = 0;
   it.n_rows = min(count * p.q_len * p.r - row0, C::ROWS);
   if (it.n_rows <= 0) return;
   it.seq0 = begin;
   it.row_off = row0;
-  attend<T, NR>(p, it, smem_dyn, seg, err);
-  const int n_slots = p.np + p.ns, slot = (OWN ? p.np : 0) + it.split;
+  fill_segments(p, it, seg, err);
+  int step0, n_steps;
+  run_of(seg.step0[1], split * C::NW + (threadIdx.x >> 5), p.np * C::NW, step0, n_steps);
+  RowState<NR> st;
+  attend<T, NR, false>(p, it, smem_dyn, &seg, 0, step0, n_steps, st, err);
+  share_results<T, NR>(smem_dyn, st);
   const int x = threadIdx.x >> 3, c8 = (threadIdx.x & 7) * 8;
   if (x >= it.n_rows) return;
   float v[8], m, l;
   join_warps<T, NR>(smem_dyn, x, c8, v, m, l);
-  const int y = row0 + x, tok = y / p.r, head = it.hk * p.r + y - tok * p.r;
-  const size_t at = ((static_cast<size_t>(begin) * p.q_len + tok) * p.H + head) * n_slots + slot;
-  if (l > 0.0f) {
-    float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + c8);
-    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+  const int y = row0 + x, tok = y / p.r;
+  write_partial(p, begin * p.q_len + tok, it.hk * p.r + y - tok * p.r, split, c8, v, m, l);
+}
+
+// Second form, own keys: one warp per (sequence, key head, row tile, split); its rows go through the
+// warp's stretch of shared memory to full lines of the partial results.
+template <typename T, int NR>
+__global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_own_kernel(const PrefixParams p, long long n_items,
+                                                                                       uint32_t* err) {
+  using C = Cfg<T, NR>;
+  static_assert(C::STAGES * 2 * C::HALF >= 8 * C::OS * 4, "a warp's ring holds eight rows of results");
+  extern __shared__ __align__(128) uint8_t smem_dyn[];
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+  long long b = static_cast<long long>(blockIdx.x) * C::NW + warp;
+  if (b >= n_items) return;
+  Item it;
+  const int split = static_cast<int>(b % p.ns);
+  b /= p.ns;
+  const int row0 = static_cast<int>(b % p.row_tiles) * C::ROWS;
+  b /= p.row_tiles;
+  it.hk = static_cast<int>(b % p.Hkv);
+  it.seq0 = static_cast<int>(b / p.Hkv);
+  it.n_own = 1;
+  it.row_off = row0;
+  it.n_rows = min(p.q_len * p.r - row0, C::ROWS);
+  const int len = own_len_of(p, it.seq0, err);
+  int step0, n_steps;
+  run_of((len + 15) / 16, split, p.ns, step0, n_steps);
+  RowState<NR> st;
+  attend<T, NR, true>(p, it, smem_dyn, nullptr, len, step0, n_steps, st, err);
+  float* so = reinterpret_cast<float*>(smem_dyn + warp * (C::STAGES * 2 * C::HALF));
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        so[(2 * tq + e) * C::OS + (C::F32 ? 4 * g + i : 16 * i + g)] = st.o[r][i][e];
+        so[(2 * tq + e) * C::OS + (C::F32 ? 32 + 4 * g + i : 16 * i + g + 8)] = st.o[r][i][e + 2];
+      }
+    __syncwarp();
+    const int c8 = (lane & 7) * 8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // four rows at a time, eight lanes each
+      const int x = 4 * h + (lane >> 3), y = row0 + 8 * r + x, tok = y / p.r;
+      // row x's maximum and sum sit in the lanes of column pair x / 2, element x % 2
+      const float m0 = __shfl_sync(0xffffffffu, st.m[r][0], x >> 1), m1 = __shfl_sync(0xffffffffu, st.m[r][1], x >> 1);
+      const float l0 = __shfl_sync(0xffffffffu, st.l[r][0], x >> 1), l1 = __shfl_sync(0xffffffffu, st.l[r][1], x >> 1);
+      if (8 * r + x < it.n_rows) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = so[x * C::OS + c8 + e];
+        write_partial(p, it.seq0 * p.q_len + tok, it.hk * p.r + y - tok * p.r, p.np + split, c8, v, x & 1 ? m1 : m0, x & 1 ? l1 : l0);
+      }
+    }
   }
-  if (c8 == 0) p.part_ml[at] = make_float2(m, l);
 }
 
 // Join of the partial results of one (token, head): sixteen lanes, four elements each.
@@ -789,24 +886,45 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PrefixParams p) 
     const int begin = p.group_start[lo], end = p.group_start[lo + 1];
     if (seq < begin || seq >= end || begin < 0 || end > p.n_seqs || end - begin > p.max_group) return;
   }
+  // lane c4 weighs slots c4, c4 + 16, ...; then every lane adds its four elements of all slots, several
+  // loads in flight (slots without keys wrote no O: weight 0, not read)
   const int n = p.np + p.ns;
   const float2* ml = p.part_ml + pair * n;
   const float* po = p.part_o + pair * n * HD + c4 * 4;
+  const uint32_t lanes = 0xffffu << (threadIdx.x & 16);  // this row's half of the warp
   float m = -CUDART_INF_F;
-  for (int i = 0; i < n; ++i) m = fmaxf(m, ml[i].x);
+  for (int i = c4; i < n; i += 16) m = fmaxf(m, ml[i].x);
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, d));
   const float u = m == -CUDART_INF_F ? 0.0f : m;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.0f;
-  for (int i = 0; i < n; ++i) {
-    const float2 x = ml[i];
-    if (!(x.y > 0.0f)) continue;  // an empty share wrote no O
-    const float f = ex2_approx(x.x - u);
-    const float4 o = *reinterpret_cast<const float4*>(po + static_cast<size_t>(i) * HD);
-    acc.x += f * o.x;
-    acc.y += f * o.y;
-    acc.z += f * o.z;
-    acc.w += f * o.w;
-    l += f * x.y;
+  for (int i0 = 0; i0 < n; i0 += 16) {
+    const float2 x = i0 + c4 < n ? ml[i0 + c4] : make_float2(0.0f, 0.0f);
+    const float f = x.y > 0.0f ? ex2_approx(x.x - u) : 0.0f;
+    float part = f * x.y;
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) part += __shfl_xor_sync(lanes, part, d);
+    l += part;
+    const int k = min(16, n - i0);
+    for (int j0 = 0; j0 < k; j0 += 8) {
+      float w[8];
+      float4 o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        w[j] = __shfl_sync(lanes, f, (j0 + j) & 15, 16);
+        if (j0 + j >= k) w[j] = 0.0f;
+        o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w[j] > 0.0f) o[j] = *reinterpret_cast<const float4*>(po + static_cast<size_t>(i0 + j0 + j) * HD);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        acc.x += w[j] * o[j].x;
+        acc.y += w[j] * o[j].y;
+        acc.z += w[j] * o[j].z;
+        acc.w += w[j] * o[j].w;
+      }
+    }
   }
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
   uint8_t* dst = p.out + token * p.out_stride + (head * HD + c4 * 4) * sizeof(T);
@@ -842,7 +960,7 @@ int row_groups(long long rows, bool f32) { return rows <= 8 ? 1 : rows <= 16 || 
 Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
   Plan pl;
   const bool f32 = a->dtype == WENC_DTYPE_F32;
-  const int kt = f32 ? Cfg<float, 1>::KT : Cfg<__nv_bfloat16, 1>::KT;
+  const int kt = f32 ? 16 * Cfg<float, 1>::NW : 16 * Cfg<__nv_bfloat16, 1>::NW;  // keys of one step of a CTA
   const long long r = a->n_heads / a->n_kv_heads;
   const long long rows_s = a->q_len * r;  // rows of one sequence per key head
   const long long group = a->k_prefix ? a->max_group : 1, n_groups = a->k_prefix ? a->n_groups : a->n_seqs;
@@ -888,8 +1006,12 @@ Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
   if (a->k_pages) {
     pl.nr_s = row_groups(rows_s, f32);
     pl.rows_s = static_cast<int>((rows_s + 8 * pl.nr_s - 1) / (8 * pl.nr_s));
+    // warps: about one round of the machine (24 an SM), no split of fewer than 64 keys
     const long long items = static_cast<long long>(a->n_seqs) * a->n_kv_heads * pl.rows_s;
-    pl.ns = splits(items, own_cap);
+    long long n = (24ll * sms + items - 1) / items;
+    if (n > (own_cap + 63) / 64) n = (own_cap + 63) / 64;
+    if (n > 32) n = 32;
+    pl.ns = static_cast<int>(n < 1 ? 1 : n);
     pl.items_s = items * pl.ns;
   }
   const size_t n = static_cast<size_t>(a->n_seqs) * a->q_len * a->n_heads * (pl.np + pl.ns);
@@ -976,15 +1098,27 @@ cudaError_t launch_cluster(const PrefixParams& p, long long blocks, uint32_t* er
   return cudaLaunchKernelEx(&cfg, kern, p, err);
 }
 
-template <typename T, int NR, bool OWN>
+template <typename T, int NR>
 cudaError_t launch_part(PrefixParams p, int row_tiles, long long blocks, uint32_t* err, cudaStream_t stream) {
   using C = Cfg<T, NR>;
-  auto kern = prefix_part_kernel<T, NR, OWN>;
+  auto kern = prefix_part_kernel<T, NR>;
   static std::atomic<int> configured{-1};
   const cudaError_t e = opt_in(kern, C::SMEM, configured);
   if (e != cudaSuccess) return e;
   p.row_tiles = row_tiles;
   return wenc_host::launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(C::THREADS), C::SMEM, stream, p, err);
+}
+
+template <typename T, int NR>
+cudaError_t launch_own(PrefixParams p, int row_tiles, long long items, uint32_t* err, cudaStream_t stream) {
+  using C = Cfg<T, NR>;
+  auto kern = prefix_own_kernel<T, NR>;
+  static std::atomic<int> configured{-1};
+  const cudaError_t e = opt_in(kern, C::RING + C::P_BYTES, configured);
+  if (e != cudaSuccess) return e;
+  p.row_tiles = row_tiles;
+  return wenc_host::launch_pdl(kern, dim3(static_cast<unsigned>((items + C::NW - 1) / C::NW)), dim3(C::THREADS),
+                               C::RING + C::P_BYTES, stream, p, items, err);
 }
 
 // The prefix part on tcgen05.
@@ -1039,11 +1173,11 @@ cudaError_t launch_all(PrefixParams p, const Plan& pl, uint32_t* err, cudaStream
   }
   constexpr int kMost = F32 ? 2 : 4;  // (more than 64 rows: the largest tiles)
   cudaError_t e = cudaSuccess;
-  if (pl.items_p > 0 && !pl.tc) e = launch_part<T, kMost, false>(p, pl.rows_p, pl.items_p, err, stream);
+  if (pl.items_p > 0 && !pl.tc) e = launch_part<T, kMost>(p, pl.rows_p, pl.items_p, err, stream);
   if (e == cudaSuccess && pl.items_s > 0) {
-    if (pl.nr_s == 1) e = launch_part<T, 1, true>(p, pl.rows_s, pl.items_s, err, stream);
-    else if (pl.nr_s == 2) e = launch_part<T, 2, true>(p, pl.rows_s, pl.items_s, err, stream);
-    else e = launch_part<T, kMost, true>(p, pl.rows_s, pl.items_s, err, stream);
+    if (pl.nr_s == 1) e = launch_own<T, 1>(p, pl.rows_s, pl.items_s, err, stream);
+    else if (pl.nr_s == 2) e = launch_own<T, 2>(p, pl.rows_s, pl.items_s, err, stream);
+    else e = launch_own<T, kMost>(p, pl.rows_s, pl.items_s, err, stream);
   }
   if (e != cudaSuccess) return e;
   const long long threads = static_cast<long long>(p.n_seqs) * p.q_len * p.H * 16;
