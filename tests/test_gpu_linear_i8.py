@@ -25,7 +25,7 @@ def _cuda(a):
 
 # ------------------------------------------------------------------ quantize_rows
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("rows,d", [(1, 16), (1, 384), (3, 48), (80, 1280), (7, 2032), (5, 5120), (2, 4112), (3, 20480),
+@pytest.mark.parametrize("rows,d", [(1, 16), (1, 384), (3, 48), (80, 1280), (7, 2032), (5, 5120), (2, 4112), (3, 20480), (2, 32784), (1, 65552),
                                     (1025, 512)])
 def test_quantize_rows_is_exact(dtype, rows, d):
     import torch

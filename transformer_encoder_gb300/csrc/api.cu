@@ -100,13 +100,11 @@ uint32_t* global_error_word(std::string* why) {
 }
 
 bool device_is_sm103(std::string* why) {
-  static std::atomic<bool> known[64] = {};  // devices found right before
   int dev = 0, major = 0, minor = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     *why = "no CUDA device";
     return false;
   }
-  if (dev >= 0 && dev < 64 && known[dev].load(std::memory_order_relaxed)) return true;
   cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
   cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
   if (major != 10 || minor != 3) {
@@ -115,17 +113,13 @@ bool device_is_sm103(std::string* why) {
     *why = b;
     return false;
   }
-  if (dev >= 0 && dev < 64) known[dev].store(true, std::memory_order_relaxed);
   return true;
 }
 
 int sm_count() {
-  static std::atomic<int> known[64] = {};
   int dev = 0, n = 0;
   cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  if (n > 0 && dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n > 0 ? n : 1;
 }
 
@@ -521,6 +515,31 @@ void wenc_internal_clear_error() { g_last_error.clear(); }
 uint32_t* wenc_internal_error_word(std::string* why) { return global_error_word(why); }
 bool wenc_internal_is_sm103(std::string* why) { return device_is_sm103(why); }
 int wenc_internal_sm_count() { return sm_count(); }
+// What a handle-less call needs of the current device, with one runtime call once it is known.
+wenc_status wenc_internal_device(int* sms, uint32_t** err) {
+  struct Known {
+    std::atomic<int> sms{0};
+    uint32_t* err = nullptr;
+  };
+  static Known known[64];
+  int dev = -1;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64) {
+    const int n = known[dev].sms.load(std::memory_order_acquire);
+    if (n > 0) {
+      *sms = n;
+      *err = known[dev].err;
+      return WENC_OK;
+    }
+  }
+  std::string why;
+  if (!device_is_sm103(&why)) return fail(WENC_ERR_UNSUPPORTED, "%s", why.c_str());
+  *err = global_error_word(&why);
+  if (!*err) return fail(WENC_ERR_CUDA, "%s", why.c_str());
+  *sms = sm_count();
+  known[dev].err = *err;  // host threads that race here store the same address
+  known[dev].sms.store(*sms, std::memory_order_release);
+  return WENC_OK;
+}
 
 extern "C" {
 

@@ -34,9 +34,7 @@
 
 wenc_status wenc_internal_fail(wenc_status s, const char* msg);
 void wenc_internal_clear_error();
-uint32_t* wenc_internal_error_word(std::string* why);
-bool wenc_internal_is_sm103(std::string* why);
-int wenc_internal_sm_count();
+wenc_status wenc_internal_device(int* sms, uint32_t** err);
 
 namespace {
 
@@ -44,7 +42,7 @@ using namespace wenc_dev;
 
 constexpr int HD = 64;
 constexpr int kWarps = 8;    // per block
-constexpr int kUnroll = 4;   // 16-byte loads a lane keeps in flight
+constexpr int kUnroll = 8;   // 16-byte loads a lane keeps in flight
 
 struct AppendParams {
   const uint8_t *q, *k, *v;             // rows of 64 elements, heads contiguous
@@ -156,6 +154,22 @@ __global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const AppendPara
 
   int s = -1, begin = 0, end = 0;
   for (int t = static_cast<int>(t0); t < t1; ++t) {
+    // ---- its first rows (queries, keys, values) are on their way while its place and angles are found
+    uint4 x[kUnroll];
+    auto fetch = [&](int r0) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int r = r0 + u * wpt * RPW + sub;
+        x[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (r >= rows) continue;
+        const uint8_t* src = r < n_q ? p.q + t * p.q_stride + r * static_cast<int>(HD * sizeof(T))
+                             : r < n_q + p.Hkv
+                                 ? p.k + t * p.k_stride + (r - n_q) * static_cast<int>(HD * sizeof(T))
+                                 : p.v + t * p.v_stride + (r - n_q - p.Hkv) * static_cast<int>(HD * sizeof(T));
+        x[u] = *reinterpret_cast<const uint4*>(src + piece * 16);
+      }
+    };
+    fetch(share * RPW);
     // ---- the token's sequence, cache position and page
     if (p.seq_start) {
       if (t >= end) {
@@ -212,20 +226,9 @@ __global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const AppendPara
       __syncwarp();
     }
 
-    // ---- its rows: queries, keys, values
+    // ---- turned and stored
     for (int r0 = share * RPW; r0 < rows; r0 += wpt * RPW * kUnroll) {
-      uint4 x[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int r = r0 + u * wpt * RPW + sub;
-        x[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (r >= rows) continue;
-        const uint8_t* src = r < n_q ? p.q + t * p.q_stride + r * static_cast<int>(HD * sizeof(T))
-                             : r < n_q + p.Hkv
-                                 ? p.k + t * p.k_stride + (r - n_q) * static_cast<int>(HD * sizeof(T))
-                                 : p.v + t * p.v_stride + (r - n_q - p.Hkv) * static_cast<int>(HD * sizeof(T));
-        x[u] = *reinterpret_cast<const uint4*>(src + piece * 16);
-      }
+      if (r0 != share * RPW) fetch(r0);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int r = r0 + u * wpt * RPW + sub;
@@ -315,10 +318,10 @@ extern "C" wenc_status wenc_kv_append(const wenc_kv_append_args* a, wenc_stream_
   for (long long x : strides)
     if (x % per16 != 0) return bad(WENC_ERR_INVALID_ARG, "strides must be multiples of 16 bytes");
   if (a->n_tokens == 0) return WENC_OK;
-  std::string why;
-  if (!wenc_internal_is_sm103(&why)) return wenc_internal_fail(WENC_ERR_UNSUPPORTED, why.c_str());
-  uint32_t* err = wenc_internal_error_word(&why);
-  if (!err) return wenc_internal_fail(WENC_ERR_CUDA, why.c_str());
+  int sms = 0;
+  uint32_t* err = nullptr;
+  const wenc_status dst = wenc_internal_device(&sms, &err);
+  if (dst != WENC_OK) return dst;
 
   AppendParams p;
   p.q = static_cast<const uint8_t*>(a->q);
@@ -352,7 +355,6 @@ extern "C" wenc_status wenc_kv_append(const wenc_kv_append_args* a, wenc_stream_
   // queries that neither turn nor move need no pass
   if (p.half == 0 && p.q == p.q_out) p.q = nullptr;
 
-  const int sms = wenc_internal_sm_count();
   const int rpw = a->dtype == WENC_DTYPE_F32 ? 2 : 4;
   const int rows = (p.q ? p.H : 0) + 2 * p.Hkv;
   // Few tokens: several warps share one token's rows, so that the rows' loads go out together.

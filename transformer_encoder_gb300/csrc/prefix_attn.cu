@@ -45,9 +45,8 @@
 
 wenc_status wenc_internal_fail(wenc_status s, const char* msg);
 void wenc_internal_clear_error();
-uint32_t* wenc_internal_error_word(std::string* why);
-bool wenc_internal_is_sm103(std::string* why);
 int wenc_internal_sm_count();
+wenc_status wenc_internal_device(int* sms, uint32_t** err);
 
 namespace {
 
@@ -1094,7 +1093,7 @@ cudaError_t launch_cluster(const PrefixParams& p, long long blocks, uint32_t* er
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = p.cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p, err);
 }
 
@@ -1224,11 +1223,11 @@ extern "C" wenc_status wenc_prefix_attention(const wenc_prefix_attention_args* a
                                a->k_pages ? a->k_page_stride : zero, a->k_pages ? a->v_page_stride : zero};
   for (long long x : strides)
     if (x % per16 != 0) return bad(WENC_ERR_INVALID_ARG, "strides must be multiples of 16 bytes");
-  std::string why;
-  if (!wenc_internal_is_sm103(&why)) return wenc_internal_fail(WENC_ERR_UNSUPPORTED, why.c_str());
-  uint32_t* err = wenc_internal_error_word(&why);
-  if (!err) return wenc_internal_fail(WENC_ERR_CUDA, why.c_str());
-  const Plan pl = make_plan(a, wenc_internal_sm_count());
+  int sms = 0;
+  uint32_t* err = nullptr;
+  const wenc_status dst = wenc_internal_device(&sms, &err);
+  if (dst != WENC_OK) return dst;
+  const Plan pl = make_plan(a, sms);
   if (pl.items_p > 0x7fffffffll || pl.items_s > 0x7fffffffll)
     return bad(WENC_ERR_UNSUPPORTED, "prefix_attention: %lld work items pass 2^31 - 1", pl.items_p > pl.items_s ? pl.items_p : pl.items_s);
   if (pl.bytes > 0 && (!a->workspace || a->workspace_bytes < pl.bytes))
@@ -1291,7 +1290,7 @@ extern "C" wenc_status wenc_prefix_attention(const wenc_prefix_attention_args* a
   p.part_o = static_cast<float*>(a->workspace);
   p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(a->workspace) + pl.part_o);
   if (pl.tc) {
-    st = launch_tc(a, p, pl, err, wenc_internal_sm_count(), reinterpret_cast<cudaStream_t>(stream));
+    st = launch_tc(a, p, pl, err, sms, reinterpret_cast<cudaStream_t>(stream));
     if (st != WENC_OK) return st;
   }
   const cudaError_t e = a->dtype == WENC_DTYPE_F32

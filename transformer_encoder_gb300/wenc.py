@@ -432,8 +432,23 @@ def attention_tf32(q, k, v, out=None, stream=None):
     return out
 
 
-def _elsewhere(dev, named):
-    """The error for a tensor that is not on the current CUDA device, where the library launches."""
+# The decode-side calls below run once per layer and token, so what they cost on the host counts: the
+# common case (packed tensors) is checked with few attribute reads, anything else more slowly.
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    lib()
+    return torch
+
+
+def _elsewhere(named):
+    """The error for tensors that are not on the current CUDA device, where the library launches."""
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
     for name, t in named:
         if t is not None and not t.is_cuda:
             return TypeError(f"{name} must be a CUDA tensor")
@@ -442,26 +457,15 @@ def _elsewhere(dev, named):
     return RuntimeError("tensors on several devices")
 
 
-def _current_device():
-    import torch
-    return torch.cuda.current_device() if torch.cuda.is_available() else -2
-
-
 def _raw_stream(stream, dev):
-    import torch
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _ints(t, name, shape):
-    """The address of a contiguous int32 tensor of this shape."""
-    import torch
-    if t.dtype is not torch.int32:
-        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
+def _bad_ints(t, name, n):
+    return (TypeError(f"{name} must be torch.int32, got {t.dtype}") if t.dtype is not _torch.int32 else
+            ValueError(f"{name} must be contiguous with shape ({n},), got {tuple(t.shape)}"))
 
 
 def _token_stride(t, name):
@@ -481,9 +485,25 @@ def _token_stride(t, name):
     return st[0] if shape[0] > 1 else heads * hd
 
 
+def _plane_strides(t, name):
+    """(elements between groups, between tokens) of [groups, tokens, heads, 64], heads packed."""
+    (G, T, heads, hd), st = t.shape, t.stride()
+    if st[3] != 1 or heads > 1 and st[2] != hd:
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return (st[0] if G > 1 else 0), (st[1] if T > 1 else heads * hd)
+
+
+def _page_stride(t, name):
+    """Elements between the pages of [pages, page_size, heads, 64], each page packed."""
+    (n, size, heads, hd), st = t.shape, t.stride()
+    if st[3] != 1 or st[2] != hd and heads > 1 or st[1] != heads * hd and size > 1:
+        raise ValueError(f"{name}: each page must be contiguous")
+    return st[0] if n > 1 else size * heads * hd
+
+
 def _pool(k_pages, v_pages, dtype, heads):
     """(pages, page size, stride of K pages, of V pages) of a paged cache [pages, page_size, heads, 64]."""
-    shape, ks, vs = k_pages.shape, k_pages.stride(), v_pages.stride()
+    shape = k_pages.shape
     if k_pages.dtype is not dtype or v_pages.dtype is not dtype:
         raise TypeError(f"k_pages and v_pages must be {dtype}, got {k_pages.dtype} and {v_pages.dtype}")
     if len(shape) != 4 or shape[2] != heads or v_pages.shape != shape:
@@ -491,32 +511,27 @@ def _pool(k_pages, v_pages, dtype, heads):
                          f"{tuple(v_pages.shape)}")
     n, size, _, hd = shape
     row = size * heads * hd
-    for name, st in (("k_pages", ks), ("v_pages", vs)):
-        if st[3] != 1 or st[2] != hd and heads > 1 or st[1] != heads * hd and size > 1:
-            raise ValueError(f"{name}: each page must be contiguous")
-    return n, size, (ks[0] if n > 1 else row), (vs[0] if n > 1 else row)
+    return (n, size, row if k_pages.is_contiguous() else _page_stride(k_pages, "k_pages"),
+            row if v_pages.is_contiguous() else _page_stride(v_pages, "v_pages"))
 
 
 def _table(t, n_seqs):
-    """(address, row stride, columns) of a block table."""
-    import torch
-    shape, st = t.shape, t.stride()
-    if t.dtype is not torch.int32:
+    """(row stride, columns) of a block table."""
+    shape = t.shape
+    if t.dtype is not _torch.int32:
         raise TypeError(f"block_table must be torch.int32, got {t.dtype}")
     if len(shape) != 2 or shape[0] != n_seqs:
         raise ValueError(f"block_table must be [{n_seqs}, pages], got {tuple(shape)}")
-    if shape[1] > 1 and st[1] != 1:
+    cols = shape[1]
+    if t.is_contiguous():
+        return cols, cols
+    if cols > 1 and t.stride(1) != 1:
         raise ValueError("block_table: the entries of a sequence must be contiguous")
-    return t.data_ptr(), (st[0] if n_seqs > 1 else shape[1]), shape[1]
+    return (t.stride(0) if n_seqs > 1 else cols), cols
 
 
-def _dtype_code(t, name):
-    import torch
-    if t.dtype is torch.bfloat16:
-        return 1
-    if t.dtype is torch.float32:
-        return 0
-    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+def _dtype_error(t, name):
+    return TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
 
 def _scratch(nbytes, like, stream):
@@ -546,58 +561,68 @@ def prefix_attention(q, k_prefix=None, v_prefix=None, *, prefix_lens=None, group
     ``workspace``: a uint8 tensor to use instead of an allocation where one is needed; it is busy
     until the call's work is done.
     """
-    import torch
+    torch = _torch or _load_torch()
     dtype = q.dtype
-    dt = _dtype_code(q, "q")
-    if q.dim() != 4:
-        raise ValueError(f"q must be [n_seqs, q_len, heads, 64], got {tuple(q.shape)}")
+    dt = 1 if dtype is torch.bfloat16 else 0
+    if not dt and dtype is not torch.float32:
+        raise _dtype_error(q, "q")
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError(f"q must be [n_seqs, q_len, heads, 64], got {tuple(shape)}")
     if (k_prefix is None) != (v_prefix is None) or (k_pages is None) != (v_pages is None):
         raise ValueError("keys and values come together")
     if k_prefix is None and k_pages is None:
         raise ValueError("neither a prefix nor pages")
-    n, t, H, hd = q.shape
+    n, t, H, hd = shape
     dev = q.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise _elsewhere(_current_device(), (("q", q),))
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise _elsewhere((("q", q),))
     if out is None:
-        out = torch.empty((n, t, H, hd), dtype=dtype, device=q.device)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
         out_stride = H * hd
     else:
-        if out.dtype is not dtype or out.shape != q.shape:
-            raise ValueError(f"out must be {dtype} {tuple(q.shape)}, got {out.dtype} {tuple(out.shape)}")
-        out_stride = _token_stride(out, "out")
+        if out.dtype is not dtype or out.shape != shape:
+            raise ValueError(f"out must be {dtype} {tuple(shape)}, got {out.dtype} {tuple(out.shape)}")
+        out_stride = H * hd if out.is_contiguous() else _token_stride(out, "out")
         if out.get_device() != dev:
-            raise _elsewhere(dev, (("out", out),))
+            raise _elsewhere((("out", out),))
     kv = G = S = T = kp = vp = kg = kt = vg = vt = p_lens = g_start = 0
     if k_prefix is not None:
-        shape, ks, vs = k_prefix.shape, k_prefix.stride(), v_prefix.stride()
+        kshape = k_prefix.shape
         if k_prefix.dtype is not dtype or v_prefix.dtype is not dtype:
             raise TypeError(f"k_prefix and v_prefix must be {dtype}, got {k_prefix.dtype} and {v_prefix.dtype}")
-        if len(shape) != 4 or shape[3] != hd or v_prefix.shape != shape:
-            raise ValueError(f"k_prefix and v_prefix must be [groups, tokens, heads, {hd}], got {tuple(shape)} and "
+        if len(kshape) != 4 or kshape[3] != hd or v_prefix.shape != kshape:
+            raise ValueError(f"k_prefix and v_prefix must be [groups, tokens, heads, {hd}], got {tuple(kshape)} and "
                              f"{tuple(v_prefix.shape)}")
-        G, T, kv, _ = shape
-        if ks[3] != 1 or vs[3] != 1 or kv > 1 and (ks[2] != hd or vs[2] != hd):
-            raise ValueError("k_prefix and v_prefix: the heads of a token must be contiguous")
+        G, T, kv, _ = kshape
+        kg = vg = T * kv * hd
+        kt = vt = kv * hd
+        if not k_prefix.is_contiguous():
+            kg, kt = _plane_strides(k_prefix, "k_prefix")
+        if not v_prefix.is_contiguous():
+            vg, vt = _plane_strides(v_prefix, "v_prefix")
         if k_prefix.get_device() != dev or v_prefix.get_device() != dev:
-            raise _elsewhere(dev, (("k_prefix", k_prefix), ("v_prefix", v_prefix)))
-        if G > 1:
-            kg, vg = ks[0], vs[0]
-        kt, vt = (ks[1], vs[1]) if T > 1 else (kv * hd, kv * hd)
+            raise _elsewhere((("k_prefix", k_prefix), ("v_prefix", v_prefix)))
         kp, vp = k_prefix.data_ptr(), v_prefix.data_ptr()
         if group_start is not None:
-            g_start = _ints(group_start, "group_start", (G + 1,))
-            S = n if max_group is None else min(max_group, n)
+            if (group_start.dtype is not torch.int32 or group_start.dim() != 1 or group_start.numel() != G + 1
+                    or not group_start.is_contiguous()):
+                raise _bad_ints(group_start, "group_start", G + 1)
             if group_start.get_device() != dev:
-                raise _elsewhere(dev, (("group_start", group_start),))
+                raise _elsewhere((("group_start", group_start),))
+            g_start = group_start.data_ptr()
+            S = n if max_group is None else min(max_group, n)
         elif G == 0 or n % G != 0:
             raise ValueError(f"{n} sequences are no multiple of {G} groups (pass group_start)")
         else:
             S = n // G
         if prefix_lens is not None:
-            p_lens = _ints(prefix_lens, "prefix_lens", (G,))
+            if (prefix_lens.dtype is not torch.int32 or prefix_lens.dim() != 1 or prefix_lens.numel() != G
+                    or not prefix_lens.is_contiguous()):
+                raise _bad_ints(prefix_lens, "prefix_lens", G)
             if prefix_lens.get_device() != dev:
-                raise _elsewhere(dev, (("prefix_lens", prefix_lens),))
+                raise _elsewhere((("prefix_lens", prefix_lens),))
+            p_lens = prefix_lens.data_ptr()
     elif prefix_lens is not None or group_start is not None:
         raise ValueError("prefix_lens and group_start go with a prefix")
     pages = size = kps = vps = kpg = vpg = tab = tab_stride = max_pages = own = 0
@@ -607,29 +632,29 @@ def prefix_attention(q, k_prefix=None, v_prefix=None, *, prefix_lens=None, group
         if k_prefix is None and k_pages.dim() == 4:
             kv = k_pages.shape[2]
         pages, size, kps, vps = _pool(k_pages, v_pages, dtype, kv)
-        tab, tab_stride, max_pages = _table(block_table, n)
-        own = _ints(lens, "lens", (n,))
-        kpg, vpg = k_pages.data_ptr(), v_pages.data_ptr()
+        tab_stride, max_pages = _table(block_table, n)
+        if lens.dtype is not torch.int32 or lens.dim() != 1 or lens.numel() != n or not lens.is_contiguous():
+            raise _bad_ints(lens, "lens", n)
         if (k_pages.get_device() != dev or v_pages.get_device() != dev or block_table.get_device() != dev
                 or lens.get_device() != dev):
-            raise _elsewhere(dev, (("k_pages", k_pages), ("v_pages", v_pages), ("block_table", block_table),
-                                   ("lens", lens)))
+            raise _elsewhere((("k_pages", k_pages), ("v_pages", v_pages), ("block_table", block_table), ("lens", lens)))
+        kpg, vpg, tab, own = k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), lens.data_ptr()
     elif block_table is not None or lens is not None:
         raise ValueError("block_table and lens go with pages")
-    L = _lib or lib()
-    args = (dt, n, t, H, kv, hd, q.data_ptr(), out.data_ptr(), _token_stride(q, "q"), out_stride, G, S, g_start, kp, vp, kg,
+    args = (dt, n, t, H, kv, hd, q.data_ptr(), out.data_ptr(),
+            H * hd if q.is_contiguous() else _token_stride(q, "q"), out_stride, G, S, g_start, kp, vp, kg,
             kt, vg, vt, T, p_lens, kpg, vpg, kps, vps, pages, size, tab, tab_stride, max_pages, own, scale)
     ws = ws_bytes = 0
     # (up to 64 rows per key head need no workspace, as the library's own count confirms)
     if workspace is not None or (S or 1) * t * H > 64 * kv:
         if workspace is None:
-            need = L.wenc_prefix_attention_workspace(_PREFIX_PACK.pack(*args, 0, 0))
+            need = _lib.wenc_prefix_attention_workspace(_PREFIX_PACK.pack(*args, 0, 0))
             workspace = _scratch(need, q, stream) if need else None
         elif workspace.get_device() != dev:
-            raise _elsewhere(dev, (("workspace", workspace),))
+            raise _elsewhere((("workspace", workspace),))
         if workspace is not None:
             ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    status = L.wenc_prefix_attention(_PREFIX_PACK.pack(*args, ws, ws_bytes), _raw_stream(stream, dev))
+    status = _lib.wenc_prefix_attention(_PREFIX_PACK.pack(*args, ws, ws_bytes), _raw_stream(stream, dev))
     if status:
         _check(status)
     return out
@@ -647,53 +672,77 @@ def kv_append(k, v, k_pages, v_pages, block_table, lens, *, seq_start=None, q=No
     (None: the cache positions); ``inv_freq`` float32 [rot_dim / 2] (None: no rotation). ``q_out``
     may be ``q``; without it the turned queries go to a new tensor, whose padding rows are zeros.
     """
-    import torch
+    torch = _torch or _load_torch()
     dtype = k.dtype
-    dt = _dtype_code(k, "k")
-    if k.dim() != 3 or v.shape != k.shape or v.dtype is not dtype:
-        raise ValueError(f"k and v must be {dtype} [tokens, heads, 64], got {tuple(k.shape)} and {v.dtype} {tuple(v.shape)}")
-    n, kv, hd = k.shape
+    dt = 1 if dtype is torch.bfloat16 else 0
+    if not dt and dtype is not torch.float32:
+        raise _dtype_error(k, "k")
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape or v.dtype is not dtype:
+        raise ValueError(f"k and v must be {dtype} [tokens, heads, 64], got {tuple(shape)} and {v.dtype} {tuple(v.shape)}")
+    n, kv, hd = shape
     dev = k.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise _elsewhere(_current_device(), (("k", k),))
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise _elsewhere((("k", k),))
+    i32 = torch.int32
     H = qp = qo = qs = qos = 0
     if q is not None:
+        qshape = q.shape
         if q.dtype is not dtype:
             raise TypeError(f"q must be {dtype}, got {q.dtype}")
-        if q.dim() != 3 or q.shape[0] != n or q.shape[2] != hd:
-            raise ValueError(f"q must be [{n}, heads, {hd}], got {tuple(q.shape)}")
+        if len(qshape) != 3 or qshape[0] != n or qshape[2] != hd:
+            raise ValueError(f"q must be [{n}, heads, {hd}], got {tuple(qshape)}")
         if q_out is None:
-            q_out = torch.zeros(q.shape, dtype=dtype, device=q.device)
-        elif q_out.dtype is not dtype or q_out.shape != q.shape:
-            raise ValueError(f"q_out must be {dtype} {tuple(q.shape)}, got {q_out.dtype} {tuple(q_out.shape)}")
-        H, qp, qo = q.shape[1], q.data_ptr(), q_out.data_ptr()
-        qs, qos = _token_stride(q, "q"), _token_stride(q_out, "q_out")
+            q_out = torch.zeros(qshape, dtype=dtype, device=q.device)
+        elif q_out.dtype is not dtype or q_out.shape != qshape:
+            raise ValueError(f"q_out must be {dtype} {tuple(qshape)}, got {q_out.dtype} {tuple(q_out.shape)}")
+        if q.get_device() != dev or q_out.get_device() != dev:
+            raise _elsewhere((("q", q), ("q_out", q_out)))
+        H = qshape[1]
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+        qs = H * hd if q.is_contiguous() else _token_stride(q, "q")
+        qos = H * hd if q_out.is_contiguous() else _token_stride(q_out, "q_out")
     elif q_out is not None:
         raise ValueError("q_out goes with q")
-    n_seqs = lens.shape[0]
+    n_seqs = lens.numel()
+    if lens.dtype is not i32 or lens.dim() != 1 or not lens.is_contiguous():
+        raise _bad_ints(lens, "lens", n_seqs)
     pages, size, kps, vps = _pool(k_pages, v_pages, dtype, kv)
-    tab, tab_stride, max_pages = _table(block_table, n_seqs)
-    own = _ints(lens, "lens", (n_seqs,))
-    start = 0 if seq_start is None else _ints(seq_start, "seq_start", (n_seqs + 1,))
-    pos = 0 if positions is None else _ints(positions, "positions", (n,))
-    freq = rot = 0
+    tab_stride, max_pages = _table(block_table, n_seqs)
+    if (v.get_device() != dev or k_pages.get_device() != dev or v_pages.get_device() != dev
+            or block_table.get_device() != dev or lens.get_device() != dev):
+        raise _elsewhere((("v", v), ("k_pages", k_pages), ("v_pages", v_pages), ("block_table", block_table),
+                          ("lens", lens)))
+    start = pos = freq = rot = 0
+    if seq_start is not None:
+        if (seq_start.dtype is not i32 or seq_start.dim() != 1 or seq_start.numel() != n_seqs + 1
+                or not seq_start.is_contiguous()):
+            raise _bad_ints(seq_start, "seq_start", n_seqs + 1)
+        if seq_start.get_device() != dev:
+            raise _elsewhere((("seq_start", seq_start),))
+        start = seq_start.data_ptr()
+    if positions is not None:
+        if positions.dtype is not i32 or positions.dim() != 1 or positions.numel() != n or not positions.is_contiguous():
+            raise _bad_ints(positions, "positions", n)
+        if positions.get_device() != dev:
+            raise _elsewhere((("positions", positions),))
+        pos = positions.data_ptr()
     if inv_freq is not None:
         if inv_freq.dtype is not torch.float32:
             raise TypeError(f"inv_freq must be torch.float32, got {inv_freq.dtype}")
         if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError(f"inv_freq must be contiguous [rot_dim / 2], got {tuple(inv_freq.shape)}")
-        freq, rot = inv_freq.data_ptr(), 2 * inv_freq.shape[0]
-    for x in (v, q, q_out, k_pages, v_pages, block_table, lens, seq_start, positions, inv_freq):
-        if x is not None and x.get_device() != dev:
-            raise _elsewhere(dev, (("v", v), ("q", q), ("q_out", q_out), ("k_pages", k_pages), ("v_pages", v_pages),
-                                   ("block_table", block_table), ("lens", lens), ("seq_start", seq_start),
-                                   ("positions", positions), ("inv_freq", inv_freq)))
+        if inv_freq.get_device() != dev:
+            raise _elsewhere((("inv_freq", inv_freq),))
+        freq, rot = inv_freq.data_ptr(), 2 * inv_freq.numel()
     if n == 0:
         return q_out
-    status = (_lib or lib()).wenc_kv_append(
-        _APPEND_PACK.pack(dt, n, n_seqs, H, kv, hd, qp, qo, k.data_ptr(), v.data_ptr(), qs, qos, _token_stride(k, "k"),
-                          _token_stride(v, "v"), k_pages.data_ptr(), v_pages.data_ptr(), kps, vps, pages, size, tab,
-                          tab_stride, max_pages, own, start, pos, freq, rot, 1 if interleaved else 0),
+    status = _lib.wenc_kv_append(
+        _APPEND_PACK.pack(dt, n, n_seqs, H, kv, hd, qp, qo, k.data_ptr(), v.data_ptr(), qs, qos,
+                          kv * hd if k.is_contiguous() else _token_stride(k, "k"),
+                          kv * hd if v.is_contiguous() else _token_stride(v, "v"), k_pages.data_ptr(), v_pages.data_ptr(),
+                          kps, vps, pages, size, block_table.data_ptr(), tab_stride, max_pages, lens.data_ptr(), start, pos,
+                          freq, rot, 1 if interleaved else 0),
         _raw_stream(stream, dev))
     if status:
         _check(status)
@@ -703,27 +752,30 @@ def kv_append(k, v, k_pages, v_pages, block_table, lens, *, seq_start=None, q=No
 def quantize_rows(x, out=None, scale=None, stream=None):
     """(int8 rows, float32 scales) of x [..., d] bf16 or float32: scale = max|row| * (1 / 127) (see
     wenc_quantize_rows)."""
-    import torch
-    dt = _dtype_code(x, "x")
-    shape = x.shape
+    torch = _torch or _load_torch()
+    dt = 1 if x.dtype is torch.bfloat16 else 0
+    if not dt and x.dtype is not torch.float32:
+        raise _dtype_error(x, "x")
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
     dev = x.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise _elsewhere(_current_device(), (("x", x),))
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise _elsewhere((("x", x),))
+    shape = x.shape
+    rows = shape[:-1]
     d = shape[-1]
     if out is None:
         out = torch.empty(shape, dtype=torch.int8, device=x.device)
     elif out.dtype is not torch.int8 or out.shape != shape or not out.is_contiguous():
         raise ValueError(f"out must be contiguous int8 {tuple(shape)}, got {out.dtype} {tuple(out.shape)}")
     if scale is None:
-        scale = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
-    elif scale.dtype is not torch.float32 or scale.shape != shape[:-1] or not scale.is_contiguous():
-        raise ValueError(f"scale must be contiguous float32 {tuple(shape[:-1])}, got {scale.dtype} {tuple(scale.shape)}")
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    elif scale.dtype is not torch.float32 or scale.shape != rows or not scale.is_contiguous():
+        raise ValueError(f"scale must be contiguous float32 {tuple(rows)}, got {scale.dtype} {tuple(scale.shape)}")
     if out.get_device() != dev or scale.get_device() != dev:
-        raise _elsewhere(dev, (("out", out), ("scale", scale)))
-    status = (_lib or lib()).wenc_quantize_rows(x.data_ptr(), dt, out.data_ptr(), scale.data_ptr(),
-                                                x.numel() // d if d else 0, d, _raw_stream(stream, dev))
+        raise _elsewhere((("out", out), ("scale", scale)))
+    status = _lib.wenc_quantize_rows(x.data_ptr(), dt, out.data_ptr(), scale.data_ptr(), scale.numel(), d,
+                                     _raw_stream(stream, dev))
     if status:
         _check(status)
     return out, scale
@@ -735,46 +787,50 @@ def linear_i8(a, a_scale, w, w_scale, bias, epilogue: int = EPI_BIAS_BF16, resid
     with float32 scales [M] (``quantize_rows``), w int8 [N, K] with float32 scales [N]; epilogues
     and outputs as ``linear``. ``workspace``: a uint8 tensor to use instead of an allocation where
     one is needed."""
-    import torch
+    torch = _torch or _load_torch()
     dev = a.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise _elsewhere(_current_device(), (("a", a),))
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise _elsewhere((("a", a),))
     i8, f32 = torch.int8, torch.float32
     if a.dtype is not i8 or w.dtype is not i8:
         raise TypeError(f"a and w must be torch.int8, got {a.dtype} and {w.dtype}")
     if a_scale.dtype is not f32 or w_scale.dtype is not f32 or bias.dtype is not f32:
         raise TypeError("a_scale, w_scale and bias must be torch.float32")
-    if a.dim() != 2 or w.dim() != 2 or a.shape[1] != w.shape[1]:
-        raise ValueError(f"a {tuple(a.shape)} and w {tuple(w.shape)} must be [M, K] and [N, K]")
-    M, K = a.shape
-    N = w.shape[0]
+    ash, wsh = a.shape, w.shape
+    if len(ash) != 2 or len(wsh) != 2 or ash[1] != wsh[1]:
+        raise ValueError(f"a {tuple(ash)} and w {tuple(wsh)} must be [M, K] and [N, K]")
+    M, K = ash
+    N = wsh[0]
     if a_scale.numel() != M or w_scale.numel() != N or bias.numel() != N:
         raise ValueError(f"a_scale must hold {M} scales, w_scale and bias {N}")
+    if not (a.is_contiguous() and w.is_contiguous() and a_scale.is_contiguous() and w_scale.is_contiguous()
+            and bias.is_contiguous()):
+        raise ValueError("linear_i8 takes contiguous tensors")
+    if (a_scale.get_device() != dev or w.get_device() != dev or w_scale.get_device() != dev
+            or bias.get_device() != dev):
+        raise _elsewhere((("a_scale", a_scale), ("w", w), ("w_scale", w_scale), ("bias", bias)))
     dt = f32 if epilogue == EPI_BIAS_RESID_F32 else torch.bfloat16
     if out is None:
         out = torch.empty((M, N), dtype=dt, device=a.device)
-    elif out.dtype is not dt or out.shape != (M, N):
-        raise ValueError(f"out must be {dt} {(M, N)}, got {out.dtype} {tuple(out.shape)}")
-    if resid is not None and (resid.dtype is not f32 or resid.shape != (M, N)):
-        raise ValueError(f"resid must be float32 {(M, N)}, got {resid.dtype} {tuple(resid.shape)}")
-    for x in (a, a_scale, w, w_scale, bias, out, resid):
-        if x is None:
-            continue
-        if not x.is_contiguous():
-            raise ValueError("linear_i8 takes contiguous tensors")
-        if x.get_device() != dev:
-            raise _elsewhere(dev, (("a_scale", a_scale), ("w", w), ("w_scale", w_scale), ("bias", bias), ("out", out),
-                                   ("resid", resid)))
-    L = _lib or lib()
+    elif out.dtype is not dt or out.shape != (M, N) or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous {dt} {(M, N)}, got {out.dtype} {tuple(out.shape)}")
+    elif out.get_device() != dev:
+        raise _elsewhere((("out", out),))
+    rp = 0
+    if resid is not None:
+        if resid.dtype is not f32 or resid.shape != (M, N) or not resid.is_contiguous():
+            raise ValueError(f"resid must be contiguous float32 {(M, N)}, got {resid.dtype} {tuple(resid.shape)}")
+        if resid.get_device() != dev:
+            raise _elsewhere((("resid", resid),))
+        rp = resid.data_ptr()
     if workspace is None:
-        need = L.wenc_linear_i8_workspace(M, N, K)
+        need = _lib.wenc_linear_i8_workspace(M, N, K)
         workspace = _scratch(need, a, stream) if need else None
     elif workspace.get_device() != dev:
-        raise _elsewhere(dev, (("workspace", workspace),))
+        raise _elsewhere((("workspace", workspace),))
     ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    status = L.wenc_linear_i8(a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), bias.data_ptr(),
-                              0 if resid is None else resid.data_ptr(), out.data_ptr(), M, N, K, epilogue, ws, ws_bytes,
-                              _raw_stream(stream, dev))
+    status = _lib.wenc_linear_i8(a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), bias.data_ptr(), rp,
+                                 out.data_ptr(), M, N, K, epilogue, ws, ws_bytes, _raw_stream(stream, dev))
     if status:
         _check(status)
     return out
