@@ -399,15 +399,18 @@ WENC_API wenc_status wenc_quantize_rows(const void* x, int x_dtype, int8_t* xq, 
  *   out = epilogue((sum_k xq[m][k] wq[n][k]) * x_scale[m] * w_scale[n] + bias[n]).
  * xq int8 [M, K], wq int8 [N, K], x_scale [M], w_scale [N], bias [N] float32; resid / out as for
  * wenc_linear. N a multiple of 128, K a multiple of 64, M >= 1; buffers 16-byte aligned (x_scale: 4).
- * The integers run as bf16 on the tensor cores (exact; sm_103a has no integer form of its
- * fifth-generation MMA), products are exact and sums fp32. workspace: wenc_linear_i8_workspace(M, N, K)
- * bytes, 256-byte aligned (NULL when that is 0); it belongs to the call until its work is done.
- * Stream-ordered; errors as wenc_linear. */
+ * The integers run as bf16 or fp16 on the tensor cores (exact; sm_103a has no integer form of its
+ * fifth-generation MMA), products are exact and sums fp32. M at most 2^28. workspace:
+ * wenc_linear_i8_workspace(M, N, K) bytes, 256-byte aligned (may be NULL when that is 0); it belongs to
+ * the call until its work is done: calls that may overlap need one each. One launch without workspace,
+ * else two; stream-ordered; errors as wenc_linear, and a stalled device wait is recorded as for
+ * wenc_attention. */
 WENC_API wenc_status wenc_linear_i8(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
                                     const float* bias, const float* resid, void* out, int M, int N, int K,
                                     int epilogue, void* workspace, size_t workspace_bytes, wenc_stream_t stream);
 
-/* wenc_linear_i8_workspace -- bytes of workspace wenc_linear_i8 needs for these sizes. */
+/* wenc_linear_i8_workspace -- bytes of workspace wenc_linear_i8 needs for these sizes on the current
+ * device. */
 WENC_API size_t wenc_linear_i8_workspace(int M, int N, int K);
 
 /* wenc_set_device_alloc_limit -- test hook for the out-of-memory path (the pages have no

@@ -143,7 +143,8 @@ def _run(a, sa, w, sw, b, resid, epilogue, **kw):
 @pytest.mark.parametrize("epilogue", [0, 1, 2])
 @pytest.mark.parametrize("M,N,K", [(1, 128, 64), (1, 1536, 384), (5, 384, 128), (16, 256, 1280), (17, 640, 192),
                                    (33, 1280, 320), (80, 1152, 1280), (127, 512, 576), (129, 128, 2048),
-                                   (300, 384, 1536), (1537, 1152, 384), (513, 2560, 640)])
+                                   (300, 384, 1536), (1537, 1152, 384), (513, 2560, 640),
+                                   (18, 128, 64), (31, 128, 8192), (128, 256, 320), (100, 5120, 1280), (2049, 256, 448)])
 def test_linear_i8(M, N, K, epilogue):
     p = _problem(M, N, K, seed=M + N + K)
     _check(_run(*p, epilogue).double().cpu().numpy(), *p, epilogue, f"{M} x {N} x {K}")
@@ -178,10 +179,10 @@ def test_linear_i8_nan_scale_stays_in_its_row(M):
 
 
 @pytest.mark.parametrize("M", [3, 70, 400])
-def test_linear_i8_in_place_residual_graph_and_workspace(M):
-    """out may be resid; a captured call replays; a given workspace of any content; another stream."""
+def test_linear_i8_in_place_residual_graph_and_stream(M):
+    """out may be resid; a captured call replays; another stream."""
     import torch
-    from transformer_encoder_gb300 import lib, linear_i8, sync_status
+    from transformer_encoder_gb300 import linear_i8, sync_status
     p = _problem(M, 384, 256, seed=4)
     a, sa, w, sw, b = (_cuda(x) for x in p[:5])
     want = _run(*p, 2)
@@ -189,11 +190,10 @@ def test_linear_i8_in_place_residual_graph_and_workspace(M):
     linear_i8(a, sa, w, sw, b, 2, resid=x, out=x)
     sync_status()
     assert torch.equal(x, want)
-    need = lib().wenc_linear_i8_workspace(M, 384, 256)
-    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")
+    r0 = _cuda(p[5])
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
-    out = linear_i8(a, sa, w, sw, b, 2, resid=_cuda(p[5]), workspace=ws, stream=s)
+    out = linear_i8(a, sa, w, sw, b, 2, resid=r0, stream=s)
     sync_status()
     assert torch.equal(out, want)
     r = _cuda(p[5])
@@ -205,6 +205,51 @@ def test_linear_i8_in_place_residual_graph_and_workspace(M):
         g.replay()
         sync_status()
         _check(out.double().cpu().numpy(), *p[:5], p[5] * np.float32(k), 2, "replayed")
+
+
+def test_every_token_count_around_the_tiles():
+    """Token counts 1 .. 33 and around 128 and 256: no column of the MMA's padding reaches the output."""
+    import torch
+    a, sa, w, sw, b, r = _problem(260, 128, 192, seed=12)
+    for M in list(range(1, 34)) + [63, 64, 65, 112, 113, 127, 128, 129, 255, 256, 257, 260]:
+        got = _run(a[:M], sa[:M], w, sw, b, r[:M], 2).double().cpu().numpy()
+        _check(got, a[:M], sa[:M], w, sw, b, r[:M], 2, f"M = {M}")
+
+
+def test_outputs_past_32_bits():
+    """More than 2^32 bytes of output and of tokens' rows: the last ones are right."""
+    import torch
+    M, N, K = (1 << 32) // (2 * 1024) + 130, 1024, 128
+    a = torch.zeros(M, K, dtype=torch.int8, device="cuda")
+    p = _problem(130, N, K, seed=13)
+    a[-130:] = _cuda(p[0])
+    sa = torch.ones(M, device="cuda")
+    sa[-130:] = _cuda(p[1])
+    from transformer_encoder_gb300 import linear_i8, sync_status
+    out = linear_i8(a, sa, _cuda(p[2]), _cuda(p[3]), _cuda(p[4]), 0)
+    sync_status()
+    _check(out[-130:].double().cpu().numpy(), *p, 0, "last rows")
+    assert torch.equal(out[0], _cuda(p[4]).to(torch.bfloat16)) and torch.equal(out[M - 131], out[0])
+
+
+@pytest.mark.parametrize("epilogue", [0, 2])
+def test_a_given_workspace(epilogue):
+    """The two-pass form in a given workspace of any content; one that is too small is refused."""
+    import torch
+    from transformer_encoder_gb300 import WencError, lib, linear_i8, sync_status
+    M, N, K = 7777, 512, 1024
+    p = _problem(M, N, K, seed=14)
+    d = [_cuda(x) for x in p]
+    need = lib().wenc_linear_i8_workspace(M, N, K)
+    assert need >= 2 * K * (M + N)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    out = linear_i8(*d[:5], epilogue, resid=d[5] if epilogue == 2 else None, workspace=ws)
+    sync_status()
+    rows = np.unique(np.r_[0, 255, 256, M - 1, np.random.default_rng(0).integers(0, M, 60)])
+    _check(out[torch.from_numpy(rows).cuda()].double().cpu().numpy(), p[0][rows], p[1][rows], p[2], p[3], p[4], p[5][rows],
+           epilogue, "given workspace")
+    with pytest.raises(WencError, match="workspace"):
+        linear_i8(*d[:5], 0, workspace=ws[:need - 256])
 
 
 @pytest.mark.parametrize("M", [5, 2000])

@@ -19,9 +19,10 @@
 // of double-precision trigonometry (GB300 runs two double FMAs a clock and SM).
 //
 // What bounds it: bytes. Each row of 64 elements is read once and written once, 16 bytes a lane.
-// A warp owns whole tokens (or a share of one token's rows, when there are few tokens): its 32
-// lanes form the 32 angles at once, and every lane then keeps the angles of its own 16-byte piece
-// in registers for all of the token's heads.
+// A warp owns a run of tokens (or a share of one token's rows, when there are few tokens). What would be
+// a chain of dependent loads per token (its sequence, length, page) is done for the whole run at once, a
+// lane a token, and so are the run's angles; then the rows stream, and every lane keeps the angles of its
+// own 16-byte piece in registers for all of a token's heads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -42,7 +43,8 @@ using namespace wenc_dev;
 
 constexpr int HD = 64;
 constexpr int kWarps = 8;    // per block
-constexpr int kUnroll = 8;   // 16-byte loads a lane keeps in flight
+constexpr int kUnroll = 2;   // rows a lane keeps in flight, two 16-byte pieces each
+constexpr int kRun = 8;      // tokens of a warp's run, at most
 
 struct AppendParams {
   const uint8_t *q, *k, *v;             // rows of 64 elements, heads contiguous
@@ -123,150 +125,149 @@ struct Piece<float> {
 
 // wpt warps share a token's rows (1, 2, 4 or 8); a group of wpt warps takes `chunk` tokens in a row.
 template <typename T>
-__global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const AppendParams p, int wpt, int chunk,
-                                                                uint32_t* err) {
+__global__ void __launch_bounds__(32 * kWarps, 3) kv_append_kernel(const AppendParams p, int wpt, int chunk, uint32_t* err) {
   using P = Piece<T>;
   constexpr int E = P::E;
-  constexpr int LPR = HD / E;        // lanes per row: 8 (bf16) or 16 (fp32)
+  constexpr int LPR = HD / E / 2;    // lanes per row: 4 (bf16) or 8 (fp32)
   constexpr int RPW = 32 / LPR;      // rows a warp moves at once
-  __shared__ float2 cs_all[kWarps][HD / 2];
+  constexpr int ROWB = HD * sizeof(T);
+  __shared__ __align__(16) float2 cs_all[kWarps][kRun][HD / 2];
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int piece = lane % LPR, sub = lane / LPR;
-  const int per_block = kWarps / wpt;
+  const int j = lane % LPR, sub = lane / LPR;
   const int share = warp % wpt;  // which of the token's row sets
-  const long long group = static_cast<long long>(blockIdx.x) * per_block + warp / wpt;
-  const long long t0 = group * chunk;
+  const long long t0 = (static_cast<long long>(blockIdx.x) * (kWarps / wpt) + warp / wpt) * chunk;
   if (t0 >= p.n_tokens) return;
-  const int t1 = static_cast<int>(min(t0 + chunk, static_cast<long long>(p.n_tokens)));
-  float2* cs = cs_all[warp];
+  const int first = static_cast<int>(t0), n = static_cast<int>(min(static_cast<long long>(chunk), p.n_tokens - t0));
 
-  const bool rotate = p.half > 0;
-  const unsigned long long step = rotate && lane < p.half ? turns64(p.inv_freq[lane]) : 0ull;
-  // this lane's piece: its first element, and which angles and partner it turns with
-  const int e0 = piece * E;
-  const bool turned = rotate && e0 < 2 * p.half;
-  const bool upper = e0 >= p.half;                 // half-split: the b of its pairs
-  const int partner = p.half / E;                  // half-split: pieces between a and b
-  const int n_q = p.q ? p.H : 0;
-  const int rows = n_q + 2 * p.Hkv;
-
-  int s = -1, begin = 0, end = 0;
-  for (int t = static_cast<int>(t0); t < t1; ++t) {
-    // ---- its first rows (queries, keys, values) are on their way while its place and angles are found
-    uint4 x[kUnroll];
-    auto fetch = [&](int r0) {
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int r = r0 + u * wpt * RPW + sub;
-        x[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (r >= rows) continue;
-        const uint8_t* src = r < n_q ? p.q + t * p.q_stride + r * static_cast<int>(HD * sizeof(T))
-                             : r < n_q + p.Hkv
-                                 ? p.k + t * p.k_stride + (r - n_q) * static_cast<int>(HD * sizeof(T))
-                                 : p.v + t * p.v_stride + (r - n_q - p.Hkv) * static_cast<int>(HD * sizeof(T));
-        x[u] = *reinterpret_cast<const uint4*>(src + piece * 16);
-      }
-    };
-    fetch(share * RPW);
-    // ---- the token's sequence, cache position and page
+  // ---- the run's places, a lane a token: sequence, cache position, page
+  int pos = 0;
+  long long k_at = -1, v_at = 0;  // byte offsets of the token's slot; -1: the token is not written
+  {
+    const int t = first + lane;
+    int s = -1, begin = 0, end = 0;
     if (p.seq_start) {
-      if (t >= end) {
-        s = find_seq(p.seq_start, p.n_seqs + 1, t, lane);
-        if (s >= p.n_seqs) return;  // behind the last sequence: padding rows, as are all that follow
-        begin = s < 0 ? 0 : p.seq_start[s];
-        end = s < 0 ? 0 : p.seq_start[s + 1];
+      s = find_seq(p.seq_start, p.n_seqs + 1, first, lane);  // the first token's; the others' at or behind it
+      if (lane < n) {
+        if (s >= 0) {
+          while (s < p.n_seqs && p.seq_start[s + 1] <= t) ++s;
+          begin = p.seq_start[s];
+          end = s < p.n_seqs ? p.seq_start[s + 1] : 0x7fffffff;
+        }
+        // (offsets that do not start at 0 or do not ascend)
+        if (s < 0 || t < begin || t >= end) {
+          *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (82u << 8);
+          s = p.n_seqs;
+        }
       }
     } else {
       s = t / p.per_seq;
-      begin = s * p.per_seq;
-      end = begin + p.per_seq;
+      end = (s + 1) * p.per_seq;
     }
-    if (s < 0 || t < begin || t >= end) {  // offsets that do not start at 0 or do not ascend
-      if (lane == 0) *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (82u << 8);
-      end = 0;
-      continue;
+    if (lane < n && s < p.n_seqs) {  // (s == n_seqs: padding rows behind the last sequence)
+      const long long at = static_cast<long long>(p.lens[s]) - (end - t);
+      pos = static_cast<int>(at);
+      const int page_i = pos / p.page_size;
+      if (at < 0 || page_i >= p.max_pages) {
+        *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (81u << 8);
+      } else {
+        const int page = p.table[s * p.table_stride + page_i];
+        if (page < 0 || page >= p.n_pages) {
+          *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (80u << 8);
+        } else {
+          const long long slot = static_cast<long long>(pos - page_i * p.page_size) * p.Hkv * ROWB;
+          k_at = page * p.k_page_stride + slot;
+          v_at = page * p.v_page_stride + slot;
+        }
+      }
     }
-    const long long pos_l = static_cast<long long>(p.lens[s]) - (end - t);
-    const int pos = static_cast<int>(pos_l);
-    const int page_i = pos / p.page_size;
-    if (pos_l < 0 || page_i >= p.max_pages) {
-      if (lane == 0) *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (81u << 8);
-      continue;
-    }
-    const int page = p.table[s * p.table_stride + page_i];
-    if (page < 0 || page >= p.n_pages) {
-      if (lane == 0) *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (80u << 8);
-      continue;
-    }
-    const long long slot = static_cast<long long>(pos - page_i * p.page_size) * p.Hkv * (HD * sizeof(T));
-    uint8_t* k_dst = p.k_pages + page * p.k_page_stride + slot;
-    uint8_t* v_dst = p.v_pages + page * p.v_page_stride + slot;
-
-    // ---- its angles: one per lane, then the E (or E / 2) of this lane's piece
-    float c[E], sn[E];
-    if (rotate) {
-      const int at = p.positions ? p.positions[t] : pos;
+    if (p.positions && lane < n) pos = p.positions[t];
+  }
+  // ---- the run's angles, a lane a frequency
+  const bool rotate = p.half > 0;
+  if (rotate) {
+    const unsigned long long step = lane < p.half ? turns64(p.inv_freq[lane]) : 0ull;
+#pragma unroll 2
+    for (int i = 0; i < n; ++i) {
+      const int at = __shfl_sync(0xffffffffu, pos, i);
       if (lane < p.half) {
         const long long turn = static_cast<long long>(static_cast<unsigned long long>(static_cast<long long>(at)) * step);
         float sv, cv;
         sincospif(static_cast<float>(turn >> 32) * 0x1p-31f, &sv, &cv);  // turn * 2 pi = pi * (turn / 2^63)
-        cs[lane] = make_float2(cv, sv);
+        cs_all[warp][i][lane] = make_float2(cv, sv);
       }
-      __syncwarp();
-      if (turned) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const float2 a = cs[p.interleaved ? (e0 + i) >> 1 : (upper ? e0 - p.half : e0) + i];
-          c[i] = a.x;
-          sn[i] = a.y;
-        }
-      }
-      __syncwarp();
     }
+    __syncwarp();
+  }
 
-    // ---- turned and stored
+  // ---- the rows: queries, keys, values
+  // Half-split: lanes 0 .. half / E - 1 take the pieces j and j + half / E, which turn with each other; the others
+  // two neighbours each of those that do not turn. Interleaved: pieces 2 j and 2 j + 1.
+  const int half_p = p.half / E;
+  const bool pair = rotate && !p.interleaved && j < half_p;
+  const bool turned = rotate && (p.interleaved ? 2 * j * E < 2 * p.half : pair);
+  const int o0 = (pair ? j : 2 * j) * 16, o1 = (pair ? j + half_p : 2 * j + 1) * 16;  // bytes into the row
+  const int n_q = p.q ? p.H : 0;
+  const int rows = n_q + 2 * p.Hkv;
+  for (int i = 0; i < n; ++i) {
+    const long long kd = __shfl_sync(0xffffffffu, k_at, i), vd = __shfl_sync(0xffffffffu, v_at, i);
+    if (kd < 0) continue;
+    const long long t = first + i;
+    const uint8_t *q = p.q + t * p.q_stride, *k = p.k + t * p.k_stride, *v = p.v + t * p.v_stride;
+    uint8_t *qd = p.q_out + t * p.q_out_stride, *kdst = p.k_pages + kd, *vdst = p.v_pages + vd;
+    float c[E], sn[E];
+    if (turned) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {  // of angle j E + e in both layouts
+        const float2 a = cs_all[warp][i][j * E + e];
+        c[e] = a.x;
+        sn[e] = a.y;
+      }
+    }
     for (int r0 = share * RPW; r0 < rows; r0 += wpt * RPW * kUnroll) {
-      if (r0 != share * RPW) fetch(r0);
+      uint4 x[kUnroll][2];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int r = r0 + u * wpt * RPW + sub;
-        uint4 y = x[u];
-        if (rotate) {
-          // every lane of the warp takes part in the exchange; values and rows past the end pass through
-          uint4 o = x[u];
-          if (!p.interleaved) {
-            const int from = upper ? lane - partner : lane + partner;
-            o.x = __shfl_sync(0xffffffffu, x[u].x, from & 31);
-            o.y = __shfl_sync(0xffffffffu, x[u].y, from & 31);
-            o.z = __shfl_sync(0xffffffffu, x[u].z, from & 31);
-            o.w = __shfl_sync(0xffffffffu, x[u].w, from & 31);
-          }
-          if (turned && r < n_q + p.Hkv) {
-            float f[E], g[E];
-            P::unpack(x[u], f);
-            if (p.interleaved) {
-#pragma unroll
-              for (int i = 0; i < E; i += 2) {
-                const float a = f[i], b = f[i + 1];
-                f[i] = a * c[i] - b * sn[i];
-                f[i + 1] = b * c[i] + a * sn[i];
-              }
-            } else {
-              P::unpack(o, g);
-#pragma unroll
-              for (int i = 0; i < E; ++i) f[i] = upper ? f[i] * c[i] + g[i] * sn[i] : f[i] * c[i] - g[i] * sn[i];
-            }
-            y = P::pack(f);
-          }
-        }
+      for (int w = 0; w < kUnroll; ++w) {
+        const int r = r0 + w * wpt * RPW + sub;
+        const uint8_t* src = r < n_q ? q + r * ROWB : r < n_q + p.Hkv ? k + (r - n_q) * ROWB : v + (r - n_q - p.Hkv) * ROWB;
         if (r < rows) {
-          uint8_t* dst = r < n_q ? p.q_out + t * p.q_out_stride + r * static_cast<int>(HD * sizeof(T))
-                         : r < n_q + p.Hkv ? k_dst + (r - n_q) * static_cast<int>(HD * sizeof(T))
-                                           : v_dst + (r - n_q - p.Hkv) * static_cast<int>(HD * sizeof(T));
-          *reinterpret_cast<uint4*>(dst + piece * 16) = y;
+          x[w][0] = *reinterpret_cast<const uint4*>(src + o0);
+          x[w][1] = *reinterpret_cast<const uint4*>(src + o1);
         }
+      }
+#pragma unroll
+      for (int w = 0; w < kUnroll; ++w) {
+        const int r = r0 + w * wpt * RPW + sub;
+        if (r >= rows) break;
+        uint4 y0 = x[w][0], y1 = x[w][1];
+        if (turned && r < n_q + p.Hkv) {
+          float a[E], b[E];
+          P::unpack(y0, a);
+          P::unpack(y1, b);
+          if (p.interleaved) {
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              const float a0 = a[e], a1 = a[e + 1], b0 = b[e], b1 = b[e + 1];
+              a[e] = a0 * c[e / 2] - a1 * sn[e / 2];
+              a[e + 1] = a1 * c[e / 2] + a0 * sn[e / 2];
+              b[e] = b0 * c[E / 2 + e / 2] - b1 * sn[E / 2 + e / 2];
+              b[e + 1] = b1 * c[E / 2 + e / 2] + b0 * sn[E / 2 + e / 2];
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              const float a0 = a[e], b0 = b[e];
+              a[e] = a0 * c[e] - b0 * sn[e];
+              b[e] = b0 * c[e] + a0 * sn[e];
+            }
+          }
+          y0 = P::pack(a);
+          y1 = P::pack(b);
+        }
+        uint8_t* dst = r < n_q ? qd + r * ROWB : r < n_q + p.Hkv ? kdst + (r - n_q) * ROWB : vdst + (r - n_q - p.Hkv) * ROWB;
+        *reinterpret_cast<uint4*>(dst + o0) = y0;
+        *reinterpret_cast<uint4*>(dst + o1) = y1;
       }
     }
   }
@@ -355,15 +356,15 @@ extern "C" wenc_status wenc_kv_append(const wenc_kv_append_args* a, wenc_stream_
   // queries that neither turn nor move need no pass
   if (p.half == 0 && p.q == p.q_out) p.q = nullptr;
 
-  const int rpw = a->dtype == WENC_DTYPE_F32 ? 2 : 4;
+  const int rpw = a->dtype == WENC_DTYPE_F32 ? 4 : 8;  // rows a warp moves at once
   const int rows = (p.q ? p.H : 0) + 2 * p.Hkv;
   // Few tokens: several warps share one token's rows, so that the rows' loads go out together.
   // Many: a warp takes a run of tokens and finds its sequence and angle steps once.
   int wpt = 1;
   while (wpt < kWarps && wpt * rpw < rows && static_cast<long long>(a->n_tokens) * wpt < 16ll * sms) wpt *= 2;
   const long long warps = static_cast<long long>(a->n_tokens) * wpt;
-  int chunk = static_cast<int>((warps + 64ll * sms - 1) / (64ll * sms));
-  if (chunk > 8) chunk = 8;
+  int chunk = static_cast<int>((warps + 24ll * sms - 1) / (24ll * sms));
+  if (chunk > kRun) chunk = kRun;
   if (wpt > 1) chunk = 1;
   const long long groups = (a->n_tokens + chunk - 1) / chunk;
   const long long blocks = (groups + kWarps / wpt - 1) / (kWarps / wpt);

@@ -9,12 +9,16 @@
 // sm_103a has no integer form of the fifth-generation MMA, and GB300's older integer units are far
 // slower than its 16-bit ones. Integers up to 128 are exact in bf16 (8 significant bits) and in fp16, a
 // product (at most 2^14) is exact in the fp32 accumulator, and so is every sum below 2^24; longer sums
-// round as any fp32 sum does. So the product runs on 16-bit tensor cores, in two forms:
-//  - many tokens: both operands are widened to bf16 in the workspace and multiplied by the tcgen05 GEMM
-//    of gemm.cu, whose epilogue applies the scales. What bounds it: the tensor pipe, plus the
-//    widening's bytes;
-//  - few tokens (a decode step): the weights are what there is to read, once, as bytes; they are widened
-//    in registers and multiplied by mma.sync, no workspace (i8_rows_kernel below).
+// round as any fp32 sum does. So the product runs on the 16-bit tensor cores, in three forms:
+//  - up to 16 tokens (a decode step of few beams): mma.sync on weights that go from global memory to
+//    registers (i8_rows_kernel): a 128-row tcgen05 tile would give too few CTAs to keep the weights' bytes
+//    coming;
+//  - up to about half an output tile of 128 x 128 per SM: tcgen05 on operands widened on the chip
+//    (i8_tc_kernel), no workspace;
+//  - more: the operands are widened to bf16 in the workspace and multiplied by the GEMM of gemm.cu, whose
+//    epilogue applies the scales. On-chip widening repeats itself in every tile, and its loads and stores then
+//    bind the shared-memory pipe (24000 x 1280 x 5120: 399 us against 266 us for both passes; at 1024 x 1280
+//    x 5120 both take 34 us, at 256 x 1280 x 5120 it is 16 against 32 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -30,6 +34,7 @@
 
 wenc_status wenc_internal_fail(wenc_status s, const char* msg);
 void wenc_internal_clear_error();
+int wenc_internal_sm_count();
 wenc_status wenc_internal_device(int* sms, uint32_t** err);
 
 namespace {
@@ -261,17 +266,16 @@ template <int NT>
 struct RowsCfg {
   static constexpr int TOK = 8 * NT;
   static constexpr int XROW = kRowsK * 2 + 16;            // bytes of a token's round in shared memory
-  static constexpr int XV = TOK * (kRowsK / 16) / 256;    // 16-byte pieces of x per thread and round
-  static constexpr int XN = XV < 1 ? 1 : XV;
+  static constexpr int XN = (TOK * (kRowsK / 16) + 255) / 256;  // 16-byte pieces of x per thread and round
   static constexpr int RED = 8 * 16 * (TOK + 1) * 4;      // the warps' sums
   static constexpr int SMEM = TOK * XROW > RED ? TOK * XROW : RED;
 };
 
-template <int NT, int EPI>
-__global__ void __launch_bounds__(256) i8_rows_kernel(const int8_t* __restrict__ xq, const float* __restrict__ x_scale,
-                                                      const int8_t* __restrict__ wq, const float* __restrict__ w_scale,
-                                                      const float* __restrict__ bias, const float* resid, void* out, int M,
-                                                      int N, int K, int ksplit) {
+template <int NT>
+__global__ void __launch_bounds__(256, 2) i8_rows_kernel(const int8_t* __restrict__ xq, const float* __restrict__ x_scale,
+                                                         const int8_t* __restrict__ wq, const float* __restrict__ w_scale,
+                                                         const float* __restrict__ bias, const float* resid, void* out, int M,
+                                                         int N, int K, int ksplit, int epilogue) {
   using C = RowsCfg<NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   pdl_trigger();
@@ -279,8 +283,7 @@ __global__ void __launch_bounds__(256) i8_rows_kernel(const int8_t* __restrict__
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
   const int c16 = warp & 1, quarter = warp >> 1;
   const int rank = blockIdx.x % ksplit;
-  const int n0 = blockIdx.x / ksplit * kRowsChannels, m0 = blockIdx.y * C::TOK;
-  const int m_here = min(C::TOK, M - m0);
+  const int n0 = blockIdx.x / ksplit * kRowsChannels;
   // this CTA's k: whole pieces of 64, as equal as they divide
   const int pieces = K / 64, per = (pieces + ksplit - 1) / ksplit;
   const int k_begin = min(rank * per, pieces) * 64, k_end = min((rank + 1) * per, pieces) * 64;
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(256) i8_rows_kernel(const int8_t* __restrict__
 #pragma unroll
     for (int i = 0; i < C::XN; ++i) {
       const int at = threadIdx.x + 256 * i, tok = at / (kRowsK / 16), kk = k0 + at % (kRowsK / 16) * 16;
-      xv[i] = tok < m_here && kk < k_end ? *reinterpret_cast<const uint4*>(xq + static_cast<size_t>(m0 + tok) * K + kk) : zero;
+      xv[i] = tok < M && kk < k_end ? *reinterpret_cast<const uint4*>(xq + static_cast<size_t>(tok) * K + kk) : zero;
     }
   };
   float acc[NT][4];
@@ -335,7 +338,6 @@ __global__ void __launch_bounds__(256) i8_rows_kernel(const int8_t* __restrict__
     const uint8_t* xs = smem + g * C::XROW + quarter * 128 + tq * 32;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if (8 * n >= m_here) break;
       const uint4 b0 = *reinterpret_cast<const uint4*>(xs + n * 8 * C::XROW);
       const uint4 b1 = *reinterpret_cast<const uint4*>(xs + n * 8 * C::XROW + 16);
       mma_f16(acc[n], wf[0], b0.x, b0.y);
@@ -361,31 +363,323 @@ __global__ void __launch_bounds__(256) i8_rows_kernel(const int8_t* __restrict__
   if (ksplit > 1) {
     for (int at = threadIdx.x; at < kRowsChannels * C::TOK; at += 256) {
       const int ch = at & 31, tok = at >> 5;
-      if (tok < m_here) red[((ch >> 4) * 16 + (ch & 15)) * RS + tok] = sum4(ch, tok);
+      if (tok < M) red[((ch >> 4) * 16 + (ch & 15)) * RS + tok] = sum4(ch, tok);
     }
     cluster_arrive_wait();
   }
   const uint32_t red_addr = smem_u32(red);
   const int ch = lane, n = n0 + ch;
   const float ws = __ldg(w_scale + n), bn = __ldg(bias + n);
-  for (int tok = warp * ksplit + rank; tok < m_here; tok += 8 * ksplit) {
+  for (int tok = warp * ksplit + rank; tok < M; tok += 8 * ksplit) {
     float a = 0.0f;
     if (ksplit > 1) {
       for (int r = 0; r < ksplit; ++r) a += ld_rank_f32(red_addr + (((ch >> 4) * 16 + (ch & 15)) * RS + tok) * 4, r);
     } else {
       a = sum4(ch, tok);
     }
-    const int m = m0 + tok;
-    float v = fmaf(a, __ldg(x_scale + m) * ws, bn), unused = 0.0f;
-    const size_t at = static_cast<size_t>(m) * N + n;
-    if constexpr (EPI == WENC_EPI_BIAS_RESID_F32) {
+    float v = fmaf(a, __ldg(x_scale + tok) * ws, bn), unused = 0.0f;
+    const size_t at = static_cast<size_t>(tok) * N + n;
+    if (epilogue == WENC_EPI_BIAS_RESID_F32) {
       static_cast<float*>(out)[at] = resid[at] + v;
     } else {
-      if constexpr (EPI == WENC_EPI_BIAS_GELU_BF16) gelu_erf_x2(v, unused);
+      if (epilogue == WENC_EPI_BIAS_GELU_BF16) gelu_erf_x2(v, unused);
       static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
     }
   }
   if (ksplit > 1) cluster_arrive_wait();  // no CTA leaves while another reads its sums
+}
+
+// ---------------------------------------------------------------- a few tiles
+// D[128 channels][up to 128 tokens] += W x^T on tcgen05, the weights as the A operand in TMEM, the tokens as
+// the B operand in shared memory. Per 64 k (a stage): four warps load 16 bytes of weight rows a lane, widen
+// them and store them to TMEM in the 16x256b shape, whose rows and columns are those of the loads
+// (lane / 4 and 2 (lane % 4) + 0, 1 of every 8); four warps load 32 bytes of a token a lane, widen them and
+// store them to the swizzled stage; one thread issues the MMAs. That order of the k is not the memory's:
+// TMEM column 8 b + 2 t + e (k pair of the MMA) holds k = 16 t + 4 b + 2 e and the next, and the tokens are
+// stored in the same order, which leaves the sum as it is. With A in TMEM the shared memory is written
+// and read once per stage for the tokens alone (2 x 16 KB in the 256 cycles of the stage's MMAs, which is its
+// bandwidth); both operands there would need twice that. Two CTAs share an SM (256 TMEM columns and 66 KB
+// each), so that one's MMAs run under the other's first loads and epilogue. The channels are D's lanes: every
+// store of a warp writes 32 neighbouring channels of one token. Few tiles: a cluster splits K and joins its sums
+// through distributed shared memory.
+// What bounds it: the widening's instructions (five per four integers) and the tensor pipe, about evenly.
+constexpr int kTcTok = 128;
+constexpr int kTcStages = 4;
+constexpr int kTcThreads = 288;  // 4 weight warps, 4 token warps, the issuing warp
+constexpr uint32_t kTcStageBytes = kTcTok * 128;
+constexpr uint32_t kTcBars = kTcStages * kTcStageBytes;
+constexpr uint32_t kTcSmem = 1024 + kTcBars + (2 * kTcStages + 2) * 8 + 16;
+constexpr uint32_t kTcColumns = 256;  // D 0..127, A stages of 32 columns from 128
+
+// kind::f16 with fp16 operands, both K-major, fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 16 TMEM lanes x 32 columns: register 4 b + h of a lane is lane (thread / 4 + 8 (h / 2)), column
+// 8 b + 2 (thread % 4) + h % 2.
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ float4 ld_rank_f4(uint32_t saddr, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(r) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kTcThreads, 2)
+    i8_tc_kernel(const int8_t* __restrict__ xq, const float* __restrict__ x_scale, const int8_t* __restrict__ wq,
+                 const float* __restrict__ w_scale, const float* __restrict__ bias, const float* resid, void* out, int M, int N,
+                 int K, int ksplit, int epilogue, uint32_t* err) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t s0 = smem_u32(smem), bar0 = s0 + kTcBars;
+  auto full = [&](int st) { return bar0 + 8u * st; };
+  auto empty = [&](int st) { return bar0 + 8u * (kTcStages + st); };
+  const uint32_t done = bar0 + 8u * (2 * kTcStages);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kTcBars + (2 * kTcStages + 2) * 8);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  const WaitCtx wc{abort_flag, err};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+  const int rank = blockIdx.x % ksplit;
+  const int n0 = blockIdx.x / ksplit * 128, m0 = blockIdx.y * kTcTok, m_here = min(kTcTok, M - m0);
+  const int pieces = K / 64, per = (pieces + ksplit - 1) / ksplit;
+  const int first = min(rank * per, pieces), n_chunks = min(per, pieces - first);
+
+  if (threadIdx.x == 0) {
+    for (int st = 0; st < kTcStages; ++st) {
+      mbar_init(full(st), 8);   // the eight converting warps
+      mbar_init(empty(st), 1);  // the MMAs' commit
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0u;
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(tmem_slot), kTcColumns);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot, a_tmem = tmem + 128;
+  pdl_trigger();  // TMEM is held: the next kernel may be scheduled
+  pdl_wait();
+
+  if (warp < 8) {
+    // ---------------- load and widen: two stages' loads are kept in flight, and the loop is unrolled over the
+    // ring, so that a stage costs little more than its widening.
+    // Weight warps: rows 8 i + g of the warp's 32, bytes 16 tq ..; token warps: rows tok and 16 + tok of the
+    // warp's 32, 32 bytes from 32 u (tok spreads the eight lanes of a store's quarter over all banks).
+    const bool is_w = warp < 4;
+    const int u = lane & 1, ti = lane >> 1, tok = ((ti & 3) << 1) | ((ti >> 2) & 1) | (ti & 8);
+    const int8_t* src[4];
+    bool there[2] = {true, true};
+    if (is_w) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) src[i] = wq + static_cast<size_t>(n0 + 32 * warp + 8 * i + g) * K + first * 64 + 16 * tq;
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = 32 * (warp & 3) + 16 * h + tok;
+        there[h] = row < m_here;  // rows past the last token read as zeros (its own row stands in for the address)
+        src[2 * h] = xq + static_cast<size_t>(m0 + (there[h] ? row : 0)) * K + first * 64 + 32 * u;
+        src[2 * h + 1] = src[2 * h] + 16;
+      }
+    }
+    auto load = [&](uint4 (&b)[4], int ahead) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = there[i >> 1] ? __ldg(reinterpret_cast<const uint4*>(src[i] + ahead * 64)) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    const uint32_t row0 = s0 + (32 * (warp & 3) + tok) * 128, a0 = a_tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    uint32_t at[4];  // where the four 16-byte pieces of a token's 32 bytes go (swizzled)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) at[c] = row0 + (((2 * c + u) ^ (tok & 7)) << 4);
+    auto convert = [&](const uint4 (&b)[4], int st, uint32_t parity) {
+      if (!mbar_wait_warp(empty(st), parity, wc, 40)) return false;
+      if (is_w) {
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // rows 16 h .. 16 h + 15 of the warp's lanes
+          const uint4 lo = b[2 * h], hi = b[2 * h + 1];
+          uint32_t r[16];
+          widen_half(lo.x, r[0], r[1]);
+          widen_half(hi.x, r[2], r[3]);
+          widen_half(lo.y, r[4], r[5]);
+          widen_half(hi.y, r[6], r[7]);
+          widen_half(lo.z, r[8], r[9]);
+          widen_half(hi.z, r[10], r[11]);
+          widen_half(lo.w, r[12], r[13]);
+          widen_half(hi.w, r[14], r[15]);
+          tmem_st_16x256b_x4(a0 + 32 * st + (static_cast<uint32_t>(16 * h) << 16), r);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t wa[4] = {b[2 * h].x, b[2 * h].y, b[2 * h].z, b[2 * h].w};
+          const uint32_t wb[4] = {b[2 * h + 1].x, b[2 * h + 1].y, b[2 * h + 1].z, b[2 * h + 1].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t a0, a1, b0, b1;
+            widen_half(wa[c], a0, a1);
+            widen_half(wb[c], b0, b1);
+            sts_v4(at[c] + st * kTcStageBytes + h * 16 * 128, a0, a1, b0, b1);
+          }
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full(st));
+      return true;
+    };
+    static_assert(kTcStages == 4, "the loop below is unrolled over four stages");
+    uint4 b0[4], b1[4];
+    if (n_chunks > 0) load(b0, 0);
+    if (n_chunks > 1) load(b1, 1);
+    bool ok = true;
+    uint32_t parity = 1;
+    for (int j = 0; ok && j < n_chunks; j += 4, parity ^= 1) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (!ok || j + q >= n_chunks) break;
+        ok = convert(q & 1 ? b1 : b0, q, parity);
+        if (j + q + 2 < n_chunks) load(q & 1 ? b1 : b0, q + 2);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) src[i] += 4 * 64;
+    }
+    // ---------------- epilogue: warp w reads the channels of TMEM lane quadrant w % 4, tokens 64 (w / 4) ..
+    if (ok && n_chunks > 0) ok = mbar_wait_warp(done, 0, wc, 41);
+    tc_fence_after();
+    const int ch = 32 * (warp & 3) + lane, tok0 = 64 * (warp >> 2);
+    const float ws = __ldg(w_scale + n0 + ch), bn = __ldg(bias + n0 + ch);
+    float* part = reinterpret_cast<float*>(smem);  // [token][128 channels], over the stages
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int t0 = tok0 + 32 * c;
+      if (!ok || t0 >= m_here) break;  // warp-uniform
+      uint32_t acc[32];
+      if (n_chunks > 0) {
+        tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + t0, acc);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[e] = 0u;
+      }
+      if (ksplit > 1) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) part[(t0 + e) * 128 + ch] = __uint_as_float(acc[e]);
+        continue;
+      }
+      // (residual rows are all on their way before the first store: `out` may be `resid`, so the compiler cannot
+      // move a load up over a store)
+#pragma unroll
+      for (int e0 = 0; e0 < 32; e0 += 16) {
+        const size_t at0 = static_cast<size_t>(m0 + t0 + e0) * N + n0 + ch;
+        float rr[16];
+        if (epilogue == WENC_EPI_BIAS_RESID_F32) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) rr[e] = t0 + e0 + e < m_here ? resid[at0 + static_cast<size_t>(e) * N] : 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const int t = t0 + e0 + e;
+          const bool in0 = t < m_here, in1 = t + 1 < m_here;
+          float v0 = fmaf(__uint_as_float(acc[e0 + e]), (in0 ? __ldg(x_scale + m0 + t) : 0.0f) * ws, bn);
+          float v1 = fmaf(__uint_as_float(acc[e0 + e + 1]), (in1 ? __ldg(x_scale + m0 + t + 1) : 0.0f) * ws, bn);
+          const size_t at = at0 + static_cast<size_t>(e) * N;
+          if (epilogue == WENC_EPI_BIAS_RESID_F32) {
+            float* o = static_cast<float*>(out);
+            if (in0) o[at] = rr[e] + v0;
+            if (in1) o[at + N] = rr[e + 1] + v1;
+          } else {
+            if (epilogue == WENC_EPI_BIAS_GELU_BF16) gelu_erf_x2(v0, v1);
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
+            if (in0) o[at] = __float2bfloat16_rn(v0);
+            if (in1) o[at + N] = __float2bfloat16_rn(v1);
+          }
+        }
+      }
+    }
+  } else {
+    // ---------------- MMA issuer: the whole warp waits, lane 0 issues
+    const uint32_t idesc = idesc_f16_f32(128, (m_here + 15) / 16 * 16);
+    for (int j = 0; j < n_chunks; ++j) {
+      const int st = j % kTcStages;
+      if (!mbar_wait_warp(full(st), (j / kTcStages) & 1, wc, 42)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint64_t bd = sdesc_sw128(s0 + st * kTcStageBytes, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) umma_f16_ts(tmem, a_tmem + 32 * st + 8 * k, bd + 2 * k, idesc, (j | k) != 0 ? 1u : 0u);
+        umma_commit(empty(st));
+      }
+      __syncwarp();
+    }
+    // every MMA issued completes before anything is read or freed
+    if (lane == 0) {
+      umma_commit(done);
+      mbar_wait_drain(done, 0);
+    }
+    __syncwarp();
+  }
+  if (ksplit > 1) {
+    // the CTAs' sums: the ranks share the tokens out, a warp a token, four channels a lane
+    __syncwarp();
+    cluster_arrive_wait();
+    if (warp < 8) {
+      const uint32_t part = s0 + lane * 16;
+      const float4 ws = __ldg(reinterpret_cast<const float4*>(w_scale + n0) + lane), bn = __ldg(reinterpret_cast<const float4*>(bias + n0) + lane);
+      for (int t = rank + ksplit * warp; t < m_here && !*abort_flag; t += ksplit * 8) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int r = 0; r < ksplit; ++r) {
+          const float4 v = ld_rank_f4(part + t * 512, r);
+          a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+        }
+        const float xs = __ldg(x_scale + m0 + t);
+        float4 v = make_float4(fmaf(a.x, xs * ws.x, bn.x), fmaf(a.y, xs * ws.y, bn.y), fmaf(a.z, xs * ws.z, bn.z), fmaf(a.w, xs * ws.w, bn.w));
+        const size_t at = static_cast<size_t>(m0 + t) * N + n0 + 4 * lane;
+        if (epilogue == WENC_EPI_BIAS_RESID_F32) {
+          const float4 r = *reinterpret_cast<const float4*>(resid + at);
+          *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(r.x + v.x, r.y + v.y, r.z + v.z, r.w + v.w);
+        } else {
+          if (epilogue == WENC_EPI_BIAS_GELU_BF16) {
+            gelu_erf_x2(v.x, v.y);
+            gelu_erf_x2(v.z, v.w);
+          }
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        }
+      }
+    }
+    __syncwarp();
+    cluster_arrive_wait();  // no CTA leaves while another reads its sums
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTcColumns);
+  }
 }
 
 // ---------------------------------------------------------------- many tokens
@@ -406,11 +700,11 @@ __global__ void __launch_bounds__(256) widen_kernel(const int8_t* __restrict__ a
                                                     const int8_t* __restrict__ w, uint16_t* __restrict__ wb, size_t nw) {
   pdl_trigger();
   pdl_wait();
-  const size_t total = (na + nw) / 16;
+  const size_t split = na / 16, total = split + nw / 16;
   for (size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; i < total;
        i += static_cast<size_t>(gridDim.x) * blockDim.x) {
-    const bool is_a = i < na / 16;
-    const size_t j = is_a ? i : i - na / 16;
+    const bool is_a = i < split;
+    const size_t j = is_a ? i : i - split;
     const uint4 v = reinterpret_cast<const uint4*>(is_a ? a : w)[j];
     const uint2 p0 = widen4(v.x), p1 = widen4(v.y), p2 = widen4(v.z), p3 = widen4(v.w);
     uint4* dst = reinterpret_cast<uint4*>(is_a ? ab : wb) + 2 * j;
@@ -435,52 +729,78 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// The few-token form up to this many tokens (in tiles of at most 128).
-constexpr int kRowsMost = 128;
+// The few-token form up to this many tokens.
+constexpr int kRowsMost = 16;
 
-template <int NT, int EPI>
-cudaError_t launch_rows(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale, const float* bias,
-                        const float* resid, void* out, int M, int N, int K, int sms, cudaStream_t stream) {
-  using C = RowsCfg<NT>;
-  auto kern = i8_rows_kernel<NT, EPI>;
+// Whether the operands are widened on the chip: up to one output tile (128 x 128) for every second SM. Measured
+// around it (us, on the chip / two passes): 5120 x 1280 at 256 tokens (80 tiles) 14.9 / 14.8, at 512 19.7 / 15.7;
+// 1280 x 5120 at 1024 (80) 34.0 / 34.2; 1536 x 512 at 512 (48) 9.1 / 8.4, at 128 (12) 6.6 / 8.0.
+bool on_chip(int M, int N, int sms) { return static_cast<long long>((M + kTcTok - 1) / kTcTok) * (N / 128) <= sms / 2; }
+
+// CTAs of a cluster that split K, for `tiles` output tiles: until the machine has a CTA per SM, none with
+// fewer than `least` of the `pieces` of 64 k.
+int pick_ksplit(long long tiles, int pieces, int least, int sms) {
+  int n = 1;
+  while (n < 8 && tiles * n <= sms && pieces >= 2 * n * least) n *= 2;
+  return n;
+}
+
+void cluster_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], dim3 grid, int threads, size_t smem, int cluster,
+                    cudaStream_t stream) {
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+}
+
+cudaError_t launch_tc(int epilogue, const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale, const float* bias,
+                      const float* resid, void* out, int M, int N, int K, int sms, uint32_t* err, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  // Shared-memory opt-in, once per device and instantiation (a repeat by a racing host thread is harmless).
+  // Shared-memory opt-in, once per device (a repeat by a racing host thread is harmless).
+  static std::atomic<int> configured_device{-1};
+  if (configured_device.load(std::memory_order_acquire) != dev) {
+    e = cudaFuncSetAttribute(i8_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTcSmem));
+    if (e != cudaSuccess) return e;
+    configured_device.store(dev, std::memory_order_release);
+  }
+  const int m_tiles = (M + kTcTok - 1) / kTcTok;
+  const int ksplit = pick_ksplit(static_cast<long long>(N / 128) * m_tiles, K / 64, 2, sms);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cluster_config(cfg, attr, dim3(N / 128 * ksplit, m_tiles), kTcThreads, kTcSmem, ksplit, stream);
+  return cudaLaunchKernelEx(&cfg, i8_tc_kernel, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, ksplit, epilogue, err);
+}
+
+template <int NT>
+cudaError_t launch_rows(int epilogue, const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale, const float* bias,
+                        const float* resid, void* out, int M, int N, int K, int sms, cudaStream_t stream) {
+  using C = RowsCfg<NT>;
+  auto kern = i8_rows_kernel<NT>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
   static std::atomic<int> configured_device{-1};
   if (C::SMEM > 48 * 1024 && configured_device.load(std::memory_order_acquire) != dev) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     configured_device.store(dev, std::memory_order_release);
   }
-  // clusters along K until the machine has a CTA per SM, none with less than one round
-  const int tiles = N / kRowsChannels, m_tiles = (M + C::TOK - 1) / C::TOK;
-  int ksplit = 1;
-  while (ksplit < 8 && static_cast<long long>(tiles) * m_tiles * ksplit * 2 <= 2ll * sms && K >= 2 * ksplit * kRowsK) ksplit *= 2;
+  const int tiles = N / kRowsChannels;
+  const int ksplit = pick_ksplit(tiles, K / 64, kRowsK / 64, sms);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles * ksplit, m_tiles);
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ksplit;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = ksplit > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, ksplit);
-}
-
-template <int NT>
-cudaError_t launch_rows_epi(int epilogue, const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
-                            const float* bias, const float* resid, void* out, int M, int N, int K, int sms, cudaStream_t s) {
-  if (epilogue == WENC_EPI_BIAS_BF16) return launch_rows<NT, WENC_EPI_BIAS_BF16>(xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, sms, s);
-  if (epilogue == WENC_EPI_BIAS_GELU_BF16)
-    return launch_rows<NT, WENC_EPI_BIAS_GELU_BF16>(xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, sms, s);
-  return launch_rows<NT, WENC_EPI_BIAS_RESID_F32>(xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, sms, s);
+  cluster_config(cfg, attr, dim3(tiles * ksplit), 256, C::SMEM, ksplit, stream);
+  return cudaLaunchKernelEx(&cfg, kern, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, ksplit, epilogue);
 }
 
 }  // namespace
@@ -508,7 +828,7 @@ extern "C" wenc_status wenc_quantize_rows(const void* x, int x_dtype, int8_t* xq
 
 extern "C" size_t wenc_linear_i8_workspace(int M, int N, int K) {
   wenc_internal_clear_error();
-  if (M <= kRowsMost || N < 1 || K < 1) return 0;
+  if (M <= kRowsMost || N < 1 || K < 1 || on_chip(M, N, wenc_internal_sm_count())) return 0;
   return up256(size_t(M) * K * 2) + up256(size_t(N) * K * 2);
 }
 
@@ -521,48 +841,48 @@ extern "C" wenc_status wenc_linear_i8(const int8_t* xq, const float* x_scale, co
   if (epilogue < 0 || epilogue > 2) return bad(WENC_ERR_INVALID_ARG, "epilogue %lld unknown", epilogue);
   if (epilogue == WENC_EPI_BIAS_RESID_F32 && !resid) return bad(WENC_ERR_INVALID_ARG, "resid is NULL");
   if (M < 1) return bad(WENC_ERR_INVALID_ARG, "M must be >= 1");
-  const int bn = wenc_host::gemm_pick_bn(N);
-  if (N < 1 || bn == 0) return bad(WENC_ERR_UNSUPPORTED, "N %lld: must be a multiple of 128", N);
+  if (M > (1 << 28)) return bad(WENC_ERR_UNSUPPORTED, "M %lld: at most 2^28", M);
+  if (N < 128 || N % 128 != 0) return bad(WENC_ERR_UNSUPPORTED, "N %lld: must be a positive multiple of 128", N);
   if (K < 64 || K % 64 != 0) return bad(WENC_ERR_UNSUPPORTED, "K %lld: must be a positive multiple of 64", K);
   if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(bias, 16) || !aligned(w_scale, 16) || !aligned(out, 16) ||
       !aligned(resid, 16) || !aligned(x_scale, 4))
     return bad(WENC_ERR_INVALID_ARG, "buffers must be 16-byte aligned (x_scale: 4)");
-  const size_t need = wenc_linear_i8_workspace(M, N, K);
-  if (need > 0 && (!workspace || workspace_bytes < need))
-    return bad(WENC_ERR_INVALID_ARG, "linear_i8: workspace of %lld bytes needed, %lld given", static_cast<long long>(need),
-               workspace ? static_cast<long long>(workspace_bytes) : 0ll);
-  if (need > 0 && !aligned(workspace, 256))
-    return bad(WENC_ERR_INVALID_ARG, "linear_i8: the workspace must be 256-byte aligned");
   int sms = 0;
   uint32_t* err = nullptr;
   const wenc_status dst = wenc_internal_device(&sms, &err);
   if (dst != WENC_OK) return dst;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (M <= kRowsMost) {
-    auto rows = M <= 8 ? launch_rows_epi<1> : M <= 16 ? launch_rows_epi<2> : M <= 32 ? launch_rows_epi<4> : M <= 64 ? launch_rows_epi<8> : launch_rows_epi<16>;
-    const cudaError_t e = rows(epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, sms, s);
+  cudaError_t e;
+  if (M <= kRowsMost || on_chip(M, N, sms)) {
+    e = M <= 8           ? launch_rows<1>(epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, sms, s)
+        : M <= kRowsMost ? launch_rows<2>(epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, sms, s)
+                         : launch_tc(epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, sms, err, s);
     if (e != cudaSuccess) return launch_failed("linear_i8 launch", e);
     return WENC_OK;
   }
-  const size_t na = size_t(M) * K, nw = size_t(N) * K;
+  const int bn = wenc_host::gemm_pick_bn(N);
+  const size_t na = size_t(M) * K, nw = size_t(N) * K, a_bytes = up256(na * 2), need = a_bytes + up256(nw * 2);
+  if (!workspace || workspace_bytes < need)
+    return bad(WENC_ERR_INVALID_ARG, "linear_i8: workspace of %lld bytes needed, %lld given", static_cast<long long>(need),
+               workspace ? static_cast<long long>(workspace_bytes) : 0ll);
+  if (!aligned(workspace, 256)) return bad(WENC_ERR_INVALID_ARG, "linear_i8: the workspace must be 256-byte aligned");
   uint16_t* ab = static_cast<uint16_t*>(workspace);
-  uint16_t* wb = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + up256(na * 2));
+  uint16_t* wb = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + a_bytes);
   std::string why;
   CUtensorMap ta, tw, tw_h;
-  const bool ok = wenc_host::make_tmap_2d_bf16(&ta, ab, K, M, size_t(K) * 2, 64, wenc_host::kGemmBM, &why) &&
-                  wenc_host::make_tmap_2d_bf16(&tw, wb, K, N, size_t(K) * 2, 64, bn, &why) &&
-                  wenc_host::make_tmap_2d_bf16(&tw_h, wb, K, N, size_t(K) * 2, 64, bn / 2, &why);
-  if (!ok) return wenc_internal_fail(WENC_ERR_INVALID_ARG, why.c_str());
+  if (!wenc_host::make_tmap_2d_bf16(&ta, ab, K, M, size_t(K) * 2, 64, wenc_host::kGemmBM, &why) ||
+      !wenc_host::make_tmap_2d_bf16(&tw, wb, K, N, size_t(K) * 2, 64, bn, &why) ||
+      !wenc_host::make_tmap_2d_bf16(&tw_h, wb, K, N, size_t(K) * 2, 64, bn / 2, &why))
+    return wenc_internal_fail(WENC_ERR_INVALID_ARG, why.c_str());
   size_t blocks = ((na + nw) / 16 + 255) / 256;
   if (blocks > size_t(16) * sms) blocks = size_t(16) * sms;
-  cudaError_t e = wenc_host::launch_pdl(widen_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, xq, ab, na, wq,
-                                        wb, nw);
+  e = wenc_host::launch_pdl(widen_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, xq, ab, na, wq, wb, nw);
   if (e != cudaSuccess) return launch_failed("linear_i8 widening", e);
   wenc_host::GemmExtra ex;
   ex.colsum = w_scale;
   ex.row_scale = x_scale;
-  e = wenc_host::launch_gemm(ta, tw, M, N, K, bn, wenc_host::kEpiScaled + epilogue, bias, resid, out, err, sms, s, false,
-                             0, ex, &tw_h);
+  e = wenc_host::launch_gemm(ta, tw, M, N, K, bn, wenc_host::kEpiScaled + epilogue, bias, resid, out, err, sms, s, false, 0, ex,
+                             &tw_h);
   if (e != cudaSuccess) return launch_failed("linear_i8 launch", e);
   return WENC_OK;
 }

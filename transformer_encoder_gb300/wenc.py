@@ -823,12 +823,16 @@ def linear_i8(a, a_scale, w, w_scale, bias, epilogue: int = EPI_BIAS_BF16, resid
         if resid.get_device() != dev:
             raise _elsewhere((("resid", resid),))
         rp = resid.data_ptr()
-    if workspace is None:
+    ws = ws_bytes = 0
+    if workspace is not None:
+        if workspace.get_device() != dev:
+            raise _elsewhere((("workspace", workspace),))
+    elif M > 16:
         need = _lib.wenc_linear_i8_workspace(M, N, K)
-        workspace = _scratch(need, a, stream) if need else None
-    elif workspace.get_device() != dev:
-        raise _elsewhere((("workspace", workspace),))
-    ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        if need:
+            workspace = _scratch(need, a, stream)
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     status = _lib.wenc_linear_i8(a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), bias.data_ptr(), rp,
                                  out.data_ptr(), M, N, K, epilogue, ws, ws_bytes, _raw_stream(stream, dev))
     if status:
