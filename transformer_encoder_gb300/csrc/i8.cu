@@ -13,7 +13,7 @@
 //  - up to 16 tokens (a decode step of few beams): mma.sync on weights that go from global memory to
 //    registers (i8_rows_kernel): a 128-row tcgen05 tile would give too few CTAs to keep the weights' bytes
 //    coming;
-//  - up to about half an output tile of 128 x 128 per SM: tcgen05 on operands widened on the chip
+//  - up to an output tile of 128 x 128 per SM: tcgen05 on operands widened on the chip
 //    (i8_tc_kernel), no workspace;
 //  - more: the operands are widened to bf16 in the workspace and multiplied by the GEMM of gemm.cu, whose
 //    epilogue applies the scales. On-chip widening repeats itself in every tile, and its loads and stores then
@@ -732,10 +732,12 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 // The few-token form up to this many tokens.
 constexpr int kRowsMost = 16;
 
-// Whether the operands are widened on the chip: up to one output tile (128 x 128) for every second SM. Measured
-// around it (us, on the chip / two passes): 5120 x 1280 at 256 tokens (80 tiles) 14.9 / 14.8, at 512 19.7 / 15.7;
-// 1280 x 5120 at 1024 (80) 34.0 / 34.2; 1536 x 512 at 512 (48) 9.1 / 8.4, at 128 (12) 6.6 / 8.0.
-bool on_chip(int M, int N, int sms) { return static_cast<long long>((M + kTcTok - 1) / kTcTok) * (N / 128) <= sms / 2; }
+// Whether the operands are widened on the chip: up to one output tile (128 x 128) per SM. Measured around it (us on
+// the device, on the chip / two passes): 1536 x 512 at 128 tokens (12 tiles) 6.6 / 8.0, at 512 (48) 9.1 / 8.4, at
+// 1024 (96) 11.1 / 9.5; 5120 x 1280 at 256 (80) 14.9 / 14.8, at 512 (160) 19.7 / 15.7; 1280 x 5120 at 256 (20) 15.6 /
+// 31.7, at 1024 (80) 34.0 / 34.2. The second form's workspace, second launch and tensor maps cost its caller about 7 us
+// more on the host, which is what an eager call of these sizes waits for.
+bool on_chip(int M, int N, int sms) { return static_cast<long long>((M + kTcTok - 1) / kTcTok) * (N / 128) <= sms; }
 
 // CTAs of a cluster that split K, for `tiles` output tiles: until the machine has a CTA per SM, none with
 // fewer than `least` of the `pieces` of 64 k.

@@ -396,6 +396,12 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[r][e] = 0.0f;
     if constexpr (F32) {
+      // the products with a small part are summed apart: the tensor core's sums truncate, and these are 2^-11 as large
+      float small[NR][4];
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) small[r][e] = 0.0f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const float4 ka = lds_f4(sk + granule<true>(g, tq + 4 * c)), kb = lds_f4(sk + granule<true>(g + 8, tq + 4 * c));
@@ -412,11 +418,15 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
-            mma_tf32(s[r], h[i], ql[r][2 * c + i][0], ql[r][2 * c + i][1]);
-            mma_tf32(s[r], w[i], qh[r][2 * c + i][0], qh[r][2 * c + i][1]);
+            mma_tf32(small[r], h[i], ql[r][2 * c + i][0], ql[r][2 * c + i][1]);
+            mma_tf32(small[r], w[i], qh[r][2 * c + i][0], qh[r][2 * c + i][1]);
             mma_tf32(s[r], h[i], qh[r][2 * c + i][0], qh[r][2 * c + i][1]);
           }
       }
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[r][e] += small[r][e];
     } else {
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
