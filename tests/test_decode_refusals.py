@@ -40,6 +40,8 @@ def _attn(**kw):
     (dict(k_group_stride=-8), 1, b"stride"), (dict(block_table_stride=2), 1, b"block_table_stride"),
     (dict(q=264), 1, b"aligned"), (dict(v_pages=258), 1, b"aligned"), (dict(n_heads=8192, n_kv_heads=8192), 2, b"heads"),
     (dict(n_seqs=1 << 28, q_len=2, max_group=1 << 27), 2, b"tokens"),
+    (dict(n_seqs=1 << 22, n_heads=4096, max_group=1 << 21, q_stride=1 << 20, out_stride=1 << 20), 2, b"rows"),
+    (dict(k_page_stride=1 << 36), 2, b"2^36"),
 ])
 def test_prefix_attention_refuses(L, kw, status, word):
     a = _attn(**kw)

@@ -787,22 +787,13 @@ template <int NT>
 cudaError_t launch_rows(int epilogue, const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale, const float* bias,
                         const float* resid, void* out, int M, int N, int K, int sms, cudaStream_t stream) {
   using C = RowsCfg<NT>;
-  auto kern = i8_rows_kernel<NT>;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  static std::atomic<int> configured_device{-1};
-  if (C::SMEM > 48 * 1024 && configured_device.load(std::memory_order_acquire) != dev) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    configured_device.store(dev, std::memory_order_release);
-  }
+  static_assert(C::SMEM <= 48 * 1024, "no opt-in for more shared memory");
   const int tiles = N / kRowsChannels;
   const int ksplit = pick_ksplit(tiles, K / 64, kRowsK / 64, sms);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cluster_config(cfg, attr, dim3(tiles * ksplit), 256, C::SMEM, ksplit, stream);
-  return cudaLaunchKernelEx(&cfg, kern, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, ksplit, epilogue);
+  return cudaLaunchKernelEx(&cfg, i8_rows_kernel<NT>, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, ksplit, epilogue);
 }
 
 }  // namespace

@@ -92,11 +92,13 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = hi + lo with both parts TF32 (11 significant bits each, nearest, ties away): the parts
-// miss x by at most 2^-24 |x|. The MMA ignores the 13 low bits of a TF32 operand, so lo keeps them.
+// x = hi + lo for two TF32 operands: hi is x rounded to 11 significant bits, lo the (exact) rest, of which the
+// MMA reads the first 11 bits (it ignores the 13 low bits of a TF32 operand): together they miss x by less
+// than 2^-22 |x|, with the sign of lo, which is that of a rounding. A NaN passes: where the addition carries
+// it out of hi's exponent, lo is the NaN.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
   hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
 }
 // Transpose of an 8 x 8 matrix of 16-bit elements (lane: row lane / 4, columns 2 (lane % 4) and the next).
 __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
@@ -622,7 +624,7 @@ __device__ __forceinline__ void join_warps(const uint8_t* smem, int x, int c8, f
 // Eight elements of an output row, normalised (a row without a visible key: zeros).
 template <typename T>
 __device__ __forceinline__ void write_out8(const PrefixParams& p, int token, int head, int c8, const float (&v)[8], float l) {
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
   uint8_t* dst = p.out + static_cast<long long>(token) * p.out_stride + (head * HD + c8) * static_cast<int>(sizeof(T));
   if constexpr (sizeof(T) == 4) {
     reinterpret_cast<float4*>(dst)[0] = make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
@@ -768,7 +770,7 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
 __device__ __forceinline__ void write_partial(const PrefixParams& p, int token, int head, int slot, int c8, const float (&v)[8],
                                              float m, float l) {
   const size_t at = (static_cast<size_t>(token) * p.H + head) * (p.np + p.ns) + slot;
-  if (l > 0.0f) {
+  if (l != 0.0f) {  // (a NaN too: it has to reach the output)
     float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + c8);
     dst[0] = make_float4(v[0], v[1], v[2], v[3]);
     dst[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -895,12 +897,19 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PrefixParams p) 
     const int begin = p.group_start[lo], end = p.group_start[lo + 1];
     if (seq < begin || seq >= end || begin < 0 || end > p.n_seqs || end - begin > p.max_group) return;
   }
-  // lane c4 weighs slots c4, c4 + 16, ...; then every lane adds its four elements of all slots, several
-  // loads in flight (slots without keys wrote no O: weight 0, not read)
+  // lane c4 weighs slots c4, c4 + 16, ...; then every lane adds its four elements of all slots, eight
+  // loads in flight, the first eight before the weights are known (slots without keys wrote no O: what
+  // their memory holds is read but not used)
   const int n = p.np + p.ns;
   const float2* ml = p.part_ml + pair * n;
   const float* po = p.part_o + pair * n * HD + c4 * 4;
   const uint32_t lanes = 0xffffu << (threadIdx.x & 16);  // this row's half of the warp
+  float4 o[8];
+  auto fetch = [&](int j0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = *reinterpret_cast<const float4*>(po + static_cast<size_t>(min(j0 + j, n - 1)) * HD);
+  };
+  fetch(0);
   float m = -CUDART_INF_F;
   for (int i = c4; i < n; i += 16) m = fmaxf(m, ml[i].x);
 #pragma unroll
@@ -910,32 +919,29 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PrefixParams p) 
   float l = 0.0f;
   for (int i0 = 0; i0 < n; i0 += 16) {
     const float2 x = i0 + c4 < n ? ml[i0 + c4] : make_float2(0.0f, 0.0f);
-    const float f = x.y > 0.0f ? ex2_approx(x.x - u) : 0.0f;
-    float part = f * x.y;
+    const float f = x.y != 0.0f ? ex2_approx(x.x - u) : 0.0f;
+    const uint32_t wrote = __ballot_sync(lanes, x.y != 0.0f) >> (threadIdx.x & 16);
+    float part = x.y != 0.0f ? f * x.y : 0.0f;
 #pragma unroll
     for (int d = 1; d < 16; d <<= 1) part += __shfl_xor_sync(lanes, part, d);
     l += part;
-    const int k = min(16, n - i0);
-    for (int j0 = 0; j0 < k; j0 += 8) {
-      float w[8];
-      float4 o[8];
+#pragma unroll
+    for (int j0 = 0; j0 < 16; j0 += 8) {
+      if (i0 + j0 >= n) break;
+      if (i0 + j0 > 0) fetch(i0 + j0);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        w[j] = __shfl_sync(lanes, f, (j0 + j) & 15, 16);
-        if (j0 + j >= k) w[j] = 0.0f;
-        o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (w[j] > 0.0f) o[j] = *reinterpret_cast<const float4*>(po + static_cast<size_t>(i0 + j0 + j) * HD);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        acc.x += w[j] * o[j].x;
-        acc.y += w[j] * o[j].y;
-        acc.z += w[j] * o[j].z;
-        acc.w += w[j] * o[j].w;
+        const float w = __shfl_sync(lanes, f, j0 + j, 16);
+        if ((wrote >> (j0 + j)) & 1u) {
+          acc.x += w * o[j].x;
+          acc.y += w * o[j].y;
+          acc.z += w * o[j].z;
+          acc.w += w * o[j].w;
+        }
       }
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
   uint8_t* dst = p.out + token * p.out_stride + (head * HD + c4 * 4) * sizeof(T);
   if constexpr (sizeof(T) == 4)
     *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
@@ -1015,9 +1021,9 @@ Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
   if (a->k_pages) {
     pl.nr_s = row_groups(rows_s, f32);
     pl.rows_s = static_cast<int>((rows_s + 8 * pl.nr_s - 1) / (8 * pl.nr_s));
-    // warps: about one round of the machine (24 an SM), no split of fewer than 64 keys
+    // warps: within one round of the machine (24 an SM), no split of fewer than 64 keys
     const long long items = static_cast<long long>(a->n_seqs) * a->n_kv_heads * pl.rows_s;
-    long long n = (24ll * sms + items - 1) / items;
+    long long n = 24ll * sms / items;
     if (n > (own_cap + 63) / 64) n = (own_cap + 63) / 64;
     if (n > 32) n = 32;
     pl.ns = static_cast<int>(n < 1 ? 1 : n);
@@ -1044,8 +1050,9 @@ bool check_sizes(const wenc_prefix_attention_args* a, wenc_status* st) {
   if (a->n_heads % a->n_kv_heads != 0)
     return no(WENC_ERR_INVALID_ARG, "prefix_attention: %lld query heads are no multiple of %lld key heads", a->n_heads,
               a->n_kv_heads);
-  if (static_cast<long long>(a->n_seqs) * a->q_len > (1ll << 28) || a->n_heads > 4096)
-    return no(WENC_ERR_UNSUPPORTED, "prefix_attention: more than 2^28 tokens or 4096 heads");
+  if (static_cast<long long>(a->n_seqs) * a->q_len > (1ll << 28) || a->n_heads > 4096 ||
+      static_cast<long long>(a->n_seqs) * a->q_len * a->n_heads > (1ll << 30))
+    return no(WENC_ERR_UNSUPPORTED, "prefix_attention: more than 2^28 tokens, 4096 heads or 2^30 rows of them");
   if (!a->k_prefix && !a->k_pages) return no(WENC_ERR_INVALID_ARG, "prefix_attention: neither prefix nor pages");
   if ((a->k_prefix == nullptr) != (a->v_prefix == nullptr) || (a->k_pages == nullptr) != (a->v_pages == nullptr))
     return no(WENC_ERR_INVALID_ARG, "prefix_attention: keys and values come together");
