@@ -27,6 +27,8 @@
  *    handle share its workspace and must be ordered by the caller (one stream, or events).
  *  - Argument errors are reported synchronously as a status; the message is available
  *    from wenc_last_error() on the same host thread. Nothing aborts the process.
+ *  - Make a first call of an entry point on a device before capturing it into a CUDA graph: it
+ *    loads the kernels and looks up device addresses.
  *  - Device-side waits are bounded (about one second); a wait that runs out records
  *    WENC_ERR_DEVICE_TIMEOUT in a device error word instead of hanging the GPU. It is
  *    reported by wenc_sync_status() and by the next wenc_forward* call on that handle.

@@ -14,8 +14,8 @@
 //
 // Up to 64 rows per key head (beams): one launch. A cluster of 1 to 8 CTAs attends one (group, key
 // head, tile of rows): its key list is the prefix followed by the own keys of each sequence of the tile,
-// cut into tiles of keys that belong to one of these segments each, and every CTA takes an equal run of
-// them. Own keys are scored against all of the tile's rows and masked to their sequence's. The CTAs'
+// cut into steps of 16 keys that belong to one of these segments each, and every warp of the cluster takes an
+// equal run of them. Own keys are scored against all of the tile's rows and masked to their sequence's. The CTAs'
 // results (m, l, O) are joined through distributed shared memory: no workspace and no second kernel.
 // More rows: a work item is a share of a group's prefix, or of one sequence's own keys; items write
 // partial results to the workspace and a second kernel joins them. The bf16 prefix then runs on the
@@ -31,6 +31,20 @@
 // bf16: P is split into two bf16 parts before the product with V, so its rounding (2^-16 after the
 // split) does not add to the output's own. fp32: every product is three TF32 products of two-part
 // operands.
+//
+// Measured (us on the device, calls of a captured graph over inputs that do not fit L2 together; bytes of K
+// and V at the measured copy rate in brackets):
+//   16 windows x 5 beams, 20 heads, 1500 cross keys, bf16     22.8 [18.2]   5.4 TB/s
+//   the same beams' self-attention, ragged, pages of 16       15.9 [7.0]
+//   4 windows x 5 beams x 3 tokens, 8 heads, fp32, pages of 24 12.5 [3.8]
+//   1 window, 1 beam, 6 heads, 1500 keys, bf16                 4.9 [0.3]: launch and latency
+// What the choices gave, on the first of these unless said: rows as the MMA's M, tiles of 128 keys by four warps 29.5;
+// four CTAs a cluster for more CTAs 40.2, one CTA an item and three an SM 23.7 (the CTAs of one round hide each
+// other's latency; more of them only repeat the start of a CTA, some 4 us); S^T with eight warps 22.3. On the
+// second: 40.7, 26.4 and 22.2, then 18.8 with 32-bit address factors and 15.9 with runs of 16-key steps (tiles of
+// 128 left warps idle at every segment's end). Three stages a warp instead of two cost the third CTA of an SM:
+// 28.8. What bounds them now: the latency of a warp's steps at 24 warps an SM (the stall counters show waits for
+// loads); in fp32, the instructions of the two-part splits at 8 warps an SM (253 registers).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -818,6 +832,8 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
   write_partial(p, begin * p.q_len + tok, it.hk * p.r + y - tok * p.r, split, c8, v, m, l);
 }
 
+// (256 sequences x 4 key heads, up to 600 own keys in pages of 64: 20 us for 78 MB; a CTA per item with its warps
+// joined was as fast alone but left twice the idle warps behind short sequences, 43.5 against 44.9 us for the call.)
 // Second form, own keys: one warp per (sequence, key head, row tile, split); its rows go through the
 // warp's stretch of shared memory to full lines of the partial results.
 template <typename T, int NR>
