@@ -8,8 +8,8 @@ are scaled so that |argument| < 128) and 2^-21 for exp2: p is off by e = 1.1 d +
 relative, numerator and denominator both. P enters the product as two bf16 parts: 2^-16 more in the
 numerator. Sums over n keys: n * 2^-23 each. Output rounding: 2^-8 (half a step of bf16).
   |err| <= 2^-8 |o| + (2 e + 2^-16 + 2 n 2^-23) sum_j p_j |v_j|
-bf16, more than 64 rows per key head behind a prefix (the tcgen05 form): P enters as one bf16 number,
-2^-8 instead of 2^-16 in the numerator.
+bf16, more than 64 rows per key head behind a prefix: where that is the tcgen05 form, P enters as one bf16
+number, 2^-8 instead of 2^-16 in the numerator.
 fp32: every operand is two TF32 parts that miss it by less than 2^-22 (11 bits rounded, 11 more of the rest cut
 off), the product of the small parts (2^-11 each) is dropped: 3 * 2^-22 a product, and three times as many
 accumulations; output 2^-24:
@@ -223,10 +223,21 @@ def test_many_rows_behind_a_long_prompt():
     c.check(c.run())
 
 
+def _joins(c):
+    """Whether the case runs in the form that joins partial results (it alone needs a workspace)."""
+    import torch
+    from transformer_encoder_gb300 import WencError, prefix_attention
+    try:
+        prefix_attention(c.tq, **c.kw, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+    except WencError as e:
+        return "workspace" in str(e)
+    return False
+
+
 @pytest.mark.parametrize("H,Hkv,q_len,sizes,pre", [
-    (2, 2, 1, [65], [1]), (2, 2, 1, [300], [129]), (6, 2, 1, [90, 5], [257, 0]), (6, 2, 4, [30, 1, 25], [128, 700, 5]),
-    (5, 1, 1, [51], [1500]), (40, 1, 1, [7, 2], [300, 64]), (128, 1, 1, [3], [200]), (4, 4, 7, [10, 40], [1000, 127]),
-    (3, 1, 1, [200], [0]), (1, 1, 1, [600], [2500])])
+    (32, 32, 1, [160], [1]), (32, 32, 1, [165], [129]), (96, 32, 1, [60, 5], [257, 0]), (48, 16, 4, [30, 1, 25], [128, 700, 5]),
+    (80, 16, 1, [70], [900]), (40, 1, 1, [130, 2], [300, 64]), (128, 1, 1, [45], [200]), (4, 4, 7, [40, 180], [500, 127]),
+    (96, 32, 1, [70], [0]), (1, 1, 1, [2500], [1700])])
 @pytest.mark.parametrize("own", [False, True])
 def test_many_rows(H, Hkv, q_len, sizes, pre, own):
     """The tcgen05 form: grouped heads that do and do not divide a tile's 128 rows, several row tiles,
@@ -236,12 +247,37 @@ def test_many_rows(H, Hkv, q_len, sizes, pre, own):
     suf = [int(r.integers(0, 20)) for _ in range(sum(sizes))] if own else None
     c = Case("bf16", sizes, q_len, H, Hkv, pre, suf, page=8, uneven=len(sizes) > 1, seed=H + q_len, prefix_max=max(pre) + 37,
              strided=own)
+    assert _joins(c)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("H,Hkv,q_len,sizes,pre", [
+    (2, 2, 1, [65], [1]), (2, 2, 1, [300], [129]), (6, 2, 1, [90, 5], [257, 0]), (6, 2, 4, [30, 1, 25], [128, 700, 5]),
+    (5, 1, 1, [51], [1500]), (40, 1, 1, [7, 2], [300, 64]), (128, 1, 1, [3], [200]), (4, 4, 7, [10, 40], [1000, 127])])
+def test_many_rows_of_little_work(dtype, H, Hkv, q_len, sizes, pre):
+    """More than 64 rows in the one-launch form: several row tiles per group, each over the whole prefix."""
+    r = np.random.default_rng(sum(sizes) + H)
+    c = Case(dtype, sizes, q_len, H, Hkv, pre, [int(r.integers(0, 20)) for _ in range(sum(sizes))], page=8,
+             uneven=len(sizes) > 1, seed=H + q_len, prefix_max=max(pre) + 37, strided=True)
+    assert not _joins(c)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("H,Hkv,q_len,sizes,pre", [(32, 32, 1, [165], [129]), (48, 16, 4, [10, 1, 25], [128, 300, 5])])
+def test_many_rows_f32(H, Hkv, q_len, sizes, pre):
+    """The form that joins partial results, fp32."""
+    r = np.random.default_rng(sum(sizes) + H)
+    c = Case("f32", sizes, q_len, H, Hkv, pre, [int(r.integers(0, 20)) for _ in range(sum(sizes))], page=8,
+             uneven=len(sizes) > 1, seed=H + q_len, prefix_max=max(pre) + 37)
+    assert _joins(c)
     c.check(c.run())
 
 
 @pytest.mark.parametrize("scale", [0.125, 0.3, -0.2, 0.0])
 def test_many_rows_scales(scale):
-    c = Case("bf16", [70], 1, 2, 2, [300], [int(x) for x in np.random.default_rng(0).integers(0, 9, 70)], seed=15)
+    c = Case("bf16", [160], 1, 32, 32, [300], [int(x) for x in np.random.default_rng(0).integers(0, 9, 160)], seed=15)
+    assert _joins(c)
     c.check(c.run(scale=scale), scale)
 
 
@@ -250,8 +286,9 @@ def test_many_rows_on_another_stream_and_in_two_graphs():
     with the workspace of its own capture."""
     import torch
     from transformer_encoder_gb300 import prefix_attention
-    cases = [Case("bf16", [80], 1, 2, 2, [700], [30] * 80, seed=s) for s in (17, 18)]
-    cases.append(Case("f32", [40], 1, 4, 2, [300], [30] * 40, seed=19))
+    cases = [Case("bf16", [170], 1, 32, 32, [700], [30] * 170, seed=s) for s in (17, 18)]
+    cases.append(Case("f32", [170], 1, 32, 32, [100], [30] * 170, seed=19))
+    assert all(_joins(c) for c in cases)
     want = [c.run() for c in cases]
     s = torch.cuda.Stream()
     torch.cuda.synchronize()
@@ -279,13 +316,14 @@ def test_many_rows_on_another_stream_and_in_two_graphs():
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("size", [3, 70])
+@pytest.mark.parametrize("size", [3, 70, 2600])
 def test_nan_queries_and_keys_reach_their_rows_alone(dtype, size):
     """A NaN query, and a NaN among a sequence's visible own keys, make those rows NaN and no others,
     in the one-launch form and in the one that joins partial results."""
     import torch
     from transformer_encoder_gb300 import prefix_attention, sync_status
     c = Case(dtype, [size], 1, 2, 2, [50], [9] * size, seed=20)
+    assert _joins(c) == (size == 2600)
     want = c.run()
     q = c.tq.clone()
     q[1, 0, 0] = float("nan")
@@ -301,7 +339,8 @@ def test_nan_queries_and_keys_reach_their_rows_alone(dtype, size):
 
 def test_many_rows_of_no_group_stay():
     import torch
-    c = Case("bf16", [80, 66], 1, 2, 2, [90, 130], None, uneven=True, extra=3, seed=16)
+    c = Case("bf16", [80, 66], 1, 32, 32, [90, 130], None, uneven=True, extra=3, seed=16)
+    assert _joins(c)
     out = torch.full_like(c.tq, 7.0)
     c.check(c.run(out=out))
     assert (out[146:] == 7.0).all()

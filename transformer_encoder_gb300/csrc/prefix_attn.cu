@@ -12,12 +12,12 @@
 // once for all of a group's rows. What bounds it: bytes of K and V, and at these sizes the latency of
 // getting at them.
 //
-// Up to 64 rows per key head (beams): one launch. A cluster of 1 to 8 CTAs attends one (group, key
+// Up to 64 rows per key head (beams), and more where there is little to do: one launch. A cluster of 1 to 8 CTAs attends one (group, key
 // head, tile of rows): its key list is the prefix followed by the own keys of each sequence of the tile,
 // cut into steps of 16 keys that belong to one of these segments each, and every warp of the cluster takes an
 // equal run of them. Own keys are scored against all of the tile's rows and masked to their sequence's. The CTAs'
 // results (m, l, O) are joined through distributed shared memory: no workspace and no second kernel.
-// More rows: a work item is a share of a group's prefix, or of one sequence's own keys; items write
+// Else: a work item is a share of a group's prefix, or of one sequence's own keys; items write
 // partial results to the workspace and a second kernel joins them. The bf16 prefix then runs on the
 // fifth-generation tensor cores (prefix_tc.cu).
 //
@@ -151,7 +151,7 @@ struct Cfg {
   static constexpr int ROWS = 8 * NR;
   static constexpr int ROWB = HD * sizeof(T);
   static constexpr int STAGES = 2;
-  static constexpr int CTAS = F32 ? (NR == 1 ? 3 : 2) : NR == 1 ? 3 : NR == 2 ? 2 : 1;  // per SM, for the registers
+  static constexpr int CTAS = NR == 1 ? 3 : 2;  // per SM, for the registers
   static constexpr uint32_t HALF = KW * ROWB;  // bytes of K (or V) per warp and stage
   static constexpr uint32_t RING = NW * STAGES * 2 * HALF;
   static constexpr uint32_t P_BYTES = F32 ? NW * NR * 16 * 8 * 4 : 0;  // fp32: P on its way to B fragments
@@ -174,7 +174,7 @@ struct Item {
   int hk;
 };
 
-constexpr int kMaxOwn = 32;  // own-key segments of an item: at most one per row of a tile
+constexpr int kMaxOwn = 16;  // own-key segments of an item: at most one per row of a tile
 struct SegTable {
   int step0[kMaxOwn + 2];    // first step of each segment, and the end
   int len[kMaxOwn + 1];      // its keys
@@ -189,7 +189,7 @@ __device__ __forceinline__ int own_len_of(const PrefixParams& p, int seq, uint32
   return n;
 }
 
-// The segments' steps: a running sum over up to 33 lengths, by warp 0. Ends with a barrier.
+// The segments' steps: a running sum over up to 17 lengths, by warp 0. Ends with a barrier.
 __device__ __forceinline__ void fill_segments(const PrefixParams& p, const Item& it, SegTable& seg, uint32_t* err) {
   const int lane = threadIdx.x & 31;
   if (threadIdx.x < 32) {
@@ -984,9 +984,10 @@ struct Plan {
   size_t part_o = 0, bytes = 0;  // offset of the (m, l) pairs; workspace bytes
 };
 
-// Groups of 8 rows per tile: as few as hold the rows, within the registers (fp32 keeps two parts of
-// every query).
-int row_groups(long long rows, bool f32) { return rows <= 8 ? 1 : rows <= 16 || f32 ? 2 : 4; }
+// Groups of 8 rows per tile: one or two. More rows take more tiles, which read K and V again from L2: four groups
+// a tile leave registers for one CTA an SM (8 windows' 64 rows over 1500 keys 20.1 us, with tiles of 16 rows 13.3;
+// 20 rows 23.9 against 10.2).
+int row_groups(long long rows) { return rows <= 8 ? 1 : 2; }
 
 Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
   Plan pl;
@@ -998,14 +999,22 @@ Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
   const long long rows = group * rows_s;
   const long long own_cap = a->k_pages ? static_cast<long long>(a->max_pages) * a->page_size : 0;
   const long long prefix = a->k_prefix ? a->prefix_max : 0;
-  pl.nr_p = row_groups(rows, f32);
+  pl.nr_p = row_groups(rows);
   pl.rows_p = static_cast<int>((rows + 8 * pl.nr_p - 1) / (8 * pl.nr_p));
-  if (rows <= 64) {
+  // The one-launch form up to 64 rows; with more, while its CTAs fit one round of the machine and the prefix is little
+  // work (2^22 pairs of a row and a key). Measured around it (us, one launch / joined): 8 key heads x 256 rows over 2000
+  // keys (4.1 M pairs) 25.0 / 27.9, 512 rows (8.2 M) 41.0 / 42.3, 128 rows over 500 13.2 / 16.9; 4 x 128 over 8000 (4.1 M)
+  // 22.6 / 22.4, 4 x 192 (6.1 M) 37.4 / 28.3; 2 windows x 20 heads x 128 rows over 1500 (320 CTAs) 61.2 / 44.1; 16 windows
+  // x 20 heads x 96 rows 96.4 / 55.6.
+  const long long items = n_groups * a->n_kv_heads * pl.rows_p;
+  // (fp32 waits on its own instructions: more CTAs than are resident at once still gain, 21.0 against 24.4 us for 4
+  // windows x 40 rows)
+  const long long round = (f32 || pl.nr_p == 1 ? 3ll : 2ll) * sms;
+  if (rows <= 64 || (items <= round && n_groups * a->n_kv_heads * rows * prefix <= (1ll << 22))) {
     const long long tiles = (prefix + kt - 1) / kt + group * ((own_cap + kt - 1) / kt);
-    const long long items = n_groups * a->n_kv_heads * pl.rows_p;
-    // CTAs for about one round of the machine, none without a tile of its own
+    // CTAs within one round of the machine, none without a tile of its own
     pl.cluster = 1;
-    while (pl.cluster < 8 && pl.cluster < tiles && 2 * items * pl.cluster <= 3ll * sms) pl.cluster *= 2;
+    while (pl.cluster < 8 && pl.cluster < tiles && 2 * items * pl.cluster <= round) pl.cluster *= 2;
     pl.items_p = items * pl.cluster;
     return pl;
   }
@@ -1035,7 +1044,7 @@ Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
     pl.items_p = items * pl.np;
   }
   if (a->k_pages) {
-    pl.nr_s = row_groups(rows_s, f32);
+    pl.nr_s = row_groups(rows_s);
     pl.rows_s = static_cast<int>((rows_s + 8 * pl.nr_s - 1) / (8 * pl.nr_s));
     // warps: within one round of the machine (24 an SM), no split of fewer than 64 keys
     const long long items = static_cast<long long>(a->n_seqs) * a->n_kv_heads * pl.rows_s;
@@ -1195,21 +1204,15 @@ wenc_status launch_tc(const wenc_prefix_attention_args* a, const PrefixParams& p
 
 template <typename T>
 cudaError_t launch_all(PrefixParams p, const Plan& pl, uint32_t* err, cudaStream_t stream) {
-  constexpr bool F32 = sizeof(T) == 4;
   if (pl.cluster > 0) {
     p.row_tiles = pl.rows_p;
-    if (pl.nr_p == 1) return launch_cluster<T, 1>(p, pl.items_p, err, stream);
-    if (pl.nr_p == 2) return launch_cluster<T, 2>(p, pl.items_p, err, stream);
-    if constexpr (!F32) return launch_cluster<T, 4>(p, pl.items_p, err, stream);
-    return cudaErrorInvalidValue;
+    return pl.nr_p == 1 ? launch_cluster<T, 1>(p, pl.items_p, err, stream) : launch_cluster<T, 2>(p, pl.items_p, err, stream);
   }
-  constexpr int kMost = F32 ? 2 : 4;  // (more than 64 rows: the largest tiles)
   cudaError_t e = cudaSuccess;
-  if (pl.items_p > 0 && !pl.tc) e = launch_part<T, kMost>(p, pl.rows_p, pl.items_p, err, stream);
+  if (pl.items_p > 0 && !pl.tc) e = launch_part<T, 2>(p, pl.rows_p, pl.items_p, err, stream);
   if (e == cudaSuccess && pl.items_s > 0) {
-    if (pl.nr_s == 1) e = launch_own<T, 1>(p, pl.rows_s, pl.items_s, err, stream);
-    else if (pl.nr_s == 2) e = launch_own<T, 2>(p, pl.rows_s, pl.items_s, err, stream);
-    else e = launch_own<T, kMost>(p, pl.rows_s, pl.items_s, err, stream);
+    e = pl.nr_s == 1 ? launch_own<T, 1>(p, pl.rows_s, pl.items_s, err, stream)
+                     : launch_own<T, 2>(p, pl.rows_s, pl.items_s, err, stream);
   }
   if (e != cudaSuccess) return e;
   const long long threads = static_cast<long long>(p.n_seqs) * p.q_len * p.H * 16;

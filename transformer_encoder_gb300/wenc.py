@@ -645,7 +645,7 @@ def prefix_attention(q, k_prefix=None, v_prefix=None, *, prefix_lens=None, group
             H * hd if q.is_contiguous() else _token_stride(q, "q"), out_stride, G, S, g_start, kp, vp, kg,
             kt, vg, vt, T, p_lens, kpg, vpg, kps, vps, pages, size, tab, tab_stride, max_pages, own, scale)
     ws = ws_bytes = 0
-    # (up to 64 rows per key head need no workspace, as the library's own count confirms)
+    # (up to 64 rows per key head never need a workspace)
     if workspace is not None or (S or 1) * t * H > 64 * kv:
         if workspace is None:
             need = _lib.wenc_prefix_attention_workspace(_PREFIX_PACK.pack(*args, 0, 0))
