@@ -264,7 +264,7 @@ def test_many_rows_of_little_work(dtype, H, Hkv, q_len, sizes, pre):
     c.check(c.run())
 
 
-@pytest.mark.parametrize("H,Hkv,q_len,sizes,pre", [(32, 32, 1, [165], [129]), (48, 16, 4, [10, 1, 25], [128, 300, 5])])
+@pytest.mark.parametrize("H,Hkv,q_len,sizes,pre", [(32, 32, 1, [245], [129]), (48, 16, 4, [10, 1, 25], [128, 300, 5])])
 def test_many_rows_f32(H, Hkv, q_len, sizes, pre):
     """The form that joins partial results, fp32."""
     r = np.random.default_rng(sum(sizes) + H)
@@ -287,7 +287,7 @@ def test_many_rows_on_another_stream_and_in_two_graphs():
     import torch
     from transformer_encoder_gb300 import prefix_attention
     cases = [Case("bf16", [170], 1, 32, 32, [700], [30] * 170, seed=s) for s in (17, 18)]
-    cases.append(Case("f32", [170], 1, 32, 32, [100], [30] * 170, seed=19))
+    cases.append(Case("f32", [245], 1, 32, 32, [100], [30] * 245, seed=19))
     assert all(_joins(c) for c in cases)
     want = [c.run() for c in cases]
     s = torch.cuda.Stream()
@@ -316,14 +316,14 @@ def test_many_rows_on_another_stream_and_in_two_graphs():
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("size", [3, 70, 2600])
+@pytest.mark.parametrize("size", [3, 70, 3700])
 def test_nan_queries_and_keys_reach_their_rows_alone(dtype, size):
     """A NaN query, and a NaN among a sequence's visible own keys, make those rows NaN and no others,
     in the one-launch form and in the one that joins partial results."""
     import torch
     from transformer_encoder_gb300 import prefix_attention, sync_status
     c = Case(dtype, [size], 1, 2, 2, [50], [9] * size, seed=20)
-    assert _joins(c) == (size == 2600)
+    assert _joins(c) == (size == 3700)
     want = c.run()
     q = c.tq.clone()
     q[1, 0, 0] = float("nan")

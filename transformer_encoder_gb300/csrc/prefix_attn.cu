@@ -798,8 +798,8 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
   using C = Cfg<T, NR>;
   extern __shared__ __align__(128) uint8_t smem_dyn[];
   __shared__ SegTable seg;
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();  // (after the wait: the own keys' kernel starts without waiting for this one to end)
   int b = blockIdx.x;
   Item it;
   const int row0 = (b % p.row_tiles) * C::ROWS;
@@ -837,13 +837,15 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
 // Second form, own keys: one warp per (sequence, key head, row tile, split); its rows go through the
 // warp's stretch of shared memory to full lines of the partial results.
 template <typename T, int NR>
-__global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_own_kernel(const PrefixParams p, long long n_items,
+__global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_own_kernel(const PrefixParams p, long long n_items, bool beside,
                                                                                        uint32_t* err) {
   using C = Cfg<T, NR>;
   static_assert(C::STAGES * 2 * C::HALF >= 8 * C::OS * 4, "a warp's ring holds eight rows of results");
   extern __shared__ __align__(128) uint8_t smem_dyn[];
   pdl_trigger();
-  pdl_wait();
+  // beside: the kernel before this one is the prefix's, which let this one start once everything before it was
+  // complete; nothing of its is read here, so it is waited for at the end only (for the join after both)
+  if (!beside) pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
   long long b = static_cast<long long>(blockIdx.x) * C::NW + warp;
   if (b >= n_items) return;
@@ -889,6 +891,7 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
       }
     }
   }
+  if (beside) pdl_wait();
 }
 
 // Join of the partial results of one (token, head): sixteen lanes, four elements each.
@@ -1151,7 +1154,7 @@ cudaError_t launch_part(PrefixParams p, int row_tiles, long long blocks, uint32_
 }
 
 template <typename T, int NR>
-cudaError_t launch_own(PrefixParams p, int row_tiles, long long items, uint32_t* err, cudaStream_t stream) {
+cudaError_t launch_own(PrefixParams p, int row_tiles, long long items, bool beside, uint32_t* err, cudaStream_t stream) {
   using C = Cfg<T, NR>;
   auto kern = prefix_own_kernel<T, NR>;
   static std::atomic<int> configured{-1};
@@ -1159,7 +1162,7 @@ cudaError_t launch_own(PrefixParams p, int row_tiles, long long items, uint32_t*
   if (e != cudaSuccess) return e;
   p.row_tiles = row_tiles;
   return wenc_host::launch_pdl(kern, dim3(static_cast<unsigned>((items + C::NW - 1) / C::NW)), dim3(C::THREADS),
-                               C::RING + C::P_BYTES, stream, p, items, err);
+                               C::RING + C::P_BYTES, stream, p, items, beside, err);
 }
 
 // The prefix part on tcgen05.
@@ -1211,8 +1214,9 @@ cudaError_t launch_all(PrefixParams p, const Plan& pl, uint32_t* err, cudaStream
   cudaError_t e = cudaSuccess;
   if (pl.items_p > 0 && !pl.tc) e = launch_part<T, 2>(p, pl.rows_p, pl.items_p, err, stream);
   if (e == cudaSuccess && pl.items_s > 0) {
-    e = pl.nr_s == 1 ? launch_own<T, 1>(p, pl.rows_s, pl.items_s, err, stream)
-                     : launch_own<T, 2>(p, pl.rows_s, pl.items_s, err, stream);
+    const bool beside = pl.items_p > 0;
+    e = pl.nr_s == 1 ? launch_own<T, 1>(p, pl.rows_s, pl.items_s, beside, err, stream)
+                     : launch_own<T, 2>(p, pl.rows_s, pl.items_s, beside, err, stream);
   }
   if (e != cudaSuccess) return e;
   const long long threads = static_cast<long long>(p.n_seqs) * p.q_len * p.H * 16;
