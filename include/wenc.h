@@ -316,7 +316,8 @@ typedef struct {
   const int32_t* seq_start;  /* [n_seqs + 1], ascending from 0: sequence s owns the rows seq_start[s] ..
                                 seq_start[s+1]-1; NULL: n_tokens / n_seqs rows each */
   const int32_t* positions;  /* [n_tokens] the position each token turns by; NULL: its cache position */
-  const float* inv_freq;     /* [rot_dim / 2] angle per position; NULL: no rotation (rot_dim ignored) */
+  const float* inv_freq;     /* [rot_dim / 2] angle per position, finite and below 2^24 in magnitude, of
+                                either sign; NULL: no rotation (rot_dim ignored) */
   int rot_dim;               /* elements of each head that turn: a multiple of 16, 16..64 */
   int interleaved;           /* pairs (2i, 2i+1) instead of (i, i + rot_dim/2) */
 } wenc_kv_append_args;

@@ -53,7 +53,7 @@ TWO_PI = Fraction("6.28318530717958647692528676655900576839433879875021164194988
 def turns64(f):
     """The kernel's double arithmetic on one fp32 frequency."""
     c1, c2 = float.fromhex("0x1.45f306dp-3"), float.fromhex("0x1.9391054a7f09dp-32")
-    hi, lo = float(np.float32(f)) * c1, float(np.float32(f)) * c2
+    hi, lo = abs(float(np.float32(f))) * c1, abs(float(np.float32(f))) * c2
     hi -= np.floor(hi)
     h32 = hi * 4294967296.0
     top = int(h32)
@@ -62,19 +62,22 @@ def turns64(f):
     l32 = lo * 4294967296.0
     ltop = int(l32)
     llow = int((l32 - float(ltop)) * 4294967296.0)
-    return ((top << 32) + low + (ltop << 32) + llow) % 2 ** 64
+    turn = (top << 32) + low + (ltop << 32) + llow
+    return (-turn if f < 0 else turn) % 2 ** 64
 
 
-@pytest.mark.parametrize("f", [1.0, 0.5, 1e-4, 0.31622776, 3.1415927, 6.2831855, 100.0, -0.3, 0.0, 1e-30, 7.5])
+@pytest.mark.parametrize("f", [1.0, 0.5, 1e-4, 0.31622776, 3.1415927, 6.2831855, 100.0, -0.3, -1e-4, 0.0, 1e-30, 7.5, 1e6, -16777213.0])
 @pytest.mark.parametrize("pos", [0, 1, 4095, 1 << 20, (1 << 31) - 1, -1000, -(1 << 31)])
 def test_angles_are_exact_modulo_a_turn(f, pos):
     """position * frequency / 2 pi modulo 1 to 2^-31 of a turn (what the single-precision sine is
-    given), for every position of 32 bits: the fraction is off by less than 2^-62."""
+    given), for every position of 32 bits. The fraction is off by at most 2^-63 + |f| 2^-84: its two
+    truncations to 2^-64; c2 in [2^-32, 2^-31) is rounded by at most 2^-85, times |f|; the product
+    f c2 < |f| 2^-31 by half a step, at most |f| 2^-31 2^-53. That is below 2^-62 for |f| <= 2^20."""
     got = Fraction(turns64(f) * pos % 2 ** 64, 2 ** 64)
     want = Fraction(float(np.float32(f))) * pos / TWO_PI
     off = (got - want) % 1
     off = min(off, 1 - off)
-    assert off <= max(abs(pos), 1) * Fraction(1, 2 ** 62)
+    assert off <= max(abs(pos), 1) * (Fraction(1, 2 ** 63) + abs(Fraction(float(np.float32(f)))) / 2 ** 84)
     signed = turns64(f) * pos % 2 ** 64
     signed -= 2 ** 64 if signed >= 2 ** 63 else 0
     top = np.float32(signed >> 32) * np.float32(2.0 ** -31)  # sincospi's argument, in half turns

@@ -150,6 +150,14 @@ def test_other_frequencies():
     c.check(c.run())
 
 
+@pytest.mark.parametrize("far", [1 << 20, (1 << 31) - 64, -(1 << 31)])
+def test_negative_frequencies_at_far_positions(far):
+    """A negative frequency turns back by exactly what the positive one turns forward."""
+    f = np.concatenate([-_inv_freq(16), [-0.3, -1e-6, -7.5, -1e-8, -0.01, -0.7, -3.0, -1e6]])
+    c = Case("f32", [20, 13], [0, 4], 2, 2, 32, positions=[far + i for i in range(33)], inv_freq=f, seed=6)
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_padding_rows_and_in_place_queries(dtype):
     """Rows behind the last sequence stay; queries may turn in place, inside the fused rows."""

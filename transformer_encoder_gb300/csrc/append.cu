@@ -63,10 +63,12 @@ struct AppendParams {
 };
 
 // 2^64 * frac(f / 2 pi): the turns a position advances the angle by, as a 64-bit fraction.
-// 1 / 2 pi = c1 + c2 with c1 of 29 bits, so f * c1 is exact in double.
+// 1 / 2 pi = c1 + c2 with c1 of 29 bits, so f * c1 is exact in double. The fraction is taken of |f|:
+// of a negative number, x - floor(x) = 1 - |x| would drop the bits of |x| below 2^-54, and a position
+// of 31 bits carries those up to 2^-23 of a turn.
 __device__ __forceinline__ unsigned long long turns64(float f) {
   const double c1 = 0x1.45f306dp-3, c2 = 0x1.9391054a7f09dp-32;
-  double hi = static_cast<double>(f) * c1, lo = static_cast<double>(f) * c2;
+  double hi = fabs(static_cast<double>(f)) * c1, lo = fabs(static_cast<double>(f)) * c2;
   hi -= floor(hi);
   // hi in [0, 1): in two 32-bit parts (a conversion of hi * 2^64 could reach 2^64)
   const double h32 = hi * 4294967296.0;
@@ -76,7 +78,8 @@ __device__ __forceinline__ unsigned long long turns64(float f) {
   const double l32 = lo * 4294967296.0;
   const unsigned long long ltop = static_cast<unsigned long long>(l32);
   const unsigned long long llow = static_cast<unsigned long long>((l32 - static_cast<double>(ltop)) * 4294967296.0);
-  return (top << 32) + low + (ltop << 32) + llow;
+  const unsigned long long turn = (top << 32) + low + (ltop << 32) + llow;
+  return f < 0.0f ? 0ull - turn : turn;
 }
 
 // The last sequence s with seq_start[s] <= t among 0 .. n-1 (-1: none), by all lanes of a warp: 32
