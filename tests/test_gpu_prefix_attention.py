@@ -346,6 +346,38 @@ def test_many_rows_of_no_group_stay():
     assert (out[146:] == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("size", [2, 70, 3700])
+def test_padding_sequences_may_hold_anything(dtype, size):
+    """Lengths and page numbers of sequences behind the last group are not looked at, in any form."""
+    import torch
+    c = Case(dtype, [size, 1], 1, 2, 2, [50, 30], [9] * (size + 4), uneven=True, extra=3, seed=23)
+    assert _joins(c) == (size == 3700)
+    c.kw["lens"][-3:] = _i32([-5, 10 ** 9, 3])
+    c.kw["block_table"][-3:] = -7
+    out = torch.full_like(c.tq, 7.0)
+    c.check(c.run(out=out))
+    assert (out[-3:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("size", [3, 70, 3700])
+def test_scores_below_every_number_weigh_nothing(dtype, size):
+    """Finite queries and keys whose products pass fp32's range: such scores are -inf, alone in a tile, in
+    a share of the prefix, and before and behind keys that count."""
+    import torch
+    c = Case(dtype, [size], 1, 2, 2, [700], None, seed=24)
+    c.q[..., 0] = 16.0
+    c.tq = _dev(c.q, dtype)
+    c.kw["k_prefix"][0, :256, :, 0] = -3e38
+    c.kw["k_prefix"][0, 400:, :, 0] = -3e38
+    k, v = c.prefixes[0]
+    c.prefixes = [(k[256:400], v[256:400])]
+    c.check(c.run())
+    c.kw["prefix_lens"] = _i32([200])  # no other keys: no weight is a number
+    assert not torch.isinf(c.run()).any()
+
+
 def test_large_prefix_group_f32_draft_rows():
     c = Case("f32", [9, 9], 3, 4, 2, [700, 651], [int(x) for x in np.random.default_rng(0).integers(0, 60, 18)], page=24,
              seed=8)

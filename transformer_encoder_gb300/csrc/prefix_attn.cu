@@ -859,6 +859,11 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
   it.n_own = 1;
   it.row_off = row0;
   it.n_rows = min(p.q_len * p.r - row0, C::ROWS);
+  if (p.np && p.group_start && it.seq0 >= p.group_start[p.n_groups]) {
+    // a sequence behind the last group (padding): its length and pages may hold anything, its rows stay as they were
+    if (beside) pdl_wait();
+    return;
+  }
   const int len = own_len_of(p, it.seq0, err);
   int step0, n_steps;
   run_of((len + 15) / 16, split, p.ns, step0, n_steps);

@@ -369,7 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mx = fmaxf(fmax3(mc[0], mc[1], mc[2]), fmax3(fmax3(mc[3], mc[4], mc[5]), mc[6], mc[7]));
         const float mx_s = mx * scale_log2;
         const float m_new = (mx_s > m + kRescaleThreshold) ? mx_s : m;
-        const float alpha = ex2_approx(m - m_new);  // 0 on the first tile (m = -inf)
+        const float ref = m_new == -CUDART_INF_F ? 0.0f : m_new;  // (scores of -inf alone so far: weights of 0)
+        const float alpha = ex2_approx(m - ref);  // 0 on the first tile (m = -inf)
 
         // Ping-pong: the two tiles take turns on the exponentials (MUFU), so that one tile's
         // exponentials overlap the other tile's loads, stores and waits instead of contending.
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // p = 2^(s * scale_log2 - m_new): packed fp32x2 FMA for the argument, packed adds for the
         // row sum; P is packed to bf16 pairs before waiting on the previous PV product.
         const uint64_t c2 = pack_f32x2(scale_log2, scale_log2);
-        const uint64_t nm2 = pack_f32x2(-m_new, -m_new);
+        const uint64_t nm2 = pack_f32x2(-ref, -ref);
         uint64_t sum2a = pack_f32x2(0.0f, 0.0f), sum2b = sum2a;
         uint32_t pk[64];
 #pragma unroll
