@@ -229,6 +229,23 @@ def test_replayed_graph(dtype):
         c.check(q_out)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_new_queries_on_another_stream(raw):
+    """The tensor that is made for the queries is cleared in the order of the call's own stream, however
+    busy the current one is."""
+    import torch
+    from transformer_encoder_gb300 import kv_append
+    c = Case("bf16", [5, 9], [3, 0], 4, 2, 64, pad=3, seed=8)
+    table, lens = torch.from_numpy(c.table).cuda(), torch.tensor(c.lens, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(40_000_000)  # some 20 ms of the current stream
+    out = kv_append(c.k, c.v, c.kc, c.vc, table, lens, stream=side.cuda_stream if raw else side, **c.kw)
+    torch.cuda.synchronize()
+    c.check(out)
+    assert (out[c.n:] == 0).all()
+
+
 def test_offsets_past_32_bits():
     """A page more than 2^32 bytes into the pool."""
     import torch

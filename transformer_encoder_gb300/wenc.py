@@ -534,16 +534,19 @@ def _dtype_error(t, name):
     return TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
 
+def _on(stream):
+    """The given stream (a torch stream or a raw handle) as torch's current one."""
+    return _torch.cuda.stream(stream if isinstance(stream, _torch.cuda.Stream) else _torch.cuda.ExternalStream(
+        stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)))
+
+
 def _scratch(nbytes, like, stream):
     """Workspace from the allocator of the stream the call runs on (so that it is reused in that
     stream's order, and is a graph's own while it is being captured)."""
-    import torch
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
-        stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
-    with torch.cuda.stream(s):
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return _torch.empty(nbytes, dtype=_torch.uint8, device=like.device)
+    with _on(stream):
+        return _torch.empty(nbytes, dtype=_torch.uint8, device=like.device)
 
 
 def prefix_attention(q, k_prefix=None, v_prefix=None, *, prefix_lens=None, group_start=None, max_group=None,
@@ -693,7 +696,12 @@ def kv_append(k, v, k_pages, v_pages, block_table, lens, *, seq_start=None, q=No
         if len(qshape) != 3 or qshape[0] != n or qshape[2] != hd:
             raise ValueError(f"q must be [{n}, heads, {hd}], got {tuple(qshape)}")
         if q_out is None:
-            q_out = torch.zeros(qshape, dtype=dtype, device=q.device)
+            q_out = torch.empty(qshape, dtype=dtype, device=q.device)
+            if stream is None:
+                q_out.zero_()
+            else:
+                with _on(stream):  # in order with the kernel that writes over the zeros
+                    q_out.zero_()
         elif q_out.dtype is not dtype or q_out.shape != qshape:
             raise ValueError(f"q_out must be {dtype} {tuple(qshape)}, got {q_out.dtype} {tuple(q_out.shape)}")
         if q.get_device() != dev or q_out.get_device() != dev:
