@@ -150,6 +150,15 @@ def test_linear_i8(M, N, K, epilogue):
     _check(_run(*p, epilogue).double().cpu().numpy(), *p, epilogue, f"{M} x {N} x {K}")
 
 
+@pytest.mark.parametrize("epilogue", [0, 2])
+@pytest.mark.parametrize("M,N,K", [(3, 20608, 64), (17, 20608, 64), (128, 19584, 192), (129, 10240, 1088), (250, 9984, 1024),
+                                   (250, 10240, 192), (300, 19584, 128)])
+def test_linear_i8_many_channels(M, N, K, epilogue):
+    """More output tiles than SMs, from few tokens: in every form."""
+    p = _problem(M, N, K, seed=M)
+    _check(_run(*p, epilogue).double().cpu().numpy(), *p, epilogue, f"{M}x{N}x{K}")
+
+
 @pytest.mark.parametrize("M", [1, 8, 40, 200])
 def test_linear_i8_largest_sums(M):
     """All products 127^2 of one sign: sums far beyond 2^24."""

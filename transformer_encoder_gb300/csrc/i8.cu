@@ -13,8 +13,8 @@
 //  - up to 16 tokens (a decode step of few beams): mma.sync on weights that go from global memory to
 //    registers (i8_rows_kernel): a 128-row tcgen05 tile would give too few CTAs to keep the weights' bytes
 //    coming;
-//  - up to an output tile of 128 x 128 per SM: tcgen05 on operands widened on the chip
-//    (i8_tc_kernel), no workspace;
+//  - up to an output tile of 128 x 128 per SM, or few tokens and many channels: tcgen05 on operands widened on the
+//    chip (i8_tc_kernel), no workspace;
 //  - more: the operands are widened to bf16 in the workspace and multiplied by the GEMM of gemm.cu, whose
 //    epilogue applies the scales. On-chip widening repeats itself in every tile, and its loads and stores then
 //    bind the shared-memory pipe (24000 x 1280 x 5120: 399 us against 266 us for both passes; at 1024 x 1280
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const T* __res
 template <typename T, int VPT>
 cudaError_t launch_quantize(const T* x, int8_t* xq, float* scale, int rows, int nv, int threads, cudaStream_t s) {
   if (threads == 32)  // a warp per row, four rows a block
-    return wenc_host::launch_pdl(quantize_rows_kernel<T, VPT, true>, dim3((rows + 3) / 4), dim3(128), 0, s, x, xq, scale, rows, nv);
+    return wenc_host::launch_pdl(quantize_rows_kernel<T, VPT, true>, dim3((rows - 1) / 4 + 1), dim3(128), 0, s, x, xq, scale, rows, nv);
   return wenc_host::launch_pdl(quantize_rows_kernel<T, VPT, false>, dim3(rows), dim3(threads), 0, s, x, xq, scale, rows, nv);
 }
 
@@ -415,8 +415,13 @@ constexpr int kTcStages = 4;
 constexpr int kTcThreads = 288;  // 4 weight warps, 4 token warps, the issuing warp
 constexpr uint32_t kTcStageBytes = kTcTok * 128;
 constexpr uint32_t kTcBars = kTcStages * kTcStageBytes;
-constexpr uint32_t kTcSmem = 1024 + kTcBars + (2 * kTcStages + 2) * 8 + 16;
 constexpr uint32_t kTcColumns = 256;  // D 0..127, A stages of 32 columns from 128
+// More shared memory than the stages take, so that a third CTA never shares an SM with two of these, nor does a CTA
+// of another TMEM kernel (they take 160 KB and more): it would wait in its TMEM allocation for one of the two to
+// end, and these wait for the others of their cluster, which could be waiting in the same way elsewhere.
+constexpr uint32_t kTcSmem = 77 * 1024;
+static_assert(kTcSmem >= 1024 + kTcBars + (2 * kTcStages + 2) * 8 + 16 && 3 * (kTcSmem + 1024) > 228 * 1024,
+              "shared memory of the on-chip form");
 
 // kind::f16 with fp16 operands, both K-major, fp32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n) {
@@ -742,12 +747,16 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 // The few-token form up to this many tokens.
 constexpr int kRowsMost = 16;
 
-// Whether the operands are widened on the chip: up to one output tile (128 x 128) per SM. Measured around it (us on
-// the device, on the chip / two passes): 1536 x 512 at 128 tokens (12 tiles) 6.6 / 8.0, at 512 (48) 9.1 / 8.4, at
+// Whether the operands are widened on the chip: up to one output tile (128 x 128) per SM, and with more tiles where
+// the weights are most of the bytes: one row of tiles, or two of long rows. Measured around it (us on the device, on the chip / two passes): 1536 x 512 at 128 tokens (12 tiles) 6.6 / 8.0, at 512 (48) 9.1 / 8.4, at
 // 1024 (96) 11.1 / 9.5; 5120 x 1280 at 256 (80) 14.9 / 14.8, at 512 (160) 19.7 / 15.7; 1280 x 5120 at 256 (20) 15.6 /
-// 31.7, at 1024 (80) 34.0 / 34.2. The second form's workspace, second launch and tensor maps cost its caller about 7 us
+// 31.7, at 1024 (80) 34.0 / 34.2; 51968 x 1280 at 80 (406 tiles) 40 / 69, at 256 62 / 71, at 384 96 / 96; 20480 x 512 at 80
+// (160) 10.8 / 16.4, at 256 20.8 / 16.4; 51968 x 384 at 80 18.6 / 25.2, at 256 31.9 / 27.3. The second form's workspace, second launch and tensor maps cost its caller about 7 us
 // more on the host, which is what an eager call of these sizes waits for.
-bool on_chip(int M, int N, int sms) { return static_cast<long long>((M + kTcTok - 1) / kTcTok) * (N / 128) <= sms; }
+bool on_chip(int M, int N, int K, int sms) {
+  const int m_tiles = (M + kTcTok - 1) / kTcTok;
+  return m_tiles == 1 || (m_tiles == 2 && K >= 1024) || static_cast<long long>(m_tiles) * (N / 128) <= sms;
+}
 
 // CTAs of a cluster that split K, for `tiles` output tiles: until the machine has a CTA per SM, none with
 // fewer than `least` of the `pieces` of 64 k.
@@ -831,7 +840,7 @@ extern "C" wenc_status wenc_quantize_rows(const void* x, int x_dtype, int8_t* xq
 
 extern "C" size_t wenc_linear_i8_workspace(int M, int N, int K) {
   wenc_internal_clear_error();
-  if (M <= kRowsMost || N < 1 || K < 1 || on_chip(M, N, wenc_internal_sm_count())) return 0;
+  if (M <= kRowsMost || N < 1 || K < 1 || on_chip(M, N, K, wenc_internal_sm_count())) return 0;
   return up256(size_t(M) * K * 2) + up256(size_t(N) * K * 2);
 }
 
@@ -856,7 +865,7 @@ extern "C" wenc_status wenc_linear_i8(const int8_t* xq, const float* x_scale, co
   if (dst != WENC_OK) return dst;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (M <= kRowsMost || on_chip(M, N, sms)) {
+  if (M <= kRowsMost || on_chip(M, N, K, sms)) {
     e = M <= 8           ? launch_rows<1>(epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, sms, s)
         : M <= kRowsMost ? launch_rows<2>(epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, sms, s)
                          : launch_tc(epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, sms, err, s);
