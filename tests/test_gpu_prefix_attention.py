@@ -256,27 +256,43 @@ def test_many_rows(H, Hkv, q_len, sizes, pre, own):
     (2, 2, 1, [65], [1]), (2, 2, 1, [300], [129]), (6, 2, 1, [90, 5], [257, 0]), (6, 2, 4, [30, 1, 25], [128, 700, 5]),
     (5, 1, 1, [51], [1500]), (40, 1, 1, [7, 2], [300, 64]), (128, 1, 1, [3], [200]), (4, 4, 7, [10, 40], [1000, 127])])
 def test_many_rows_of_little_work(dtype, H, Hkv, q_len, sizes, pre):
-    """More than 64 rows in the one-launch form: several row tiles per group, each over the whole prefix."""
+    """More than 64 rows in the one-launch form (fp32: where the work is less than 3 * 2^18 pairs of a row and a
+    key): several row tiles per group, each over the whole prefix."""
     r = np.random.default_rng(sum(sizes) + H)
     c = Case(dtype, sizes, q_len, H, Hkv, pre, [int(r.integers(0, 20)) for _ in range(sum(sizes))], page=8,
              uneven=len(sizes) > 1, seed=H + q_len, prefix_max=max(pre) + 37, strided=True)
-    assert not _joins(c)
+    pairs = len(sizes) * H * q_len * max(sizes) * (max(pre) + 37)
+    assert _joins(c) == (dtype == "f32" and pairs > 3 << 18)
     c.check(c.run())
 
 
-@pytest.mark.parametrize("H,Hkv,q_len,sizes,pre", [(32, 32, 1, [245], [129]), (48, 16, 4, [10, 1, 25], [128, 300, 5])])
-def test_many_rows_f32(H, Hkv, q_len, sizes, pre):
-    """The form that joins partial results, fp32."""
+@pytest.mark.parametrize("H,Hkv,q_len,sizes,pre", [
+    (32, 32, 1, [245], [129]), (48, 16, 4, [10, 1, 25], [128, 300, 5]), (96, 32, 1, [60, 5], [257, 0]), (80, 16, 1, [70], [900]),
+    (40, 1, 1, [130, 2], [300, 64]), (128, 1, 1, [45], [200]), (130, 1, 1, [50], [150]), (4, 4, 7, [40, 180], [500, 127]),
+    (1, 1, 1, [2500], [1700]), (8, 8, 1, [1200], [1]), (8, 8, 1, [1200], [63]), (8, 8, 1, [1200], [64]), (8, 8, 1, [1200], [65]),
+    (16, 16, 1, [70, 70, 69, 3], [450, 449, 192, 1])])
+@pytest.mark.parametrize("own", [False, True])
+def test_many_rows_f32(H, Hkv, q_len, sizes, pre, own):
+    """The form that joins partial results, fp32: on tcgen05 up to 128 query heads per key head."""
     r = np.random.default_rng(sum(sizes) + H)
-    c = Case("f32", sizes, q_len, H, Hkv, pre, [int(r.integers(0, 20)) for _ in range(sum(sizes))], page=8,
-             uneven=len(sizes) > 1, seed=H + q_len, prefix_max=max(pre) + 37)
+    suf = [int(r.integers(0, 20)) for _ in range(sum(sizes))] if own else None
+    c = Case("f32", sizes, q_len, H, Hkv, pre, suf, page=8, uneven=len(sizes) > 1, seed=H + q_len, prefix_max=max(pre) + 37,
+             strided=own)
     assert _joins(c)
     c.check(c.run())
 
 
+def test_many_heads_per_key_head_bf16():
+    """More query heads per key head than a tcgen05 row tile holds."""
+    c = Case("bf16", [300], 1, 130, 1, [300], None, seed=25)
+    assert _joins(c)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("scale", [0.125, 0.3, -0.2, 0.0])
-def test_many_rows_scales(scale):
-    c = Case("bf16", [160], 1, 32, 32, [300], [int(x) for x in np.random.default_rng(0).integers(0, 9, 160)], seed=15)
+def test_many_rows_scales(dtype, scale):
+    c = Case(dtype, [160], 1, 32, 32, [300], [int(x) for x in np.random.default_rng(0).integers(0, 9, 160)], seed=15)
     assert _joins(c)
     c.check(c.run(scale=scale), scale)
 

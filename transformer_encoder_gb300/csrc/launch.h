@@ -171,6 +171,20 @@ struct PrefixTcArgs {
 };
 cudaError_t launch_prefix_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PrefixTcArgs& p,
                              uint32_t* err, int num_sms, cudaStream_t stream);
+// The same for float32 query rows (prefix_tc32.cu). Work items ((group * Hkv + key head) * n_x + row tile) * np + split,
+// one CTA each; strides in bytes.
+struct PrefixTc32Args {
+  const uint8_t *q, *kp, *vp;
+  long long q_stride, k_group, k_token, v_group, v_token;
+  const int32_t *group_start, *prefix_lens;
+  int n_seqs, q_len, H, Hkv, r, max_group, prefix_max;
+  int tokens, n_x, np, n_items, n_slots;
+  float scale_log2;
+  uint32_t q_flip, q_keep;  // a negative scale turns the queries' signs, a zero one clears them
+  float* part_o;
+  float2* part_ml;
+};
+cudaError_t launch_prefix_tc32(const PrefixTc32Args& p, uint32_t* err, cudaStream_t stream);
 // 3-D bf16 view [dim2][dim1][inner] with a box of box_inner x box1 x box2 (128-byte swizzle).
 bool make_tmap_3d_bf16_box(CUtensorMap* map, const void* base, uint64_t inner, uint64_t dim1, uint64_t dim2,
                            uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box_inner, uint32_t box1,

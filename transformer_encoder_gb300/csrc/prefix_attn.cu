@@ -12,14 +12,14 @@
 // once for all of a group's rows. What bounds it: bytes of K and V, and at these sizes the latency of
 // getting at them.
 //
-// Up to 64 rows per key head (beams), and more where there is little to do: one launch. A cluster of 1 to 8 CTAs attends one (group, key
-// head, tile of rows): its key list is the prefix followed by the own keys of each sequence of the tile,
-// cut into steps of 16 keys that belong to one of these segments each, and every warp of the cluster takes an
+// Up to 64 rows per key head (beams), and more where there is little to do: one launch. A cluster of 1 to 8 CTAs
+// attends one (group, key head, tile of rows): its key list is the prefix followed by the own keys of each sequence of
+// the tile, cut into steps of 16 keys that belong to one of these segments each, and every warp of the cluster takes an
 // equal run of them. Own keys are scored against all of the tile's rows and masked to their sequence's. The CTAs'
 // results (m, l, O) are joined through distributed shared memory: no workspace and no second kernel.
-// Else: a work item is a share of a group's prefix, or of one sequence's own keys; items write
-// partial results to the workspace and a second kernel joins them. The bf16 prefix then runs on the
-// fifth-generation tensor cores (prefix_tc.cu).
+// Else: a work item is a share of a group's prefix, or of one sequence's own keys; items write partial results to
+// the workspace and a third kernel joins them. The prefix then runs on the fifth-generation tensor cores
+// (prefix_tc.cu, and prefix_tc32.cu for fp32; prefix_part_kernel below takes what those two do not).
 //
 // Every warp has a ring of cp.async stages of its own and no barrier with other warps until their results
 // are joined at the end; an own-key item of the second form is one warp's. The products are transposed:
@@ -987,7 +987,7 @@ struct Plan {
   int rows_p = 0, rows_s = 0;   // row tiles
   int np = 0, ns = 0;           // key splits
   long long items_p = 0, items_s = 0;  // CTAs (one-launch form: items_p; tcgen05 form: work items)
-  bool tc = false;              // the prefix runs in prefix_tc.cu
+  bool tc = false;              // the prefix runs in prefix_tc.cu (bf16) or prefix_tc32.cu (fp32)
   int tokens = 0;               // its tokens per row tile
   size_t part_o = 0, bytes = 0;  // offset of the (m, l) pairs; workspace bytes
 };
@@ -996,6 +996,9 @@ struct Plan {
 // a tile leave registers for one CTA an SM (8 windows' 64 rows over 1500 keys 20.1 us, with tiles of 16 rows 13.3;
 // 20 rows 23.9 against 10.2).
 int row_groups(long long rows) { return rows <= 8 ? 1 : 2; }
+
+// What a CTA of prefix_tc32.cu costs beside its key tiles, in key tiles.
+constexpr int kTc32Start = 6;
 
 Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
   Plan pl;
@@ -1010,15 +1013,17 @@ Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
   pl.nr_p = row_groups(rows);
   pl.rows_p = static_cast<int>((rows + 8 * pl.nr_p - 1) / (8 * pl.nr_p));
   // The one-launch form up to 64 rows; with more, while its CTAs fit one round of the machine and the prefix is little
-  // work (2^22 pairs of a row and a key). Measured around it (us, one launch / joined): 8 key heads x 256 rows over 2000
+  // work (2^22 pairs of a row and a key; fp32, whose products run as three here, 3 * 2^18). Measured around it (us, one launch / joined): 8 key heads x 256 rows over 2000
   // keys (4.1 M pairs) 25.0 / 27.9, 512 rows (8.2 M) 41.0 / 42.3, 128 rows over 500 13.2 / 16.9; 4 x 128 over 8000 (4.1 M)
   // 22.6 / 22.4, 4 x 192 (6.1 M) 37.4 / 28.3; 2 windows x 20 heads x 128 rows over 1500 (320 CTAs) 61.2 / 44.1; 16 windows
-  // x 20 heads x 96 rows 96.4 / 55.6.
+  // x 20 heads x 96 rows 96.4 / 55.6. fp32: 2 key heads x 200 rows over 1500 (0.6 M) 9.5 / 13.9, 8 x 100 over 1000 (0.8 M)
+  // 14.9 / 12.8, 2 x 6 heads x 224 over 671 with own keys (1.8 M) 39.1 / 29.0, 8 x 100 over 3000 (2.4 M) 25.8 / 15.2.
   const long long items = n_groups * a->n_kv_heads * pl.rows_p;
   // (fp32 waits on its own instructions: more CTAs than are resident at once still gain, 21.0 against 24.4 us for 4
   // windows x 40 rows)
   const long long round = (f32 || pl.nr_p == 1 ? 3ll : 2ll) * sms;
-  if (rows <= 64 || (items <= round && n_groups * a->n_kv_heads * rows * prefix <= (1ll << 22))) {
+  const long long little = f32 ? 3ll << 18 : 1ll << 22;
+  if (rows <= 64 || (items <= round && n_groups * a->n_kv_heads * rows * prefix <= little)) {
     const long long tiles = (prefix + kt - 1) / kt + group * ((own_cap + kt - 1) / kt);
     // CTAs within one round of the machine, none without a tile of its own
     pl.cluster = 1;
@@ -1033,10 +1038,25 @@ Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
     if (n > 32) n = 32;
     return static_cast<int>(n < 1 ? 1 : n);
   };
-  // (a negative or zero scale, a group stride of 0 and more than 128 query heads per key head stay with
-  // the general form)
-  pl.tc = !f32 && a->k_prefix && r <= 128 && a->scale > 0.0f && (n_groups == 1 || (a->k_group_stride > 0 && a->v_group_stride > 0));
-  if (pl.tc) {
+  // (more than 128 query heads per key head, and in bf16 a negative or zero scale and a group stride of 0, stay
+  // with the general form)
+  pl.tc = a->k_prefix && r <= 128 &&
+          (f32 || (a->scale > 0.0f && (n_groups == 1 || (a->k_group_stride > 0 && a->v_group_stride > 0))));
+  if (pl.tc && f32) {
+    pl.tokens = static_cast<int>(128 / r);
+    pl.rows_p = static_cast<int>((group * a->q_len + pl.tokens - 1) / pl.tokens);
+    const long long items = n_groups * a->n_kv_heads * pl.rows_p, tiles = (prefix + 63) / 64;
+    // the split whose rounds of CTAs take the least time
+    long long best = 0;
+    for (int n = 1; n <= 32 && n <= tiles; ++n) {
+      const long long cost = ((items * n + sms - 1) / sms) * ((tiles + n - 1) / n + kTc32Start);
+      if (n == 1 || cost < best) {
+        best = cost;
+        pl.np = n;
+      }
+    }
+    pl.items_p = items * pl.np;
+  } else if (pl.tc) {
     pl.tokens = static_cast<int>(128 / r);
     pl.rows_p = static_cast<int>((group * a->q_len + 2 * pl.tokens - 1) / (2 * pl.tokens));  // pairs of row tiles
     const long long items = n_groups * a->n_kv_heads * pl.rows_p, tiles = (prefix + 127) / 128;
@@ -1210,6 +1230,45 @@ wenc_status launch_tc(const wenc_prefix_attention_args* a, const PrefixParams& p
   return WENC_OK;
 }
 
+// The fp32 prefix part on tcgen05.
+wenc_status launch_tc32(const PrefixParams& p, const Plan& pl, uint32_t* err, cudaStream_t stream) {
+  wenc_host::PrefixTc32Args t;
+  t.q = p.q;
+  t.kp = p.kp;
+  t.vp = p.vp;
+  t.q_stride = p.q_stride;
+  t.k_group = p.k_group;
+  t.k_token = p.k_token;
+  t.v_group = p.v_group;
+  t.v_token = p.v_token;
+  t.group_start = p.group_start;
+  t.prefix_lens = p.prefix_lens;
+  t.n_seqs = p.n_seqs;
+  t.q_len = p.q_len;
+  t.H = p.H;
+  t.Hkv = p.Hkv;
+  t.r = p.r;
+  t.max_group = p.max_group;
+  t.prefix_max = p.prefix_max;
+  t.tokens = pl.tokens;
+  t.n_x = pl.rows_p;
+  t.np = pl.np;
+  t.n_items = static_cast<int>(pl.items_p);
+  t.n_slots = pl.np + pl.ns;
+  t.scale_log2 = p.scale_log2;
+  t.q_flip = p.q_flip;
+  t.q_keep = p.q_keep;
+  t.part_o = p.part_o;
+  t.part_ml = p.part_ml;
+  const cudaError_t e = wenc_host::launch_prefix_tc32(t, err, stream);
+  if (e != cudaSuccess) {
+    char buf[200];
+    snprintf(buf, sizeof(buf), "prefix_attention launch: %s", cudaGetErrorString(e));
+    return wenc_internal_fail(WENC_ERR_CUDA, buf);
+  }
+  return WENC_OK;
+}
+
 template <typename T>
 cudaError_t launch_all(PrefixParams p, const Plan& pl, uint32_t* err, cudaStream_t stream) {
   if (pl.cluster > 0) {
@@ -1335,7 +1394,8 @@ extern "C" wenc_status wenc_prefix_attention(const wenc_prefix_attention_args* a
   p.part_o = static_cast<float*>(a->workspace);
   p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(a->workspace) + pl.part_o);
   if (pl.tc) {
-    st = launch_tc(a, p, pl, err, sms, reinterpret_cast<cudaStream_t>(stream));
+    st = bf ? launch_tc(a, p, pl, err, sms, reinterpret_cast<cudaStream_t>(stream))
+            : launch_tc32(p, pl, err, reinterpret_cast<cudaStream_t>(stream));
     if (st != WENC_OK) return st;
   }
   const cudaError_t e = a->dtype == WENC_DTYPE_F32
