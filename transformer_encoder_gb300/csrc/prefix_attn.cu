@@ -997,8 +997,23 @@ struct Plan {
 // 20 rows 23.9 against 10.2).
 int row_groups(long long rows) { return rows <= 8 ? 1 : 2; }
 
-// What a CTA of prefix_tc32.cu costs beside its key tiles, in key tiles.
-constexpr int kTc32Start = 6;
+// Into how many shares a prefix of `tiles` key tiles is split for `items` row tiles: as the rounds of one CTA an SM
+// take the least time, with `start` key tiles of time for what an item costs beside its own.
+int split_rounds(long long items, long long tiles, long long start, int sms) {
+  int np = 1;
+  long long best = 0;
+  for (int n = 1; n <= 32 && (n == 1 || n <= tiles); ++n) {
+    const long long cost = (items * n + sms - 1) / sms * ((tiles + n - 1) / n + start);
+    if (n == 1 || cost < best) {
+      best = cost;
+      np = n;
+    }
+  }
+  return np;
+}
+// In key tiles of 128 (prefix_tc.cu: with 1 tile 4 groups x 400 rows of 4 key heads over 2000 keys take 44.8 us, with 2 37.2;
+// with 3 16 groups x 20 heads x 128 rows over 1500 take 55.8, with 2 52.9) and of 64 (prefix_tc32.cu: 3 to 10 are alike).
+constexpr int kTcStart = 2, kTc32Start = 6;
 
 Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
   Plan pl;
@@ -1046,25 +1061,13 @@ Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
     pl.tokens = static_cast<int>(128 / r);
     pl.rows_p = static_cast<int>((group * a->q_len + pl.tokens - 1) / pl.tokens);
     const long long items = n_groups * a->n_kv_heads * pl.rows_p, tiles = (prefix + 63) / 64;
-    // the split whose rounds of CTAs take the least time
-    long long best = 0;
-    for (int n = 1; n <= 32 && n <= tiles; ++n) {
-      const long long cost = ((items * n + sms - 1) / sms) * ((tiles + n - 1) / n + kTc32Start);
-      if (n == 1 || cost < best) {
-        best = cost;
-        pl.np = n;
-      }
-    }
+    pl.np = split_rounds(items, tiles, kTc32Start, sms);
     pl.items_p = items * pl.np;
   } else if (pl.tc) {
     pl.tokens = static_cast<int>(128 / r);
     pl.rows_p = static_cast<int>((group * a->q_len + 2 * pl.tokens - 1) / (2 * pl.tokens));  // pairs of row tiles
     const long long items = n_groups * a->n_kv_heads * pl.rows_p, tiles = (prefix + 127) / 128;
-    // fill one round of the persistent CTAs, if the keys reach; at most 32 shares
-    long long n = sms / items;
-    if (n > tiles) n = tiles;
-    if (n > 32) n = 32;
-    pl.np = static_cast<int>(n < 1 ? 1 : n);
+    pl.np = split_rounds(items, tiles, kTcStart, sms);
     pl.items_p = items * pl.np;
   } else if (a->k_prefix) {
     const long long items = n_groups * a->n_kv_heads * pl.rows_p;
