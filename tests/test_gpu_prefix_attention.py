@@ -163,6 +163,24 @@ def test_uneven_groups(dtype, sizes):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("H,Hkv,pre", [(3, 1, None), (2, 2, [70, 0]), (40, 20, None), (40, 20, [300, 65])])
+def test_long_drafts(dtype, H, Hkv, pre):
+    """Many new tokens a sequence: rows of one sequence over many tiles, causal among its newest keys; own keys fewer
+    than, as many as, and more than the tokens."""
+    sizes = [3, 2] if pre else [1] * 5
+    c = Case(dtype, sizes, 130, H, Hkv, pre, [200, 130, 64, 0, 131], page=24, uneven=pre is not None, seed=26)
+    assert _joins(c) == (H == 40)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("page", [1, 3, 5, 1000])
+def test_page_sizes(dtype, page):
+    c = Case(dtype, [2, 3], 2, 4, 2, [20, 33], [17, 100, 2, 64, 31], page=page, uneven=True, seed=27)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_rows_of_no_group_stay(dtype):
     """Sequences behind the last group keep their rows of the output."""
     import torch
@@ -494,9 +512,20 @@ def test_offsets_past_32_bits():
 def test_bad_device_data_is_reported(what):
     """Lengths, offsets and page numbers out of range: reported, nothing out of range accessed, and
     the next call is clean again."""
+    _bad_device_data(Case("bf16", [2, 2], 1, 2, 2, [20, 30], [10, 20, 18, 17], seed=13, uneven=True, prefix_max=32), what)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("what", ["page", "negative page", "length", "negative length", "prefix length", "offsets", "group"])
+def test_bad_device_data_is_reported_by_many_rows(dtype, what):
+    c = Case(dtype, [130, 130], 1, 32, 32, [20, 30], [17] * 260, seed=13, uneven=True, prefix_max=32)
+    assert _joins(c)
+    _bad_device_data(c, what)
+
+
+def _bad_device_data(c, what):
     import torch
     from transformer_encoder_gb300 import WencError, prefix_attention, sync_status
-    c = Case("bf16", [2, 2], 1, 2, 2, [20, 30], [10, 20, 18, 17], seed=13, uneven=True, prefix_max=32)
     kw = {k: v.clone() if torch.is_tensor(v) else v for k, v in c.kw.items()}
     if what == "page":
         kw["block_table"][1, 0] = kw["k_pages"].shape[0]
@@ -511,7 +540,7 @@ def test_bad_device_data_is_reported(what):
     if what == "offsets":
         kw["group_start"][1] = 1 << 20
     if what == "group":
-        kw["group_start"][1] = 3  # three sequences, max_group 2
+        kw["group_start"][1] = kw["max_group"] + 1
     prefix_attention(c.tq, **kw)
     with pytest.raises(WencError, match="out of range") as e:
         sync_status()
