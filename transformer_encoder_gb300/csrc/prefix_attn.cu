@@ -1032,7 +1032,7 @@ Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
   // keys (4.1 M pairs) 25.0 / 27.9, 512 rows (8.2 M) 41.0 / 42.3, 128 rows over 500 13.2 / 16.9; 4 x 128 over 8000 (4.1 M)
   // 22.6 / 22.4, 4 x 192 (6.1 M) 37.4 / 28.3; 2 windows x 20 heads x 128 rows over 1500 (320 CTAs) 61.2 / 44.1; 16 windows
   // x 20 heads x 96 rows 96.4 / 55.6. fp32: 2 key heads x 200 rows over 1500 (0.6 M) 9.5 / 13.9, 8 x 100 over 1000 (0.8 M)
-  // 14.9 / 12.8, 2 x 6 heads x 224 over 671 with own keys (1.8 M) 39.1 / 29.0, 8 x 100 over 3000 (2.4 M) 25.8 / 15.2.
+  // 14.9 / 12.9, 2 x 6 heads x 224 over 671 with own keys (1.8 M) 39.1 / 28.4, 8 x 100 over 3000 (2.4 M) 25.8 / 14.8.
   const long long items = n_groups * a->n_kv_heads * pl.rows_p;
   // (fp32 waits on its own instructions: more CTAs than are resident at once still gain, 21.0 against 24.4 us for 4
   // windows x 40 rows)

@@ -16,17 +16,19 @@
 //    registers; each keeps a state of its own, joined at the end through shared memory;
 //  - one of converting warps: rows of K and V from global memory to registers, split, and stored to the swizzled
 //    stage (four stages of 48 KB; the next tile's loads are under way meanwhile);
-//  - one with the issuing warps, one for S = Q K^T and one for O = P V. Both products read their A operand (P, and
-//    Q's first two parts) from TMEM: with N = 64 a shared A would ask shared memory for more than its 128 bytes a cycle.
+//  - one of issuing warps, for S = Q K^T and for O = P V of each softmax warpgroup (a thread takes some 80 cycles for
+//    an MMA, the tensor core 45). Both products read their A operand (P, and Q's first two parts) from TMEM: with
+//    N = 64 a shared A would ask shared memory for more than its 128 bytes a cycle.
 // A row tile holds 128 / r tokens of all r query heads of the key head, as in prefix_tc.cu; the item's partial
 // result (m, l, O) goes to the workspace and prefix_join_kernel joins it with the others.
 //
 // Measured (us on the device; the mma.sync form of prefix_attn.cu in brackets): 2 groups x 410 rows of each of 8 key heads
-// over 5848 keys 94 (181), 59 GFLOP of bf16 products at 630 TFLOP/s; 2352 rows of each of 2 over 5101 45 (121); 64
-// sequences x 5 rows of 4 over 4000 27 (39). What bounds it: the 48 MMAs of a key tile, which take some 70 cycles each beside
-// the other warps' traffic (45 alone, and 32 if N were larger), and the latency of a tile's way through the four
-// roles. Tried on the first case: one warpgroup of softmax 116; one issuing warp 129; both rings apart, V two tiles behind
-// K, 109; sixteen lanes a row in the conversion 99; the six products of one k together 95.
+// over 5848 keys 80 (181), 59 GFLOP of bf16 products at 740 TFLOP/s; 2352 rows of each of 2 over 5101 40 (121); 64
+// sequences x 5 rows of 4 over 4000 26 (39). What bounds it: the converting warps (some 2500 cycles a key tile beside the
+// two softmax warps of their schedulers) and the 48 MMAs of a tile (2150 cycles alone; with N larger 1540). Steps on the first
+// case: one warpgroup of softmax 116; two, one issuing warp 129; two issuing warps 94, four 89; packed subtractions
+// 80. Not kept: K and V in rings of their own, V two tiles behind K, 108; sixteen lanes a row in the conversion 99 (of
+// 94); the six products of one k together 95 (of 94); a branch for whole tiles in place of predicated loads 125 (of 80).
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
@@ -53,8 +55,8 @@ constexpr uint32_t kPart = BKV * HD * 2;      // one part of K or V: 8 KB
 constexpr uint32_t kStageBytes = 6 * kPart;   // K in three parts, V in three parts
 constexpr uint32_t OFF_Q = kStages * kStageBytes;  // the queries' third part, 16 KB
 constexpr uint32_t OFF_BARS = OFF_Q + BQ * HD * 2;
-// full[4], empty[4], and per softmax warpgroup s_full, s_free, p_full, o_full; q_full, drain[2]
-constexpr int NUM_BARS = 2 * kStages + 8 + 3;
+// full[4], empty[4], and per softmax warpgroup s_full, s_free, p_full, o_full; q_full, drain[4]
+constexpr int NUM_BARS = 2 * kStages + 8 + 5;
 constexpr size_t SMEM = 1024 + OFF_BARS + NUM_BARS * 8 + 16;
 static_assert(SMEM <= 232448, "shared memory of the fp32 prefix kernel");
 constexpr uint32_t TMEM_COLS = 512;  // per softmax warpgroup S (64), O (64) and P (3 parts of 32); Q's first two parts (32 each)
@@ -80,6 +82,13 @@ __device__ __forceinline__ uint32_t cut_pair(float& x, float& y) {
   const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
   x -= __uint_as_float(a & 0xffff0000u);
   y -= __uint_as_float(b & 0xffff0000u);
+  return __byte_perm(a, b, 0x7632);
+}
+// The same with one packed subtraction (the softmax has no registers left for its aligned pairs).
+__device__ __forceinline__ uint32_t cut_pair_packed(float& x, float& y) {
+  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+  const float cx = __uint_as_float((a & 0xffff0000u) ^ 0x80000000u), cy = __uint_as_float((b & 0xffff0000u) ^ 0x80000000u);
+  unpack_f32x2(add_f32x2(pack_f32x2(x, y), pack_f32x2(cx, cy)), x, y);
   return __byte_perm(a, b, 0x7632);
 }
 __device__ __forceinline__ uint32_t top_pair(float x, float y) {
@@ -145,8 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc32_kernel(const wenc_hos
       mbar_init(o_full(b), 1);
     }
     mbar_init(q_full, 4);
-    mbar_init(drain, 1);
-    mbar_init(drain + 8u, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(drain + 8u * i, 1);
     *abort_flag = 0u;
     fence_barrier_init();
   }
@@ -358,7 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc32_kernel(const wenc_hos
         if (j + 1 < n_kv) load(i);
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
-          const uint32_t a = cut_pair(f[0], f[1]), b = cut_pair(f[2], f[3]), d = cut_pair(f[4], f[5]), e = cut_pair(f[6], f[7]);
+          const uint32_t a = cut_pair_packed(f[0], f[1]), b = cut_pair_packed(f[2], f[3]);
+          const uint32_t d = cut_pair_packed(f[4], f[5]), e = cut_pair_packed(f[6], f[7]);
           sts_v4(at + part * kPart, a, b, d, e);
         }
         sts_v4(at + 2 * kPart, top_pair(f[0], f[1]), top_pair(f[2], f[3]), top_pair(f[4], f[5]), top_pair(f[6], f[7]));
@@ -370,13 +379,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc32_kernel(const wenc_hos
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kIssueRegs) : "memory");
-    // ---------------- the issuing warps, one for S and one for O: all of a warp waits, lane 0 issues
-    if (warp == 12 && n_kv > 0) {
+    // ---------------- the issuing warps, two for S and two for O: all of a warp waits, lane 0 issues
+    const int odd = warp & 1;  // the tiles a warp issues for: those of one softmax warpgroup
+    if (warp < 14 && n_kv > 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(BQ, BKV, false);  // B = K tile, K-major
       const uint64_t qdesc = sdesc_sw128(s0 + OFF_Q, 16, 1024);
       bool ok = mbar_wait_warp(q_full, 0, wc, 54);
-      for (int j = 0; ok && j < n_kv; ++j) {
-        const int st = j % kStages, b = j & 1;
+      for (int j = odd; ok && j < n_kv; j += 2) {
+        const int st = j % kStages, b = odd;
         if (!mbar_wait_warp(full(st), (j / kStages) & 1, wc, 55)) break;
         if (j >= 2 && !mbar_wait_warp(s_free(b), ((j >> 1) - 1) & 1, wc, 56)) break;
         tc_fence_after();
@@ -394,10 +404,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc32_kernel(const wenc_hos
         }
         __syncwarp();
       }
-    } else if (warp == 13 && n_kv > 0) {
+    } else if (n_kv > 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(BQ, HD, true);  // B = V tile, MN-major
-      for (int j = 0; j < n_kv; ++j) {
-        const int st = j % kStages, b = j & 1;
+      for (int j = odd; j < n_kv; j += 2) {
+        const int st = j % kStages, b = odd;
         if (!mbar_wait_warp(p_full(b), (j >> 1) & 1, wc, 57)) break;
         tc_fence_after();
         if (lane == 0) {
@@ -414,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc32_kernel(const wenc_hos
       }
     }
     // every MMA issued completes before TMEM is released
-    if ((warp == 12 || warp == 13) && n_kv > 0) {
+    if (n_kv > 0) {
       if (lane == 0) {
         umma_commit(drain + 8u * (warp - 12));
         mbar_wait_drain(drain + 8u * (warp - 12), 0);
