@@ -259,10 +259,12 @@ __device__ __forceinline__ float ld_rank_f32(uint32_t saddr, int rank) {
 // takes 16 consecutive bytes of a weight row, which are four MMAs' worth of its fragments, so weights go from
 // global memory to registers in full 64-byte pieces and are widened there; the tokens are widened once
 // per CTA and round into shared memory, in the same order, rows 16 bytes past a multiple of 128 apart so
-// that the fragment loads touch all banks. Weights and tokens of the next round are on their way meanwhile.
+// that the fragment loads touch all banks. Weights and tokens of the next rounds are on their way meanwhile, and the
+// tokens' two buffers leave one barrier a round.
 // What bounds it: at a decode step's sizes, latency; the weights' bytes beyond. 1 x 1536 x 384 with its quantize_rows:
-// 3.2 us (10.0 in the two-pass form); 8 x 5120 x 1280: 4.5 us for 6.6 MB of weights. Against the tcgen05 form below: at 16
-// tokens 5.5 us (5120 x 1280), 3.9 (1536 x 512), 7.7 (1280 x 5120); at 32, 6.9 / 7.0, 5.5 / 4.5 and 10.7 / 9.4; at 80, 13.9
+// 3.2 us (10.0 in the two-pass form); 8 x 5120 x 1280: 3.7 us for 6.6 MB of weights (4.5 with one round under way); 1 x
+// 51968 x 1280: 15.6 us, 4.3 TB/s; 1 x 20480 x 5120: 27 us, 3.9 TB/s (35.6). Against the tcgen05 form below, with one round
+// under way: at 16 tokens 5.5 us (5120 x 1280; now 4.6), 3.9 (1536 x 512), 7.7 (1280 x 5120; now 6.4); at 32, 6.9 / 7.0, 5.5 / 4.5 and 10.7 / 9.4; at 80, 13.9
 // / 9.1, 9.5 / 5.9 and 21.3 / 12.1.
 constexpr int kRowsChannels = 32;
 constexpr int kRowsK = 256;  // k per round
@@ -273,11 +275,13 @@ struct RowsCfg {
   static constexpr int XROW = kRowsK * 2 + 16;            // bytes of a token's round in shared memory
   static constexpr int XN = (TOK * (kRowsK / 16) + 255) / 256;  // 16-byte pieces of x per thread and round
   static constexpr int RED = 8 * 16 * (TOK + 1) * 4;      // the warps' sums
-  static constexpr int SMEM = TOK * XROW > RED ? TOK * XROW : RED;
+  static constexpr int XBUF = TOK * XROW;                 // two of them
+  static constexpr int SMEM = 2 * XBUF > RED ? 2 * XBUF : RED;
 };
 
-template <int NT>
-__global__ void __launch_bounds__(256, 2) i8_rows_kernel(const int8_t* __restrict__ xq, const float* __restrict__ x_scale,
+// AHEAD rounds of weights are under way (even: the tokens' buffers alternate), and the registers are for CTAS per SM.
+template <int NT, int AHEAD, int CTAS>
+__global__ void __launch_bounds__(256, CTAS) i8_rows_kernel(const int8_t* __restrict__ xq, const float* __restrict__ x_scale,
                                                          const int8_t* __restrict__ wq, const float* __restrict__ w_scale,
                                                          const float* __restrict__ bias, const float* resid, void* out, int M,
                                                          int N, int K, int ksplit, int epilogue) {
@@ -296,15 +300,18 @@ __global__ void __launch_bounds__(256, 2) i8_rows_kernel(const int8_t* __restric
   const int8_t* wa = wq + static_cast<size_t>(n0 + 16 * c16 + g) * K + 16 * tq;
   const int8_t* wb = wa + static_cast<size_t>(8) * K;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  uint4 w0 = zero, w1 = zero, xv[C::XN];
-  auto fetch = [&](int k0) {  // the round that starts at k0, as far as it lies before k_end
+  uint4 w[AHEAD][2], xv[2][C::XN];
+  // weights and tokens of the round that starts at k0, as far as it lies before k_end
+  auto fetch_w = [&](uint4 (&w)[2], int k0) {
     const int k = k0 + 64 * quarter;
-    w0 = k < k_end ? __ldg(reinterpret_cast<const uint4*>(wa + k)) : zero;
-    w1 = k < k_end ? __ldg(reinterpret_cast<const uint4*>(wb + k)) : zero;
+    w[0] = k < k_end ? __ldg(reinterpret_cast<const uint4*>(wa + k)) : zero;
+    w[1] = k < k_end ? __ldg(reinterpret_cast<const uint4*>(wb + k)) : zero;
+  };
+  auto fetch_x = [&](uint4 (&x)[C::XN], int k0) {
 #pragma unroll
     for (int i = 0; i < C::XN; ++i) {
       const int at = threadIdx.x + 256 * i, tok = at / (kRowsK / 16), kk = k0 + at % (kRowsK / 16) * 16;
-      xv[i] = tok < M && kk < k_end ? *reinterpret_cast<const uint4*>(xq + static_cast<size_t>(tok) * K + kk) : zero;
+      x[i] = tok < M && kk < k_end ? *reinterpret_cast<const uint4*>(xq + static_cast<size_t>(tok) * K + kk) : zero;
     }
   };
   float acc[NT][4];
@@ -312,46 +319,58 @@ __global__ void __launch_bounds__(256, 2) i8_rows_kernel(const int8_t* __restric
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
-  fetch(k_begin);
-  for (int k0 = k_begin; k0 < k_end; k0 += kRowsK) {
-    // tokens of this round into shared memory as fp16, each 16-byte piece as 32 bytes
 #pragma unroll
-    for (int i = 0; i < C::XN; ++i) {
-      const int at = threadIdx.x + 256 * i, tok = at / (kRowsK / 16), piece = at % (kRowsK / 16);
-      if (tok < C::TOK) {
-        uint4 a, b;
-        widen_half(xv[i].x, a.x, a.y);
-        widen_half(xv[i].y, a.z, a.w);
-        widen_half(xv[i].z, b.x, b.y);
-        widen_half(xv[i].w, b.z, b.w);
-        uint4* dst = reinterpret_cast<uint4*>(smem + tok * C::XROW + piece * 32);
-        dst[0] = a;
-        dst[1] = b;
+  for (int d = 0; d < AHEAD; ++d) fetch_w(w[d], k_begin + d * kRowsK);
+  fetch_x(xv[0], k_begin);
+  fetch_x(xv[1], k_begin + kRowsK);
+  for (int k00 = k_begin; k00 < k_end; k00 += AHEAD * kRowsK) {
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) {
+      const int k0 = k00 + d * kRowsK;
+      if (k0 >= k_end) break;
+      uint8_t* buf = smem + (d & 1) * C::XBUF;
+      // tokens of this round into shared memory as fp16, each 16-byte piece as 32 bytes
+#pragma unroll
+      for (int i = 0; i < C::XN; ++i) {
+        const int at = threadIdx.x + 256 * i, tok = at / (kRowsK / 16), piece = at % (kRowsK / 16);
+        const uint4 x = xv[d & 1][i];
+        if (tok < C::TOK) {
+          uint4 a, b;
+          widen_half(x.x, a.x, a.y);
+          widen_half(x.y, a.z, a.w);
+          widen_half(x.z, b.x, b.y);
+          widen_half(x.w, b.z, b.w);
+          uint4* dst = reinterpret_cast<uint4*>(buf + tok * C::XROW + piece * 32);
+          dst[0] = a;
+          dst[1] = b;
+        }
+      }
+      fetch_x(xv[d & 1], k0 + 2 * kRowsK);
+      uint32_t wf[4][4];  // the fragments of four MMAs
+      const uint4 w0 = w[d][0], w1 = w[d][1];
+      widen_half(w0.x, wf[0][0], wf[0][2]);
+      widen_half(w1.x, wf[0][1], wf[0][3]);
+      widen_half(w0.y, wf[1][0], wf[1][2]);
+      widen_half(w1.y, wf[1][1], wf[1][3]);
+      widen_half(w0.z, wf[2][0], wf[2][2]);
+      widen_half(w1.z, wf[2][1], wf[2][3]);
+      widen_half(w0.w, wf[3][0], wf[3][2]);
+      widen_half(w1.w, wf[3][1], wf[3][3]);
+      fetch_w(w[d], k0 + AHEAD * kRowsK);
+      __syncthreads();  // (the next round writes the other buffer, which the last one's products have left)
+      const uint8_t* xs = buf + g * C::XROW + quarter * 128 + tq * 32;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint4 b0 = *reinterpret_cast<const uint4*>(xs + n * 8 * C::XROW);
+        const uint4 b1 = *reinterpret_cast<const uint4*>(xs + n * 8 * C::XROW + 16);
+        mma_f16(acc[n], wf[0], b0.x, b0.y);
+        mma_f16(acc[n], wf[1], b0.z, b0.w);
+        mma_f16(acc[n], wf[2], b1.x, b1.y);
+        mma_f16(acc[n], wf[3], b1.z, b1.w);
       }
     }
-    uint32_t wf[4][4];  // the fragments of four MMAs
-    widen_half(w0.x, wf[0][0], wf[0][2]);
-    widen_half(w1.x, wf[0][1], wf[0][3]);
-    widen_half(w0.y, wf[1][0], wf[1][2]);
-    widen_half(w1.y, wf[1][1], wf[1][3]);
-    widen_half(w0.z, wf[2][0], wf[2][2]);
-    widen_half(w1.z, wf[2][1], wf[2][3]);
-    widen_half(w0.w, wf[3][0], wf[3][2]);
-    widen_half(w1.w, wf[3][1], wf[3][3]);
-    __syncthreads();
-    if (k0 + kRowsK < k_end) fetch(k0 + kRowsK);
-    const uint8_t* xs = smem + g * C::XROW + quarter * 128 + tq * 32;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const uint4 b0 = *reinterpret_cast<const uint4*>(xs + n * 8 * C::XROW);
-      const uint4 b1 = *reinterpret_cast<const uint4*>(xs + n * 8 * C::XROW + 16);
-      mma_f16(acc[n], wf[0], b0.x, b0.y);
-      mma_f16(acc[n], wf[1], b0.z, b0.w);
-      mma_f16(acc[n], wf[2], b1.x, b1.y);
-      mma_f16(acc[n], wf[3], b1.z, b1.w);
-    }
-    __syncthreads();  // the next round overwrites the tokens
   }
+  __syncthreads();  // the sums go over the tokens
   // sums of the four quarters through shared memory: [warp][channel][token]
   float* red = reinterpret_cast<float*>(smem);
   constexpr int RS = C::TOK + 1;
@@ -802,17 +821,33 @@ cudaError_t launch_tc(int epilogue, const int8_t* xq, const float* x_scale, cons
   return cudaLaunchKernelEx(&cfg, i8_tc_kernel, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, ksplit, epilogue, err);
 }
 
+template <int NT, int AHEAD, int CTAS>
+cudaError_t launch_rows_as(int ksplit, int epilogue, const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
+                           const float* bias, const float* resid, void* out, int M, int N, int K, cudaStream_t stream) {
+  using C = RowsCfg<NT>;
+  static_assert(C::SMEM <= 48 * 1024, "no opt-in for more shared memory");
+  static_assert(AHEAD % 2 == 0, "the tokens' buffers alternate with the rounds");
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cluster_config(cfg, attr, dim3(N / kRowsChannels * ksplit), 256, C::SMEM, ksplit, stream);
+  return cudaLaunchKernelEx(&cfg, i8_rows_kernel<NT, AHEAD, CTAS>, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, ksplit, epilogue);
+}
+
 template <int NT>
 cudaError_t launch_rows(int epilogue, const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale, const float* bias,
                         const float* resid, void* out, int M, int N, int K, int sms, cudaStream_t stream) {
-  using C = RowsCfg<NT>;
-  static_assert(C::SMEM <= 48 * 1024, "no opt-in for more shared memory");
   const int tiles = N / kRowsChannels;
   const int ksplit = pick_ksplit(tiles, K / 64, kRowsK / 64, sms);
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  cluster_config(cfg, attr, dim3(tiles * ksplit), 256, C::SMEM, ksplit, stream);
-  return cudaLaunchKernelEx(&cfg, i8_rows_kernel<NT>, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, ksplit, epilogue);
+  // More CTAs than two an SM: three are resident, and cover each other's latency. Else the loads under way have to: two
+  // rounds, or four for up to 8 tokens (16 leave no registers) and rows of so many rounds. Measured (us, 1 and 16
+  // tokens; three CTAs / two rounds / four): 51968 x 1280 15.6 17.8 23.8 and 22.2 27.4 27.9; 5120 x 5120 14.3 13.5 12.8
+  // and 16.7 14.0 15.0; 5120 x 1280 4.5 4.1 3.7 and 5.6 4.7 4.8; 1536 x 384 2.07 2.07 2.23 and 2.6 2.75 2.7.
+  if (tiles * ksplit > 2 * sms)
+    return launch_rows_as<NT, 2, 3>(ksplit, epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, stream);
+  if constexpr (NT == 1)
+    if (K / ksplit >= 4 * kRowsK)
+      return launch_rows_as<NT, 4, 2>(ksplit, epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, stream);
+  return launch_rows_as<NT, 2, 2>(ksplit, epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, stream);
 }
 
 }  // namespace
