@@ -15,8 +15,10 @@
 //    behind the last key are zeroed in shared memory before the product (0 x NaN would not be 0);
 //  - every item writes partial results (m, l, O), which prefix_join_kernel joins with those of the
 //    sequences' own keys.
-// P is rounded to bf16 (2^-8) before the second product, as in attn.cu: a second part of P would cost
-// half as much tensor time again and does not fit TMEM beside S and O.
+// P enters the second product as two bf16 numbers (it is off by 2^-16 then), as in the one-launch form, so that a
+// row's result does not depend on how many others share its prefix. The large part is the A operand in TMEM, as in
+// attn.cu; the small one, for which TMEM has no columns left beside S and O, is one in shared memory. With the large
+// part alone the error of long prompts was 1.4 times that of rounding the output.
 // What bounds it: the exponentials (256 x 128 of them a key tile are 1.1 us of an SM) and the tensor pipe together, as
 // in attn.cu, and at this length the ends of a CTA's work: 1280 rows of each of 4 key heads over 8191 keys, 10.7 GFLOP,
 // take 21 us (510 TFLOP/s; 144 CTAs of 11 key tiles, of which 14 us are the tiles at attn.cu's rate). On mma.sync, with
@@ -41,6 +43,9 @@ __device__ __forceinline__ void named_arrive(int id, int count) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
+__device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                              uint32_t accumulate) {
   asm volatile(
@@ -61,8 +66,8 @@ constexpr int kThreads = 384;             // producer, 3 MMA issuers, 2 softmax 
 // (producer and MMA issuers) gives up registers that the two softmax warpgroups take, which keeps
 // a row's 128 scores and the exponential pipeline out of local memory. The sum must fit in what
 // the CTA is launched with (checked on the host before the first launch).
-constexpr int kCtrlRegs = 104;
-constexpr int kSoftmaxRegs = 200;
+constexpr int kCtrlRegs = 72;
+constexpr int kSoftmaxRegs = 216;
 constexpr int kRegsNeeded = kCtrlRegs * 128 + kSoftmaxRegs * 256;
 static_assert(kRegsNeeded <= (65536 / kThreads) / 8 * 8 * kThreads, "register split exceeds the launch budget");
 
@@ -71,12 +76,15 @@ constexpr uint32_t KV_BYTES = BKV * HD * 2;         // 16 KB per K or V tile
 constexpr uint32_t OFF_Q = 0;                       // two buffers of (Q_A, Q_B): this item's and the next's
 constexpr uint32_t OFF_K = OFF_Q + 4 * Q_BYTES;
 constexpr uint32_t OFF_V = OFF_K + NK * KV_BYTES;
-constexpr uint32_t OFF_BARS = OFF_V + NV * KV_BYTES;
+constexpr uint32_t P_BYTES = BQ * BKV * 2;          // 32 KB: the small part of a tile's P, two blocks of 64 keys
+constexpr uint32_t OFF_P = OFF_V + NV * KV_BYTES;
+constexpr uint32_t OFF_BARS = OFF_P + 2 * P_BYTES;
 // bars: q_full[2], q_empty[2], k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], and per query
 // tile t: s_full[t], s_free[t], p_full[t], pv_done[t]; drain. (The exponential turn uses the
 // hardware named barriers 1 and 2.)
 constexpr int NUM_BARS = 4 + 2 * NK + 2 * NV + 8 + 1;
 constexpr size_t SMEM = 1024 + OFF_BARS + NUM_BARS * 8 + 16;
+static_assert(SMEM <= 232448, "shared memory of the bf16 prefix kernel");
 constexpr uint32_t TMEM_COLS = 512;  // S_A 0..127, S_B 128..255, O_A 256..319, O_B 320..383, P_A 384..447, P_B 448..511
 // Grow the running maximum only when a tile's maximum exceeds it by more than this (log2
 // units); otherwise keep it, so p <= 2^8 and O is rescaled rarely. The result is unchanged:
@@ -89,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t s0 = smem_u32(smem);
-  const uint32_t sQ = s0 + OFF_Q, sK = s0 + OFF_K, sV = s0 + OFF_V;
+  const uint32_t sQ = s0 + OFF_Q, sK = s0 + OFF_K, sV = s0 + OFF_V, sP = s0 + OFF_P;
   const uint32_t bar0 = s0 + OFF_BARS;
   auto q_full = [&](int u) { return bar0 + 8u * u; };
   auto q_empty = [&](int u) { return bar0 + 8u * (2 + u); };
@@ -286,9 +294,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (lane == 0) {
               const uint64_t vdesc = sdesc_sw128(sV + st * KV_BYTES, 1024, 1024);
+              const uint64_t pdesc = sdesc_sw128(sP + t * P_BYTES, 16, 1024);
 #pragma unroll
-              for (int k = 0; k < BKV / 16; ++k)
-                umma_bf16_ts(tO(t), tP(t) + 8 * k, vdesc + k * 128, idesc_o, (j > 0 || k > 0) ? 1u : 0u);
+              for (int k = 0; k < BKV / 16; ++k)  // (64 keys a block of 128-byte rows)
+                umma_bf16_ss(tO(t), pdesc + (k >> 2) * (P_BYTES / 2 >> 4) + (k & 3) * 2, vdesc + k * 128, idesc_o,
+                             (j > 0 || k > 0) ? 1u : 0u);
+#pragma unroll
+              for (int k = 0; k < BKV / 16; ++k) umma_bf16_ts(tO(t), tP(t) + 8 * k, vdesc + k * 128, idesc_o, 1u);
               umma_commit(pv_done(t));
               umma_commit(v_empty(st));
             }
@@ -378,19 +390,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t == 1 || g > 0) named_sync(1 + t, 256);
 
         // p = 2^(s * scale_log2 - m_new): packed fp32x2 FMA for the argument, packed adds for the
-        // row sum; P is packed to bf16 pairs before waiting on the previous PV product.
+        // row sum; P is cut into its two bf16 parts before waiting on the previous PV product.
         const uint64_t c2 = pack_f32x2(scale_log2, scale_log2);
         const uint64_t nm2 = pack_f32x2(-ref, -ref);
         uint64_t sum2a = pack_f32x2(0.0f, 0.0f), sum2b = sum2a;
-        uint32_t pk[64];
+        const uint64_t minus1 = pack_f32x2(-1.0f, -1.0f);
+        uint32_t pk[64], pl[64];
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
           float a0, a1;
           unpack_f32x2(fma_f32x2(pack_f32x2(sv[2 * i], sv[2 * i + 1]), c2, nm2), a0, a1);
           const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
-          if (i & 1) sum2b = add_f32x2(sum2b, pack_f32x2(p0, p1));
-          else sum2a = add_f32x2(sum2a, pack_f32x2(p0, p1));
+          const uint64_t pp = pack_f32x2(p0, p1);
+          if (i & 1) sum2b = add_f32x2(sum2b, pp);
+          else sum2a = add_f32x2(sum2a, pp);
           pk[i] = pack_bf16x2(p0, p1);
+          float l0, l1;  // what the large part leaves (exact)
+          unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(pk[i] << 16), __uint_as_float(pk[i] & 0xffff0000u)), minus1, pp), l0, l1);
+          pl[i] = pack_bf16x2(l0, l1);
         }
         float sa0, sa1, sb0, sb1;
         unpack_f32x2(sum2a, sa0, sa1);
@@ -418,8 +435,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
 
-        // P row (128 keys as 64 bf16 pairs) into the tile's P columns of TMEM.
+        // P row (128 keys as 64 bf16 pairs): the large part into the tile's P columns of TMEM, the small one into
+        // its swizzled rows of shared memory (16 bytes are 8 keys).
         {
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            sts_v4(sP + t * P_BYTES + (c >> 3) * (P_BYTES / 2) + row * 128u + (((c & 7) ^ (row & 7)) << 4), pl[4 * c], pl[4 * c + 1],
+                   pl[4 * c + 2], pl[4 * c + 3]);
+          fence_proxy_async_smem();
           uint32_t p0[32], p1[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
