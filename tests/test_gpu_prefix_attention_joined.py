@@ -34,3 +34,63 @@ def test_probabilities_keep_two_parts_with_many_rows(H, Hkv, q_len, sizes, pre):
     c = Case("bf16", sizes, q_len, H, Hkv, pre, None, uneven=len(sizes) > 1, seed=H + q_len, prefix_max=max(pre) + 37)
     assert _joins(c)
     _check_two_parts(c, c.run())
+
+
+@pytest.mark.parametrize("dtype,H,Hkv,n,T", [("bf16", 32, 32, 160, 300), ("f32", 32, 32, 245, 100), ("bf16", 130, 1, 300, 300)])
+def test_append_and_joined_attention_back_to_back(dtype, H, Hkv, n, T):
+    """Steps of an append and the joined form in one stream, nothing waiting between them, with new keys, lengths,
+    tables and queries in the same buffers each time: the same bits as with a synchronisation after every call, eager
+    and captured. (The own keys' kernel reads what the append two launches before it wrote.)"""
+    import torch
+    from transformer_encoder_gb300 import kv_append, prefix_attention, sync_status
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device="cuda").manual_seed(n)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dt)
+    PAGE, WIDTH, STEPS = 8, 4, 6
+    kp, vp = rnd(1, T, Hkv, 64), rnd(1, T, Hkv, 64)
+    feeds = [dict(q=rnd(n, 1, H, 64), k=rnd(9 * n, Hkv, 64), v=rnd(9 * n, Hkv, 64),
+                  lens=torch.randint(9, PAGE * WIDTH + 1, (n,), generator=g, device="cuda", dtype=torch.int32),
+                  table=torch.randperm(n * WIDTH, generator=g, device="cuda").to(torch.int32).view(n, WIDTH))
+             for _ in range(STEPS)]
+    live = {k: torch.zeros_like(t) for k, t in feeds[0].items()}
+    pages = torch.zeros(2, n * WIDTH, PAGE, Hkv, 64, dtype=dt, device="cuda")
+
+    def append_and_attend():  # nine new tokens a sequence, then the newest of them attends
+        kv_append(live["k"], live["v"], pages[0], pages[1], live["table"], live["lens"])
+        return prefix_attention(live["q"], kp, vp, k_pages=pages[0], v_pages=pages[1], block_table=live["table"],
+                                lens=live["lens"])
+
+    def steps(once, wait):
+        pages.zero_()
+        outs = []
+        for f in feeds:
+            for k, t in f.items():
+                live[k].copy_(t)
+            if wait:
+                torch.cuda.synchronize()
+            outs.append(once().clone())
+            if wait:
+                torch.cuda.synchronize()
+        sync_status()
+        return outs
+
+    def apart():
+        kv_append(live["k"], live["v"], pages[0], pages[1], live["table"], live["lens"])
+        torch.cuda.synchronize()
+        return prefix_attention(live["q"], kp, vp, k_pages=pages[0], v_pages=pages[1], block_table=live["table"],
+                                lens=live["lens"])
+
+    want = steps(apart, True)
+    assert not torch.equal(want[0], want[1])
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(steps(append_and_attend, False), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = append_and_attend()
+
+    def replay():
+        graph.replay()
+        return out
+
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(steps(replay, False), want))

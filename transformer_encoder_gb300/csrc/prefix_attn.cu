@@ -798,8 +798,8 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
   using C = Cfg<T, NR>;
   extern __shared__ __align__(128) uint8_t smem_dyn[];
   __shared__ SegTable seg;
+  pdl_trigger();
   pdl_wait();
-  pdl_trigger();  // (after the wait: the own keys' kernel starts without waiting for this one to end)
   int b = blockIdx.x;
   Item it;
   const int row0 = (b % p.row_tiles) * C::ROWS;
@@ -837,15 +837,15 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
 // Second form, own keys: one warp per (sequence, key head, row tile, split); its rows go through the
 // warp's stretch of shared memory to full lines of the partial results.
 template <typename T, int NR>
-__global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_own_kernel(const PrefixParams p, long long n_items, bool beside,
+__global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_own_kernel(const PrefixParams p, long long n_items,
                                                                                        uint32_t* err) {
   using C = Cfg<T, NR>;
   static_assert(C::STAGES * 2 * C::HALF >= 8 * C::OS * 4, "a warp's ring holds eight rows of results");
   extern __shared__ __align__(128) uint8_t smem_dyn[];
   pdl_trigger();
-  // beside: the kernel before this one is the prefix's, which let this one start once everything before it was
-  // complete; nothing of its is read here, so it is waited for at the end only (for the join after both)
-  if (!beside) pdl_wait();
+  // Before the first read, although nothing of the prefix's kernel is read here: only a wait of this grid's own makes
+  // the writes of the calls before (new keys, lengths, tables) visible to it.
+  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
   long long b = static_cast<long long>(blockIdx.x) * C::NW + warp;
   if (b >= n_items) return;
@@ -859,11 +859,8 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
   it.n_own = 1;
   it.row_off = row0;
   it.n_rows = min(p.q_len * p.r - row0, C::ROWS);
-  if (p.np && p.group_start && it.seq0 >= p.group_start[p.n_groups]) {
-    // a sequence behind the last group (padding): its length and pages may hold anything, its rows stay as they were
-    if (beside) pdl_wait();
-    return;
-  }
+  // a sequence behind the last group (padding): its length and pages may hold anything, its rows stay as they were
+  if (p.np && p.group_start && it.seq0 >= p.group_start[p.n_groups]) return;
   const int len = own_len_of(p, it.seq0, err);
   int step0, n_steps;
   run_of((len + 15) / 16, split, p.ns, step0, n_steps);
@@ -896,7 +893,6 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
       }
     }
   }
-  if (beside) pdl_wait();
 }
 
 // Join of the partial results of one (token, head): sixteen lanes, four elements each.
@@ -1182,7 +1178,7 @@ cudaError_t launch_part(PrefixParams p, int row_tiles, long long blocks, uint32_
 }
 
 template <typename T, int NR>
-cudaError_t launch_own(PrefixParams p, int row_tiles, long long items, bool beside, uint32_t* err, cudaStream_t stream) {
+cudaError_t launch_own(PrefixParams p, int row_tiles, long long items, uint32_t* err, cudaStream_t stream) {
   using C = Cfg<T, NR>;
   auto kern = prefix_own_kernel<T, NR>;
   static std::atomic<int> configured{-1};
@@ -1190,7 +1186,7 @@ cudaError_t launch_own(PrefixParams p, int row_tiles, long long items, bool besi
   if (e != cudaSuccess) return e;
   p.row_tiles = row_tiles;
   return wenc_host::launch_pdl(kern, dim3(static_cast<unsigned>((items + C::NW - 1) / C::NW)), dim3(C::THREADS),
-                               C::RING + C::P_BYTES, stream, p, items, beside, err);
+                               C::RING + C::P_BYTES, stream, p, items, err);
 }
 
 // The prefix part on tcgen05.
@@ -1281,9 +1277,7 @@ cudaError_t launch_all(PrefixParams p, const Plan& pl, uint32_t* err, cudaStream
   cudaError_t e = cudaSuccess;
   if (pl.items_p > 0 && !pl.tc) e = launch_part<T, 2>(p, pl.rows_p, pl.items_p, err, stream);
   if (e == cudaSuccess && pl.items_s > 0) {
-    const bool beside = pl.items_p > 0;
-    e = pl.nr_s == 1 ? launch_own<T, 1>(p, pl.rows_s, pl.items_s, beside, err, stream)
-                     : launch_own<T, 2>(p, pl.rows_s, pl.items_s, beside, err, stream);
+    e = pl.nr_s == 1 ? launch_own<T, 1>(p, pl.rows_s, pl.items_s, err, stream) : launch_own<T, 2>(p, pl.rows_s, pl.items_s, err, stream);
   }
   if (e != cudaSuccess) return e;
   const long long threads = static_cast<long long>(p.n_seqs) * p.q_len * p.H * 16;

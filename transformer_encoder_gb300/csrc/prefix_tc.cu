@@ -187,9 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  pdl_wait();  // queries, prefix and lengths from the previous kernels are complete from here on
-  // Only now may the next kernel start: the own keys' kernel does so without waiting for this one to end (TMEM is held)
-  pdl_trigger();
+  pdl_trigger();  // TMEM is held: the next kernel may be scheduled
+  pdl_wait();     // queries, prefix and lengths from the previous kernels are complete from here on
   auto tS = [&](int t) { return tmem_base + 128u * t; };
   auto tO = [&](int t) { return tmem_base + 256u + 64u * t; };
   auto tP = [&](int t) { return tmem_base + 384u + 64u * t; };  // P as bf16 pairs: 64 columns per tile

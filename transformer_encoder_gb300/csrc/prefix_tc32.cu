@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc32_kernel(const wenc_hos
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_trigger();  // TMEM is held: the next kernel may be scheduled
   pdl_wait();
-  pdl_trigger();  // (after the wait: the own keys' kernel starts without waiting for this one to end)
   auto tS = [&](int b) { return tmem + 64u * b; };
   auto tO = [&](int b) { return tmem + 128u + 64u * b; };
   auto tP = [&](int b, int part) { return tmem + 256u + 96u * b + 32u * part; };
