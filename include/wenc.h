@@ -375,9 +375,11 @@ typedef struct {
  *   out = softmax(scale * q [K_prefix; K_own]^T) [V_prefix; V_own],
  * and zeros where it sees no key. The prefix is read once for all of a group's queries. Keys behind
  * a length are never read as numbers (they may hold anything). Scores, statistics and accumulators
- * are fp32; float32 products are formed from three TF32 products each, or for many rows from six
- * bf16 products, so that an infinite key or value that is seen may turn its rows to NaN. Sequences
- * outside every group's range keep their rows of `out` as they were.
+ * are fp32; bf16 probabilities enter the product with V as two bf16 numbers (2^-16), float32 products are
+ * formed from three TF32 products each, or for many rows from six bf16 products. A NaN or an infinity
+ * that a row does not see never reaches it; what it does see it takes as a plain evaluation would, except
+ * that in calls with a workspace an infinite prefix value (float32: key, value or query) may turn the elements it
+ * reaches to NaN. Sequences outside every group's range keep their rows of `out` as they were.
  * A length, offset or page number out of range records WENC_ERR_INVALID_ARG in the device error
  * word (wenc_sync_status(NULL)); nothing out of range is accessed and the output rows it concerns are
  * undefined. The workspace belongs to the call until its work is done: calls that may overlap need

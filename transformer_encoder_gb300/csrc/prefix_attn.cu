@@ -240,6 +240,142 @@ struct RowState {
   float o[NR][4][4], m[NR][2], l[NR][2];  // m in log2 units; l of this thread's keys alone until reduced
 };
 
+// One 16-byte piece of a key or query row as fp32.
+__device__ __forceinline__ void unpack_piece(const uint4& u, float (&f)[4]) {
+  f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
+  f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ void unpack_piece(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// The products with V are formed for all of a tile's rows, with weights of 0 where a row does not see a key, and in
+// two parts; but 0 x inf and 0 x NaN are NaN, so a value that is no number would reach rows that do not see it. And the
+// TF32 part of a float32 next to the largest one is infinite. Such elements of O, and rows whose sum is no number
+// (rare: attend() finds them by that), are formed again here in plain fp32, from the keys each row sees alone. A key at a
+// time: a lane a row for the scores, then every lane its own elements. (A function of its own:
+// looking for them costs a call up to 0.4 us, 1.0 in the joined form; inlined, the calls took 0.3 to 0.5 us more.)
+template <typename T, int NR, bool SOLO>
+__device__ __noinline__ void redo_non_numbers(const PrefixParams& p, const Item& it, const SegTable* seg, int solo_len, int step0,
+                                              int n_mine, RowState<NR>& st) {
+  using C = Cfg<T, NR>;
+  constexpr int E = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+  uint32_t bad = 0u;  // bit 16 r + 4 i + e: o[r][i][e]
+  bool rows = false;  // some row's sum is no number
+#pragma unroll
+  for (int r = 0; r < NR; ++r)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool row = !(fabsf(st.l[r][e & 1]) < CUDART_INF_F), in = 8 * r + 2 * tq + (e & 1) < it.n_rows;
+      rows |= row && in;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (in && (row || !(fabsf(st.o[r][i][e]) < CUDART_INF_F))) {
+          bad |= 1u << (16 * r + 4 * i + e);
+          st.o[r][i][e] = 0.0f;
+        }
+    }
+  rows = __any_sync(0xffffffffu, rows);
+  // this lane's row: its queries, sequence, token, maximum and sum
+  const int x = it.row_off + lane, tok = x / p.r, per_seq = p.q_len * p.r, row_seq = x / per_seq, row_tok = (x - row_seq * per_seq) / p.r;
+  const uint8_t* q = p.q + (static_cast<long long>(it.seq0) * p.q_len + tok) * p.q_stride + (it.hk * p.r + x - tok * p.r) * C::ROWB;
+  float m = -CUDART_INF_F, l = 0.0f;
+#pragma unroll
+  for (int r = 0; r < NR; ++r)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {  // row 8 r + y sits in the lanes of column pair y / 2, element y % 2
+      const float y = __shfl_sync(0xffffffffu, st.m[r][e], (lane & 7) >> 1), z = __shfl_sync(0xffffffffu, st.l[r][e], (lane & 7) >> 1);
+      if ((lane >> 3) == r && (lane & 1) == e) {
+        m = y;
+        l = z;
+      }
+    }
+  const bool again = !(fabsf(l) < CUDART_INF_F);
+  if (again) {
+    m = -CUDART_INF_F;
+    l = 0.0f;
+  }
+  // every key of the run: f(its value row, whether this lane's row sees it, that row's score in log2 units)
+  auto each_key = [&](auto&& f) {
+    int sg = SOLO ? 1 : 0;
+#pragma unroll 1
+    for (int t = step0; t < step0 + n_mine; ++t) {
+      int begin = 0, n_keys = solo_len;
+      if constexpr (!SOLO) {
+        while (t >= seg->step0[sg + 1]) ++sg;
+        begin = seg->step0[sg];
+        n_keys = seg->len[sg];
+      }
+      const int last = min(n_keys, (t - begin + 1) * C::KW);
+#pragma unroll 1
+      for (int key = (t - begin) * C::KW; key < last; ++key) {
+        const uint8_t *k, *v;
+        if (sg == 0) {
+          k = it.kp + key * p.k_token;
+          v = it.vp + key * p.v_token;
+        } else {
+          const int pi = key / p.page_size, page = p.table[(it.seq0 + sg - 1) * p.table_stride + pi];
+          if (page < 0 || page >= p.n_pages) continue;  // (reported when its step was loaded)
+          const uint64_t at = static_cast<uint64_t>(key - pi * p.page_size) * p.row16 + it.hk * (C::ROWB / 16);
+          k = p.k_pages + ((static_cast<uint64_t>(page) * p.k_page16 + at) << 4);
+          v = p.v_pages + ((static_cast<uint64_t>(page) * p.v_page16 + at) << 4);
+        }
+        const bool sees = lane < it.n_rows && (sg == 0 || (row_seq == sg - 1 && key < n_keys - p.q_len + 1 + row_tok));
+        float dot = 0.0f;
+        if (sees) {
+#pragma unroll 1
+          for (int c = 0; c < C::ROWB / 16; ++c) {
+            uint4 qc = *reinterpret_cast<const uint4*>(q + 16 * c);
+            qc = make_uint4((qc.x & p.q_keep) ^ p.q_flip, (qc.y & p.q_keep) ^ p.q_flip, (qc.z & p.q_keep) ^ p.q_flip, (qc.w & p.q_keep) ^ p.q_flip);
+            float a[E], b[E];
+            unpack_piece(qc, a);
+            unpack_piece(*reinterpret_cast<const uint4*>(k + 16 * c), b);
+#pragma unroll
+            for (int e = 0; e < E; ++e) dot = fmaf(a[e], b[e], dot);
+          }
+        }
+        f(v, sees, dot * p.scale_log2);
+      }
+    }
+  };
+  if (rows)
+    each_key([&](const uint8_t*, bool sees, float s) {
+      if (sees && again) m = fmaxf(m, s);
+    });
+  const float u = m == -CUDART_INF_F ? 0.0f : m;
+  each_key([&](const uint8_t* v, bool sees, float s) {
+    const float w = sees ? ex2_approx(s - u) : -1.0f;  // -1: not seen
+    if (sees && again) l += w;
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float y = __shfl_sync(0xffffffffu, w, 8 * r + 2 * tq + e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (((bad >> (16 * r + 4 * i + e + 2 * h)) & 1u) && !(y < 0.0f)) {
+              const T z = reinterpret_cast<const T*>(v)[C::F32 ? 32 * h + 4 * g + i : 16 * i + 8 * h + g];
+              st.o[r][i][e + 2 * h] += y * static_cast<float>(z);
+            }
+      }
+  });
+#pragma unroll
+  for (int r = 0; r < NR; ++r)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      st.m[r][e] = __shfl_sync(0xffffffffu, m, 8 * r + 2 * tq + e);
+      st.l[r][e] = __shfl_sync(0xffffffffu, l, 8 * r + 2 * tq + e);
+    }
+}
+
 // One warp's run of steps [step0, step0 + n_mine). SOLO: the item is one own-key segment of solo_len keys
 // (no table); else the segments are in `seg`.
 template <typename T, int NR, bool SOLO>
@@ -585,6 +721,21 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
       l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], 8);
       l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], 16);
     }
+  float zero[2] = {0.0f, 0.0f};  // 0 unless some sum or element is no number
+#pragma unroll
+  for (int r = 0; r < NR; ++r)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      zero[e] = fmaf(l[r][e], 0.0f, zero[e]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) zero[e] = fmaf(o[r][i][e + 2], 0.0f, fmaf(o[r][i][e], 0.0f, zero[e]));
+    }
+  if (__any_sync(0xffffffffu, !(zero[0] + zero[1] == 0.0f))) {
+    RowState<NR> copy = st;  // (so that st stays in registers)
+    const Item item = it;
+    redo_non_numbers<T, NR, SOLO>(p, item, seg, solo_len, step0, n_mine, copy);
+    st = copy;
+  }
 }
 
 // All warps' results into shared memory, over the rings; begins and ends with a barrier.
@@ -699,7 +850,7 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t a) {
 
 // One-launch form: a cluster of p.cluster CTAs attends one (group, key head, tile of rows).
 template <typename T, int NR>
-__global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_cluster_kernel(const PrefixParams p, uint32_t* err) {
+__global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_cluster_kernel(const __grid_constant__ PrefixParams p, uint32_t* err) {
   using C = Cfg<T, NR>;
   extern __shared__ __align__(128) uint8_t smem_dyn[];
   __shared__ SegTable seg;
@@ -794,7 +945,7 @@ __device__ __forceinline__ void write_partial(const PrefixParams& p, int token, 
 
 // Second form, the prefix: one CTA per (group, key head, split, row tile); writes its rows' partial results.
 template <typename T, int NR>
-__global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_part_kernel(const PrefixParams p, uint32_t* err) {
+__global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_part_kernel(const __grid_constant__ PrefixParams p, uint32_t* err) {
   using C = Cfg<T, NR>;
   extern __shared__ __align__(128) uint8_t smem_dyn[];
   __shared__ SegTable seg;
@@ -837,7 +988,7 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
 // Second form, own keys: one warp per (sequence, key head, row tile, split); its rows go through the
 // warp's stretch of shared memory to full lines of the partial results.
 template <typename T, int NR>
-__global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_own_kernel(const PrefixParams p, long long n_items,
+__global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_own_kernel(const __grid_constant__ PrefixParams p, long long n_items,
                                                                                        uint32_t* err) {
   using C = Cfg<T, NR>;
   static_assert(C::STAGES * 2 * C::HALF >= 8 * C::OS * 4, "a warp's ring holds eight rows of results");
