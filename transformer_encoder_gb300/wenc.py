@@ -4,6 +4,10 @@ Every step of the encoder runs in the library's CUDA kernels; this module only t
 PyTorch tensors (used here for device memory and streams) into the pointers and sizes
 of the C ABI declared in include/wenc.h, and turns non-OK statuses into exceptions.
 There is no fallback: if the library is missing or the device is not sm_103a, calls raise.
+
+A call with ``stream=`` (a torch stream or a raw handle) runs there, and tensors that it makes come from that
+stream's allocator: a caller that uses them on another stream orders the two streams and, before the tensor
+is dropped, calls its ``record_stream``, as for any tensor made on another stream.
 """
 from __future__ import annotations
 
@@ -186,6 +190,23 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _on(stream):
+    """The given stream (a torch stream or a raw handle) as torch's current one."""
+    import torch
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
+        stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)))
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor (an output, a workspace) from the allocator of the stream the call runs on: its block was
+    last used, and will be used again, in that stream's order, and is a graph's own while one is captured."""
+    torch = _torch or _load_torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _require(t, dtype, name):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -254,7 +275,7 @@ class Encoder:
         if count is None:
             count = self.n_layers - first
         if out is None:
-            out = torch.empty_like(x)
+            out = _empty(x.shape, x.dtype, x.device, stream)
         _require(out, torch.float32, "out")
         B = x.shape[0]
         _check(lib().wenc_forward_layers(self._h, _ptr(x), _ptr(out), B, first, count, int(final_ln), _stream(stream)))
@@ -279,7 +300,7 @@ class Encoder:
         import torch
         _require(mel, torch.float32, "mel")
         if out is None:
-            out = torch.empty((mel.shape[0], self.seq_len, self.d_model), dtype=torch.float32, device=mel.device)
+            out = _empty((mel.shape[0], self.seq_len, self.d_model), torch.float32, mel.device, stream)
         _require(out, torch.float32, "out")
         _check(lib().wenc_stem(self._h, _ptr(mel), _ptr(out), mel.shape[0], _stream(stream)))
         return out
@@ -289,7 +310,7 @@ class Encoder:
         import torch
         _require(mel, torch.float32, "mel")
         if out is None:
-            out = torch.empty((mel.shape[0], self.seq_len, self.d_model), dtype=torch.float32, device=mel.device)
+            out = _empty((mel.shape[0], self.seq_len, self.d_model), torch.float32, mel.device, stream)
         _require(out, torch.float32, "out")
         _check(lib().wenc_encode(self._h, _ptr(mel), _ptr(out), mel.shape[0], _stream(stream)))
         return out
@@ -319,7 +340,7 @@ class Encoder:
         if self.n_dec == 0:  # the library reports the missing weights
             _check(lib().wenc_cross_kv(self._h, _ptr(enc_out), None, B, _stream(stream)))
         if out is None:
-            out = torch.empty((2 * self.n_dec, B * self.seq_len, self.d_model), dtype=dt, device=enc_out.device)
+            out = _empty((2 * self.n_dec, B * self.seq_len, self.d_model), dt, enc_out.device, stream)
         _require(out, dt, "out")
         _check(lib().wenc_cross_kv(self._h, _ptr(enc_out), _ptr(out), B, _stream(stream)))
         return out
@@ -362,7 +383,7 @@ def attention(q, k, v, out=None, stream=None):
         _require(t, torch.bfloat16, n)
     B, T, H, hd = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _require(out, torch.bfloat16, "out")
     _check(lib().wenc_attention(_ptr(q), _ptr(k), _ptr(v), _ptr(out), B, T, H, hd, _stream(stream)))
     return out
@@ -380,7 +401,7 @@ def layernorm(x, w, b, eps: float = 1e-5, out_bf16: bool = True, out=None, strea
     d = x.shape[-1]
     rows = x.numel() // d
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.bfloat16 if fmt == LN_OUT_BF16 else torch.float32, device=x.device)
+        out = _empty(x.shape, torch.bfloat16 if fmt == LN_OUT_BF16 else torch.float32, x.device, stream)
     _check(lib().wenc_layernorm(_ptr(x), _ptr(w), _ptr(b), _ptr(out), rows, d, eps, fmt, _stream(stream)))
     return out
 
@@ -395,7 +416,7 @@ def linear(a, w, bias, epilogue: int = EPI_BIAS_BF16, resid=None, out=None, stre
     N = w.shape[0]
     if out is None:
         dt = torch.float32 if epilogue == EPI_BIAS_RESID_F32 else torch.bfloat16
-        out = torch.empty((M, N), dtype=dt, device=a.device)
+        out = _empty((M, N), dt, a.device, stream)
     _check(lib().wenc_linear(_ptr(a), _ptr(w), _ptr(bias), _ptr(resid), _ptr(out), M, N, K, epilogue, _stream(stream)))
     return out
 
@@ -412,7 +433,7 @@ def linear_tf32(a, w, bias, epilogue: int = EPI_BIAS_BF16, resid=None, out=None,
     M, K = a.shape
     N = w.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=a.device)
+        out = _empty((M, N), torch.float32, a.device, stream)
     _require(out, torch.float32, "out")
     _check(lib().wenc_linear_tf32(_ptr(a), _ptr(w), _ptr(bias), _ptr(resid), _ptr(out), M, N, K, epilogue,
                                   _stream(stream)))
@@ -426,7 +447,7 @@ def attention_tf32(q, k, v, out=None, stream=None):
         _require(t, torch.float32, n)
     B, T, H, hd = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _require(out, torch.float32, "out")
     _check(lib().wenc_attention_tf32(_ptr(q), _ptr(k), _ptr(v), _ptr(out), B, T, H, hd, _stream(stream)))
     return out
@@ -534,21 +555,6 @@ def _dtype_error(t, name):
     return TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
 
-def _on(stream):
-    """The given stream (a torch stream or a raw handle) as torch's current one."""
-    return _torch.cuda.stream(stream if isinstance(stream, _torch.cuda.Stream) else _torch.cuda.ExternalStream(
-        stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)))
-
-
-def _scratch(nbytes, like, stream):
-    """Workspace from the allocator of the stream the call runs on (so that it is reused in that
-    stream's order, and is a graph's own while it is being captured)."""
-    if stream is None:
-        return _torch.empty(nbytes, dtype=_torch.uint8, device=like.device)
-    with _on(stream):
-        return _torch.empty(nbytes, dtype=_torch.uint8, device=like.device)
-
-
 def prefix_attention(q, k_prefix=None, v_prefix=None, *, prefix_lens=None, group_start=None, max_group=None,
                      k_pages=None, v_pages=None, block_table=None, lens=None, scale: float = 0.125, out=None,
                      workspace=None, stream=None):
@@ -581,7 +587,7 @@ def prefix_attention(q, k_prefix=None, v_prefix=None, *, prefix_lens=None, group
     if dev < 0 or dev != torch._C._cuda_getDevice():
         raise _elsewhere((("q", q),))
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
+        out = _empty(shape, dtype, q.device, stream)
         out_stride = H * hd
     else:
         if out.dtype is not dtype or out.shape != shape:
@@ -652,7 +658,7 @@ def prefix_attention(q, k_prefix=None, v_prefix=None, *, prefix_lens=None, group
     if workspace is not None or (S or 1) * t * H > 64 * kv:
         if workspace is None:
             need = _lib.wenc_prefix_attention_workspace(_PREFIX_PACK.pack(*args, 0, 0))
-            workspace = _scratch(need, q, stream) if need else None
+            workspace = _empty(need, torch.uint8, q.device, stream) if need else None
         elif workspace.get_device() != dev:
             raise _elsewhere((("workspace", workspace),))
         if workspace is not None:
@@ -696,7 +702,7 @@ def kv_append(k, v, k_pages, v_pages, block_table, lens, *, seq_start=None, q=No
         if len(qshape) != 3 or qshape[0] != n or qshape[2] != hd:
             raise ValueError(f"q must be [{n}, heads, {hd}], got {tuple(qshape)}")
         if q_out is None:
-            q_out = torch.empty(qshape, dtype=dtype, device=q.device)
+            q_out = _empty(qshape, dtype, q.device, stream)
             if stream is None:
                 q_out.zero_()
             else:
@@ -773,11 +779,11 @@ def quantize_rows(x, out=None, scale=None, stream=None):
     rows = shape[:-1]
     d = shape[-1]
     if out is None:
-        out = torch.empty(shape, dtype=torch.int8, device=x.device)
+        out = _empty(shape, torch.int8, x.device, stream)
     elif out.dtype is not torch.int8 or out.shape != shape or not out.is_contiguous():
         raise ValueError(f"out must be contiguous int8 {tuple(shape)}, got {out.dtype} {tuple(out.shape)}")
     if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+        scale = _empty(rows, torch.float32, x.device, stream)
     elif scale.dtype is not torch.float32 or scale.shape != rows or not scale.is_contiguous():
         raise ValueError(f"scale must be contiguous float32 {tuple(rows)}, got {scale.dtype} {tuple(scale.shape)}")
     if out.get_device() != dev or scale.get_device() != dev:
@@ -819,7 +825,7 @@ def linear_i8(a, a_scale, w, w_scale, bias, epilogue: int = EPI_BIAS_BF16, resid
         raise _elsewhere((("a_scale", a_scale), ("w", w), ("w_scale", w_scale), ("bias", bias)))
     dt = f32 if epilogue == EPI_BIAS_RESID_F32 else torch.bfloat16
     if out is None:
-        out = torch.empty((M, N), dtype=dt, device=a.device)
+        out = _empty((M, N), dt, a.device, stream)
     elif out.dtype is not dt or out.shape != (M, N) or not out.is_contiguous():
         raise ValueError(f"out must be contiguous {dt} {(M, N)}, got {out.dtype} {tuple(out.shape)}")
     elif out.get_device() != dev:
@@ -838,7 +844,7 @@ def linear_i8(a, a_scale, w, w_scale, bias, epilogue: int = EPI_BIAS_BF16, resid
     elif M > 16:
         need = _lib.wenc_linear_i8_workspace(M, N, K)
         if need:
-            workspace = _scratch(need, a, stream)
+            workspace = _empty(need, torch.uint8, a.device, stream)
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     status = _lib.wenc_linear_i8(a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), bias.data_ptr(), rp,
@@ -858,7 +864,7 @@ def selftest_gemm_pair_abort(a, w, bias, stop_after: int, out=None, stream=None)
     M, K = a.shape
     N = w.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+        out = _empty((M, N), torch.bfloat16, a.device, stream)
     _check(lib().wenc_selftest_gemm_pair_abort(_ptr(a), _ptr(w), _ptr(bias), _ptr(out), M, N, K, int(stop_after),
                                               _stream(stream)))
     return out
@@ -872,7 +878,7 @@ def selftest_attention_abort(q, k, v, stop_after: int, out=None, stream=None):
         _require(t, torch.bfloat16, n)
     B, T, H, hd = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _check(lib().wenc_selftest_attention_abort(_ptr(q), _ptr(k), _ptr(v), _ptr(out), B, T, H, int(stop_after),
                                               _stream(stream)))
     return out
