@@ -1,0 +1,53 @@
+"""The binding of the decode-side calls without a GPU: tensors that say they are on device 0, and a library that records
+what it is called with. What the binding accepts is what reaches the library, in the layout the library expects."""
+import pytest
+
+
+class _Lib:
+    """Every function of the library: records its name and arguments and returns 0."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        return lambda *a: self.calls.append((name, a)) or 0
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    import torch
+    from transformer_encoder_gb300 import wenc
+    fake = _Lib()
+    monkeypatch.setattr(wenc, "_torch", torch)
+    monkeypatch.setattr(wenc, "_lib", fake)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    return fake
+
+
+def _cache(hd=64, heads=4, n=3):
+    import torch
+    pages = torch.zeros(6, 8, heads, hd)
+    table = torch.zeros(n, 2, dtype=torch.int32)
+    return pages, table, torch.ones(n, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("hd", [32, 128])
+def test_pages_of_another_head_width_are_refused(lib, hd):
+    """Pages [n, size, heads, 128] would give a page stride that is merely larger than it has to be."""
+    import torch
+    from transformer_encoder_gb300 import kv_append, prefix_attention
+    q, k = torch.zeros(3, 1, 4, 64), torch.zeros(3, 4, 64)
+    prefix = torch.zeros(1, 5, 4, 64)
+    pages, table, lens = _cache(hd)
+    for kw in (dict(), dict(k_prefix=prefix, v_prefix=prefix)):
+        with pytest.raises(ValueError, match="page_size, 4, 64"):
+            prefix_attention(q, **kw, k_pages=pages, v_pages=pages, block_table=table, lens=lens)
+    with pytest.raises(ValueError, match="page_size, 4, 64"):
+        kv_append(k, k, pages, pages, table, lens)
+    assert not lib.calls
+    pages = _cache()[0]
+    prefix_attention(q, prefix, prefix, k_pages=pages, v_pages=pages, block_table=table, lens=lens)
+    kv_append(k, k, pages, pages, table, lens)
+    assert [c[0] for c in lib.calls] == ["wenc_prefix_attention", "wenc_kv_append"]

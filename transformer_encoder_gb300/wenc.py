@@ -522,15 +522,15 @@ def _page_stride(t, name):
     return st[0] if n > 1 else size * heads * hd
 
 
-def _pool(k_pages, v_pages, dtype, heads):
-    """(pages, page size, stride of K pages, of V pages) of a paged cache [pages, page_size, heads, 64]."""
+def _pool(k_pages, v_pages, dtype, heads, hd):
+    """(pages, page size, stride of K pages, of V pages) of a paged cache [pages, page_size, heads, hd]."""
     shape = k_pages.shape
     if k_pages.dtype is not dtype or v_pages.dtype is not dtype:
         raise TypeError(f"k_pages and v_pages must be {dtype}, got {k_pages.dtype} and {v_pages.dtype}")
-    if len(shape) != 4 or shape[2] != heads or v_pages.shape != shape:
-        raise ValueError(f"k_pages and v_pages must be [pages, page_size, {heads}, 64], got {tuple(shape)} and "
+    if len(shape) != 4 or shape[2] != heads or shape[3] != hd or v_pages.shape != shape:
+        raise ValueError(f"k_pages and v_pages must be [pages, page_size, {heads}, {hd}], got {tuple(shape)} and "
                          f"{tuple(v_pages.shape)}")
-    n, size, _, hd = shape
+    n, size = shape[:2]
     row = size * heads * hd
     return (n, size, row if k_pages.is_contiguous() else _page_stride(k_pages, "k_pages"),
             row if v_pages.is_contiguous() else _page_stride(v_pages, "v_pages"))
@@ -640,7 +640,7 @@ def prefix_attention(q, k_prefix=None, v_prefix=None, *, prefix_lens=None, group
             raise ValueError("pages need block_table and lens")
         if k_prefix is None and k_pages.dim() == 4:
             kv = k_pages.shape[2]
-        pages, size, kps, vps = _pool(k_pages, v_pages, dtype, kv)
+        pages, size, kps, vps = _pool(k_pages, v_pages, dtype, kv, hd)
         tab_stride, max_pages = _table(block_table, n)
         if lens.dtype is not torch.int32 or lens.dim() != 1 or lens.numel() != n or not lens.is_contiguous():
             raise _bad_ints(lens, "lens", n)
@@ -721,7 +721,7 @@ def kv_append(k, v, k_pages, v_pages, block_table, lens, *, seq_start=None, q=No
     n_seqs = lens.numel()
     if lens.dtype is not i32 or lens.dim() != 1 or not lens.is_contiguous():
         raise _bad_ints(lens, "lens", n_seqs)
-    pages, size, kps, vps = _pool(k_pages, v_pages, dtype, kv)
+    pages, size, kps, vps = _pool(k_pages, v_pages, dtype, kv, hd)
     tab_stride, max_pages = _table(block_table, n_seqs)
     if (v.get_device() != dev or k_pages.get_device() != dev or v_pages.get_device() != dev
             or block_table.get_device() != dev or lens.get_device() != dev):
