@@ -51,3 +51,26 @@ def test_pages_of_another_head_width_are_refused(lib, hd):
     prefix_attention(q, prefix, prefix, k_pages=pages, v_pages=pages, block_table=table, lens=lens)
     kv_append(k, k, pages, pages, table, lens)
     assert [c[0] for c in lib.calls] == ["wenc_prefix_attention", "wenc_kv_append"]
+
+
+def test_a_workspace_of_fewer_bytes_than_elements_is_refused(lib):
+    """One byte that is expanded counts 2^30 elements; the library would write behind it."""
+    import torch
+    from transformer_encoder_gb300 import linear_i8, prefix_attention
+    from transformer_encoder_gb300.wenc import _PREFIX_PACK
+    q, prefix = torch.zeros(200, 1, 4, 64), torch.zeros(1, 5, 4, 64)
+    a, w, f = torch.zeros(64, 128, dtype=torch.int8), torch.zeros(128, 128, dtype=torch.int8), torch.zeros(128)
+    wide = torch.empty(1, dtype=torch.uint8).expand(1 << 30)
+    strided = torch.empty(4096, dtype=torch.uint8)[::2]
+    for ws in (wide, strided):
+        with pytest.raises(ValueError, match="workspace"):
+            prefix_attention(q, prefix, prefix, workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            linear_i8(a, f[:64], w, f, f, workspace=ws)
+    assert not lib.calls
+    room = torch.empty(1024, dtype=torch.float32)
+    prefix_attention(q, prefix, prefix, workspace=room)
+    linear_i8(a, f[:64], w, f, f, workspace=room)
+    (_, (packed, _)), (_, args) = lib.calls
+    assert _PREFIX_PACK.unpack(packed)[-2:] == (room.data_ptr(), 4096)
+    assert args[11:13] == (room.data_ptr(), 4096)

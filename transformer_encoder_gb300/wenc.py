@@ -551,6 +551,15 @@ def _table(t, n_seqs):
     return (t.stride(0) if n_seqs > 1 else cols), cols
 
 
+def _room(workspace, dev):
+    """(address, bytes) of a workspace tensor."""
+    if workspace.get_device() != dev:
+        raise _elsewhere((("workspace", workspace),))
+    if not workspace.is_contiguous():  # its elements may be fewer bytes than they count
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _dtype_error(t, name):
     return TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
@@ -659,10 +668,8 @@ def prefix_attention(q, k_prefix=None, v_prefix=None, *, prefix_lens=None, group
         if workspace is None:
             need = _lib.wenc_prefix_attention_workspace(_PREFIX_PACK.pack(*args, 0, 0))
             workspace = _empty(need, torch.uint8, q.device, stream) if need else None
-        elif workspace.get_device() != dev:
-            raise _elsewhere((("workspace", workspace),))
         if workspace is not None:
-            ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+            ws, ws_bytes = _room(workspace, dev)
     status = _lib.wenc_prefix_attention(_PREFIX_PACK.pack(*args, ws, ws_bytes), _raw_stream(stream, dev))
     if status:
         _check(status)
@@ -838,15 +845,12 @@ def linear_i8(a, a_scale, w, w_scale, bias, epilogue: int = EPI_BIAS_BF16, resid
             raise _elsewhere((("resid", resid),))
         rp = resid.data_ptr()
     ws = ws_bytes = 0
-    if workspace is not None:
-        if workspace.get_device() != dev:
-            raise _elsewhere((("workspace", workspace),))
-    elif M > 16:
+    if workspace is None and M > 16:
         need = _lib.wenc_linear_i8_workspace(M, N, K)
         if need:
             workspace = _empty(need, torch.uint8, a.device, stream)
     if workspace is not None:
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws, ws_bytes = _room(workspace, dev)
     status = _lib.wenc_linear_i8(a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), bias.data_ptr(), rp,
                                  out.data_ptr(), M, N, K, epilogue, ws, ws_bytes, _raw_stream(stream, dev))
     if status:
