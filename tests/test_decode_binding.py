@@ -74,3 +74,24 @@ def test_a_workspace_of_fewer_bytes_than_elements_is_refused(lib):
     (_, (packed, _)), (_, args) = lib.calls
     assert _PREFIX_PACK.unpack(packed)[-2:] == (room.data_ptr(), 4096)
     assert args[11:13] == (room.data_ptr(), 4096)
+
+
+def test_an_empty_batch_gives_an_empty_output(lib):
+    import torch
+    from transformer_encoder_gb300 import EPI_BIAS_RESID_F32, kv_append, linear_i8, prefix_attention, quantize_rows
+    pages, table, lens = _cache(n=0)
+    prefix = torch.zeros(2, 5, 4, 64)
+    for kw in (dict(k_prefix=prefix, v_prefix=prefix), dict(k_prefix=prefix[:0], v_prefix=prefix[:0]),
+               dict(k_pages=pages, v_pages=pages, block_table=table, lens=lens)):
+        assert prefix_attention(torch.zeros(0, 1, 4, 64), **kw).shape == (0, 1, 4, 64)
+    assert prefix_attention(torch.zeros(2, 0, 4, 64), prefix, prefix).shape == (2, 0, 4, 64)
+    with pytest.raises(ValueError, match="groups"):
+        prefix_attention(torch.zeros(3, 1, 4, 64), prefix, prefix)
+    q, scale = quantize_rows(torch.zeros(2, 0, 64))
+    assert q.shape == (2, 0, 64) and q.dtype is torch.int8 and scale.shape == (2, 0)
+    w, f = torch.zeros(128, 64, dtype=torch.int8), torch.zeros(128)
+    assert linear_i8(q[0], scale[0], w, f, f).shape == (0, 128)
+    assert linear_i8(q[0], scale[0], w, f, f, EPI_BIAS_RESID_F32, resid=torch.zeros(0, 128)).dtype is torch.float32
+    k = torch.zeros(0, 4, 64)
+    assert kv_append(k, k, pages, pages, table, lens, q=k).shape == (0, 4, 64)
+    assert not lib.calls

@@ -74,3 +74,27 @@ def test_values_near_the_largest_number(size):
             t.zero_()
         where.fill_(big)
         assert ((c.run() - want).abs() <= 2.0 ** -19 * big).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("H,sizes", [(2, [3, 2]), (32, [160, 90])])
+def test_a_prefix_of_no_tokens(dtype, H, sizes):
+    """As one of length zero: the own keys alone, zeros where there are none, and rows of no group as they were."""
+    import torch
+    r = np.random.default_rng(H)
+    c = Case(dtype, sizes, 2, H, H, [0, 0], [int(x) for x in r.integers(0, 20, sum(sizes) + 3)], uneven=True, extra=3, seed=33)
+    side = torch.cuda.Stream()
+    want = torch.full_like(c.tq, 7.0)
+    c.check(c.run(out=want))
+    for name in ("k_prefix", "v_prefix"):
+        c.kw[name] = c.kw[name][:, :0]
+    for kw in (dict(), dict(stream=side)):
+        for lens in (c.kw["prefix_lens"], None):
+            c.kw["prefix_lens"] = lens
+            out = torch.full_like(c.tq, 7.0)
+            side.wait_stream(torch.cuda.current_stream())
+            c.run(out=out, **kw)
+            assert torch.equal(out, want)
+        c.kw["prefix_lens"] = torch.zeros(2, dtype=torch.int32, device="cuda")
+    del c.kw["k_pages"], c.kw["v_pages"], c.kw["lens"], c.kw["block_table"]
+    assert (c.run()[:sum(sizes)] == 0).all()

@@ -577,7 +577,8 @@ def prefix_attention(q, k_prefix=None, v_prefix=None, *, prefix_lens=None, group
     ``k_pages``, ``v_pages`` [pages, page_size, Hkv, 64] with ``block_table`` int32 [n_seqs, pages]
     and ``lens`` int32 [n_seqs]: each sequence's own keys, its q_len newest tokens included.
     ``workspace``: a uint8 tensor to use instead of an allocation where one is needed; it is busy
-    until the call's work is done.
+    until the call's work is done. A batch of no sequences gives an empty output, a prefix of no tokens counts as
+    one of length zero.
     """
     torch = _torch or _load_torch()
     dtype = q.dtype
@@ -613,6 +614,14 @@ def prefix_attention(q, k_prefix=None, v_prefix=None, *, prefix_lens=None, group
             raise ValueError(f"k_prefix and v_prefix must be [groups, tokens, heads, {hd}], got {tuple(kshape)} and "
                              f"{tuple(v_prefix.shape)}")
         G, T, kv, _ = kshape
+        if T == 0:  # a prefix of no tokens: of one that is not counted
+            T = 1
+            k_prefix = v_prefix = _empty((G, 1, kv, hd), dtype, q.device, stream)
+            if stream is None:
+                prefix_lens = torch.zeros(G, dtype=torch.int32, device=q.device)
+            else:
+                with _on(stream):
+                    prefix_lens = torch.zeros(G, dtype=torch.int32, device=q.device)
         kg = vg = T * kv * hd
         kt = vt = kv * hd
         if not k_prefix.is_contiguous():
@@ -630,6 +639,8 @@ def prefix_attention(q, k_prefix=None, v_prefix=None, *, prefix_lens=None, group
                 raise _elsewhere((("group_start", group_start),))
             g_start = group_start.data_ptr()
             S = n if max_group is None else min(max_group, n)
+        elif n == 0:
+            S = 0
         elif G == 0 or n % G != 0:
             raise ValueError(f"{n} sequences are no multiple of {G} groups (pass group_start)")
         else:
@@ -659,6 +670,8 @@ def prefix_attention(q, k_prefix=None, v_prefix=None, *, prefix_lens=None, group
         kpg, vpg, tab, own = k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), lens.data_ptr()
     elif block_table is not None or lens is not None:
         raise ValueError("block_table and lens go with pages")
+    if n == 0 or t == 0:
+        return out
     args = (dt, n, t, H, kv, hd, q.data_ptr(), out.data_ptr(),
             H * hd if q.is_contiguous() else _token_stride(q, "q"), out_stride, G, S, g_start, kp, vp, kg,
             kt, vg, vt, T, p_lens, kpg, vpg, kps, vps, pages, size, tab, tab_stride, max_pages, own, scale)
@@ -795,6 +808,8 @@ def quantize_rows(x, out=None, scale=None, stream=None):
         raise ValueError(f"scale must be contiguous float32 {tuple(rows)}, got {scale.dtype} {tuple(scale.shape)}")
     if out.get_device() != dev or scale.get_device() != dev:
         raise _elsewhere((("out", out), ("scale", scale)))
+    if scale.numel() == 0:
+        return out, scale
     status = _lib.wenc_quantize_rows(x.data_ptr(), dt, out.data_ptr(), scale.data_ptr(), scale.numel(), d,
                                      _raw_stream(stream, dev))
     if status:
@@ -844,6 +859,8 @@ def linear_i8(a, a_scale, w, w_scale, bias, epilogue: int = EPI_BIAS_BF16, resid
         if resid.get_device() != dev:
             raise _elsewhere((("resid", resid),))
         rp = resid.data_ptr()
+    if M == 0:
+        return out
     ws = ws_bytes = 0
     if workspace is None and M > 16:
         need = _lib.wenc_linear_i8_workspace(M, N, K)
