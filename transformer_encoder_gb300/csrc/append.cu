@@ -201,9 +201,13 @@ __global__ void __launch_bounds__(32 * kWarps, 3) kv_append_kernel(const AppendP
       const int at = __shfl_sync(0xffffffffu, pos, i);
       if (lane < p.half) {
         const long long turn = static_cast<long long>(static_cast<unsigned long long>(static_cast<long long>(at)) * step);
+        // The angle is pi (turn / 2^63): its leading 24 bits go to sincospif, exactly, and the rest, an angle l < 2^-21,
+        // turns the result: sin(h + l) = sin h + l cos h to l^2 / 2 < 2^-43.
+        const int top = static_cast<int>(turn >> 32) & ~0xff;
+        const float l = static_cast<float>(static_cast<uint32_t>(turn >> 8)) * (3.14159265f * 0x1p-55f);
         float sv, cv;
-        sincospif(static_cast<float>(turn >> 32) * 0x1p-31f, &sv, &cv);  // turn * 2 pi = pi * (turn / 2^63)
-        cs_all[warp][i][lane] = make_float2(cv, sv);
+        sincospif(static_cast<float>(top) * 0x1p-31f, &sv, &cv);
+        cs_all[warp][i][lane] = make_float2(fmaf(-l, sv, cv), fmaf(l, cv, sv));
       }
     }
     __syncwarp();
