@@ -477,6 +477,18 @@ WENC_API wenc_status wenc_selftest_attention_abort(const uint16_t* q, const uint
 WENC_API wenc_status wenc_selftest_gemm_schedule(int M, int N, int pair, int max_units, int* cover, int cover_len,
                                                  int* unit_halves, int* units, int* halves);
 
+/* Host only, no device work: the index and angle arithmetic of the decode-side kernels, by the code that they run.
+ * wenc_selftest_append_sequence -- the sequence of row t, searched from row first <= t on as a warp of wenc_kv_append
+ *   does for a run of rows: 0 .. n_seqs - 1, with *left its rows from t on; n_seqs for a row behind the last; -1 where
+ *   seq_start [n_seqs + 1] is out of range.
+ * wenc_selftest_append_angle -- the angle position * inv_freq as pi * h + l modulo 2 pi, as the sine and cosine take it.
+ * wenc_selftest_attention_runs -- adds to seen[k] how often the warps of wenc_prefix_attention's one-launch form, `parts` of
+ *   them, score key k: the prefix's prefix_len keys first, then those of each of the n_own <= 16
+ *   sequences. */
+WENC_API int wenc_selftest_append_sequence(const int32_t* seq_start, int n_seqs, int first, int t, int* left);
+WENC_API void wenc_selftest_append_angle(float inv_freq, int position, float* h, float* l);
+WENC_API void wenc_selftest_attention_runs(int prefix_len, const int32_t* own, int n_own, int parts, int32_t* seen);
+
 /* wenc_sync_status -- synchronise the device and read the device error word of `h`
  * (or, when h is NULL, the word shared by the handle-less entry points), clearing it.
  * Returns WENC_OK, WENC_ERR_DEVICE_TIMEOUT, WENC_ERR_INVALID_ARG (a kernel met a length, offset or

@@ -22,6 +22,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "decode_index.cuh"
 #include "launch.h"
 #include "ptx.cuh"
 #include "wenc.h"
@@ -1172,6 +1173,38 @@ wenc_status wenc_selftest_attention_abort(const uint16_t* q, const uint16_t* k, 
                                                    stop_after);
   if (e != cudaSuccess) return cuda_fail(e, "self-test launch");
   return WENC_OK;
+}
+
+int wenc_selftest_append_sequence(const int32_t* seq_start, int n_seqs, int first, int t, int* left) {
+  const int s = wenc_dev::last_start(n_seqs + 1, [&](int lo, int step, int len) {
+    int n = 0;
+    for (int i = 0; i < 32; ++i)
+      if (static_cast<long long>(i) * step < len && seq_start[lo + i * step] <= first) ++n;
+    return n;
+  });
+  return wenc_dev::sequence_of(seq_start, n_seqs, t, s, *left);
+}
+
+void wenc_selftest_append_angle(float inv_freq, int position, float* h, float* l) {
+  wenc_dev::angle_parts(position, wenc_dev::turns64(inv_freq), *h, *l);
+}
+
+void wenc_selftest_attention_runs(int prefix_len, const int32_t* own, int n_own, int parts, int32_t* seen) {
+  constexpr int kMost = 16;  // sequences of a tile of 16 rows
+  if (n_own < 0 || n_own > kMost || parts < 1) return;
+  int step0[kMost + 2] = {0, (prefix_len + 15) / 16}, at[kMost + 2] = {0, prefix_len};  // a segment's first step, and key of `seen`
+  for (int i = 0; i < n_own; ++i) {
+    step0[i + 2] = step0[i + 1] + (own[i] + 15) / 16;
+    at[i + 2] = at[i + 1] + own[i];
+  }
+  for (int part = 0; part < parts; ++part) {
+    int first, count, sg = 0;
+    wenc_dev::run_of(step0[n_own + 1], part, parts, first, count);
+    for (int t = first; t < first + count; ++t) {
+      sg = wenc_dev::segment_of(step0, t, sg);
+      for (int key = at[sg] + (t - step0[sg]) * 16, end = key + 16; key < end && key < at[sg + 1]; ++key) ++seen[key];
+    }
+  }
 }
 
 wenc_status wenc_selftest_gemm_schedule(int M, int N, int pair, int max_units, int* cover, int cover_len,

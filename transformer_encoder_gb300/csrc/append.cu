@@ -34,6 +34,7 @@
 #include <cstdio>
 #include <string>
 
+#include "decode_index.cuh"
 #include "launch.h"
 #include "ptx.cuh"
 #include "wenc.h"
@@ -62,42 +63,13 @@ struct AppendParams {
   int n_tokens, n_seqs, per_seq, H, Hkv, n_pages, page_size, max_pages, half, interleaved;
 };
 
-// 2^64 * frac(f / 2 pi): the turns a position advances the angle by, as a 64-bit fraction.
-// 1 / 2 pi = c1 + c2 with c1 of 29 bits, so f * c1 is exact in double. The fraction is taken of |f|:
-// of a negative number, x - floor(x) = 1 - |x| would drop the bits of |x| below 2^-54, and a position
-// of 31 bits carries those up to 2^-23 of a turn.
-__device__ __forceinline__ unsigned long long turns64(float f) {
-  const double c1 = 0x1.45f306dp-3, c2 = 0x1.9391054a7f09dp-32;
-  double hi = fabs(static_cast<double>(f)) * c1, lo = fabs(static_cast<double>(f)) * c2;
-  hi -= floor(hi);
-  // hi in [0, 1): in two 32-bit parts (a conversion of hi * 2^64 could reach 2^64)
-  const double h32 = hi * 4294967296.0;
-  const unsigned long long top = static_cast<unsigned long long>(h32);
-  const unsigned long long low = static_cast<unsigned long long>((h32 - static_cast<double>(top)) * 4294967296.0);
-  lo -= floor(lo);
-  const double l32 = lo * 4294967296.0;
-  const unsigned long long ltop = static_cast<unsigned long long>(l32);
-  const unsigned long long llow = static_cast<unsigned long long>((l32 - static_cast<double>(ltop)) * 4294967296.0);
-  const unsigned long long turn = (top << 32) + low + (ltop << 32) + llow;
-  return f < 0.0f ? 0ull - turn : turn;
-}
-
 // The last sequence s with seq_start[s] <= t among 0 .. n-1 (-1: none), by all lanes of a warp: 32
 // probes a step.
 __device__ __forceinline__ int find_seq(const int32_t* start, int n, int t, int lane) {
-  int lo = 0, len = n;  // the answer + 1 lies in [lo, lo + len]
-  while (len > 0) {
-    const int step = (len + 31) / 32;
-    const int at = lo + lane * step;
-    const bool le = lane * step < len && start[at] <= t;
-    const int hits = __popc(__ballot_sync(0xffffffffu, le));
-    if (hits == 0) return lo - 1;
-    const int base = (hits - 1) * step;  // start[lo + base] <= t, and the next probe is not
-    const int rest = min(step, len - base) - 1;
-    lo += base + 1;
-    len = rest;
-  }
-  return lo - 1;
+  return last_start(n, [&](int lo, int step, int len) {
+    const bool le = lane * step < len && start[lo + lane * step] <= t;
+    return __popc(__ballot_sync(0xffffffffu, le));
+  });
 }
 
 // One 16-byte piece of a row: E elements as fp32.
@@ -154,27 +126,22 @@ __global__ void __launch_bounds__(32 * kWarps, 3) kv_append_kernel(const AppendP
   long long k_at = -1, v_at = 0;  // byte offsets of the token's slot; -1: the token is not written
   {
     const int t = first + lane;
-    int s = -1, begin = 0, end = 0;
+    int s = -1, left = 0;  // the token's sequence, and its rows from the token on
     if (p.seq_start) {
       s = find_seq(p.seq_start, p.n_seqs + 1, first, lane);  // the first token's; the others' at or behind it
       if (lane < n) {
-        if (s >= 0) {
-          while (s < p.n_seqs && p.seq_start[s + 1] <= t) ++s;
-          begin = p.seq_start[s];
-          end = s < p.n_seqs ? p.seq_start[s + 1] : 0x7fffffff;
-        }
-        // (offsets that do not start at 0 or do not ascend)
-        if (s < 0 || t < begin || t >= end) {
+        s = sequence_of(p.seq_start, p.n_seqs, t, s, left);
+        if (s < 0) {
           *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (82u << 8);
           s = p.n_seqs;
         }
       }
     } else {
       s = t / p.per_seq;
-      end = (s + 1) * p.per_seq;
+      left = (s + 1) * p.per_seq - t;
     }
     if (lane < n && s < p.n_seqs) {  // (s == n_seqs: padding rows behind the last sequence)
-      const long long at = static_cast<long long>(p.lens[s]) - (end - t);
+      const long long at = static_cast<long long>(p.lens[s]) - left;
       pos = static_cast<int>(at);
       const int page_i = pos / p.page_size;
       if (at < 0 || page_i >= p.max_pages) {
@@ -200,13 +167,10 @@ __global__ void __launch_bounds__(32 * kWarps, 3) kv_append_kernel(const AppendP
     for (int i = 0; i < n; ++i) {
       const int at = __shfl_sync(0xffffffffu, pos, i);
       if (lane < p.half) {
-        const long long turn = static_cast<long long>(static_cast<unsigned long long>(static_cast<long long>(at)) * step);
-        // The angle is pi (turn / 2^63): its leading 24 bits go to sincospif, exactly, and the rest, an angle l < 2^-21,
-        // turns the result: sin(h + l) = sin h + l cos h to l^2 / 2 < 2^-43.
-        const int top = static_cast<int>(turn >> 32) & ~0xff;
-        const float l = static_cast<float>(static_cast<uint32_t>(turn >> 8)) * (3.14159265f * 0x1p-55f);
-        float sv, cv;
-        sincospif(static_cast<float>(top) * 0x1p-31f, &sv, &cv);
+        // pi h goes to sincospi, and the rest turns the result: sin(h + l) = sin h + l cos h to l^2 / 2 < 2^-43
+        float h, l, sv, cv;
+        angle_parts(at, step, h, l);
+        sincospif(h, &sv, &cv);
         cs_all[warp][i][lane] = make_float2(fmaf(-l, sv, cv), fmaf(l, cv, sv));
       }
     }

@@ -53,6 +53,7 @@
 #include <cstdio>
 #include <string>
 
+#include "decode_index.cuh"
 #include "launch.h"
 #include "ptx.cuh"
 #include "wenc.h"
@@ -216,13 +217,6 @@ __device__ __forceinline__ void fill_segments(const PrefixParams& p, const Item&
   __syncthreads();
 }
 
-// Share `part` of `parts` equal runs of n steps.
-__device__ __forceinline__ void run_of(int n, int part, int parts, int& first, int& count) {
-  const int per = (n + parts - 1) / parts;
-  first = part * per;
-  count = max(0, min(per, n - first));
-}
-
 // 16-byte granule `c` of key row `row` within a warp's stage. bf16 rows have 8 granules (all 32 banks),
 // fp32 rows 16; the XOR spreads the rows that an ldmatrix (or a quarter of a fragment load) touches at
 // once over all banks.
@@ -308,7 +302,7 @@ __device__ __noinline__ void redo_non_numbers(const PrefixParams& p, const Item&
     for (int t = step0; t < step0 + n_mine; ++t) {
       int begin = 0, n_keys = solo_len;
       if constexpr (!SOLO) {
-        while (t >= seg->step0[sg + 1]) ++sg;
+        sg = segment_of(seg->step0, t, sg);
         begin = seg->step0[sg];
         n_keys = seg->len[sg];
       }
@@ -405,7 +399,7 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
       end = 0x7fffffff;
       keys = solo_len;
     } else {
-      while (t >= seg->step0[sg + 1]) ++sg;
+      sg = segment_of(seg->step0, t, sg);
       begin = seg->step0[sg];
       end = seg->step0[sg + 1];
       keys = seg->len[sg];

@@ -43,7 +43,8 @@ EXPORTED_SYMBOLS = (
     "wenc_set_cross_kv", "wenc_cross_kv", "wenc_selftest_gemm_schedule", "wenc_selftest_gemm_pair_abort",
     "wenc_set_device_alloc_limit", "wenc_device_bytes_held", "wenc_selftest_attention_abort",
     "wenc_prefix_attention", "wenc_prefix_attention_workspace", "wenc_kv_append", "wenc_quantize_rows",
-    "wenc_linear_i8", "wenc_linear_i8_workspace",
+    "wenc_linear_i8", "wenc_linear_i8_workspace", "wenc_selftest_append_sequence", "wenc_selftest_append_angle",
+    "wenc_selftest_attention_runs",
 )
 
 
@@ -159,6 +160,12 @@ def lib() -> ctypes.CDLL:
         L.wenc_linear_i8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, vp, ctypes.c_size_t, vp]
         L.wenc_linear_i8_workspace.argtypes = [i, i, i]
         L.wenc_linear_i8_workspace.restype = ctypes.c_size_t
+        L.wenc_selftest_append_sequence.argtypes = [vp, i, i, i, ip]
+        L.wenc_selftest_append_sequence.restype = ctypes.c_int
+        L.wenc_selftest_append_angle.argtypes = [ctypes.c_float, i, vp, vp]
+        L.wenc_selftest_append_angle.restype = None
+        L.wenc_selftest_attention_runs.argtypes = [i, vp, i, i, vp]
+        L.wenc_selftest_attention_runs.restype = None
         L.wenc_destroy.argtypes = [vp]
         L.wenc_destroy.restype = None
         L.wenc_last_error.restype = ctypes.c_char_p
