@@ -314,7 +314,8 @@ typedef struct {
   int max_pages;             /* max_pages * page_size <= 2^31 - 1 */
   const int32_t* lens;       /* [n_seqs] cache length of each sequence, the call's tokens included */
   const int32_t* seq_start;  /* [n_seqs + 1], ascending from 0: sequence s owns the rows seq_start[s] ..
-                                seq_start[s+1]-1; NULL: n_tokens / n_seqs rows each */
+                                seq_start[s+1]-1, all of them below n_tokens; NULL: n_tokens / n_seqs rows
+                                each */
   const int32_t* positions;  /* [n_tokens] the position each token turns by; NULL: its cache position */
   const float* inv_freq;     /* [rot_dim / 2] angle per position, finite and below 2^24 in magnitude, of
                                 either sign; NULL: no rotation (rot_dim ignored) */
@@ -478,14 +479,14 @@ WENC_API wenc_status wenc_selftest_gemm_schedule(int M, int N, int pair, int max
                                                  int* unit_halves, int* units, int* halves);
 
 /* Host only, no device work: the index and angle arithmetic of the decode-side kernels, by the code that they run.
- * wenc_selftest_append_sequence -- the sequence of row t, searched from row first <= t on as a warp of wenc_kv_append
+ * wenc_selftest_append_sequence -- the sequence of row t of n_tokens, searched from row first <= t on as a warp of wenc_kv_append
  *   does for a run of rows: 0 .. n_seqs - 1, with *left its rows from t on; n_seqs for a row behind the last; -1 where
  *   seq_start [n_seqs + 1] is out of range.
  * wenc_selftest_append_angle -- the angle position * inv_freq as pi * h + l modulo 2 pi, as the sine and cosine take it.
  * wenc_selftest_attention_runs -- adds to seen[k] how often the warps of wenc_prefix_attention's one-launch form, `parts` of
  *   them, score key k: the prefix's prefix_len keys first, then those of each of the n_own <= 16
  *   sequences. */
-WENC_API int wenc_selftest_append_sequence(const int32_t* seq_start, int n_seqs, int first, int t, int* left);
+WENC_API int wenc_selftest_append_sequence(const int32_t* seq_start, int n_seqs, int n_tokens, int first, int t, int* left);
 WENC_API void wenc_selftest_append_angle(float inv_freq, int position, float* h, float* l);
 WENC_API void wenc_selftest_attention_runs(int prefix_len, const int32_t* own, int n_own, int parts, int32_t* seen);
 

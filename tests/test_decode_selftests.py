@@ -18,10 +18,10 @@ def L():
     return lib()
 
 
-def _sequence(L, start, t, first=None):
+def _sequence(L, start, t, first=None, rows=2 ** 31 - 1):
     start = np.ascontiguousarray(start, np.int32)
     left = ctypes.c_int(-7)
-    s = L.wenc_selftest_append_sequence(start.ctypes.data, len(start) - 1, t if first is None else first, t, ctypes.byref(left))
+    s = L.wenc_selftest_append_sequence(start.ctypes.data, len(start) - 1, rows, t if first is None else first, t, ctypes.byref(left))
     return s, left.value
 
 
@@ -38,6 +38,14 @@ def test_a_tokens_sequence(L, n):
             assert s == want if t < total else s == n
             if t < total:
                 assert left == start[s + 1] - t
+
+
+def test_a_sequence_that_ends_behind_the_rows(L):
+    start = [0, 3, 3, 10]
+    assert _sequence(L, start, 2, rows=9) == (0, 1)
+    assert _sequence(L, start, 3, rows=9)[0] == -1
+    assert _sequence(L, start, 3, rows=10) == (2, 7)
+    assert _sequence(L, start, 10, rows=11)[0] == 3
 
 
 def test_offsets_out_of_range(L):

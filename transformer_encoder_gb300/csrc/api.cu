@@ -1175,14 +1175,14 @@ wenc_status wenc_selftest_attention_abort(const uint16_t* q, const uint16_t* k, 
   return WENC_OK;
 }
 
-int wenc_selftest_append_sequence(const int32_t* seq_start, int n_seqs, int first, int t, int* left) {
+int wenc_selftest_append_sequence(const int32_t* seq_start, int n_seqs, int n_tokens, int first, int t, int* left) {
   const int s = wenc_dev::last_start(n_seqs + 1, [&](int lo, int step, int len) {
     int n = 0;
     for (int i = 0; i < 32; ++i)
       if (static_cast<long long>(i) * step < len && seq_start[lo + i * step] <= first) ++n;
     return n;
   });
-  return wenc_dev::sequence_of(seq_start, n_seqs, t, s, *left);
+  return wenc_dev::sequence_of(seq_start, n_seqs, n_tokens, t, s, *left);
 }
 
 void wenc_selftest_append_angle(float inv_freq, int position, float* h, float* l) {

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) kv_append_kernel(const AppendP
     if (p.seq_start) {
       s = find_seq(p.seq_start, p.n_seqs + 1, first, lane);  // the first token's; the others' at or behind it
       if (lane < n) {
-        s = sequence_of(p.seq_start, p.n_seqs, t, s, left);
+        s = sequence_of(p.seq_start, p.n_seqs, p.n_tokens, t, s, left);
         if (s < 0) {
           *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (82u << 8);
           s = p.n_seqs;

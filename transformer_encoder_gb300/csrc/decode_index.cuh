@@ -57,14 +57,18 @@ __host__ __device__ __forceinline__ int last_start(int n, const Hits& hits) {
   return lo - 1;
 }
 
-// The sequence of row t, at or behind sequence s (as last_start gives it for a row at or before t): 0 .. n_seqs - 1, and
-// how many rows `left` it has from t on; n_seqs for a row behind the last sequence; -1 where the offsets are out of range.
-__host__ __device__ __forceinline__ int sequence_of(const int32_t* start, int n_seqs, int t, int s, int& left) {
+// The sequence of row t of n_rows, at or behind sequence s (as last_start gives it for a row at or before t): 0 .. n_seqs -
+// 1, and how many rows `left` it has from t on; n_seqs for a row behind the last sequence; -1 where the offsets are out of
+// range.
+__host__ __device__ __forceinline__ int sequence_of(const int32_t* start, int n_seqs, int n_rows, int t, int s, int& left) {
   left = 0;
   if (s < 0) return -1;  // (offsets that do not start at 0)
   while (s < n_seqs && start[s + 1] <= t) ++s;
   if (start[s] > t) return -1;  // (offsets that do not ascend)
-  if (s < n_seqs) left = start[s + 1] - t;
+  if (s < n_seqs) {
+    if (start[s + 1] > n_rows) return -1;  // (a sequence that ends behind the rows: where they go would be wrong)
+    left = start[s + 1] - t;
+  }
   return s;
 }
 

@@ -160,7 +160,7 @@ def lib() -> ctypes.CDLL:
         L.wenc_linear_i8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, vp, ctypes.c_size_t, vp]
         L.wenc_linear_i8_workspace.argtypes = [i, i, i]
         L.wenc_linear_i8_workspace.restype = ctypes.c_size_t
-        L.wenc_selftest_append_sequence.argtypes = [vp, i, i, i, ip]
+        L.wenc_selftest_append_sequence.argtypes = [vp, i, i, i, i, ip]
         L.wenc_selftest_append_sequence.restype = ctypes.c_int
         L.wenc_selftest_append_angle.argtypes = [ctypes.c_float, i, vp, vp]
         L.wenc_selftest_append_angle.restype = None
