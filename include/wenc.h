@@ -301,7 +301,7 @@ typedef struct {
   int n_heads, n_kv_heads;   /* query heads (read only with q) and key heads, each at most 4096 */
   int head_dim;              /* must be 64 */
   const void* q;             /* [n_tokens][n_heads][64], or NULL with q_out NULL: no queries */
-  void* q_out;               /* where the turned queries go (may be q) */
+  void* q_out;               /* where the turned queries go (may be q, with q_stride; else apart from every input) */
   const void* k;             /* [n_tokens][n_kv_heads][64] */
   const void* v;
   int64_t q_stride, q_out_stride, k_stride, v_stride; /* between tokens */
@@ -327,7 +327,7 @@ typedef struct {
  * queries, into q_out) by their positions on the way (inferencelayer DEC_WRITE; oxinfer
  * LayerCache; Whisper itself has learned positions: pass inv_freq = NULL). Token t of sequence s
  * goes to cache position lens[s] - (seq_start[s+1] - t). Rows behind seq_start[n_seqs] are neither
- * read nor written. Which key stays is undefined when two sequences' tables lead to one slot.
+ * read nor written. Which elements stay is undefined where two tokens' tables lead to one slot.
  * A length, offset or page number out of range leaves that token unwritten and records
  * WENC_ERR_INVALID_ARG in the device error word (wenc_sync_status(NULL)). One launch,
  * stream-ordered. */

@@ -294,6 +294,10 @@ extern "C" wenc_status wenc_kv_append(const wenc_kv_append_args* a, wenc_stream_
                                a->k_page_stride, a->v_page_stride};
   for (long long x : strides)
     if (x % per16 != 0) return bad(WENC_ERR_INVALID_ARG, "strides must be multiples of 16 bytes");
+  // (in place, a warp rewrites the rows it has read; with two strides it would write rows that others have yet to read)
+  if (a->q && a->q == a->q_out && a->q_stride != a->q_out_stride && a->n_tokens > 1)
+    return bad(WENC_ERR_INVALID_ARG, "kv_append: in place, q_stride %lld and q_out_stride %lld must be the same", a->q_stride,
+               a->q_out_stride);
   if (a->n_tokens == 0) return WENC_OK;
   int sms = 0;
   uint32_t* err = nullptr;
@@ -329,7 +333,7 @@ extern "C" wenc_status wenc_kv_append(const wenc_kv_append_args* a, wenc_stream_
   p.max_pages = a->max_pages;
   p.half = rot / 2;
   p.interleaved = a->interleaved;
-  // queries that neither turn nor move need no pass
+  // queries that neither turn nor move need no pass (in place, the strides are one: checked above)
   if (p.half == 0 && p.q == p.q_out) p.q = nullptr;
 
   const int rpw = a->dtype == WENC_DTYPE_F32 ? 4 : 8;  // rows a warp moves at once
