@@ -234,142 +234,6 @@ struct RowState {
   float o[NR][4][4], m[NR][2], l[NR][2];  // m in log2 units; l of this thread's keys alone until reduced
 };
 
-// One 16-byte piece of a key or query row as fp32.
-__device__ __forceinline__ void unpack_piece(const uint4& u, float (&f)[4]) {
-  f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
-  f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
-}
-__device__ __forceinline__ void unpack_piece(const uint4& u, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
-// The products with V are formed for all of a tile's rows, with weights of 0 where a row does not see a key, and in
-// two parts; but 0 x inf and 0 x NaN are NaN, so a value that is no number would reach rows that do not see it. And the
-// TF32 part of a float32 next to the largest one is infinite. Such elements of O, and rows whose sum is no number
-// (rare: attend() finds them by that), are formed again here in plain fp32, from the keys each row sees alone. A key at a
-// time: a lane a row for the scores, then every lane its own elements. (A function of its own:
-// looking for them costs a call up to 0.4 us, 1.0 in the joined form; inlined, the calls took 0.3 to 0.5 us more.)
-template <typename T, int NR, bool SOLO>
-__device__ __noinline__ void redo_non_numbers(const PrefixParams& p, const Item& it, const SegTable* seg, int solo_len, int step0,
-                                              int n_mine, RowState<NR>& st) {
-  using C = Cfg<T, NR>;
-  constexpr int E = 16 / sizeof(T);
-  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
-  uint32_t bad = 0u;  // bit 16 r + 4 i + e: o[r][i][e]
-  bool rows = false;  // some row's sum is no number
-#pragma unroll
-  for (int r = 0; r < NR; ++r)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const bool row = !(fabsf(st.l[r][e & 1]) < CUDART_INF_F), in = 8 * r + 2 * tq + (e & 1) < it.n_rows;
-      rows |= row && in;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (in && (row || !(fabsf(st.o[r][i][e]) < CUDART_INF_F))) {
-          bad |= 1u << (16 * r + 4 * i + e);
-          st.o[r][i][e] = 0.0f;
-        }
-    }
-  rows = __any_sync(0xffffffffu, rows);
-  // this lane's row: its queries, sequence, token, maximum and sum
-  const int x = it.row_off + lane, tok = x / p.r, per_seq = p.q_len * p.r, row_seq = x / per_seq, row_tok = (x - row_seq * per_seq) / p.r;
-  const uint8_t* q = p.q + (static_cast<long long>(it.seq0) * p.q_len + tok) * p.q_stride + (it.hk * p.r + x - tok * p.r) * C::ROWB;
-  float m = -CUDART_INF_F, l = 0.0f;
-#pragma unroll
-  for (int r = 0; r < NR; ++r)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {  // row 8 r + y sits in the lanes of column pair y / 2, element y % 2
-      const float y = __shfl_sync(0xffffffffu, st.m[r][e], (lane & 7) >> 1), z = __shfl_sync(0xffffffffu, st.l[r][e], (lane & 7) >> 1);
-      if ((lane >> 3) == r && (lane & 1) == e) {
-        m = y;
-        l = z;
-      }
-    }
-  const bool again = !(fabsf(l) < CUDART_INF_F);
-  if (again) {
-    m = -CUDART_INF_F;
-    l = 0.0f;
-  }
-  // every key of the run: f(its value row, whether this lane's row sees it, that row's score in log2 units)
-  auto each_key = [&](auto&& f) {
-    int sg = SOLO ? 1 : 0;
-#pragma unroll 1
-    for (int t = step0; t < step0 + n_mine; ++t) {
-      int begin = 0, n_keys = solo_len;
-      if constexpr (!SOLO) {
-        sg = segment_of(seg->step0, t, sg);
-        begin = seg->step0[sg];
-        n_keys = seg->len[sg];
-      }
-      const int last = min(n_keys, (t - begin + 1) * C::KW);
-#pragma unroll 1
-      for (int key = (t - begin) * C::KW; key < last; ++key) {
-        const uint8_t *k, *v;
-        if (sg == 0) {
-          k = it.kp + key * p.k_token;
-          v = it.vp + key * p.v_token;
-        } else {
-          const int pi = key / p.page_size, page = p.table[(it.seq0 + sg - 1) * p.table_stride + pi];
-          if (page < 0 || page >= p.n_pages) continue;  // (reported when its step was loaded)
-          const uint64_t at = static_cast<uint64_t>(key - pi * p.page_size) * p.row16 + it.hk * (C::ROWB / 16);
-          k = p.k_pages + ((static_cast<uint64_t>(page) * p.k_page16 + at) << 4);
-          v = p.v_pages + ((static_cast<uint64_t>(page) * p.v_page16 + at) << 4);
-        }
-        const bool sees = lane < it.n_rows && (sg == 0 || (row_seq == sg - 1 && key < n_keys - p.q_len + 1 + row_tok));
-        float dot = 0.0f;
-        if (sees) {
-#pragma unroll 1
-          for (int c = 0; c < C::ROWB / 16; ++c) {
-            uint4 qc = *reinterpret_cast<const uint4*>(q + 16 * c);
-            qc = make_uint4((qc.x & p.q_keep) ^ p.q_flip, (qc.y & p.q_keep) ^ p.q_flip, (qc.z & p.q_keep) ^ p.q_flip, (qc.w & p.q_keep) ^ p.q_flip);
-            float a[E], b[E];
-            unpack_piece(qc, a);
-            unpack_piece(*reinterpret_cast<const uint4*>(k + 16 * c), b);
-#pragma unroll
-            for (int e = 0; e < E; ++e) dot = fmaf(a[e], b[e], dot);
-          }
-        }
-        f(v, sees, dot * p.scale_log2);
-      }
-    }
-  };
-  if (rows)
-    each_key([&](const uint8_t*, bool sees, float s) {
-      if (sees && again) m = fmaxf(m, s);
-    });
-  const float u = m == -CUDART_INF_F ? 0.0f : m;
-  each_key([&](const uint8_t* v, bool sees, float s) {
-    const float w = sees ? ex2_approx(s - u) : -1.0f;  // -1: not seen
-    if (sees && again) l += w;
-#pragma unroll
-    for (int r = 0; r < NR; ++r)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float y = __shfl_sync(0xffffffffu, w, 8 * r + 2 * tq + e);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (((bad >> (16 * r + 4 * i + e + 2 * h)) & 1u) && !(y < 0.0f)) {
-              const T z = reinterpret_cast<const T*>(v)[C::F32 ? 32 * h + 4 * g + i : 16 * i + 8 * h + g];
-              st.o[r][i][e + 2 * h] += y * static_cast<float>(z);
-            }
-      }
-  });
-#pragma unroll
-  for (int r = 0; r < NR; ++r)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      st.m[r][e] = __shfl_sync(0xffffffffu, m, 8 * r + 2 * tq + e);
-      st.l[r][e] = __shfl_sync(0xffffffffu, l, 8 * r + 2 * tq + e);
-    }
-}
-
 // One warp's run of steps [step0, step0 + n_mine). SOLO: the item is one own-key segment of solo_len keys
 // (no table); else the segments are in `seg`.
 template <typename T, int NR, bool SOLO>
@@ -715,21 +579,6 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
       l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], 8);
       l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], 16);
     }
-  float zero[2] = {0.0f, 0.0f};  // 0 unless some sum or element is no number
-#pragma unroll
-  for (int r = 0; r < NR; ++r)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      zero[e] = fmaf(l[r][e], 0.0f, zero[e]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) zero[e] = fmaf(o[r][i][e + 2], 0.0f, fmaf(o[r][i][e], 0.0f, zero[e]));
-    }
-  if (__any_sync(0xffffffffu, !(zero[0] + zero[1] == 0.0f))) {
-    RowState<NR> copy = st;  // (so that st stays in registers)
-    const Item item = it;
-    redo_non_numbers<T, NR, SOLO>(p, item, seg, solo_len, step0, n_mine, copy);
-    st = copy;
-  }
 }
 
 // All warps' results into shared memory, over the rings; begins and ends with a barrier.
@@ -778,6 +627,133 @@ __device__ __forceinline__ void join_warps(const uint8_t* smem, int x, int c8, f
     v[0] += f * a.x; v[1] += f * a.y; v[2] += f * a.z; v[3] += f * a.w;
     v[4] += f * b.x; v[5] += f * b.y; v[6] += f * b.z; v[7] += f * b.w;
   }
+}
+
+// Eight elements of a key or query row as fp32.
+__device__ __forceinline__ void load8(const float* x, float (&f)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(x)[0], b = reinterpret_cast<const float4*>(x)[1];
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* x, float (&f)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(x);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// The products with V are formed for all of a tile's rows, with weights of 0 where a row does not see a key, and in
+// two parts; but 0 x inf and 0 x NaN are NaN, so a value that is no number would reach rows that do not see it. And the
+// TF32 part of a float32 next to the largest one is infinite. Such elements of a row's O, and all of a row whose sum is
+// no number (rare: they are found by that), are formed again here in plain fp32, from the keys alone that the row sees among
+// steps [step0, step0 + n_steps). Eight lanes hold a row: x, its elements c8 .. c8 + 7 in v, maximum m and sum l. (Looking
+// for them on the joined results of a CTA costs a call 0.1 to 0.2 us, the joined form 0.7; on each warp's own state, before the
+// join, it cost 0.4 to 1.3.)
+template <typename T, bool SOLO>
+__device__ __noinline__ void redo_rows(const PrefixParams& p, const Item& it, const SegTable* seg, int solo_len, int step0, int n_steps,
+                                       int x, int c8, float (&v)[8], float& m, float& l) {
+  const bool in = x < it.n_rows, again = in && !(fabsf(l) < CUDART_INF_F);
+  bool bad[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    bad[e] = in && (again || !(fabsf(v[e]) < CUDART_INF_F));
+    if (bad[e]) v[e] = 0.0f;
+  }
+  if (again) {
+    m = -CUDART_INF_F;
+    l = 0.0f;
+  }
+  const int y = it.row_off + x, tok = y / p.r, per_seq = p.q_len * p.r, row_seq = y / per_seq, row_tok = (y - row_seq * per_seq) / p.r;
+  float q[8] = {};
+  if (in) load8(reinterpret_cast<const T*>(p.q + (static_cast<long long>(it.seq0) * p.q_len + tok) * p.q_stride) + (it.hk * p.r + y - tok * p.r) * HD + c8, q);
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (p.q_keep == 0u) q[e] = 0.0f;
+    else if (p.q_flip != 0u) q[e] = -q[e];
+  // every key of the steps: f(its value row, whether this lane's row sees it, that row's score in log2 units)
+  auto each_key = [&](auto&& f) {
+    int sg = SOLO ? 1 : 0;
+#pragma unroll 1
+    for (int t = step0; t < step0 + n_steps; ++t) {
+      int begin = 0, n_keys = solo_len;
+      if constexpr (!SOLO) {
+        sg = segment_of(seg->step0, t, sg);
+        begin = seg->step0[sg];
+        n_keys = seg->len[sg];
+      }
+      const int last = min(n_keys, (t - begin + 1) * 16);
+#pragma unroll 1
+      for (int key = (t - begin) * 16; key < last; ++key) {
+        const uint8_t *k, *vr;
+        if (sg == 0) {
+          k = it.kp + key * p.k_token;
+          vr = it.vp + key * p.v_token;
+        } else {
+          const int pi = key / p.page_size, page = p.table[(it.seq0 + sg - 1) * p.table_stride + pi];
+          if (page < 0 || page >= p.n_pages) continue;  // (reported when its step was loaded)
+          const uint64_t at = static_cast<uint64_t>(key - pi * p.page_size) * p.row16 + it.hk * (HD * sizeof(T) / 16);
+          k = p.k_pages + ((static_cast<uint64_t>(page) * p.k_page16 + at) << 4);
+          vr = p.v_pages + ((static_cast<uint64_t>(page) * p.v_page16 + at) << 4);
+        }
+        const bool sees = in && (sg == 0 || (row_seq == sg - 1 && key < n_keys - p.q_len + 1 + row_tok));
+        float kf[8], dot = 0.0f;
+        load8(reinterpret_cast<const T*>(k) + c8, kf);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dot = fmaf(q[e], kf[e], dot);
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+        f(reinterpret_cast<const T*>(vr) + c8, sees, dot * p.scale_log2);
+      }
+    }
+  };
+  if (__any_sync(0xffffffffu, again))
+    each_key([&](const T*, bool sees, float s) {
+      if (sees && again) m = fmaxf(m, s);
+    });
+  const float u = m == -CUDART_INF_F ? 0.0f : m;
+  each_key([&](const T* row, bool sees, float s) {
+    if (!sees) return;
+    const float w = ex2_approx(s - u);
+    if (again) l += w;
+    float vf[8];
+    load8(row, vf);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (bad[e]) v[e] = fmaf(w, vf[e], v[e]);
+  });
+}
+
+// The check, and rarely the call, with copies so that the values stay in registers otherwise. steps(): the steps.
+template <typename T, bool SOLO, class Steps>
+__device__ __forceinline__ void redo_if_needed(const PrefixParams& p, const Item& it, const SegTable* seg, int solo_len, const Steps& steps,
+                                               int x, int c8, float (&v)[8], float& m, float& l) {
+  float zero = l * 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) zero = fmaf(v[e], 0.0f, zero);
+  if (!__any_sync(0xffffffffu, !(zero == 0.0f))) return;
+  const Item item = it;
+  int step0, n_steps;
+  float vc[8], mc = m, lc = l;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) vc[e] = v[e];
+  steps(step0, n_steps);
+  redo_rows<T, SOLO>(p, item, seg, solo_len, step0, n_steps, x, c8, vc, mc, lc);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = vc[e];
+  m = mc;
+  l = lc;
+}
+
+// The steps that the NW warps of a CTA take, parts first_part .. first_part + NW - 1 of `parts`.
+template <int NW>
+__device__ __forceinline__ void cta_run(int n, int first_part, int parts, int& first, int& count) {
+  int last, n_last;
+  run_of(n, first_part, parts, first, count);
+  run_of(n, first_part + NW - 1, parts, last, n_last);
+  count = min(n, last + n_last) - first;
 }
 
 // Eight elements of an output row, normalised (a row without a visible key: zeros).
@@ -881,7 +857,12 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
     write_out8<T>(p, it.seq0 * p.q_len + tok, it.hk * p.r + y - tok * p.r, c8, v, l);
   };
   float v[8], m, l;
-  if (x < C::ROWS) join_warps<T, NR>(smem_dyn, x, c8, v, m, l);
+  if (x < C::ROWS) {  // (whole warps)
+    join_warps<T, NR>(smem_dyn, x, c8, v, m, l);
+    redo_if_needed<T, false>(p, it, &seg, 0, [&](int& first, int& n) {
+      cta_run<C::NW>(seg.step0[1 + it.n_own], rank * C::NW, p.cluster * C::NW, first, n);
+    }, x, c8, v, m, l);
+  }
   if (p.cluster == 1) {
     if (x < it.n_rows) put(x, v, l);
     return;
@@ -970,9 +951,12 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
   attend<T, NR, false>(p, it, smem_dyn, &seg, 0, step0, n_steps, st, err);
   share_results<T, NR>(smem_dyn, st);
   const int x = threadIdx.x >> 3, c8 = (threadIdx.x & 7) * 8;
-  if (x >= it.n_rows) return;
+  if (x >= C::ROWS) return;  // (whole warps)
   float v[8], m, l;
   join_warps<T, NR>(smem_dyn, x, c8, v, m, l);
+  redo_if_needed<T, false>(p, it, &seg, 0, [&](int& first, int& n) { cta_run<C::NW>(seg.step0[1], split * C::NW, p.np * C::NW, first, n); },
+                           x, c8, v, m, l);
+  if (x >= it.n_rows) return;
   const int y = row0 + x, tok = y / p.r;
   write_partial(p, begin * p.q_len + tok, it.hk * p.r + y - tok * p.r, split, c8, v, m, l);
 }
@@ -1030,12 +1014,12 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
       // row x's maximum and sum sit in the lanes of column pair x / 2, element x % 2
       const float m0 = __shfl_sync(0xffffffffu, st.m[r][0], x >> 1), m1 = __shfl_sync(0xffffffffu, st.m[r][1], x >> 1);
       const float l0 = __shfl_sync(0xffffffffu, st.l[r][0], x >> 1), l1 = __shfl_sync(0xffffffffu, st.l[r][1], x >> 1);
-      if (8 * r + x < it.n_rows) {
-        float v[8];
+      float v[8], m = x & 1 ? m1 : m0, l = x & 1 ? l1 : l0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = so[x * C::OS + c8 + e];
-        write_partial(p, it.seq0 * p.q_len + tok, it.hk * p.r + y - tok * p.r, p.np + split, c8, v, x & 1 ? m1 : m0, x & 1 ? l1 : l0);
-      }
+      for (int e = 0; e < 8; ++e) v[e] = so[x * C::OS + c8 + e];
+      redo_if_needed<T, true>(p, it, nullptr, len, [&](int& first, int& n) { run_of((len + 15) / 16, split, p.ns, first, n); },
+                              8 * r + x, c8, v, m, l);
+      if (8 * r + x < it.n_rows) write_partial(p, it.seq0 * p.q_len + tok, it.hk * p.r + y - tok * p.r, p.np + split, c8, v, m, l);
     }
   }
 }
