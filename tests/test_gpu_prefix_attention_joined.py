@@ -94,3 +94,47 @@ def test_append_and_joined_attention_back_to_back(dtype, H, Hkv, n, T):
 
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(steps(replay, False), want))
+
+
+def _room(c):
+    """Bytes of workspace the case needs, exactly."""
+    import re
+    import torch
+    from transformer_encoder_gb300 import WencError, prefix_attention
+    with pytest.raises(WencError) as e:
+        prefix_attention(c.tq, **c.kw, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+    return int(re.search(r"workspace of (\d+) bytes needed", str(e.value)).group(1))
+
+
+@pytest.mark.parametrize("dtype,H,Hkv,sizes,pre", [
+    ("bf16", 32, 32, [160, 90], [700, 0]), ("bf16", 130, 1, [300], [300]), ("f32", 32, 32, [245, 60], [0, 200]),
+    ("f32", 130, 1, [50, 44], [150, 3])])
+def test_a_given_workspace_may_hold_anything(dtype, H, Hkv, sizes, pre):
+    """Many slots of the partial results stay unwritten (short and empty prefixes and own lists): what their memory held,
+    NaN or the call's before, is not in the result; and two such calls at once, each with its own, give the same bits."""
+    import torch
+    from transformer_encoder_gb300 import prefix_attention, sync_status
+    r = np.random.default_rng(H + sizes[0])
+    cases = [Case(dtype, sizes, 1, H, Hkv, pre, [int(x) for x in r.integers(0, 40, sum(sizes)) * r.integers(0, 2, sum(sizes))],
+                  page=8, uneven=len(sizes) > 1, seed=s, prefix_max=900) for s in (34, 35)]
+    assert all(_joins(c) for c in cases)
+    want = [c.run() for c in cases]
+    cases[0].check(want[0])
+    guard = 4096
+    rooms = [torch.full((_room(c) + guard,), 255, dtype=torch.uint8, device="cuda") for c in cases]
+    for _ in range(3):  # NaN in every slot, then what the last call left
+        assert torch.equal(cases[0].run(workspace=rooms[0][:-guard]), want[0])
+    assert torch.equal(cases[1].run(workspace=rooms[0][:_room(cases[1])]), want[1])  # another call's partial results
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [torch.empty_like(w) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for c, s, w, o in zip(cases, streams, rooms, outs):
+            prefix_attention(c.tq, **c.kw, out=o, workspace=w[:-guard], stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    sync_status()
+    assert all((w[-guard:] == 255).all() for w in rooms)
