@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) kv_append_kernel(const AppendP
       left = (s + 1) * p.per_seq - t;
     }
     if (lane < n && s < p.n_seqs) {  // (s == n_seqs: padding rows behind the last sequence)
-      const long long at = static_cast<long long>(p.lens[s]) - left;
+      const long long at = in_bounds(s >= 0 && s < p.n_seqs, err, 97) ? static_cast<long long>(p.lens[s]) - left : -1;
       pos = static_cast<int>(at);
       const int page_i = pos / p.page_size;
       if (at < 0 || page_i >= p.max_pages) {
@@ -190,6 +190,9 @@ __global__ void __launch_bounds__(32 * kWarps, 3) kv_append_kernel(const AppendP
     const long long kd = __shfl_sync(0xffffffffu, k_at, i), vd = __shfl_sync(0xffffffffu, v_at, i);
     if (kd < 0) continue;
     const long long t = first + i;
+    if (!in_bounds(t < p.n_tokens && kd + p.Hkv * ROWB <= p.n_pages * p.k_page_stride && vd + p.Hkv * ROWB <= p.n_pages * p.v_page_stride,
+                   err, 98))
+      continue;
     const uint8_t *q = p.q + t * p.q_stride, *k = p.k + t * p.k_stride, *v = p.v + t * p.v_stride;
     uint8_t *qd = p.q_out + t * p.q_out_stride, *kdst = p.k_pages + kd, *vdst = p.v_pages + vd;
     float c[E], sn[E];

@@ -130,7 +130,8 @@ __device__ __forceinline__ void quantize_vec(const float (&f)[E], const RowScale
 // maximum and the division. What bounds it: bytes (x once, the integers once).
 template <typename T, int VPT, bool WARP>
 __global__ void __launch_bounds__(WARP ? 128 : 1024) quantize_rows_kernel(const T* __restrict__ x, int8_t* __restrict__ xq,
-                                                             float* __restrict__ scale, int rows, int nv) {
+                                                             float* __restrict__ scale, int rows, int nv,
+                                                             uint32_t* err) {
   using V = Vec<T>;
   __shared__ uint32_t part[32];
   pdl_trigger();
@@ -138,6 +139,8 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) quantize_rows_kernel(const 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long row = WARP ? static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
   if (row >= rows) return;  // (a whole warp; the block form has a block for each row)
+  // (the threads' vectors cover the row, and each is checked against its end)
+  if (!in_bounds(VPT * (WARP ? 32 : static_cast<int>(blockDim.x)) >= nv, err, 99)) return;
   const int first = WARP ? lane : threadIdx.x, step = WARP ? 32 : blockDim.x;
   const uint4* xr = reinterpret_cast<const uint4*>(x) + row * nv;
   uint4 v[VPT];
@@ -197,16 +200,16 @@ __global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const T* __res
 }
 
 template <typename T, int VPT>
-cudaError_t launch_quantize(const T* x, int8_t* xq, float* scale, int rows, int nv, int threads, cudaStream_t s) {
+cudaError_t launch_quantize(const T* x, int8_t* xq, float* scale, int rows, int nv, int threads, uint32_t* err, cudaStream_t s) {
   if (threads == 32)  // a warp per row, four rows a block
-    return wenc_host::launch_pdl(quantize_rows_kernel<T, VPT, true>, dim3((rows - 1) / 4 + 1), dim3(128), 0, s, x, xq, scale, rows, nv);
-  return wenc_host::launch_pdl(quantize_rows_kernel<T, VPT, false>, dim3(rows), dim3(threads), 0, s, x, xq, scale, rows, nv);
+    return wenc_host::launch_pdl(quantize_rows_kernel<T, VPT, true>, dim3((rows - 1) / 4 + 1), dim3(128), 0, s, x, xq, scale, rows, nv, err);
+  return wenc_host::launch_pdl(quantize_rows_kernel<T, VPT, false>, dim3(rows), dim3(threads), 0, s, x, xq, scale, rows, nv, err);
 }
 
 // Threads per row: a warp up to 64 vectors (two a lane); else the fewest, from 128, that keep a row within
 // eight vectors a thread.
 template <typename T>
-cudaError_t quantize(const T* x, int8_t* xq, float* scale, int rows, int d, cudaStream_t s) {
+cudaError_t quantize(const T* x, int8_t* xq, float* scale, int rows, int d, uint32_t* err, cudaStream_t s) {
   const int nv = d / Vec<T>::E;
   if (nv > 8 * 1024)
     return wenc_host::launch_pdl(quantize_long_rows_kernel<T>, dim3(rows), dim3(1024), 0, s, x, xq, scale, nv);
@@ -216,10 +219,10 @@ cudaError_t quantize(const T* x, int8_t* xq, float* scale, int rows, int d, cuda
     while (threads * 8 < nv) threads *= 2;
   }
   const int vpt = (nv + threads - 1) / threads;
-  if (vpt <= 2) return launch_quantize<T, 2>(x, xq, scale, rows, nv, threads, s);
-  if (vpt <= 4) return launch_quantize<T, 4>(x, xq, scale, rows, nv, threads, s);
-  if (vpt <= 6) return launch_quantize<T, 6>(x, xq, scale, rows, nv, threads, s);
-  return launch_quantize<T, 8>(x, xq, scale, rows, nv, threads, s);
+  if (vpt <= 2) return launch_quantize<T, 2>(x, xq, scale, rows, nv, threads, err, s);
+  if (vpt <= 4) return launch_quantize<T, 4>(x, xq, scale, rows, nv, threads, err, s);
+  if (vpt <= 6) return launch_quantize<T, 6>(x, xq, scale, rows, nv, threads, err, s);
+  return launch_quantize<T, 8>(x, xq, scale, rows, nv, threads, err, s);
 }
 
 // ---------------------------------------------------------------- few tokens
@@ -284,7 +287,7 @@ template <int NT, int AHEAD, int CTAS>
 __global__ void __launch_bounds__(256, CTAS) i8_rows_kernel(const int8_t* __restrict__ xq, const float* __restrict__ x_scale,
                                                          const int8_t* __restrict__ wq, const float* __restrict__ w_scale,
                                                          const float* __restrict__ bias, const float* resid, void* out, int M,
-                                                         int N, int K, int ksplit, int epilogue) {
+                                                         int N, int K, int ksplit, int epilogue, uint32_t* err) {
   using C = RowsCfg<NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   pdl_trigger();
@@ -304,14 +307,15 @@ __global__ void __launch_bounds__(256, CTAS) i8_rows_kernel(const int8_t* __rest
   // weights and tokens of the round that starts at k0, as far as it lies before k_end
   auto fetch_w = [&](uint4 (&w)[2], int k0) {
     const int k = k0 + 64 * quarter;
-    w[0] = k < k_end ? __ldg(reinterpret_cast<const uint4*>(wa + k)) : zero;
-    w[1] = k < k_end ? __ldg(reinterpret_cast<const uint4*>(wb + k)) : zero;
+    const bool in = k < k_end && in_bounds(n0 + kRowsChannels <= N && k >= 0 && k + 64 <= K, err, 100);
+    w[0] = in ? __ldg(reinterpret_cast<const uint4*>(wa + k)) : zero;
+    w[1] = in ? __ldg(reinterpret_cast<const uint4*>(wb + k)) : zero;
   };
   auto fetch_x = [&](uint4 (&x)[C::XN], int k0) {
 #pragma unroll
     for (int i = 0; i < C::XN; ++i) {
       const int at = threadIdx.x + 256 * i, tok = at / (kRowsK / 16), kk = k0 + at % (kRowsK / 16) * 16;
-      x[i] = tok < M && kk < k_end ? *reinterpret_cast<const uint4*>(xq + static_cast<size_t>(tok) * K + kk) : zero;
+      x[i] = tok < M && kk < k_end && in_bounds(kk >= 0 && kk + 16 <= K, err, 101) ? *reinterpret_cast<const uint4*>(xq + static_cast<size_t>(tok) * K + kk) : zero;
     }
   };
   float acc[NT][4];
@@ -403,6 +407,7 @@ __global__ void __launch_bounds__(256, CTAS) i8_rows_kernel(const int8_t* __rest
     }
     float v = fmaf(a, __ldg(x_scale + tok) * ws, bn), unused = 0.0f;
     const size_t at = static_cast<size_t>(tok) * N + n;
+    if (!in_bounds(n < N, err, 102)) continue;
     if (epilogue == WENC_EPI_BIAS_RESID_F32) {
       static_cast<float*>(out)[at] = resid[at] + v;
     } else {
@@ -537,7 +542,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     }
     auto load = [&](uint4 (&b)[4], int ahead) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) b[i] = there[i >> 1] ? __ldg(reinterpret_cast<const uint4*>(src[i] + ahead * 64)) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < 4; ++i)
+        b[i] = there[i >> 1] && in_bounds(src[i] + ahead * 64 >= (is_w ? wq : xq) &&
+                                              src[i] + ahead * 64 + 16 <= (is_w ? wq + static_cast<size_t>(N) * K : xq + static_cast<size_t>(M) * K),
+                                          err, 103)
+                   ? __ldg(reinterpret_cast<const uint4*>(src[i] + ahead * 64))
+                   : make_uint4(0u, 0u, 0u, 0u);
     };
     const uint32_t row0 = s0 + (32 * (warp & 3) + tok) * 128, a0 = a_tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     uint32_t at[4];  // where the four 16-byte pieces of a token's 32 bytes go (swizzled)
@@ -634,7 +644,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
           const int t = t0 + e0 + e;
-          const bool in0 = t < m_here, in1 = t + 1 < m_here;
+          const bool in0 = t < m_here && in_bounds(m0 + t < M && n0 + ch < N, err, 104);
+          const bool in1 = t + 1 < m_here && in_bounds(m0 + t + 1 < M && n0 + ch < N, err, 104);
           float v0 = fmaf(__uint_as_float(acc[e0 + e]), (in0 ? __ldg(x_scale + m0 + t) : 0.0f) * ws, bn);
           float v1 = fmaf(__uint_as_float(acc[e0 + e + 1]), (in1 ? __ldg(x_scale + m0 + t + 1) : 0.0f) * ws, bn);
           const size_t at = at0 + static_cast<size_t>(e) * N;
@@ -690,6 +701,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         const float xs = __ldg(x_scale + m0 + t);
         float4 v = make_float4(fmaf(a.x, xs * ws.x, bn.x), fmaf(a.y, xs * ws.y, bn.y), fmaf(a.z, xs * ws.z, bn.z), fmaf(a.w, xs * ws.w, bn.w));
         const size_t at = static_cast<size_t>(m0 + t) * N + n0 + 4 * lane;
+        if (!in_bounds(m0 + t < M && n0 + 128 <= N, err, 104)) break;
         if (epilogue == WENC_EPI_BIAS_RESID_F32) {
           const float4 r = *reinterpret_cast<const float4*>(resid + at);
           *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(r.x + v.x, r.y + v.y, r.z + v.z, r.w + v.w);
@@ -823,19 +835,19 @@ cudaError_t launch_tc(int epilogue, const int8_t* xq, const float* x_scale, cons
 
 template <int NT, int AHEAD, int CTAS>
 cudaError_t launch_rows_as(int ksplit, int epilogue, const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
-                           const float* bias, const float* resid, void* out, int M, int N, int K, cudaStream_t stream) {
+                           const float* bias, const float* resid, void* out, int M, int N, int K, uint32_t* err, cudaStream_t stream) {
   using C = RowsCfg<NT>;
   static_assert(C::SMEM <= 48 * 1024, "no opt-in for more shared memory");
   static_assert(AHEAD % 2 == 0, "the tokens' buffers alternate with the rounds");
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cluster_config(cfg, attr, dim3(N / kRowsChannels * ksplit), 256, C::SMEM, ksplit, stream);
-  return cudaLaunchKernelEx(&cfg, i8_rows_kernel<NT, AHEAD, CTAS>, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, ksplit, epilogue);
+  return cudaLaunchKernelEx(&cfg, i8_rows_kernel<NT, AHEAD, CTAS>, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, ksplit, epilogue, err);
 }
 
 template <int NT>
 cudaError_t launch_rows(int epilogue, const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale, const float* bias,
-                        const float* resid, void* out, int M, int N, int K, int sms, cudaStream_t stream) {
+                        const float* resid, void* out, int M, int N, int K, int sms, uint32_t* err, cudaStream_t stream) {
   const int tiles = N / kRowsChannels;
   const int ksplit = pick_ksplit(tiles, K / 64, kRowsK / 64, sms);
   // More CTAs than two an SM: three are resident, and cover each other's latency. Else the loads under way have to: two
@@ -843,11 +855,11 @@ cudaError_t launch_rows(int epilogue, const int8_t* xq, const float* x_scale, co
   // tokens; three CTAs / two rounds / four): 51968 x 1280 15.6 17.8 23.8 and 22.2 27.4 27.9; 5120 x 5120 14.3 13.5 12.8
   // and 16.7 14.0 15.0; 5120 x 1280 4.5 4.1 3.7 and 5.6 4.7 4.8; 1536 x 384 2.07 2.07 2.23 and 2.6 2.75 2.7.
   if (tiles * ksplit > 2 * sms)
-    return launch_rows_as<NT, 2, 3>(ksplit, epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, stream);
+    return launch_rows_as<NT, 2, 3>(ksplit, epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, err, stream);
   if constexpr (NT == 1)
     if (K / ksplit >= 4 * kRowsK)
-      return launch_rows_as<NT, 4, 2>(ksplit, epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, stream);
-  return launch_rows_as<NT, 2, 2>(ksplit, epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, stream);
+      return launch_rows_as<NT, 4, 2>(ksplit, epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, err, stream);
+  return launch_rows_as<NT, 2, 2>(ksplit, epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, err, stream);
 }
 
 }  // namespace
@@ -867,8 +879,8 @@ extern "C" wenc_status wenc_quantize_rows(const void* x, int x_dtype, int8_t* xq
   const wenc_status dst = wenc_internal_device(&sms, &err);
   if (dst != WENC_OK) return dst;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = x_dtype == WENC_DTYPE_F32 ? quantize(static_cast<const float*>(x), xq, scale, rows, d, s)
-                                                  : quantize(static_cast<const __nv_bfloat16*>(x), xq, scale, rows, d, s);
+  const cudaError_t e = x_dtype == WENC_DTYPE_F32 ? quantize(static_cast<const float*>(x), xq, scale, rows, d, err, s)
+                                                  : quantize(static_cast<const __nv_bfloat16*>(x), xq, scale, rows, d, err, s);
   if (e != cudaSuccess) return launch_failed("quantize_rows launch", e);
   return WENC_OK;
 }
@@ -901,8 +913,8 @@ extern "C" wenc_status wenc_linear_i8(const int8_t* xq, const float* x_scale, co
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (M <= kRowsMost || on_chip(M, N, K, sms)) {
-    e = M <= 8           ? launch_rows<1>(epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, sms, s)
-        : M <= kRowsMost ? launch_rows<2>(epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, sms, s)
+    e = M <= 8           ? launch_rows<1>(epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, sms, err, s)
+        : M <= kRowsMost ? launch_rows<2>(epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, sms, err, s)
                          : launch_tc(epilogue, xq, x_scale, wq, w_scale, bias, resid, out, M, N, K, sms, err, s);
     if (e != cudaSuccess) return launch_failed("linear_i8 launch", e);
     return WENC_OK;

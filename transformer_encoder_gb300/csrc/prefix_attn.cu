@@ -181,7 +181,23 @@ struct SegTable {
   int len[kMaxOwn + 1];      // its keys
 };
 
+// What the index-checked build asks of every access (ptx.cuh): a token and head of the call, a sequence's table entry, a
+// slot of the pool, a key of the prefix, a slot of the partial results.
+__device__ __forceinline__ bool row_in(const PrefixParams& p, long long token, int head, uint32_t* err, uint32_t site) {
+  return in_bounds(token >= 0 && token < static_cast<long long>(p.n_seqs) * p.q_len && head >= 0 && head < p.H, err, site);
+}
+__device__ __forceinline__ bool entry_in(const PrefixParams& p, int seq, int page_i, uint32_t* err, uint32_t site) {
+  return in_bounds(seq >= 0 && seq < p.n_seqs && page_i >= 0 && page_i < p.max_pages, err, site);
+}
+__device__ __forceinline__ bool slot_in(const PrefixParams& p, int page, int slot, int hk, uint32_t* err, uint32_t site) {
+  return in_bounds(page >= 0 && page < p.n_pages && slot >= 0 && slot < p.page_size && hk >= 0 && hk < p.Hkv, err, site);
+}
+__device__ __forceinline__ bool key_in(const PrefixParams& p, int key, int hk, uint32_t* err, uint32_t site) {
+  return in_bounds(key >= 0 && key < p.prefix_max && hk >= 0 && hk < p.Hkv, err, site);
+}
+
 __device__ __forceinline__ int own_len_of(const PrefixParams& p, int seq, uint32_t* err) {
+  if (!in_bounds(seq >= 0 && seq < p.n_seqs, err, 83)) return 0;
   int n = p.lens[seq];
   if (n < 0 || n > static_cast<long long>(p.max_pages) * p.page_size) {
     *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (81u << 8);
@@ -274,7 +290,7 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
     if (!SOLO && lseg == 0) return;
     const int key = (step0 + j - lbegin) * KW + (lane & 15);
     const int pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-    next_page = key < lkeys ? p.table[(it.seq0 + lseg - 1) * p.table_stride + pi] : -1;
+    next_page = key < lkeys && entry_in(p, it.seq0 + lseg - 1, pi, err, 84) ? p.table[(it.seq0 + lseg - 1) * p.table_stride + pi] : -1;
   };
   auto load = [&](int j, int stage) {
     const uint32_t sk = s0 + stage * (2 * C::HALF), sv = sk + C::HALF;
@@ -284,7 +300,7 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
       const uint8_t* vs = it.vp + (key0 + lr) * p.v_token + lc * 16;
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        const bool ok = key0 + lr + i * RPI < lkeys;
+        const bool ok = key0 + lr + i * RPI < lkeys && key_in(p, key0 + lr + i * RPI, it.hk, err, 85);
         const uint32_t at = ((i & 1) ? at1 : at0) + i * 512;
         cp_async16(sk + at, ok ? ks : it.kp, ok);
         cp_async16(sv + at, ok ? vs : it.vp, ok);
@@ -296,7 +312,7 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
       const int pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
       const bool in = static_cast<uint32_t>(next_page) < static_cast<uint32_t>(p.n_pages);
       if (!in && key < lkeys) *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (80u << 8);
-      const int page = in ? next_page : -1;
+      const int page = in && slot_in(p, next_page, key - pi * p.page_size, it.hk, err, 86) ? next_page : -1;
       const uint32_t slot = (key - pi * p.page_size) * p.row16, head = it.hk * CH + lc;
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
@@ -326,7 +342,7 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
   for (int r = 0; r < NR; ++r) {
     const int x = it.row_off + 8 * r + g;
     const int tok = x / p.r;
-    const bool in = 8 * r + g < it.n_rows;
+    const bool in = 8 * r + g < it.n_rows && row_in(p, static_cast<long long>(it.seq0) * p.q_len + tok, it.hk * p.r + x - tok * p.r, err, 87);
     const uint8_t* q = p.q + (static_cast<long long>(it.seq0) * p.q_len + tok) * p.q_stride + (it.hk * p.r + x - tok * p.r) * C::ROWB;
     if constexpr (F32) {
       // k index tq (and tq + 4) of step 2j (and 2j + 1) stands for element 4 (tq + 4j) + 0, 1 (2, 3)
@@ -654,7 +670,7 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* x, float (&f)[8]) {
 // join, it cost 0.4 to 1.3.)
 template <typename T, bool SOLO>
 __device__ __noinline__ void redo_rows(const PrefixParams& p, const Item& it, const SegTable* seg, int solo_len, int step0, int n_steps,
-                                       int x, int c8, float (&v)[8], float& m, float& l) {
+                                       int x, int c8, float (&v)[8], float& m, float& l, uint32_t* err) {
   const bool in = x < it.n_rows, again = in && !(fabsf(l) < CUDART_INF_F);
   bool bad[8];
 #pragma unroll
@@ -668,7 +684,7 @@ __device__ __noinline__ void redo_rows(const PrefixParams& p, const Item& it, co
   }
   const int y = it.row_off + x, tok = y / p.r, per_seq = p.q_len * p.r, row_seq = y / per_seq, row_tok = (y - row_seq * per_seq) / p.r;
   float q[8] = {};
-  if (in) load8(reinterpret_cast<const T*>(p.q + (static_cast<long long>(it.seq0) * p.q_len + tok) * p.q_stride) + (it.hk * p.r + y - tok * p.r) * HD + c8, q);
+  if (in && row_in(p, static_cast<long long>(it.seq0) * p.q_len + tok, it.hk * p.r + y - tok * p.r, err, 88)) load8(reinterpret_cast<const T*>(p.q + (static_cast<long long>(it.seq0) * p.q_len + tok) * p.q_stride) + (it.hk * p.r + y - tok * p.r) * HD + c8, q);
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     if (p.q_keep == 0u) q[e] = 0.0f;
@@ -689,10 +705,13 @@ __device__ __noinline__ void redo_rows(const PrefixParams& p, const Item& it, co
       for (int key = (t - begin) * 16; key < last; ++key) {
         const uint8_t *k, *vr;
         if (sg == 0) {
+          if (!key_in(p, key, it.hk, err, 88)) continue;
           k = it.kp + key * p.k_token;
           vr = it.vp + key * p.v_token;
         } else {
-          const int pi = key / p.page_size, page = p.table[(it.seq0 + sg - 1) * p.table_stride + pi];
+          const int pi = key / p.page_size;
+          if (!entry_in(p, it.seq0 + sg - 1, pi, err, 88)) continue;
+          const int page = p.table[(it.seq0 + sg - 1) * p.table_stride + pi];
           if (page < 0 || page >= p.n_pages) continue;  // (reported when its step was loaded)
           const uint64_t at = static_cast<uint64_t>(key - pi * p.page_size) * p.row16 + it.hk * (HD * sizeof(T) / 16);
           k = p.k_pages + ((static_cast<uint64_t>(page) * p.k_page16 + at) << 4);
@@ -729,7 +748,7 @@ __device__ __noinline__ void redo_rows(const PrefixParams& p, const Item& it, co
 // The check, and rarely the call, with copies so that the values stay in registers otherwise. steps(): the steps.
 template <typename T, bool SOLO, class Steps>
 __device__ __forceinline__ void redo_if_needed(const PrefixParams& p, const Item& it, const SegTable* seg, int solo_len, const Steps& steps,
-                                               int x, int c8, float (&v)[8], float& m, float& l) {
+                                               int x, int c8, float (&v)[8], float& m, float& l, uint32_t* err) {
   float zero = l * 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) zero = fmaf(v[e], 0.0f, zero);
@@ -740,7 +759,7 @@ __device__ __forceinline__ void redo_if_needed(const PrefixParams& p, const Item
 #pragma unroll
   for (int e = 0; e < 8; ++e) vc[e] = v[e];
   steps(step0, n_steps);
-  redo_rows<T, SOLO>(p, item, seg, solo_len, step0, n_steps, x, c8, vc, mc, lc);
+  redo_rows<T, SOLO>(p, item, seg, solo_len, step0, n_steps, x, c8, vc, mc, lc, err);
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = vc[e];
   m = mc;
@@ -758,7 +777,8 @@ __device__ __forceinline__ void cta_run(int n, int first_part, int parts, int& f
 
 // Eight elements of an output row, normalised (a row without a visible key: zeros).
 template <typename T>
-__device__ __forceinline__ void write_out8(const PrefixParams& p, int token, int head, int c8, const float (&v)[8], float l) {
+__device__ __forceinline__ void write_out8(const PrefixParams& p, int token, int head, int c8, const float (&v)[8], float l, uint32_t* err) {
+  if (!row_in(p, token, head, err, 89)) return;
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;
   uint8_t* dst = p.out + static_cast<long long>(token) * p.out_stride + (head * HD + c8) * static_cast<int>(sizeof(T));
   if constexpr (sizeof(T) == 4) {
@@ -854,14 +874,14 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
   const int x = threadIdx.x >> 3, c8 = (threadIdx.x & 7) * 8;  // 8 threads a row, 8 elements each
   auto put = [&](int row, const float (&v)[8], float l) {
     const int y = it.row_off + row, tok = y / p.r;
-    write_out8<T>(p, it.seq0 * p.q_len + tok, it.hk * p.r + y - tok * p.r, c8, v, l);
+    write_out8<T>(p, it.seq0 * p.q_len + tok, it.hk * p.r + y - tok * p.r, c8, v, l, err);
   };
   float v[8], m, l;
   if (x < C::ROWS) {  // (whole warps)
     join_warps<T, NR>(smem_dyn, x, c8, v, m, l);
     redo_if_needed<T, false>(p, it, &seg, 0, [&](int& first, int& n) {
       cta_run<C::NW>(seg.step0[1 + it.n_own], rank * C::NW, p.cluster * C::NW, first, n);
-    }, x, c8, v, m, l);
+    }, x, c8, v, m, l, err);
   }
   if (p.cluster == 1) {
     if (x < it.n_rows) put(x, v, l);
@@ -908,7 +928,8 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
 }
 
 __device__ __forceinline__ void write_partial(const PrefixParams& p, int token, int head, int slot, int c8, const float (&v)[8],
-                                             float m, float l) {
+                                             float m, float l, uint32_t* err) {
+  if (!row_in(p, token, head, err, 90) || !in_bounds(slot >= 0 && slot < p.np + p.ns, err, 90)) return;
   const size_t at = (static_cast<size_t>(token) * p.H + head) * (p.np + p.ns) + slot;
   if (l != 0.0f) {  // (a NaN too: it has to reach the output)
     float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + c8);
@@ -955,10 +976,10 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
   float v[8], m, l;
   join_warps<T, NR>(smem_dyn, x, c8, v, m, l);
   redo_if_needed<T, false>(p, it, &seg, 0, [&](int& first, int& n) { cta_run<C::NW>(seg.step0[1], split * C::NW, p.np * C::NW, first, n); },
-                           x, c8, v, m, l);
+                           x, c8, v, m, l, err);
   if (x >= it.n_rows) return;
   const int y = row0 + x, tok = y / p.r;
-  write_partial(p, begin * p.q_len + tok, it.hk * p.r + y - tok * p.r, split, c8, v, m, l);
+  write_partial(p, begin * p.q_len + tok, it.hk * p.r + y - tok * p.r, split, c8, v, m, l, err);
 }
 
 // (256 sequences x 4 key heads, up to 600 own keys in pages of 64: 20 us for 78 MB; a CTA per item with its warps
@@ -1018,15 +1039,15 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = so[x * C::OS + c8 + e];
       redo_if_needed<T, true>(p, it, nullptr, len, [&](int& first, int& n) { run_of((len + 15) / 16, split, p.ns, first, n); },
-                              8 * r + x, c8, v, m, l);
-      if (8 * r + x < it.n_rows) write_partial(p, it.seq0 * p.q_len + tok, it.hk * p.r + y - tok * p.r, p.np + split, c8, v, m, l);
+                              8 * r + x, c8, v, m, l, err);
+      if (8 * r + x < it.n_rows) write_partial(p, it.seq0 * p.q_len + tok, it.hk * p.r + y - tok * p.r, p.np + split, c8, v, m, l, err);
     }
   }
 }
 
 // Join of the partial results of one (token, head): sixteen lanes, four elements each.
 template <typename T>
-__global__ void __launch_bounds__(256) prefix_join_kernel(const PrefixParams p) {
+__global__ void __launch_bounds__(256) prefix_join_kernel(const PrefixParams p, uint32_t* err) {
   pdl_trigger();
   pdl_wait();
   const long long pair = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 4;
@@ -1091,6 +1112,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PrefixParams p) 
     }
   }
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+  if (!row_in(p, token, head, err, 91)) return;
   uint8_t* dst = p.out + token * p.out_stride + (head * HD + c4 * 4) * sizeof(T);
   if constexpr (sizeof(T) == 4)
     *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
@@ -1411,7 +1433,7 @@ cudaError_t launch_all(PrefixParams p, const Plan& pl, uint32_t* err, cudaStream
   if (e != cudaSuccess) return e;
   const long long threads = static_cast<long long>(p.n_seqs) * p.q_len * p.H * 16;
   return wenc_host::launch_pdl(prefix_join_kernel<T>, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0,
-                               stream, p);
+                               stream, p, err);
 }
 
 }  // namespace

@@ -225,6 +225,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Item it = decode(w);
         if (it.n_kv == 0) continue;
         const int qb = qi & 1;
+        if (!in_bounds(it.token0 >= 0 && it.token0 < p.n_seqs * p.q_len && it.hk < p.Hkv && it.split < p.np &&
+                           (it.kv0 + it.n_kv - 1) * BKV < it.len && it.len <= p.prefix_max,
+                       err, 93)) {
+          *abort_flag = 1u;  // an item outside the problem: stop as a failed wait would
+          break;
+        }
         if (!mbar_wait(q_empty(qb), ((qi >> 1) & 1) ^ 1u, wc, 9)) break;
         mbar_arrive_expect_tx(q_full(qb), 2 * q_bytes);
         tma_load_3d(sQ + qb * 2 * Q_BYTES, &tq, q_full(qb), 0, it.hk * p.r, it.token0);
@@ -332,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g_turn = 0;  // the first key tile whose turn operations have not run
     const int tok = row / p.r, hr = row - tok * p.r;  // token of the tile and head of the group this row holds
     const float scale_log2 = p.scale_log2;
+    const size_t n_parts = static_cast<size_t>(p.n_seqs) * p.q_len * p.H * p.n_slots;  // (for the index checks)
     for (int w = blockIdx.x; ok && w < p.n_items; w += gridDim.x) {
       const Item it = decode(w);
       const int n_kv = it.n_kv;
@@ -339,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (size_t: rows x slots x 64 floats pass 2^32 bytes)
       const size_t pi = (static_cast<size_t>(it.token0 + t * p.tokens + tok) * p.H + it.hk * p.r + hr) * p.n_slots + it.split;
       if (n_kv == 0) {
-        if (mine) p.part_ml[pi] = make_float2(-CUDART_INF_F, 0.0f);
+        if (mine && in_bounds(pi < n_parts, err, 92)) p.part_ml[pi] = make_float2(-CUDART_INF_F, 0.0f);
         continue;
       }
       float m = -CUDART_INF_F;  // running maximum, in units of scale_log2
@@ -470,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t o[32];
           tmem_ld_32x32b_x32(tO(t) + lane_off + half * 32, o);
           tmem_ld_wait();
-          if (mine) {
+          if (mine && in_bounds(pi < n_parts, err, 92)) {
             float4* d4 = reinterpret_cast<float4*>(p.part_o + pi * HD + half * 32);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
@@ -478,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
           }
         }
-        if (mine) p.part_ml[pi] = make_float2(m, l);
+        if (mine && in_bounds(pi < n_parts, err, 92)) p.part_ml[pi] = make_float2(m, l);
         tc_fence_before();
       }
     }

@@ -212,7 +212,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc32_kernel(const wenc_hos
       const float4* src = reinterpret_cast<const float4*>(p.q + (token0 + tok) * p.q_stride + (hk * p.r + hr) * (HD * 4));
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float4 v = mine ? src[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 v = mine && in_bounds(token0 + tok < static_cast<long long>(p.n_seqs) * p.q_len && hk * p.r + hr < p.H, err, 94)
+                             ? src[i]
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
         const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) q[4 * i + e] = __uint_as_float((__float_as_uint(f[e]) & p.q_keep) ^ p.q_flip);
@@ -317,8 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc32_kernel(const wenc_hos
     named_sync(1, 256);
     const float m1 = take[32 * BQ], l1 = take[33 * BQ], mm = fmaxf(m, m1), u = mm == -CUDART_INF_F ? 0.0f : mm;
     const float f0 = ex2_approx(m - u), f1 = ex2_approx(m1 - u);
-    if (ok && mine && !*abort_flag) {
-      const size_t at = (static_cast<size_t>(token0 + tok) * p.H + hk * p.r + hr) * p.n_slots + split;
+    const size_t at = (static_cast<size_t>(token0 + tok) * p.H + hk * p.r + hr) * p.n_slots + split;
+    if (ok && mine && !*abort_flag && in_bounds(at < static_cast<size_t>(p.n_seqs) * p.q_len * p.H * p.n_slots, err, 95)) {
       if (n_kv > 0) {
         float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + 32 * b);
 #pragma unroll
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc32_kernel(const wenc_hos
     const uint8_t* vp = p.vp + grp * p.v_group + hk * (HD * 4) + c * 32 + key * p.v_token;
     float4 v[8][2];  // four rows of K, four of V
     auto load = [&](int i) {
-      const bool in = key + 4 * (i & 3) < len;  // rows behind the prefix are zeros, whatever memory holds there
+      const bool in = key + 4 * (i & 3) < len && in_bounds(key >= 0 && key + 4 * (i & 3) < p.prefix_max && hk < p.Hkv, err, 96);  // rows behind the prefix are zeros, whatever memory holds there
       const float4* src = reinterpret_cast<const float4*>(i < 4 ? kp + 4 * i * p.k_token : vp + 4 * (i - 4) * p.v_token);
 #pragma unroll
       for (int h = 0; h < 2; ++h) v[i][h] = in ? __ldg(src + h) : make_float4(0.f, 0.f, 0.f, 0.f);
