@@ -44,26 +44,6 @@ namespace {
 
 using namespace wenc_dev;
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, kind::f16 with bf16 operands; A = 128 lanes x 8 columns, each
-// 32-bit column holding two consecutive K elements (the lower one in the low half).
-// Hardware named barriers (ids 1 and 2; __syncthreads uses 0): `count` threads in whole warps.
-__device__ __forceinline__ void named_sync(int id, int count) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-__device__ __forceinline__ void named_arrive(int id, int count) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 constexpr int BQ = wenc_host::kAttnBQ;    // query rows per tile (two tiles per CTA)
 constexpr int BKV = wenc_host::kAttnBKV;  // keys per tile
 constexpr int HD = 64;
@@ -565,19 +545,12 @@ cudaError_t launch_attention_main(const CUtensorMap& tq, const CUtensorMap& tk, 
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  // Shared-memory opt-in, once per device (a repeat by a racing host thread is harmless).
-  static std::atomic<int> configured_device{-1};
-  if (configured_device.load(std::memory_order_acquire) != dev) {
-    e = cudaFuncSetAttribute(attn_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM));
-    if (e != cudaSuccess) return e;
-    configured_device.store(dev, std::memory_order_release);
-  }
-  // The softmax warpgroups' register increase is met only from the registers the CTA was
-  // launched with: refuse to launch a build that was given fewer (a property of the build).
-  static const int launch_regs = [] {
-    cudaFuncAttributes fa;
-    return cudaFuncGetAttributes(&fa, attn_fwd_kernel) == cudaSuccess ? fa.numRegs : 0;
-  }();
+  static std::atomic<int> configured{-1};
+  e = opt_in_smem(attn_fwd_kernel, SMEM, dev, configured);
+  if (e != cudaSuccess) return e;
+  // The softmax warpgroups' register increase is met only from the registers the CTA was launched with: refuse to
+  // launch a build that was given fewer (a property of the build).
+  static const int launch_regs = registers_of(attn_fwd_kernel);
   if (launch_regs * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
   int num_sms = 0;
   e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);

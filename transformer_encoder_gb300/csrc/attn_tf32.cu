@@ -447,13 +447,9 @@ cudaError_t launch_attention_tf32(const CUtensorMap& tq, const CUtensorMap& tk, 
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  // Shared-memory opt-in, once per device (a repeat by a racing host thread is harmless).
-  static std::atomic<int> configured_device{-1};
-  if (configured_device.load(std::memory_order_acquire) != dev) {
-    e = cudaFuncSetAttribute(attn_tf32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM));
-    if (e != cudaSuccess) return e;
-    configured_device.store(dev, std::memory_order_release);
-  }
+  static std::atomic<int> configured{-1};
+  e = opt_in_smem(attn_tf32_kernel, SMEM, dev, configured);
+  if (e != cudaSuccess) return e;
   int num_sms = 0;
   e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;

@@ -244,14 +244,9 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void cluster_arrive_wait() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ float ld_rank_f32(uint32_t saddr, int rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(rank_addr(saddr, rank)) : "memory");
   return v;
 }
 
@@ -469,16 +464,6 @@ __device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ float4 ld_rank_f4(uint32_t saddr, int rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(r) : "memory");
-  return v;
-}
 
 __global__ void __launch_bounds__(kTcThreads, 2)
     i8_tc_kernel(const int8_t* __restrict__ xq, const float* __restrict__ x_scale, const int8_t* __restrict__ wq,
@@ -695,7 +680,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int r = 0; r < ksplit; ++r) {
-          const float4 v = ld_rank_f4(part + t * 512, r);
+          const float4 v = ld_cluster_f4(rank_addr(part + t * 512, r));
           a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
         }
         const float xs = __ldg(x_scale + m0 + t);
@@ -818,13 +803,9 @@ cudaError_t launch_tc(int epilogue, const int8_t* xq, const float* x_scale, cons
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  // Shared-memory opt-in, once per device (a repeat by a racing host thread is harmless).
-  static std::atomic<int> configured_device{-1};
-  if (configured_device.load(std::memory_order_acquire) != dev) {
-    e = cudaFuncSetAttribute(i8_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTcSmem));
-    if (e != cudaSuccess) return e;
-    configured_device.store(dev, std::memory_order_release);
-  }
+  static std::atomic<int> configured{-1};
+  e = wenc_host::opt_in_smem(i8_tc_kernel, kTcSmem, dev, configured);
+  if (e != cudaSuccess) return e;
   const int m_tiles = (M + kTcTok - 1) / kTcTok;
   const int ksplit = pick_ksplit(static_cast<long long>(N / 128) * m_tiles, K / 64, 2, sms);
   cudaLaunchConfig_t cfg = {};

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
 #include <utility>
 
@@ -26,6 +27,22 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Shared-memory opt-in of a kernel, once per device: `configured` holds the device it was last made on (a repeat by
+// a racing host thread is harmless).
+template <typename K>
+inline cudaError_t opt_in_smem(K kernel, size_t smem, int dev, std::atomic<int>& configured) {
+  if (configured.load(std::memory_order_acquire) == dev) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess) configured.store(dev, std::memory_order_release);
+  return e;
+}
+// Registers a thread that a kernel is launched with (0: unknown).
+template <typename K>
+inline int registers_of(K kernel) {
+  cudaFuncAttributes fa;
+  return cudaFuncGetAttributes(&fa, kernel) == cudaSuccess ? fa.numRegs : 0;
 }
 
 // Tensor-map construction (cuTensorMapEncodeTiled through the runtime's driver entry

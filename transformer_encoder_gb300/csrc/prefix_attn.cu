@@ -816,22 +816,6 @@ __device__ __forceinline__ int prefix_len_of(const PrefixParams& p, int grp, uin
   return n;
 }
 
-__device__ __forceinline__ void cluster_arrive_wait() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t rank_addr(uint32_t saddr, int rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
 __device__ __forceinline__ float2 ld_cluster_f2(uint32_t a) {
   float2 v;
   asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
@@ -1279,18 +1263,11 @@ bool check_sizes(const wenc_prefix_attention_args* a, wenc_status* st) {
   return true;
 }
 
-// Shared-memory opt-in, once per device and kernel (a repeat by a racing host thread is harmless).
 template <typename K>
-cudaError_t opt_in(K kern, uint32_t smem, std::atomic<int>& configured_device) {
+cudaError_t opt_in(K kern, uint32_t smem, std::atomic<int>& configured) {
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (configured_device.load(std::memory_order_acquire) != dev) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    configured_device.store(dev, std::memory_order_release);
-  }
-  return cudaSuccess;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : wenc_host::opt_in_smem(kern, smem, dev, configured);
 }
 
 template <typename T, int NR>

@@ -35,27 +35,6 @@ namespace {
 
 using namespace wenc_dev;
 
-// Hardware named barriers (ids 1 and 2; __syncthreads uses 0): `count` threads in whole warps.
-__device__ __forceinline__ void named_sync(int id, int count) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-__device__ __forceinline__ void named_arrive(int id, int count) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 constexpr int BQ = 128;    // query rows per tile (two tiles per CTA)
 constexpr int BKV = 128;  // keys per tile
 constexpr int HD = 64;
@@ -520,19 +499,12 @@ cudaError_t launch_prefix_tc(const CUtensorMap& tq, const CUtensorMap& tk, const
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  // Shared-memory opt-in, once per device (a repeat by a racing host thread is harmless).
-  static std::atomic<int> configured_device{-1};
-  if (configured_device.load(std::memory_order_acquire) != dev) {
-    e = cudaFuncSetAttribute(prefix_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM));
-    if (e != cudaSuccess) return e;
-    configured_device.store(dev, std::memory_order_release);
-  }
-  // The softmax warpgroups' register increase is met only from the registers the CTA was
-  // launched with: refuse to launch a build that was given fewer (a property of the build).
-  static const int launch_regs = [] {
-    cudaFuncAttributes fa;
-    return cudaFuncGetAttributes(&fa, prefix_tc_kernel) == cudaSuccess ? fa.numRegs : 0;
-  }();
+  static std::atomic<int> configured{-1};
+  e = opt_in_smem(prefix_tc_kernel, SMEM, dev, configured);
+  if (e != cudaSuccess) return e;
+  // The softmax warpgroups' register increase is met only from the registers the CTA was launched with: refuse to
+  // launch a build that was given fewer (a property of the build).
+  static const int launch_regs = registers_of(prefix_tc_kernel);
   if (launch_regs * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
   const int grid = p.n_items < num_sms ? p.n_items : num_sms;
   return launch_pdl(prefix_tc_kernel, dim3(grid), dim3(kThreads), SMEM, stream, tq, tk, tv, p, err);

@@ -62,21 +62,6 @@ static_assert(SMEM <= 232448, "shared memory of the fp32 prefix kernel");
 constexpr uint32_t TMEM_COLS = 512;  // per softmax warpgroup S (64), O (64) and P (3 parts of 32); Q's first two parts (32 each)
 constexpr float kRescaleThreshold = 8.0f;  // as in attn.cu: p <= 2^8, and rows are rescaled rarely
 
-__device__ __forceinline__ void named_sync(int id, int count) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
 // The leading eight bits of x and y as a pair of bf16 numbers; x and y keep the rest (exact).
 __device__ __forceinline__ uint32_t cut_pair(float& x, float& y) {
   const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
@@ -451,19 +436,12 @@ cudaError_t launch_prefix_tc32(const PrefixTc32Args& p, uint32_t* err, cudaStrea
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  // Shared-memory opt-in, once per device (a repeat by a racing host thread is harmless).
-  static std::atomic<int> configured_device{-1};
-  if (configured_device.load(std::memory_order_acquire) != dev) {
-    e = cudaFuncSetAttribute(prefix_tc32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM));
-    if (e != cudaSuccess) return e;
-    configured_device.store(dev, std::memory_order_release);
-  }
+  static std::atomic<int> configured{-1};
+  e = opt_in_smem(prefix_tc32_kernel, SMEM, dev, configured);
+  if (e != cudaSuccess) return e;
   // The softmax warpgroups' register increase is met only from the registers the CTA was launched with: refuse to
   // launch a build that was given fewer (a property of the build).
-  static const int launch_regs = [] {
-    cudaFuncAttributes fa;
-    return cudaFuncGetAttributes(&fa, prefix_tc32_kernel) == cudaSuccess ? fa.numRegs : 0;
-  }();
+  static const int launch_regs = registers_of(prefix_tc32_kernel);
   if (launch_regs * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
   return launch_pdl(prefix_tc32_kernel, dim3(p.n_items), dim3(kThreads), SMEM, stream, p, err);
 }
