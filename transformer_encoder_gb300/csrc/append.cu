@@ -24,8 +24,8 @@
 // lane a token, and so are the run's angles; then the rows stream, and every lane keeps the angles of its
 // own 16-byte piece in registers for all of a token's heads.
 // Measured (us on the device in a captured graph; bytes at the measured copy rate in brackets): 27465 tokens of 16
-// prompts, 20 + 2 x 4 heads, bf16, rotated: 40.2 [29.0], 4.9 TB/s of reads and writes, where a library copy of the
-// same 98 MB takes 66 and the call without rotation 38; 1300 tokens of 80 sequences, fp32: 8.1 [2.6]; one token 3.5, of
+// prompts, 20 + 2 x 4 heads, bf16, rotated: 39.1 [29.0], 5.0 TB/s of reads and writes, where a library copy of the
+// same 98 MB takes 66 and the call without rotation 38; 1300 tokens of 80 sequences, fp32: 7.9 [2.6]; one token 3.4, of
 // which a launch is most. One token at a time with its lookups in a chain, and pairs exchanged by shuffles: 50.5,
 // 9.9 and 4.1. Three blocks an SM beat four (43.6: the two pieces of two rows spill) and two (47.7).
 #include <cuda_bf16.h>

@@ -35,9 +35,9 @@
 // Measured (us on the device, calls of a captured graph over inputs that do not fit L2 together; bytes of K
 // and V at the measured copy rate in brackets):
 //   16 windows x 5 beams, 20 heads, 1500 cross keys, bf16     22.8 [18.2]   5.4 TB/s
-//   the same beams' self-attention, ragged, pages of 16       15.9 [7.0]
+//   the same beams' self-attention, ragged, pages of 16       16.0 [7.0]
 //   4 windows x 5 beams x 3 tokens, 8 heads, fp32, pages of 24 12.5 [3.8]
-//   1 window, 1 beam, 6 heads, 1500 keys, bf16                 4.9 [0.3]: launch and latency
+//   1 window, 1 beam, 6 heads, 1500 keys, bf16                 5.3 [0.3]: launch and latency
 // What the choices gave, on the first of these unless said: rows as the MMA's M, tiles of 128 keys by four warps 29.5;
 // four CTAs a cluster for more CTAs 40.2, one CTA an item and three an SM 23.7 (the CTAs of one round hide each
 // other's latency; more of them only repeat the start of a CTA, some 4 us); S^T with eight warps 22.3. On the
@@ -967,7 +967,7 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
 }
 
 // (256 sequences x 4 key heads, up to 600 own keys in pages of 64: 20 us for 78 MB; a CTA per item with its warps
-// joined was as fast alone but left twice the idle warps behind short sequences, 43.5 against 44.9 us for the call.)
+// joined was as fast alone but left twice the idle warps behind short sequences, 43.5 against 44.9 us for the call as it then was.)
 // Second form, own keys: one warp per (sequence, key head, row tile, split); its rows go through the
 // warp's stretch of shared memory to full lines of the partial results.
 template <typename T, int NR>
@@ -1142,8 +1142,9 @@ int split_rounds(long long items, long long tiles, long long start, int sms) {
   }
   return np;
 }
-// In key tiles of 128 (prefix_tc.cu: with 1 tile 4 groups x 400 rows of 4 key heads over 2000 keys take 44.8 us, with 2 37.2;
-// with 3 16 groups x 20 heads x 128 rows over 1500 take 55.8, with 2 52.9) and of 64 (prefix_tc32.cu: 3 to 10 are alike).
+// In key tiles of 128 (prefix_tc.cu: 1 to 4 are alike for 4 groups x 400 rows of 4 key heads over 2000 keys, 17.2 us, and for 16 groups
+// x 20 heads x 128 rows over 1500, 82; with 96 rows 1 and 2 take 77, 3 and 4 78.5) and of 64 (prefix_tc32.cu: 3 to 10 are
+// alike).
 constexpr int kTcStart = 2, kTc32Start = 6;
 
 Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
@@ -1159,10 +1160,10 @@ Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
   pl.nr_p = row_groups(rows);
   pl.rows_p = static_cast<int>((rows + 8 * pl.nr_p - 1) / (8 * pl.nr_p));
   // The one-launch form up to 64 rows; with more, while its CTAs fit one round of the machine and the prefix is little
-  // work (2^22 pairs of a row and a key; fp32, whose products run as three here, 3 * 2^18). Measured around it (us, one launch / joined): 8 key heads x 256 rows over 2000
-  // keys (4.1 M pairs) 25.0 / 27.9, 512 rows (8.2 M) 41.0 / 42.3, 128 rows over 500 13.2 / 16.9; 4 x 128 over 8000 (4.1 M)
-  // 22.6 / 22.4, 4 x 192 (6.1 M) 37.4 / 28.3; 2 windows x 20 heads x 128 rows over 1500 (320 CTAs) 61.2 / 44.1; 16 windows
-  // x 20 heads x 96 rows 96.4 / 55.6. fp32: 2 key heads x 200 rows over 1500 (0.6 M) 9.5 / 13.9, 8 x 100 over 1000 (0.8 M)
+  // work (2^22 pairs of a row and a key; fp32, whose products run as three here, 3 * 2^18). Measured around it (us, one launch / joined; bf16 without own keys): 8 key heads x 256
+  // rows over 2000 keys (4.1 M pairs) 13.7 / 14.9, 384 rows (6.1 M) 20.1 / 14.6, 128 rows over 500 7.1 / 8.6; 4 x 128 over 8000
+  // (4.1 M) 14.1 / 13.4, 4 x 160 (5.1 M) 21.5 / 13.8; 20 x 150 over 1500 (4.5 M) 16.3 / 13.8; 2 windows x 20 heads x 128 rows over
+  // 1500 (320 CTAs) 25.4 / 16.2; 16 windows x 20 heads x 96 rows 99.3 / 77.0. fp32: 2 key heads x 200 rows over 1500 (0.6 M) 9.5 / 13.9, 8 x 100 over 1000 (0.8 M)
   // 14.9 / 12.9, 2 x 6 heads x 224 over 671 with own keys (1.8 M) 39.1 / 28.4, 8 x 100 over 3000 (2.4 M) 25.8 / 14.8.
   const long long items = n_groups * a->n_kv_heads * pl.rows_p;
   // (fp32 waits on its own instructions: more CTAs than are resident at once still gain, 21.0 against 24.4 us for 4
