@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <climits>
 #include <cstdlib>
 #include <cstdarg>
 #include <cstdio>
@@ -1176,6 +1177,7 @@ wenc_status wenc_selftest_attention_abort(const uint16_t* q, const uint16_t* k, 
 }
 
 int wenc_selftest_append_sequence(const int32_t* seq_start, int n_seqs, int n_tokens, int first, int t, int* left) {
+  if (!seq_start || !left || n_seqs < 1 || n_seqs == INT_MAX) return -1;
   const int s = wenc_dev::last_start(n_seqs + 1, [&](int lo, int step, int len) {
     int n = 0;
     for (int i = 0; i < 32; ++i)
@@ -1186,12 +1188,13 @@ int wenc_selftest_append_sequence(const int32_t* seq_start, int n_seqs, int n_to
 }
 
 void wenc_selftest_append_angle(float inv_freq, int position, float* h, float* l) {
+  if (!h || !l) return;
   wenc_dev::angle_parts(position, wenc_dev::turns64(inv_freq), *h, *l);
 }
 
 void wenc_selftest_attention_runs(int prefix_len, const int32_t* own, int n_own, int parts, int32_t* seen) {
   constexpr int kMost = 16;  // sequences of a tile of 16 rows
-  if (n_own < 0 || n_own > kMost || parts < 1) return;
+  if (!seen || (!own && n_own > 0) || prefix_len < 0 || n_own < 0 || n_own > kMost || parts < 1) return;
   int step0[kMost + 2] = {0, (prefix_len + 15) / 16}, at[kMost + 2] = {0, prefix_len};  // a segment's first step, and key of `seen`
   for (int i = 0; i < n_own; ++i) {
     step0[i + 2] = step0[i + 1] + (own[i] + 15) / 16;

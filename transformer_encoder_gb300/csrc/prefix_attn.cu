@@ -290,7 +290,8 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
     if (!SOLO && lseg == 0) return;
     const int key = (step0 + j - lbegin) * KW + (lane & 15);
     const int pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-    next_page = key < lkeys && entry_in(p, it.seq0 + lseg - 1, pi, err, 84) ? p.table[(it.seq0 + lseg - 1) * p.table_stride + pi] : -1;
+    const int seq = it.seq0 + lseg - 1;
+    next_page = key < lkeys && entry_in(p, seq, pi, err, 84) ? p.table[seq * p.table_stride + pi] : -1;
   };
   auto load = [&](int j, int stage) {
     const uint32_t sk = s0 + stage * (2 * C::HALF), sv = sk + C::HALF;
@@ -342,8 +343,10 @@ __device__ __forceinline__ void attend(const PrefixParams& p, const Item& it, ui
   for (int r = 0; r < NR; ++r) {
     const int x = it.row_off + 8 * r + g;
     const int tok = x / p.r;
-    const bool in = 8 * r + g < it.n_rows && row_in(p, static_cast<long long>(it.seq0) * p.q_len + tok, it.hk * p.r + x - tok * p.r, err, 87);
-    const uint8_t* q = p.q + (static_cast<long long>(it.seq0) * p.q_len + tok) * p.q_stride + (it.hk * p.r + x - tok * p.r) * C::ROWB;
+    const long long token = static_cast<long long>(it.seq0) * p.q_len + tok;
+    const int head = it.hk * p.r + x - tok * p.r;
+    const bool in = 8 * r + g < it.n_rows && row_in(p, token, head, err, 87);
+    const uint8_t* q = p.q + token * p.q_stride + head * C::ROWB;
     if constexpr (F32) {
       // k index tq (and tq + 4) of step 2j (and 2j + 1) stands for element 4 (tq + 4j) + 0, 1 (2, 3)
 #pragma unroll
@@ -662,12 +665,12 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* x, float (&f)[8]) {
 }
 
 // The products with V are formed for all of a tile's rows, with weights of 0 where a row does not see a key, and in
-// two parts; but 0 x inf and 0 x NaN are NaN, so a value that is no number would reach rows that do not see it. And the
-// TF32 part of a float32 next to the largest one is infinite. Such elements of a row's O, and all of a row whose sum is
-// no number (rare: they are found by that), are formed again here in plain fp32, from the keys alone that the row sees among
-// steps [step0, step0 + n_steps). Eight lanes hold a row: x, its elements c8 .. c8 + 7 in v, maximum m and sum l. (Looking
-// for them on the joined results of a CTA costs a call 0.1 to 0.2 us, the joined form 0.7; on each warp's own state, before the
-// join, it cost 0.4 to 1.3.)
+// two parts; but 0 x inf and 0 x NaN are NaN, so a value that is no number would reach rows that do not see it. And
+// the TF32 part of a float32 next to the largest one is infinite. Such elements of a row's O, and all of a row whose
+// sum is no number (rare: they are found by that), are formed again here in plain fp32, from the keys alone that the
+// row sees among steps [step0, step0 + n_steps). Eight lanes hold a row: x, its elements c8 .. c8 + 7 in v, maximum m
+// and sum l. (Looking for them on the joined results of a CTA costs a call 0.1 to 0.2 us, the joined form 0.7; on
+// each warp's own state, before the join, it cost 0.4 to 1.3.)
 template <typename T, bool SOLO>
 __device__ __noinline__ void redo_rows(const PrefixParams& p, const Item& it, const SegTable* seg, int solo_len, int step0, int n_steps,
                                        int x, int c8, float (&v)[8], float& m, float& l, uint32_t* err) {
@@ -683,8 +686,10 @@ __device__ __noinline__ void redo_rows(const PrefixParams& p, const Item& it, co
     l = 0.0f;
   }
   const int y = it.row_off + x, tok = y / p.r, per_seq = p.q_len * p.r, row_seq = y / per_seq, row_tok = (y - row_seq * per_seq) / p.r;
+  const long long token = static_cast<long long>(it.seq0) * p.q_len + tok;
+  const int head = it.hk * p.r + y - tok * p.r;
   float q[8] = {};
-  if (in && row_in(p, static_cast<long long>(it.seq0) * p.q_len + tok, it.hk * p.r + y - tok * p.r, err, 88)) load8(reinterpret_cast<const T*>(p.q + (static_cast<long long>(it.seq0) * p.q_len + tok) * p.q_stride) + (it.hk * p.r + y - tok * p.r) * HD + c8, q);
+  if (in && row_in(p, token, head, err, 88)) load8(reinterpret_cast<const T*>(p.q + token * p.q_stride) + head * HD + c8, q);
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     if (p.q_keep == 0u) q[e] = 0.0f;
@@ -967,7 +972,8 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, Cfg<T, NR>::CTAS) prefix_
 }
 
 // (256 sequences x 4 key heads, up to 600 own keys in pages of 64: 20 us for 78 MB; a CTA per item with its warps
-// joined was as fast alone but left twice the idle warps behind short sequences, 43.5 against 44.9 us for the call as it then was.)
+// joined was as fast alone but left twice the idle warps behind short sequences, 43.5 against 44.9 us for the call as
+// it then was.)
 // Second form, own keys: one warp per (sequence, key head, row tile, split); its rows go through the
 // warp's stretch of shared memory to full lines of the partial results.
 template <typename T, int NR>
@@ -1142,9 +1148,9 @@ int split_rounds(long long items, long long tiles, long long start, int sms) {
   }
   return np;
 }
-// In key tiles of 128 (prefix_tc.cu: 1 to 4 are alike for 4 groups x 400 rows of 4 key heads over 2000 keys, 17.2 us, and for 16 groups
-// x 20 heads x 128 rows over 1500, 82; with 96 rows 1 and 2 take 77, 3 and 4 78.5) and of 64 (prefix_tc32.cu: 3 to 10 are
-// alike).
+// In key tiles of 128 (prefix_tc.cu: 1 to 4 are alike for 4 groups x 400 rows of 4 key heads over 2000 keys, 17.2 us,
+// and for 16 groups x 20 heads x 128 rows over 1500, 82; with 96 rows 1 and 2 take 77, 3 and 4 78.5) and of 64
+// (prefix_tc32.cu: 3 to 10 are alike).
 constexpr int kTcStart = 2, kTc32Start = 6;
 
 Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
@@ -1159,12 +1165,14 @@ Plan make_plan(const wenc_prefix_attention_args* a, int sms) {
   const long long prefix = a->k_prefix ? a->prefix_max : 0;
   pl.nr_p = row_groups(rows);
   pl.rows_p = static_cast<int>((rows + 8 * pl.nr_p - 1) / (8 * pl.nr_p));
-  // The one-launch form up to 64 rows; with more, while its CTAs fit one round of the machine and the prefix is little
-  // work (2^22 pairs of a row and a key; fp32, whose products run as three here, 3 * 2^18). Measured around it (us, one launch / joined; bf16 without own keys): 8 key heads x 256
-  // rows over 2000 keys (4.1 M pairs) 13.7 / 14.9, 384 rows (6.1 M) 20.1 / 14.6, 128 rows over 500 7.1 / 8.6; 4 x 128 over 8000
-  // (4.1 M) 14.1 / 13.4, 4 x 160 (5.1 M) 21.5 / 13.8; 20 x 150 over 1500 (4.5 M) 16.3 / 13.8; 2 windows x 20 heads x 128 rows over
-  // 1500 (320 CTAs) 25.4 / 16.2; 16 windows x 20 heads x 96 rows 99.3 / 77.0. fp32: 2 key heads x 200 rows over 1500 (0.6 M) 9.5 / 13.9, 8 x 100 over 1000 (0.8 M)
-  // 14.9 / 12.9, 2 x 6 heads x 224 over 671 with own keys (1.8 M) 39.1 / 28.4, 8 x 100 over 3000 (2.4 M) 25.8 / 14.8.
+  // The one-launch form up to 64 rows; with more, while its CTAs fit one round of the machine and the prefix is
+  // little work (2^22 pairs of a row and a key; fp32, whose products run as three here, 3 * 2^18). Measured around it
+  // (us, one launch / joined; bf16 without own keys): 8 key heads x 256 rows over 2000 keys (4.1 M pairs) 13.7 /
+  // 14.9, 384 rows (6.1 M) 20.1 / 14.6, 128 rows over 500 7.1 / 8.6; 4 x 128 over 8000 (4.1 M) 14.1 / 13.4, 4 x 160
+  // (5.1 M) 21.5 / 13.8; 20 x 150 over 1500 (4.5 M) 16.3 / 13.8; 2 windows x 20 heads x 128 rows over 1500 (320 CTAs)
+  // 25.4 / 16.2; 16 windows x 20 heads x 96 rows 99.3 / 77.0. fp32: 2 key heads x 200 rows over 1500 (0.6 M) 9.5 /
+  // 13.9, 8 x 100 over 1000 (0.8 M) 14.9 / 12.9, 2 x 6 heads x 224 over 671 with own keys (1.8 M) 39.1 / 28.4, 8 x
+  // 100 over 3000 (2.4 M) 25.8 / 14.8.
   const long long items = n_groups * a->n_kv_heads * pl.rows_p;
   // (fp32 waits on its own instructions: more CTAs than are resident at once still gain, 21.0 against 24.4 us for 4
   // windows x 40 rows)

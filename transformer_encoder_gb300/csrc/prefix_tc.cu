@@ -19,12 +19,13 @@
 // row's result does not depend on how many others share its prefix. The large part is the A operand in TMEM, as in
 // attn.cu; the small one, for which TMEM has no columns left beside S and O, is one in shared memory. With the large
 // part alone the error of long prompts was 1.4 times that of rounding the output.
-// What bounds it: the softmax warps' instructions (the exponentials, 256 x 128 a key tile or 1.1 us of an SM, and five
-// for every two probabilities to cut them in two), and at this length the ends of a CTA's work: 1280 rows of each of 4
-// key heads over 8191 keys, 10.7 GFLOP, take 29.5 us cold (144 CTAs of 11 key tiles), with one part 22.7, and with the join 28.5 in a captured
-// graph. Of the difference the second product is 1 us: without it as many instructions remain. Subtractions by scalar (56.0 us for the call, as it is 51.6) or
-// fp32 += bf16 FMAs (55.8), parts cut off instead of rounded (52.0), and the parts formed behind the exponentials (56.6) cost
-// more. On mma.sync, with 64 rows a CTA, the same part took about 80 us.
+// What bounds it: the softmax warps' instructions (the exponentials, 256 x 128 a key tile or 1.1 us of an SM, and
+// five for every two probabilities to cut them in two), and at this length the ends of a CTA's work: 1280 rows of
+// each of 4 key heads over 8191 keys, 10.7 GFLOP, take 29.5 us cold (144 CTAs of 11 key tiles), with one part 22.7,
+// and with the join 28.5 in a captured graph. Of the difference the second product is 1 us: without it as many
+// instructions remain. Subtractions by scalar (56.0 us for the call, as it is 51.6) or fp32 += bf16 FMAs (55.8),
+// parts cut off instead of rounded (52.0), and the parts formed behind the exponentials (56.6) cost more. On
+// mma.sync, with 64 rows a CTA, the same part took about 80 us.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
