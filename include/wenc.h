@@ -380,7 +380,8 @@ typedef struct {
  * formed from three TF32 products each, or for many rows from six bf16 products. A NaN or an infinity
  * that a row does not see never reaches it; what it does see it takes as a plain evaluation would, except
  * that in calls with a workspace an infinite prefix value (float32: key, value or query) may turn the elements it
- * reaches to NaN. Sequences outside every group's range keep their rows of `out` as they were.
+ * reaches to NaN. Weighted values are summed before they are divided by the weights' sum, with weights of up to 2^8:
+ * values beyond 2^119 over the number of keys may leave fp32's range. Sequences outside every group's range keep their rows of `out` as they were.
  * A length, offset or page number out of range records WENC_ERR_INVALID_ARG in the device error
  * word (wenc_sync_status(NULL)); nothing out of range is accessed and the output rows it concerns are
  * undefined. The workspace belongs to the call until its work is done: calls that may overlap need
