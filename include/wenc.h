@@ -421,6 +421,129 @@ WENC_API wenc_status wenc_linear_i8(const int8_t* xq, const float* x_scale, cons
  * device. */
 WENC_API size_t wenc_linear_i8_workspace(int M, int N, int K);
 
+/* Arguments of wenc_chunk_attention. Strides in elements, multiples of 16 bytes; buffers 16-byte
+ * aligned device pointers owned by the caller. */
+typedef struct {
+  int dtype;                 /* wenc_dtype of q, out and the pages */
+  int n_tokens, n_seqs;      /* rows of q and out (0 is a no-op), and sequences */
+  int max_new;               /* at least the most tokens that one sequence brings, 1..n_tokens */
+  int n_heads, n_kv_heads;   /* n_heads a multiple of n_kv_heads: query head h reads key head
+                                h / (n_heads / n_kv_heads) */
+  int head_dim;              /* must be 64 */
+  const void* q;             /* [n_tokens][n_heads][64], tokens q_stride apart */
+  void* out;                 /* the same, tokens out_stride apart; apart from every input */
+  int64_t q_stride, out_stride;
+  const void* k_pages;       /* [n_pages][page_size][n_kv_heads][64], as written by wenc_kv_append */
+  const void* v_pages;
+  int64_t k_page_stride, v_page_stride;
+  int n_pages, page_size;
+  const int32_t* block_table; /* [n_seqs][max_pages], rows block_table_stride apart */
+  int64_t block_table_stride;
+  int max_pages;             /* max_pages * page_size <= 2^30 */
+  const int32_t* lens;       /* [n_seqs] cache length of each sequence, the call's tokens included */
+  const int32_t* seq_start;  /* [n_seqs + 1], ascending from 0: sequence s owns the rows seq_start[s] ..
+                                seq_start[s+1]-1; NULL: n_tokens / n_seqs rows each */
+  int window;                /* how many newest keys a token sees, its own among them; 0: all */
+  int sinks;                 /* with a window: how many first keys stay visible as well */
+  float scale;               /* of the scores; 0.125 = 64^-0.5 in Whisper */
+  void* workspace;           /* wenc_chunk_attention_workspace(args) bytes, 256-byte aligned */
+  size_t workspace_bytes;
+} wenc_chunk_attention_args;
+
+/* wenc_chunk_attention -- attention of chunks of new tokens over a paged cache (inferencelayer DEC_QATTN; oxinfer
+ * attention_masked): prompts, parts of them, drafts and single tokens in one call, each sequence with as many tokens
+ * as it brings. Token t of sequence s stands at position p = lens[s] - (seq_start[s+1] - t) and sees the keys
+ *   j <= p  with  j > p - window  or  j < sinks
+ * of its sequence: out = softmax(scale * q k^T) v over these, and zeros where there are none (p < 0). Rows behind
+ * seq_start[n_seqs] are neither read nor written. Keys that no token of a sequence sees are not read, so the pages that hold
+ * them alone may be gone (any entry in the table). Arithmetic as wenc_prefix_attention's: fp32 scores, statistics and
+ * sums, bf16 probabilities in two bf16 parts, float32 products from three TF32 ones each. A NaN or an infinity reaches
+ * exactly the rows that see it. A length, offset or page number out of range records
+ * WENC_ERR_INVALID_ARG in the device error word (wenc_sync_status(NULL)); nothing out of range is accessed and the output
+ * rows it concerns are undefined. The workspace belongs to the call until its work is done: calls that may
+ * overlap need one each. At most four launches, no allocation, stream-ordered; a stalled device wait is recorded as
+ * for wenc_attention. */
+WENC_API wenc_status wenc_chunk_attention(const wenc_chunk_attention_args* args, wenc_stream_t stream);
+
+/* wenc_chunk_attention_workspace -- bytes of workspace the call needs on the current device (0 for
+ * arguments it would refuse). Depends on the sizes, not on device data. */
+WENC_API size_t wenc_chunk_attention_workspace(const wenc_chunk_attention_args* args);
+
+/* Arguments of wenc_kv_extend: device pointers owned by the caller. */
+typedef struct {
+  int n_seqs;                /* sequences, 0..65536 */
+  int n_rows;                /* rows of positions and slots: at least the step's new tokens (the others are padding) */
+  const int32_t* new_tokens; /* [n_seqs] tokens each sequence gets in this step */
+  const int32_t* lens;       /* [n_seqs] cache lengths before them */
+  int32_t* block_table;      /* [n_seqs][max_pages], rows block_table_stride apart; new entries are written */
+  int64_t block_table_stride;
+  int max_pages, page_size;  /* max_pages * page_size <= 2^31 - 1 */
+  const int32_t* free_pages; /* [n_free_pages] the first *free_count are free; they are taken from the end */
+  int n_free_pages;
+  const int32_t* free_count; /* [1] */
+  int32_t* lens_out;         /* [n_seqs] lengths with the new tokens; apart from lens */
+  int32_t* free_count_out;   /* [1] pages that stay free; apart from free_count */
+  int32_t* seq_start;        /* [n_seqs + 1] row offsets, as wenc_kv_append and wenc_chunk_attention take them */
+  int32_t* positions;        /* [n_rows] each row's position, 0 for padding; 16-byte aligned */
+  int64_t* slots;            /* [n_rows] page * page_size + place of each row, -1 for padding; 16-byte aligned */
+} wenc_kv_extend_args;
+
+/* wenc_kv_extend -- the places of a step's new tokens in a paged cache, from lengths in device memory: pages taken from the free
+ * ones, block-table entries, row offsets, positions and slots (the pages have no counterpart: their caches grow by
+ * copying). Sequence s gets need = ceil((lens + new_tokens) / page_size) - ceil(lens / page_size) pages; entry i of these is
+ * free_pages[*free_count - 1 - (base + i)], base the pages that the sequences before s get. Where a length is
+ * negative or passes the table, the rows pass n_rows, or more pages are needed than are free, the call gives nothing to any sequence
+ * (lens_out and free_count_out as before, seq_start zeros, every row padding) and records
+ * WENC_ERR_INVALID_ARG in the device error word (wenc_sync_status(NULL)). A page number below 0, in the table or among the
+ * free ones, is reported too; its rows get slot -1. One launch, stream-ordered. */
+WENC_API wenc_status wenc_kv_extend(const wenc_kv_extend_args* args, wenc_stream_t stream);
+
+/* Arguments of wenc_kv_release: device pointers owned by the caller. */
+typedef struct {
+  int n_seqs;                /* sequences, 0..65536 */
+  const int32_t* lens;       /* [n_seqs] cache lengths */
+  const uint8_t* finished;   /* [n_seqs] not 0: the sequence gives all its pages back; NULL: none does */
+  const int32_t* block_table; /* [n_seqs][max_pages], rows block_table_stride apart */
+  int64_t block_table_stride;
+  int max_pages, page_size;  /* max_pages * page_size <= 2^31 - 1 */
+  int window, sinks;         /* as of wenc_chunk_attention; window 0: pages go back with their sequence alone */
+  const int32_t* trimmed;    /* with a window: [n_seqs] entries below it went back before, but for those that hold the
+                                first `sinks` keys */
+  int32_t* free_pages;       /* [n_free_pages]; what goes back is written from *free_count on */
+  int n_free_pages;
+  const int32_t* free_count; /* [1] */
+  int32_t* lens_out;         /* [n_seqs] 0 for finished sequences, else lens; apart from lens */
+  int32_t* free_count_out;   /* [1] apart from free_count */
+  int32_t* trimmed_out;      /* with a window: [n_seqs] the next call's trimmed; apart from trimmed */
+} wenc_kv_release_args;
+
+/* wenc_kv_release -- pages of a paged cache that no later token needs, back to the free ones: all pages of finished
+ * sequences, and with a window those whose keys the next token (at position lens) no longer sees. They are written behind the
+ * free pages in order of sequence and entry. The table keeps its entries: those given back must not be read
+ * any more (wenc_chunk_attention with the same window and sinks does not). Where a length or a mark is out of range, or the pages do not
+ * fit, the call gives nothing back (outputs as before) and records WENC_ERR_INVALID_ARG in the device error word
+ * (wenc_sync_status(NULL)); an entry below 0 among those given back is reported and passed on. One launch,
+ * stream-ordered. */
+WENC_API wenc_status wenc_kv_release(const wenc_kv_release_args* args, wenc_stream_t stream);
+
+/* wenc_linear_i4 -- wenc_linear on weights of 4 bits with a scale for each group of inputs (oxinfer make_lin's quantised
+ * forms, with groups):
+ *   out = epilogue(sum_g w_scale[n][g] sum_{k in g} (u[n][k] - 8) x[m][k] + bias[n]).
+ * x [M, K] in x_dtype (wenc_dtype); w [N, K / 2]: byte k / 2 of a row holds u[n][k], 0..15, for even k in its low half and for the
+ * odd k + 1 in its high half; w_scale [N, K / group] in scale_dtype (wenc_dtype); bias [N] float32. Epilogues as
+ * wenc_epilogue: the first two write x's type, the third adds resid [M, N] float32 and writes float32 (out may be resid).
+ * group 32, 64 or 128; N a multiple of 128, K of 128, 1 <= M <= 2^28; buffers 16-byte aligned. bf16
+ * products are exact, float32 x enters as three bf16 parts (exact together); sums are fp32, a group's before its scale.
+ * workspace: wenc_linear_i4_workspace(...) bytes, 256-byte aligned (may be NULL when that is 0); it belongs to the call until its
+ * work is done: calls that may overlap need one each. At most two launches; stream-ordered; errors as
+ * wenc_linear, and a stalled device wait is recorded as for wenc_attention. */
+WENC_API wenc_status wenc_linear_i4(const void* x, int x_dtype, const uint8_t* w, const void* w_scale, int scale_dtype,
+                                    const float* bias, const float* resid, void* out, int M, int N, int K, int group,
+                                    int epilogue, void* workspace, size_t workspace_bytes, wenc_stream_t stream);
+
+/* wenc_linear_i4_workspace -- bytes of workspace wenc_linear_i4 needs for these sizes on the current device. */
+WENC_API size_t wenc_linear_i4_workspace(int M, int N, int K, int x_dtype, int group);
+
 /* wenc_set_device_alloc_limit -- test hook for the out-of-memory path (the pages have no
  * counterpart). Caps the device memory the library holds in its handles' arenas (weights,
  * workspace, stem, cross K/V) at `bytes`; an allocation that would exceed the cap fails as if
@@ -486,9 +609,16 @@ WENC_API wenc_status wenc_selftest_gemm_schedule(int M, int N, int pair, int max
  * wenc_selftest_append_angle -- the angle position * inv_freq as pi * h + l modulo 2 pi, as the sine and cosine take it.
  * wenc_selftest_attention_runs -- adds to seen[k] how often the warps of wenc_prefix_attention's one-launch form, `parts` of
  *   them, score key k: the prefix's prefix_len keys first, then those of each of the n_own <= 16
- *   sequences. */
+ *   sequences.
+ * wenc_selftest_chunk_steps -- adds to seen[k] (n_keys numbers) how often the steps of `step` keys that wenc_chunk_attention
+ *   takes for tokens at positions first .. last load key k, and returns the steps; -1 where one leads outside the array.
+ *   The steps behind the first tokens' start at a multiple of align.
+ * wenc_selftest_gives -- the block-table entries that wenc_kv_release gives back for a sequence: two ranges, and the mark that
+ *   follows `gone`, as five numbers. */
 WENC_API int wenc_selftest_append_sequence(const int32_t* seq_start, int n_seqs, int n_tokens, int first, int t, int* left);
 WENC_API void wenc_selftest_append_angle(float inv_freq, int position, float* h, float* l);
+WENC_API int wenc_selftest_chunk_steps(int first, int last, int window, int sinks, int step, int align, int32_t* seen, int n_keys);
+WENC_API void wenc_selftest_gives(int len, int finished, int gone, int window, int sinks, int page_size, int32_t* out);
 WENC_API void wenc_selftest_attention_runs(int prefix_len, const int32_t* own, int n_own, int parts, int32_t* seen);
 
 /* wenc_sync_status -- synchronise the device and read the device error word of `h`

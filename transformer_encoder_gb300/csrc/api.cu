@@ -1210,6 +1210,28 @@ void wenc_selftest_attention_runs(int prefix_len, const int32_t* own, int n_own,
   }
 }
 
+int wenc_selftest_chunk_steps(int first, int last, int window, int sinks, int step, int align, int32_t* seen, int n_keys) {
+  if (!seen || window < 0 || sinks < 0 || step < 1 || align < 1 || first > last || n_keys < 0) return -1;
+  const int most = 1 << 30;
+  const wenc_dev::KeySteps ks(first, last, window > 0 && window < most ? window : most, window > 0 ? sinks : 0, step, align);
+  for (int t = 0; t < ks.n; ++t)
+    for (int key = ks.key0(t, step), end = key + step; key < end; ++key) {
+      if (!ks.seen(key)) continue;
+      if (key < 0 || key >= n_keys) return -1;
+      ++seen[key];
+    }
+  return ks.n;
+}
+
+void wenc_selftest_gives(int len, int finished, int gone, int window, int sinks, int page_size, int32_t* out) {
+  if (!out || len < 0 || gone < 0 || window < 0 || sinks < 0 || page_size < 1) return;
+  int mark;
+  const int4 x = wenc_dev::gives(len, finished != 0, gone, window, window > 0 ? static_cast<int>(wenc_dev::pages_of(sinks, page_size)) : 0,
+                                 page_size, mark);
+  const int v[5] = {x.x, x.y, x.z, x.w, mark};
+  for (int i = 0; i < 5; ++i) out[i] = v[i];
+}
+
 wenc_status wenc_selftest_gemm_schedule(int M, int N, int pair, int max_units, int* cover, int cover_len,
                                         int* unit_halves, int* units, int* halves) {
   g_last_error.clear();
@@ -1242,7 +1264,10 @@ wenc_status wenc_sync_status(wenc* h) {
   }
   if (word != 0 && (word & 0xffu) == WENC_ERR_INVALID_ARG)
     return fail(WENC_ERR_INVALID_ARG, "a kernel met a %s out of range in device memory (site %u)",
-                ((word >> 8) & 0xffu) == 80 ? "page number" : ((word >> 8) & 0xffu) == 81 ? "length" : "sequence offset",
+                ((word >> 8) & 0xffu) == 79   ? "count of free pages"
+                : ((word >> 8) & 0xffu) == 80 ? "page number"
+                : ((word >> 8) & 0xffu) == 81 ? "length"
+                                              : "sequence offset",
                 (word >> 8) & 0xffu);
   if (word != 0 && (word & 0xffu) == WENC_ERR_CUDA)
     return fail(WENC_ERR_CUDA, "an index check of the bounds-checked build failed (site %u)", (word >> 8) & 0xffu);

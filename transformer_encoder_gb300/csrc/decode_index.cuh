@@ -1,5 +1,5 @@
-// decode_index.cuh -- the index and angle arithmetic of the decode-side kernels (append.cu, prefix_attn.cu), compiled for
-// the host too: the wenc_selftest_* entries of api.cu replay it without a GPU.
+// decode_index.cuh -- the index and angle arithmetic of the decode-side kernels (append.cu, prefix_attn.cu,
+// chunk_attn.cu, chunk_tc.cu, pages.cu), compiled for the host too: the wenc_selftest_* entries of api.cu replay it without a GPU.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -85,6 +85,48 @@ __host__ __device__ __forceinline__ void run_of(int n, int part, int parts, int&
 __host__ __device__ __forceinline__ int segment_of(const int* step0, int t, int sg) {
   while (t >= step0[sg + 1]) ++sg;
   return sg;
+}
+
+// ------------------------------------------------------------------ keys of a run of tokens (chunk_attn.cu, chunk_tc.cu)
+// The keys that tokens at positions first .. last of a sequence see between them, in steps of `step` keys: the leading n_first steps
+// [0, step), .. for the first `sinks` keys, then the others from lo_step on (a multiple of `align`) up to the last token's own.
+// Where the two meet they are one run (n_first 0, lo_step 0). Keys from `lo` on, and below `first`, are seen by some token.
+struct KeySteps {
+  int lo, hi, first;      // keys [lo, hi) and [0, first)
+  int n_first, lo_step, n;
+
+  __host__ __device__ __forceinline__ KeySteps(int pos0, int pos1, int window, int sinks, int step, int align) {
+    hi = pos1 + 1 > 0 ? pos1 + 1 : 0;
+    const long long l = static_cast<long long>(pos0) + 1 - window;
+    lo = l > 0 ? (l < hi ? static_cast<int>(l) : hi) : 0;
+    first = sinks < lo ? sinks : lo;
+    n_first = (first + step - 1) / step;
+    lo_step = lo / align * align;
+    if (lo_step <= static_cast<long long>(n_first) * step) n_first = lo_step = 0;
+    n = n_first + (hi - lo_step + step - 1) / step;
+  }
+  __host__ __device__ __forceinline__ int key0(int t, int step) const { return t < n_first ? t * step : lo_step + (t - n_first) * step; }
+  __host__ __device__ __forceinline__ bool seen(int key) const { return key < hi && (key >= lo || key < first); }
+};
+
+// ------------------------------------------------------------------ pages (pages.cu)
+// The pages that n tokens take.
+__host__ __device__ __forceinline__ long long pages_of(long long n, int page_size) { return (n + page_size - 1) / page_size; }
+
+// The table entries that a sequence of `len` tokens gives back, as ranges [x, y) and [z, w). `gone`: entries below it went
+// back in earlier calls, but for the first `first` ones, which stay while the sequence does. A window (0: none) is past an
+// entry when no later token sees any of its keys: the next one, at position len, sees those behind len - window. mark: the
+// `gone` of the next call.
+__host__ __device__ __forceinline__ int4 gives(int len, bool finished, int gone, int window, int first, int page_size, int& mark) {
+  const int total = static_cast<int>(pages_of(len, page_size));
+  const int low = first > gone ? first : gone;
+  if (finished) {
+    mark = 0;
+    return make_int4(0, first < total ? first : total, low, total > low ? total : low);
+  }
+  const int end = window > 0 && len >= window ? (len - window + 1) / page_size : 0;
+  mark = gone > end ? gone : end;
+  return make_int4(0, 0, low, end > low ? end : low);
 }
 
 }  // namespace wenc_dev

@@ -19,7 +19,7 @@ __all__ = [
     "WencError", "lib", "lib_path", "Encoder", "attention", "attention_tf32", "layernorm", "linear", "linear_tf32",
     "sync_status", "selftest_gemm_pair_abort", "EPI_BIAS_BF16", "EPI_BIAS_GELU_BF16", "EPI_BIAS_RESID_F32", "LN_OUT_F32", "LN_OUT_BF16",
     "LN_OUT_TF32", "PREC_BF16", "PREC_TF32", "EXPORTED_SYMBOLS", "prefix_attention", "kv_append", "quantize_rows",
-    "linear_i8",
+    "linear_i8", "chunk_attention", "kv_extend", "kv_release", "linear_i4",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -44,7 +44,8 @@ EXPORTED_SYMBOLS = (
     "wenc_set_device_alloc_limit", "wenc_device_bytes_held", "wenc_selftest_attention_abort",
     "wenc_prefix_attention", "wenc_prefix_attention_workspace", "wenc_kv_append", "wenc_quantize_rows",
     "wenc_linear_i8", "wenc_linear_i8_workspace", "wenc_selftest_append_sequence", "wenc_selftest_append_angle",
-    "wenc_selftest_attention_runs",
+    "wenc_selftest_attention_runs", "wenc_chunk_attention", "wenc_chunk_attention_workspace", "wenc_kv_extend",
+    "wenc_kv_release", "wenc_linear_i4", "wenc_linear_i4_workspace", "wenc_selftest_chunk_steps", "wenc_selftest_gives",
 )
 
 
@@ -103,12 +104,44 @@ class PrefixAttentionArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+def _fields(text):
+    """[(name, type)] of "type name name, type name ..." with the types of ctypes."""
+    kinds = {"int": ctypes.c_int, "int64": ctypes.c_int64, "ptr": ctypes.c_void_p, "float": ctypes.c_float,
+             "size": ctypes.c_size_t}
+    return [(name, kinds[part.split()[0]]) for part in text.split(",") for name in part.split()[1:]]
+
+
+class ChunkAttentionArgs(ctypes.Structure):
+    _fields_ = _fields("int dtype n_tokens n_seqs max_new n_heads n_kv_heads head_dim, ptr q out, int64 q_stride "
+                       "out_stride, ptr k_pages v_pages, int64 k_page_stride v_page_stride, int n_pages page_size, ptr "
+                       "block_table, int64 block_table_stride, int max_pages, ptr lens seq_start, int window sinks, "
+                       "float scale, ptr workspace, size workspace_bytes")
+
+
+class KvExtendArgs(ctypes.Structure):
+    _fields_ = _fields("int n_seqs n_rows, ptr new_tokens lens block_table, int64 block_table_stride, int max_pages "
+                       "page_size, ptr free_pages, int n_free_pages, ptr free_count lens_out free_count_out seq_start "
+                       "positions slots")
+
+
+class KvReleaseArgs(ctypes.Structure):
+    _fields_ = _fields("int n_seqs, ptr lens finished block_table, int64 block_table_stride, int max_pages page_size "
+                       "window sinks, ptr trimmed free_pages, int n_free_pages, ptr free_count lens_out free_count_out "
+                       "trimmed_out")
+
+
 # The same structures as one pack() each: a decode step makes these calls for every layer and token,
 # and a ctypes field assignment each costs more there than everything else in the call.
 _PREFIX_PACK = struct.Struct("@6i2P2q2i3P4qi3P2q2iPqiPfPN")
 _APPEND_PACK = struct.Struct("@6i4P4q2P2q2iPqi4P2i")
 assert _PREFIX_PACK.size == ctypes.sizeof(PrefixAttentionArgs) - ctypes.sizeof(PrefixAttentionArgs) % 8
 assert _APPEND_PACK.size == ctypes.sizeof(KvAppendArgs)
+_CHUNK_PACK = struct.Struct("@7i2P2q2P2q2iPqi2P2ifPN")
+_EXTEND_PACK = struct.Struct("@2i3Pq2iPi6P")
+_RELEASE_PACK = struct.Struct("@i3Pq4i2Pi4P")
+assert _CHUNK_PACK.size == ctypes.sizeof(ChunkAttentionArgs)
+assert _EXTEND_PACK.size == ctypes.sizeof(KvExtendArgs)
+assert _RELEASE_PACK.size == ctypes.sizeof(KvReleaseArgs)
 
 _lib = None
 
@@ -160,6 +193,17 @@ def lib() -> ctypes.CDLL:
         L.wenc_linear_i8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, vp, ctypes.c_size_t, vp]
         L.wenc_linear_i8_workspace.argtypes = [i, i, i]
         L.wenc_linear_i8_workspace.restype = ctypes.c_size_t
+        L.wenc_chunk_attention.argtypes = [vp, vp]
+        L.wenc_chunk_attention_workspace.argtypes = [vp]
+        L.wenc_chunk_attention_workspace.restype = ctypes.c_size_t
+        L.wenc_kv_extend.argtypes = [vp, vp]
+        L.wenc_kv_release.argtypes = [vp, vp]
+        L.wenc_linear_i4.argtypes = [vp, i, vp, vp, i, vp, vp, vp, i, i, i, i, i, vp, ctypes.c_size_t, vp]
+        L.wenc_linear_i4_workspace.argtypes = [i, i, i, i, i]
+        L.wenc_linear_i4_workspace.restype = ctypes.c_size_t
+        L.wenc_selftest_chunk_steps.argtypes = [i, i, i, i, i, i, vp, i]
+        L.wenc_selftest_gives.argtypes = [i, i, i, i, i, i, vp]
+        L.wenc_selftest_gives.restype = None
         L.wenc_selftest_append_sequence.argtypes = [vp, i, i, i, i, ip]
         L.wenc_selftest_append_sequence.restype = ctypes.c_int
         L.wenc_selftest_append_angle.argtypes = [ctypes.c_float, i, vp, vp]
@@ -175,7 +219,9 @@ def lib() -> ctypes.CDLL:
                      "wenc_selftest_wait_timeout", "wenc_linear_tf32", "wenc_attention_tf32", "wenc_set_stem",
                      "wenc_stem", "wenc_encode", "wenc_encode_launches", "wenc_set_cross_kv", "wenc_cross_kv",
                      "wenc_selftest_gemm_schedule", "wenc_selftest_gemm_pair_abort", "wenc_selftest_attention_abort",
-                     "wenc_prefix_attention", "wenc_kv_append", "wenc_quantize_rows", "wenc_linear_i8"):
+                     "wenc_prefix_attention", "wenc_kv_append", "wenc_quantize_rows", "wenc_linear_i8",
+                     "wenc_chunk_attention", "wenc_kv_extend", "wenc_kv_release", "wenc_linear_i4",
+                     "wenc_selftest_chunk_steps"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -877,6 +923,241 @@ def linear_i8(a, a_scale, w, w_scale, bias, epilogue: int = EPI_BIAS_BF16, resid
         ws, ws_bytes = _room(workspace, dev)
     status = _lib.wenc_linear_i8(a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), bias.data_ptr(), rp,
                                  out.data_ptr(), M, N, K, epilogue, ws, ws_bytes, _raw_stream(stream, dev))
+    if status:
+        _check(status)
+    return out
+
+
+def chunk_attention(q, k_pages, v_pages, block_table, lens, *, seq_start=None, max_new=None, window=None, sinks: int = 0,
+                    scale: float = 0.125, out=None, workspace=None, stream=None):
+    """Attention of chunks of new tokens over a paged cache (see wenc_chunk_attention).
+
+    ``q`` [tokens, H, 64] bf16 or float32 (slices of a fused projection's rows will do); ``k_pages``, ``v_pages``
+    [pages, page_size, Hkv, 64], ``block_table`` int32 [n_seqs, pages], ``lens`` int32 [n_seqs] (the call's tokens
+    included) and ``seq_start`` int32 [n_seqs + 1] (None: tokens / n_seqs each) as ``kv_append`` takes them.
+    ``max_new``: at least the most tokens of a sequence (None: all of the call's). A token sees the keys up to its own, of
+    these the ``window`` newest (None: all) and the ``sinks`` first. Without ``out`` the result is a new tensor, whose
+    padding rows are zeros. ``workspace``: a uint8 tensor to use instead of an allocation where one is needed; it is
+    busy until the call's work is done.
+    """
+    torch = _torch or _load_torch()
+    dtype = q.dtype
+    dt = 1 if dtype is torch.bfloat16 else 0
+    if not dt and dtype is not torch.float32:
+        raise _dtype_error(q, "q")
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError(f"q must be [tokens, heads, 64], got {tuple(shape)}")
+    n, H, hd = shape
+    dev = q.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise _elsewhere((("q", q),))
+    if k_pages.dim() != 4:
+        raise ValueError(f"k_pages and v_pages must be [pages, page_size, heads, {hd}], got {tuple(k_pages.shape)} and "
+                         f"{tuple(v_pages.shape)}")
+    kv = k_pages.shape[2]
+    pages, size, kps, vps = _pool(k_pages, v_pages, dtype, kv, hd)
+    n_seqs = lens.numel()
+    if lens.dtype is not torch.int32 or lens.dim() != 1 or not lens.is_contiguous():
+        raise _bad_ints(lens, "lens", n_seqs)
+    tab_stride, max_pages = _table(block_table, n_seqs)
+    if (k_pages.get_device() != dev or v_pages.get_device() != dev or block_table.get_device() != dev
+            or lens.get_device() != dev):
+        raise _elsewhere((("k_pages", k_pages), ("v_pages", v_pages), ("block_table", block_table), ("lens", lens)))
+    start = 0
+    if seq_start is not None:
+        if (seq_start.dtype is not torch.int32 or seq_start.dim() != 1 or seq_start.numel() != n_seqs + 1
+                or not seq_start.is_contiguous()):
+            raise _bad_ints(seq_start, "seq_start", n_seqs + 1)
+        if seq_start.get_device() != dev:
+            raise _elsewhere((("seq_start", seq_start),))
+        start = seq_start.data_ptr()
+    if window is not None and window < 1:
+        raise ValueError(f"window must be at least 1 (None: every key), got {window}")
+    if out is None:
+        out = _empty(shape, dtype, q.device, stream)
+        out_stride = H * hd
+        if start:
+            if stream is None:
+                out.zero_()
+            else:
+                with _on(stream):  # in order with the kernels that write over the zeros
+                    out.zero_()
+    else:
+        if out.dtype is not dtype or out.shape != shape:
+            raise ValueError(f"out must be {dtype} {tuple(shape)}, got {out.dtype} {tuple(out.shape)}")
+        out_stride = H * hd if out.is_contiguous() else _token_stride(out, "out")
+        if out.get_device() != dev:
+            raise _elsewhere((("out", out),))
+    if n == 0 or n_seqs == 0:
+        return out
+    if max_new is None:
+        max_new = n if start else -(-n // n_seqs)
+    args = (dt, n, n_seqs, min(max_new, n), H, kv, hd, q.data_ptr(), out.data_ptr(),
+            H * hd if q.is_contiguous() else _token_stride(q, "q"), out_stride, k_pages.data_ptr(), v_pages.data_ptr(),
+            kps, vps, pages, size, block_table.data_ptr(), tab_stride, max_pages, lens.data_ptr(), start, window or 0,
+            sinks, scale)
+    ws = ws_bytes = 0
+    if workspace is None:
+        need = _lib.wenc_chunk_attention_workspace(_CHUNK_PACK.pack(*args, 0, 0))
+        workspace = _empty(need, torch.uint8, q.device, stream) if need else None
+    if workspace is not None:
+        ws, ws_bytes = _room(workspace, dev)
+    status = _lib.wenc_chunk_attention(_CHUNK_PACK.pack(*args, ws, ws_bytes), _raw_stream(stream, dev))
+    if status:
+        _check(status)
+    return out
+
+
+def _ints(t, name, n, dev, dtype=None):
+    """The address of an int32 (or other) array of n elements."""
+    if t.dtype is not (dtype or _torch.int32) or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise (_bad_ints(t, name, n) if dtype is None else
+               TypeError(f"{name} must be contiguous {dtype} of shape ({n},), got {t.dtype} {tuple(t.shape)}"))
+    if t.get_device() != dev:
+        raise _elsewhere(((name, t),))
+    return t.data_ptr()
+
+
+def kv_extend(new_tokens, lens, block_table, free_pages, free_count, page_size: int, rows: int, *, lens_out=None,
+              free_count_out=None, seq_start=None, positions=None, slots=None, stream=None):
+    """The places of a step's new tokens in a paged cache (see wenc_kv_extend): pages from the free ones, block-table
+    entries, row offsets, positions and slots.
+
+    ``new_tokens`` and ``lens`` int32 [n_seqs]; ``block_table`` int32 [n_seqs, pages], whose new entries are written;
+    ``free_pages`` int32 [pages], of which the first ``free_count`` (int32 [1]) are free and are taken from the end;
+    ``rows``: rows of the step, at least its tokens. Returns (lens with the new tokens, pages that stay free, seq_start
+    int32 [n_seqs + 1], positions int32 [rows], slots int64 [rows]; padding rows have position 0 and slot -1), in the
+    given tensors or new ones. ``lens_out`` and ``free_count_out`` lie apart from ``lens`` and ``free_count``.
+    """
+    torch = _torch or _load_torch()
+    dev = lens.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise _elsewhere((("lens", lens),))
+    n, i32 = lens.numel(), torch.int32
+    lp, mp = _ints(lens, "lens", n, dev), _ints(new_tokens, "new_tokens", n, dev)
+    tab_stride, max_pages = _table(block_table, n)
+    if block_table.get_device() != dev:
+        raise _elsewhere((("block_table", block_table),))
+    fp, cp = _ints(free_pages, "free_pages", free_pages.numel(), dev), _ints(free_count, "free_count", 1, dev)
+    if rows < 0:
+        raise ValueError(f"rows must not be negative, got {rows}")
+
+    def made(t, size, dtype=i32):
+        return _empty(size, dtype, lens.device, stream) if t is None else t
+    lens_out, free_count_out, seq_start = made(lens_out, n), made(free_count_out, 1), made(seq_start, n + 1)
+    positions, slots = made(positions, rows), made(slots, rows, torch.int64)
+    status = _lib.wenc_kv_extend(
+        _EXTEND_PACK.pack(n, rows, mp, lp, block_table.data_ptr(), tab_stride, max_pages, page_size, fp, free_pages.numel(),
+                          cp, _ints(lens_out, "lens_out", n, dev), _ints(free_count_out, "free_count_out", 1, dev),
+                          _ints(seq_start, "seq_start", n + 1, dev), _ints(positions, "positions", rows, dev),
+                          _ints(slots, "slots", rows, dev, torch.int64)), _raw_stream(stream, dev))
+    if status:
+        _check(status)
+    return lens_out, free_count_out, seq_start, positions, slots
+
+
+def kv_release(lens, block_table, free_pages, free_count, page_size: int, *, finished=None, window=None, sinks: int = 0,
+               trimmed=None, lens_out=None, free_count_out=None, trimmed_out=None, stream=None):
+    """Pages that no later token needs, back to the free ones (see wenc_kv_release): those of ``finished`` sequences
+    (bool [n_seqs]), and with a ``window`` those that it has moved past.
+
+    ``lens``, ``block_table``, ``free_pages`` and ``free_count`` as ``kv_extend`` takes them; ``window`` and ``sinks`` as
+    ``chunk_attention`` does; ``trimmed`` int32 [n_seqs] goes with a window: what the last call returned (at first, and for a
+    new sequence, 0). Returns (lens, 0 for finished sequences; pages that are free now; trimmed, None without a window) in the
+    given tensors or new ones, which lie apart from what they follow. ``free_pages`` is written in place.
+    """
+    torch = _torch or _load_torch()
+    dev = lens.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise _elsewhere((("lens", lens),))
+    n = lens.numel()
+    lp = _ints(lens, "lens", n, dev)
+    tab_stride, max_pages = _table(block_table, n)
+    if block_table.get_device() != dev:
+        raise _elsewhere((("block_table", block_table),))
+    fp, cp = _ints(free_pages, "free_pages", free_pages.numel(), dev), _ints(free_count, "free_count", 1, dev)
+    if window is not None and window < 1:
+        raise ValueError(f"window must be at least 1 (None: none), got {window}")
+    if (trimmed is None) != (window is None) or (trimmed_out is not None and window is None):
+        raise ValueError("trimmed goes with a window")
+    if finished is None and window is None:
+        raise ValueError("neither finished nor a window")
+    dp = _ints(finished, "finished", n, dev, torch.bool) if finished is not None else 0
+    tp = top = 0
+    lens_out = _empty(n, torch.int32, lens.device, stream) if lens_out is None else lens_out
+    free_count_out = _empty(1, torch.int32, lens.device, stream) if free_count_out is None else free_count_out
+    if window is not None:
+        trimmed_out = _empty(n, torch.int32, lens.device, stream) if trimmed_out is None else trimmed_out
+        tp, top = _ints(trimmed, "trimmed", n, dev), _ints(trimmed_out, "trimmed_out", n, dev)
+    status = _lib.wenc_kv_release(
+        _RELEASE_PACK.pack(n, lp, dp, block_table.data_ptr(), tab_stride, max_pages, page_size, window or 0, sinks, tp, fp,
+                           free_pages.numel(), cp, _ints(lens_out, "lens_out", n, dev),
+                           _ints(free_count_out, "free_count_out", 1, dev), top), _raw_stream(stream, dev))
+    if status:
+        _check(status)
+    return lens_out, free_count_out, trimmed_out
+
+
+def linear_i4(x, w, w_scale, bias, epilogue: int = EPI_BIAS_BF16, resid=None, out=None, workspace=None, stream=None):
+    """out = epilogue(x W^T + bias) with 4-bit weights that have a scale for each group of inputs (see wenc_linear_i4).
+
+    ``x`` [M, K] bf16 or float32; ``w`` uint8 [N, K / 2], two weights u of 0..15 to a byte, the even input's in the low
+    half; ``w_scale`` [N, K / group] bf16 or float32, group 32, 64 or 128: W = (u - 8) * scale; ``bias`` float32 [N].
+    Epilogues as ``linear``: the first two give ``x``'s type, the third adds ``resid`` and gives float32 (``out`` may be
+    ``resid``). ``workspace``: a uint8 tensor to use instead of an allocation where one is needed.
+    """
+    torch = _torch or _load_torch()
+    dev = x.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise _elsewhere((("x", x),))
+    f32, bf16 = torch.float32, torch.bfloat16
+    if x.dtype is not bf16 and x.dtype is not f32:
+        raise _dtype_error(x, "x")
+    if w_scale.dtype is not bf16 and w_scale.dtype is not f32:
+        raise _dtype_error(w_scale, "w_scale")
+    if w.dtype is not torch.uint8 or bias.dtype is not f32:
+        raise TypeError(f"w must be torch.uint8 and bias torch.float32, got {w.dtype} and {bias.dtype}")
+    xsh, wsh, ssh = x.shape, w.shape, w_scale.shape
+    if len(xsh) != 2 or len(wsh) != 2 or xsh[1] != 2 * wsh[1]:
+        raise ValueError(f"x {tuple(xsh)} and w {tuple(wsh)} must be [M, K] and [N, K / 2]")
+    M, K = xsh
+    N = wsh[0]
+    if len(ssh) != 2 or ssh[0] != N or ssh[1] == 0 or K % ssh[1]:
+        raise ValueError(f"w_scale must be [{N}, {K} / group], got {tuple(ssh)}")
+    if bias.numel() != N:
+        raise ValueError(f"bias must hold {N} elements")
+    if not (x.is_contiguous() and w.is_contiguous() and w_scale.is_contiguous() and bias.is_contiguous()):
+        raise ValueError("linear_i4 takes contiguous tensors")
+    if w.get_device() != dev or w_scale.get_device() != dev or bias.get_device() != dev:
+        raise _elsewhere((("w", w), ("w_scale", w_scale), ("bias", bias)))
+    dt = f32 if epilogue == EPI_BIAS_RESID_F32 else x.dtype
+    if out is None:
+        out = _empty((M, N), dt, x.device, stream)
+    elif out.dtype is not dt or out.shape != (M, N) or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous {dt} {(M, N)}, got {out.dtype} {tuple(out.shape)}")
+    elif out.get_device() != dev:
+        raise _elsewhere((("out", out),))
+    rp = 0
+    if resid is not None:
+        if resid.dtype is not f32 or resid.shape != (M, N) or not resid.is_contiguous():
+            raise ValueError(f"resid must be contiguous float32 {(M, N)}, got {resid.dtype} {tuple(resid.shape)}")
+        if resid.get_device() != dev:
+            raise _elsewhere((("resid", resid),))
+        rp = resid.data_ptr()
+    if M == 0:
+        return out
+    x_type, group = int(x.dtype is bf16), K // ssh[1]
+    ws = ws_bytes = 0
+    if workspace is None:
+        need = _lib.wenc_linear_i4_workspace(M, N, K, x_type, group)
+        if need:
+            workspace = _empty(need, torch.uint8, x.device, stream)
+    if workspace is not None:
+        ws, ws_bytes = _room(workspace, dev)
+    status = _lib.wenc_linear_i4(x.data_ptr(), x_type, w.data_ptr(), w_scale.data_ptr(), int(w_scale.dtype is bf16),
+                                 bias.data_ptr(), rp, out.data_ptr(), M, N, K, group, epilogue, ws, ws_bytes,
+                                 _raw_stream(stream, dev))
     if status:
         _check(status)
     return out
