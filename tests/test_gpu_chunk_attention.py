@@ -289,7 +289,7 @@ def test_bad_lengths_offsets_and_pages_are_reported(dtype, case):
     import torch
     from transformer_encoder_gb300 import WencError, sync_status
     c = Case(dtype, [1, 200, 3, 40], [100, 300, 20, 60], 4, 2, seed=10)
-    want = c.run()
+    want, ref = c.run(), c.reference()[0]
     kw = {}
     if case == "page":
         c.table[1, 2] = c.kc.shape[0]
@@ -315,16 +315,12 @@ def test_bad_lengths_offsets_and_pages_are_reported(dtype, case):
     with pytest.raises(WencError, match="out of range") as e:
         sync_status()
     assert e.value.status == 1
+    # (not bit by bit: where long rows are cut into pieces depends on the whole call; within the bound of the rounding)
     for s in range(4):
         if s not in hurt:
             rows = slice(int(c.start[s]), int(c.start[s + 1]))
-            assert torch.equal(out[rows], want[rows]) or case == "many", s
-    if case == "many":  # (another bound may take another form for the others)
-        c2 = Case(dtype, [1, 200, 3, 40], [100, 300, 20, 60], 4, 2, seed=10)
-        ref = c2.reference()[0]
-        for s in (0, 2, 3):
-            rows = slice(int(c.start[s]), int(c.start[s + 1]))
-            assert float((out[rows].double() - ref[rows]).norm()) <= 2.0 ** -8 * float(ref[rows].norm())
+            limit = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -19
+            assert float((out[rows].double() - ref[rows]).norm()) <= limit * float(ref[rows].norm()), s
 
 
 @pytest.mark.parametrize("dtype", DTYPES)

@@ -156,3 +156,23 @@ __device__ __forceinline__ void chunk_write8(const ChunkParams& p, int token, in
 }
 
 }  // namespace wenc_dev
+
+namespace wenc_host {
+
+// A unit of chunk_tc.cu that was cut: where it belongs and its pieces (0: no unit was cut here).
+struct ChunkCut {
+  int seq, hk, x, pieces;
+};
+struct ChunkTcArgs {
+  int few;             // rows per key head up to which a sequence is chunk_attn.cu's
+  int tokens;          // of a row tile: 128 / r
+  int per_unit;        // of a unit: two tiles'
+  ChunkCut* cuts;      // [CTAs]
+  float* part_o;       // [CTAs][2][256][64]
+  float2* part_ml;     // [CTAs][2][256]: (maximum in log2 units, sum)
+};
+size_t chunk_tc_workspace(int sms);
+// The sequences with more than `few` rows per key head (bf16, scale > 0, at most 128 query heads per key head). Two launches.
+cudaError_t launch_chunk_tc(const wenc_dev::ChunkParams& p, int few, void* workspace, uint32_t* err, int sms, cudaStream_t stream);
+
+}  // namespace wenc_host

@@ -269,13 +269,22 @@ struct Plan {
   int nr = 0;              // groups of 8 rows per tile
   RowsPlan rows = {};
   long long blocks = 0;
+  bool tc = false;         // sequences with more than rows.most rows per key head go to chunk_tc.cu
   size_t bytes = 0;
 };
+
+constexpr int kFew = 16;  // rows per key head up to which a bf16 sequence is attended here
 
 Plan make_plan(const wenc_chunk_attention_args* a, int sms) {
   Plan pl;
   const bool f32 = a->dtype == WENC_DTYPE_F32;
-  const long long r = a->n_heads / a->n_kv_heads, most = static_cast<long long>(a->max_new) * r;
+  const long long r = a->n_heads / a->n_kv_heads;
+  long long most = static_cast<long long>(a->max_new) * r;
+  if (!f32 && r <= 128 && a->scale > 0.0f && most > kFew) {
+    pl.tc = true;
+    pl.bytes = wenc_host::chunk_tc_workspace(sms);
+    most = kFew;
+  }
   pl.nr = most <= 8 ? 1 : most <= 16 || f32 ? 2 : 4;
   const long long rows = 8 * pl.nr;
   pl.rows.most = static_cast<int>(most);
@@ -442,7 +451,10 @@ extern "C" wenc_status wenc_chunk_attention(const wenc_chunk_attention_args* a, 
   p.q_keep = a->scale == 0.0f ? 0u : 0xffffffffu;
   p.scale_log2 = (a->scale == 0.0f ? 1.0f : a->scale < 0.0f ? -a->scale : a->scale) * 1.4426950408889634f;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = bf ? launch_all<__nv_bfloat16>(p, pl, err, s) : launch_all<float>(p, pl, err, s);
+  cudaError_t e = cudaSuccess;
+  if (pl.tc) e = wenc_host::launch_chunk_tc(p, pl.rows.most, a->workspace, err, sms, s);
+  // (every sequence with more rows than that: nothing is left for the few)
+  if (e == cudaSuccess && !(pl.tc && !a->seq_start)) e = bf ? launch_all<__nv_bfloat16>(p, pl, err, s) : launch_all<float>(p, pl, err, s);
   if (e != cudaSuccess) {
     char buf[200];
     snprintf(buf, sizeof(buf), "chunk_attention launch: %s", cudaGetErrorString(e));

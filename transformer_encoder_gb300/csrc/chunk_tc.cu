@@ -1,0 +1,764 @@
+// chunk_tc.cu -- the chunks of chunk_attn.cu that bring many bf16 query rows (prompts and their parts), on the 5th-generation
+// tensor cores.
+//
+// Of a sequence with more rows per key head than the few of chunk_attn.cu, a unit of work is 2 x 128 / r tokens of one key head (r
+// query heads share it; two row tiles of 128) against the keys that these tokens see, in steps of 128. Units differ in length: a prompt's later
+// tokens see more keys, sequences bring what they bring. So all units' steps are laid end to end, each with kStart more for its
+// beginning and end, and every CTA (one per SM) takes an equal run of them, which it finds itself from the lengths: there is
+// no plan to build and read, and no CTA idles while another works on a long unit. A unit that is whole within a run goes straight to the output;
+// of one that is cut, the pieces (at most one at either end of a run) go to the workspace, and chunk_join_kernel joins them, in order.
+//
+// Within a CTA, as in prefix_tc.cu: S = Q K^T and O += P V by tcgen05.mma into TMEM, one softmax thread per query row, the two
+// row tiles taking turns on the exponentials through named barriers, P as two bf16 parts (the large one in TMEM as the A operand, the small one in shared
+// memory). What differs: two warps gather K and V by cp.async, 128 bytes a row from wherever its page lies, so pages may
+// have any size; keys that no token of the unit sees are zero-filled and not read; and steps at the borders of what the rows see are masked.
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include <atomic>
+
+#include "chunk.cuh"
+#include "decode_index.cuh"
+#include "launch.h"
+#include "mma.cuh"
+#include "ptx.cuh"
+
+namespace {
+
+using namespace wenc_dev;
+
+constexpr int BQ = 128;    // query rows per tile (two tiles per unit)
+constexpr int BKV = 128;   // keys per step
+constexpr int HD = 64;
+constexpr int NK = 3;      // K ring depth
+constexpr int NV = 3;      // V ring depth
+constexpr int NP = 4;      // ring of pieces
+constexpr int kThreads = 384;  // K and V producers, 2 MMA issuers, 2 softmax warpgroups
+constexpr int kWarps = kThreads / 32;
+constexpr int kStart = 1;  // what a unit's beginning and end cost, in steps
+constexpr int kLeast = 4;  // no CTA takes fewer steps
+// Registers per thread after the start-up reallocation (setmaxnreg), as in prefix_tc.cu; the sum must fit in what the CTA is
+// launched with (checked on the host before the first launch).
+constexpr int kCtrlRegs = 104;
+constexpr int kSoftmaxRegs = 200;
+constexpr int kRegsNeeded = kCtrlRegs * 128 + kSoftmaxRegs * 256;
+static_assert(kRegsNeeded <= (65536 / kThreads) / 8 * 8 * kThreads, "register split exceeds the launch budget");
+
+constexpr uint32_t Q_BYTES = BQ * HD * 2;    // 16 KB per query tile
+constexpr uint32_t KV_BYTES = BKV * HD * 2;  // 16 KB per K or V tile
+constexpr uint32_t P_BYTES = BQ * BKV * 2;   // 32 KB: the small part of a tile's P, two blocks of 64 keys
+constexpr uint32_t OFF_Q = 0;
+constexpr uint32_t OFF_K = OFF_Q + 2 * Q_BYTES;
+constexpr uint32_t OFF_V = OFF_K + NK * KV_BYTES;
+constexpr uint32_t OFF_P = OFF_V + NV * KV_BYTES;
+constexpr uint32_t OFF_BARS = OFF_P + 2 * P_BYTES;
+// bars: q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], and per query tile t: s_full[t], s_free[t],
+// p_full[t], pv_done[t]; drain; piece_full[NP], piece_empty[NP].
+constexpr int NUM_BARS = 2 + 2 * NK + 2 * NV + 8 + 1 + 2 * NP;
+constexpr int kTakers = 11;  // warps that take pieces from the ring: all but the one that walks
+constexpr size_t SMEM = 1024 + OFF_BARS + NUM_BARS * 8 + 16;
+static_assert(SMEM + 2600 <= 232448, "shared memory of the chunk kernel");
+constexpr uint32_t TMEM_COLS = 512;  // S_A 0..127, S_B 128..255, O_A 256..319, O_B 320..383, P_A 384..447, P_B 448..511
+// The running maximum grows only when a step's maximum exceeds it by more than this (log2 units), so p <= 2^8.
+constexpr float kRescaleThreshold = 8.0f;
+
+using wenc_host::ChunkCut;
+using wenc_host::ChunkTcArgs;
+
+// Unit x of a sequence: its tokens i0 .. i1 (of the sequence's) and their keys.
+struct Unit {
+  int i0, i1;
+  KeySteps ks;
+  Unit() = default;
+  __device__ __forceinline__ Unit(const ChunkParams& p, int m, int len, int per_unit, int x)
+      : i0(x * per_unit), i1(min(m, (x + 1) * per_unit) - 1), ks(len - m + i0, len - m + i1, p.window, p.sinks, BKV, 1) {}
+  // (at least one, of which nothing is seen: tokens in front of the cache have rows of zeros)
+  __device__ __forceinline__ int steps() const { return max(1, ks.n); }
+};
+
+// The sequence's tokens where its units are this kernel's, else 0; and its length.
+__device__ __forceinline__ int long_tokens(const ChunkParams& p, int few, int s, int& len, uint32_t* err) {
+  const ChunkSeq q = chunk_seq(p, s, err);
+  len = q.len;
+  return q.m * p.r > few ? q.m : 0;
+}
+
+// Steps k0 .. k1 - 1 of a unit's n, and where the unit's last one ends among all.
+struct Piece {
+  Unit u;
+  int hk, seq, x, row0, pos0, k0, k1, n;  // row0, pos0: of the sequence's first token
+  long long end;
+};
+
+// The way through a CTA's run of steps. One warp walks; it hands the pieces to the other roles through a ring in shared memory
+// (walking in every role made the kernel's code 164 KB, and 4.4 of the 5.6 warps that waited on average waited for instructions).
+struct Walk {
+  Piece pc;                           // the piece in hand
+  int hk, seq, x, row0, m, len, skip;  // where the run goes on: step `skip` (of n + kStart) of that unit
+  long long left, at;                 // steps left, and the number of the unit's first step among all
+
+  // The next piece; false at the end of the run. All lanes of a warp call.
+  __device__ __forceinline__ bool next(const ChunkParams& p, const ChunkTcArgs& a, uint32_t* err) {
+    while (left > 0) {
+      const Unit u(p, m, len, a.per_unit, x);
+      const int n = u.steps(), all = n + kStart, take = static_cast<int>(min(left, static_cast<long long>(all - skip)));
+      pc = Piece{u, hk, seq, x, row0, len - m, max(0, skip - kStart), max(0, skip + take - kStart), n, at + all};
+      left -= take;
+      skip += take;
+      if (skip == all && left > 0) {  // on to the next unit
+        at += all;
+        skip = 0;
+        if ((x + 1) * a.per_unit < m) {
+          ++x;
+        } else {
+          x = 0;
+          find(p, a, seq + 1, err);
+        }
+      }
+      if (pc.k1 > pc.k0) return true;
+    }
+    return false;
+  }
+
+  // The first sequence with units from s on (of the next key head behind the last).
+  __device__ __forceinline__ void find(const ChunkParams& p, const ChunkTcArgs& a, int s, uint32_t* err) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int turn = 0; turn < 2; ++turn) {
+#pragma unroll 1
+      for (; s < p.n_seqs; s += 32) {
+        int l = 0;
+        const int mine = s + lane < p.n_seqs ? long_tokens(p, a.few, s + lane, l, err) : 0;
+        const uint32_t some = __ballot_sync(0xffffffffu, mine > 0);
+        if (some) {
+          const int i = __ffs(some) - 1;
+          seq = s + i;
+          m = __shfl_sync(0xffffffffu, mine, i);
+          len = __shfl_sync(0xffffffffu, l, i);
+          row0 = p.seq_start ? p.seq_start[seq] : seq * p.per_seq;
+          return;
+        }
+      }
+      ++hk;
+      s = 0;
+    }
+    left = 0;  // (not reached: a run ends within the units)
+  }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ ChunkTcArgs a, uint32_t* err) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ long long sums[kWarps];
+  __shared__ int start[6];
+  __shared__ Piece pieces[NP];
+  __shared__ long long places[2][BKV];
+  __shared__ long long of_run[2];  // all steps, and the CTAs that share them
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t s0 = smem_u32(smem);
+  const uint32_t sQ = s0 + OFF_Q, sK = s0 + OFF_K, sV = s0 + OFF_V, sP = s0 + OFF_P;
+  const uint32_t bar0 = s0 + OFF_BARS;
+  const uint32_t q_full = bar0, q_empty = bar0 + 8u;
+  auto k_full = [&](int s) { return bar0 + 8u * (2 + s); };
+  auto k_empty = [&](int s) { return bar0 + 8u * (2 + NK + s); };
+  auto v_full = [&](int s) { return bar0 + 8u * (2 + 2 * NK + s); };
+  auto v_empty = [&](int s) { return bar0 + 8u * (2 + 2 * NK + NV + s); };
+  const uint32_t tb0 = bar0 + 8u * (2 + 2 * NK + 2 * NV);
+  auto s_full = [&](int t) { return tb0 + 8u * t; };
+  auto s_free = [&](int t) { return tb0 + 16u + 8u * t; };
+  auto p_full = [&](int t) { return tb0 + 32u + 8u * t; };
+  auto pv_done = [&](int t) { return tb0 + 48u + 8u * t; };
+  const uint32_t drain = tb0 + 64u;
+  auto piece_full = [&](int i) { return tb0 + 72u + 8u * i; };
+  auto piece_empty = [&](int i) { return tb0 + 72u + 8u * (NP + i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_BARS + NUM_BARS * 8);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  const WaitCtx wc{abort_flag, err};
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);  // released by the S issuer's commit after a piece's last S
+    for (int s = 0; s < NK; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 1);
+    }
+    for (int s = 0; s < NV; ++s) {
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(s_full(t), 1);
+      mbar_init(s_free(t), 4);  // one arrival per softmax warp of the tile
+      mbar_init(p_full(t), 4);
+      mbar_init(pv_done(t), 1);
+    }
+    mbar_init(drain, 2);  // one commit per MMA-issuing thread
+    for (int i = 0; i < NP; ++i) {
+      mbar_init(piece_full(i), 1);
+      mbar_init(piece_empty(i), kTakers);
+    }
+    *abort_flag = 0u;
+    fence_barrier_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();  // TMEM is held: the next kernel may be scheduled
+  pdl_wait();     // queries, cache and lengths from the previous kernels are complete from here on
+
+  // ---- the CTA's run of steps: the warps sum the steps of a share of the sequences each (lanes over a sequence's units) ...
+  const int per_warp = (p.n_seqs + kWarps - 1) / kWarps;
+  const int seq_a = min(p.n_seqs, warp * per_warp), seq_b = min(p.n_seqs, seq_a + per_warp);
+  auto weigh = [&](int m, int len, int x) { return x * a.per_unit < m ? Unit(p, m, len, a.per_unit, x).steps() + kStart : 0; };
+  // f(sequence, its tokens, its length) for the warp's sequences with units, until it returns true
+  auto each_seq = [&](auto&& f) {
+#pragma unroll 1
+    for (int s = seq_a; s < seq_b; s += 32) {
+      int l = 0;
+      const int mine = s + lane < seq_b ? long_tokens(p, a.few, s + lane, l, err) : 0;
+#pragma unroll 1
+      for (uint32_t some = __ballot_sync(0xffffffffu, mine > 0); some; some &= some - 1) {
+        const int i = __ffs(some) - 1;
+        if (f(s + i, __shfl_sync(0xffffffffu, mine, i), __shfl_sync(0xffffffffu, l, i))) return;
+      }
+    }
+  };
+  auto warp_sum = [&](long long v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+  };
+  {
+    long long sum = 0;
+    each_seq([&](int, int m, int len) {
+#pragma unroll 1
+      for (int x = lane; x * a.per_unit < m; x += 32) sum += weigh(m, len, x);
+      return false;
+    });
+    sum = warp_sum(sum);
+    if (lane == 0) sums[warp] = sum;
+  }
+  __syncthreads();
+  long long of_head = 0, before = 0;  // steps of one key head, and of the sequences before this warp's
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += sums[w];
+    of_head += sums[w];
+  }
+  // ... and the run's beginning is found by the warp whose share holds it.
+  const long long total = of_head * p.Hkv;
+  const long long ctas = max(1ll, min(static_cast<long long>(gridDim.x), total / kLeast));
+  const long long b0 = min(total, total * blockIdx.x / ctas), b1 = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : b0;
+  const bool busy = b1 > b0 && blockIdx.x < ctas;
+  if (busy) {
+    const long long t = b0 % of_head;
+    if (t >= before && t < before + sums[warp]) {
+      long long at = before;
+      each_seq([&](int s, int m, int len) {
+#pragma unroll 1
+        for (int x0 = 0; x0 * a.per_unit < m; x0 += 32) {
+          const int w = weigh(m, len, x0 + lane);
+          int sum = w;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += up;
+          }
+          const uint32_t past = __ballot_sync(0xffffffffu, t < at + sum);
+          if (past) {
+            if (lane == __ffs(past) - 1) {
+              start[0] = s;
+              start[1] = x0 + lane;
+              start[2] = static_cast<int>(t - (at + sum - w));
+              start[3] = m;
+              start[4] = len;
+              start[5] = p.seq_start ? p.seq_start[s] : s * p.per_seq;
+            }
+            return true;
+          }
+          at += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        return false;
+      });
+    }
+  }
+  __syncthreads();
+  const uint32_t tmem_base = *tmem_slot;
+  if (threadIdx.x == 0) {
+    a.cuts[blockIdx.x].pieces = 0;
+    of_run[0] = total;
+    of_run[1] = ctas;
+  }
+  __syncthreads();  // (the piece that is cut at the run's end writes the mark again)
+
+  auto tS = [&](int t) { return tmem_base + 128u * t; };
+  auto tO = [&](int t) { return tmem_base + 256u + 64u * t; };
+  auto tP = [&](int t) { return tmem_base + 384u + 64u * t; };  // P as bf16 pairs: 64 columns per tile
+
+  // Every role takes the same pieces in the same order and counts K/V tiles across them, so ring slots and barrier parities
+  // continue from one piece to the next. take(i): piece i, false behind the last (or after a failed wait); give(i): it is done with.
+  auto take = [&](int i) { return mbar_wait_warp(piece_full(i % NP), (i / NP) & 1, wc, 8) && pieces[i % NP].k1 > 0; };
+  auto give = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(piece_empty(i % NP));
+  };
+  if (warp < 4) {
+    // control warpgroup: registers to the softmax warpgroups first
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kCtrlRegs) : "memory");
+    if (warp < 2) {
+      // ---------------- gathering: warp 0 the queries and K, warp 1 V. A tile's copies are under way while the next slot is
+      // waited for; a tile is handed over once they have landed and the proxy fence has run.
+      const bool is_k = warp == 0;
+      const uint8_t* pages = is_k ? p.k_pages : p.v_pages;
+      const uint32_t page16 = is_k ? p.k_page16 : p.v_page16;
+      const uint32_t ring = is_k ? sK : sV;
+      const int c = lane & 7, r4 = lane >> 3;  // 16-byte piece of a row, and row of the four that an instruction copies
+      const uint32_t even = r4 * 128u + ((c ^ r4) << 4), odd = (r4 + 4) * 128u + ((c ^ (r4 + 4)) << 4);
+      uint32_t pending = 0;  // the barrier of the tile under way
+      auto hand_over = [&]() {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pending);
+      };
+      auto flush = [&]() {
+        cp_async_wait<0>();
+        if (pending) hand_over();
+        pending = 0;
+      };
+      // waits for a slot, and hands the tile under way over first if that takes long
+      auto acquire = [&](uint32_t bar, uint32_t parity, uint32_t site) {
+        if (!__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) flush();
+        return mbar_wait_warp(bar, parity, wc, site);
+      };
+      auto commit = [&](uint32_t bar) {
+        cp_async_commit();
+        if (pending) {
+          cp_async_wait<1>();
+          hand_over();
+        }
+        pending = bar;
+      };
+      Walk run;
+      if (is_k) {
+        run.left = busy ? b1 - b0 : 0;
+        run.hk = busy ? static_cast<int>(b0 / of_head) : 0;
+        run.seq = start[0];
+        run.x = start[1];
+        run.skip = start[2];
+        run.m = start[3];
+        run.len = start[4];
+        run.row0 = start[5];
+        run.at = b0 - start[2];
+      }
+      int kc = 0;  // tiles
+      bool ok = true;
+#pragma unroll 1
+      for (int np = 0; ok; ++np) {
+        const Piece& pc = pieces[np % NP];
+        if (is_k) {
+          const bool more = run.next(p, a, err);
+          if (!more) run.pc.k0 = run.pc.k1 = 0;
+          if (!acquire(piece_empty(np % NP), ((np / NP) & 1) ^ 1u, 8)) break;
+          if (lane == 0) {
+            pieces[np % NP] = run.pc;
+            mbar_arrive(piece_full(np % NP));
+          }
+          __syncwarp();
+          if (!more) break;
+          if (!acquire(q_empty, (np & 1) ^ 1u, 9)) break;
+        } else if (!take(np)) {
+          break;
+        }
+        const Unit u = pc.u;
+        if (is_k) {
+#pragma unroll 1
+          for (int i = 0; i < 2 * BQ / 4; ++i) {
+            const int row = 4 * (i & 31) + r4, tok = row / p.r, hr = row - tok * p.r;
+            const int at = u.i0 + (i >> 5) * a.tokens + tok;  // token of the sequence
+            const bool in = tok < a.tokens && at <= u.i1 &&
+                            in_bounds(pc.row0 + at < p.n_tokens && pc.hk * p.r + hr < p.H, err, 121);
+            const uint8_t* src = p.q + (in ? static_cast<long long>(pc.row0 + at) * p.q_stride + (pc.hk * p.r + hr) * (HD * 2) + c * 16 : 0);
+            cp_async16(sQ + (i >> 5) * Q_BYTES + (i & 31) / 2 * 1024 + (i & 1 ? odd : even), src, in);
+          }
+          commit(q_full);
+        }
+#pragma unroll 1
+        for (int j = pc.k0; j < pc.k1; ++j, ++kc) {
+          const int st = kc % NK;
+          static_assert(NK == NV, "one ring arithmetic for both");
+          // places of the step's keys, four a lane, as units of 16 bytes from the pages' beginning (-1: not there)
+          const int key0 = u.ks.key0(j, BKV);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = key0 + 32 * i + lane;
+            long long unit = -1;
+            if (u.ks.seen(key)) {
+              const int pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+              const int page = in_bounds(pc.seq < p.n_seqs && pi < p.max_pages, err, 122) ? p.table[pc.seq * p.table_stride + pi] : -1;
+              if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.n_pages))
+                unit = static_cast<long long>(static_cast<uint64_t>(page) * page16 + static_cast<uint32_t>(key - pi * p.page_size) * p.row16);
+              else
+                *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (80u << 8);
+            }
+            places[warp][32 * i + lane] = unit;
+          }
+          __syncwarp();
+          if (!acquire(is_k ? k_empty(st) : v_empty(st), ((kc / NK) & 1) ^ 1u, is_k ? 11 : 10)) {
+            ok = false;
+            break;
+          }
+          const uint32_t head = pc.hk * (HD * 2 / 16) + c, dst = ring + st * KV_BYTES;
+#pragma unroll 4
+          for (int i = 0; i < BKV / 8; ++i) {
+            const long long x = places[warp][8 * i + r4], y = places[warp][8 * i + 4 + r4];
+            cp_async16(dst + i * 1024 + even, pages + (x >= 0 ? (x + head) << 4 : 0), x >= 0);
+            cp_async16(dst + i * 1024 + odd, pages + (y >= 0 ? (y + head) << 4 : 0), y >= 0);
+          }
+          __syncwarp();  // (before the places of the next step)
+          commit(is_k ? k_full(st) : v_full(st));
+        }
+        if (!is_k) give(np);
+      }
+      flush();  // (also on the error path: the copies land before the CTA exits)
+    } else {
+      // ---------------- UMMA issuers: warp 2 S_A and S_B, warp 3 O_A and O_B. The whole warp waits; lane 0 issues.
+      bool ok = true;
+      if (warp == 2) {
+        constexpr uint32_t idesc_s = idesc_bf16_f32(BQ, BKV, false);  // B = K tile, K-major, N = 128
+        int kc = 0;  // K tiles consumed, across pieces
+        for (int np = 0; ok && take(np); ++np) {
+          if (!mbar_wait_warp(q_full, np & 1, wc, 12)) break;
+#pragma unroll 1
+          for (int j = pieces[np % NP].k0, j1 = pieces[np % NP].k1; j < j1; ++j, ++kc) {
+            const int st = kc % NK;
+            if (!mbar_wait_warp(k_full(st), (kc / NK) & 1, wc, 13)) { ok = false; break; }
+            const uint64_t kdesc = sdesc_sw128(sK + st * KV_BYTES, 16, 1024);
+#pragma unroll 1
+            for (int t = 0; t < 2 && ok; ++t) {
+              if (kc >= 1 && !mbar_wait_warp(s_free(t), (kc - 1) & 1, wc, 14)) { ok = false; break; }
+              tc_fence_after();
+              if (lane == 0) {
+                const uint64_t qdesc = sdesc_sw128(sQ + t * Q_BYTES, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < HD / 16; ++k) umma_bf16_ss(tS(t), qdesc + k * 2, kdesc + k * 2, idesc_s, k > 0);
+                umma_commit(s_full(t));
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+            if (lane == 0) umma_commit(k_empty(st));
+          }
+          if (ok && lane == 0) umma_commit(q_empty);  // the Q tiles are free once the piece's S products are done
+          give(np);
+        }
+      } else {
+        constexpr uint32_t idesc_o = idesc_bf16_f32(BQ, HD, true);  // B = V tile, MN-major, N = 64
+        int vc = 0;  // V tiles consumed, across pieces
+        for (int np = 0; ok && take(np); ++np) {
+          const int k0 = pieces[np % NP].k0, k1 = pieces[np % NP].k1;
+#pragma unroll 1
+          for (int j = k0; ok && j < k1; ++j, ++vc) {
+            const int st = vc % NV;
+            if (!mbar_wait_warp(v_full(st), (vc / NV) & 1, wc, 15)) { ok = false; break; }
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t) {
+              if (!mbar_wait_warp(p_full(t), vc & 1, wc, 16)) { ok = false; break; }
+              tc_fence_after();
+              if (lane == 0) {
+                const uint64_t vdesc = sdesc_sw128(sV + st * KV_BYTES, 1024, 1024);
+                const uint64_t pdesc = sdesc_sw128(sP + t * P_BYTES, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < BKV / 16; ++k)  // (64 keys a block of 128-byte rows)
+                  umma_bf16_ss(tO(t), pdesc + (k >> 2) * (P_BYTES / 2 >> 4) + (k & 3) * 2, vdesc + k * 128, idesc_o,
+                               (j > k0 || k > 0) ? 1u : 0u);
+#pragma unroll
+                for (int k = 0; k < BKV / 16; ++k) umma_bf16_ts(tO(t), tP(t) + 8 * k, vdesc + k * 128, idesc_o, 1u);
+                umma_commit(pv_done(t));
+                if (t == 1) umma_commit(v_empty(st));
+              }
+              __syncwarp();
+            }
+          }
+          give(np);
+        }
+      }
+      // Every MMA this thread issued completes before TMEM is released.
+      if (lane == 0) {
+        umma_commit(drain);
+        mbar_wait_drain(drain, 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs) : "memory");
+    // ---------------- softmax / correction / output: one query row per thread
+    const int t = (warp - 4) >> 2;  // query tile of this warpgroup
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    bool ok = true;
+    int g = 0;  // steps processed, across pieces
+    const int tok = row / p.r, hr = row - tok * p.r;  // token of the tile and head of the group this row holds
+    const float scale_log2 = p.scale_log2;
+    for (int np = 0; ok && take(np); ++np) {
+      const Piece& pc = pieces[np % NP];
+      // (what concerns the piece stays in shared memory until it is needed: the registers hold scores)
+      float m = -CUDART_INF_F;  // running maximum, in units of scale_log2
+      float l = 0.0f;           // running denominator
+#pragma unroll 1
+      for (int j = pc.k0; j < pc.k1; ++j, ++g) {
+        if (!mbar_wait_warp(s_full(t), g & 1, wc, 17)) { ok = false; break; }
+        tc_fence_after();
+        const int key0 = pc.u.ks.key0(j, BKV);
+        const int first = pc.pos0 + pc.u.i0 + t * a.tokens, last = pc.pos0 + pc.u.i1;  // (of the tile's tokens, and of all)
+        // visible: key <= hi and (key > hi - window or key < sinks); rows without a token see what the unit's last one does
+        const bool border = key0 + BKV - 1 > first || (key0 <= last - p.window && key0 + BKV > p.sinks);
+        const int ca = min(first + tok, last) - key0 + 1, cb = ca - p.window, cd = p.sinks - key0;  // keys [cb, ca), and [0, cd) below ca
+        auto hide = [&](uint32_t (&r)[32], int c0) {  // scores of keys c0 .. c0 + 31 of the step
+          auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+          const uint32_t sees = below(ca - c0) & (~below(cb - c0) | below(cd - c0));
+#pragma unroll
+          for (int c = 0; c < 32; ++c) r[c] = (sees >> c) & 1u ? r[c] : 0xff800000u;
+        };
+        // The row's scores are read twice, for the maximum and for the exponentials, 32 at a time in loops that are not unrolled: with
+        // all 128 in registers and unrolled loops, warps waited for instructions more than for anything else.
+        float mx = -CUDART_INF_F;
+#pragma unroll 1
+        for (int b = 0; b < 4; b += 2) {
+          uint32_t r[2][32];
+          tmem_ld_32x32b_x32(tS(t) + lane_off + 32 * b, r[0]);
+          tmem_ld_32x32b_x32(tS(t) + lane_off + 32 * b + 32, r[1]);
+          tmem_ld_wait();
+          if (border) {
+            hide(r[0], 32 * b);
+            hide(r[1], 32 * b + 32);
+          }
+          float mc[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // independent chains of three-input max
+            auto at = [&](int e) { return __uint_as_float(r[k >> 1][16 * (k & 1) + e]); };
+            float x = fmax3(at(0), at(1), at(2));
+#pragma unroll
+            for (int e = 3; e < 15; e += 2) x = fmax3(x, at(e), at(e + 1));
+            mc[k] = fmaxf(x, at(15));
+          }
+          mx = fmaxf(fmax3(mx, mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+        }
+        const float mx_s = mx * scale_log2;
+        const float m_new = (mx_s > m + kRescaleThreshold) ? mx_s : m;
+        const float ref = m_new == -CUDART_INF_F ? 0.0f : m_new;  // (nothing visible so far: weights of 0)
+        const float alpha = ex2_approx(m - ref);  // 0 on the first step (m = -inf)
+
+        if (j > pc.k0) {
+          // PV[j-1] must be complete: P is overwritten below and O may be rescaled.
+          if (!mbar_wait_warp(pv_done(t), (g - 1) & 1, wc, 18)) { ok = false; break; }
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, m_new != m)) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(tO(t) + lane_off + half * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+              tmem_st_32x32b_x32(tO(t) + lane_off + half * 32, o);
+            }
+          }
+        }
+
+        // p = 2^(s * scale_log2 - m_new): packed fp32x2 FMA for the argument, packed adds for the row sum; P is cut into its
+        // two bf16 parts, 32 keys at a time: the large part into the tile's P columns of TMEM, the small one into its swizzled
+        // rows of shared memory (16 bytes are 8 keys).
+        const uint64_t c2 = pack_f32x2(scale_log2, scale_log2);
+        const uint64_t nm2 = pack_f32x2(-ref, -ref);
+        uint64_t sum2a = pack_f32x2(0.0f, 0.0f), sum2b = sum2a;
+        const uint64_t minus1 = pack_f32x2(-1.0f, -1.0f);
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+          uint32_t r[32], pk[16], pl[16];
+          tmem_ld_32x32b_x32(tS(t) + lane_off + 32 * b, r);
+          tmem_ld_wait();
+          if (border) hide(r, 32 * b);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float a0, a1;
+            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), c2, nm2), a0, a1);
+            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+            const uint64_t pp = pack_f32x2(p0, p1);
+            if (i & 1) sum2b = add_f32x2(sum2b, pp);
+            else sum2a = add_f32x2(sum2a, pp);
+            pk[i] = pack_bf16x2(p0, p1);
+            float l0, l1;  // what the large part leaves (exact)
+            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(pk[i] << 16), __uint_as_float(pk[i] & 0xffff0000u)), minus1, pp), l0, l1);
+            pl[i] = pack_bf16x2(l0, l1);
+          }
+          const uint32_t to = sP + t * P_BYTES + (b >> 1) * (P_BYTES / 2) + row * 128u;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            sts_v4(to + (((4 * (b & 1) + c) ^ (row & 7)) << 4), pl[4 * c], pl[4 * c + 1], pl[4 * c + 2], pl[4 * c + 3]);
+          tmem_st_32x32b_x16(tP(t) + lane_off + 16 * b, pk);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free(t));  // the MMA may overwrite S with the next step's
+        float sa0, sa1, sb0, sb1;
+        unpack_f32x2(sum2a, sa0, sa1);
+        unpack_f32x2(sum2b, sb0, sb1);
+        const float sum = (sa0 + sa1) + (sb0 + sb1);
+        fence_proxy_async_smem();
+        tmem_st_wait();
+        l = l * alpha + sum;
+        m = m_new;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(t));
+      }
+      if (!ok || !mbar_wait_warp(pv_done(t), (g - 1) & 1, wc, 19)) break;
+      // The piece's result, from O in TMEM once the PV product of its last step is done; the next piece's first PV product
+      // (which overwrites O) waits for P that this warp writes only after these reads.
+      tc_fence_after();
+      const bool whole = pc.k0 == 0 && pc.k1 == pc.n;
+      const int i = pc.u.i0 + t * a.tokens + tok;  // the row's token of the sequence
+      const bool mine = tok < a.tokens && i <= pc.u.i1;
+      const int token = pc.row0 + i, head = pc.hk * p.r + hr;
+      const bool put = mine && in_bounds(token >= 0 && token < p.n_tokens && head < p.H, err, 123);
+      const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+      const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (pc.k0 == 0 ? 1 : 0);
+      float zero = l * 0.0f;  // a number, as long as all of the row's are
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(tO(t) + lane_off + half * 32, o);
+        tmem_ld_wait();
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<long long>(token) * p.out_stride + head * (HD * 2) + half * 64);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              f[e] = __uint_as_float(o[8 * q + e]);
+              zero = fmaf(f[e], 0.0f, zero);
+            }
+            if (put)
+              dst[q] = make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
+                                  pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
+          }
+        } else if (put) {
+          float4* d4 = reinterpret_cast<float4*>(a.part_o + (slot * 2 * BQ + t * BQ + row) * HD + half * 32);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            d4[q] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]), __uint_as_float(o[4 * q + 2]),
+                                __uint_as_float(o[4 * q + 3]));
+        }
+      }
+      tc_fence_before();
+      if (!whole) {
+        if (put) a.part_ml[slot * 2 * BQ + t * BQ + row] = make_float2(m, l);
+        if (warp == 4 && lane == 0 && pc.k0 == 0) {  // the first piece of a unit that is cut: how many follow
+          long long c = blockIdx.x + 1;
+          while (c < of_run[1] && of_run[0] * c / of_run[1] < pc.end) ++c;
+          a.cuts[blockIdx.x] = ChunkCut{pc.seq, pc.hk, pc.x, static_cast<int>(c - blockIdx.x)};
+        }
+      } else {
+        for (uint32_t some = __ballot_sync(0xffffffffu, put && !(zero == 0.0f)); some; some &= some - 1) {  // (rare: see chunk_redo)
+          const int who = __ffs(some) - 1;
+          const int w_token = __shfl_sync(0xffffffffu, token, who), w_head = __shfl_sync(0xffffffffu, head, who);
+          const int w_pos = pc.pos0 + __shfl_sync(0xffffffffu, i, who), c8 = (lane & 7) * 8;
+          float v[8], w_l = CUDART_NAN_F;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = CUDART_NAN_F;
+          chunk_redo<__nv_bfloat16>(p, pc.seq, pc.hk, p.q + static_cast<long long>(w_token) * p.q_stride + w_head * (HD * 2), w_pos, true,
+                                              pc.u.ks.lo, pc.u.ks.hi, pc.u.ks.first, c8, v, &w_l, err);
+          if (lane < 8) chunk_write8<__nv_bfloat16>(p, w_token, w_head, c8, v, w_l, err);
+        }
+      }
+      give(np);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+// Units that were cut: block (c, y) joins rows 32 y .. of the unit whose first piece CTA c wrote with those of the CTAs behind it.
+__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ ChunkTcArgs a,
+                                                         uint32_t* err) {
+  pdl_trigger();
+  pdl_wait();
+  const ChunkCut cut = a.cuts[blockIdx.x];
+  if (cut.pieces == 0) return;
+  const ChunkSeq sq = chunk_seq(p, cut.seq, err);
+  const Unit u(p, sq.m, sq.len, a.per_unit, cut.x);
+  const int row = 32 * blockIdx.y + (threadIdx.x >> 3), c8 = (threadIdx.x & 7) * 8;  // 8 threads a row
+  const int t = row / BQ, tok = row % BQ / p.r, hr = row % BQ - tok * p.r;
+  const int i = u.i0 + t * a.tokens + tok, token = sq.row0 + i, head = cut.hk * p.r + hr;
+  const bool in = tok < a.tokens && i <= u.i1 && in_bounds(token < p.n_tokens && head < p.H, err, 124);
+  // piece k: the first CTA's second slot, then the first slots of the CTAs behind it
+  auto slot = [&](int k) { return (2 * static_cast<size_t>(blockIdx.x + k) + (k == 0 ? 1 : 0)) * 2 * BQ + row; };
+  float v[8] = {}, m = -CUDART_INF_F, l = 0.0f;
+  if (in) {
+    for (int k = 0; k < cut.pieces; ++k) m = fmaxf(m, a.part_ml[slot(k)].x);
+    const float ref = m == -CUDART_INF_F ? 0.0f : m;
+#pragma unroll 2
+    for (int k = 0; k < cut.pieces; ++k) {
+      const float2 ml = a.part_ml[slot(k)];
+      const float4* o = reinterpret_cast<const float4*>(a.part_o + slot(k) * HD + c8);
+      const float4 o0 = o[0], o1 = o[1];
+      const float f = ex2_approx(ml.x - ref);
+      l += f * ml.y;
+      v[0] += f * o0.x; v[1] += f * o0.y; v[2] += f * o0.z; v[3] += f * o0.w;
+      v[4] += f * o1.x; v[5] += f * o1.y; v[6] += f * o1.z; v[7] += f * o1.w;
+    }
+  }
+  if (__any_sync(0xffffffffu, in && !chunk_numbers(v, l))) {
+    const int tt = in ? token : sq.row0, hh = in ? head : 0;
+    chunk_redo<__nv_bfloat16>(p, cut.seq, cut.hk, p.q + static_cast<long long>(tt) * p.q_stride + hh * (HD * 2), sq.len - sq.m + i, in,
+                              u.ks.lo, u.ks.hi, u.ks.first, c8, v, &l, err);
+  }
+  if (in) chunk_write8<__nv_bfloat16>(p, token, head, c8, v, l, err);
+}
+
+}  // namespace
+
+namespace wenc_host {
+
+size_t chunk_tc_workspace(int sms) {
+  return (static_cast<size_t>(sms) * sizeof(ChunkCut) + 255) / 256 * 256 + static_cast<size_t>(sms) * 2 * 2 * BQ * (HD * sizeof(float) + sizeof(float2));
+}
+
+cudaError_t launch_chunk_tc(const ChunkParams& p, int few, void* workspace, uint32_t* err, int sms, cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static std::atomic<int> configured{-1};
+  e = opt_in_smem(chunk_tc_kernel, SMEM, dev, configured);
+  if (e != cudaSuccess) return e;
+  // The softmax warpgroups' register increase is met only from the registers the CTA was launched with: refuse to
+  // launch a build that was given fewer (a property of the build).
+  static const int launch_regs = registers_of(chunk_tc_kernel);
+  if (launch_regs * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
+  ChunkTcArgs a;
+  a.few = few;
+  a.tokens = BQ / p.r;
+  a.per_unit = 2 * a.tokens;
+  uint8_t* room = static_cast<uint8_t*>(workspace);
+  a.cuts = reinterpret_cast<ChunkCut*>(room);
+  a.part_o = reinterpret_cast<float*>(room + (static_cast<size_t>(sms) * sizeof(ChunkCut) + 255) / 256 * 256);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(sms) * 2 * 2 * BQ * HD);
+  e = launch_pdl(chunk_tc_kernel, dim3(sms), dim3(kThreads), SMEM, stream, p, a, err);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(chunk_join_kernel, dim3(sms, 2 * BQ / 32), dim3(256), 0, stream, p, a, err);
+}
+
+}  // namespace wenc_host

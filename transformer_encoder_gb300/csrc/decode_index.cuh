@@ -95,6 +95,7 @@ struct KeySteps {
   int lo, hi, first;      // keys [lo, hi) and [0, first)
   int n_first, lo_step, n;
 
+  KeySteps() = default;
   __host__ __device__ __forceinline__ KeySteps(int pos0, int pos1, int window, int sinks, int step, int align) {
     hi = pos1 + 1 > 0 ? pos1 + 1 : 0;
     const long long l = static_cast<long long>(pos0) + 1 - window;
