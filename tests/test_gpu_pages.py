@@ -58,7 +58,8 @@ def _want(c, new, rows):
 
 @pytest.mark.parametrize("n,most,past,page,pad", [
     (1, 1, 0, 16, 0), (1, 1, 16, 16, 1), (3, 2, 5, 1, 0), (7, 40, 100, 16, 5), (256, 1, 500, 16, 0), (33, 600, 50, 24, 3),
-    (513, 9, 33, 8, 100), (2047, 3, 10, 16, 2), (2049, 20, 100, 64, 1), (5000, 2, 4, 3, 0), (2, 9000, 3, 5, 7)])
+    (513, 9, 33, 8, 100), (2047, 3, 10, 16, 2), (2049, 20, 100, 64, 1), (5000, 2, 4, 3, 0), (2, 9000, 3, 5, 7), (512, 3, 40, 16, 1),
+    (2048, 1, 40, 16, 0), (9000, 1, 4, 8, 0), (9000, 0, 4, 8, 9), (20000, 1, 30, 16, 3)])
 def test_extend(n, most, past, page, pad):
     from transformer_encoder_gb300 import sync_status
     r = np.random.default_rng(n + most)

@@ -1226,7 +1226,7 @@ int wenc_selftest_chunk_steps(int first, int last, int window, int sinks, int st
 void wenc_selftest_gives(int len, int finished, int gone, int window, int sinks, int page_size, int32_t* out) {
   if (!out || len < 0 || gone < 0 || window < 0 || sinks < 0 || page_size < 1) return;
   int mark;
-  const int4 x = wenc_dev::gives(len, finished != 0, gone, window, window > 0 ? static_cast<int>(wenc_dev::pages_of(sinks, page_size)) : 0,
+  const int4 x = wenc_dev::gives(len, finished != 0, gone, window, window > 0 ? wenc_dev::pages_of(sinks, page_size) : 0,
                                  page_size, mark);
   const int v[5] = {x.x, x.y, x.z, x.w, mark};
   for (int i = 0; i < 5; ++i) out[i] = v[i];

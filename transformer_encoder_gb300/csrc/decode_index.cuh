@@ -112,14 +112,16 @@ struct KeySteps {
 
 // ------------------------------------------------------------------ pages (pages.cu)
 // The pages that n tokens take.
-__host__ __device__ __forceinline__ long long pages_of(long long n, int page_size) { return (n + page_size - 1) / page_size; }
+__host__ __device__ __forceinline__ int pages_of(int n, int page_size) {
+  return static_cast<int>((static_cast<uint32_t>(n) + static_cast<uint32_t>(page_size) - 1u) / static_cast<uint32_t>(page_size));
+}
 
 // The table entries that a sequence of `len` tokens gives back, as ranges [x, y) and [z, w). `gone`: entries below it went
 // back in earlier calls, but for the first `first` ones, which stay while the sequence does. A window (0: none) is past an
 // entry when no later token sees any of its keys: the next one, at position len, sees those behind len - window. mark: the
 // `gone` of the next call.
 __host__ __device__ __forceinline__ int4 gives(int len, bool finished, int gone, int window, int first, int page_size, int& mark) {
-  const int total = static_cast<int>(pages_of(len, page_size));
+  const int total = pages_of(len, page_size);
   const int low = first > gone ? first : gone;
   if (finished) {
     mark = 0;

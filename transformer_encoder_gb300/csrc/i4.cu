@@ -46,6 +46,15 @@ __device__ __forceinline__ uint32_t widen_pair(uint32_t w, int s) {
   return *reinterpret_cast<const uint32_t*>(&y);
 }
 
+// Weights 2 i and 2 i + 1 of a word as bf16 (hi: the word shifted right by 4), likewise.
+__device__ __forceinline__ uint32_t widen_byte(uint32_t w, uint32_t hi, int i) {
+  // (bytes i of both: the low one's low half in bits 0 .. 3, the high one's in bits 16 .. 19)
+  uint32_t v = (__byte_perm(w, hi, i | i << 4 | (4 + i) << 8 | (4 + i) << 12) & 0x000f000fu) | 0x43004300u;
+  const __nv_bfloat162 base = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));  // 136
+  const __nv_bfloat162 y = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&v), base);
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+
 __device__ __forceinline__ float scale_at(const I4Params& p, size_t i) {
   return p.scale_f32 ? __ldg(static_cast<const float*>(p.scale) + i)
                      : __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p.scale) + i)) << 16);
@@ -73,6 +82,22 @@ __device__ __forceinline__ void put(const I4Params& p, size_t at, float v) {
   if (p.epilogue == WENC_EPI_BIAS_GELU_BF16) v = gelu_erf(v);
   if (p.out_f32) static_cast<float*>(p.out)[at] = v;
   else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+}
+
+// Four neighbours; res: the residual's.
+__device__ __forceinline__ void put4(const I4Params& p, size_t at, float4 v, const float4& res) {
+  if (p.epilogue == WENC_EPI_BIAS_RESID_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(res.x + v.x, res.y + v.y, res.z + v.z, res.w + v.w);
+  } else if (p.out_f32) {
+    if (p.epilogue == WENC_EPI_BIAS_GELU_BF16) v = make_float4(gelu_erf(v.x), gelu_erf(v.y), gelu_erf(v.z), gelu_erf(v.w));
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = v;
+  } else {
+    if (p.epilogue == WENC_EPI_BIAS_GELU_BF16) {
+      gelu_erf_x2(v.x, v.y);
+      gelu_erf_x2(v.z, v.w);
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  }
 }
 
 // ---------------------------------------------------------------- few tokens
@@ -205,10 +230,325 @@ __global__ void __launch_bounds__(32 * kRowsWarps) i4_rows_kernel(const __grid_c
   }
 }
 
+// ---------------------------------------------------------------- many tokens
+// out^T = W x^T on tcgen05: a CTA takes 128 channels (the MMA's M, TMEM's lanes) and up to 160 tokens (its N), and the CTAs of a cluster share K
+// where there are few tiles. Four warps widen the weights from global memory straight into TMEM, a channel a thread: the A
+// operand. x comes by TMA as it lies (float32: its three parts, cut apart by i4_split_kernel first). A group's products make an
+// accumulator of their own, one of two in TMEM; eight warps, a channel a thread again, add it times the group's scale to
+// their sums in registers while the MMAs fill the other. So a scale is one number a thread and group, and no weight is rounded.
+// What bounds it: the MMAs (80 cycles for each 16 inputs of 160 tokens), and with groups of 32 the reading of accumulators.
+constexpr int kTcMost = 160;                // tokens of a tile
+constexpr int kTcThreads = 512;             // 4 widening warps, MMA issuer, TMA producer, 2 idle, 8 summing warps
+constexpr int kAStages = 2, kXStages = 5;   // of 128 inputs
+constexpr uint32_t kXHalf = kTcMost * 128;  // 64 inputs of a tile's tokens
+constexpr uint32_t kXBytes = 2 * kXHalf;
+constexpr uint32_t kTcBars = kXStages * kXBytes;
+constexpr int kTcNumBars = 2 * kAStages + 2 * kXStages + 4 + 1;
+constexpr size_t kTcSmem = 1024 + kTcBars + kTcNumBars * 8 + 16;
+constexpr uint32_t kTcColumns = 512;        // sums 0..159, 160..319; A stages from 384 on, 64 each
+static_assert(kTcSmem <= 232448 && kTcMost * 128 * 4 <= static_cast<int>(kTcBars), "the sums of the output lie over the stages");
+
+struct I4Tc {
+  int tok, n_tiles;  // tokens of a tile; channel tiles
+};
+
+// PARTS of x: 1, or 3 (planes of M rows).
+template <int PARTS>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    i4_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ I4Params p, const I4Tc c, uint32_t* err) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t s0 = smem_u32(smem), bar0 = s0 + kTcBars;
+  auto a_full = [&](int i) { return bar0 + 8u * i; };
+  auto a_empty = [&](int i) { return bar0 + 8u * (kAStages + i); };
+  auto x_full = [&](int i) { return bar0 + 8u * (2 * kAStages + i); };
+  auto x_empty = [&](int i) { return bar0 + 8u * (2 * kAStages + kXStages + i); };
+  auto d_full = [&](int i) { return bar0 + 8u * (2 * kAStages + 2 * kXStages + i); };
+  auto d_empty = [&](int i) { return bar0 + 8u * (2 * kAStages + 2 * kXStages + 2 + i); };
+  const uint32_t drain = bar0 + 8u * (2 * kAStages + 2 * kXStages + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kTcBars + kTcNumBars * 8);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  const WaitCtx wc{abort_flag, err};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % p.ksplit, tile = blockIdx.x / p.ksplit;
+  const int n0 = tile % c.n_tiles * 128, m0 = tile / c.n_tiles * c.tok, m_here = min(c.tok, p.M - m0);
+  // this CTA's share of K, in pieces of 128 (whole groups)
+  const int pieces = p.K / kPiece, per = (pieces + p.ksplit - 1) / p.ksplit;
+  const int first = min(rank * per, pieces), n_pieces = min(per, pieces - first);
+  const int k_begin = first * kPiece, n_groups = n_pieces * kPiece / p.group;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kAStages; ++i) {
+      mbar_init(a_full(i), 4);   // the widening warps
+      mbar_init(a_empty(i), 1);  // the MMAs' commit
+    }
+    for (int i = 0; i < kXStages; ++i) {
+      mbar_init(x_full(i), 1);
+      mbar_init(x_empty(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(d_full(i), 1);
+      mbar_init(d_empty(i), 8);  // the summing warps
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0u;
+    fence_barrier_init();
+    tma_prefetch_desc(&tx);
+  }
+  if (warp == 4) {
+    tmem_alloc(smem_u32(tmem_slot), kTcColumns);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();  // TMEM is held: the next kernel may be scheduled
+  pdl_wait();
+  auto tD = [&](int i) { return tmem + kTcMost * i; };
+  auto tA = [&](int i) { return tmem + 384u + 64u * i; };
+  const bool fits = in_bounds(n0 + 128 <= p.N && k_begin + n_pieces * kPiece <= p.K && m0 < p.M, err, 125);
+
+  bool ok = fits;
+  if (warp < 4) {
+    // ---------------- widening: thread = channel; the next piece's weights are under way
+    const uint4* row = reinterpret_cast<const uint4*>(p.w + static_cast<size_t>(n0 + threadIdx.x) * (p.K / 2) + k_begin / 2);
+    uint4 w[4];
+    auto fetch = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __ldg(row + 4 * j + i);
+    };
+    if (ok && n_pieces > 0) fetch(0);
+#pragma unroll 1
+    for (int j = 0; ok && j < n_pieces; ++j) {
+      const int st = j % kAStages;
+      uint32_t r[2][32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t v[8] = {w[2 * h].x, w[2 * h].y, w[2 * h].z, w[2 * h].w, w[2 * h + 1].x, w[2 * h + 1].y, w[2 * h + 1].z, w[2 * h + 1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) r[h][4 * i + e] = widen_byte(v[i], v[i] >> 4, e);
+      }
+      if (j + 1 < n_pieces) fetch(j + 1);
+      if (!mbar_wait_warp(a_empty(st), ((j / kAStages) & 1) ^ 1u, wc, 60)) break;
+      tc_fence_after();
+      tmem_st_32x32b_x32(tA(st) + (static_cast<uint32_t>(32 * warp) << 16), r[0]);
+      tmem_st_32x32b_x32(tA(st) + 32u + (static_cast<uint32_t>(32 * warp) << 16), r[1]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(a_full(st));
+    }
+  } else if (warp == 4) {
+    // ---------------- MMA issuer, one thread. What it does between MMAs is all that keeps them apart, so nothing is divided or
+    // looked up: slots and parities run along (with remainders and descriptors formed for each MMA, 2700 cycles a 64 inputs).
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(128, (m_here + 15) / 16 * 16, false);
+      const int ends = p.group / 16 - 1;  // a group ends behind the MMA steps whose number has these bits set
+      uint32_t a_slot = 0, a_par = 0, x_slot = 0, x_par = 0, buf = 0, d_par = 1;
+      bool fresh = true;  // the next step begins a group
+#pragma unroll 1
+      for (int j = 0; ok && j < n_pieces; ++j) {
+        uint64_t desc[PARTS];
+        uint32_t x_bar[PARTS];
+        ok = mbar_wait(a_full(a_slot), a_par, wc, 61);
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+          ok = ok && mbar_wait(x_full(x_slot), x_par, wc, 62);
+          desc[q] = sdesc_sw128(s0 + x_slot * kXBytes, 16, 1024);
+          x_bar[q] = x_empty(x_slot);
+          if (++x_slot == kXStages) {
+            x_slot = 0;
+            x_par ^= 1u;
+          }
+        }
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t a_at = tA(a_slot);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (fresh) {
+            if (!mbar_wait(d_empty(buf), d_par, wc, 63)) { ok = false; break; }
+            tc_fence_after();
+          }
+          const uint32_t d_at = tmem + (buf ? static_cast<uint32_t>(kTcMost) : 0u);
+#pragma unroll
+          for (int q = 0; q < PARTS; ++q)
+            umma_bf16_ts(d_at, a_at + 8 * k, desc[q] + (k >> 2) * (kXHalf >> 4) + 2 * (k & 3), idesc, !fresh || q > 0 ? 1u : 0u);
+          fresh = (k & ends) == ends;
+          if (fresh) {
+            umma_commit(d_full(buf));
+            buf ^= 1u;
+            if (buf == 0) d_par ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit(a_empty(a_slot));
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) umma_commit(x_bar[q]);
+        if (++a_slot == kAStages) {
+          a_slot = 0;
+          a_par ^= 1u;
+        }
+      }
+      // every MMA issued completes before anything is freed
+      umma_commit(drain);
+      mbar_wait_drain(drain, 0);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    // ---------------- x by TMA, its small parts first (the tensor core's sums truncate)
+    if (lane == 0) {
+      int xi = 0;
+      for (int j = 0; ok && j < n_pieces; ++j)
+        for (int q = PARTS - 1; q >= 0; --q, ++xi) {
+          const int st = xi % kXStages;
+          if (!mbar_wait(x_empty(st), ((xi / kXStages) & 1) ^ 1u, wc, 64)) { ok = false; break; }
+          mbar_arrive_expect_tx(x_full(st), static_cast<uint32_t>(c.tok) * 256u);
+          tma_load_2d(s0 + st * kXBytes, &tx, x_full(st), k_begin + kPiece * j, q * p.M + m0);
+          tma_load_2d(s0 + st * kXBytes + kXHalf, &tx, x_full(st), k_begin + kPiece * j + 64, q * p.M + m0);
+        }
+      if (*abort_flag)  // error path: let the copies already issued land before the CTA exits
+        for (int i = (xi > kXStages ? xi - kXStages : 0); i < xi; ++i) mbar_wait_drain(x_full(i % kXStages), (i / kXStages) & 1);
+    }
+    __syncwarp();
+  }
+  // ---------------- summing: thread = channel; warps 8 .. 11 the first half of the tokens, 12 .. 15 the second
+  const int ch = 32 * (warp & 3) + lane, half = c.tok / 2, t0 = warp >= 12 ? half : 0;  // (tok is a multiple of 16)
+  float acc[kTcMost / 2];
+  if (warp >= 8) {
+#pragma unroll
+    for (int i = 0; i < kTcMost / 2; ++i) acc[i] = 0.0f;
+    const size_t s_at = static_cast<size_t>(n0 + ch) * p.groups + k_begin / p.group;
+    float scale[4], next[4];
+    auto fetch = [&](float (&f)[4], int g) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = fits && g + i < n_groups ? scale_at(p, s_at + g + i) : 0.0f;
+    };
+    fetch(scale, 0);
+    for (int g0 = 0; ok && g0 < n_groups; g0 += 4) {
+      fetch(next, g0 + 4);
+#pragma unroll 1
+      for (int i = 0; i < 4 && g0 + i < n_groups; ++i) {
+        const int g = g0 + i, buf = g & 1;
+        const float s = i < 2 ? (i == 0 ? scale[0] : scale[1]) : (i == 2 ? scale[2] : scale[3]);
+        if (!mbar_wait_warp(d_full(buf), (g >> 1) & 1, wc, 65)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t s2 = pack_f32x2(s, s);
+        const uint32_t from = tD(buf) + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + t0;
+        // (columns of the other half or behind the tokens add what nobody reads)
+        auto add = [&](const uint32_t* r, int b, int n) {
+#pragma unroll
+          for (int e = 0; e < n; e += 2) {
+            float x, y;
+            unpack_f32x2(fma_f32x2(s2, pack_f32x2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), pack_f32x2(acc[b + e], acc[b + e + 1])), x, y);
+            acc[b + e] = x;
+            acc[b + e + 1] = y;
+          }
+        };
+        static_assert(kTcMost / 2 == 80, "two loads of 32 and one of 16");
+#pragma unroll
+        for (int b = 0; b < 64; b += 32) {
+          if (b >= half) break;  // (uniform)
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(from + b, r);
+          tmem_ld_wait();
+          add(r, b, 32);
+        }
+        if (half > 64) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(from + 64, r);
+          tmem_ld_wait();
+          add(r, 64, 16);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(d_empty(buf));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) scale[i] = next[i];
+    }
+  }
+  // ---------------- output. The sums go over the stages as [token][channel] (every MMA and copy is done: the sums waited for the
+  // last group, and the last MMA read the last tile); then the warps of the cluster's CTAs share the tokens out, four channels a
+  // lane, in a loop that is small: the epilogue unrolled over 80 sums a thread was 150 KB of code, and 30 us of a cold call.
+  __syncthreads();
+  if (warp >= 8) {
+    float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int i = 0; i < kTcMost / 2; ++i)
+      if (i < half && t0 + i < m_here) part[(t0 + i) * 128 + ch] = acc[i];
+  }
+  if (p.ksplit > 1) cluster_arrive_wait();
+  else __syncthreads();
+  if (fits && !*abort_flag) {
+    constexpr int kAhead = 4;  // tokens whose residual is on its way before the first store (`out` may be `resid`)
+    const int stride = p.ksplit * (kTcThreads / 32);
+    const float4 bn = __ldg(reinterpret_cast<const float4*>(p.bias + n0) + lane);
+#pragma unroll 1
+    for (int t = rank + p.ksplit * warp; t < m_here; t += kAhead * stride) {
+      float4 v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (p.epilogue == WENC_EPI_BIAS_RESID_F32 && t + i * stride < m_here)
+          v[i] = *(reinterpret_cast<const float4*>(p.resid + static_cast<size_t>(m0 + t + i * stride) * p.N + n0) + lane);
+      }
+#pragma unroll 1
+      for (int i = 0; i < kAhead && t + i * stride < m_here; ++i) {
+        const int tt = t + i * stride;
+        float4 y = bn;
+        if (p.ksplit == 1) {
+          const float4 z = *reinterpret_cast<const float4*>(smem + tt * 512 + lane * 16);
+          y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
+        } else {
+          for (int r = 0; r < p.ksplit; ++r) {
+            const float4 z = ld_cluster_f4(rank_addr(s0 + tt * 512 + lane * 16, r));
+            y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
+          }
+        }
+        const float4 res = i < 2 ? (i == 0 ? v[0] : v[1]) : (i == 2 ? v[2] : v[3]);
+        put4(p, static_cast<size_t>(m0 + tt) * p.N + n0 + 4 * lane, y, res);
+      }
+    }
+  }
+  if (p.ksplit > 1) cluster_arrive_wait();  // no CTA leaves while another reads its sums
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTcColumns);
+  }
+}
+
+// float32 rows as three planes of bf16 parts.
+__global__ void __launch_bounds__(256) i4_split_kernel(const float4* __restrict__ x, uint2* __restrict__ planes, long long n4, uint32_t* err) {
+  pdl_trigger();
+  pdl_wait();
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n4; i += gridDim.x * 256ll) {
+    const float4 v = x[i];
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    uint32_t part[4][3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split3(f[e], part[e][0], part[e][1], part[e][2]);
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      planes[q * n4 + i] = make_uint2(__byte_perm(part[0][q], part[1][q], 0x7632), __byte_perm(part[2][q], part[3][q], 0x7632));
+  }
+}
+
 wenc_status bad(wenc_status s, const char* fmt, long long a = 0, long long b = 0) {
   char buf[256];
   snprintf(buf, sizeof(buf), fmt, a, b);
   return wenc_internal_fail(s, buf);
+}
+
+wenc_status launch_failed(cudaError_t e) {
+  char buf[200];
+  snprintf(buf, sizeof(buf), "linear_i4 launch: %s", cudaGetErrorString(e));
+  return wenc_internal_fail(WENC_ERR_CUDA, buf);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -240,11 +580,86 @@ cudaError_t launch_rows(I4Params p, int sms, uint32_t* err, cudaStream_t stream)
   return cudaLaunchKernelEx(&cfg, i4_rows_kernel<T, NT>, p, err);
 }
 
+constexpr int kRowsMost = 16;  // tokens up to which the product runs on mma.sync
+
+size_t split_bytes(int M, int K, int x_dtype) {
+  return M > kRowsMost && x_dtype == WENC_DTYPE_F32 ? (static_cast<size_t>(M) * K * 6 + 255) / 256 * 256 : 0;
+}
+
+// Tokens of a tile and CTAs that share K: the division whose rounds of the machine take least, in cycles of a piece of 128
+// inputs (the MMAs' 4 a token, but no less than widening and, of every group, summing take) and of a CTA's beginning and end.
+constexpr long long kWidenCycles = 600, kSumCycles = 350, kEndCycles = 5000, kJoinCycles = 1500;
+void pick_tiles(int M, int n_tiles, int K, int group, int parts, int sms, int& tok, int& ksplit) {
+  const int least = (M + kTcMost - 1) / kTcMost, pieces = K / kPiece;
+  long long best = -1;
+  for (int tiles = least; tiles <= least + 16 && tiles <= (M + 15) / 16; ++tiles) {
+    const int t = ((M + tiles - 1) / tiles + 15) / 16 * 16;
+    long long piece = 4ll * parts * t;
+    if (piece < kWidenCycles) piece = kWidenCycles;
+    if (piece < kPiece / group * kSumCycles) piece = kPiece / group * kSumCycles;
+    for (int ks = 1; ks <= 8 && pieces >= ks; ks *= 2) {
+      const long long ctas = static_cast<long long>(n_tiles) * ((M + t - 1) / t) * ks, rounds = (ctas + sms - 1) / sms;
+      const long long cost = rounds * ((pieces + ks - 1) / ks * piece + kEndCycles + (ks > 1 ? kJoinCycles : 0));
+      if (best < 0 || cost < best) {
+        best = cost;
+        tok = t;
+        ksplit = ks;
+      }
+    }
+  }
+}
+
+wenc_status launch_tc(I4Params p, bool f32, void* workspace, int sms, uint32_t* err, cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  auto kern = f32 ? i4_tc_kernel<3> : i4_tc_kernel<1>;
+  static std::atomic<int> configured[2] = {{-1}, {-1}};
+  if (e == cudaSuccess) e = wenc_host::opt_in_smem(kern, kTcSmem, dev, configured[f32]);
+  const void* x = p.x;
+  if (e == cudaSuccess && f32) {
+    const long long n4 = static_cast<long long>(p.M) * p.K / 4;
+    long long blocks = (n4 + 255) / 256;
+    if (blocks > 16ll * sms) blocks = 16ll * sms;
+    e = wenc_host::launch_pdl(i4_split_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, static_cast<const float4*>(x),
+                              static_cast<uint2*>(workspace), n4, err);
+    x = workspace;
+  }
+  if (e == cudaSuccess) {
+    I4Tc c;
+    c.n_tiles = p.N / 128;
+    const int parts = f32 ? 3 : 1;
+    pick_tiles(p.M, c.n_tiles, p.K, p.group, parts, sms, c.tok, p.ksplit);
+    const long long tiles = static_cast<long long>(c.n_tiles) * ((p.M + c.tok - 1) / c.tok);
+    if (tiles * p.ksplit > 0x7fffffffll) return bad(WENC_ERR_UNSUPPORTED, "linear_i4: %lld tiles pass 2^31 - 1", tiles);
+    CUtensorMap tx;
+    std::string why;
+    if (!wenc_host::make_tmap_2d_bf16(&tx, x, p.K, static_cast<uint64_t>(p.M) * parts, static_cast<uint64_t>(p.K) * 2, 64, c.tok, &why))
+      return wenc_internal_fail(WENC_ERR_INVALID_ARG, why.c_str());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.ksplit));
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = kTcSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.ksplit);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.ksplit > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kern, tx, p, c, err);
+  }
+  return e == cudaSuccess ? WENC_OK : launch_failed(e);
+}
+
 }  // namespace
 
 extern "C" size_t wenc_linear_i4_workspace(int M, int N, int K, int x_dtype, int group) {
   wenc_internal_clear_error();
-  return 0;
+  if (M < 1 || N < 1 || K < 1 || group < 1) return 0;
+  return split_bytes(M, K, x_dtype);
 }
 
 extern "C" wenc_status wenc_linear_i4(const void* x, int x_dtype, const uint8_t* w, const void* w_scale, int scale_dtype,
@@ -284,14 +699,16 @@ extern "C" wenc_status wenc_linear_i4(const void* x, int x_dtype, const uint8_t*
   p.epilogue = epilogue;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool f32 = x_dtype == WENC_DTYPE_F32;
+  if (M > kRowsMost) {
+    const size_t need = split_bytes(M, K, x_dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+      return bad(WENC_ERR_INVALID_ARG, "linear_i4: workspace of %lld bytes needed, %lld given", static_cast<long long>(need),
+                 workspace ? static_cast<long long>(workspace_bytes) : 0ll);
+    if (need > 0 && !aligned(workspace, 256)) return bad(WENC_ERR_INVALID_ARG, "linear_i4: the workspace must be 256-byte aligned");
+    return launch_tc(p, f32, workspace, sms, err, s);
+  }
   cudaError_t e;
   if (M <= 8) e = f32 ? launch_rows<float, 1>(p, sms, err, s) : launch_rows<__nv_bfloat16, 1>(p, sms, err, s);
-  else if (M <= 16) e = f32 ? launch_rows<float, 2>(p, sms, err, s) : launch_rows<__nv_bfloat16, 2>(p, sms, err, s);
-  else e = f32 ? launch_rows<float, 4>(p, sms, err, s) : launch_rows<__nv_bfloat16, 4>(p, sms, err, s);
-  if (e != cudaSuccess) {
-    char buf[200];
-    snprintf(buf, sizeof(buf), "linear_i4 launch: %s", cudaGetErrorString(e));
-    return wenc_internal_fail(WENC_ERR_CUDA, buf);
-  }
-  return WENC_OK;
+  else e = f32 ? launch_rows<float, 2>(p, sms, err, s) : launch_rows<__nv_bfloat16, 2>(p, sms, err, s);
+  return e == cudaSuccess ? WENC_OK : launch_failed(e);
 }

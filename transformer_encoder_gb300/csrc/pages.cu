@@ -43,6 +43,8 @@ struct ExtendParams {
   int32_t *lens_out, *count_out, *seq_start, *positions;
   long long* slots;
   int n_seqs, n_rows, n_free, page_size, max_pages;
+  int page_shift;      // of a power of two, else -1
+  int per;             // sequences a thread takes of a chunk, at most kPer
   int rows_per_block;  // a multiple of 4
 };
 
@@ -71,13 +73,13 @@ __device__ __forceinline__ void block_sum2(long long& a, long long& b, long long
   }
 }
 
-// Exclusive running sums of (a, b) over the block's threads, and the sums in (ta, tb). Begins with a barrier.
-__device__ __forceinline__ void block_scan2(int& a, int& b, int& ta, int& tb, int* part) {
+// Exclusive running sums of (a, b) over the block's threads, and the sums in (ta, tb). Begins with a barrier; `part` as above.
+__device__ __forceinline__ void block_scan2(long long& a, long long& b, long long& ta, long long& tb, long long* part) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int sa = a, sb = b;
+  long long sa = a, sb = b;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int ua = __shfl_up_sync(0xffffffffu, sa, d), ub = __shfl_up_sync(0xffffffffu, sb, d);
+    const long long ua = __shfl_up_sync(0xffffffffu, sa, d), ub = __shfl_up_sync(0xffffffffu, sb, d);
     if (lane >= d) {
       sa += ua;
       sb += ub;
@@ -89,11 +91,11 @@ __device__ __forceinline__ void block_scan2(int& a, int& b, int& ta, int& tb, in
     part[kWarps + warp] = sb;
   }
   __syncthreads();
-  int ba = 0, bb = 0;
+  long long ba = 0, bb = 0;
   ta = tb = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const int pa = part[w], pb = part[kWarps + w];
+    const long long pa = part[w], pb = part[kWarps + w];
     if (w < warp) {
       ba += pa;
       bb += pb;
@@ -112,73 +114,99 @@ __global__ void __launch_bounds__(kThreads) kv_extend_kernel(const ExtendParams 
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x;
-  const long long cap = static_cast<long long>(p.max_pages) * p.page_size;
+  const int cap = p.max_pages * p.page_size;
+  auto pages = [&](int n) {  // that n tokens take
+    return p.page_shift >= 0 ? static_cast<int>((static_cast<uint32_t>(n) + p.page_size - 1u) >> p.page_shift) : pages_of(n, p.page_size);
+  };
   const int count = p.free_count[0];
-  // ---- is there room for all of it? (else the call gives nothing to anyone)
-  long long rows = 0, pages = 0;
-  bool bad_len = false;
-  for (int s = tid; s < p.n_seqs; s += kThreads) {
-    const int m = p.new_tokens[s], l = p.lens[s];
-    if (m < 0 || l < 0 || static_cast<long long>(m) + l > cap) {
-      bad_len = true;
-    } else {
-      rows += m;
-      pages += pages_of(static_cast<long long>(l) + m, p.page_size) - pages_of(l, p.page_size);
-    }
-  }
-  bad_len = __syncthreads_or(bad_len);
-  block_sum2(rows, pages, part);
-  const bool bad_rows = rows > p.n_rows, bad_pages = count < 0 || count > p.n_free || pages > count;
-  const bool bad = bad_len || bad_rows || bad_pages;
-  if (bad && blockIdx.x == 0 && tid == 0) data_error(err, bad_len ? 81 : bad_rows ? 82 : 79);
-  if (blockIdx.x == 0 && tid == 0) {
-    p.count_out[0] = bad ? count : count - static_cast<int>(pages);
-    p.seq_start[0] = 0;
-  }
   const int r0 = static_cast<int>(min(static_cast<long long>(blockIdx.x) * p.rows_per_block, static_cast<long long>(p.n_rows)));
   const int r1 = static_cast<int>(min(static_cast<long long>(r0) + p.rows_per_block, static_cast<long long>(p.n_rows)));
-  const int total = bad ? 0 : static_cast<int>(rows);
+  // Is there room for all of it? (Else the call gives nothing to anyone.) Known from a first pass over the lengths when they are
+  // more than one chunk, else from the chunk's own sums.
+  long long all_rows = 0, all_pages = 0;
+  bool bad_len = false, bad = false;
+  auto fits = [&](int m, int l) { return m >= 0 && l >= 0 && l <= cap && m <= cap - l; };
+  auto judge = [&]() {
+    bad = bad_len || all_rows > p.n_rows || count < 0 || count > p.n_free || all_pages > count;
+    if (blockIdx.x == 0 && tid == 0) {
+      if (bad) data_error(err, bad_len ? 81 : all_rows > p.n_rows ? 82 : 79);
+      p.count_out[0] = bad ? count : count - static_cast<int>(all_pages);
+      p.seq_start[0] = 0;
+    }
+  };
+  const bool one_chunk = p.n_seqs <= kChunk;
+  if (!one_chunk) {
+#pragma unroll 4
+    for (int s = tid; s < p.n_seqs; s += kThreads) {
+      const int m = p.new_tokens[s], l = p.lens[s];
+      if (fits(m, l)) {
+        all_rows += m;
+        all_pages += pages(l + m) - pages(l);
+      } else {
+        bad_len = true;
+      }
+    }
+    bad_len = __syncthreads_or(bad_len);
+    block_sum2(all_rows, all_pages, part);
+    judge();
+  }
 
   int row_base = 0, page_base = 0;
-  for (int c = 0; c * kChunk < p.n_seqs; ++c) {
+  for (int c = 0; c == 0 || c * kChunk < p.n_seqs; ++c) {
     const bool mine = c % gridDim.x == blockIdx.x;
-    // (a chunk whose rows lie behind the block's, and whose lengths are another's, is of no use to it)
-    if (row_base >= r1 && static_cast<int>(blockIdx.x) < c) break;
-    const int s0 = c * kChunk + tid * kPer;
-    int m[kPer], l[kPer], need[kPer], a = 0, b = 0;
+    // (chunks whose rows lie behind the block's are of no use to it, unless a later one's lengths are its own)
+    const int ahead = static_cast<int>((blockIdx.x + gridDim.x - c % gridDim.x) % gridDim.x);
+    if (c > 0 && row_base >= r1 && static_cast<long long>(c + ahead) * kChunk >= p.n_seqs) break;
+    const int s0 = c * kChunk + tid * p.per;  // (per: sequences a thread takes, kPer but in a small batch)
+    int m[kPer], l[kPer], need[kPer];
+    long long a = 0, b = 0, ta, tb;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const bool in = s0 + i < p.n_seqs;
+      const bool in = i < p.per && s0 + i < p.n_seqs;
       m[i] = in ? p.new_tokens[s0 + i] : 0;
       l[i] = in ? p.lens[s0 + i] : 0;
-      if (mine && in) p.lens_out[s0 + i] = bad ? l[i] : l[i] + m[i];
-      if (bad) m[i] = 0;
-      need[i] = bad ? 0 : static_cast<int>(pages_of(static_cast<long long>(l[i]) + m[i], p.page_size) - pages_of(l[i], p.page_size));
-      a += m[i];
-      b += need[i];
     }
-    int ta, tb;
-    block_scan2(a, b, ta, tb, reinterpret_cast<int*>(part));  // (its barrier: the last chunk's rows are done with the tables)
-    a += row_base;
-    b += page_base;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      start[tid * kPer + i] = a;
-      len[tid * kPer + i] = l[i];
-      first_free[tid * kPer + i] = count - 1 - b;
-      a += m[i];
+      const bool ok = !bad && fits(m[i], l[i]);
+      if (!bad && !ok) bad_len = true;
+      need[i] = ok ? pages(l[i] + m[i]) - pages(l[i]) : 0;
+      a += ok ? m[i] : 0;
       b += need[i];
-      if (mine && s0 + i < p.n_seqs) p.seq_start[s0 + i + 1] = a;
     }
-    if (tid == 0) start[kChunk] = row_base + ta;
+    if (one_chunk) bad_len = __syncthreads_or(bad_len);
+    block_scan2(a, b, ta, tb, part);  // (its barrier: the last chunk's rows are done with the tables)
+    if (one_chunk) {
+      all_rows = ta;
+      all_pages = tb;
+      judge();
+      if (bad) a = b = ta = tb = 0;
+    }
+    int ra = static_cast<int>(a) + row_base, pb = static_cast<int>(b) + page_base;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (i >= p.per) break;
+      start[tid * p.per + i] = ra;
+      len[tid * p.per + i] = l[i];
+      first_free[tid * p.per + i] = count - 1 - pb;
+      if (!bad) {
+        ra += m[i];
+        pb += need[i];
+      }
+      if (mine && s0 + i < p.n_seqs) {
+        p.lens_out[s0 + i] = bad ? l[i] : l[i] + m[i];
+        p.seq_start[s0 + i + 1] = ra;
+      }
+    }
+    if (tid == 0) start[kThreads * p.per] = row_base + static_cast<int>(ta);
     __syncthreads();
     // ---- the block's rows of this chunk, four neighbours a thread
-    const int lo = max(r0, row_base), hi = min(r1, row_base + ta);
+    const int lo = max(r0, row_base), hi = min(r1, row_base + static_cast<int>(ta));
     for (int t0 = (lo & ~3) + 4 * tid; t0 < hi; t0 += 4 * kThreads) {
       int s = 0;  // the last sequence of the chunk that starts at or before the first of the rows
       {
         const int t = max(t0, lo);
-        int n = kChunk;
+        int n = kThreads * p.per;
         while (n > 1) {
           const int half = n >> 1;
           if (start[s + half] <= t) {
@@ -198,8 +226,8 @@ __global__ void __launch_bounds__(kThreads) kv_extend_kernel(const ExtendParams 
         slot[i] = -1;
         if (t < lo || t >= hi) continue;
         while (start[s + 1] <= t) ++s;  // (t < hi: a sequence of the chunk has the row)
-        const int at = len[s] + (t - start[s]), entry = at / p.page_size, off = at - entry * p.page_size;
-        const int fresh = entry - static_cast<int>(pages_of(len[s], p.page_size));
+        const int at = len[s] + (t - start[s]), entry = p.page_shift >= 0 ? at >> p.page_shift : at / p.page_size;
+        const int off = at - entry * p.page_size, fresh = entry - pages(len[s]);
         int32_t* place = p.table + static_cast<long long>(c * kChunk + s) * p.table_stride + entry;
         int page = -1;
         if (in_bounds(c * kChunk + s < p.n_seqs && entry >= 0 && entry < p.max_pages, err, 110)) {
@@ -231,11 +259,11 @@ __global__ void __launch_bounds__(kThreads) kv_extend_kernel(const ExtendParams 
           }
       }
     }
-    row_base += ta;
-    page_base += tb;
+    row_base += static_cast<int>(ta);
+    page_base += static_cast<int>(tb);
   }
   // ---- rows behind the last sequence's
-  for (int t = max(r0, total) + tid; t < r1; t += kThreads) {
+  for (int t = max(r0, bad ? 0 : static_cast<int>(all_rows)) + tid; t < r1; t += kThreads) {
     p.positions[t] = 0;
     p.slots[t] = -1;
   }
@@ -274,6 +302,7 @@ __global__ void __launch_bounds__(kThreads) kv_release_kernel(const ReleaseParam
   // ---- all that goes back, and what goes back before this block's
   long long all = 0, before = 0;
   bool bad_len = false;
+#pragma unroll 4
   for (int s = tid; s < p.n_seqs; s += kThreads) {
     int mark;
     const int4 x = spans(s, mark, bad_len);
@@ -393,6 +422,10 @@ extern "C" wenc_status wenc_kv_extend(const wenc_kv_extend_args* a, wenc_stream_
   p.n_free = a->n_free_pages;
   p.page_size = a->page_size;
   p.max_pages = a->max_pages;
+  p.page_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (a->page_size == 1 << s) p.page_shift = s;
+  p.per = a->n_seqs <= kThreads ? 1 : kPer;
   // four rows a thread and pass; two blocks an SM at most
   long long blocks = (static_cast<long long>(a->n_rows) + 4 * kThreads - 1) / (4 * kThreads);
   if (blocks > 2ll * sms) blocks = 2ll * sms;
@@ -442,7 +475,7 @@ extern "C" wenc_status wenc_kv_release(const wenc_kv_release_args* a, wenc_strea
   p.page_size = a->page_size;
   p.max_pages = a->max_pages;
   p.window = a->window;
-  p.first = a->window > 0 ? static_cast<int>(pages_of(a->sinks, a->page_size)) : 0;
+  p.first = a->window > 0 ? pages_of(a->sinks, a->page_size) : 0;
   // (a block reads every length before its own: more sequences a block when there are many)
   const int per = (a->n_seqs + 2 * sms - 1) / (2 * sms);
   p.seqs_per_block = (per + 31) / 32 * 32;

@@ -998,7 +998,8 @@ def chunk_attention(q, k_pages, v_pages, block_table, lens, *, seq_start=None, m
             kps, vps, pages, size, block_table.data_ptr(), tab_stride, max_pages, lens.data_ptr(), start, window or 0,
             sinks, scale)
     ws = ws_bytes = 0
-    if workspace is None:
+    # (float32 calls, and those of up to 16 rows per key head and sequence, never need a workspace)
+    if workspace is None and dt and max_new * H > 16 * kv:
         need = _lib.wenc_chunk_attention_workspace(_CHUNK_PACK.pack(*args, 0, 0))
         workspace = _empty(need, torch.uint8, q.device, stream) if need else None
     if workspace is not None:
@@ -1043,15 +1044,25 @@ def kv_extend(new_tokens, lens, block_table, free_pages, free_count, page_size: 
     if rows < 0:
         raise ValueError(f"rows must not be negative, got {rows}")
 
-    def made(t, size, dtype=i32):
-        return _empty(size, dtype, lens.device, stream) if t is None else t
-    lens_out, free_count_out, seq_start = made(lens_out, n), made(free_count_out, 1), made(seq_start, n + 1)
-    positions, slots = made(positions, rows), made(slots, rows, torch.int64)
+    # (tensors made here need no checks; directly by torch.empty, which costs half of _empty)
+    if lens_out is free_count_out is seq_start is positions is slots is None and stream is None:
+        empty, where = torch.empty, lens.device
+        lens_out, free_count_out = empty(n, dtype=i32, device=where), empty(1, dtype=i32, device=where)
+        seq_start, positions = empty(n + 1, dtype=i32, device=where), empty(rows, dtype=i32, device=where)
+        slots = empty(rows, dtype=torch.int64, device=where)
+        out = (lens_out.data_ptr(), free_count_out.data_ptr(), seq_start.data_ptr(), positions.data_ptr(), slots.data_ptr())
+    else:
+        lens_out = _empty(n, i32, lens.device, stream) if lens_out is None else lens_out
+        free_count_out = _empty(1, i32, lens.device, stream) if free_count_out is None else free_count_out
+        seq_start = _empty(n + 1, i32, lens.device, stream) if seq_start is None else seq_start
+        positions = _empty(rows, i32, lens.device, stream) if positions is None else positions
+        slots = _empty(rows, torch.int64, lens.device, stream) if slots is None else slots
+        out = (_ints(lens_out, "lens_out", n, dev), _ints(free_count_out, "free_count_out", 1, dev),
+               _ints(seq_start, "seq_start", n + 1, dev), _ints(positions, "positions", rows, dev),
+               _ints(slots, "slots", rows, dev, torch.int64))
     status = _lib.wenc_kv_extend(
         _EXTEND_PACK.pack(n, rows, mp, lp, block_table.data_ptr(), tab_stride, max_pages, page_size, fp, free_pages.numel(),
-                          cp, _ints(lens_out, "lens_out", n, dev), _ints(free_count_out, "free_count_out", 1, dev),
-                          _ints(seq_start, "seq_start", n + 1, dev), _ints(positions, "positions", rows, dev),
-                          _ints(slots, "slots", rows, dev, torch.int64)), _raw_stream(stream, dev))
+                          cp, *out), _raw_stream(stream, dev))
     if status:
         _check(status)
     return lens_out, free_count_out, seq_start, positions, slots
@@ -1084,16 +1095,24 @@ def kv_release(lens, block_table, free_pages, free_count, page_size: int, *, fin
     if finished is None and window is None:
         raise ValueError("neither finished nor a window")
     dp = _ints(finished, "finished", n, dev, torch.bool) if finished is not None else 0
-    tp = top = 0
-    lens_out = _empty(n, torch.int32, lens.device, stream) if lens_out is None else lens_out
-    free_count_out = _empty(1, torch.int32, lens.device, stream) if free_count_out is None else free_count_out
-    if window is not None:
-        trimmed_out = _empty(n, torch.int32, lens.device, stream) if trimmed_out is None else trimmed_out
-        tp, top = _ints(trimmed, "trimmed", n, dev), _ints(trimmed_out, "trimmed_out", n, dev)
+    i32 = torch.int32
+    tp = _ints(trimmed, "trimmed", n, dev) if window is not None else 0
+    if lens_out is free_count_out is trimmed_out is None and stream is None:
+        empty, where = torch.empty, lens.device
+        lens_out, free_count_out = empty(n, dtype=i32, device=where), empty(1, dtype=i32, device=where)
+        if window is not None:
+            trimmed_out = empty(n, dtype=i32, device=where)
+        out = (lens_out.data_ptr(), free_count_out.data_ptr(), trimmed_out.data_ptr() if window is not None else 0)
+    else:
+        lens_out = _empty(n, i32, lens.device, stream) if lens_out is None else lens_out
+        free_count_out = _empty(1, i32, lens.device, stream) if free_count_out is None else free_count_out
+        if window is not None and trimmed_out is None:
+            trimmed_out = _empty(n, i32, lens.device, stream)
+        out = (_ints(lens_out, "lens_out", n, dev), _ints(free_count_out, "free_count_out", 1, dev),
+               _ints(trimmed_out, "trimmed_out", n, dev) if window is not None else 0)
     status = _lib.wenc_kv_release(
         _RELEASE_PACK.pack(n, lp, dp, block_table.data_ptr(), tab_stride, max_pages, page_size, window or 0, sinks, tp, fp,
-                           free_pages.numel(), cp, _ints(lens_out, "lens_out", n, dev),
-                           _ints(free_count_out, "free_count_out", 1, dev), top), _raw_stream(stream, dev))
+                           free_pages.numel(), cp, *out), _raw_stream(stream, dev))
     if status:
         _check(status)
     return lens_out, free_count_out, trimmed_out
@@ -1149,7 +1168,7 @@ def linear_i4(x, w, w_scale, bias, epilogue: int = EPI_BIAS_BF16, resid=None, ou
         return out
     x_type, group = int(x.dtype is bf16), K // ssh[1]
     ws = ws_bytes = 0
-    if workspace is None:
+    if workspace is None and M > 16:
         need = _lib.wenc_linear_i4_workspace(M, N, K, x_type, group)
         if need:
             workspace = _empty(need, torch.uint8, x.device, stream)
