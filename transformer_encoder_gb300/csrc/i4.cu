@@ -252,8 +252,8 @@ struct I4Tc {
   int tok, n_tiles;  // tokens of a tile; channel tiles
 };
 
-// PARTS of x: 1, or 3 (planes of M rows).
-template <int PARTS>
+// PARTS of x: 1, or 3 (planes of M rows); groups of GROUP inputs.
+template <int PARTS, int GROUP>
 __global__ void __launch_bounds__(kTcThreads, 1)
     i4_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ I4Params p, const I4Tc c, uint32_t* err) {
   extern __shared__ uint8_t smem_raw[];
@@ -269,7 +269,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kTcBars + kTcNumBars * 8);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const WaitCtx wc{abort_flag, err};
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (numbers of the whole warp come from lane 0, so that the compiler knows them for such: operands of an MMA that it takes
+  // for a lane's own are moved for every MMA)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = blockIdx.x % p.ksplit, tile = blockIdx.x / p.ksplit;
   const int n0 = tile % c.n_tiles * 128, m0 = tile / c.n_tiles * c.tok, m_here = min(c.tok, p.M - m0);
   // this CTA's share of K, in pieces of 128 (whole groups)
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   pdl_trigger();  // TMEM is held: the next kernel may be scheduled
   pdl_wait();
   auto tD = [&](int i) { return tmem + kTcMost * i; };
@@ -342,58 +344,65 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (lane == 0) mbar_arrive(a_full(st));
     }
   } else if (warp == 4) {
-    // ---------------- MMA issuer, one thread. What it does between MMAs is all that keeps them apart, so nothing is divided or
-    // looked up: slots and parities run along (with remainders and descriptors formed for each MMA, 2700 cycles a 64 inputs).
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(128, (m_here + 15) / 16 * 16, false);
-      const int ends = p.group / 16 - 1;  // a group ends behind the MMA steps whose number has these bits set
-      uint32_t a_slot = 0, a_par = 0, x_slot = 0, x_par = 0, buf = 0, d_par = 1;
-      bool fresh = true;  // the next step begins a group
+    // ---------------- MMA issuer: the whole warp waits, one thread issues. A group's MMAs are one straight line behind one election (44
+    // cycles each, or their own time; with a branch between them 110 to 130), and between groups nothing is divided or looked up: slots
+    // and parities run along, and barriers are tested ahead, while MMAs are under way.
+    constexpr int kSteps = GROUP / 16, kGroups = kPiece / GROUP;  // MMAs of a group and part, groups of a piece
+    const uint32_t idesc = idesc_bf16_f32(128, (m_here + 15) / 16 * 16, false);
+    uint32_t a_slot = 0, a_par = 0, x_slot = 0, x_par = 0, buf = 0, d_par = 1;
+    bool a_there = false, x_there = false, d_there = false;  // of the tests ahead
+    auto there = [&](uint32_t bar, uint32_t par) { return __all_sync(0xffffffffu, mbar_test_wait(bar, par)) != 0; };
 #pragma unroll 1
-      for (int j = 0; ok && j < n_pieces; ++j) {
-        uint64_t desc[PARTS];
-        uint32_t x_bar[PARTS];
-        ok = mbar_wait(a_full(a_slot), a_par, wc, 61);
+    for (int j = 0; ok && j < n_pieces; ++j) {
+      uint64_t desc[PARTS];
+      uint32_t x_bar[PARTS];
+      ok = a_there || mbar_wait_warp(a_full(a_slot), a_par, wc, 61);
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q) {
-          ok = ok && mbar_wait(x_full(x_slot), x_par, wc, 62);
-          desc[q] = sdesc_sw128(s0 + x_slot * kXBytes, 16, 1024);
-          x_bar[q] = x_empty(x_slot);
-          if (++x_slot == kXStages) {
-            x_slot = 0;
-            x_par ^= 1u;
-          }
-        }
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t a_at = tA(a_slot);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (fresh) {
-            if (!mbar_wait(d_empty(buf), d_par, wc, 63)) { ok = false; break; }
-            tc_fence_after();
-          }
-          const uint32_t d_at = tmem + (buf ? static_cast<uint32_t>(kTcMost) : 0u);
-#pragma unroll
-          for (int q = 0; q < PARTS; ++q)
-            umma_bf16_ts(d_at, a_at + 8 * k, desc[q] + (k >> 2) * (kXHalf >> 4) + 2 * (k & 3), idesc, !fresh || q > 0 ? 1u : 0u);
-          fresh = (k & ends) == ends;
-          if (fresh) {
-            umma_commit(d_full(buf));
-            buf ^= 1u;
-            if (buf == 0) d_par ^= 1u;
-          }
-        }
-        if (!ok) break;
-        umma_commit(a_empty(a_slot));
-#pragma unroll
-        for (int q = 0; q < PARTS; ++q) umma_commit(x_bar[q]);
-        if (++a_slot == kAStages) {
-          a_slot = 0;
-          a_par ^= 1u;
+      for (int q = 0; q < PARTS; ++q) {
+        ok = ok && ((q == 0 && x_there) || mbar_wait_warp(x_full(x_slot), x_par, wc, 62));
+        desc[q] = sdesc_sw128(s0 + x_slot * kXBytes, 16, 1024);
+        x_bar[q] = x_empty(x_slot);
+        if (++x_slot == kXStages) {
+          x_slot = 0;
+          x_par ^= 1u;
         }
       }
-      // every MMA issued completes before anything is freed
+      if (!ok) break;
+      const uint32_t a_at = tA(a_slot), a_bar = a_empty(a_slot);
+      if (++a_slot == kAStages) {
+        a_slot = 0;
+        a_par ^= 1u;
+      }
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        if (!d_there && !mbar_wait_warp(d_empty(buf), d_par, wc, 63)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d_at = tmem + (buf ? static_cast<uint32_t>(kTcMost) : 0u), d_bar = d_full(buf);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = i * kSteps; k < (i + 1) * kSteps; ++k)
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q)
+              umma_bf16_ts(d_at, a_at + 8 * k, desc[q] + (k >> 2) * (kXHalf >> 4) + 2 * (k & 3), idesc, k > i * kSteps || q > 0 ? 1u : 0u);
+          umma_commit(d_bar);
+          if (i == kGroups - 1) {
+            umma_commit(a_bar);
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) umma_commit(x_bar[q]);
+          }
+        }
+        buf ^= 1u;
+        if (buf == 0) d_par ^= 1u;
+        __syncwarp();
+        d_there = there(d_empty(buf), d_par);
+      }
+      if (j + 1 < n_pieces) {
+        a_there = there(a_full(a_slot), a_par);
+        x_there = there(x_full(x_slot), x_par);
+      }
+    }
+    // every MMA issued completes before anything is freed
+    if (elect_one()) {  // (the thread that issued them)
       umma_commit(drain);
       mbar_wait_drain(drain, 0);
     }
@@ -422,10 +431,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
     for (int i = 0; i < kTcMost / 2; ++i) acc[i] = 0.0f;
     const size_t s_at = static_cast<size_t>(n0 + ch) * p.groups + k_begin / p.group;
-    float scale[4], next[4];
-    auto fetch = [&](float (&f)[4], int g) {
+    // four groups' scales as they lie, widened where they are used: nothing waits for a load before that
+    uint32_t scale[4], next[4];
+    auto fetch = [&](uint32_t (&f)[4], int g) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = fits && g + i < n_groups ? scale_at(p, s_at + g + i) : 0.0f;
+      for (int i = 0; i < 4; ++i) {
+        f[i] = 0;
+        if (fits && g + i < n_groups) {
+          if (p.scale_f32) f[i] = __ldg(static_cast<const uint32_t*>(p.scale) + s_at + g + i);
+          else f[i] = __ldg(static_cast<const uint16_t*>(p.scale) + s_at + g + i);
+        }
+      }
     };
     fetch(scale, 0);
     for (int g0 = 0; ok && g0 < n_groups; g0 += 4) {
@@ -433,7 +449,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < 4 && g0 + i < n_groups; ++i) {
         const int g = g0 + i, buf = g & 1;
-        const float s = i < 2 ? (i == 0 ? scale[0] : scale[1]) : (i == 2 ? scale[2] : scale[3]);
+        const uint32_t bits = i < 2 ? (i == 0 ? scale[0] : scale[1]) : (i == 2 ? scale[2] : scale[3]);
+        const float s = __uint_as_float(p.scale_f32 ? bits : bits << 16);
         if (!mbar_wait_warp(d_full(buf), (g >> 1) & 1, wc, 65)) { ok = false; break; }
         tc_fence_after();
         const uint64_t s2 = pack_f32x2(s, s);
@@ -612,9 +629,13 @@ void pick_tiles(int M, int n_tiles, int K, int group, int parts, int sms, int& t
 wenc_status launch_tc(I4Params p, bool f32, void* workspace, int sms, uint32_t* err, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  auto kern = f32 ? i4_tc_kernel<3> : i4_tc_kernel<1>;
-  static std::atomic<int> configured[2] = {{-1}, {-1}};
-  if (e == cudaSuccess) e = wenc_host::opt_in_smem(kern, kTcSmem, dev, configured[f32]);
+  using Kernel = void (*)(const CUtensorMap, const I4Params, const I4Tc, uint32_t*);
+  static const Kernel kernels[6] = {i4_tc_kernel<1, 32>, i4_tc_kernel<1, 64>, i4_tc_kernel<1, 128>,
+                                    i4_tc_kernel<3, 32>, i4_tc_kernel<3, 64>, i4_tc_kernel<3, 128>};
+  static std::atomic<int> configured[6] = {{-1}, {-1}, {-1}, {-1}, {-1}, {-1}};
+  const int which = (f32 ? 3 : 0) + (p.group == 32 ? 0 : p.group == 64 ? 1 : 2);
+  const Kernel kern = kernels[which];
+  if (e == cudaSuccess) e = wenc_host::opt_in_smem(kern, kTcSmem, dev, configured[which]);
   const void* x = p.x;
   if (e == cudaSuccess && f32) {
     const long long n4 = static_cast<long long>(p.M) * p.K / 4;

@@ -198,6 +198,18 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// One thread of a converged warp, always the same. Code behind it is known to the compiler to run in one thread, so that the operands
+// of an MMA, if they are the whole warp's, are not made such for every lane first.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(one));
+  return one != 0;
+}
+
 // ------------------------------------------------------------------ tcgen05: UMMA
 // Shared-memory matrix descriptor for a tile stored with the 128-byte swizzle: rows of
 // 128 bytes, 8-row atoms of 1024 bytes. `lbo`/`sbo` in bytes. Fields: start address>>4
