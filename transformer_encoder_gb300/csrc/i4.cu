@@ -238,15 +238,18 @@ __global__ void __launch_bounds__(32 * kRowsWarps) i4_rows_kernel(const __grid_c
 // their sums in registers while the MMAs fill the other. So a scale is one number a thread and group, and no weight is rounded.
 // What bounds it: the MMAs (80 cycles for each 16 inputs of 160 tokens), and with groups of 32 the reading of accumulators.
 constexpr int kTcMost = 160;                // tokens of a tile
-constexpr int kTcThreads = 512;             // 4 widening warps, MMA issuer, TMA producer, 2 idle, 8 summing warps
-constexpr int kAStages = 2, kXStages = 5;   // of 128 inputs
+constexpr int kTcThreads = 512;             // 4 widening warps, 2 MMA issuers, TMA producer, a warp for the scales, 8 summing warps
+constexpr int kAStages = 2, kXStages = 4;   // of 128 inputs
 constexpr uint32_t kXHalf = kTcMost * 128;  // 64 inputs of a tile's tokens
 constexpr uint32_t kXBytes = 2 * kXHalf;
-constexpr uint32_t kTcBars = kXStages * kXBytes;
-constexpr int kTcNumBars = 2 * kAStages + 2 * kXStages + 4 + 1;
+constexpr int kSStages = 3, kSGroups = 8;   // scales: stages of eight groups, [group][128 channels] as fp32
+constexpr uint32_t kSBytes = kSGroups * 128 * 4;
+constexpr uint32_t kTcScales = kXStages * kXBytes;
+constexpr uint32_t kTcBars = kTcScales + kSStages * kSBytes;
+constexpr int kTcNumBars = 2 * kAStages + 2 * kXStages + 4 + 1 + 2 * kSStages + 2;
 constexpr size_t kTcSmem = 1024 + kTcBars + kTcNumBars * 8 + 16;
 constexpr uint32_t kTcColumns = 512;        // sums 0..159, 160..319; A stages from 384 on, 64 each
-static_assert(kTcSmem <= 232448 && kTcMost * 128 * 4 <= static_cast<int>(kTcBars), "the sums of the output lie over the stages");
+static_assert(kTcSmem <= 232448 && kTcMost * 128 * 4 <= static_cast<int>(kTcScales), "the sums of the output lie over the stages");
 
 struct I4Tc {
   int tok, n_tiles;  // tokens of a tile; channel tiles
@@ -266,6 +269,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   auto d_full = [&](int i) { return bar0 + 8u * (2 * kAStages + 2 * kXStages + i); };
   auto d_empty = [&](int i) { return bar0 + 8u * (2 * kAStages + 2 * kXStages + 2 + i); };
   const uint32_t drain = bar0 + 8u * (2 * kAStages + 2 * kXStages + 4);
+  auto s_full = [&](int i) { return drain + 8u * (1 + i); };
+  auto s_empty = [&](int i) { return drain + 8u * (1 + kSStages + i); };
+  auto turn = [&](int i) { return drain + 8u * (1 + 2 * kSStages + i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kTcBars + kTcNumBars * 8);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const WaitCtx wc{abort_flag, err};
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // this CTA's share of K, in pieces of 128 (whole groups)
   const int pieces = p.K / kPiece, per = (pieces + p.ksplit - 1) / p.ksplit;
   const int first = min(rank * per, pieces), n_pieces = min(per, pieces - first);
-  const int k_begin = first * kPiece, n_groups = n_pieces * kPiece / p.group;
+  const int k_begin = first * kPiece, n_groups = n_pieces * kPiece / GROUP;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kAStages; ++i) {
@@ -292,7 +298,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(d_full(i), 1);
       mbar_init(d_empty(i), 8);  // the summing warps
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
+    mbar_init(turn(0), 1);       // the issuers take turns
+    mbar_init(turn(1), 1);
+    for (int i = 0; i < kSStages; ++i) {
+      mbar_init(s_full(i), 1);   // the warp that fetches scales
+      mbar_init(s_empty(i), 8);  // the summing warps
+    }
     *abort_flag = 0u;
     fence_barrier_init();
     tma_prefetch_desc(&tx);
@@ -343,39 +355,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(a_full(st));
     }
-  } else if (warp == 4) {
-    // ---------------- MMA issuer: the whole warp waits, one thread issues. A group's MMAs are one straight line behind one election (44
-    // cycles each, or their own time; with a branch between them 110 to 130), and between groups nothing is divided or looked up: slots
-    // and parities run along, and barriers are tested ahead, while MMAs are under way.
-    constexpr int kSteps = GROUP / 16, kGroups = kPiece / GROUP;  // MMAs of a group and part, groups of a piece
+  } else if (warp == 4 || warp == 6) {
+    // ---------------- MMA issuers, two for every other piece: the whole warp waits, one thread issues. A group's MMAs are straight lines behind
+    // one election (44 cycles each, or their own time; with a branch between them 110 to 130). What lies between the lines, waits that
+    // are over and a descriptor, is some 700 cycles a piece, more than its MMAs take: so the other issuer's run meanwhile. They go in turn: a
+    // wait for an accumulator tells one phase of its barrier from the next, not from the one after.
+    constexpr int kLine = GROUP < 64 ? GROUP : 64, kSteps = kLine / 16, kLines = kPiece / kLine;  // (a group of 128 in two)
+    static_assert(kXStages == 4 && kAStages == 2, "slots and parities by masks");
     const uint32_t idesc = idesc_bf16_f32(128, (m_here + 15) / 16 * 16, false);
-    uint32_t a_slot = 0, a_par = 0, x_slot = 0, x_par = 0, buf = 0, d_par = 1;
-    bool a_there = false, x_there = false, d_there = false;  // of the tests ahead
-    auto there = [&](uint32_t bar, uint32_t par) { return __all_sync(0xffffffffu, mbar_test_wait(bar, par)) != 0; };
 #pragma unroll 1
-    for (int j = 0; ok && j < n_pieces; ++j) {
+    for (int j = warp == 6; ok && j < n_pieces; j += 2) {
+      const uint32_t a_slot = j & 1;
       uint64_t desc[PARTS];
       uint32_t x_bar[PARTS];
-      ok = a_there || mbar_wait_warp(a_full(a_slot), a_par, wc, 61);
+      ok = mbar_wait_warp(a_full(a_slot), j >> 1 & 1, wc, 61);
 #pragma unroll
       for (int q = 0; q < PARTS; ++q) {
-        ok = ok && ((q == 0 && x_there) || mbar_wait_warp(x_full(x_slot), x_par, wc, 62));
-        desc[q] = sdesc_sw128(s0 + x_slot * kXBytes, 16, 1024);
-        x_bar[q] = x_empty(x_slot);
-        if (++x_slot == kXStages) {
-          x_slot = 0;
-          x_par ^= 1u;
-        }
+        const uint32_t xi = j * PARTS + q;
+        ok = ok && mbar_wait_warp(x_full(xi & 3), xi >> 2 & 1, wc, 62);
+        desc[q] = sdesc_sw128(s0 + (xi & 3) * kXBytes, 16, 1024);
+        x_bar[q] = x_empty(xi & 3);
       }
-      if (!ok) break;
-      const uint32_t a_at = tA(a_slot), a_bar = a_empty(a_slot);
-      if (++a_slot == kAStages) {
-        a_slot = 0;
-        a_par ^= 1u;
-      }
+      const uint32_t a_at = tA(a_slot), a_bar = a_empty(a_slot), other = turn(a_slot ^ 1);
+      if (j > 0) ok = ok && mbar_wait_warp(turn(a_slot), (j - 1) >> 1 & 1, wc, 68);
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        if (!d_there && !mbar_wait_warp(d_empty(buf), d_par, wc, 63)) { ok = false; break; }
+      for (int i = 0; i < kLines; ++i) {
+        const bool begins = i * kLine % GROUP == 0, ends = (i + 1) * kLine % GROUP == 0;
+        const uint32_t grp = j * (kPiece / GROUP) + i * kLine / GROUP, buf = grp & 1;
+        if (begins) ok = ok && mbar_wait_warp(d_empty(buf), (grp >> 1 & 1) ^ 1u, wc, 63);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d_at = tmem + (buf ? static_cast<uint32_t>(kTcMost) : 0u), d_bar = d_full(buf);
         if (elect_one()) {
@@ -383,22 +391,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int k = i * kSteps; k < (i + 1) * kSteps; ++k)
 #pragma unroll
             for (int q = 0; q < PARTS; ++q)
-              umma_bf16_ts(d_at, a_at + 8 * k, desc[q] + (k >> 2) * (kXHalf >> 4) + 2 * (k & 3), idesc, k > i * kSteps || q > 0 ? 1u : 0u);
-          umma_commit(d_bar);
-          if (i == kGroups - 1) {
+              umma_bf16_ts(d_at, a_at + 8 * k, desc[q] + (k >> 2) * (kXHalf >> 4) + 2 * (k & 3), idesc,
+                           !begins || k > i * kSteps || q > 0 ? 1u : 0u);
+          if (ends) umma_commit(d_bar);
+          if (i == kLines - 1) {
             umma_commit(a_bar);
 #pragma unroll
             for (int q = 0; q < PARTS; ++q) umma_commit(x_bar[q]);
+            mbar_arrive(other);
           }
         }
-        buf ^= 1u;
-        if (buf == 0) d_par ^= 1u;
         __syncwarp();
-        d_there = there(d_empty(buf), d_par);
-      }
-      if (j + 1 < n_pieces) {
-        a_there = there(a_full(a_slot), a_par);
-        x_there = there(x_full(x_slot), x_par);
       }
     }
     // every MMA issued completes before anything is freed
@@ -423,6 +426,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = (xi > kXStages ? xi - kXStages : 0); i < xi; ++i) mbar_wait_drain(x_full(i % kXStages), (i / kXStages) & 1);
     }
     __syncwarp();
+  } else if (warp == 7) {
+    // ---------------- the scales of eight groups at a time, four channels a lane, two stages ahead of what is stored: their latency
+    // would be the summing warps' otherwise
+    const size_t row = static_cast<size_t>(n0 + lane) * p.groups + k_begin / GROUP, step = static_cast<size_t>(32) * p.groups;
+    uint32_t raw[2][4][kSGroups];
+    auto fetch = [&](uint32_t (&r)[4][kSGroups], int g0) {  // (as they lie: nothing waits for a load before it is widened)
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int i = 0; i < kSGroups; ++i) {
+          r[h][i] = 0;
+          if (fits && g0 + i < n_groups) {
+            if (p.scale_f32) asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r[h][i]) : "l"(static_cast<const uint32_t*>(p.scale) + row + h * step + g0 + i));
+            else asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(r[h][i]) : "l"(static_cast<const uint16_t*>(p.scale) + row + h * step + g0 + i));
+          }
+        }
+    };
+    fetch(raw[0], 0);
+    fetch(raw[1], kSGroups);
+    const int shift = p.scale_f32 ? 0 : 16;
+#pragma unroll 1
+    for (int g0 = 0, b = 0; ok && g0 < n_groups; g0 += 2 * kSGroups) {
+#pragma unroll
+      for (int d = 0; d < 2; ++d, ++b) {
+        if (!ok || g0 + d * kSGroups >= n_groups) break;
+        const int st = b % kSStages;
+        if (!mbar_wait_warp(s_empty(st), ((b / kSStages) & 1) ^ 1u, wc, 66)) { ok = false; break; }
+        float* to = reinterpret_cast<float*>(smem + kTcScales + st * kSBytes) + lane;
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+          for (int i = 0; i < kSGroups; ++i) to[i * 128 + 32 * h] = __uint_as_float(raw[d][h][i] << shift);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_full(st));
+        fetch(raw[d], g0 + (d + 2) * kSGroups);
+      }
+    }
   }
   // ---------------- summing: thread = channel; warps 8 .. 11 the first half of the tokens, 12 .. 15 the second
   const int ch = 32 * (warp & 3) + lane, half = c.tok / 2, t0 = warp >= 12 ? half : 0;  // (tok is a multiple of 16)
@@ -430,27 +470,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp >= 8) {
 #pragma unroll
     for (int i = 0; i < kTcMost / 2; ++i) acc[i] = 0.0f;
-    const size_t s_at = static_cast<size_t>(n0 + ch) * p.groups + k_begin / p.group;
-    // four groups' scales as they lie, widened where they are used: nothing waits for a load before that
-    uint32_t scale[4], next[4];
-    auto fetch = [&](uint32_t (&f)[4], int g) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[i] = 0;
-        if (fits && g + i < n_groups) {
-          if (p.scale_f32) f[i] = __ldg(static_cast<const uint32_t*>(p.scale) + s_at + g + i);
-          else f[i] = __ldg(static_cast<const uint16_t*>(p.scale) + s_at + g + i);
-        }
-      }
-    };
-    fetch(scale, 0);
-    for (int g0 = 0; ok && g0 < n_groups; g0 += 4) {
-      fetch(next, g0 + 4);
+    for (int g0 = 0, b = 0; ok && g0 < n_groups; g0 += kSGroups, ++b) {
+      const int st = b % kSStages;
+      if (!mbar_wait_warp(s_full(st), (b / kSStages) & 1, wc, 67)) { ok = false; break; }
+      const float* scales = reinterpret_cast<const float*>(smem + kTcScales + st * kSBytes) + ch;
 #pragma unroll 1
-      for (int i = 0; i < 4 && g0 + i < n_groups; ++i) {
+      for (int i = 0; i < kSGroups && g0 + i < n_groups; ++i) {
         const int g = g0 + i, buf = g & 1;
-        const uint32_t bits = i < 2 ? (i == 0 ? scale[0] : scale[1]) : (i == 2 ? scale[2] : scale[3]);
-        const float s = __uint_as_float(p.scale_f32 ? bits : bits << 16);
+        const float s = scales[i * 128];
         if (!mbar_wait_warp(d_full(buf), (g >> 1) & 1, wc, 65)) { ok = false; break; }
         tc_fence_after();
         const uint64_t s2 = pack_f32x2(s, s);
@@ -484,8 +511,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(d_empty(buf));
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) scale[i] = next[i];
+      if (lane == 0) mbar_arrive(s_empty(st));  // (behind the last group's __syncwarp)
     }
   }
   // ---------------- output. The sums go over the stages as [token][channel] (every MMA and copy is done: the sums waited for the
