@@ -52,13 +52,17 @@ constexpr uint32_t OFF_K = OFF_Q + 2 * Q_BYTES;
 constexpr uint32_t OFF_V = OFF_K + NK * KV_BYTES;
 constexpr uint32_t OFF_P = OFF_V + NV * KV_BYTES;
 constexpr uint32_t OFF_BARS = OFF_P + 2 * P_BYTES;
-// bars: q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], and per query tile t: s_full[t], s_free[t],
-// p_full[t], pv_done[t]; drain; piece_full[NP], piece_empty[NP].
-constexpr int NUM_BARS = 2 + 2 * NK + 2 * NV + 8 + 1 + 2 * NP;
+// bars: q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], and per query tile t: s_full[t][2] and
+// pv_done[t][2] (of even and odd steps: a wait tells one phase from the next only, and an S may be a step ahead of its softmax, a
+// PV one of the S issuer's wait for the last), p_full[t]; drain; piece_full[NP], piece_empty[NP].
+constexpr int NUM_BARS = 2 + 2 * NK + 2 * NV + 10 + 1 + 2 * NP;
 constexpr int kTakers = 11;  // warps that take pieces from the ring: all but the one that walks
 constexpr size_t SMEM = 1024 + OFF_BARS + NUM_BARS * 8 + 16;
 static_assert(SMEM + 2600 <= 232448, "shared memory of the chunk kernel");
-constexpr uint32_t TMEM_COLS = 512;  // S_A 0..127, S_B 128..255, O_A 256..319, O_B 320..383, P_A 384..447, P_B 448..511
+// TMEM: three buffers of S at 0, 128 and 256, O_A 384..447, O_B 448..511. Step g of tile t is S number 2 g + t, in buffer number
+// modulo three, and its P overwrites the scores that have been read: so the next step's S is there before this one's P has
+// been used, and no softmax waits for an S.
+constexpr uint32_t TMEM_COLS = 512;
 // The running maximum grows only when a step's maximum exceeds it by more than this (log2 units), so p <= 2^8.
 constexpr float kRescaleThreshold = 8.0f;
 
@@ -152,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ long long sums[kWarps];
   __shared__ int start[6];
   __shared__ Piece pieces[NP];
-  __shared__ long long places[2][BKV];
+  __shared__ uint64_t places[2][BKV];
   __shared__ long long of_run[2];  // all steps, and the CTAs that share them
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t s0 = smem_u32(smem);
@@ -164,17 +168,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto v_full = [&](int s) { return bar0 + 8u * (2 + 2 * NK + s); };
   auto v_empty = [&](int s) { return bar0 + 8u * (2 + 2 * NK + NV + s); };
   const uint32_t tb0 = bar0 + 8u * (2 + 2 * NK + 2 * NV);
-  auto s_full = [&](int t) { return tb0 + 8u * t; };
-  auto s_free = [&](int t) { return tb0 + 16u + 8u * t; };
+  auto s_full = [&](int t, int g) { return tb0 + 16u * t + 8u * (g & 1); };
   auto p_full = [&](int t) { return tb0 + 32u + 8u * t; };
-  auto pv_done = [&](int t) { return tb0 + 48u + 8u * t; };
-  const uint32_t drain = tb0 + 64u;
-  auto piece_full = [&](int i) { return tb0 + 72u + 8u * i; };
-  auto piece_empty = [&](int i) { return tb0 + 72u + 8u * (NP + i); };
+  auto pv_done = [&](int t, int g) { return tb0 + 48u + 16u * t + 8u * (g & 1); };
+  const uint32_t drain = tb0 + 80u;
+  auto piece_full = [&](int i) { return tb0 + 88u + 8u * i; };
+  auto piece_empty = [&](int i) { return tb0 + 88u + 8u * (NP + i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_BARS + NUM_BARS * 8);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const WaitCtx wc{abort_flag, err};
-  const int warp = threadIdx.x >> 5;
+  // (from lane 0, so that the compiler knows it for the whole warp's)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -189,10 +193,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(v_empty(s), 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(s_full(t), 1);
-      mbar_init(s_free(t), 4);  // one arrival per softmax warp of the tile
-      mbar_init(p_full(t), 4);
-      mbar_init(pv_done(t), 1);
+      mbar_init(s_full(t, 0), 1);
+      mbar_init(s_full(t, 1), 1);
+      mbar_init(p_full(t), 4);  // one arrival per softmax warp of the tile
+      mbar_init(pv_done(t, 0), 1);
+      mbar_init(pv_done(t, 1), 1);
     }
     mbar_init(drain, 2);  // one commit per MMA-issuing thread
     for (int i = 0; i < NP; ++i) {
@@ -289,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   if (threadIdx.x == 0) {
     a.cuts[blockIdx.x].pieces = 0;
     of_run[0] = total;
@@ -297,9 +302,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();  // (the piece that is cut at the run's end writes the mark again)
 
-  auto tS = [&](int t) { return tmem_base + 128u * t; };
-  auto tO = [&](int t) { return tmem_base + 256u + 64u * t; };
-  auto tP = [&](int t) { return tmem_base + 384u + 64u * t; };  // P as bf16 pairs: 64 columns per tile
+  auto tS = [&](int buf) { return tmem_base + 128u * buf; };  // (and the P that follows, bf16 pairs in its first 64 columns)
+  auto tO = [&](int t) { return tmem_base + 384u + 64u * t; };
 
   // Every role takes the same pieces in the same order and counts K/V tiles across them, so ring slots and barrier parities
   // continue from one piece to the next. take(i): piece i, false behind the last (or after a failed wait); give(i): it is done with.
@@ -388,37 +392,56 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           commit(q_full);
         }
-#pragma unroll 1
-        for (int j = pc.k0; j < pc.k1; ++j, ++kc) {
-          const int st = kc % NK;
-          static_assert(NK == NV, "one ring arithmetic for both");
-          // places of the step's keys, four a lane, as units of 16 bytes from the pages' beginning (-1: not there)
-          const int key0 = u.ks.key0(j, BKV);
+        // A step's keys, four a lane: their pages are read a step ahead, and their rows' addresses go through shared memory to
+        // the lanes that copy them (0: not there). With both in one chain, a step took its producers 4300 cycles.
+        const int32_t* row = p.table + pc.seq * p.table_stride;
+        const int seq = pc.seq, k1 = pc.k1;
+        const uint8_t* head = pages + pc.hk * (HD * 2);
+        int page[4];
+        auto look = [&](int j) {
+          const int key0 = u.ks.key0(j, BKV) + lane;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int key = key0 + 32 * i + lane;
-            long long unit = -1;
+            const int key = key0 + 32 * i, pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+            page[i] = -1;
+            // (volatile: else the compiler moves the load down to its use)
+            if (u.ks.seen(key) && in_bounds(seq < p.n_seqs && pi >= 0 && pi < p.max_pages, err, 122))
+              asm volatile("ld.global.b32 %0, [%1];" : "=r"(page[i]) : "l"(row + pi) : "memory");
+          }
+        };
+        look(pc.k0);
+#pragma unroll 1
+        for (int j = pc.k0; j < k1; ++j, ++kc) {
+          const int st = kc % NK;
+          static_assert(NK == NV, "one ring arithmetic for both");
+          const int key0 = u.ks.key0(j, BKV) + lane;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = key0 + 32 * i, pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+            uint64_t at = 0;
             if (u.ks.seen(key)) {
-              const int pi = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-              const int page = in_bounds(pc.seq < p.n_seqs && pi < p.max_pages, err, 122) ? p.table[pc.seq * p.table_stride + pi] : -1;
-              if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.n_pages))
-                unit = static_cast<long long>(static_cast<uint64_t>(page) * page16 + static_cast<uint32_t>(key - pi * p.page_size) * p.row16);
+              if (static_cast<uint32_t>(page[i]) < static_cast<uint32_t>(p.n_pages))
+                at = reinterpret_cast<uint64_t>(head) + ((static_cast<uint64_t>(page[i]) * page16 + static_cast<uint32_t>(key - pi * p.page_size) * p.row16) << 4);
               else
                 *reinterpret_cast<volatile uint32_t*>(err) = kErrData | (80u << 8);
             }
-            places[warp][32 * i + lane] = unit;
+            places[warp][32 * i + lane] = at;
           }
+          if (j + 1 < k1) look(j + 1);
           __syncwarp();
           if (!acquire(is_k ? k_empty(st) : v_empty(st), ((kc / NK) & 1) ^ 1u, is_k ? 11 : 10)) {
             ok = false;
             break;
           }
-          const uint32_t head = pc.hk * (HD * 2 / 16) + c, dst = ring + st * KV_BYTES;
-#pragma unroll 4
-          for (int i = 0; i < BKV / 8; ++i) {
-            const long long x = places[warp][8 * i + r4], y = places[warp][8 * i + 4 + r4];
-            cp_async16(dst + i * 1024 + even, pages + (x >= 0 ? (x + head) << 4 : 0), x >= 0);
-            cp_async16(dst + i * 1024 + odd, pages + (y >= 0 ? (y + head) << 4 : 0), y >= 0);
+          const uint32_t dst = ring + st * KV_BYTES;
+#pragma unroll 1
+          for (int i8 = 0; i8 < BKV / 8; i8 += 4) {
+            uint64_t at[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) at[i] = places[warp][8 * i8 + 4 * i + r4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              cp_async16(dst + (i8 + (i >> 1)) * 1024 + (i & 1 ? odd : even), reinterpret_cast<const uint8_t*>(at[i] != 0 ? at[i] + c * 16 : reinterpret_cast<uint64_t>(pages)), at[i] != 0);
           }
           __syncwarp();  // (before the places of the next step)
           commit(is_k ? k_full(st) : v_full(st));
@@ -431,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       if (warp == 2) {
         constexpr uint32_t idesc_s = idesc_bf16_f32(BQ, BKV, false);  // B = K tile, K-major, N = 128
-        int kc = 0;  // K tiles consumed, across pieces
+        int kc = 0, buf = 0;  // K tiles consumed, across pieces, and the buffer of the next S
         for (int np = 0; ok && take(np); ++np) {
           if (!mbar_wait_warp(q_full, np & 1, wc, 12)) break;
 #pragma unroll 1
@@ -439,27 +462,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int st = kc % NK;
             if (!mbar_wait_warp(k_full(st), (kc / NK) & 1, wc, 13)) { ok = false; break; }
             const uint64_t kdesc = sdesc_sw128(sK + st * KV_BYTES, 16, 1024);
-#pragma unroll 1
-            for (int t = 0; t < 2 && ok; ++t) {
-              if (kc >= 1 && !mbar_wait_warp(s_free(t), (kc - 1) & 1, wc, 14)) { ok = false; break; }
-              tc_fence_after();
-              if (lane == 0) {
-                const uint64_t qdesc = sdesc_sw128(sQ + t * Q_BYTES, 16, 1024);
 #pragma unroll
-                for (int k = 0; k < HD / 16; ++k) umma_bf16_ss(tS(t), qdesc + k * 2, kdesc + k * 2, idesc_s, k > 0);
-                umma_commit(s_full(t));
+            for (int t = 0; t < 2 && ok; ++t) {
+              // the buffer's last P, of the S three before, has to have been used
+              if (t == 0 ? kc >= 2 : kc >= 1) ok = mbar_wait_warp(pv_done(1 - t, kc + t), ((kc - 2 + t) >> 1) & 1, wc, 14);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t qdesc = sdesc_sw128(sQ + t * Q_BYTES, 16, 1024);
+              const uint32_t to = tS(buf), bar = s_full(t, kc);
+              if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < HD / 16; ++k) umma_bf16_ss(to, qdesc + k * 2, kdesc + k * 2, idesc_s, k > 0);
+                umma_commit(bar);
+                if (t == 1) umma_commit(k_empty(st));
+                if (t == 1 && j + 1 == j1) umma_commit(q_empty);  // the Q tiles are free once the piece's S products are done
               }
               __syncwarp();
+              buf = buf == 2 ? 0 : buf + 1;
             }
             if (!ok) break;
-            if (lane == 0) umma_commit(k_empty(st));
           }
-          if (ok && lane == 0) umma_commit(q_empty);  // the Q tiles are free once the piece's S products are done
           give(np);
         }
       } else {
         constexpr uint32_t idesc_o = idesc_bf16_f32(BQ, HD, true);  // B = V tile, MN-major, N = 64
-        int vc = 0;  // V tiles consumed, across pieces
+        int vc = 0, buf = 0;  // V tiles consumed, across pieces, and the buffer of the next P
         for (int np = 0; ok && take(np); ++np) {
           const int k0 = pieces[np % NP].k0, k1 = pieces[np % NP].k1;
 #pragma unroll 1
@@ -470,26 +497,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = 0; t < 2; ++t) {
               if (!mbar_wait_warp(p_full(t), vc & 1, wc, 16)) { ok = false; break; }
               tc_fence_after();
-              if (lane == 0) {
-                const uint64_t vdesc = sdesc_sw128(sV + st * KV_BYTES, 1024, 1024);
-                const uint64_t pdesc = sdesc_sw128(sP + t * P_BYTES, 16, 1024);
+              const uint64_t vdesc = sdesc_sw128(sV + st * KV_BYTES, 1024, 1024);
+              const uint64_t pdesc = sdesc_sw128(sP + t * P_BYTES, 16, 1024);
+              const uint32_t to = tO(t), from = tS(buf), bar = pv_done(t, vc), v_bar = v_empty(st), more = j > k0;
+              if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < BKV / 16; ++k)  // (64 keys a block of 128-byte rows)
-                  umma_bf16_ss(tO(t), pdesc + (k >> 2) * (P_BYTES / 2 >> 4) + (k & 3) * 2, vdesc + k * 128, idesc_o,
-                               (j > k0 || k > 0) ? 1u : 0u);
+                  umma_bf16_ss(to, pdesc + (k >> 2) * (P_BYTES / 2 >> 4) + (k & 3) * 2, vdesc + k * 128, idesc_o, k > 0 ? 1u : more);
 #pragma unroll
-                for (int k = 0; k < BKV / 16; ++k) umma_bf16_ts(tO(t), tP(t) + 8 * k, vdesc + k * 128, idesc_o, 1u);
-                umma_commit(pv_done(t));
-                if (t == 1) umma_commit(v_empty(st));
+                for (int k = 0; k < BKV / 16; ++k) umma_bf16_ts(to, from + 8 * k, vdesc + k * 128, idesc_o, 1u);
+                umma_commit(bar);
+                if (t == 1) umma_commit(v_bar);
               }
               __syncwarp();
+              buf = buf == 2 ? 0 : buf + 1;
             }
           }
           give(np);
         }
       }
       // Every MMA this thread issued completes before TMEM is released.
-      if (lane == 0) {
+      if (elect_one()) {  // (the thread that issued them)
         umma_commit(drain);
         mbar_wait_drain(drain, 0);
       }
@@ -503,7 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     bool ok = true;
-    int g = 0;  // steps processed, across pieces
+    int g = 0;    // steps processed, across pieces
+    int buf = t;  // of the step's S: two further, modulo three, each step
     const int tok = row / p.r, hr = row - tok * p.r;  // token of the tile and head of the group this row holds
     const float scale_log2 = p.scale_log2;
     for (int np = 0; ok && take(np); ++np) {
@@ -512,8 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -CUDART_INF_F;  // running maximum, in units of scale_log2
       float l = 0.0f;           // running denominator
 #pragma unroll 1
-      for (int j = pc.k0; j < pc.k1; ++j, ++g) {
-        if (!mbar_wait_warp(s_full(t), g & 1, wc, 17)) { ok = false; break; }
+      for (int j = pc.k0; j < pc.k1; ++j, ++g, buf = buf == 0 ? 2 : buf - 1) {
+        if (!mbar_wait_warp(s_full(t, g), (g >> 1) & 1, wc, 17)) { ok = false; break; }
         tc_fence_after();
         const int key0 = pc.u.ks.key0(j, BKV);
         const int first = pc.pos0 + pc.u.i0 + t * a.tokens, last = pc.pos0 + pc.u.i1;  // (of the tile's tokens, and of all)
@@ -532,8 +561,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int b = 0; b < 4; b += 2) {
           uint32_t r[2][32];
-          tmem_ld_32x32b_x32(tS(t) + lane_off + 32 * b, r[0]);
-          tmem_ld_32x32b_x32(tS(t) + lane_off + 32 * b + 32, r[1]);
+          tmem_ld_32x32b_x32(tS(buf) + lane_off + 32 * b, r[0]);
+          tmem_ld_32x32b_x32(tS(buf) + lane_off + 32 * b + 32, r[1]);
           tmem_ld_wait();
           if (border) {
             hide(r[0], 32 * b);
@@ -557,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         if (j > pc.k0) {
           // PV[j-1] must be complete: P is overwritten below and O may be rescaled.
-          if (!mbar_wait_warp(pv_done(t), (g - 1) & 1, wc, 18)) { ok = false; break; }
+          if (!mbar_wait_warp(pv_done(t, g - 1), ((g - 1) >> 1) & 1, wc, 18)) { ok = false; break; }
           tc_fence_after();
           if (__any_sync(0xffffffffu, m_new != m)) {
 #pragma unroll
@@ -573,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 
         // p = 2^(s * scale_log2 - m_new): packed fp32x2 FMA for the argument, packed adds for the row sum; P is cut into its
-        // two bf16 parts, 32 keys at a time: the large part into the tile's P columns of TMEM, the small one into its swizzled
+        // two bf16 parts, 32 keys at a time: the large part into TMEM, the small one into its swizzled
         // rows of shared memory (16 bytes are 8 keys).
         const uint64_t c2 = pack_f32x2(scale_log2, scale_log2);
         const uint64_t nm2 = pack_f32x2(-ref, -ref);
@@ -582,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int b = 0; b < 4; ++b) {
           uint32_t r[32], pk[16], pl[16];
-          tmem_ld_32x32b_x32(tS(t) + lane_off + 32 * b, r);
+          tmem_ld_32x32b_x32(tS(buf) + lane_off + 32 * b, r);
           tmem_ld_wait();
           if (border) hide(r, 32 * b);
 #pragma unroll
@@ -602,11 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             sts_v4(to + (((4 * (b & 1) + c) ^ (row & 7)) << 4), pl[4 * c], pl[4 * c + 1], pl[4 * c + 2], pl[4 * c + 3]);
-          tmem_st_32x32b_x16(tP(t) + lane_off + 16 * b, pk);
+          tmem_st_32x32b_x16(tS(buf) + lane_off + 16 * b, pk);  // (over scores that have been read)
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free(t));  // the MMA may overwrite S with the next step's
         float sa0, sa1, sb0, sb1;
         unpack_f32x2(sum2a, sa0, sa1);
         unpack_f32x2(sum2b, sb0, sb1);
@@ -619,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(t));
       }
-      if (!ok || !mbar_wait_warp(pv_done(t), (g - 1) & 1, wc, 19)) break;
+      if (!ok || !mbar_wait_warp(pv_done(t, g - 1), ((g - 1) >> 1) & 1, wc, 19)) break;
       // The piece's result, from O in TMEM once the PV product of its last step is done; the next piece's first PV product
       // (which overwrites O) waits for P that this warp writes only after these reads.
       tc_fence_after();
