@@ -30,8 +30,8 @@ using namespace wenc_dev;
 constexpr int BQ = 128;    // query rows per tile (two tiles per unit)
 constexpr int BKV = 128;   // keys per step
 constexpr int HD = 64;
-constexpr int NK = 3;      // K ring depth
-constexpr int NV = 3;      // V ring depth
+constexpr int NK = 4;      // K ring depth
+constexpr int NV = 4;      // V ring depth
 constexpr int NP = 4;      // ring of pieces
 constexpr int kThreads = 384;  // K and V producers, 2 MMA issuers, 2 softmax warpgroups
 constexpr int kWarps = kThreads / 32;
@@ -46,12 +46,10 @@ static_assert(kRegsNeeded <= (65536 / kThreads) / 8 * 8 * kThreads, "register sp
 
 constexpr uint32_t Q_BYTES = BQ * HD * 2;    // 16 KB per query tile
 constexpr uint32_t KV_BYTES = BKV * HD * 2;  // 16 KB per K or V tile
-constexpr uint32_t P_BYTES = BQ * BKV * 2;   // 32 KB: the small part of a tile's P, two blocks of 64 keys
 constexpr uint32_t OFF_Q = 0;
 constexpr uint32_t OFF_K = OFF_Q + 2 * Q_BYTES;
 constexpr uint32_t OFF_V = OFF_K + NK * KV_BYTES;
-constexpr uint32_t OFF_P = OFF_V + NV * KV_BYTES;
-constexpr uint32_t OFF_BARS = OFF_P + 2 * P_BYTES;
+constexpr uint32_t OFF_BARS = OFF_V + NV * KV_BYTES;
 // bars: q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], and per query tile t: s_full[t][2] and
 // pv_done[t][2] (of even and odd steps: a wait tells one phase from the next only, and an S may be a step ahead of its softmax, a
 // PV one of the S issuer's wait for the last), p_full[t]; drain; piece_full[NP], piece_empty[NP].
@@ -63,8 +61,19 @@ static_assert(SMEM + 2600 <= 232448, "shared memory of the chunk kernel");
 // modulo three, and its P overwrites the scores that have been read: so the next step's S is there before this one's P has
 // been used, and no softmax waits for an S.
 constexpr uint32_t TMEM_COLS = 512;
-// The running maximum grows only when a step's maximum exceeds it by more than this (log2 units), so p <= 2^8.
-constexpr float kRescaleThreshold = 8.0f;
+// The sum of a row's weights of 32 keys above which its reference moves.
+constexpr float kTooMuch = 0x1p20f;
+
+// The largest of 32 scores, in independent chains of three-input max.
+__device__ __forceinline__ float max32(const uint32_t (&r)[32]) {
+  float mc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    auto at = [&](int e) { return __uint_as_float(r[8 * k + e]); };
+    mc[k] = fmaxf(fmax3(fmax3(at(0), at(1), at(2)), at(3), at(4)), fmax3(at(5), at(6), at(7)));
+  }
+  return fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+}
 
 using wenc_host::ChunkCut;
 using wenc_host::ChunkTcArgs;
@@ -160,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ long long of_run[2];  // all steps, and the CTAs that share them
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t s0 = smem_u32(smem);
-  const uint32_t sQ = s0 + OFF_Q, sK = s0 + OFF_K, sV = s0 + OFF_V, sP = s0 + OFF_P;
+  const uint32_t sQ = s0 + OFF_Q, sK = s0 + OFF_K, sV = s0 + OFF_V;
   const uint32_t bar0 = s0 + OFF_BARS;
   const uint32_t q_full = bar0, q_empty = bar0 + 8u;
   auto k_full = [&](int s) { return bar0 + 8u * (2 + s); };
@@ -302,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();  // (the piece that is cut at the run's end writes the mark again)
 
-  auto tS = [&](int buf) { return tmem_base + 128u * buf; };  // (and the P that follows, bf16 pairs in its first 64 columns)
+  auto tS = [&](int buf) { return tmem_base + 128u * buf; };  // (and the P that follows)
   auto tO = [&](int t) { return tmem_base + 384u + 64u * t; };
 
   // Every role takes the same pieces in the same order and counts K/V tiles across them, so ring slots and barrier parities
@@ -498,14 +507,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!mbar_wait_warp(p_full(t), vc & 1, wc, 16)) { ok = false; break; }
               tc_fence_after();
               const uint64_t vdesc = sdesc_sw128(sV + st * KV_BYTES, 1024, 1024);
-              const uint64_t pdesc = sdesc_sw128(sP + t * P_BYTES, 16, 1024);
               const uint32_t to = tO(t), from = tS(buf), bar = pv_done(t, vc), v_bar = v_empty(st), more = j > k0;
               if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < BKV / 16; ++k)  // (64 keys a block of 128-byte rows)
-                  umma_bf16_ss(to, pdesc + (k >> 2) * (P_BYTES / 2 >> 4) + (k & 3) * 2, vdesc + k * 128, idesc_o, k > 0 ? 1u : more);
+                for (int part = 1; part >= 0; --part)  // (the small parts first: the tensor core's sums truncate)
 #pragma unroll
-                for (int k = 0; k < BKV / 16; ++k) umma_bf16_ts(to, from + 8 * k, vdesc + k * 128, idesc_o, 1u);
+                  for (int k = 0; k < BKV / 16; ++k)
+                    umma_bf16_ts(to, from + 32 * (k >> 1) + 16 * part + 8 * (k & 1), vdesc + k * 128, idesc_o, part == 0 || k > 0 ? 1u : more);
                 umma_commit(bar);
                 if (t == 1) umma_commit(v_bar);
               }
@@ -555,89 +563,98 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 32; ++c) r[c] = (sees >> c) & 1u ? r[c] : 0xff800000u;
         };
-        // The row's scores are read twice, for the maximum and for the exponentials, 32 at a time in loops that are not unrolled: with
-        // all 128 in registers and unrolled loops, warps waited for instructions more than for anything else.
-        float mx = -CUDART_INF_F;
+        // The row's reference is the maximum (rounded up to a whole number, so that references differ by powers of two) of the first
+        // step of which it sees a key, and stays as long as the weights stay below 2^20. The maximum of every step, formed
+        // first, took a quarter of the time. Loops are not unrolled further: with 128 scores in registers and straight code,
+        // warps waited for instructions more than for anything else.
+        float m_new = m;
+        if (__any_sync(0xffffffffu, m == -CUDART_INF_F)) {
+          float mx = -CUDART_INF_F;
 #pragma unroll 1
-        for (int b = 0; b < 4; b += 2) {
-          uint32_t r[2][32];
-          tmem_ld_32x32b_x32(tS(buf) + lane_off + 32 * b, r[0]);
-          tmem_ld_32x32b_x32(tS(buf) + lane_off + 32 * b + 32, r[1]);
-          tmem_ld_wait();
-          if (border) {
-            hide(r[0], 32 * b);
-            hide(r[1], 32 * b + 32);
+          for (int b = 0; b < 4; ++b) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(tS(buf) + lane_off + 32 * b, r);
+            tmem_ld_wait();
+            if (border) hide(r, 32 * b);
+            mx = fmaxf(mx, max32(r));
           }
-          float mc[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // independent chains of three-input max
-            auto at = [&](int e) { return __uint_as_float(r[k >> 1][16 * (k & 1) + e]); };
-            float x = fmax3(at(0), at(1), at(2));
-#pragma unroll
-            for (int e = 3; e < 15; e += 2) x = fmax3(x, at(e), at(e + 1));
-            mc[k] = fmaxf(x, at(15));
-          }
-          mx = fmaxf(fmax3(mx, mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+          if (m == -CUDART_INF_F) m_new = ceilf(mx * scale_log2);
         }
-        const float mx_s = mx * scale_log2;
-        const float m_new = (mx_s > m + kRescaleThreshold) ? mx_s : m;
-        const float ref = m_new == -CUDART_INF_F ? 0.0f : m_new;  // (nothing visible so far: weights of 0)
-        const float alpha = ex2_approx(m - ref);  // 0 on the first step (m = -inf)
-
-        if (j > pc.k0) {
-          // PV[j-1] must be complete: P is overwritten below and O may be rescaled.
+        if (j > pc.k0) {  // PV[j-1] must be complete: P is overwritten below and O may be rescaled
           if (!mbar_wait_warp(pv_done(t, g - 1), ((g - 1) >> 1) & 1, wc, 18)) { ok = false; break; }
           tc_fence_after();
-          if (__any_sync(0xffffffffu, m_new != m)) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(tO(t) + lane_off + half * 32, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-              tmem_st_32x32b_x32(tO(t) + lane_off + half * 32, o);
-            }
-          }
         }
 
         // p = 2^(s * scale_log2 - m_new): packed fp32x2 FMA for the argument, packed adds for the row sum; P is cut into its
-        // two bf16 parts, 32 keys at a time: the large part into TMEM, the small one into its swizzled
-        // rows of shared memory (16 bytes are 8 keys).
+        // two bf16 parts, 32 keys at a time, which go over these keys' scores: 16 columns of the large parts, 16 of the small ones.
         const uint64_t c2 = pack_f32x2(scale_log2, scale_log2);
-        const uint64_t nm2 = pack_f32x2(-ref, -ref);
-        uint64_t sum2a = pack_f32x2(0.0f, 0.0f), sum2b = sum2a;
         const uint64_t minus1 = pack_f32x2(-1.0f, -1.0f);
+        float sum = 0.0f;
 #pragma unroll 1
         for (int b = 0; b < 4; ++b) {
-          uint32_t r[32], pk[16], pl[16];
+          uint32_t r[32], pp16[32];  // (the large parts of the 32 keys' weights, two to a column, then the small ones)
           tmem_ld_32x32b_x32(tS(buf) + lane_off + 32 * b, r);
           tmem_ld_wait();
           if (border) hide(r, 32 * b);
+          float part;
+#pragma unroll 1
+          for (bool again = false;; again = true) {
+            const float ref = m_new == -CUDART_INF_F ? 0.0f : m_new;  // (nothing visible so far: weights of 0)
+            const uint64_t nm2 = pack_f32x2(-ref, -ref);
+            uint64_t sum2a = pack_f32x2(0.0f, 0.0f), sum2b = sum2a;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float a0, a1;
-            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), c2, nm2), a0, a1);
-            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
-            const uint64_t pp = pack_f32x2(p0, p1);
-            if (i & 1) sum2b = add_f32x2(sum2b, pp);
-            else sum2a = add_f32x2(sum2a, pp);
-            pk[i] = pack_bf16x2(p0, p1);
-            float l0, l1;  // what the large part leaves (exact)
-            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(pk[i] << 16), __uint_as_float(pk[i] & 0xffff0000u)), minus1, pp), l0, l1);
-            pl[i] = pack_bf16x2(l0, l1);
+            for (int i = 0; i < 16; ++i) {
+              float a0, a1;
+              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), c2, nm2), a0, a1);
+              const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+              const uint64_t pp = pack_f32x2(p0, p1);
+              if (i & 1) sum2b = add_f32x2(sum2b, pp);
+              else sum2a = add_f32x2(sum2a, pp);
+              const uint32_t large = pack_bf16x2(p0, p1);
+              float l0, l1;  // what the large part leaves (exact)
+              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(large << 16), __uint_as_float(large & 0xffff0000u)), minus1, pp), l0, l1);
+              pp16[i] = large;
+              pp16[16 + i] = pack_bf16x2(l0, l1);
+            }
+            float sa0, sa1, sb0, sb1;
+            unpack_f32x2(sum2a, sa0, sa1);
+            unpack_f32x2(sum2b, sb0, sb1);
+            part = (sa0 + sa1) + (sb0 + sb1);
+            const bool much = !(part <= kTooMuch);
+            if (again || !__any_sync(0xffffffffu, much)) break;
+            // Rare: scores far above the reference (or none at all). It moves, by a power of two, and the step's weights that are
+            // written already move with it.
+            const float moved = much ? fmaxf(m_new, ceilf(max32(r) * scale_log2)) : m_new;
+            const float f = m_new == moved ? 1.0f : ex2_approx(m_new - moved);
+            sum *= f;
+            m_new = moved;
+            auto scaled = [&](uint32_t x) { return pack_bf16x2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f); };
+            tmem_st_wait();
+#pragma unroll 1
+            for (int c = 0; c < b; ++c) {
+              uint32_t x[32];
+              tmem_ld_32x32b_x32(tS(buf) + lane_off + 32 * c, x);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = scaled(x[e]);
+              tmem_st_32x32b_x32(tS(buf) + lane_off + 32 * c, x);
+            }
           }
-          const uint32_t to = sP + t * P_BYTES + (b >> 1) * (P_BYTES / 2) + row * 128u;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            sts_v4(to + (((4 * (b & 1) + c) ^ (row & 7)) << 4), pl[4 * c], pl[4 * c + 1], pl[4 * c + 2], pl[4 * c + 3]);
-          tmem_st_32x32b_x16(tS(buf) + lane_off + 16 * b, pk);  // (over scores that have been read)
+          sum += part;
+          tmem_st_32x32b_x32(tS(buf) + lane_off + 32 * b, pp16);  // (over the 32 scores)
         }
-        float sa0, sa1, sb0, sb1;
-        unpack_f32x2(sum2a, sa0, sa1);
-        unpack_f32x2(sum2b, sb0, sb1);
-        const float sum = (sa0 + sa1) + (sb0 + sb1);
-        fence_proxy_async_smem();
+        const float alpha = ex2_approx(m - (m_new == -CUDART_INF_F ? 0.0f : m_new));  // 0 on the first step (m = -inf)
+        if (j > pc.k0 && __any_sync(0xffffffffu, m_new != m)) {
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(tO(t) + lane_off + half * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+            tmem_st_32x32b_x32(tO(t) + lane_off + half * 32, o);
+          }
+        }
         tmem_st_wait();
         l = l * alpha + sum;
         m = m_new;
