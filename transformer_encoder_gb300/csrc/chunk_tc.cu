@@ -191,14 +191,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
+    mbar_init(q_full, 32);  // the lanes of the warp that copies
     mbar_init(q_empty, 1);  // released by the S issuer's commit after a piece's last S
     for (int s = 0; s < NK; ++s) {
-      mbar_init(k_full(s), 1);
+      mbar_init(k_full(s), 32);
       mbar_init(k_empty(s), 1);
     }
     for (int s = 0; s < NV; ++s) {
-      mbar_init(v_full(s), 1);
+      mbar_init(v_full(s), 32);
       mbar_init(v_empty(s), 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -325,37 +325,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // control warpgroup: registers to the softmax warpgroups first
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kCtrlRegs) : "memory");
     if (warp < 2) {
-      // ---------------- gathering: warp 0 the queries and K, warp 1 V. A tile's copies are under way while the next slot is
-      // waited for; a tile is handed over once they have landed and the proxy fence has run.
+      // ---------------- gathering: warp 0 the queries and K, warp 1 V.
       const bool is_k = warp == 0;
       const uint8_t* pages = is_k ? p.k_pages : p.v_pages;
       const uint32_t page16 = is_k ? p.k_page16 : p.v_page16;
       const uint32_t ring = is_k ? sK : sV;
       const int c = lane & 7, r4 = lane >> 3;  // 16-byte piece of a row, and row of the four that an instruction copies
       const uint32_t even = r4 * 128u + ((c ^ r4) << 4), odd = (r4 + 4) * 128u + ((c ^ (r4 + 4)) << 4);
-      uint32_t pending = 0;  // the barrier of the tile under way
-      auto hand_over = [&]() {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(pending);
-      };
-      auto flush = [&]() {
-        cp_async_wait<0>();
-        if (pending) hand_over();
-        pending = 0;
-      };
-      // waits for a slot, and hands the tile under way over first if that takes long
-      auto acquire = [&](uint32_t bar, uint32_t parity, uint32_t site) {
-        if (!__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) flush();
-        return mbar_wait_warp(bar, parity, wc, site);
-      };
-      auto commit = [&](uint32_t bar) {
-        cp_async_commit();
-        if (pending) {
-          cp_async_wait<1>();
-          hand_over();
-        }
-        pending = bar;
+      // (all 32 lanes arrive, each when its own copies have landed: nobody waits here, and nothing is fenced here, which would wait
+      // for the copies just issued; the thread that issues the MMAs fences)
+      auto hand_over = [&](uint32_t bar) {
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
       };
       Walk run;
       if (is_k) {
@@ -377,14 +357,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (is_k) {
           const bool more = run.next(p, a, err);
           if (!more) run.pc.k0 = run.pc.k1 = 0;
-          if (!acquire(piece_empty(np % NP), ((np / NP) & 1) ^ 1u, 8)) break;
+          if (!mbar_wait_warp(piece_empty(np % NP), ((np / NP) & 1) ^ 1u, wc, 8)) break;
           if (lane == 0) {
             pieces[np % NP] = run.pc;
             mbar_arrive(piece_full(np % NP));
           }
           __syncwarp();
           if (!more) break;
-          if (!acquire(q_empty, (np & 1) ^ 1u, 9)) break;
+          if (!mbar_wait_warp(q_empty, (np & 1) ^ 1u, wc, 9)) break;
         } else if (!take(np)) {
           break;
         }
@@ -399,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint8_t* src = p.q + (in ? static_cast<long long>(pc.row0 + at) * p.q_stride + (pc.hk * p.r + hr) * (HD * 2) + c * 16 : 0);
             cp_async16(sQ + (i >> 5) * Q_BYTES + (i & 31) / 2 * 1024 + (i & 1 ? odd : even), src, in);
           }
-          commit(q_full);
+          hand_over(q_full);
         }
         // A step's keys, four a lane: their pages are read a step ahead, and their rows' addresses go through shared memory to
         // the lanes that copy them (0: not there). With both in one chain, a step took its producers 4300 cycles.
@@ -438,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (j + 1 < k1) look(j + 1);
           __syncwarp();
-          if (!acquire(is_k ? k_empty(st) : v_empty(st), ((kc / NK) & 1) ^ 1u, is_k ? 11 : 10)) {
+          if (!mbar_wait_warp(is_k ? k_empty(st) : v_empty(st), ((kc / NK) & 1) ^ 1u, wc, is_k ? 11 : 10)) {
             ok = false;
             break;
           }
@@ -453,11 +433,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               cp_async16(dst + (i8 + (i >> 1)) * 1024 + (i & 1 ? odd : even), reinterpret_cast<const uint8_t*>(at[i] != 0 ? at[i] + c * 16 : reinterpret_cast<uint64_t>(pages)), at[i] != 0);
           }
           __syncwarp();  // (before the places of the next step)
-          commit(is_k ? k_full(st) : v_full(st));
+          hand_over(is_k ? k_full(st) : v_full(st));
         }
         if (!is_k) give(np);
       }
-      flush();  // (also on the error path: the copies land before the CTA exits)
+      cp_async_commit();
+      cp_async_wait<0>();  // (also on the error path: the copies land before the CTA exits)
     } else {
       // ---------------- UMMA issuers: warp 2 S_A and S_B, warp 3 O_A and O_B. The whole warp waits; lane 0 issues.
       bool ok = true;
@@ -470,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = pieces[np % NP].k0, j1 = pieces[np % NP].k1; j < j1; ++j, ++kc) {
             const int st = kc % NK;
             if (!mbar_wait_warp(k_full(st), (kc / NK) & 1, wc, 13)) { ok = false; break; }
+            fence_proxy_async_smem();  // (K's rows, and before a piece's first product the queries, were written by cp.async)
             const uint64_t kdesc = sdesc_sw128(sK + st * KV_BYTES, 16, 1024);
 #pragma unroll
             for (int t = 0; t < 2 && ok; ++t) {
@@ -502,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = k0; ok && j < k1; ++j, ++vc) {
             const int st = vc % NV;
             if (!mbar_wait_warp(v_full(st), (vc / NV) & 1, wc, 15)) { ok = false; break; }
+            fence_proxy_async_smem();
 #pragma unroll 1
             for (int t = 0; t < 2; ++t) {
               if (!mbar_wait_warp(p_full(t), vc & 1, wc, 16)) { ok = false; break; }
@@ -580,11 +563,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (m == -CUDART_INF_F) m_new = ceilf(mx * scale_log2);
         }
-        if (j > pc.k0) {  // PV[j-1] must be complete: P is overwritten below and O may be rescaled
-          if (!mbar_wait_warp(pv_done(t, g - 1), ((g - 1) >> 1) & 1, wc, 18)) { ok = false; break; }
-          tc_fence_after();
-        }
-
         // p = 2^(s * scale_log2 - m_new): packed fp32x2 FMA for the argument, packed adds for the row sum; P is cut into its
         // two bf16 parts, 32 keys at a time, which go over these keys' scores: 16 columns of the large parts, 16 of the small ones.
         const uint64_t c2 = pack_f32x2(scale_log2, scale_log2);
@@ -644,7 +622,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_32x32b_x32(tS(buf) + lane_off + 32 * b, pp16);  // (over the 32 scores)
         }
         const float alpha = ex2_approx(m - (m_new == -CUDART_INF_F ? 0.0f : m_new));  // 0 on the first step (m = -inf)
-        if (j > pc.k0 && __any_sync(0xffffffffu, m_new != m)) {
+        if (j > pc.k0 && __any_sync(0xffffffffu, m_new != m)) {  // O moves with the reference, once PV[j-1] is complete
+          if (!mbar_wait_warp(pv_done(t, g - 1), ((g - 1) >> 1) & 1, wc, 18)) { ok = false; break; }
+          tc_fence_after();
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
             uint32_t o[32];
