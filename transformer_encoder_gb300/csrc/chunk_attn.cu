@@ -293,13 +293,14 @@ Plan make_plan(const wenc_chunk_attention_args* a, int sms) {
   const bool search = a->n_seqs * each > 2 * dense;
   pl.rows.tiles = search ? 0 : static_cast<int>(each);
   const long long items = (search ? dense : a->n_seqs * each) * a->n_kv_heads;
-  // CTAs within one round of the machine, none without steps for its warps
+  // CTAs within two rounds of the machine (lengths differ, and a round that is full waits for its longest), none without steps
+  // for its warps
   const long long cap = static_cast<long long>(a->max_pages) * a->page_size;
   const long long seen = a->window > 0 ? static_cast<long long>(a->window) + a->sinks + a->max_new : cap;
   const long long kt = f32 ? 64 : 128, key_tiles = ((seen < cap ? seen : cap) + kt - 1) / kt;
   const long long round = (f32 || pl.nr == 1 ? 3ll : pl.nr == 2 ? 2ll : 1ll) * sms;
   pl.rows.cluster = 1;
-  while (pl.rows.cluster < 8 && pl.rows.cluster < key_tiles && 2 * items * pl.rows.cluster <= round) pl.rows.cluster *= 2;
+  while (pl.rows.cluster < 8 && pl.rows.cluster < key_tiles && items * pl.rows.cluster <= round) pl.rows.cluster *= 2;
   pl.blocks = items * pl.rows.cluster;
   return pl;
 }
