@@ -8,10 +8,21 @@
 // no plan to build and read, and no CTA idles while another works on a long unit. A unit that is whole within a run goes straight to the output;
 // of one that is cut, the pieces (at most one at either end of a run) go to the workspace, and chunk_join_kernel joins them, in order.
 //
-// Within a CTA, as in prefix_tc.cu: S = Q K^T and O += P V by tcgen05.mma into TMEM, one softmax thread per query row, the two
-// row tiles taking turns on the exponentials through named barriers, P as two bf16 parts (the large one in TMEM as the A operand, the small one in shared
-// memory). What differs: two warps gather K and V by cp.async, 128 bytes a row from wherever its page lies, so pages may
-// have any size; keys that no token of the unit sees are zero-filled and not read; and steps at the borders of what the rows see are masked.
+// Within a CTA, in the manner of prefix_tc.cu: S = Q K^T and O += P V by tcgen05.mma into TMEM, one softmax thread per query row,
+// P as two bf16 parts (2^-16), the A operands of the second product. What differs:
+//  - two warps gather K and V by cp.async, 128 bytes a row from wherever its page lies, so pages may have any size; keys that no
+//    token of the unit sees are zero-filled and not read, and steps at the borders of what the rows see are masked;
+//  - three score buffers go round the two row tiles, and both parts of P lie in the 32 columns of the 32 scores they come from: no
+//    shared memory for P, and the next scores are there before this step's P has been used;
+//  - a row's reference is the maximum of its first step, moved only when weights pass 2^20, so no step forms a maximum; it is a
+//    whole number (of log2), so moving it is exact.
+// What bounds it: the two softmax warps of a scheduler (2000 instructions a step of 256 x 128, at 56% of the issue slots: what they
+// wait for are TMEM loads and each other's results, and more warps find no registers). 2048 tokens of 20 heads over 4 behind 14000 keys
+// take 245 us, 640 TFLOP/s of the two products, 960 with the second part of P, a step some 3200 cycles; single products of its
+// MMAs alone would take 1650. On the way there (us): first form 567 (every role walked, loops unrolled: warps waited for
+// instructions), 442 walked by one warp, 313 with rolled loops, 270 with the pages looked up a step ahead and three score
+// buffers, 257 with P in TMEM alone, 245 with tiles handed over by their copies' own arrival. Not kept: taking turns on the exponentials,
+// unrolled exponentials (331), the next 32 scores loaded ahead (256), four gathering warps (252).
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -50,10 +61,11 @@ constexpr uint32_t OFF_Q = 0;
 constexpr uint32_t OFF_K = OFF_Q + 2 * Q_BYTES;
 constexpr uint32_t OFF_V = OFF_K + NK * KV_BYTES;
 constexpr uint32_t OFF_BARS = OFF_V + NV * KV_BYTES;
-// bars: q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], and per query tile t: s_full[t][2] and
-// pv_done[t][2] (of even and odd steps: a wait tells one phase from the next only, and an S may be a step ahead of its softmax, a
-// PV one of the S issuer's wait for the last), p_full[t]; drain; piece_full[NP], piece_empty[NP].
-constexpr int NUM_BARS = 2 + 2 * NK + 2 * NV + 10 + 1 + 2 * NP;
+// bars: q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], and per query tile t: s_full[t][2], p_full[t][2] and
+// pv_done[t][2]; drain; piece_full[NP], piece_empty[NP]. (Pairs, of even and odd steps: a wait tells a phase from the next one only,
+// and an S may be a step ahead of its softmax, a P one ahead of the PV issuer, which may wait for V, a PV one ahead of the S issuer's
+// wait for the last.)
+constexpr int NUM_BARS = 2 + 2 * NK + 2 * NV + 12 + 1 + 2 * NP;
 constexpr int kTakers = 11;  // warps that take pieces from the ring: all but the one that walks
 constexpr size_t SMEM = 1024 + OFF_BARS + NUM_BARS * 8 + 16;
 static_assert(SMEM + 2600 <= 232448, "shared memory of the chunk kernel");
@@ -178,11 +190,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto v_empty = [&](int s) { return bar0 + 8u * (2 + 2 * NK + NV + s); };
   const uint32_t tb0 = bar0 + 8u * (2 + 2 * NK + 2 * NV);
   auto s_full = [&](int t, int g) { return tb0 + 16u * t + 8u * (g & 1); };
-  auto p_full = [&](int t) { return tb0 + 32u + 8u * t; };
-  auto pv_done = [&](int t, int g) { return tb0 + 48u + 16u * t + 8u * (g & 1); };
-  const uint32_t drain = tb0 + 80u;
-  auto piece_full = [&](int i) { return tb0 + 88u + 8u * i; };
-  auto piece_empty = [&](int i) { return tb0 + 88u + 8u * (NP + i); };
+  auto p_full = [&](int t, int g) { return tb0 + 32u + 16u * t + 8u * (g & 1); };
+  auto pv_done = [&](int t, int g) { return tb0 + 64u + 16u * t + 8u * (g & 1); };
+  const uint32_t drain = tb0 + 96u;
+  auto piece_full = [&](int i) { return tb0 + 104u + 8u * i; };
+  auto piece_empty = [&](int i) { return tb0 + 104u + 8u * (NP + i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_BARS + NUM_BARS * 8);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const WaitCtx wc{abort_flag, err};
@@ -202,11 +214,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(v_empty(s), 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(s_full(t, 0), 1);
-      mbar_init(s_full(t, 1), 1);
-      mbar_init(p_full(t), 4);  // one arrival per softmax warp of the tile
-      mbar_init(pv_done(t, 0), 1);
-      mbar_init(pv_done(t, 1), 1);
+      for (int g = 0; g < 2; ++g) {
+        mbar_init(s_full(t, g), 1);
+        mbar_init(p_full(t, g), 4);  // one arrival per softmax warp of the tile
+        mbar_init(pv_done(t, g), 1);
+      }
     }
     mbar_init(drain, 2);  // one commit per MMA-issuing thread
     for (int i = 0; i < NP; ++i) {
@@ -440,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cp_async_commit();
       cp_async_wait<0>();  // (also on the error path: the copies land before the CTA exits)
     } else {
-      // ---------------- UMMA issuers: warp 2 S_A and S_B, warp 3 O_A and O_B. The whole warp waits; lane 0 issues.
+      // ---------------- UMMA issuers: warp 2 S_A and S_B, warp 3 O_A and O_B. The whole warp waits; one thread issues.
       bool ok = true;
       if (warp == 2) {
         constexpr uint32_t idesc_s = idesc_bf16_f32(BQ, BKV, false);  // B = K tile, K-major, N = 128
@@ -487,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
 #pragma unroll 1
             for (int t = 0; t < 2; ++t) {
-              if (!mbar_wait_warp(p_full(t), vc & 1, wc, 16)) { ok = false; break; }
+              if (!mbar_wait_warp(p_full(t, vc), (vc >> 1) & 1, wc, 16)) { ok = false; break; }
               tc_fence_after();
               const uint64_t vdesc = sdesc_sw128(sV + st * KV_BYTES, 1024, 1024);
               const uint32_t to = tO(t), from = tS(buf), bar = pv_done(t, vc), v_bar = v_empty(st), more = j > k0;
@@ -548,8 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // The row's reference is the maximum (rounded up to a whole number, so that references differ by powers of two) of the first
         // step of which it sees a key, and stays as long as the weights stay below 2^20. The maximum of every step, formed
-        // first, took a quarter of the time. Loops are not unrolled further: with 128 scores in registers and straight code,
-        // warps waited for instructions more than for anything else.
+        // first, costs a quarter of the instructions.
         float m_new = m;
         if (__any_sync(0xffffffffu, m == -CUDART_INF_F)) {
           float mx = -CUDART_INF_F;
@@ -603,7 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Rare: scores far above the reference (or none at all). It moves, by a power of two, and the step's weights that are
             // written already move with it.
             const float moved = much ? fmaxf(m_new, ceilf(max32(r) * scale_log2)) : m_new;
-            const float f = m_new == moved ? 1.0f : ex2_approx(m_new - moved);
+            const float down = m_new - moved;  // (a whole number)
+            const float f = m_new == moved ? 1.0f : down > -126.5f ? __int_as_float((127 + static_cast<int>(down)) << 23) : 0.0f;
             sum *= f;
             m_new = moved;
             auto scaled = [&](uint32_t x) { return pack_bf16x2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f); };
@@ -640,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = m_new;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(t));
+        if (lane == 0) mbar_arrive(p_full(t, g));
       }
       if (!ok || !mbar_wait_warp(pv_done(t, g - 1), ((g - 1) >> 1) & 1, wc, 19)) break;
       // The piece's result, from O in TMEM once the PV product of its last step is done; the next piece's first PV product
