@@ -481,8 +481,8 @@ typedef struct {
   const int32_t* free_pages; /* [n_free_pages] the first *free_count are free; they are taken from the end */
   int n_free_pages;
   const int32_t* free_count; /* [1] */
-  int32_t* lens_out;         /* [n_seqs] lengths with the new tokens; apart from lens */
-  int32_t* free_count_out;   /* [1] pages that stay free; apart from free_count */
+  int32_t* lens_out;         /* [n_seqs] lengths with the new tokens; this and the next two apart from every input */
+  int32_t* free_count_out;   /* [1] pages that stay free */
   int32_t* seq_start;        /* [n_seqs + 1] row offsets, as wenc_kv_append and wenc_chunk_attention take them */
   int32_t* positions;        /* [n_rows] each row's position, 0 for padding; 16-byte aligned */
   int64_t* slots;            /* [n_rows] page * page_size + place of each row, -1 for padding; 16-byte aligned */
@@ -512,9 +512,9 @@ typedef struct {
   int32_t* free_pages;       /* [n_free_pages]; what goes back is written from *free_count on */
   int n_free_pages;
   const int32_t* free_count; /* [1] */
-  int32_t* lens_out;         /* [n_seqs] 0 for finished sequences, else lens; apart from lens */
-  int32_t* free_count_out;   /* [1] apart from free_count */
-  int32_t* trimmed_out;      /* with a window: [n_seqs] the next call's trimmed; apart from trimmed */
+  int32_t* lens_out;         /* [n_seqs] 0 for finished sequences, else lens; the outputs lie apart from every input */
+  int32_t* free_count_out;   /* [1] */
+  int32_t* trimmed_out;      /* with a window: [n_seqs] the next call's trimmed */
 } wenc_kv_release_args;
 
 /* wenc_kv_release -- pages of a paged cache that no later token needs, back to the free ones: all pages of finished

@@ -40,7 +40,7 @@ def _chunk(**kw):
     (dict(v_pages=None), 1, b"NULL"), (dict(block_table=None), 1, b"NULL"), (dict(lens=None), 1, b"NULL"),
     (dict(q_stride=504), 1, b"stride"), (dict(out_stride=511), 1, b"stride"), (dict(q_stride=516), 1, b"16 bytes"),
     (dict(k_page_stride=2048), 1, b"stride"), (dict(v_page_stride=4100), 1, b"16 bytes"), (dict(k_page_stride=1 << 36), 2, b"2^36"),
-    (dict(block_table_stride=2), 1, b"block_table_stride"), (dict(q=264), 1, b"aligned"), (dict(out=258), 1, b"aligned"),
+    (dict(block_table_stride=2), 1, b"block_table_stride"), (dict(q=264), 1, b"aligned"), (dict(out=258), 1, b"aligned"), (dict(), 1, b"apart"),
 ])
 def test_chunk_attention_refuses(L, kw, status, word):
     assert L.wenc_chunk_attention(ctypes.byref(_chunk(**kw)), None) == status
@@ -68,7 +68,8 @@ def _extend(**kw):
     (dict(n_rows=-1), 1, b"positive"), (dict(n_seqs=65537), 2, b"sequences"), (dict(n_rows=0x7fffffff), 2, b"n_rows"),
     (dict(page_size=1 << 30), 2, b"2^31"), (dict(block_table_stride=3), 1, b"block_table_stride"),
     (dict(positions=9220), 1, b"aligned"), (dict(slots=10248), 1, b"aligned"), (dict(lens_out=512), 1, b"apart"),
-    (dict(lens_out=520), 1, b"apart"), (dict(free_count_out=4096), 1, b"apart"),
+    (dict(lens_out=520), 1, b"apart"), (dict(free_count_out=4096), 1, b"apart"), (dict(lens_out=260), 1, b"apart"),
+    (dict(seq_start=500), 1, b"apart"), (dict(seq_start=244), 1, b"apart"),
 ])
 def test_kv_extend_refuses(L, kw, status, word):
     assert L.wenc_kv_extend(ctypes.byref(_extend(**kw)), None) == status
@@ -89,6 +90,7 @@ def _release(**kw):
     (dict(sinks=-1), 1, b"sinks"), (dict(n_seqs=65537), 2, b"sequences"), (dict(n_free_pages=0), 1, b"positive"),
     (dict(page_size=1 << 30), 2, b"2^31"), (dict(block_table_stride=3), 1, b"block_table_stride"),
     (dict(lens_out=516), 1, b"apart"), (dict(trimmed_out=1536), 1, b"apart"), (dict(free_count_out=4096), 1, b"apart"),
+    (dict(lens_out=1540), 1, b"apart"),
 ])
 def test_kv_release_refuses(L, kw, status, word):
     assert L.wenc_kv_release(ctypes.byref(_release(**kw)), None) == status

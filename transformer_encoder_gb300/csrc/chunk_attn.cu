@@ -404,6 +404,7 @@ extern "C" wenc_status wenc_chunk_attention(const wenc_chunk_attention_args* a, 
   for (long long x : strides)
     if (x % per16 != 0) return bad(WENC_ERR_INVALID_ARG, "strides must be multiples of 16 bytes");
   if (a->n_tokens == 0) return WENC_OK;
+  if (a->q == a->out) return bad(WENC_ERR_INVALID_ARG, "chunk_attention: out must lie apart from q");
   int sms = 0;
   uint32_t* err = nullptr;
   const wenc_status dst = wenc_internal_device(&sms, &err);

@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ---------------- MMA issuers, two for every other piece: the whole warp waits, one thread issues. A group's MMAs are straight lines behind
     // one election (44 cycles each, or their own time; with a branch between them 110 to 130). What lies between the lines, waits that
     // are over and a descriptor, is some 700 cycles a piece, more than its MMAs take: so the other issuer's run meanwhile. They go in turn: a
-    // wait for an accumulator tells one phase of its barrier from the next, not from the one after.
+    // wait tells one phase of a barrier from the next, not from the one after.
     constexpr int kLine = GROUP < 64 ? GROUP : 64, kSteps = kLine / 16, kLines = kPiece / kLine;  // (a group of 128 in two)
     static_assert(kXStages == 4 && kAStages == 2, "slots and parities by masks");
     const uint32_t idesc = idesc_bf16_f32(128, (m_here + 15) / 16 * 16, false);
@@ -369,15 +369,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       uint64_t desc[PARTS];
       uint32_t x_bar[PARTS];
       ok = mbar_wait_warp(a_full(a_slot), j >> 1 & 1, wc, 61);
+      auto tiles = [&]() {
 #pragma unroll
-      for (int q = 0; q < PARTS; ++q) {
-        const uint32_t xi = j * PARTS + q;
-        ok = ok && mbar_wait_warp(x_full(xi & 3), xi >> 2 & 1, wc, 62);
-        desc[q] = sdesc_sw128(s0 + (xi & 3) * kXBytes, 16, 1024);
-        x_bar[q] = x_empty(xi & 3);
-      }
+        for (int q = 0; q < PARTS; ++q) {
+          const uint32_t xi = j * PARTS + q;
+          ok = ok && mbar_wait_warp(x_full(xi & 3), xi >> 2 & 1, wc, 62);
+          desc[q] = sdesc_sw128(s0 + (xi & 3) * kXBytes, 16, 1024);
+          x_bar[q] = x_empty(xi & 3);
+        }
+      };
+      // (one tile a piece: an issuer's slots are its own; three: the other issuer's tiles come between, so its turn comes first)
+      if (PARTS == 1) tiles();
       const uint32_t a_at = tA(a_slot), a_bar = a_empty(a_slot), other = turn(a_slot ^ 1);
       if (j > 0) ok = ok && mbar_wait_warp(turn(a_slot), (j - 1) >> 1 & 1, wc, 68);
+      if (PARTS > 1) tiles();
 #pragma unroll
       for (int i = 0; i < kLines; ++i) {
         const bool begins = i * kLine % GROUP == 0, ends = (i + 1) * kLine % GROUP == 0;
@@ -524,6 +529,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int i = 0; i < kTcMost / 2; ++i)
       if (i < half && t0 + i < m_here) part[(t0 + i) * 128 + ch] = acc[i];
   }
+  __syncwarp();
   if (p.ksplit > 1) cluster_arrive_wait();
   else __syncthreads();
   if (fits && !*abort_flag) {
@@ -557,6 +563,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
   }
+  __syncwarp();
   if (p.ksplit > 1) cluster_arrive_wait();  // no CTA leaves while another reads its sums
   tc_fence_before();
   __syncthreads();

@@ -367,10 +367,18 @@ wenc_status bad(wenc_status s, const char* fmt, long long a = 0, long long b = 0
   return wenc_internal_fail(s, buf);
 }
 
-// Whether two arrays of n and m 32-bit numbers share bytes.
-bool overlap(const void* a, long long n, const void* b, long long m) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + 4 * m && y < x + 4 * n;
+struct Range {  // of 32-bit numbers
+  const void* at;
+  long long n;
+};
+// Whether an input shares bytes with an output.
+bool share(const Range (&in)[3], const Range (&out)[3]) {
+  for (const Range& i : in)
+    for (const Range& o : out) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(i.at), y = reinterpret_cast<uintptr_t>(o.at);
+      if (x && y && x < y + 4 * o.n && y < x + 4 * i.n) return true;
+    }
+  return false;
 }
 
 wenc_status launch_failed(const char* what, cudaError_t e) {
@@ -398,9 +406,10 @@ extern "C" wenc_status wenc_kv_extend(const wenc_kv_extend_args* a, wenc_stream_
     return bad(WENC_ERR_INVALID_ARG, "kv_extend: block_table_stride %lld < max_pages %lld", a->block_table_stride, a->max_pages);
   if ((reinterpret_cast<uintptr_t>(a->positions) | reinterpret_cast<uintptr_t>(a->slots)) & 15u)
     return bad(WENC_ERR_INVALID_ARG, "kv_extend: positions and slots must be 16-byte aligned");
-  // (blocks read the lengths while others write the new ones)
-  if (overlap(a->lens, a->n_seqs, a->lens_out, a->n_seqs) || overlap(a->free_count, 1, a->free_count_out, 1))
-    return bad(WENC_ERR_INVALID_ARG, "kv_extend: lens_out and free_count_out must lie apart from lens and free_count");
+  // (blocks read the inputs while others write)
+  const Range in[] = {{a->new_tokens, a->n_seqs}, {a->lens, a->n_seqs}, {a->free_count, 1}};
+  const Range out[] = {{a->lens_out, a->n_seqs}, {a->free_count_out, 1}, {a->seq_start, a->n_seqs + 1}};
+  if (share(in, out)) return bad(WENC_ERR_INVALID_ARG, "kv_extend: lens_out, free_count_out and seq_start must lie apart from the inputs");
   int sms = 0;
   uint32_t* err = nullptr;
   const wenc_status dst = wenc_internal_device(&sms, &err);
@@ -452,9 +461,9 @@ extern "C" wenc_status wenc_kv_release(const wenc_kv_release_args* a, wenc_strea
     return bad(WENC_ERR_UNSUPPORTED, "kv_release: max_pages %lld x page_size %lld passes 2^31 - 1", a->max_pages, a->page_size);
   if (a->n_seqs > 1 && a->block_table_stride < a->max_pages)
     return bad(WENC_ERR_INVALID_ARG, "kv_release: block_table_stride %lld < max_pages %lld", a->block_table_stride, a->max_pages);
-  if (overlap(a->lens, a->n_seqs, a->lens_out, a->n_seqs) || overlap(a->free_count, 1, a->free_count_out, 1) ||
-      overlap(a->trimmed, a->n_seqs, a->trimmed_out, a->n_seqs))
-    return bad(WENC_ERR_INVALID_ARG, "kv_release: lens_out, free_count_out and trimmed_out must lie apart from what they follow");
+  const Range in[] = {{a->lens, a->n_seqs}, {a->trimmed, a->n_seqs}, {a->free_count, 1}};
+  const Range out[] = {{a->lens_out, a->n_seqs}, {a->trimmed_out, a->n_seqs}, {a->free_count_out, 1}};
+  if (share(in, out)) return bad(WENC_ERR_INVALID_ARG, "kv_release: lens_out, trimmed_out and free_count_out must lie apart from the inputs");
   int sms = 0;
   uint32_t* err = nullptr;
   const wenc_status dst = wenc_internal_device(&sms, &err);
