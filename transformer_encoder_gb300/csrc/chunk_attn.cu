@@ -273,14 +273,16 @@ struct Plan {
   size_t bytes = 0;
 };
 
-constexpr int kFew = 16;  // rows per key head up to which a bf16 sequence is attended here
+// bf16: up to kLeastTc rows per key head, every sequence is attended here, in tiles of up to 32 rows; a call that may have more
+// leaves sequences of more than kFew to chunk_tc.cu, and takes tiles of 16 for the others.
+constexpr int kFew = 16, kLeastTc = 64;
 
 Plan make_plan(const wenc_chunk_attention_args* a, int sms) {
   Plan pl;
   const bool f32 = a->dtype == WENC_DTYPE_F32;
   const long long r = a->n_heads / a->n_kv_heads;
   long long most = static_cast<long long>(a->max_new) * r;
-  if (!f32 && r <= 128 && a->scale > 0.0f && most > kFew) {
+  if (!f32 && r <= 128 && a->scale > 0.0f && most > kLeastTc) {
     pl.tc = true;
     pl.bytes = wenc_host::chunk_tc_workspace(sms);
     most = kFew;

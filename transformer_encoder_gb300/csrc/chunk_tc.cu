@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 32);  // the lanes of the warp that copies
+    mbar_init(q_full, 64);  // the lanes of the two warps that copy
     mbar_init(q_empty, 1);  // released by the S issuer's commit after a piece's last S
     for (int s = 0; s < NK; ++s) {
       mbar_init(k_full(s), 32);
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // control warpgroup: registers to the softmax warpgroups first
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kCtrlRegs) : "memory");
     if (warp < 2) {
-      // ---------------- gathering: warp 0 the queries and K, warp 1 V.
+      // ---------------- gathering: warp 0 K, warp 1 V, and a tile of the queries each.
       const bool is_k = warp == 0;
       const uint8_t* pages = is_k ? p.k_pages : p.v_pages;
       const uint32_t page16 = is_k ? p.k_page16 : p.v_page16;
@@ -376,20 +376,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           if (!more) break;
-          if (!mbar_wait_warp(q_empty, (np & 1) ^ 1u, wc, 9)) break;
         } else if (!take(np)) {
           break;
         }
         const Unit u = pc.u;
-        if (is_k) {
-#pragma unroll 1
-          for (int i = 0; i < 2 * BQ / 4; ++i) {
-            const int row = 4 * (i & 31) + r4, tok = row / p.r, hr = row - tok * p.r;
-            const int at = u.i0 + (i >> 5) * a.tokens + tok;  // token of the sequence
-            const bool in = tok < a.tokens && at <= u.i1 &&
-                            in_bounds(pc.row0 + at < p.n_tokens && pc.hk * p.r + hr < p.H, err, 121);
-            const uint8_t* src = p.q + (in ? static_cast<long long>(pc.row0 + at) * p.q_stride + (pc.hk * p.r + hr) * (HD * 2) + c * 16 : 0);
-            cp_async16(sQ + (i >> 5) * Q_BYTES + (i & 31) / 2 * 1024 + (i & 1 ? odd : even), src, in);
+        if (!mbar_wait_warp(q_empty, (np & 1) ^ 1u, wc, 9)) break;
+        {
+          // the queries: a row tile a warp. Token and head of a row run along (divided for each of them, a piece's queries took
+          // 15000 cycles, 8 us).
+          int tok = r4 / p.r, hr = r4 - tok * p.r;
+          const int d_tok = 4 / p.r, d_hr = 4 - d_tok * p.r, at0 = u.i0 + warp * a.tokens;
+          const uint8_t* src = p.q + static_cast<long long>(pc.row0) * p.q_stride + pc.hk * p.r * (HD * 2) + c * 16;
+          const uint32_t dst = sQ + warp * Q_BYTES;
+#pragma unroll 4
+          for (int i = 0; i < BQ / 4; ++i) {
+            const bool in = tok < a.tokens && at0 + tok <= u.i1 &&
+                            in_bounds(pc.row0 + at0 + tok < p.n_tokens && pc.hk * p.r + hr < p.H, err, 121);
+            cp_async16(dst + (i >> 1) * 1024 + (i & 1 ? odd : even), in ? src + (at0 + tok) * p.q_stride + hr * (HD * 2) : p.q, in);
+            tok += d_tok;
+            hr += d_hr;
+            if (hr >= p.r) {
+              hr -= p.r;
+              ++tok;
+            }
           }
           hand_over(q_full);
         }

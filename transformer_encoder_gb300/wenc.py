@@ -998,8 +998,8 @@ def chunk_attention(q, k_pages, v_pages, block_table, lens, *, seq_start=None, m
             kps, vps, pages, size, block_table.data_ptr(), tab_stride, max_pages, lens.data_ptr(), start, window or 0,
             sinks, scale)
     ws = ws_bytes = 0
-    # (float32 calls, and those of up to 16 rows per key head and sequence, never need a workspace)
-    if workspace is None and dt and max_new * H > 16 * kv:
+    # (float32 calls, and those of up to 64 rows per key head and sequence, never need a workspace)
+    if workspace is None and dt and max_new * H > 64 * kv:
         need = _lib.wenc_chunk_attention_workspace(_CHUNK_PACK.pack(*args, 0, 0))
         workspace = _empty(need, torch.uint8, q.device, stream) if need else None
     if workspace is not None:
