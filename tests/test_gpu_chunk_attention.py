@@ -44,9 +44,11 @@ def plain(q, k, v, pos, window, sinks, scale):
 
 
 class Case:
-    """One problem. Keys that no token sees, and pages without one, hold NaN; so do padding rows of q."""
+    """One problem. Keys that no token sees, and pages without one, hold NaN; so do padding rows of q. wide: a block table for
+    caches so long that the call is not taken for a little one, and its long chunks go to the tensor cores' form (bf16)."""
 
-    def __init__(self, dtype, new, past, H, Hkv, window=0, sinks=0, page=16, pad=0, strided=False, seed=0, extra_pages=3, odd_pages=False):
+    def __init__(self, dtype, new, past, H, Hkv, window=0, sinks=0, page=16, pad=0, strided=False, seed=0, extra_pages=3, odd_pages=False,
+                 wide=False):
         import torch
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
@@ -56,15 +58,15 @@ class Case:
         self.window, self.sinks, self.page = window, sinks, page
         self.start = np.cumsum([0] + self.new)
         rows = int(self.start[-1]) + pad
-        wide = torch.full((rows, H + 3, 64), float("nan"), device="cuda", dtype=self.dt)
+        around = torch.full((rows, H + 3, 64), float("nan"), device="cuda", dtype=self.dt)
         q = torch.randn(rows, H, 64, generator=g, device="cuda").to(self.dt)
         q[int(self.start[-1]):] = float("nan")
         if strided:
-            wide[:, 1:1 + H] = q
-            q = wide[:, 1:1 + H]
+            around[:, 1:1 + H] = q
+            q = around[:, 1:1 + H]
         self.q = q
         need = [-(-n // page) for n in self.lens]
-        total, width = max(1, sum(need)) + extra_pages, max(1, max(need)) + 1
+        total, width = max(1, sum(need)) + extra_pages, max(1, max(need)) + (4096 if wide else 1)
         order = r.permutation(total)
         shape = (total, page, Hkv, 64)
         self.kc, self.vc = (torch.full(shape, float("nan"), device="cuda", dtype=self.dt) for _ in range(2))
@@ -153,11 +155,12 @@ def test_windows_and_sinks(dtype, window, sinks, new):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("H,Hkv", [(1, 1), (6, 6), (20, 4), (5, 1), (16, 2), (40, 1)])
 @pytest.mark.parametrize("window", [0, 50])
-def test_head_layouts_of_ragged_chunks(dtype, H, Hkv, window):
+@pytest.mark.parametrize("wide", [False, True])
+def test_head_layouts_of_ragged_chunks(dtype, H, Hkv, window, wide):
     """Chunks of every size in one call, padding rows behind them that stay as they are."""
     import torch
     new = [1, 0, 2, 130, 1, 33, 7, 1, 257, 0]
-    c = Case(dtype, new, _ints(H, len(new), 0, 300), H, Hkv, window, 3 if window else 0, page=24, pad=9, strided=H == 6, seed=H)
+    c = Case(dtype, new, _ints(H, len(new), 0, 300), H, Hkv, window, 3 if window else 0, page=24, pad=9, strided=H == 6, seed=H, wide=wide)
     out = torch.full(c.q.shape, 7.0, device="cuda", dtype=c.dt)
     assert c.run(out=out) is out
     c.check(out)
@@ -169,10 +172,59 @@ def test_head_layouts_of_ragged_chunks(dtype, H, Hkv, window):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("new,past", [([300], [0]), ([511, 129], [700, 5]), ([64, 64, 64], [64, 2000, 0]), ([1000], [3000])])
 @pytest.mark.parametrize("H,Hkv", [(4, 4), (10, 2)])
-def test_prompts(dtype, new, past, H, Hkv):
+@pytest.mark.parametrize("wide", [False, True])
+def test_prompts(dtype, new, past, H, Hkv, wide):
     """Many tokens of one sequence: rows over several tiles, keys from a prompt's first to those of a long cache."""
-    c = Case(dtype, new, past, H, Hkv, page=16, seed=sum(new))
+    c = Case(dtype, new, past, H, Hkv, page=16, seed=sum(new), wide=wide)
     c.check(c.run())
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 4), (17, 0), (100, 40), (64, 200), (128, 0), (5000, 3)])
+def test_windows_of_many_rows(window, sinks):
+    """The same borders in the tensor cores' form: enough rows that a short window's call is no little one."""
+    c = Case("bf16", [300, 70], [1000, 20], 40, 20, window, sinks, page=8, seed=window + sinks)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("page", [1, 3, 24, 100])
+def test_pages_of_many_rows(page):
+    c = Case("bf16", [130, 1, 270], [0, 40, 515], 20, 4, page=page, seed=page, wide=True)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("H,Hkv", [(128, 1), (130, 1), (66, 1), (3, 1)])
+def test_many_query_heads_a_key_head(H, Hkv):
+    """One token a row tile, rows that leave most of a tile empty, and more heads than a tile has rows (the other form)."""
+    c = Case("bf16", [90, 1, 3], [200, 40, 0], H, Hkv, page=16, seed=H, wide=True)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("jump", [30.0, 200.0, 3000.0])
+def test_scores_that_leave_their_reference_behind(jump):
+    """Scores far above those of a row's first keys, suddenly and step by step: the reference that weights are formed against follows."""
+    import torch
+    c = Case("bf16", [200], [1500], 4, 2, seed=14, wide=True)
+    pages = c.table[0, :-(-1700 // 16)].long()
+    k = torch.zeros(1712, 2, 64, device="cuda", dtype=torch.bfloat16)
+    k[:1700] = c.keys[0][0].to(torch.bfloat16) * 0.25
+    # along the mean query, so that every row's scores jump: at key 700, and a little at every 60th
+    c.q.fill_(0.25)
+    k[700, :, :] += jump / 16
+    for i, key in enumerate(range(900, 1690, 60)):
+        k[key, 1] += jump / 16 * (1 + i / 8)
+    c.kc[pages] = k.view(-1, 16, 2, 64)
+    c.keys[0] = (k[:1700].double(), c.keys[0][1])
+    out, (ref, absv, _) = c.run().double(), c.reference()
+    # The bound above, whose two roundings of the exponent's argument (2^-24 each of up to 1.4427 A) are not held to arguments
+    # below 128 here. A <= 64 * 0.25 * (187.5 * 2.625 + 2) * 0.125 < 990, e < 0.01, so first order in e still holds (e^2 < 2^-13 is
+    # added).
+    _, _, A = c.reference()
+    assert (A < 990).all()
+    e = 1.1 * A * 64 * 2.0 ** -23 + 2 * 1.4427 * A * 2.0 ** -24 + 2.0 ** -16 + 2.0 ** -21
+    bound = 2.0 ** -8 * ref.abs() + (2 * e + 2.0 ** -13 + 2.0 ** -16 + 2 * 1700 * 2.0 ** -23) * absv
+    assert torch.isfinite(out).all()
+    err = (out - ref).abs()
+    assert (err <= bound + 1e-30).all(), float((err / (bound + 1e-30)).max())
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -191,25 +243,28 @@ def test_equal_chunks_without_offsets(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_a_bound_on_the_tokens_does_not_change_them(dtype):
+@pytest.mark.parametrize("wide", [False, True])
+def test_a_bound_on_the_tokens_does_not_change_them(dtype, wide):
     """What a sequence brings decides its results' exactness, not how many the call allows."""
-    c = Case(dtype, [1, 3, 200, 12], [500, 60, 10, 4000], 8, 2, seed=5)
+    c = Case(dtype, [1, 3, 200, 12], [500, 60, 10, 4000], 8, 2, seed=5, wide=wide)
     c.check(c.run())
     c.check(c.run(max_new=None))
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("scale", [1.0 / 64, -0.125, 0.0])
-def test_scales(dtype, scale):
-    c = Case(dtype, [1, 40, 200], [300, 70, 90], 4, 2, seed=6)
+@pytest.mark.parametrize("wide", [False, True])
+def test_scales(dtype, scale, wide):
+    c = Case(dtype, [1, 40, 200], [300, 70, 90], 4, 2, seed=6, wide=wide)
     c.check(c.run(scale=scale), scale)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_tokens_in_front_of_the_cache_see_nothing(dtype):
+@pytest.mark.parametrize("wide", [False, True])
+def test_tokens_in_front_of_the_cache_see_nothing(dtype, wide):
     """A length below the tokens that a sequence brings: the first of them stand at negative positions."""
     import torch
-    c = Case(dtype, [6, 150], [0, 0], 4, 2, seed=7)
+    c = Case(dtype, [6, 150], [0, 0], 4, 2, seed=7, wide=wide)
     full = c.reference()[0]
     c.tlens.copy_(torch.tensor([2, 40], dtype=torch.int32))
     out = c.run().double()
@@ -221,10 +276,12 @@ def test_tokens_in_front_of_the_cache_see_nothing(dtype):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("new,past,H,Hkv", [([1, 1, 8], [200, 30, 100], 4, 2), ([200, 1, 300], [50, 400, 900], 4, 2)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 3e38])
-def test_values_that_are_no_numbers_reach_the_rows_that_see_them(dtype, new, past, H, Hkv, bad):
+@pytest.mark.parametrize("many", [1, 10])
+def test_values_that_are_no_numbers_reach_the_rows_that_see_them(dtype, new, past, H, Hkv, bad, many):
     """A value (and a key) behind a token's own position, or outside its window, leaves its row as it is; the rows that see it take it
     as a plain evaluation does."""
     import torch
+    H, Hkv = H * many, Hkv * many  # (with ten times the heads the long chunks are no little call)
     c = Case(dtype, new, past, H, Hkv, 120, 2, page=8, seed=8)
     clean = c.run()
     s, n, m = 2, c.lens[2], new[2]
@@ -240,7 +297,7 @@ def test_values_that_are_no_numbers_reach_the_rows_that_see_them(dtype, new, pas
             pos = torch.arange(n - m, n, device="cuda")
             sees = (key <= pos) & ((key > pos - 120) | (key < 2))
             rows = torch.zeros(sum(new), H, dtype=torch.bool, device="cuda")
-            rows[sum(new[:2]):, H // Hkv:] = sees.view(-1, 1)
+            rows[sum(new[:2]):, H // Hkv:2 * (H // Hkv)] = sees.view(-1, 1)
             # Rows that do not see it keep their values. Not every bit: the element beside the bad value is formed a second way, and a
             # score that moves the running maximum of one row of a tile moves its other rows' references too (to what they are
             # anyway). Both results lie within the bound above of one value: 2^-8 each of it for the rounding; the rest, for
@@ -263,10 +320,11 @@ def test_values_that_are_no_numbers_reach_the_rows_that_see_them(dtype, new, pas
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_a_lowest_score_is_no_mask(dtype):
+@pytest.mark.parametrize("wide", [False, True])
+def test_a_lowest_score_is_no_mask(dtype, wide):
     """Keys whose scores are the type's lowest values for all that a row sees: an even mean, not zeros."""
     import torch
-    c = Case(dtype, [3, 150], [40, 3], 2, 2, seed=9)
+    c = Case(dtype, [3, 150], [40, 3], 2, 2, seed=9, wide=wide)
     c.q[:] = 0
     out = c.run()
     c.check(out)
@@ -284,11 +342,12 @@ def test_a_lowest_score_is_no_mask(dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("case", ["page", "length", "long", "offset", "behind", "many"])
-def test_bad_lengths_offsets_and_pages_are_reported(dtype, case):
+@pytest.mark.parametrize("wide", [False, True])
+def test_bad_lengths_offsets_and_pages_are_reported(dtype, case, wide):
     """Reported, nothing out of range accessed, and the other sequences right."""
     import torch
     from transformer_encoder_gb300 import WencError, sync_status
-    c = Case(dtype, [1, 200, 3, 40], [100, 300, 20, 60], 4, 2, seed=10)
+    c = Case(dtype, [1, 200, 3, 40], [100, 300, 20, 60], 4, 2, seed=10, wide=wide)
     want, ref = c.run(), c.reference()[0]
     kw = {}
     if case == "page":
@@ -324,16 +383,17 @@ def test_bad_lengths_offsets_and_pages_are_reported(dtype, case):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_strided_tensors(dtype):
+@pytest.mark.parametrize("wide", [False, True])
+def test_strided_tensors(dtype, wide):
     import torch
-    c = Case(dtype, [1, 60, 300], [100, 3, 500], 6, 2, page=24, strided=True, odd_pages=True, seed=11)
-    wide = torch.full((c.q.shape[0], 10, 64), 5.0, device="cuda", dtype=c.dt)
-    out = wide[:, 2:8]
+    c = Case(dtype, [1, 60, 300], [100, 3, 500], 6, 2, page=24, strided=True, odd_pages=True, seed=11, wide=wide)
+    around = torch.full((c.q.shape[0], 10, 64), 5.0, device="cuda", dtype=c.dt)
+    out = around[:, 2:8]
     table = torch.full((3, c.table.shape[1] + 5), -9, dtype=torch.int32, device="cuda")
     table[:, 2:2 + c.table.shape[1]] = c.table
     c.table = table[:, 2:2 + c.table.shape[1]]
     c.check(c.run(out=out))
-    assert (wide[:, :2] == 5).all() and (wide[:, 8:] == 5).all()
+    assert (around[:, :2] == 5).all() and (around[:, 8:] == 5).all()
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -354,11 +414,12 @@ def test_offsets_past_32_bits(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_streams_workspaces_and_graphs(dtype):
+@pytest.mark.parametrize("wide", [False, True])
+def test_streams_workspaces_and_graphs(dtype, wide):
     """On a stream of its own, with a given workspace, captured and replayed with other lengths."""
     import torch
     from transformer_encoder_gb300 import chunk_attention, sync_status
-    c = Case(dtype, [1, 200, 3, 40], [100, 300, 20, 600], 4, 2, seed=13)
+    c = Case(dtype, [1, 200, 3, 40], [100, 300, 20, 600], 4, 2, seed=13, wide=wide)
     want = c.run()
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())

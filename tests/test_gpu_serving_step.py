@@ -66,7 +66,7 @@ def test_a_loop_of_steps(window, captured):
     from transformer_encoder_gb300 import kv_append, sync_status
     r = np.random.default_rng(3)
     n, rows, steps, max_new = 9, 330, 7, 150
-    m, pool = Model(window, 5), Pool(n, 400, 90)
+    m, pool = Model(window, 5), Pool(n, 400, 900)
     m.marks = torch.zeros(n, dtype=torch.int32, device="cuda")
     x, stream = torch.zeros(rows, D, device="cuda", dtype=torch.bfloat16), torch.zeros(rows, D, device="cuda")
     new, finished = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.bool, device="cuda")
@@ -135,7 +135,7 @@ def test_two_calls_at_once_have_a_workspace_each():
     import torch
     from test_gpu_chunk_attention import Case
     from transformer_encoder_gb300 import chunk_attention, sync_status
-    a, b = Case("bf16", [600, 1], [900, 50], 8, 2, seed=21), Case("bf16", [40, 700], [3, 1500], 8, 2, 300, 4, seed=22)
+    a, b = Case("bf16", [600, 1], [900, 50], 8, 2, seed=21, wide=True), Case("bf16", [40, 700], [3, 1500], 8, 2, 300, 4, seed=22, wide=True)
     want = [c.run() for c in (a, b)]
     streams = [torch.cuda.Stream() for _ in range(2)]
     for s in streams:

@@ -273,16 +273,22 @@ struct Plan {
   size_t bytes = 0;
 };
 
-// bf16: up to kLeastTc rows per key head, every sequence is attended here, in tiles of up to 32 rows; a call that may have more
-// leaves sequences of more than kFew to chunk_tc.cu, and takes tiles of 16 for the others.
+// bf16: up to kLeastTc rows per key head, and calls of up to kLittle pairs of a query row and a key that they may have, are attended
+// here, in tiles of up to 32 rows. Other calls leave sequences of more than kFew rows to chunk_tc.cu, and take tiles of 16 for
+// the rest. Measured (us, here / there with its three launches): 40 rows of each of 32 sequences, 4 key heads, 3000 keys 28 / 52;
+// 8 heads, 1 x 256 tokens behind 256 (0.8 M pairs) 17 / 26, 2 x 256 behind 1000 (4.6 M) 23 / 27, 8 x 256 behind 256 (6.3 M) 31 /
+// 29, 16 x 100 behind 500 (7 M) 38 / 30; 20 heads over 4, 128 tokens behind 2000 (5.3 M) 29 / 28, behind 8000 71 / 35.
 constexpr int kFew = 16, kLeastTc = 64;
+constexpr long long kLittle = 1ll << 22;
 
 Plan make_plan(const wenc_chunk_attention_args* a, int sms) {
   Plan pl;
   const bool f32 = a->dtype == WENC_DTYPE_F32;
   const long long r = a->n_heads / a->n_kv_heads;
   long long most = static_cast<long long>(a->max_new) * r;
-  if (!f32 && r <= 128 && a->scale > 0.0f && most > kLeastTc) {
+  const long long cap = static_cast<long long>(a->max_pages) * a->page_size;
+  const long long in_window = a->window > 0 ? static_cast<long long>(a->window) + a->sinks + a->max_new : cap, seen = in_window < cap ? in_window : cap;
+  if (!f32 && r <= 128 && a->scale > 0.0f && most > kLeastTc && static_cast<long long>(a->n_tokens) * a->n_heads > kLittle / seen) {
     pl.tc = true;
     pl.bytes = wenc_host::chunk_tc_workspace(sms);
     most = kFew;
@@ -297,9 +303,7 @@ Plan make_plan(const wenc_chunk_attention_args* a, int sms) {
   const long long items = (search ? dense : a->n_seqs * each) * a->n_kv_heads;
   // CTAs within two rounds of the machine (lengths differ, and a round that is full waits for its longest), none without steps
   // for its warps
-  const long long cap = static_cast<long long>(a->max_pages) * a->page_size;
-  const long long seen = a->window > 0 ? static_cast<long long>(a->window) + a->sinks + a->max_new : cap;
-  const long long kt = f32 ? 64 : 128, key_tiles = ((seen < cap ? seen : cap) + kt - 1) / kt;
+  const long long kt = f32 ? 64 : 128, key_tiles = (seen + kt - 1) / kt;
   const long long round = (f32 || pl.nr == 1 ? 3ll : pl.nr == 2 ? 2ll : 1ll) * sms;
   pl.rows.cluster = 1;
   while (pl.rows.cluster < 8 && pl.rows.cluster < key_tiles && items * pl.rows.cluster <= round) pl.rows.cluster *= 2;
