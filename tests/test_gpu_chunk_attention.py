@@ -243,6 +243,42 @@ def test_equal_chunks_without_offsets(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m", [1, 4, 70])
+def test_a_loose_bound_without_offsets(dtype, m):
+    """Sequences of equal chunks, for which the call allows far more tokens than they bring: every row is written."""
+    import torch
+    c = Case(dtype, [m] * 40, _ints(m, 40, 0, 300), 8, 4, seed=m, wide=True)
+    for start in (None, c.tstart):
+        out = torch.full(c.q.shape, float("nan"), device="cuda", dtype=c.dt)
+        c.check(c.run(seq_start=start, max_new=40 * m, out=out))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_call_that_allows_chunks_and_gets_none(dtype):
+    """Room for long chunks: single tokens alone, then padding alone (rows behind the last sequence stay as they are)."""
+    import torch
+    c = Case(dtype, [1] * 9 + [0], _ints(1, 10, 0, 400), 20, 4, pad=600, seed=15, wide=True)
+    out = torch.full(c.q.shape, 7.0, device="cuda", dtype=c.dt)
+    c.check(c.run(max_new=600, out=out))
+    assert (out[9:] == 7).all()
+    c = Case(dtype, [0] * 3, [5, 0, 90], 20, 4, pad=600, seed=16, wide=True)
+    out = torch.full(c.q.shape, 7.0, device="cuda", dtype=c.dt)
+    c.run(max_new=600, out=out)
+    assert (out == 7).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_chunks_that_lie_in_front_of_the_cache(dtype):
+    """Whole runs of tokens at negative positions, a sequence of length 0 among them: rows of zeros."""
+    import torch
+    c = Case(dtype, [600, 300], [0, 0], 4, 2, seed=17, wide=True)
+    c.tlens.copy_(torch.tensor([30, 0], dtype=torch.int32))
+    out = c.run(out=torch.full(c.q.shape, 7.0, device="cuda", dtype=c.dt))
+    assert (out[:570] == 0).all() and (out[600:] == 0).all()
+    assert torch.isfinite(out).all() and (out[570:600] != 7).any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("wide", [False, True])
 def test_a_bound_on_the_tokens_does_not_change_them(dtype, wide):
     """What a sequence brings decides its results' exactness, not how many the call allows."""

@@ -285,9 +285,11 @@ Plan make_plan(const wenc_chunk_attention_args* a, int sms) {
   Plan pl;
   const bool f32 = a->dtype == WENC_DTYPE_F32;
   const long long r = a->n_heads / a->n_kv_heads;
-  long long most = static_cast<long long>(a->max_new) * r;
+  // (without offsets every sequence's tokens are known, whatever bound was given)
+  const int max_new = a->seq_start ? a->max_new : a->n_tokens / a->n_seqs;
+  long long most = static_cast<long long>(max_new) * r;
   const long long cap = static_cast<long long>(a->max_pages) * a->page_size;
-  const long long in_window = a->window > 0 ? static_cast<long long>(a->window) + a->sinks + a->max_new : cap, seen = in_window < cap ? in_window : cap;
+  const long long in_window = a->window > 0 ? static_cast<long long>(a->window) + a->sinks + max_new : cap, seen = in_window < cap ? in_window : cap;
   if (!f32 && r <= 128 && a->scale > 0.0f && most > kLeastTc && static_cast<long long>(a->n_tokens) * a->n_heads > kLittle / seen) {
     pl.tc = true;
     pl.bytes = wenc_host::chunk_tc_workspace(sms);
@@ -461,7 +463,7 @@ extern "C" wenc_status wenc_chunk_attention(const wenc_chunk_attention_args* a, 
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (pl.tc) e = wenc_host::launch_chunk_tc(p, pl.rows.most, a->workspace, err, sms, s);
-  // (every sequence with more rows than that: nothing is left for the few)
+  // (without offsets every sequence has the rows that the plan counted, more than the few: nothing is left for them)
   if (e == cudaSuccess && !(pl.tc && !a->seq_start)) e = bf ? launch_all<__nv_bfloat16>(p, pl, err, s) : launch_all<float>(p, pl, err, s);
   if (e != cudaSuccess) {
     char buf[200];
