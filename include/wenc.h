@@ -431,7 +431,8 @@ typedef struct {
                                 h / (n_heads / n_kv_heads) */
   int head_dim;              /* must be 64 */
   const void* q;             /* [n_tokens][n_heads][64], tokens q_stride apart */
-  void* out;                 /* the same, tokens out_stride apart; apart from every input */
+  void* out;                 /* the same, tokens out_stride apart; shares no byte with an input (rows of q and
+                                out may lie side by side within one stride) */
   int64_t q_stride, out_stride;
   const void* k_pages;       /* [n_pages][page_size][n_kv_heads][64], as written by wenc_kv_append */
   const void* v_pages;
@@ -445,7 +446,7 @@ typedef struct {
                                 seq_start[s+1]-1; NULL: n_tokens / n_seqs rows each */
   int window;                /* how many newest keys a token sees, its own among them; 0: all */
   int sinks;                 /* with a window: how many first keys stay visible as well */
-  float scale;               /* of the scores; 0.125 = 64^-0.5 in Whisper */
+  float scale;               /* of the scores, below 2^127; 0.125 = 64^-0.5 in Whisper */
   void* workspace;           /* wenc_chunk_attention_workspace(args) bytes, 256-byte aligned */
   size_t workspace_bytes;
 } wenc_chunk_attention_args;
@@ -461,12 +462,12 @@ typedef struct {
  * exactly the rows that see it. A length, offset or page number out of range records
  * WENC_ERR_INVALID_ARG in the device error word (wenc_sync_status(NULL)); nothing out of range is accessed and the output
  * rows it concerns are undefined. The workspace belongs to the call until its work is done: calls that may
- * overlap need one each. At most four launches, no allocation, stream-ordered; a stalled device wait is recorded as
+ * overlap need one each. At most three launches, no allocation, stream-ordered; a stalled device wait is recorded as
  * for wenc_attention. */
 WENC_API wenc_status wenc_chunk_attention(const wenc_chunk_attention_args* args, wenc_stream_t stream);
 
 /* wenc_chunk_attention_workspace -- bytes of workspace the call needs on the current device (0 for
- * arguments it would refuse). Depends on the sizes, not on device data. */
+ * arguments it would refuse). Depends on the sizes, the scale's sign and whether seq_start is there, not on device data. */
 WENC_API size_t wenc_chunk_attention_workspace(const wenc_chunk_attention_args* args);
 
 /* Arguments of wenc_kv_extend: device pointers owned by the caller. */
@@ -481,7 +482,7 @@ typedef struct {
   const int32_t* free_pages; /* [n_free_pages] the first *free_count are free; they are taken from the end */
   int n_free_pages;
   const int32_t* free_count; /* [1] */
-  int32_t* lens_out;         /* [n_seqs] lengths with the new tokens; this and the next two apart from every input */
+  int32_t* lens_out;         /* [n_seqs] lengths with the new tokens; the outputs lie apart from every input */
   int32_t* free_count_out;   /* [1] pages that stay free */
   int32_t* seq_start;        /* [n_seqs + 1] row offsets, as wenc_kv_append and wenc_chunk_attention take them */
   int32_t* positions;        /* [n_rows] each row's position, 0 for padding; 16-byte aligned */
@@ -531,7 +532,8 @@ WENC_API wenc_status wenc_kv_release(const wenc_kv_release_args* args, wenc_stre
  *   out = epilogue(sum_g w_scale[n][g] sum_{k in g} (u[n][k] - 8) x[m][k] + bias[n]).
  * x [M, K] in x_dtype (wenc_dtype); w [N, K / 2]: byte k / 2 of a row holds u[n][k], 0..15, for even k in its low half and for the
  * odd k + 1 in its high half; w_scale [N, K / group] in scale_dtype (wenc_dtype); bias [N] float32. Epilogues as
- * wenc_epilogue: the first two write x's type, the third adds resid [M, N] float32 and writes float32 (out may be resid).
+ * wenc_epilogue: the first two write x's type, the third adds resid [M, N] float32 and writes float32 (out may be resid, and
+ * shares no byte with the other inputs).
  * group 32, 64 or 128; N a multiple of 128, K of 128, 1 <= M <= 2^28; buffers 16-byte aligned. bf16
  * products are exact, float32 x enters as three bf16 parts (exact together); sums are fp32, a group's before its scale.
  * workspace: wenc_linear_i4_workspace(...) bytes, 256-byte aligned (may be NULL when that is 0); it belongs to the call until its

@@ -47,6 +47,30 @@ def test_chunk_attention_refuses(L, kw, status, word):
     assert word in L.wenc_last_error(), L.wenc_last_error()
 
 
+@pytest.mark.parametrize("kw,status,word", [
+    (dict(scale=3e38), 1, b"scale"), (dict(scale=-2.4e38), 1, b"scale"),
+    # out within q's rows: a head further on, before it, rows at another stride, the last row alone
+    (dict(out=256 + 128), 1, b"apart"), (dict(q=256 + 128), 1, b"apart"), (dict(out=256 + 1024 * 3, out_stride=1024), 1, b"apart"),
+    (dict(out=256 + 1024 * 11), 1, b"apart"), (dict(q_stride=1024, out_stride=1024, out=256 + 1008), 1, b"apart"),
+])
+def test_chunk_attention_refuses_what_overlaps(L, kw, status, word):
+    assert L.wenc_chunk_attention(ctypes.byref(_chunk(**kw)), None) == status
+    assert word in L.wenc_last_error(), L.wenc_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=256 + 1024 * 12), dict(q=256 + 1024 * 12), dict(q_stride=1024, out_stride=1024, out=256 + 1024),
+    dict(q_stride=1792, out_stride=1792, out=256 + 2048),
+])
+def test_chunk_attention_takes_rows_side_by_side(L, kw):
+    """(Without a GPU the call ends at the device, behind every check of its arguments; a workspace is refused before it.)"""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    L.wenc_chunk_attention(ctypes.byref(_chunk(**kw)), None)
+    assert b"apart" not in L.wenc_last_error(), L.wenc_last_error()
+
+
 def test_chunk_attention_without_tokens(L):
     assert L.wenc_chunk_attention(None, None) == 1
     assert L.wenc_chunk_attention_workspace(None) == 0
@@ -76,6 +100,13 @@ def test_kv_extend_refuses(L, kw, status, word):
     assert word in L.wenc_last_error(), L.wenc_last_error()
 
 
+@pytest.mark.parametrize("kw", [dict(positions=512), dict(slots=496), dict(lens_out=2048 + 44), dict(positions=1024 + 32),
+                                dict(free_count_out=2048), dict(seq_start=1024)])
+def test_kv_extend_refuses_outputs_over_pages_and_tables(L, kw):
+    assert L.wenc_kv_extend(ctypes.byref(_extend(**kw)), None) == 1
+    assert b"apart" in L.wenc_last_error(), L.wenc_last_error()
+
+
 def _release(**kw):
     from transformer_encoder_gb300.wenc import KvReleaseArgs
     return _set(KvReleaseArgs(n_seqs=3, lens=512, finished=256, block_table=1024, block_table_stride=4, max_pages=4, page_size=16,
@@ -97,6 +128,13 @@ def test_kv_release_refuses(L, kw, status, word):
     assert word in L.wenc_last_error(), L.wenc_last_error()
 
 
+@pytest.mark.parametrize("kw", [dict(lens_out=256), dict(free_pages=1024), dict(free_pages=480), dict(trimmed_out=1064),
+                                dict(free_count_out=256)])
+def test_kv_release_refuses_outputs_over_marks_and_tables(L, kw):
+    assert L.wenc_kv_release(ctypes.byref(_release(**kw)), None) == 1
+    assert b"apart" in L.wenc_last_error(), L.wenc_last_error()
+
+
 def _i4(L, **kw):
     d = dict(x=256, x_dtype=1, w=256, w_scale=256, scale_dtype=1, bias=256, resid=None, out=256, M=4, N=256, K=256, group=64,
              epilogue=0, workspace=None, workspace_bytes=0, stream=None)
@@ -114,6 +152,13 @@ def _i4(L, **kw):
 def test_linear_i4_refuses(L, kw, status, word):
     assert _i4(L, **kw) == status
     assert word in L.wenc_last_error(), L.wenc_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(out=256 + 2032), dict(x=256 + 2032), dict(epilogue=2, resid=65536, x=256 + 4080),
+                                dict(x_dtype=0, out=256 + 4080)])
+def test_linear_i4_refuses_an_output_over_its_input(L, kw):
+    assert _i4(L, **kw) == 1
+    assert b"apart" in L.wenc_last_error(), L.wenc_last_error()
 
 
 def test_the_binding_packs_the_structures_as_declared():

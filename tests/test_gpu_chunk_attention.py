@@ -497,3 +497,29 @@ def test_what_the_binding_refuses():
         with pytest.raises(Exception):
             chunk_attention(*args, **{"seq_start": c.tstart, **kw})
     assert chunk_attention(c.q[:0], *args[1:], seq_start=torch.zeros(3, dtype=torch.int32, device="cuda")).shape == (0, 4, 64)
+
+
+def test_tokens_of_no_sequence_are_refused():
+    import torch
+    from transformer_encoder_gb300 import chunk_attention
+    c = Case("bf16", [1, 2], [10, 20], 4, 2)
+    none = dict(block_table=c.table[:0], lens=c.tlens[:0])
+    with pytest.raises(ValueError, match="no sequence"):
+        chunk_attention(c.q, c.kc, c.vc, **none)
+    start = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert (chunk_attention(c.q, c.kc, c.vc, **none, seq_start=start) == 0).all()  # (all of it padding)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_queries_and_results_side_by_side(dtype):
+    """Results into other columns of the rows that the queries come from; into the queries' own they are refused."""
+    import torch
+    c = Case(dtype, [1, 90, 4], [200, 30, 9], 4, 2, seed=18, wide=True)
+    rows = torch.full((c.q.shape[0], 12, 64), 3.0, device="cuda", dtype=c.dt)
+    rows[:, 1:5] = c.q
+    want = c.run()
+    c.q = rows[:, 1:5]
+    assert torch.equal(c.run(out=rows[:, 6:10]), want)
+    assert (rows[:, 0] == 3).all() and (rows[:, 5] == 3).all() and (rows[:, 10:] == 3).all()
+    with pytest.raises(Exception, match="apart"):
+        c.run(out=rows[:, 4:8])

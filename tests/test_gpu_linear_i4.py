@@ -160,3 +160,24 @@ def test_what_the_binding_refuses():
         with pytest.raises(Exception):
             linear_i4(*a, **kw)
     assert linear_i4(c.x[:0], *a[1:]).shape == (0, 256)
+
+
+@pytest.mark.parametrize("x,M,N", [("bf16", (1 << 21) + 77, 1152), ("f32", (1 << 20) + 5, 2304)])
+def test_offsets_past_32_bits(x, M, N):
+    """More than 2^31 results. Whole numbers of which every sum is exact, so any division of the rows gives the same bits."""
+    import torch
+    from transformer_encoder_gb300 import linear_i4, sync_status
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+    assert M * N > 1 << 31
+    a = torch.randint(-3, 4, (M, 128), generator=g, device="cuda").to(torch.bfloat16 if x == "bf16" else torch.float32)
+    w = torch.randint(0, 256, (N, 64), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.full((N, 2), 0.125, device="cuda")
+    b = torch.zeros(N, device="cuda")
+    out = linear_i4(a, w, s, b)
+    for lo in (0, M // 2 - 40, M - 300):
+        assert torch.equal(out[lo:lo + 300], linear_i4(a[lo:lo + 300], w, s, b))
+    u = torch.stack([w & 15, w >> 4], 2).view(N, 128).double() - 8
+    want = (a[-8:].double() @ u.t() * 0.125).to(out.dtype)
+    assert torch.equal(out[-8:], want)
+    sync_status()

@@ -313,6 +313,17 @@ Plan make_plan(const wenc_chunk_attention_args* a, int sms) {
   return pl;
 }
 
+// Whether n rows of `row` bytes at x and at y share none: apart as wholes, or, at one stride, side by side within it.
+bool apart(const void* x, long long x_stride, const void* y, long long y_stride, long long row, long long n) {
+  const long long a = static_cast<long long>(reinterpret_cast<uintptr_t>(x)), b = static_cast<long long>(reinterpret_cast<uintptr_t>(y));
+  if (a + (n - 1) * x_stride + row <= b || b + (n - 1) * y_stride + row <= a) return true;
+  if (x_stride != y_stride) return false;
+  const long long d = ((b - a) % x_stride + x_stride) % x_stride;
+  return d >= row && x_stride - d >= row;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
 bool check_sizes(const wenc_chunk_attention_args* a, wenc_status* st) {
   auto no = [&](wenc_status s) {
     *st = s;
@@ -341,7 +352,8 @@ bool check_sizes(const wenc_chunk_attention_args* a, wenc_status* st) {
     return no(bad(WENC_ERR_UNSUPPORTED, "chunk_attention: max_pages %lld x page_size %lld passes 2^30", a->max_pages, a->page_size));
   if ((static_cast<long long>(a->n_tokens) + a->n_seqs) * a->n_heads > 0x3fffffffll)
     return no(bad(WENC_ERR_UNSUPPORTED, "chunk_attention: %lld tokens of %lld heads are too many rows", a->n_tokens, a->n_heads));
-  if (!(a->scale - a->scale == 0.0f)) return no(bad(WENC_ERR_INVALID_ARG, "chunk_attention: scale must be finite"));
+  const float log2_scale = a->scale * kLog2e;
+  if (!(log2_scale - log2_scale == 0.0f)) return no(bad(WENC_ERR_INVALID_ARG, "chunk_attention: scale must be below 2^127 (and finite)"));
   return true;
 }
 
@@ -412,7 +424,8 @@ extern "C" wenc_status wenc_chunk_attention(const wenc_chunk_attention_args* a, 
   for (long long x : strides)
     if (x % per16 != 0) return bad(WENC_ERR_INVALID_ARG, "strides must be multiples of 16 bytes");
   if (a->n_tokens == 0) return WENC_OK;
-  if (a->q == a->out) return bad(WENC_ERR_INVALID_ARG, "chunk_attention: out must lie apart from q");
+  if (!apart(a->q, a->q_stride * es, a->out, a->out_stride * es, q_row * es, a->n_tokens))
+    return bad(WENC_ERR_INVALID_ARG, "chunk_attention: out must lie apart from q");
   int sms = 0;
   uint32_t* err = nullptr;
   const wenc_status dst = wenc_internal_device(&sms, &err);
@@ -459,7 +472,7 @@ extern "C" wenc_status wenc_chunk_attention(const wenc_chunk_attention_args* a, 
   const bool bf = a->dtype == WENC_DTYPE_BF16;
   p.q_flip = a->scale < 0.0f ? (bf ? 0x80008000u : 0x80000000u) : 0u;
   p.q_keep = a->scale == 0.0f ? 0u : 0xffffffffu;
-  p.scale_log2 = (a->scale == 0.0f ? 1.0f : a->scale < 0.0f ? -a->scale : a->scale) * 1.4426950408889634f;
+  p.scale_log2 = (a->scale == 0.0f ? 1.0f : a->scale < 0.0f ? -a->scale : a->scale) * kLog2e;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (pl.tc) e = wenc_host::launch_chunk_tc(p, pl.rows.most, a->workspace, err, sms, s);

@@ -732,6 +732,11 @@ extern "C" wenc_status wenc_linear_i4(const void* x, int x_dtype, const uint8_t*
   if (group != 32 && group != 64 && group != 128) return bad(WENC_ERR_UNSUPPORTED, "group %lld: 32, 64 or 128", group);
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(w_scale, 16) || !aligned(bias, 16) || !aligned(resid, 16) || !aligned(out, 16))
     return bad(WENC_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
+  // (tiles of x are read while others' results are written)
+  const uintptr_t xa = reinterpret_cast<uintptr_t>(x), oa = reinterpret_cast<uintptr_t>(out);
+  const size_t x_bytes = static_cast<size_t>(M) * K * (x_dtype == WENC_DTYPE_F32 ? 4 : 2);
+  const size_t out_bytes = static_cast<size_t>(M) * N * (x_dtype == WENC_DTYPE_F32 || epilogue == WENC_EPI_BIAS_RESID_F32 ? 4 : 2);
+  if (xa < oa + out_bytes && oa < xa + x_bytes) return bad(WENC_ERR_INVALID_ARG, "linear_i4: out must lie apart from x");
   int sms = 0;
   uint32_t* err = nullptr;
   const wenc_status dst = wenc_internal_device(&sms, &err);

@@ -367,19 +367,22 @@ wenc_status bad(wenc_status s, const char* fmt, long long a = 0, long long b = 0
   return wenc_internal_fail(s, buf);
 }
 
-struct Range {  // of 32-bit numbers
+struct Range {
   const void* at;
-  long long n;
+  long long bytes;
 };
 // Whether an input shares bytes with an output.
-bool share(const Range (&in)[3], const Range (&out)[3]) {
+template <int IN, int OUT>
+bool share(const Range (&in)[IN], const Range (&out)[OUT]) {
   for (const Range& i : in)
     for (const Range& o : out) {
       const uintptr_t x = reinterpret_cast<uintptr_t>(i.at), y = reinterpret_cast<uintptr_t>(o.at);
-      if (x && y && x < y + 4 * o.n && y < x + 4 * i.n) return true;
+      if (i.bytes > 0 && o.bytes > 0 && x && y && x < y + o.bytes && y < x + i.bytes) return true;
     }
   return false;
 }
+// What a block table takes, from its first row's begin to its last one's end.
+long long table_bytes(int n_seqs, long long stride, int max_pages) { return n_seqs > 0 ? ((n_seqs - 1) * stride + max_pages) * 4 : 0; }
 
 wenc_status launch_failed(const char* what, cudaError_t e) {
   char buf[200];
@@ -407,9 +410,11 @@ extern "C" wenc_status wenc_kv_extend(const wenc_kv_extend_args* a, wenc_stream_
   if ((reinterpret_cast<uintptr_t>(a->positions) | reinterpret_cast<uintptr_t>(a->slots)) & 15u)
     return bad(WENC_ERR_INVALID_ARG, "kv_extend: positions and slots must be 16-byte aligned");
   // (blocks read the inputs while others write)
-  const Range in[] = {{a->new_tokens, a->n_seqs}, {a->lens, a->n_seqs}, {a->free_count, 1}};
-  const Range out[] = {{a->lens_out, a->n_seqs}, {a->free_count_out, 1}, {a->seq_start, a->n_seqs + 1}};
-  if (share(in, out)) return bad(WENC_ERR_INVALID_ARG, "kv_extend: lens_out, free_count_out and seq_start must lie apart from the inputs");
+  const long long seqs = 4ll * a->n_seqs, rows = a->n_rows;
+  const Range in[] = {{a->new_tokens, seqs}, {a->lens, seqs}, {a->free_count, 4}, {a->free_pages, 4ll * a->n_free_pages},
+                      {a->block_table, table_bytes(a->n_seqs, a->block_table_stride, a->max_pages)}};
+  const Range out[] = {{a->lens_out, seqs}, {a->free_count_out, 4}, {a->seq_start, seqs + 4}, {a->positions, 4 * rows}, {a->slots, 8 * rows}};
+  if (share(in, out)) return bad(WENC_ERR_INVALID_ARG, "kv_extend: the outputs must lie apart from the inputs");
   int sms = 0;
   uint32_t* err = nullptr;
   const wenc_status dst = wenc_internal_device(&sms, &err);
@@ -461,9 +466,11 @@ extern "C" wenc_status wenc_kv_release(const wenc_kv_release_args* a, wenc_strea
     return bad(WENC_ERR_UNSUPPORTED, "kv_release: max_pages %lld x page_size %lld passes 2^31 - 1", a->max_pages, a->page_size);
   if (a->n_seqs > 1 && a->block_table_stride < a->max_pages)
     return bad(WENC_ERR_INVALID_ARG, "kv_release: block_table_stride %lld < max_pages %lld", a->block_table_stride, a->max_pages);
-  const Range in[] = {{a->lens, a->n_seqs}, {a->trimmed, a->n_seqs}, {a->free_count, 1}};
-  const Range out[] = {{a->lens_out, a->n_seqs}, {a->trimmed_out, a->n_seqs}, {a->free_count_out, 1}};
-  if (share(in, out)) return bad(WENC_ERR_INVALID_ARG, "kv_release: lens_out, trimmed_out and free_count_out must lie apart from the inputs");
+  const long long seqs = 4ll * a->n_seqs;
+  const Range in[] = {{a->lens, seqs}, {a->trimmed, seqs}, {a->free_count, 4}, {a->finished, a->n_seqs},
+                      {a->block_table, table_bytes(a->n_seqs, a->block_table_stride, a->max_pages)}};
+  const Range out[] = {{a->lens_out, seqs}, {a->trimmed_out, seqs}, {a->free_count_out, 4}, {a->free_pages, 4ll * a->n_free_pages}};
+  if (share(in, out)) return bad(WENC_ERR_INVALID_ARG, "kv_release: the outputs and free_pages must lie apart from the inputs");
   int sms = 0;
   uint32_t* err = nullptr;
   const wenc_status dst = wenc_internal_device(&sms, &err);

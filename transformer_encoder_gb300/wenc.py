@@ -990,6 +990,8 @@ def chunk_attention(q, k_pages, v_pages, block_table, lens, *, seq_start=None, m
         if out.get_device() != dev:
             raise _elsewhere((("out", out),))
     if n == 0 or n_seqs == 0:
+        if n and not start:
+            raise ValueError(f"{n} tokens of no sequence")
         return out
     if max_new is None:
         max_new = n if start else -(-n // n_seqs)
