@@ -16,13 +16,14 @@
 //    shared memory for P, and the next scores are there before this step's P has been used;
 //  - a row's reference is the maximum of its first step, moved only when weights pass 2^20, so no step forms a maximum; it is a
 //    whole number (of log2), so moving it is exact.
-// What bounds it: the two softmax warps of a scheduler (2000 instructions a step of 256 x 128, at 56% of the issue slots: what they
-// wait for are TMEM loads and each other's results, and more warps find no registers). 2048 tokens of 20 heads over 4 behind 14000 keys
-// take 245 us, 640 TFLOP/s of the two products, 960 with the second part of P, a step some 3200 cycles; single products of its
-// MMAs alone would take 1650. On the way there (us): first form 567 (every role walked, loops unrolled: warps waited for
-// instructions), 442 walked by one warp, 313 with rolled loops, 270 with the pages looked up a step ahead and three score
-// buffers, 257 with P in TMEM alone, 245 with tiles handed over by their copies' own arrival. Not kept: taking turns on the exponentials,
-// unrolled exponentials (331), the next 32 scores loaded ahead (256), four gathering warps (252).
+// What bounds it: the two softmax warps of a scheduler (all warps together issue 1970 instructions a scheduler and step of 256 x 128, in 58%
+// of the cycles; what they wait for are TMEM loads and results of their own, and more warps find no registers). The tensor pipe is
+// busy for 47%. 2048 tokens of 20 heads over 4 behind 14000 keys take 228 us, 687 TFLOP/s of the two products, a
+// step some 3400 cycles; its MMAs alone, in straight lines, would take 1650, its exponentials (16 an SM and cycle) 2048. On the way there (us): first form 567
+// (every role walked, loops unrolled: warps waited for instructions), 442 walked by one warp, 313 with rolled loops, 270 with
+// the pages looked up a step ahead and three score buffers, 257 with P in TMEM alone, 245 with tiles handed over by their
+// copies' own arrival and P's barriers in pairs, 228 with a piece's queries addressed without divisions. Not kept: taking turns on the
+// exponentials, unrolled exponentials (331), the next 32 scores loaded ahead (256 against 245), four gathering warps (252).
 #include <cuda_bf16.h>
 #include <math_constants.h>
 

@@ -6,6 +6,10 @@
 // u - 8 is exact in bf16, a bf16 x times it is exact in fp32, so a group's product runs on the bf16 tensor cores without a
 // rounding of either operand, and the scale, which would not fit into the weight exactly, multiplies the group's fp32 sum. float32 x is
 // cut into three bf16 parts (8 + 8 + 8 significant bits: exact together), the products of which share a group's sum.
+//
+// Two forms, on the device in us: up to 16 tokens on mma.sync, where a token costs little beside the weights' bytes and latency
+// (tokens x N x K: 1 x 1152 x 384 3.7, 16 x 5120 x 1280 6.3, 1 x 7680 x 5120 14.4), more on tcgen05 (24 x 5120 x 1280 8.0, 80 x 5120 x
+// 1280 11.4, 2240 x 1280 x 5120 33.4, 880 TFLOP/s; float32 300 x 1280 x 1280 15).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -236,7 +240,10 @@ __global__ void __launch_bounds__(32 * kRowsWarps) i4_rows_kernel(const __grid_c
 // operand. x comes by TMA as it lies (float32: its three parts, cut apart by i4_split_kernel first). A group's products make an
 // accumulator of their own, one of two in TMEM; eight warps, a channel a thread again, add it times the group's scale to
 // their sums in registers while the MMAs fill the other. So a scale is one number a thread and group, and no weight is rounded.
-// What bounds it: the MMAs (80 cycles for each 16 inputs of 160 tokens), and with groups of 32 the reading of accumulators.
+// What bounds it: the MMAs (80 cycles for each 16 inputs of 160 tokens; busy 41% of the cycles at 2240 x 1280 x 5120, whose 140 CTAs begin and end
+// together), and with groups of 32 the reading of accumulators. At 80 x 5120 x 1280 the latency of 10 pieces in a row. Not kept:
+// four pieces unrolled in the issuers (41.6 us against 35 for the large one: code past the instruction cache), four accumulators of 80
+// tokens (no gain), the output unrolled (12.5 us against 11.4 for the small one).
 constexpr int kTcMost = 160;                // tokens of a tile
 constexpr int kTcThreads = 512;             // 4 widening warps, 2 MMA issuers, TMA producer, a warp for the scales, 8 summing warps
 constexpr int kAStages = 2, kXStages = 4;   // of 128 inputs
@@ -637,7 +644,8 @@ size_t split_bytes(int M, int K, int x_dtype) {
 }
 
 // Tokens of a tile and CTAs that share K: the division whose rounds of the machine take least, in cycles of a piece of 128
-// inputs (the MMAs' 4 a token, but no less than widening and, of every group, summing take) and of a CTA's beginning and end.
+// inputs (the MMAs' 4 a token, but no less than widening and, of every group, summing take) and of a CTA's beginning and end. The
+// constants are fitted to measured times. Where K is shared, an end adds the joining: 80 x 5120 x 1280 with four CTAs to a K takes 25 us, alone 11.4.
 constexpr long long kWidenCycles = 600, kSumCycles = 350, kEndCycles = 5000, kJoinCycles = 1500;
 void pick_tiles(int M, int n_tiles, int K, int group, int parts, int sms, int& tok, int& ksplit) {
   const int least = (M + kTcMost - 1) / kTcMost, pieces = K / kPiece;
