@@ -23,7 +23,8 @@
 // (every role walked, loops unrolled: warps waited for instructions), 442 walked by one warp, 313 with rolled loops, 270 with
 // the pages looked up a step ahead and three score buffers, 257 with P in TMEM alone, 245 with tiles handed over by their
 // copies' own arrival and P's barriers in pairs, 228 with a piece's queries addressed without divisions. Not kept: taking turns on the
-// exponentials, unrolled exponentials (331), the next 32 scores loaded ahead (256 against 245), four gathering warps (252).
+// exponentials, unrolled exponentials (331), the next 32 scores loaded ahead (256 against 245), four gathering warps (252); a
+// polynomial on the FMA pipe for one pair of exponentials in 8, 4 or 2 (238, 249, 293 against 230): it is instructions that count.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
