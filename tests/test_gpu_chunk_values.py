@@ -1,0 +1,53 @@
+"""Chunk attention where values that are no numbers meet rows that see no key.
+
+Bounds: rows that do not see a bad value are formed from the same keys a second way at most. Each result lies within the
+bound of test_gpu_chunk_attention.py of one value: 2^-8 of it for bf16's rounding and, for some hundred keys and weighted
+magnitudes below 4, less than 2^-13 times these (float32: 2^-16). Two results differ by twice that.
+"""
+import pytest
+
+from test_gpu_chunk_attention import Case
+
+pytestmark = pytest.mark.gpu
+
+# [dtype, new tokens, heads, key heads, wide]: tiles of 8, 16 and 32 rows on mma.sync, of one CTA and of clusters, and the tensor
+# cores' form with units that are whole within a CTA's run and units that are cut
+FORMS = [(dtype, new, H, kv, wide) for dtype in ("bf16", "f32") for new, H, kv in (([4, 8], 4, 4), ([8, 3], 4, 2), ([30, 9], 4, 4))
+         for wide in (False, True)] + [("bf16", [256, 300], 40, 40, True), ("bf16", [600, 70], 20, 4, True)]
+
+
+def near(got, clean, dtype):
+    far = clean.float()
+    slack = 2.0 ** -7 * far.abs() + 4 * 2.0 ** -12 if dtype == "bf16" else 4 * 2.0 ** -15
+    return bool(((got.float() - far).abs() <= slack).all())
+
+
+@pytest.mark.parametrize("dtype,new,H,kv,wide", FORMS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("what", ["v", "k"])
+def test_rows_without_a_key_beside_rows_that_see_no_number(dtype, new, H, kv, wide, bad, what):
+    """Tokens in front of the cache give zeros, whatever the other rows of their tile see."""
+    import torch
+    lens = [max(1, (5 * m) // 8) for m in new]
+    c = Case(dtype, new, [0] * len(new), H, kv, seed=sum(new), wide=wide)
+    c.tlens.copy_(torch.tensor(lens, dtype=torch.int32))
+    clean = c.run()
+    for s, n in enumerate(lens):
+        for key in sorted({0, n // 2, n - 1}):
+            d = Case(dtype, new, [0] * len(new), H, kv, seed=sum(new), wide=wide)
+            d.tlens.copy_(c.tlens)
+            (d.vc if what == "v" else d.kc)[int(d.table[s, key // 16]), key % 16, :, 9] = bad
+            got = d.run()
+            for x, (m, v) in enumerate(zip(new, lens)):
+                rows, pos = got[int(c.start[x]):int(c.start[x + 1])], torch.arange(v - m, v, device="cuda")
+                assert (rows[pos < 0] == 0).all(), (s, key, x)
+                sees = pos >= key if x == s else torch.zeros_like(pos, dtype=torch.bool)
+                base = clean[int(c.start[x]):int(c.start[x + 1])]
+                assert near(rows[~sees], base[~sees], dtype), (s, key, x)
+                if what == "v":
+                    hit = rows[sees][..., 9]
+                    assert (torch.isnan(hit) if bad != bad else hit == bad).all(), (s, key, x)
+                    rest = [e for e in range(64) if e != 9]
+                    assert near(rows[sees][..., rest], base[sees][..., rest], dtype), (s, key, x)
+                elif bad != bad:
+                    assert torch.isnan(rows[sees]).all(), (s, key, x)

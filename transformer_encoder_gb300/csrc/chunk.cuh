@@ -119,9 +119,10 @@ __device__ __noinline__ void chunk_redo(const ChunkParams& p, int seq, int hk, c
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = fmaf(w, vf[e], o[e]);
   });
-  // (the lane's other elements turn to the sum of these weights, so that none leaves the range on its way to the division)
+  // (the lane's other elements turn to the sum of these weights, so that none leaves the range on its way to the division; a row
+  // without weights, which a value that it does not see may have turned to NaN, is all formed here: zeros)
   bool bad[8], any = false;
-  const bool again = !(fabsf(*l_io) < CUDART_INF_F);
+  const bool again = !(fabsf(*l_io) < CUDART_INF_F) || *l_io == 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) any |= bad[e] = again || !(fabsf(v[e]) < CUDART_INF_F);
   if (!in || !any) return;
