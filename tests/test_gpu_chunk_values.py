@@ -1,4 +1,4 @@
-"""Chunk attention where values that are no numbers meet rows that see no key.
+"""Chunk attention where values that are no numbers meet rows that see no key, and long caches.
 
 Bounds: rows that do not see a bad value are formed from the same keys a second way at most. Each result lies within the
 bound of test_gpu_chunk_attention.py of one value: 2^-8 of it for bf16's rounding and, for some hundred keys and weighted
@@ -51,3 +51,31 @@ def test_rows_without_a_key_beside_rows_that_see_no_number(dtype, new, H, kv, wi
                     assert near(rows[sees][..., rest], base[sees][..., rest], dtype), (s, key, x)
                 elif bad != bad:
                     assert torch.isnan(rows[sees]).all(), (s, key, x)
+
+
+def test_no_wait_runs_out_while_rows_are_formed_again():
+    """A value that is no number in a cache of 60000 keys, seen by rows of two units that lie whole in a CTA's run, with more of the
+    run behind them: those rows take a second evaluation over all their keys, which no role of the kernel may wait for. The
+    error word stays clear (run() reads it), and rows that do not see the value keep theirs."""
+    import torch
+    m, n, H, window = 1000, 61000, 128, 59000  # one key head: units of two tokens, 463 steps each, some three units a CTA
+    case = dict(dtype="bf16", new=[m], past=[n - m], H=H, Hkv=1, window=window, sinks=0, page=64, seed=21)
+    c = Case(**case)
+    clean = c.run()
+    key = n - m - window + 3  # in the windows of the first three tokens alone
+    pos = torch.arange(n - m, n, device="cuda")
+    sees = (key <= pos) & (key > pos - window)
+    assert sees.nonzero().flatten().tolist() == [0, 1, 2]
+    c.vc[int(c.table[0, key // 64]), key % 64, 0, 9] = float("nan")
+    got = c.run()
+    # (units of which no row sees the value: the same bits)
+    assert torch.equal(got[4:], clean[4:])
+    assert torch.isnan(got[:3, :, 9]).all()
+    # Elsewhere both results lie within the bound of test_gpu_chunk_attention.py of one value: its d with A < 64 (|q . k| sums
+    # of 64 products of unit normals), 59000 keys, weighted magnitudes below 1; and as there 2^-8 each over all elements.
+    e = 1.1 * 64 * 64 * 2.0 ** -23 + 2.0 ** -16 + 2.0 ** -21
+    seen = torch.ones_like(got[:4], dtype=torch.bool)
+    seen[:3, :, 9] = False
+    far, err = clean[:4][seen].double(), (got[:4][seen].double() - clean[:4][seen].double())
+    assert (err.abs() <= 2.0 ** -7 * far.abs() + 2 * (2 * e + 2.0 ** -16 + 2 * window * 2.0 ** -23)).all()
+    assert float(err.norm()) <= 2.0 ** -7 * float(far.norm())

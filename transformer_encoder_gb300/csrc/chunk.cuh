@@ -77,7 +77,7 @@ __device__ __forceinline__ bool chunk_slot(const ChunkParams& p, int seq, int ke
 // 0 x inf and 0 x NaN are NaN, so a value that is no number would reach rows that do not see it, and weighted sums of values
 // near the largest float may leave the range. Elements of a row's O that are no numbers, and all of a row whose sum is none
 // (rare: they are found by that), are formed again here, in plain fp32 from the keys alone that the row sees, with weights of at
-// most 1. Eight lanes hold a row: token position pos, elements c8 .. c8 + 7 in v and sum l; all lanes of a warp call, in: the
+// most 1. That goes through all keys twice, so nothing whose waits have a limit may wait for it. Eight lanes hold a row: token position pos, elements c8 .. c8 + 7 in v and sum l; all lanes of a warp call, in: the
 // lane's row is one of the call's. lo, hi, first: keys [lo, hi) and [0, first) hold all that the warp's rows see.
 template <typename T>
 __device__ __noinline__ void chunk_redo(const ChunkParams& p, int seq, int hk, const uint8_t* q_row, int pos, bool in, int lo, int hi,
@@ -164,11 +164,21 @@ namespace wenc_host {
 struct ChunkCut {
   int seq, hk, x, pieces;
 };
+// A CTA's run of steps: where it begins and how many it holds (as chunk_tc.cu's Walk has them), and whether rows of units that are
+// whole within it have to be formed again (they carry kChunkMark).
+struct ChunkRun {
+  int redo;
+  int hk, seq, x, skip, m, len, row0;
+  long long left, at;
+};
+// In an output row's first elements: two bf16 numbers that no rounding gives (a NaN comes out as 0x7fff).
+constexpr uint32_t kChunkMark = 0xffffffffu;
 struct ChunkTcArgs {
   int few;             // rows per key head up to which a sequence is chunk_attn.cu's
   int tokens;          // of a row tile: 128 / r
   int per_unit;        // of a unit: two tiles'
   ChunkCut* cuts;      // [CTAs]
+  ChunkRun* runs;      // [CTAs]
   float* part_o;       // [CTAs][2][256][64]
   float2* part_ml;     // [CTAs][2][256]: (maximum in log2 units, sum)
 };

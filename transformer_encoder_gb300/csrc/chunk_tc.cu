@@ -15,7 +15,9 @@
 //  - three score buffers go round the two row tiles, and both parts of P lie in the 32 columns of the 32 scores they come from: no
 //    shared memory for P, and the next scores are there before this step's P has been used;
 //  - a row's reference is the maximum of its first step, moved only when weights pass 2^20, so no step forms a maximum; it is a
-//    whole number (of log2), so moving it is exact.
+//    whole number (of log2), so moving it is exact;
+//  - rows that come out as no numbers are formed again behind this kernel, by chunk_join_kernel: that takes as long as the cache is
+//    long, and the other roles' waits have a limit.
 // What bounds it: the two softmax warps of a scheduler (all warps together issue 1970 instructions a scheduler and step of 256 x 128, in 58%
 // of the cycles; what they wait for are TMEM loads and results of their own, and more warps find no registers). The tensor pipe is
 // busy for 47%. 2048 tokens of 20 heads over 4 behind 14000 keys take 228 us, 687 TFLOP/s of the two products, a
@@ -90,7 +92,9 @@ __device__ __forceinline__ float max32(const uint32_t (&r)[32]) {
 }
 
 using wenc_host::ChunkCut;
+using wenc_host::ChunkRun;
 using wenc_host::ChunkTcArgs;
+using wenc_host::kChunkMark;
 
 // Unit x of a sequence: its tokens i0 .. i1 (of the sequence's) and their keys.
 struct Unit {
@@ -123,6 +127,10 @@ struct Walk {
   Piece pc;                           // the piece in hand
   int hk, seq, x, row0, m, len, skip;  // where the run goes on: step `skip` (of n + kStart) of that unit
   long long left, at;                 // steps left, and the number of the unit's first step among all
+
+  Walk() = default;
+  __device__ __forceinline__ explicit Walk(const ChunkRun& r)
+      : hk(r.hk), seq(r.seq), x(r.x), row0(r.row0), m(r.m), len(r.len), skip(r.skip), left(r.left), at(r.at) {}
 
   // The next piece; false at the end of the run. All lanes of a warp call.
   __device__ __forceinline__ bool next(const ChunkParams& p, const ChunkTcArgs& a, uint32_t* err) {
@@ -177,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ ChunkTcArgs a, uint32_t* err) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ long long sums[kWarps];
-  __shared__ int start[6];
+  __shared__ ChunkRun start;  // of this CTA's run
   __shared__ Piece pieces[NP];
   __shared__ uint64_t places[2][BKV];
   __shared__ long long of_run[2];  // all steps, and the CTAs that share them
@@ -301,12 +309,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t past = __ballot_sync(0xffffffffu, t < at + sum);
           if (past) {
             if (lane == __ffs(past) - 1) {
-              start[0] = s;
-              start[1] = x0 + lane;
-              start[2] = static_cast<int>(t - (at + sum - w));
-              start[3] = m;
-              start[4] = len;
-              start[5] = p.seq_start ? p.seq_start[s] : s * p.per_seq;
+              const int skip = static_cast<int>(t - (at + sum - w));
+              start = ChunkRun{0, static_cast<int>(b0 / of_head), s, x0 + lane, skip, m, len,
+                               p.seq_start ? p.seq_start[s] : s * p.per_seq, b1 - b0, b0 - skip};
             }
             return true;
           }
@@ -319,11 +324,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   if (threadIdx.x == 0) {
+    if (!busy) start = ChunkRun{};
     a.cuts[blockIdx.x].pieces = 0;
+    a.runs[blockIdx.x] = start;
     of_run[0] = total;
     of_run[1] = ctas;
   }
-  __syncthreads();  // (the piece that is cut at the run's end writes the mark again)
+  __syncthreads();  // (a piece that is cut at the run's end writes into `cuts`, a whole one without numbers into `runs`)
 
   auto tS = [&](int buf) { return tmem_base + 128u * buf; };  // (and the P that follows)
   auto tO = [&](int t) { return tmem_base + 384u + 64u * t; };
@@ -352,17 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
       };
       Walk run;
-      if (is_k) {
-        run.left = busy ? b1 - b0 : 0;
-        run.hk = busy ? static_cast<int>(b0 / of_head) : 0;
-        run.seq = start[0];
-        run.x = start[1];
-        run.skip = start[2];
-        run.m = start[3];
-        run.len = start[4];
-        run.row0 = start[5];
-        run.at = b0 - start[2];
-      }
+      if (is_k) run = Walk(start);
       int kc = 0;  // tiles
       bool ok = true;
 #pragma unroll 1
@@ -712,18 +709,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           while (c < of_run[1] && of_run[0] * c / of_run[1] < pc.end) ++c;
           a.cuts[blockIdx.x] = ChunkCut{pc.seq, pc.hk, pc.x, static_cast<int>(c - blockIdx.x)};
         }
-      } else {
-        for (uint32_t some = __ballot_sync(0xffffffffu, put && !(zero == 0.0f)); some; some &= some - 1) {  // (rare: see chunk_redo)
-          const int who = __ffs(some) - 1;
-          const int w_token = __shfl_sync(0xffffffffu, token, who), w_head = __shfl_sync(0xffffffffu, head, who);
-          const int w_pos = pc.pos0 + __shfl_sync(0xffffffffu, i, who), c8 = (lane & 7) * 8;
-          float v[8], w_l = CUDART_NAN_F;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = CUDART_NAN_F;
-          chunk_redo<__nv_bfloat16>(p, pc.seq, pc.hk, p.q + static_cast<long long>(w_token) * p.q_stride + w_head * (HD * 2), w_pos, true,
-                                              pc.u.ks.lo, pc.u.ks.hi, pc.u.ks.first, c8, v, &w_l, err);
-          if (lane < 8) chunk_write8<__nv_bfloat16>(p, w_token, w_head, c8, v, w_l, err);
-        }
+      } else if (put && !(zero == 0.0f)) {  // (rare: see chunk_redo)
+        *reinterpret_cast<uint4*>(p.out + static_cast<long long>(token) * p.out_stride + head * (HD * 2)) =
+            make_uint4(kChunkMark, kChunkMark, kChunkMark, kChunkMark);
+        a.runs[blockIdx.x].redo = 1;
       }
       give(np);
     }
@@ -737,11 +726,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// The marked rows of the units that were whole within CTA blockIdx.x's run: block (c, y) forms rows 32 y .. of each again, four rows
+// a warp. All warps walk the run. Measured: 2048 tokens behind 14000 keys, a fourth of whose rows see a NaN, 39 ms instead of 0.28
+// (a key takes some 1.2 us, from dependent loads); three tokens of 128 heads behind 59000 keys 138 ms.
+__device__ __noinline__ void redo_run(const ChunkParams& p, const ChunkTcArgs& a, uint32_t* err) {
+  const int row = 32 * blockIdx.y + (threadIdx.x >> 3), c8 = (threadIdx.x & 7) * 8;  // 8 threads a row
+  const int t = row / BQ, tok = row % BQ / p.r, hr = row % BQ - tok * p.r;
+  Walk run(a.runs[blockIdx.x]);
+  while (run.next(p, a, err)) {
+    const Piece& pc = run.pc;
+    if (pc.k0 != 0 || pc.k1 != pc.n) continue;
+    const int i = pc.u.i0 + t * a.tokens + tok, token = pc.row0 + i, head = pc.hk * p.r + hr;
+    bool mine = tok < a.tokens && i <= pc.u.i1 && in_bounds(token >= 0 && token < p.n_tokens && head < p.H, err, 126);
+    if (mine)
+      mine = *reinterpret_cast<const uint32_t*>(p.out + static_cast<long long>(token) * p.out_stride + head * (HD * 2)) == kChunkMark;
+    if (!__any_sync(0xffffffffu, mine)) continue;
+    const int tt = mine ? token : pc.row0, hh = mine ? head : 0;
+    float v[8], l = CUDART_NAN_F;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = CUDART_NAN_F;
+    chunk_redo<__nv_bfloat16>(p, pc.seq, pc.hk, p.q + static_cast<long long>(tt) * p.q_stride + hh * (HD * 2), pc.pos0 + i, mine,
+                              pc.u.ks.lo, pc.u.ks.hi, pc.u.ks.first, c8, v, &l, err);
+    if (mine) chunk_write8<__nv_bfloat16>(p, token, head, c8, v, l, err);
+  }
+}
+
 // Units that were cut: block (c, y) joins rows 32 y .. of the unit whose first piece CTA c wrote with those of the CTAs behind it.
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ ChunkTcArgs a,
                                                          uint32_t* err) {
   pdl_trigger();
   pdl_wait();
+  if (a.runs[blockIdx.x].redo) redo_run(p, a, err);
   const ChunkCut cut = a.cuts[blockIdx.x];
   if (cut.pieces == 0) return;
   const ChunkSeq sq = chunk_seq(p, cut.seq, err);
@@ -779,9 +794,21 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
 
 namespace wenc_host {
 
-size_t chunk_tc_workspace(int sms) {
-  return (static_cast<size_t>(sms) * sizeof(ChunkCut) + 255) / 256 * 256 + static_cast<size_t>(sms) * 2 * 2 * BQ * (HD * sizeof(float) + sizeof(float2));
-}
+namespace {
+// The workspace's parts, and its size in `end`.
+struct Room {
+  size_t runs, part_o, part_ml, end;
+  explicit Room(int sms) {
+    const size_t n = static_cast<size_t>(sms);
+    runs = (n * sizeof(ChunkCut) + 255) / 256 * 256;
+    part_o = runs + (n * sizeof(ChunkRun) + 255) / 256 * 256;
+    part_ml = part_o + n * 2 * 2 * BQ * HD * sizeof(float);
+    end = part_ml + n * 2 * 2 * BQ * sizeof(float2);
+  }
+};
+}  // namespace
+
+size_t chunk_tc_workspace(int sms) { return Room(sms).end; }
 
 cudaError_t launch_chunk_tc(const ChunkParams& p, int few, void* workspace, uint32_t* err, int sms, cudaStream_t stream) {
   int dev = 0;
@@ -799,9 +826,11 @@ cudaError_t launch_chunk_tc(const ChunkParams& p, int few, void* workspace, uint
   a.tokens = BQ / p.r;
   a.per_unit = 2 * a.tokens;
   uint8_t* room = static_cast<uint8_t*>(workspace);
+  const Room at(sms);
   a.cuts = reinterpret_cast<ChunkCut*>(room);
-  a.part_o = reinterpret_cast<float*>(room + (static_cast<size_t>(sms) * sizeof(ChunkCut) + 255) / 256 * 256);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(sms) * 2 * 2 * BQ * HD);
+  a.runs = reinterpret_cast<ChunkRun*>(room + at.runs);
+  a.part_o = reinterpret_cast<float*>(room + at.part_o);
+  a.part_ml = reinterpret_cast<float2*>(room + at.part_ml);
   e = launch_pdl(chunk_tc_kernel, dim3(sms), dim3(kThreads), SMEM, stream, p, a, err);
   if (e != cudaSuccess) return e;
   return launch_pdl(chunk_join_kernel, dim3(sms, 2 * BQ / 32), dim3(256), 0, stream, p, a, err);
