@@ -459,7 +459,8 @@ typedef struct {
  * seq_start[n_seqs] are neither read nor written. Keys that no token of a sequence sees are not read, so the pages that hold
  * them alone may be gone (any entry in the table). Arithmetic as wenc_prefix_attention's: fp32 scores, statistics and
  * sums, bf16 probabilities in two bf16 parts, float32 products from three TF32 ones each. A NaN or an infinity reaches
- * exactly the rows that see it. A length, offset or page number out of range records
+ * exactly the rows that see it; a row all of whose scores are -inf is NaN. Such rows are formed a second time, from
+ * each key they see in turn: slowly, in a long cache. A length, offset or page number out of range records
  * WENC_ERR_INVALID_ARG in the device error word (wenc_sync_status(NULL)); nothing out of range is accessed and the output
  * rows it concerns are undefined. The workspace belongs to the call until its work is done: calls that may
  * overlap need one each. At most three launches, no allocation, stream-ordered; a stalled device wait is recorded as

@@ -1,4 +1,4 @@
-"""Chunk attention where values that are no numbers meet rows that see no key, and long caches.
+"""Chunk attention where values and scores that are no numbers meet rows that see no key, or nothing else, and long caches.
 
 Bounds: rows that do not see a bad value are formed from the same keys a second way at most. Each result lies within the
 bound of test_gpu_chunk_attention.py of one value: 2^-8 of it for bf16's rounding and, for some hundred keys and weighted
@@ -6,7 +6,7 @@ magnitudes below 4, less than 2^-13 times these (float32: 2^-16). Two results di
 """
 import pytest
 
-from test_gpu_chunk_attention import Case
+from test_gpu_chunk_attention import Case, plain
 
 pytestmark = pytest.mark.gpu
 
@@ -51,6 +51,38 @@ def test_rows_without_a_key_beside_rows_that_see_no_number(dtype, new, H, kv, wi
                     assert near(rows[sees][..., rest], base[sees][..., rest], dtype), (s, key, x)
                 elif bad != bad:
                     assert torch.isnan(rows[sees]).all(), (s, key, x)
+
+
+@pytest.mark.parametrize("dtype,new,H,kv,wide", FORMS)
+@pytest.mark.parametrize("window", [0, 1])
+def test_rows_whose_every_score_is_minus_infinity(dtype, new, H, kv, wide, window):
+    """exp(s - max s) of nothing but -inf is no number, and neither is the row; a row that sees one other key gives that key no
+    weight. (A row that sees no key at all gives zeros.)"""
+    import torch
+    c = Case(dtype, new, [0] * len(new), H, kv, window=window, seed=sum(new) + 1, wide=wide)
+    c.q[..., 9] = c.q[..., 9].abs() + 0.5
+    A = c.reference()[2]
+    at = [m // 2 if window else 0 for m in new]
+    for s, key in enumerate(at):
+        c.kc[int(c.table[s, key // 16]), key % 16, :, 9] = -float("inf")
+        c.keys[s][0][key, :, 9] = -float("inf")
+    got = c.run().double()
+    keys = max(new)
+    # (the bounds of test_gpu_chunk_attention.py; A without the infinite scores, whose weights are zeros exactly)
+    for s, (m, key) in enumerate(zip(new, at)):
+        rows = slice(int(c.start[s]), int(c.start[s + 1]))
+        ref, absv, _ = plain(c.q[rows].double(), *c.keys[s], torch.arange(m, device="cuda"), window, 0, 0.125)
+        assert torch.isnan(ref[key]).all() and torch.isnan(got[rows][key]).all(), s
+        rest = [i for i in range(m) if i != key]
+        e = 2.0 ** -16 + 2.0 ** -21
+        if dtype == "bf16":
+            e = e + 1.1 * A[rows][rest] * 64 * 2.0 ** -23
+            bound = 2.0 ** -8 * ref[rest].abs() + (2 * e + 2.0 ** -16 + 2 * keys * 2.0 ** -23) * absv[rest]
+        else:
+            e = e + 1.1 * A[rows][rest] * (3 * 2.0 ** -22 + 192 * 2.0 ** -23)
+            bound = 2.0 ** -24 * ref[rest].abs() + (2 * e + 3 * 2.0 ** -22 + 4 * keys * 2.0 ** -23) * absv[rest]
+        err = (got[rows][rest] - ref[rest]).abs()
+        assert (err <= bound + 1e-30).all(), (s, float((err / (bound + 1e-30)).max()))
 
 
 def test_no_wait_runs_out_while_rows_are_formed_again():

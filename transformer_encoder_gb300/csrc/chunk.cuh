@@ -75,10 +75,11 @@ __device__ __forceinline__ bool chunk_slot(const ChunkParams& p, int seq, int ke
 
 // The products with V are formed for all of a tile's rows, with weights of 0 where a row does not see a key, and in parts; but
 // 0 x inf and 0 x NaN are NaN, so a value that is no number would reach rows that do not see it, and weighted sums of values
-// near the largest float may leave the range. Elements of a row's O that are no numbers, and all of a row whose sum is none
-// (rare: they are found by that), are formed again here, in plain fp32 from the keys alone that the row sees, with weights of at
-// most 1. That goes through all keys twice, so nothing whose waits have a limit may wait for it. Eight lanes hold a row: token position pos, elements c8 .. c8 + 7 in v and sum l; all lanes of a warp call, in: the
-// lane's row is one of the call's. lo, hi, first: keys [lo, hi) and [0, first) hold all that the warp's rows see.
+// near the largest float may leave the range. Elements of a row's O that are no numbers, and all of a row whose sum is none or
+// 0 (rare: they are found by that), are formed again here, in plain fp32 from the keys alone that the row sees, with weights of
+// at most 1. That goes through all keys twice, so nothing whose waits have a limit may wait for it. Eight lanes hold a row:
+// token position pos, elements c8 .. c8 + 7 in v and sum l; all lanes of a warp call, in: the lane's row is one of the call's.
+// lo, hi, first: keys [lo, hi) and [0, first) hold all that the warp's rows see.
 template <typename T>
 __device__ __noinline__ void chunk_redo(const ChunkParams& p, int seq, int hk, const uint8_t* q_row, int pos, bool in, int lo, int hi,
                                         int first, int c8, float* v, float* l_io, uint32_t* err) {
@@ -129,11 +130,13 @@ __device__ __noinline__ void chunk_redo(const ChunkParams& p, int seq, int hk, c
   const float f = l / *l_io;
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = bad[e] ? o[e] : v[e] * f;
-  *l_io = l;
+  // (scores of -inf alone leave no weights either, but exp(s - max s) of them is no number; from position 0 on a token sees a key)
+  *l_io = l == 0.0f && pos >= 0 ? CUDART_NAN_F : l;
 }
 
-// Whether a row's sum and values are all numbers.
-__device__ __forceinline__ bool chunk_numbers(const float (&v)[8], float l) {
+// Whether a row needs no second evaluation: its sum and values are all numbers, and it has weights where it sees a key.
+__device__ __forceinline__ bool chunk_numbers(const float (&v)[8], float l, int pos) {
+  if (l == 0.0f && pos >= 0) return false;
   float zero = l * 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) zero = fmaf(v[e], 0.0f, zero);

@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(Cfg<T, NR>::THREADS, NR == 4 ? 1 : Cfg<T, NR>:
   auto put = [&](int y, float (&v)[8], float l) {
     const int z = row0 + y, tok = z / p.r, head = hk * p.r + z - tok * p.r;
     const bool in = y < n_rows && in_bounds(head < p.H && sq.row0 + tok < p.n_tokens, err, 120);
-    if (__any_sync(0xffffffffu, in && !chunk_numbers(v, l))) {
+    if (__any_sync(0xffffffffu, in && !chunk_numbers(v, l, pos0 + tok))) {
       float vc[8], lc = l;
 #pragma unroll
       for (int e = 0; e < 8; ++e) vc[e] = v[e];

@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           while (c < of_run[1] && of_run[0] * c / of_run[1] < pc.end) ++c;
           a.cuts[blockIdx.x] = ChunkCut{pc.seq, pc.hk, pc.x, static_cast<int>(c - blockIdx.x)};
         }
-      } else if (put && !(zero == 0.0f)) {  // (rare: see chunk_redo)
+      } else if (put && (!(zero == 0.0f) || (l == 0.0f && pc.pos0 + i >= 0))) {  // (rare: see chunk_redo)
         *reinterpret_cast<uint4*>(p.out + static_cast<long long>(token) * p.out_stride + head * (HD * 2)) =
             make_uint4(kChunkMark, kChunkMark, kChunkMark, kChunkMark);
         a.runs[blockIdx.x].redo = 1;
@@ -782,7 +782,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
       v[4] += f * o1.x; v[5] += f * o1.y; v[6] += f * o1.z; v[7] += f * o1.w;
     }
   }
-  if (__any_sync(0xffffffffu, in && !chunk_numbers(v, l))) {
+  if (__any_sync(0xffffffffu, in && !chunk_numbers(v, l, sq.len - sq.m + i))) {
     const int tt = in ? token : sq.row0, hh = in ? head : 0;
     chunk_redo<__nv_bfloat16>(p, cut.seq, cut.hk, p.q + static_cast<long long>(tt) * p.q_stride + hh * (HD * 2), sq.len - sq.m + i, in,
                               u.ks.lo, u.ks.hi, u.ks.first, c8, v, &l, err);
