@@ -283,6 +283,9 @@ struct Plan {
 // 29, 16 x 100 behind 500 (7 M) 38 / 30; 20 heads over 4, 128 tokens behind 2000 (5.3 M) 29 / 28, behind 8000 71 / 35.
 constexpr int kFew = 16, kLeastTc = 64;
 constexpr long long kLittle = 1ll << 22;
+// Sequences up to which a call may take chunk_tc.cu's kernel: a warp of it looks for the next sequence with work, 32 of them in
+// about a microsecond, while others wait under their limit of a second (2^20: some 30 ms).
+constexpr int kMostWalked = 1 << 20;
 
 Plan make_plan(const wenc_chunk_attention_args* a, int sms) {
   Plan pl;
@@ -293,7 +296,8 @@ Plan make_plan(const wenc_chunk_attention_args* a, int sms) {
   long long most = static_cast<long long>(max_new) * r;
   const long long cap = static_cast<long long>(a->max_pages) * a->page_size;
   const long long in_window = a->window > 0 ? static_cast<long long>(a->window) + a->sinks + max_new : cap, seen = in_window < cap ? in_window : cap;
-  if (!f32 && r <= 128 && a->scale > 0.0f && most > kLeastTc && static_cast<long long>(a->n_tokens) * a->n_heads > kLittle / seen) {
+  if (!f32 && r <= 128 && a->scale > 0.0f && most > kLeastTc && a->n_seqs <= kMostWalked &&
+      static_cast<long long>(a->n_tokens) * a->n_heads > kLittle / seen) {
     pl.tc = true;
     pl.bytes = wenc_host::chunk_tc_workspace(sms);
     most = kFew;
