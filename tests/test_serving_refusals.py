@@ -1,7 +1,9 @@
 """More of what the serving operators refuse or plan on the host (no GPU needed)."""
 import ctypes
 
-from test_chunk_refusals import L, _chunk  # noqa: F401 (L: the library, a fixture)
+import pytest
+
+from test_chunk_refusals import L, _chunk, _i4  # noqa: F401 (L: the library, a fixture)
 
 
 def test_calls_of_very_many_sequences_stay_on_the_form_without_limited_waits(L):  # noqa: F811
@@ -9,3 +11,36 @@ def test_calls_of_very_many_sequences_stay_on_the_form_without_limited_waits(L):
     sizes = dict(n_tokens=1 << 20, max_new=1000, max_pages=4096, window=0, sinks=0)
     need = [L.wenc_chunk_attention_workspace(ctypes.byref(_chunk(n_seqs=n, **sizes))) for n in (4, 1 << 20, (1 << 20) + 1, 1 << 25)]
     assert need[0] > 0 and need[1] == need[0] and need[2:] == [0, 0]
+
+
+# M 4, N 256, K 256, group 64 of _i4: x 2048 bytes (bf16), w 32768, w_scale 2048, bias 1024, out 2048 (4096 with a residual)
+APART = dict(x=1 << 20, w=2 << 20, w_scale=3 << 20, bias=4 << 20, out=5 << 20)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=(2 << 20) + 32752), dict(w=(5 << 20) + 2032), dict(out=(3 << 20) + 2032), dict(bias=(5 << 20) + 2032), dict(out=(4 << 20) + 1008),
+    dict(scale_dtype=0, out=(3 << 20) + 4080), dict(x=(5 << 20) + 2032), dict(x_dtype=0, x=(5 << 20) + 4080),
+    # a residual that begins before the output or behind its begin
+    dict(epilogue=2, resid=(5 << 20) - 4080), dict(epilogue=2, resid=(5 << 20) + 16), dict(epilogue=2, resid=(5 << 20) + 4080),
+    # (20 tokens of float32: a workspace of 30720 bytes)
+    dict(M=20, x_dtype=0, workspace=(1 << 20) + 20224), dict(M=20, x_dtype=0, workspace=(2 << 20) - 30464),
+    dict(M=20, x_dtype=0, workspace=(3 << 20) - 30464), dict(M=20, x_dtype=0, workspace=4 << 20), dict(M=20, x_dtype=0, workspace=(5 << 20) + 20224),
+    dict(M=20, x_dtype=0, epilogue=2, resid=6 << 20, workspace=(6 << 20) + 20224),
+])
+def test_linear_i4_refuses_what_overlaps(L, kw):  # noqa: F811
+    assert _i4(L, **{**APART, "workspace_bytes": 1 << 20, **kw}) == 1
+    assert b"apart" in L.wenc_last_error(), L.wenc_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(epilogue=2, resid=5 << 20), dict(epilogue=2, resid=(5 << 20) + 4096), dict(epilogue=2, resid=(5 << 20) - 4096),
+    dict(resid=(5 << 20) + 16), dict(out=(4 << 20) + 1024), dict(out=(1 << 20) - 2048), dict(M=16, x_dtype=0, workspace=1 << 20),
+    dict(M=20, x_dtype=0, workspace=6 << 20), dict(M=20, workspace=1 << 20),
+])
+def test_linear_i4_takes_what_lies_side_by_side(L, kw):  # noqa: F811
+    """(Without a GPU the call ends at the device, behind these checks.)"""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    _i4(L, **{**APART, "workspace_bytes": 1 << 20, **kw})
+    assert b"apart" not in L.wenc_last_error(), L.wenc_last_error()

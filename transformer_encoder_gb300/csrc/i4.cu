@@ -30,6 +30,8 @@ wenc_status wenc_internal_device(int* sms, uint32_t** err);
 namespace {
 
 using namespace wenc_dev;
+using wenc_host::Range;
+using wenc_host::share;
 
 struct I4Params {
   const void* x;
@@ -740,11 +742,16 @@ extern "C" wenc_status wenc_linear_i4(const void* x, int x_dtype, const uint8_t*
   if (group != 32 && group != 64 && group != 128) return bad(WENC_ERR_UNSUPPORTED, "group %lld: 32, 64 or 128", group);
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(w_scale, 16) || !aligned(bias, 16) || !aligned(resid, 16) || !aligned(out, 16))
     return bad(WENC_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
-  // (tiles of x are read while others' results are written)
-  const uintptr_t xa = reinterpret_cast<uintptr_t>(x), oa = reinterpret_cast<uintptr_t>(out);
-  const size_t x_bytes = static_cast<size_t>(M) * K * (x_dtype == WENC_DTYPE_F32 ? 4 : 2);
-  const size_t out_bytes = static_cast<size_t>(M) * N * (x_dtype == WENC_DTYPE_F32 || epilogue == WENC_EPI_BIAS_RESID_F32 ? 4 : 2);
-  if (xa < oa + out_bytes && oa < xa + x_bytes) return bad(WENC_ERR_INVALID_ARG, "linear_i4: out must lie apart from x");
+  // (inputs are read while others' results are written; a residual is read by the threads that write over it)
+  const bool joins = epilogue == WENC_EPI_BIAS_RESID_F32;
+  const long long es = x_dtype == WENC_DTYPE_F32 ? 4 : 2, ss = scale_dtype == WENC_DTYPE_F32 ? 4 : 2, rows = M;
+  const Range out_at[] = {{out, rows * N * (joins ? 4 : es)}}, room_at[] = {{workspace, static_cast<long long>(split_bytes(M, K, x_dtype))}};
+  const Range resid_at[] = {{joins ? resid : nullptr, rows * N * 4}};
+  const Range in[] = {{x, rows * K * es}, {w, static_cast<long long>(N) * (K / 2)}, {w_scale, static_cast<long long>(N) * (K / group) * ss}, {bias, 4ll * N}};
+  if (share(in, out_at)) return bad(WENC_ERR_INVALID_ARG, "linear_i4: out must lie apart from x, w, w_scale and bias");
+  if (resid != out && share(resid_at, out_at)) return bad(WENC_ERR_INVALID_ARG, "linear_i4: out must be resid or lie apart from it");
+  if (share(in, room_at) || share(resid_at, room_at) || share(out_at, room_at))
+    return bad(WENC_ERR_INVALID_ARG, "linear_i4: the workspace must lie apart from the other arguments");
   int sms = 0;
   uint32_t* err = nullptr;
   const wenc_status dst = wenc_internal_device(&sms, &err);

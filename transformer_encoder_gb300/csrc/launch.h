@@ -45,6 +45,22 @@ inline int registers_of(K kernel) {
   return cudaFuncGetAttributes(&fa, kernel) == cudaSuccess ? fa.numRegs : 0;
 }
 
+// Bytes that an argument of a call takes (none where `at` is NULL or `bytes` 0).
+struct Range {
+  const void* at;
+  long long bytes;
+};
+// Whether one of `in` shares bytes with one of `out`.
+template <int IN, int OUT>
+bool share(const Range (&in)[IN], const Range (&out)[OUT]) {
+  for (const Range& i : in)
+    for (const Range& o : out) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(i.at), y = reinterpret_cast<uintptr_t>(o.at);
+      if (i.bytes > 0 && o.bytes > 0 && x && y && x < y + o.bytes && y < x + i.bytes) return true;
+    }
+  return false;
+}
+
 // Tensor-map construction (cuTensorMapEncodeTiled through the runtime's driver entry
 // point, so the library does not link libcuda directly).
 // 2-D bf16 view: `outer` rows of `inner` elements, rows `row_stride_bytes` apart; the box is

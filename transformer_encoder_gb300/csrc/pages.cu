@@ -31,6 +31,8 @@ wenc_status wenc_internal_device(int* sms, uint32_t** err);
 namespace {
 
 using namespace wenc_dev;
+using wenc_host::Range;
+using wenc_host::share;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
@@ -369,20 +371,6 @@ wenc_status bad(wenc_status s, const char* fmt, long long a = 0, long long b = 0
   return wenc_internal_fail(s, buf);
 }
 
-struct Range {
-  const void* at;
-  long long bytes;
-};
-// Whether an input shares bytes with an output.
-template <int IN, int OUT>
-bool share(const Range (&in)[IN], const Range (&out)[OUT]) {
-  for (const Range& i : in)
-    for (const Range& o : out) {
-      const uintptr_t x = reinterpret_cast<uintptr_t>(i.at), y = reinterpret_cast<uintptr_t>(o.at);
-      if (i.bytes > 0 && o.bytes > 0 && x && y && x < y + o.bytes && y < x + i.bytes) return true;
-    }
-  return false;
-}
 // What a block table takes, from its first row's begin to its last one's end.
 long long table_bytes(int n_seqs, long long stride, int max_pages) { return n_seqs > 0 ? ((n_seqs - 1) * stride + max_pages) * 4 : 0; }
 
