@@ -13,6 +13,33 @@ def test_calls_of_very_many_sequences_stay_on_the_form_without_limited_waits(L):
     assert need[0] > 0 and need[1] == need[0] and need[2:] == [0, 0]
 
 
+# _chunk's 12 tokens of 8 heads: q and out 12288 bytes (bf16), pages 73728, table 48, lens 16, seq_start 20
+CHUNK_APART = dict(q=1 << 20, out=2 << 20, k_pages=3 << 20, v_pages=4 << 20, block_table=5 << 20, lens=6 << 20, seq_start=7 << 20)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=(3 << 20) + 73712), dict(k_pages=(2 << 20) + 12272), dict(out=(4 << 20) + 73712), dict(v_pages=(2 << 20) + 12272),
+    dict(out=(5 << 20) + 32), dict(block_table=(2 << 20) + 12284), dict(lens=(2 << 20) - 12), dict(lens=(2 << 20) + 12284),
+    dict(seq_start=(2 << 20) - 16), dict(seq_start=(2 << 20) + 12284), dict(k_page_stride=8192, out=(3 << 20) + 135168 + 3840),
+])
+def test_chunk_attention_refuses_an_output_over_its_inputs(L, kw):  # noqa: F811
+    assert L.wenc_chunk_attention(ctypes.byref(_chunk(**{**CHUNK_APART, **kw})), None) == 1
+    assert b"shares memory" in L.wenc_last_error(), L.wenc_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(out=(3 << 20) + 73728), dict(out=(3 << 20) - 12288), dict(lens=(2 << 20) - 16), dict(seq_start=(2 << 20) + 12288),
+    dict(block_table=(2 << 20) - 48), dict(seq_start=None, lens=(2 << 20) - 16),
+])
+def test_chunk_attention_takes_what_lies_side_by_side(L, kw):  # noqa: F811
+    """(Without a GPU the call ends at the device, behind these checks.)"""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    L.wenc_chunk_attention(ctypes.byref(_chunk(**{**CHUNK_APART, **kw})), None)
+    assert b"shares" not in L.wenc_last_error() and b"apart" not in L.wenc_last_error(), L.wenc_last_error()
+
+
 # M 4, N 256, K 256, group 64 of _i4: x 2048 bytes (bf16), w 32768, w_scale 2048, bias 1024, out 2048 (4096 with a residual)
 APART = dict(x=1 << 20, w=2 << 20, w_scale=3 << 20, bias=4 << 20, out=5 << 20)
 

@@ -38,6 +38,9 @@ wenc_status wenc_internal_device(int* sms, uint32_t** err);
 namespace {
 
 using namespace wenc_dev;
+using wenc_host::Range;
+using wenc_host::share;
+using wenc_host::table_bytes;
 
 constexpr int HD = 64;
 
@@ -433,6 +436,13 @@ extern "C" wenc_status wenc_chunk_attention(const wenc_chunk_attention_args* a, 
   if (a->n_tokens == 0) return WENC_OK;
   if (!apart(a->q, a->q_stride * es, a->out, a->out_stride * es, q_row * es, a->n_tokens))
     return bad(WENC_ERR_INVALID_ARG, "chunk_attention: out must lie apart from q");
+  // (rows are written while others read the cache, the lengths and their queries)
+  const long long pages_before = a->n_pages - 1, page = kv_row * a->page_size;
+  const Range out_at[] = {{a->out, ((a->n_tokens - 1ll) * a->out_stride + q_row) * es}};
+  const Range in[] = {{a->k_pages, (pages_before * a->k_page_stride + page) * es}, {a->v_pages, (pages_before * a->v_page_stride + page) * es},
+                      {a->block_table, table_bytes(a->n_seqs, a->block_table_stride, a->max_pages)}, {a->lens, 4ll * a->n_seqs},
+                      {a->seq_start, 4ll * a->n_seqs + 4}};
+  if (share(in, out_at)) return bad(WENC_ERR_INVALID_ARG, "chunk_attention: out shares memory with the pages, their table, lens or seq_start");
   int sms = 0;
   uint32_t* err = nullptr;
   const wenc_status dst = wenc_internal_device(&sms, &err);
@@ -444,6 +454,9 @@ extern "C" wenc_status wenc_chunk_attention(const wenc_chunk_attention_args* a, 
                a->workspace ? static_cast<long long>(a->workspace_bytes) : 0ll);
   if (pl.bytes > 0 && (reinterpret_cast<uintptr_t>(a->workspace) & 255u))
     return bad(WENC_ERR_INVALID_ARG, "chunk_attention: the workspace must be 256-byte aligned");
+  const Range room_at[] = {{a->workspace, static_cast<long long>(pl.bytes)}}, q_at[] = {{a->q, ((a->n_tokens - 1ll) * a->q_stride + q_row) * es}};
+  if (share(in, room_at) || share(q_at, room_at) || share(out_at, room_at))
+    return bad(WENC_ERR_INVALID_ARG, "chunk_attention: the workspace must lie apart from the other arguments");
 
   ChunkParams p = {};
   p.q = static_cast<const uint8_t*>(a->q);

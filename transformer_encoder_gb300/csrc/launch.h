@@ -61,6 +61,11 @@ bool share(const Range (&in)[IN], const Range (&out)[OUT]) {
   return false;
 }
 
+// What a block table takes, from its first row's begin to its last one's end.
+inline long long table_bytes(int n_seqs, long long stride, int max_pages) {
+  return n_seqs > 0 ? ((n_seqs - 1) * stride + max_pages) * 4 : 0;
+}
+
 // Tensor-map construction (cuTensorMapEncodeTiled through the runtime's driver entry
 // point, so the library does not link libcuda directly).
 // 2-D bf16 view: `outer` rows of `inner` elements, rows `row_stride_bytes` apart; the box is

@@ -33,6 +33,7 @@ namespace {
 using namespace wenc_dev;
 using wenc_host::Range;
 using wenc_host::share;
+using wenc_host::table_bytes;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
@@ -371,8 +372,6 @@ wenc_status bad(wenc_status s, const char* fmt, long long a = 0, long long b = 0
   return wenc_internal_fail(s, buf);
 }
 
-// What a block table takes, from its first row's begin to its last one's end.
-long long table_bytes(int n_seqs, long long stride, int max_pages) { return n_seqs > 0 ? ((n_seqs - 1) * stride + max_pages) * 4 : 0; }
 
 wenc_status launch_failed(const char* what, cudaError_t e) {
   char buf[200];
