@@ -483,7 +483,8 @@ typedef struct {
   const int32_t* free_pages; /* [n_free_pages] the first *free_count are free; they are taken from the end */
   int n_free_pages;
   const int32_t* free_count; /* [1] */
-  int32_t* lens_out;         /* [n_seqs] lengths with the new tokens; the outputs lie apart from every input */
+  int32_t* lens_out;         /* [n_seqs] lengths with the new tokens; the outputs lie apart from every input,
+                                the table from the other ones, and none over another */
   int32_t* free_count_out;   /* [1] pages that stay free */
   int32_t* seq_start;        /* [n_seqs + 1] row offsets, as wenc_kv_append and wenc_chunk_attention take them */
   int32_t* positions;        /* [n_rows] each row's position, 0 for padding; 16-byte aligned */
@@ -514,7 +515,8 @@ typedef struct {
   int32_t* free_pages;       /* [n_free_pages]; what goes back is written from *free_count on */
   int n_free_pages;
   const int32_t* free_count; /* [1] */
-  int32_t* lens_out;         /* [n_seqs] 0 for finished sequences, else lens; the outputs lie apart from every input */
+  int32_t* lens_out;         /* [n_seqs] 0 for finished sequences, else lens; the outputs lie apart from every
+                                input, and none over another */
   int32_t* free_count_out;   /* [1] */
   int32_t* trimmed_out;      /* with a window: [n_seqs] the next call's trimmed */
 } wenc_kv_release_args;

@@ -3,7 +3,7 @@ import ctypes
 
 import pytest
 
-from test_chunk_refusals import L, _chunk, _i4  # noqa: F401 (L: the library, a fixture)
+from test_chunk_refusals import L, _chunk, _extend, _i4, _release  # noqa: F401 (L: the library, a fixture)
 
 
 def test_calls_of_very_many_sequences_stay_on_the_form_without_limited_waits(L):  # noqa: F811
@@ -70,4 +70,35 @@ def test_linear_i4_takes_what_lies_side_by_side(L, kw):  # noqa: F811
     if torch.cuda.is_available():
         pytest.skip("the addresses are made up")
     _i4(L, **{**APART, "workspace_bytes": 1 << 20, **kw})
+    assert b"apart" not in L.wenc_last_error(), L.wenc_last_error()
+
+
+# 3 sequences and 8 rows: lens_out 12 bytes at 8192, free_count_out 4 at 8448, seq_start 16 at 8704, positions 32 at 9216, slots 64 at
+# 10240; the table 48 at 1024
+@pytest.mark.parametrize("kw", [
+    dict(free_pages=1024 + 44), dict(free_pages=1024 - 44), dict(lens=1024 + 44), dict(new_tokens=1024 - 8), dict(free_count=1024),
+    dict(lens_out=8444), dict(free_count_out=8704 + 12), dict(seq_start=8192 + 8), dict(positions=10240 + 48), dict(slots=9216 - 48),
+    dict(positions=8704), dict(slots=8192 - 48),
+])
+def test_kv_extend_refuses_what_it_writes_over_one_another(L, kw):  # noqa: F811
+    assert L.wenc_kv_extend(ctypes.byref(_extend(**kw)), None) == 1
+    assert b"apart" in L.wenc_last_error(), L.wenc_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(lens_out=8444), dict(free_pages=8192 - 44), dict(free_pages=8192 + 8), dict(trimmed_out=8192 + 8),
+                                dict(free_count_out=8704 + 8), dict(free_count_out=2048 + 44)])
+def test_kv_release_refuses_what_it_writes_over_one_another(L, kw):  # noqa: F811
+    assert L.wenc_kv_release(ctypes.byref(_release(**kw)), None) == 1
+    assert b"apart" in L.wenc_last_error(), L.wenc_last_error()
+
+
+@pytest.mark.parametrize("call,args", [("wenc_kv_extend", kw) for kw in (
+    dict(), dict(free_pages=1024 + 48), dict(lens=1024 - 12), dict(lens_out=8448 - 12), dict(slots=9216 + 32))] + [("wenc_kv_release", kw) for kw in (
+        dict(), dict(lens_out=8448 - 12), dict(free_pages=8192 - 48), dict(trimmed_out=8192 + 12))])
+def test_page_plans_take_what_lies_side_by_side(L, call, args):  # noqa: F811
+    """(Without a GPU the call ends at the device, behind these checks.)"""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    getattr(L, call)(ctypes.byref((_extend if call == "wenc_kv_extend" else _release)(**args)), None)
     assert b"apart" not in L.wenc_last_error(), L.wenc_last_error()

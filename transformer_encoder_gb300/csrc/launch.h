@@ -61,6 +61,17 @@ bool share(const Range (&in)[IN], const Range (&out)[OUT]) {
   return false;
 }
 
+// Whether two of them share bytes.
+template <int N>
+bool share(const Range (&all)[N]) {
+  for (int i = 0; i < N; ++i)
+    for (int j = i + 1; j < N; ++j) {
+      const Range a[] = {all[i]}, b[] = {all[j]};
+      if (share(a, b)) return true;
+    }
+  return false;
+}
+
 // What a block table takes, from its first row's begin to its last one's end.
 inline long long table_bytes(int n_seqs, long long stride, int max_pages) {
   return n_seqs > 0 ? ((n_seqs - 1) * stride + max_pages) * 4 : 0;

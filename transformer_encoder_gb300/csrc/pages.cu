@@ -400,10 +400,11 @@ extern "C" wenc_status wenc_kv_extend(const wenc_kv_extend_args* a, wenc_stream_
     return bad(WENC_ERR_INVALID_ARG, "kv_extend: positions and slots must be 16-byte aligned");
   // (blocks read the inputs while others write)
   const long long seqs = 4ll * a->n_seqs, rows = a->n_rows;
-  const Range in[] = {{a->new_tokens, seqs}, {a->lens, seqs}, {a->free_count, 4}, {a->free_pages, 4ll * a->n_free_pages},
-                      {a->block_table, table_bytes(a->n_seqs, a->block_table_stride, a->max_pages)}};
-  const Range out[] = {{a->lens_out, seqs}, {a->free_count_out, 4}, {a->seq_start, seqs + 4}, {a->positions, 4 * rows}, {a->slots, 8 * rows}};
-  if (share(in, out)) return bad(WENC_ERR_INVALID_ARG, "kv_extend: the outputs must lie apart from the inputs");
+  const Range in[] = {{a->new_tokens, seqs}, {a->lens, seqs}, {a->free_count, 4}, {a->free_pages, 4ll * a->n_free_pages}};
+  const Range out[] = {{a->lens_out, seqs}, {a->free_count_out, 4}, {a->seq_start, seqs + 4}, {a->positions, 4 * rows}, {a->slots, 8 * rows},
+                       {a->block_table, table_bytes(a->n_seqs, a->block_table_stride, a->max_pages)}};
+  if (share(in, out)) return bad(WENC_ERR_INVALID_ARG, "kv_extend: the outputs and the table must lie apart from the inputs");
+  if (share(out)) return bad(WENC_ERR_INVALID_ARG, "kv_extend: the outputs and the table must lie apart from one another");
   int sms = 0;
   uint32_t* err = nullptr;
   const wenc_status dst = wenc_internal_device(&sms, &err);
@@ -460,6 +461,7 @@ extern "C" wenc_status wenc_kv_release(const wenc_kv_release_args* a, wenc_strea
                       {a->block_table, table_bytes(a->n_seqs, a->block_table_stride, a->max_pages)}};
   const Range out[] = {{a->lens_out, seqs}, {a->trimmed_out, seqs}, {a->free_count_out, 4}, {a->free_pages, 4ll * a->n_free_pages}};
   if (share(in, out)) return bad(WENC_ERR_INVALID_ARG, "kv_release: the outputs and free_pages must lie apart from the inputs");
+  if (share(out)) return bad(WENC_ERR_INVALID_ARG, "kv_release: the outputs and free_pages must lie apart from one another");
   int sms = 0;
   uint32_t* err = nullptr;
   const wenc_status dst = wenc_internal_device(&sms, &err);
