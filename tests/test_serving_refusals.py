@@ -3,6 +3,7 @@ import ctypes
 
 import pytest
 
+import test_chunk_refusals
 from test_chunk_refusals import L, _chunk, _extend, _i4, _release  # noqa: F401 (L: the library, a fixture)
 
 
@@ -11,6 +12,11 @@ def test_calls_of_very_many_sequences_stay_on_the_form_without_limited_waits(L):
     sizes = dict(n_tokens=1 << 20, max_new=1000, max_pages=4096, window=0, sinks=0)
     need = [L.wenc_chunk_attention_workspace(ctypes.byref(_chunk(n_seqs=n, **sizes))) for n in (4, 1 << 20, (1 << 20) + 1, 1 << 25)]
     assert need[0] > 0 and need[1] == need[0] and need[2:] == [0, 0]
+
+
+def test_the_steps_of_a_unit_on_the_tensor_cores(L):  # noqa: F811
+    """Steps of 128 keys from the first visible one on, at any key (the other steps and alignments: test_chunk_refusals.py)."""
+    test_chunk_refusals.test_the_steps_of_a_run_of_tokens(L, 128, 1)
 
 
 # _chunk's 12 tokens of 8 heads: q and out 12288 bytes (bf16), pages 73728, table 48, lens 16, seq_start 20
