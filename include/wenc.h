@@ -460,11 +460,12 @@ typedef struct {
  * them alone may be gone (any entry in the table). Arithmetic as wenc_prefix_attention's: fp32 scores, statistics and
  * sums, bf16 probabilities in two bf16 parts, float32 products from three TF32 ones each. A NaN or an infinity reaches
  * exactly the rows that see it; a row all of whose scores are -inf is NaN. Such rows are formed a second time, from
- * each key they see in turn: slowly, in a long cache. A length, offset or page number out of range records
+ * each key they see in turn: slowly, in a long cache. Weighted values are summed before they are divided by the weights' sum:
+ * values beyond 2^127 over the number of keys may leave fp32's range. A length, offset or page number out of range records
  * WENC_ERR_INVALID_ARG in the device error word (wenc_sync_status(NULL)); nothing out of range is accessed and the output
  * rows it concerns are undefined. The workspace belongs to the call until its work is done: calls that may
- * overlap need one each. At most three launches, no allocation, stream-ordered; a stalled device wait is recorded as
- * for wenc_attention. */
+ * overlap need one each, apart from every other argument. At most three launches, no allocation, stream-ordered; a
+ * stalled device wait is recorded as for wenc_attention. */
 WENC_API wenc_status wenc_chunk_attention(const wenc_chunk_attention_args* args, wenc_stream_t stream);
 
 /* wenc_chunk_attention_workspace -- bytes of workspace the call needs on the current device (0 for
@@ -540,8 +541,8 @@ WENC_API wenc_status wenc_kv_release(const wenc_kv_release_args* args, wenc_stre
  * group 32, 64 or 128; N a multiple of 128, K of 128, 1 <= M <= 2^28; buffers 16-byte aligned. bf16
  * products are exact, float32 x enters as three bf16 parts (exact together); sums are fp32, a group's before its scale.
  * workspace: wenc_linear_i4_workspace(...) bytes, 256-byte aligned (may be NULL when that is 0); it belongs to the call until its
- * work is done: calls that may overlap need one each. At most two launches; stream-ordered; errors as
- * wenc_linear, and a stalled device wait is recorded as for wenc_attention. */
+ * work is done: calls that may overlap need one each, apart from every other argument. At most two launches; stream-ordered;
+ * errors as wenc_linear, and a stalled device wait is recorded as for wenc_attention. */
 WENC_API wenc_status wenc_linear_i4(const void* x, int x_dtype, const uint8_t* w, const void* w_scale, int scale_dtype,
                                     const float* bias, const float* resid, void* out, int M, int N, int K, int group,
                                     int epilogue, void* workspace, size_t workspace_bytes, wenc_stream_t stream);

@@ -7,14 +7,15 @@
 // (inferencelayer 0.2.4 src/whisper_gpu.rs, DEC_QATTN; oxinfer 0.0.5 src/whisper/model.rs, attention_masked).
 //
 // A cluster of 1 to 8 CTAs attends one item: a tile of 8 NR rows (token, query head) of one sequence and key head. The keys
-// that some row of the tile sees (KeySteps) are cut into steps of 16, of which every warp of the cluster takes an equal run;
-// a warp has a ring of cp.async stages of its own, with its keys' pages looked up a step ahead, and no barrier with other warps until their
-// results are joined: through shared memory, and between CTAs through distributed shared memory. Only steps at the borders
-// of what the rows see are masked (attend.cuh has the steps' arithmetic).
-// What bounds it: the bytes of K and V (each read once for a tile's rows), and at small calls the latency of getting at them. Measured on
-// the device: 80 single tokens of 20 heads, each behind 1500 keys of a window and 4 first ones (606 MB), 100 us, 6.0 TB/s (6.8: a plain
-// copy); one token of 6 heads behind 452 keys 5.7 us; fp32, up to 33 tokens of 24 sequences, 8 heads, windows of 500, 21 us: there the
-// instructions that cut the operands in parts, at 8 warps an SM (255 registers).
+// that some row of the tile sees (KeySteps) are cut into steps of 16, of which every warp of the cluster takes an equal run; a
+// warp has a ring of cp.async stages of its own, with its keys' pages looked up a step ahead, and no barrier with other warps
+// until their results are joined: through shared memory, and between CTAs through distributed shared memory. Only steps at the
+// borders of what the rows see are masked (attend.cuh has the steps' arithmetic).
+// What bounds it: the bytes of K and V (each read once for a tile's rows), and at small calls the latency of getting at them.
+// Measured on the device: 80 single tokens of 20 heads, each behind 1500 keys of a window and 4 first ones (606 MB), 100 us,
+// 6.0 TB/s (6.8: a plain copy); one token of 6 heads behind 452 keys 5.7 us; fp32, up to 33 tokens of 24 sequences, 8 heads,
+// windows of 500, 21 us: there latency, at 8 warps an SM (255 registers; they issue in 34% of the cycles, the tensor pipe is
+// busy in 30%).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -279,11 +280,13 @@ struct Plan {
   size_t bytes = 0;
 };
 
-// bf16: up to kLeastTc rows per key head, and calls of up to kLittle pairs of a query row and a key that they may have, are attended
-// here, in tiles of up to 32 rows. Other calls leave sequences of more than kFew rows to chunk_tc.cu, and take tiles of 16 for
-// the rest. Measured (us, here / there with its three launches): 40 rows of each of 32 sequences, 4 key heads, 3000 keys 28 / 52;
-// 8 heads, 1 x 256 tokens behind 256 (0.8 M pairs) 17 / 26, 2 x 256 behind 1000 (4.6 M) 23 / 27, 8 x 256 behind 256 (6.3 M) 31 /
-// 29, 16 x 100 behind 500 (7 M) 38 / 30; 20 heads over 4, 128 tokens behind 2000 (5.3 M) 29 / 28, behind 8000 71 / 35.
+// bf16: up to kLeastTc rows per key head, and calls of up to kLittle pairs of a query row and a key that they may have, are
+// attended here, in tiles of up to 32 rows. Other calls leave sequences of more than kFew rows to chunk_tc.cu, and take tiles
+// of 16 for the rest. Measured (us, here / there with its three launches): 40 rows of each of 32 sequences, 4 key heads, 3000
+// keys 28 / 52; 8 heads, 1 x 256 tokens behind 256 (0.8 M pairs) 17 / 26, 2 x 256 behind 1000 (4.6 M) 23 / 27, 8 x 256 behind
+// 256 (6.3 M) 31 / 29, 16 x 100 behind 500 (7 M) 38 / 30; 20 heads over 4, 128 tokens behind 2000 (5.3 M) 29 / 28, behind 8000
+// 71 / 35. The host knows the block table's width, not the lengths: with a table for 32 thousand keys the first of these calls,
+// and any other whose caches are much shorter than its table, goes there.
 constexpr int kFew = 16, kLeastTc = 64;
 constexpr long long kLittle = 1ll << 22;
 // Sequences up to which a call may take chunk_tc.cu's kernel: a warp of it looks for the next sequence with work, 32 of them in
@@ -439,10 +442,12 @@ extern "C" wenc_status wenc_chunk_attention(const wenc_chunk_attention_args* a, 
   // (rows are written while others read the cache, the lengths and their queries)
   const long long pages_before = a->n_pages - 1, page = kv_row * a->page_size;
   const Range out_at[] = {{a->out, ((a->n_tokens - 1ll) * a->out_stride + q_row) * es}};
-  const Range in[] = {{a->k_pages, (pages_before * a->k_page_stride + page) * es}, {a->v_pages, (pages_before * a->v_page_stride + page) * es},
+  const Range in[] = {{a->k_pages, (pages_before * a->k_page_stride + page) * es},
+                      {a->v_pages, (pages_before * a->v_page_stride + page) * es},
                       {a->block_table, table_bytes(a->n_seqs, a->block_table_stride, a->max_pages)}, {a->lens, 4ll * a->n_seqs},
                       {a->seq_start, 4ll * a->n_seqs + 4}};
-  if (share(in, out_at)) return bad(WENC_ERR_INVALID_ARG, "chunk_attention: out shares memory with the pages, their table, lens or seq_start");
+  if (share(in, out_at))
+    return bad(WENC_ERR_INVALID_ARG, "chunk_attention: out shares memory with the pages, their table, lens or seq_start");
   int sms = 0;
   uint32_t* err = nullptr;
   const wenc_status dst = wenc_internal_device(&sms, &err);
@@ -454,7 +459,8 @@ extern "C" wenc_status wenc_chunk_attention(const wenc_chunk_attention_args* a, 
                a->workspace ? static_cast<long long>(a->workspace_bytes) : 0ll);
   if (pl.bytes > 0 && (reinterpret_cast<uintptr_t>(a->workspace) & 255u))
     return bad(WENC_ERR_INVALID_ARG, "chunk_attention: the workspace must be 256-byte aligned");
-  const Range room_at[] = {{a->workspace, static_cast<long long>(pl.bytes)}}, q_at[] = {{a->q, ((a->n_tokens - 1ll) * a->q_stride + q_row) * es}};
+  const Range room_at[] = {{a->workspace, static_cast<long long>(pl.bytes)}};
+  const Range q_at[] = {{a->q, ((a->n_tokens - 1ll) * a->q_stride + q_row) * es}};
   if (share(in, room_at) || share(q_at, room_at) || share(out_at, room_at))
     return bad(WENC_ERR_INVALID_ARG, "chunk_attention: the workspace must lie apart from the other arguments");
 

@@ -1,12 +1,13 @@
 // chunk_tc.cu -- the chunks of chunk_attn.cu that bring many bf16 query rows (prompts and their parts), on the 5th-generation
 // tensor cores.
 //
-// Of a sequence with more rows per key head than the few of chunk_attn.cu, a unit of work is 2 x 128 / r tokens of one key head (r
-// query heads share it; two row tiles of 128) against the keys that these tokens see, in steps of 128. Units differ in length: a prompt's later
-// tokens see more keys, sequences bring what they bring. So all units' steps are laid end to end, each with kStart more for its
-// beginning and end, and every CTA (one per SM) takes an equal run of them, which it finds itself from the lengths: there is
-// no plan to build and read, and no CTA idles while another works on a long unit. A unit that is whole within a run goes straight to the output;
-// of one that is cut, the pieces (at most one at either end of a run) go to the workspace, and chunk_join_kernel joins them, in order.
+// Of a sequence with more rows per key head than the few of chunk_attn.cu, a unit of work is 2 x 128 / r tokens of one key head
+// (r query heads share it; two row tiles of 128) against the keys that these tokens see, in steps of 128. Units differ in
+// length: a prompt's later tokens see more keys, sequences bring what they bring. So all units' steps are laid end to end, each
+// with kStart more for its beginning and end, and every CTA (one per SM) takes an equal run of them, which it finds itself from
+// the lengths: there is no plan to build and read, and no CTA idles while another works on a long unit. A unit that is whole
+// within a run goes straight to the output; of one that is cut, the pieces (at most one at either end of a run) go to the
+// workspace, and chunk_join_kernel joins them, in order.
 //
 // Within a CTA, in the manner of prefix_tc.cu: S = Q K^T and O += P V by tcgen05.mma into TMEM, one softmax thread per query row,
 // P as two bf16 parts (2^-16), the A operands of the second product. What differs:
@@ -18,15 +19,17 @@
 //    whole number (of log2), so moving it is exact;
 //  - rows that come out as no numbers are formed again behind this kernel, by chunk_join_kernel: that takes as long as the cache is
 //    long, and the other roles' waits have a limit.
-// What bounds it: the two softmax warps of a scheduler (all warps together issue 1970 instructions a scheduler and step of 256 x 128, in 58%
-// of the cycles; what they wait for are TMEM loads and results of their own, and more warps find no registers). The tensor pipe is
-// busy for 47%. 2048 tokens of 20 heads over 4 behind 14000 keys take 228 us, 687 TFLOP/s of the two products, a
-// step some 3400 cycles; its MMAs alone, in straight lines, would take 1650, its exponentials (16 an SM and cycle) 2048. On the way there (us): first form 567
-// (every role walked, loops unrolled: warps waited for instructions), 442 walked by one warp, 313 with rolled loops, 270 with
-// the pages looked up a step ahead and three score buffers, 257 with P in TMEM alone, 245 with tiles handed over by their
-// copies' own arrival and P's barriers in pairs, 228 with a piece's queries addressed without divisions. Not kept: taking turns on the
-// exponentials, unrolled exponentials (331), the next 32 scores loaded ahead (256 against 245), four gathering warps (252); a
-// polynomial on the FMA pipe for one pair of exponentials in 8, 4 or 2 (238, 249, 293 against 230): it is instructions that count.
+// What bounds it: the two softmax warps of a scheduler (all warps together issue 1970 instructions a scheduler and step of 256
+// x 128, in 58% of the cycles; what they wait for are TMEM loads and results of their own, and more warps find no registers).
+// The tensor pipe is busy for 47%. 2048 tokens of 20 heads over 4 behind 14000 keys take 228 us, 687 TFLOP/s of the two
+// products, a step some 3400 cycles; its MMAs alone, in straight lines, would take 1650, its exponentials (16 an SM and cycle)
+// 2048. (These are 7.7 instructions a score; the arithmetic as it is written here counts some 4.5.) On the way there (us):
+// first form 567 (every role walked, loops unrolled: warps waited for instructions), 442 walked by one warp, 313 with rolled
+// loops, 270 with the pages looked up a step ahead and three score buffers, 257 with P in TMEM alone, 245 with tiles handed
+// over by their copies' own arrival and P's barriers in pairs, 228 with a piece's queries addressed without divisions. Not
+// kept: taking turns on the exponentials, unrolled exponentials (331), the next 32 scores loaded ahead (256 against 245), four
+// gathering warps (252); a polynomial on the FMA pipe for one pair of exponentials in 8, 4 or 2 (238, 249, 293 against 230): it
+// is instructions that count.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -66,9 +69,9 @@ constexpr uint32_t OFF_K = OFF_Q + 2 * Q_BYTES;
 constexpr uint32_t OFF_V = OFF_K + NK * KV_BYTES;
 constexpr uint32_t OFF_BARS = OFF_V + NV * KV_BYTES;
 // bars: q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], and per query tile t: s_full[t][2], p_full[t][2] and
-// pv_done[t][2]; drain; piece_full[NP], piece_empty[NP]. (Pairs, of even and odd steps: a wait tells a phase from the next one only,
-// and an S may be a step ahead of its softmax, a P one ahead of the PV issuer, which may wait for V, a PV one ahead of the S issuer's
-// wait for the last.)
+// pv_done[t][2]; drain; piece_full[NP], piece_empty[NP]. (Pairs, of even and odd steps: a wait tells a phase from the next one
+// only, and an S may be a step ahead of its softmax, a P one ahead of the PV issuer, which may wait for V, a PV one ahead of
+// the S issuer's wait for the last.)
 constexpr int NUM_BARS = 2 + 2 * NK + 2 * NV + 12 + 1 + 2 * NP;
 constexpr int kTakers = 11;  // warps that take pieces from the ring: all but the one that walks
 constexpr size_t SMEM = 1024 + OFF_BARS + NUM_BARS * 8 + 16;
@@ -336,7 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tO = [&](int t) { return tmem_base + 384u + 64u * t; };
 
   // Every role takes the same pieces in the same order and counts K/V tiles across them, so ring slots and barrier parities
-  // continue from one piece to the next. take(i): piece i, false behind the last (or after a failed wait); give(i): it is done with.
+  // continue from one piece to the next. take(i): piece i, false behind the last (or after a failed wait); give(i): it is done
+  // with.
   auto take = [&](int i) { return mbar_wait_warp(piece_full(i % NP), (i / NP) & 1, wc, 8) && pieces[i % NP].k1 > 0; };
   auto give = [&](int i) {
     __syncwarp();
@@ -566,9 +570,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 32; ++c) r[c] = (sees >> c) & 1u ? r[c] : 0xff800000u;
         };
-        // The row's reference is the maximum (rounded up to a whole number, so that references differ by powers of two) of the first
-        // step of which it sees a key, and stays as long as the weights stay below 2^20. The maximum of every step, formed
-        // first, costs a quarter of the instructions.
+        // The row's reference is the maximum (rounded up to a whole number, so that references differ by powers of two) of the
+        // first step of which it sees a key, and stays as long as the weights stay below 2^20. The maximum of every step,
+        // formed first, costs a quarter of the instructions.
         float m_new = m;
         if (__any_sync(0xffffffffu, m == -CUDART_INF_F)) {
           float mx = -CUDART_INF_F;
@@ -726,9 +730,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The marked rows of the units that were whole within CTA blockIdx.x's run: block (c, y) forms rows 32 y .. of each again, four rows
-// a warp. All warps walk the run. Measured: 2048 tokens behind 14000 keys, a fourth of whose rows see a NaN, 39 ms instead of 0.28
-// (a key takes some 1.2 us, from dependent loads); three tokens of 128 heads behind 59000 keys 138 ms.
+// The marked rows of the units that were whole within CTA blockIdx.x's run: block (c, y) forms rows 32 y .. of each again, four
+// rows a warp. All warps walk the run. Measured: 2048 tokens behind 14000 keys, a fourth of whose rows see a NaN, 39 ms instead
+// of 0.23 (a key takes some 1.2 us, from dependent loads); three tokens of 128 heads behind 59000 keys 138 ms.
 __device__ __noinline__ void redo_run(const ChunkParams& p, const ChunkTcArgs& a, uint32_t* err) {
   const int row = 32 * blockIdx.y + (threadIdx.x >> 3), c8 = (threadIdx.x & 7) * 8;  // 8 threads a row
   const int t = row / BQ, tok = row % BQ / p.r, hr = row % BQ - tok * p.r;
@@ -738,8 +742,10 @@ __device__ __noinline__ void redo_run(const ChunkParams& p, const ChunkTcArgs& a
     if (pc.k0 != 0 || pc.k1 != pc.n) continue;
     const int i = pc.u.i0 + t * a.tokens + tok, token = pc.row0 + i, head = pc.hk * p.r + hr;
     bool mine = tok < a.tokens && i <= pc.u.i1 && in_bounds(token >= 0 && token < p.n_tokens && head < p.H, err, 126);
-    if (mine)
-      mine = *reinterpret_cast<const uint32_t*>(p.out + static_cast<long long>(token) * p.out_stride + head * (HD * 2)) == kChunkMark;
+    if (mine) {
+      const uint8_t* at = p.out + static_cast<long long>(token) * p.out_stride + head * (HD * 2);
+      mine = *reinterpret_cast<const uint32_t*>(at) == kChunkMark;
+    }
     if (!__any_sync(0xffffffffu, mine)) continue;
     const int tt = mine ? token : pc.row0, hh = mine ? head : 0;
     float v[8], l = CUDART_NAN_F;

@@ -88,9 +88,10 @@ __host__ __device__ __forceinline__ int segment_of(const int* step0, int t, int 
 }
 
 // ------------------------------------------------------------------ keys of a run of tokens (chunk_attn.cu, chunk_tc.cu)
-// The keys that tokens at positions first .. last of a sequence see between them, in steps of `step` keys: the leading n_first steps
-// [0, step), .. for the first `sinks` keys, then the others from lo_step on (a multiple of `align`) up to the last token's own.
-// Where the two meet they are one run (n_first 0, lo_step 0). Keys from `lo` on, and below `first`, are seen by some token.
+// The keys that tokens at positions first .. last of a sequence see between them, in steps of `step` keys: the leading n_first
+// steps [0, step), .. for the first `sinks` keys, then the others from lo_step on (a multiple of `align`) up to the last
+// token's own. Where the two meet they are one run (n_first 0, lo_step 0). Keys from `lo` on, and below `first`, are seen by
+// some token.
 struct KeySteps {
   int lo, hi, first;      // keys [lo, hi) and [0, first)
   int n_first, lo_step, n;

@@ -4,12 +4,14 @@
 // (oxinfer 0.0.5 src/whisper/model.rs, make_lin: quantised weights; here with groups of inputs).
 //
 // u - 8 is exact in bf16, a bf16 x times it is exact in fp32, so a group's product runs on the bf16 tensor cores without a
-// rounding of either operand, and the scale, which would not fit into the weight exactly, multiplies the group's fp32 sum. float32 x is
-// cut into three bf16 parts (8 + 8 + 8 significant bits: exact together), the products of which share a group's sum.
+// rounding of either operand, and the scale, which would not fit into the weight exactly, multiplies the group's fp32 sum.
+// float32 x is cut into three bf16 parts (8 + 8 + 8 significant bits: exact together), the products of which share a group's
+// sum.
 //
 // Two forms, on the device in us: up to 16 tokens on mma.sync, where a token costs little beside the weights' bytes and latency
-// (tokens x N x K: 1 x 1152 x 384 3.7, 16 x 5120 x 1280 6.3, 1 x 7680 x 5120 14.4), more on tcgen05 (24 x 5120 x 1280 8.0, 80 x 5120 x
-// 1280 11.4, 2240 x 1280 x 5120 33.4, 880 TFLOP/s; float32 300 x 1280 x 1280 15).
+// (tokens x N x K: 1 x 1152 x 384 3.7, 16 x 5120 x 1280 6.3, 1 x 7680 x 5120 14.4, where 1.4 TB/s of weights wait for loads of
+// four bytes a lane, one piece ahead), more on tcgen05 (24 x 5120 x 1280 8.0, 80 x 5120 x 1280 11.4, 2240 x 1280 x 5120 33.4,
+// 880 TFLOP/s; float32 300 x 1280 x 1280 15).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -108,9 +110,9 @@ __device__ __forceinline__ void put4(const I4Params& p, size_t at, float4 v, con
 
 // ---------------------------------------------------------------- few tokens
 // out^T = W x^T for up to 8 NT tokens: a CTA takes 16 channels (the MMA's M), its warps share K in pieces of 128, and the CTAs
-// of a cluster share it further; they are joined through shared memory, in the order of the warps. Weights go from global memory to registers: a
-// lane takes the word (8 weights) that its MMA rows need of each 32 inputs, so a group's products stay together for
-// every group size, and x comes in the same order of k from L1 or L2.
+// of a cluster share it further; they are joined through shared memory, in the order of the warps. Weights go from global
+// memory to registers: a lane takes the word (8 weights) that its MMA rows need of each 32 inputs, so a group's products stay
+// together for every group size, and x comes in the same order of k from L1 or L2.
 constexpr int kRowsWarps = 8;
 constexpr int kPiece = 128;  // inputs of a warp's piece
 
@@ -237,15 +239,17 @@ __global__ void __launch_bounds__(32 * kRowsWarps) i4_rows_kernel(const __grid_c
 }
 
 // ---------------------------------------------------------------- many tokens
-// out^T = W x^T on tcgen05: a CTA takes 128 channels (the MMA's M, TMEM's lanes) and up to 160 tokens (its N), and the CTAs of a cluster share K
-// where there are few tiles. Four warps widen the weights from global memory straight into TMEM, a channel a thread: the A
-// operand. x comes by TMA as it lies (float32: its three parts, cut apart by i4_split_kernel first). A group's products make an
-// accumulator of their own, one of two in TMEM; eight warps, a channel a thread again, add it times the group's scale to
-// their sums in registers while the MMAs fill the other. So a scale is one number a thread and group, and no weight is rounded.
-// What bounds it: the MMAs (80 cycles for each 16 inputs of 160 tokens; busy 41% of the cycles at 2240 x 1280 x 5120, whose 140 CTAs begin and end
-// together), and with groups of 32 the reading of accumulators. At 80 x 5120 x 1280 the latency of 10 pieces in a row. Not kept:
-// four pieces unrolled in the issuers (41.6 us against 35 for the large one: code past the instruction cache), four accumulators of 80
-// tokens (no gain), the output unrolled (12.5 us against 11.4 for the small one).
+// out^T = W x^T on tcgen05: a CTA takes 128 channels (the MMA's M, TMEM's lanes) and up to 160 tokens (its N), and the CTAs of
+// a cluster share K where there are few tiles. Four warps widen the weights from global memory straight into TMEM, a channel a
+// thread: the A operand. x comes by TMA as it lies (float32: its three parts, cut apart by i4_split_kernel first). A group's
+// products make an accumulator of their own, one of two in TMEM; eight warps, a channel a thread again, add it times the
+// group's scale to their sums in registers while the MMAs fill the other. So a scale is one number a thread and group, and no
+// weight is rounded.
+// What bounds it: the MMAs (80 cycles for each 16 inputs of 160 tokens; busy 41% of the cycles at 2240 x
+// 1280 x 5120, whose 140 CTAs begin and end together), and with groups of 32 the reading of accumulators. At 80 x 5120 x 1280,
+// two CTAs to a K, five pieces in a row of some 0.8 us each, and some 7 us of a CTA's beginning, join and end. Not kept: four
+// pieces unrolled in the issuers (41.6 us against 35 for the large one: code past the instruction cache), four accumulators of
+// 80 tokens (no gain), the output unrolled (12.5 us against 11.4 for the small one).
 constexpr int kTcMost = 160;                // tokens of a tile
 constexpr int kTcThreads = 512;             // 4 widening warps, 2 MMA issuers, TMA producer, a warp for the scales, 8 summing warps
 constexpr int kAStages = 2, kXStages = 4;   // of 128 inputs
@@ -365,10 +369,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (lane == 0) mbar_arrive(a_full(st));
     }
   } else if (warp == 4 || warp == 6) {
-    // ---------------- MMA issuers, two for every other piece: the whole warp waits, one thread issues. A group's MMAs are straight lines behind
-    // one election (44 cycles each, or their own time; with a branch between them 110 to 130). What lies between the lines, waits that
-    // are over and a descriptor, is some 700 cycles a piece, more than its MMAs take: so the other issuer's run meanwhile. They go in turn: a
-    // wait tells one phase of a barrier from the next, not from the one after.
+    // ---------------- MMA issuers, two for every other piece: the whole warp waits, one thread issues.
+    // A group's MMAs are straight lines behind one election (44 cycles each, or their own time; with a branch between them 110 to 130). What lies between the lines,
+    // waits that are over and a descriptor, is some 700 cycles a piece, more than its MMAs take: so the other issuer's run
+    // meanwhile. They go in turn: a wait tells one phase of a barrier from the next, not from the one after.
     constexpr int kLine = GROUP < 64 ? GROUP : 64, kSteps = kLine / 16, kLines = kPiece / kLine;  // (a group of 128 in two)
     static_assert(kXStages == 4 && kAStages == 2, "slots and parities by masks");
     const uint32_t idesc = idesc_bf16_f32(128, (m_here + 15) / 16 * 16, false);
@@ -441,8 +445,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     __syncwarp();
   } else if (warp == 7) {
-    // ---------------- the scales of eight groups at a time, four channels a lane, two stages ahead of what is stored: their latency
-    // would be the summing warps' otherwise
+    // ---------------- the scales of eight groups at a time, four channels a lane, two stages ahead of what is stored: their
+    // latency would be the summing warps' otherwise
     const size_t row = static_cast<size_t>(n0 + lane) * p.groups + k_begin / GROUP, step = static_cast<size_t>(32) * p.groups;
     uint32_t raw[2][4][kSGroups];
     auto fetch = [&](uint32_t (&r)[4][kSGroups], int g0) {  // (as they lie: nothing waits for a load before it is widened)
@@ -647,7 +651,10 @@ size_t split_bytes(int M, int K, int x_dtype) {
 
 // Tokens of a tile and CTAs that share K: the division whose rounds of the machine take least, in cycles of a piece of 128
 // inputs (the MMAs' 4 a token, but no less than widening and, of every group, summing take) and of a CTA's beginning and end. The
-// constants are fitted to measured times. Where K is shared, an end adds the joining: 80 x 5120 x 1280 with four CTAs to a K takes 25 us, alone 11.4.
+// constants put divisions that were measured in their order; they foretell no times (some half of the measured cycles at 2240 x
+// 1280 x 5120, and 24 and 80 tokens x 5120 x 1280 come out alike, which take 8.0 and 11.4 us). Where K is shared, an end adds
+// the joining. 80 x 5120 x 1280, on 152 SMs: one CTA to a K (ten pieces) 15.4 us, two 11.4, three 10.9 (only powers of two are
+// tried), four 17.6 (160 CTAs: a second round).
 constexpr long long kWidenCycles = 600, kSumCycles = 350, kEndCycles = 5000, kJoinCycles = 1500;
 void pick_tiles(int M, int n_tiles, int K, int group, int parts, int sms, int& tok, int& ksplit) {
   const int least = (M + kTcMost - 1) / kTcMost, pieces = K / kPiece;
@@ -745,11 +752,14 @@ extern "C" wenc_status wenc_linear_i4(const void* x, int x_dtype, const uint8_t*
   // (inputs are read while others' results are written; a residual is read by the threads that write over it)
   const bool joins = epilogue == WENC_EPI_BIAS_RESID_F32;
   const long long es = x_dtype == WENC_DTYPE_F32 ? 4 : 2, ss = scale_dtype == WENC_DTYPE_F32 ? 4 : 2, rows = M;
-  const Range out_at[] = {{out, rows * N * (joins ? 4 : es)}}, room_at[] = {{workspace, static_cast<long long>(split_bytes(M, K, x_dtype))}};
+  const Range out_at[] = {{out, rows * N * (joins ? 4 : es)}};
+  const Range room_at[] = {{workspace, static_cast<long long>(split_bytes(M, K, x_dtype))}};
   const Range resid_at[] = {{joins ? resid : nullptr, rows * N * 4}};
-  const Range in[] = {{x, rows * K * es}, {w, static_cast<long long>(N) * (K / 2)}, {w_scale, static_cast<long long>(N) * (K / group) * ss}, {bias, 4ll * N}};
+  const Range in[] = {{x, rows * K * es}, {w, static_cast<long long>(N) * (K / 2)},
+                      {w_scale, static_cast<long long>(N) * (K / group) * ss}, {bias, 4ll * N}};
   if (share(in, out_at)) return bad(WENC_ERR_INVALID_ARG, "linear_i4: out must lie apart from x, w, w_scale and bias");
-  if (resid != out && share(resid_at, out_at)) return bad(WENC_ERR_INVALID_ARG, "linear_i4: out must be resid or lie apart from it");
+  if (resid != out && share(resid_at, out_at))
+    return bad(WENC_ERR_INVALID_ARG, "linear_i4: out must be resid or lie apart from it");
   if (share(in, room_at) || share(resid_at, room_at) || share(out_at, room_at))
     return bad(WENC_ERR_INVALID_ARG, "linear_i4: the workspace must lie apart from the other arguments");
   int sms = 0;

@@ -7,14 +7,14 @@
 //   entry b + i of a sequence <- free_pages[count - 1 - (base + i)],
 //   row t of sequence s: position len + (t - seq_start[s]), slot = table[position / page] * page + position % page.
 // And when sequences end, or a window has moved past a page: the entries of sequence s that go back, in two ranges [a0, b0)
-// and [a1, b1) (gives() below), are written behind the free pages in order of sequence and entry.
+// and [a1, b1) (gives() in decode_index.cuh), are written behind the free pages in order of sequence and entry.
 //
 // What bounds them: launch and latency for a decode step (a few kilobytes), and the rows' 12 bytes each for prompts. Every
 // block sums the lengths itself (4 or 9 bytes a sequence, from L2) instead of waiting for another's sums, so there is one
-// launch, no barrier over the grid and nothing kept between calls. kv_extend works by rows: a row knows whether it opens a
-// page (position % page == 0) and then fetches that page from the free ones itself, so no row waits for the table. Measured on the device:
-// kv_extend 5.2 us for a token of each of 256 sequences, 10.1 us for 2048 with up to 500 tokens each (half a million rows);
-// kv_release 5.2 us for 256 sequences, 9.4 us for 4096 streams with a window.
+// launch, no barrier over the grid and nothing kept between calls. kv_extend works by rows: a row knows whether it opens a page
+// (position % page == 0) and then fetches that page from the free ones itself, so no row waits for the table. Measured on the
+// device: kv_extend 5.2 us for a token of each of 256 sequences, 10.1 us for 2048 with up to 500 tokens each (half a million
+// rows); kv_release 5.2 us for 256 sequences, 9.4 us for 4096 streams with a window.
 #include <cuda_runtime.h>
 
 #include <cstdio>
@@ -401,8 +401,8 @@ extern "C" wenc_status wenc_kv_extend(const wenc_kv_extend_args* a, wenc_stream_
   // (blocks read the inputs while others write)
   const long long seqs = 4ll * a->n_seqs, rows = a->n_rows;
   const Range in[] = {{a->new_tokens, seqs}, {a->lens, seqs}, {a->free_count, 4}, {a->free_pages, 4ll * a->n_free_pages}};
-  const Range out[] = {{a->lens_out, seqs}, {a->free_count_out, 4}, {a->seq_start, seqs + 4}, {a->positions, 4 * rows}, {a->slots, 8 * rows},
-                       {a->block_table, table_bytes(a->n_seqs, a->block_table_stride, a->max_pages)}};
+  const Range out[] = {{a->lens_out, seqs}, {a->free_count_out, 4}, {a->seq_start, seqs + 4}, {a->positions, 4 * rows},
+                       {a->slots, 8 * rows}, {a->block_table, table_bytes(a->n_seqs, a->block_table_stride, a->max_pages)}};
   if (share(in, out)) return bad(WENC_ERR_INVALID_ARG, "kv_extend: the outputs and the table must lie apart from the inputs");
   if (share(out)) return bad(WENC_ERR_INVALID_ARG, "kv_extend: the outputs and the table must lie apart from one another");
   int sms = 0;
